@@ -447,7 +447,8 @@ def _run_evict(st):
         import gemv_w4a16_group_gb300 as w4
         kept, new_lens, weights = w4.kv4_evict(
             st["cache"], st["table"], st["lens"], st["weights"], st["out_table"], budget,
-            st["max_len"], first=first, recent=recent, weights_out=st["weights_out"])
+            st["max_len"], c["head_dim"], first=first, recent=recent, group=group,
+            weights_out=st["weights_out"])
         k, v = w4.kv4_read(st["cache"], st["out_table"], new_lens, st["starts"],
                            sum(st["kept_list"]), c["head_dim"], group=group)
         return {"kept": kept, "lens": new_lens, "weights": weights, "k": k, "v": v}
