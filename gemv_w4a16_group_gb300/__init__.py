@@ -25,6 +25,9 @@ Formats ("Low-Precision Kernels: INT4, INT8 and FP8 Matmuls, Measured", Step 2;
     x bfloat16 [K]; y bfloat16 [N]; w_hat = e2m1(q) * e4m3(scale) * tensor_scale.
   * MXFP4A16 ("Low-Precision Kernels ...", Step 6): codes as NVFP4; scales uint8 [N, K/32]
     (E8M0 bits); w_hat = e2m1(q) * 2^(scale - 127).
+  * KV4, a paged key/value cache in 4 bits: uint8 [pages, kv_heads, page_size / 16, record] as
+    ``kv4_cache`` allocates it (see include/w4a16.h), a page table int32 [batch, width], lengths
+    int32 [batch] and the packed new tokens' offsets ``starts`` int32 [batch + 1].
 """
 from __future__ import annotations
 
@@ -47,17 +50,25 @@ __all__ = [
     "testing_set_prepared_min_m", "testing_set_prepared_max_m",
     "w4a16_matmul_prepared_uses_prepared", "testing_set_fp4_variant",
     "fp4_matmul_workspace_bytes", "nvfp4_matmul", "mxfp4_matmul", "testing_set_w8_variant",
+    "kv4_cache", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_workspace_bytes",
+    "kv4_evict",
 ]
 
 STATUS_NAMES = {0: "W4A16_OK", 1: "W4A16_ERR_INVALID_ARG", 2: "W4A16_ERR_UNSUPPORTED",
                 3: "W4A16_ERR_MISALIGNED", 4: "W4A16_ERR_CUDA", 5: "W4A16_ERR_TIMEOUT",
-                6: "W4A16_ERR_WORKSPACE", 7: "W4A16_ERR_LAYOUT"}
+                6: "W4A16_ERR_WORKSPACE", 7: "W4A16_ERR_LAYOUT", 8: "W4A16_ERR_INDEX"}
 
 
 class W4A16Error(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} failed: {STATUS_NAMES.get(status, status)}")
         self.status = status
+
+
+class _Kv4Cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+    _fields_ += [(n, ctypes.c_int32) for n in ("pages", "kv_heads", "head_dim", "group",
+                                               "page_size", "batch", "table_width")]
 
 
 def library_path() -> str:
@@ -71,6 +82,7 @@ def _load():
             "`python -m gemv_w4a16_group_gb300.build` on a machine with nvcc")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, S, U32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint32
+    L, F, C = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(_Kv4Cache)
     sigs = {
         "w4a16_quantize": [P, I, I, I, P, P, P, P],
         "w4a16_pack": [P, I, I, P, P],
@@ -94,6 +106,10 @@ def _load():
         "mxfp4_matmul": [P, P, P, P, I, I, I, P, S, P],
         "w4a16_prepare": [P, P, P, I, I, I, P, S, P],
         "w4a16_matmul_prepared": [P, P, P, P, P, P, I, I, I, I, P, S, P],
+        "kv4_append": [C, P, P, L, P, L, I, P, I, P],
+        "kv4_read": [C, P, P, P, I, P],
+        "kv4_attention": [C, P, P, L, P, P, I, I, I, I, F, P, P, I, P, S, P],
+        "kv4_evict": [C, P, I, P, I, I, I, I, I, P, P, P, I, P],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -106,6 +122,10 @@ def _load():
     lib.w4a16_prepared_bytes.restype = S
     lib.fp4_matmul_workspace_bytes.argtypes = [I, I]
     lib.fp4_matmul_workspace_bytes.restype = S
+    lib.kv4_cache_bytes.argtypes = [I, I, I, I, I]
+    lib.kv4_cache_bytes.restype = S
+    lib.kv4_attention_workspace_bytes.argtypes = [I] * 9
+    lib.kv4_attention_workspace_bytes.restype = S
     lib.w4a16_status_string.argtypes = [I]
     lib.w4a16_status_string.restype = ctypes.c_char_p
     for name in ("w4a16_testing_force_kernel", "w4a16_testing_set_gemv_max_m",
@@ -600,3 +620,153 @@ def testing_set_fp4_variant(v: int) -> int:
     """Kernel of nvfp4_gemv / mxfp4_gemv: 1 = tensor-pipe ring (default), 0 = plain loads;
     other values only query. Returns the previous value."""
     return int(_lib.w4a16_testing_set_fp4_variant(v))
+
+
+def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, group: int = 64,
+              device="cuda") -> torch.Tensor:
+    """A 4-bit key/value cache: uint8 [pages, kv_heads, page_size / 16, record], not filled."""
+    nbytes = int(_lib.kv4_cache_bytes(pages, kv_heads, head_dim, group, page_size))
+    if nbytes == 0:
+        raise W4A16Error("kv4_cache", 2)
+    return torch.empty((pages, kv_heads, page_size // 16, 16 * (head_dim + 8 * (head_dim // group))),
+                       dtype=torch.uint8, device=device)
+
+
+def _kv4(cache, table, lens, head_dim: int, group: int):
+    if cache.dim() != 4 or table.dim() != 2:
+        raise ValueError("cache must have 4 dims (see kv4_cache) and table 2")
+    pages, kv_heads, records, nbytes = cache.shape
+    if group > 0 and nbytes != 16 * (head_dim + 8 * (head_dim // group)):
+        raise ValueError(f"cache has records of {nbytes} bytes, not those of head_dim {head_dim} "
+                         f"in groups of {group}")
+    batch, width = table.shape
+    return _Kv4Cache(_dev(cache, "cache", torch.uint8), _dev(table, "table", torch.int32),
+                     _dev(lens, "lens", torch.int32, (batch,)), pages, kv_heads, head_dim, group,
+                     16 * records, batch, width)
+
+
+def _tokens(t: torch.Tensor, name: str):
+    """[tokens, heads, head_dim] whose heads are dense; the tokens may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with dense heads")
+    dense = t.shape[1] * t.shape[2]
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else dense)
+
+
+def _kv4_weights(t, name: str, batch: int, kv_heads: int):
+    if t is None:
+        return None, 0
+    if t.dim() != 3 or tuple(t.shape[:2]) != (batch, kv_heads):
+        raise ValueError(f"{name} must be [{batch}, {kv_heads}, length]")
+    return _dev(t, name, torch.float32), t.shape[2]
+
+
+def kv4_append(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+               starts: torch.Tensor, k: torch.Tensor, v: torch.Tensor, group: int = 64,
+               weights=None, stream=None) -> torch.Tensor:
+    """Quantizes k and v (bf16 [tokens, kv_heads, head_dim], tokens may be strided) into the
+    cache. ``lens`` counts the new tokens, ``starts`` int32 [batch + 1] are their offsets; the
+    entries of the new tokens in ``weights`` (fp32 [batch, kv_heads, length]) become 0."""
+    c = _kv4(cache, table, lens, k.shape[-1], group)
+    kp, ks = _tokens(k, "k")
+    vp, vs = _tokens(v, "v")
+    if k.shape != v.shape or k.shape[1] != c.kv_heads:
+        raise ValueError("k and v must have the same shape and the cache's heads")
+    wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
+    _check("kv4_append", _lib.kv4_append(
+        c, _dev(starts, "starts", torch.int32, (c.batch + 1,)), kp, ks, vp, vs, k.shape[0], wp,
+        wl, _stream(stream)))
+    return cache
+
+
+def kv4_read(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor,
+             tokens: int, head_dim: int, group: int = 64, k=None, v=None, stream=None):
+    """(k, v) bf16 [tokens, kv_heads, head_dim]: the last starts[b + 1] - starts[b] tokens of
+    each sequence as the cache holds them."""
+    c = _kv4(cache, table, lens, head_dim, group)
+    shape = (tokens, c.kv_heads, head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    _check("kv4_read", _lib.kv4_read(
+        c, _dev(starts, "starts", torch.int32, (c.batch + 1,)),
+        _dev(k, "k", torch.bfloat16, shape), _dev(v, "v", torch.bfloat16, shape), tokens,
+        _stream(stream)))
+    return k, v
+
+
+def kv4_attention_workspace_bytes(batch: int, tokens: int, max_new: int, max_len: int, heads: int,
+                                  kv_heads: int, head_dim: int, group: int = 64,
+                                  with_weights: bool = False) -> int:
+    return int(_lib.kv4_attention_workspace_bytes(batch, tokens, max_new, max_len, heads, kv_heads,
+                                                  head_dim, group, int(with_weights)))
+
+
+def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                  starts: torch.Tensor, max_len: int, max_new: int, group: int = 64, scale=None,
+                  out=None, lse=None, weights=None, weights_out=None, workspace=None,
+                  stream=None) -> torch.Tensor:
+    """out bf16 [tokens, heads, head_dim]: causal attention of q (bf16 [tokens, heads, head_dim],
+    tokens may be strided), the last tokens of each sequence, over the cache. ``max_len`` and
+    ``max_new`` bound the lengths and new tokens of a sequence; scale defaults to
+    head_dim ** -0.5. ``lse`` (fp32 [tokens, heads]) receives ln sum exp; ``weights_out`` (fp32
+    [batch, kv_heads, length]) ``weights`` (or 0) plus the attention weight of each cached token.
+    Without a ``workspace`` (kv4_attention_workspace_bytes, zero-filled once) one is allocated
+    and zero-filled for the call."""
+    T, heads, head_dim = q.shape
+    c = _kv4(cache, table, lens, head_dim, group)
+    qp, qs = _tokens(q, "q")
+    on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_stream(q.device)
+    if workspace is None:
+        with torch.cuda.stream(on):
+            workspace = torch.zeros(kv4_attention_workspace_bytes(
+                c.batch, T, max_new, max_len, heads, c.kv_heads, head_dim, group,
+                weights_out is not None), dtype=torch.uint8, device=q.device)
+    if out is None:
+        with torch.cuda.stream(on):
+            out = torch.empty((T, heads, head_dim), dtype=torch.bfloat16, device=q.device)
+    wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
+    op, ol = _kv4_weights(weights_out, "weights_out", c.batch, c.kv_heads)
+    if weights is not None and wl != ol:
+        raise ValueError("weights and weights_out must have the same shape")
+    lp = None if lse is None else _dev(lse, "lse", torch.float32, (T, heads))
+    ws_ptr, ws_bytes = _workspace(workspace)
+    _check("kv4_attention", _lib.kv4_attention(
+        c, _dev(starts, "starts", torch.int32, (c.batch + 1,)), qp, qs,
+        _dev(out, "out", torch.bfloat16, (T, heads, head_dim)), lp, T, heads, max_new, max_len,
+        head_dim ** -0.5 if scale is None else scale, wp, op, ol, ws_ptr, ws_bytes,
+        _stream(stream)))
+    return out
+
+
+def kv4_evict(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor,
+              out_table: torch.Tensor, budget: int, max_len: int, head_dim: int, first: int = 0,
+              recent: int = 0, group: int = 64, kept=None, new_lens=None, weights_out=None,
+              stream=None):
+    """(kept int32 [batch, kv_heads, budget], new_lens int32 [batch], weights_out fp32
+    [batch, kv_heads, >= budget]): the first, the last ``recent`` and the heaviest other tokens of
+    each head move to the pages of ``out_table``."""
+    c = _kv4(cache, table, lens, head_dim, group)
+    wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
+    if kept is None:
+        kept = torch.empty((c.batch, c.kv_heads, budget), dtype=torch.int32, device=cache.device)
+    if new_lens is None:
+        new_lens = torch.empty((c.batch,), dtype=torch.int32, device=cache.device)
+    if weights_out is None:
+        weights_out = torch.empty((c.batch, c.kv_heads, budget), dtype=torch.float32,
+                                  device=cache.device)
+    op, ol = _kv4_weights(weights_out, "weights_out", c.batch, c.kv_heads)
+    if out_table.dim() != 2 or out_table.shape[0] != c.batch:
+        raise ValueError("out_table must be [batch, width]")
+    _check("kv4_evict", _lib.kv4_evict(
+        c, _dev(out_table, "out_table", torch.int32), out_table.shape[1], wp, wl, budget, first,
+        recent, max_len, _dev(kept, "kept", torch.int32, (c.batch, c.kv_heads, budget)),
+        _dev(new_lens, "new_lens", torch.int32, (c.batch,)), op, ol, _stream(stream)))
+    return kept, new_lens, weights_out

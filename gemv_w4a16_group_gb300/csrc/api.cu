@@ -114,6 +114,7 @@ const char* w4a16_status_string(w4a16_status status) {
     case W4A16_ERR_TIMEOUT: return "W4A16_ERR_TIMEOUT";
     case W4A16_ERR_WORKSPACE: return "W4A16_ERR_WORKSPACE";
     case W4A16_ERR_LAYOUT: return "W4A16_ERR_LAYOUT";
+    case W4A16_ERR_INDEX: return "W4A16_ERR_INDEX";
   }
   return "W4A16_ERR_UNKNOWN";
 }
@@ -532,7 +533,8 @@ w4a16_status w4a16_device_status(w4a16_stream_t stream) {
       return W4A16_ERR_CUDA;
   }
   if (word & w4k::kStatusTimeout) return W4A16_ERR_TIMEOUT;
-  return (word & w4k::kStatusLayout) ? W4A16_ERR_LAYOUT : W4A16_OK;
+  if (word & w4k::kStatusLayout) return W4A16_ERR_LAYOUT;
+  return (word & w4k::kStatusIndex) ? W4A16_ERR_INDEX : W4A16_OK;
 }
 
 w4a16_status w4a16_selftest_bounded_wait(uint32_t limit_us, w4a16_stream_t stream) {

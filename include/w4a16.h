@@ -54,8 +54,10 @@ typedef enum {
   W4A16_ERR_CUDA = 4,        /* a CUDA runtime call or launch failed            */
   W4A16_ERR_TIMEOUT = 5,     /* a kernel's bounded wait expired (device status) */
   W4A16_ERR_WORKSPACE = 6,   /* workspace pointer/size does not meet the query  */
-  W4A16_ERR_LAYOUT = 7       /* a kernel found its shared memory misaligned and
+  W4A16_ERR_LAYOUT = 7,      /* a kernel found its shared memory misaligned and
                                 skipped its work (device status)                  */
+  W4A16_ERR_INDEX = 8        /* a kernel found a page number, length or offset out of
+                                its range and left those tokens out (device status) */
 } w4a16_status;
 
 /* Human-readable name of a status (static string, never NULL). */
@@ -384,11 +386,126 @@ w4a16_status mxfp4_matmul(const uint16_t* x, const uint8_t* codes, const uint8_t
                           size_t workspace_bytes, w4a16_stream_t stream);
 
 /*
+ * The 4-bit key/value cache: what a decoder on 4-bit weights needs beside its matrix products.
+ * (The pages stop at the linear layers; the value format is their group rule, "Low-Precision
+ * Kernels ...", Step 2, along the head dimension.)
+ *
+ * Values. Per token, head and group of `group` dims: BF16 scale s = bf16((max - min) / 15),
+ * BF16 minimum m = bf16(min), codes q = clamp(rint((x - m) / s), 0, 15) in fp32 (0 where s is 0);
+ * the cache stands for x_hat = q s + m. 4 + 32 / group bits a value.
+ *
+ * Pages. `data` is [pages, kv_heads, page_size / 16, record] bytes; a record holds 16 tokens of
+ * a head in 16 (head_dim + 8 head_dim / group) bytes. With NG = head_dim / group, NB =
+ * head_dim / 32, t the token in the record, and 32-bit words:
+ *   K codes   from byte 0:        word t 4 NB + c NB + s (c < 4, s < NB) holds dims 32 s + 8 c + e,
+ *                                 e = 0..7, in bits 4 (e / 2) + 16 (e % 2)
+ *   K params  from 8 head_dim:    word 16 g + t holds group g's scale (low half) and minimum
+ *   V codes   from 8 head_dim + 64 NG: word ((t / 2) 8 + r) NB + b (r < 8, b < NB) holds, in half
+ *                                 t % 2, dims 32 b + 4 r + i, i = 0..3, in bits 4 i
+ *   V params  from 16 head_dim + 64 NG: as K's
+ * Token p of sequence b lies in page table[b, p / page_size]. Entries past a sequence's length
+ * are not read. Sequences may share pages that nothing is appended to. Stale bytes (tokens past a
+ * length) may hold anything.
+ *
+ * Tokens of a batch are packed: sequence b has the rows starts[b] .. starts[b + 1] - 1 of k, v, q
+ * and out, and they are its last ones: row i of m stands at position lens[b] - m + i. So one
+ * `lens`, already raised by the new tokens, serves a step's append and its attention.
+ *
+ * lens, starts, table, new lengths and kept indices are int32, weights fp32 (4-byte alignment is
+ * enough for these). A page number, length or offset outside the arrays is never followed: the
+ * tokens are left out (an attention row then is that of the tokens that remain), and
+ * w4a16_device_status() returns W4A16_ERR_INDEX.
+ *
+ * head_dim 64 or 128; group 32, 64 or 128, at most head_dim; page_size a power of two from 16 to
+ * 2^20; table_width * page_size at most 2^30; W4A16_ERR_UNSUPPORTED otherwise.
+ */
+typedef struct {
+  void* data;             /* kv4_cache_bytes(pages, kv_heads, head_dim, group, page_size) bytes */
+  const int32_t* table;   /* [batch, table_width]                                               */
+  const int32_t* lens;    /* [batch]                                                            */
+  int32_t pages, kv_heads, head_dim, group, page_size;
+  int32_t batch, table_width;
+} kv4_cache;
+
+/* Bytes of a cache; 0 for a shape that is not supported. */
+size_t kv4_cache_bytes(int pages, int kv_heads, int head_dim, int group, int page_size);
+
+/*
+ * kv4_append -- quantizes the new tokens' keys and values into the cache.
+ *   k, v    bf16 [tokens, kv_heads, head_dim], finite, k_stride and v_stride elements between
+ *           tokens (a multiple of 8, at least kv_heads * head_dim: slices of a fused projection)
+ *   weights fp32 [batch, kv_heads, weights_stride] or NULL: the new tokens' entries become 0
+ *           (weights_stride >= table_width * page_size)
+ * No other token of a record that is written changes.
+ */
+w4a16_status kv4_append(const kv4_cache* cache, const int32_t* starts, const uint16_t* k,
+                        int64_t k_stride, const uint16_t* v, int64_t v_stride, int tokens,
+                        float* weights, int weights_stride, w4a16_stream_t stream);
+
+/*
+ * kv4_read -- the last starts[b + 1] - starts[b] tokens of each sequence in BF16:
+ *   k, v  bf16 [tokens, kv_heads, head_dim] = bf16(q s + m). Rows that the cache does not hold
+ *   become 0.
+ */
+w4a16_status kv4_read(const kv4_cache* cache, const int32_t* starts, uint16_t* k, uint16_t* v,
+                      int tokens, w4a16_stream_t stream);
+
+/*
+ * kv4_attention -- causal attention of the new tokens over the cache (they are in it already):
+ *   out[i, h] = sum_j p_ij v_hat_j,  p_ij = softmax over j <= lens - m + i of scale q_i . k_hat_j
+ *   q       bf16 [tokens, heads, head_dim], q_stride elements between tokens (a multiple of 8);
+ *           heads is a multiple of kv_heads, query head h reads key/value head
+ *           h / (heads / kv_heads)
+ *   out     bf16 [tokens, heads, head_dim]
+ *   lse     fp32 [tokens, heads] or NULL: ln sum_j exp(s_ij)
+ *   weights, weights_out  fp32 [batch, kv_heads, weights_stride] (weights_stride >= max_len), or
+ *           weights_out NULL: weights_out[b, g, j] = weights[b, g, j] + the sum of p_ij over the
+ *           new tokens and the query heads of g, for j < lens[b]; other entries are not touched.
+ *           weights NULL stands for zeros; the two may be the same array.
+ *   max_new, max_len  upper bounds, known on the host, of a sequence's new tokens and length; they
+ *           size the launch, while the work is that of the real lengths.
+ * A row that sees no token (an empty sequence) gives out = 0 and lse = -inf. Tokens that a row
+ * does not see do not touch it, whatever they hold. Sums, the softmax's maxima and sums, lse and
+ * weights are fp32; codes and probabilities meet as BF16 products with fp32 sums. Results do not
+ * depend on timing (no floating-point atomics).
+ * Workspace: kv4_attention_workspace_bytes() bytes, 16-byte aligned, zero-filled before its first
+ * use (the kernels leave its counters zero) and not shared by calls that may run concurrently;
+ * W4A16_ERR_WORKSPACE if NULL or smaller. Calls of other shapes may use the same buffer only
+ * after it has been zero-filled again.
+ */
+size_t kv4_attention_workspace_bytes(int batch, int tokens, int max_new, int max_len, int heads,
+                                     int kv_heads, int head_dim, int group, int with_weights);
+w4a16_status kv4_attention(const kv4_cache* cache, const int32_t* starts, const uint16_t* q,
+                           int64_t q_stride, uint16_t* out, float* lse, int tokens, int heads,
+                           int max_new, int max_len, float scale, const float* weights,
+                           float* weights_out, int weights_stride, void* workspace,
+                           size_t workspace_bytes, w4a16_stream_t stream);
+
+/*
+ * kv4_evict -- keeps `budget` tokens of each head of each sequence: the first `first`, the last
+ * `recent` and, of the others, those with the largest weights (ties: the lower index; NaN counts
+ * as the lowest). They move, in their order, to the pages of out_table.
+ *   out_table    int32 [batch, out_width]: pages of the same cache that no sequence of this call
+ *                reads, out_width * page_size >= budget
+ *   weights      fp32 [batch, kv_heads, weights_stride], weights_stride >= max_len >= lens
+ *   kept         int32 [batch, kv_heads, budget]: old positions, ascending, -1 past new_lens
+ *   new_lens     int32 [batch]: min(lens, budget); not the array cache->lens
+ *   weights_out  fp32 [batch, kv_heads, weights_out_stride] (>= budget): the kept tokens' weights
+ * The old pages stay as they were: they may be shared, and heads keep different tokens of them.
+ * first + recent <= budget.
+ */
+w4a16_status kv4_evict(const kv4_cache* cache, const int32_t* out_table, int out_width,
+                       const float* weights, int weights_stride, int budget, int first,
+                       int recent, int max_len, int32_t* kept, int32_t* new_lens,
+                       float* weights_out, int weights_out_stride, w4a16_stream_t stream);
+
+/*
  * w4a16_device_status -- synchronizes `stream`, then reads and clears the current
  * device's status word. Returns W4A16_ERR_TIMEOUT if any kernel of this library gave
  * up a bounded wait since the last query, W4A16_ERR_LAYOUT if a kernel found its
  * dynamic shared memory less than 128-byte aligned and skipped its work (its output is
- * then not written), W4A16_ERR_CUDA if the synchronization failed, W4A16_OK otherwise.
+ * then not written), W4A16_ERR_INDEX if a kernel met a page number, a length or an offset
+ * outside the arrays it was given and left those tokens out, W4A16_ERR_CUDA if the synchronization failed, W4A16_OK otherwise.
  * (The pages have no counterpart; this is the library's failure-detection hook.)
  */
 w4a16_status w4a16_device_status(w4a16_stream_t stream);

@@ -1,0 +1,400 @@
+"""The 4-bit key/value cache on the GPU against tests/kv4_reference.py (64-bit sums).
+
+Append, read and eviction are exact. Attention's bound, per output, before any run:
+  * out is rounded to BF16: 2^-9 |out|; p scale (or v_hat) and p are rounded to BF16: 2^-9 each of
+    a term, at most 2^-8 of reach = sum p (|v - min| + |min|);
+  * k_hat may be rounded to BF16: a logit moves by at most E = 2^-9 span, span the row's largest
+    sum |q k| scale, so a probability by a factor within e^(+-2E): (e^2E - 1) reach;
+  * fp32 sums add about 1e-6 of the same terms each: 2^-14 covers them (the 128 that the codes
+    carry costs up to seven bits of a sum).
+lse moves by at most E, a token's weight by (e^2E - 1) of itself."""
+import numpy as np
+import pytest
+import torch
+
+import kv4_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+w4 = pytest.importorskip("gemv_w4a16_group_gb300") if torch.cuda.is_available() else None
+DEV = "cuda"
+SHAPES = [(128, 64, 64), (128, 128, 16), (128, 32, 32), (64, 64, 16), (64, 32, 128)]
+
+
+def _starts(new):
+    return np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+
+
+def _tables(lens, page, extra, seed, spare=2):
+    """A shuffled page table wide enough for lens, -1 where nothing may be read."""
+    g = np.random.default_rng(seed)
+    need = [(n + page - 1) // page for n in lens]
+    order = g.permutation(sum(need) + spare + extra).astype(np.int32)
+    table = np.full((len(lens), max(max(need), 1) + 1), -1, dtype=np.int32)
+    at = 0
+    for b, k in enumerate(need):
+        table[b, :k] = order[at:at + k]
+        at += k
+    return table, order, at
+
+
+def _fill(lens, H, D, group, page, seed, extra=0, stale=0xFF):
+    """A cache with every token of lens in it; all other bytes are `stale` (0xFF: NaN
+    parameters)."""
+    g = np.random.default_rng(seed)
+    table, order, at = _tables(lens, page, extra, seed)
+    data = np.full((len(order), H, page // 16, ref.record_bytes(D, group)), stale, dtype=np.uint8)
+    cache = ref.Cache(data, table, D, group)
+    chan = np.where(g.random((H, D)) < 0.05, 4.0, 1.0)
+    for b, n in enumerate(lens):
+        k = ref.bf16(g.standard_normal((n, H, D)) * chan)
+        v = ref.bf16(g.standard_normal((n, H, D)))
+        kq, ks, km = ref.quantize(k, group)
+        vq, vs, vm = ref.quantize(v, group)
+        for h in range(H):
+            cache.put(b, h, np.arange(n), *(x[:, h] for x in (kq, ks, km, vq, vs, vm)))
+    return cache, order, at
+
+
+def _gpu(x, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(x))
+    return t.to(dtype).to(DEV) if dtype else t.to(DEV)
+
+
+def _ok():
+    assert w4.w4a16_device_status() == 0
+
+
+@pytest.mark.parametrize("D,group,page", SHAPES)
+@pytest.mark.parametrize("lens,new", [([1], [1]), ([19, 40, 5, 16], [3, 40, 1, 0]),
+                                      ([33, 64, 47], [32, 17, 1])])
+def test_append_and_read_are_exact(D, group, page, lens, new):
+    H, seed = 3, 5
+    g = np.random.default_rng(seed)
+    cache, _, _ = _fill(lens, H, D, group, page, seed, stale=0x5A)
+    starts, T = _starts(new), sum(new)
+    x = ref.bf16(g.standard_normal((T, 2 * H + 1, D)) * 3)
+    x[0, 0, :] = 1.5                       # a constant group: scale 0
+    x[T // 2, H, :32] = np.linspace(-8, 7, 32)
+    k, v = x[:, :H], x[:, H + 1:]
+    gd = _gpu(cache.data)
+    lens_t, table = _gpu(np.array(lens, np.int32)), _gpu(cache.table)
+    fused = _gpu(x, torch.bfloat16)
+    weights = torch.ones(len(lens), H, table.shape[1] * page, device=DEV)
+    w4.kv4_append(gd, table, lens_t, _gpu(starts), fused[:, :H], fused[:, H + 1:], group=group,
+                  weights=weights)
+    kq, ks, km = ref.quantize(k, group)
+    vq, vs, vm = ref.quantize(v, group)
+    want_w = np.ones(weights.shape, np.float32)
+    for b, n in enumerate(lens):
+        m = new[b]
+        want_w[b, :, n - m:n] = 0
+        for i in range(m):
+            for h in range(H):
+                t = starts[b] + i
+                cache.put(b, h, n - m + i, kq[t, h], ks[t, h], km[t, h], vq[t, h], vs[t, h],
+                          vm[t, h])
+    assert np.array_equal(gd.cpu().numpy(), cache.data)
+    assert np.array_equal(weights.cpu().numpy(), want_w)
+    k2, v2 = w4.kv4_read(gd, table, lens_t, _gpu(starts), T, D, group=group)
+    for got, q, s, m in ((k2, kq, ks, km), (v2, vq, vs, vm)):
+        assert np.array_equal(got.float().cpu().numpy(), ref.bf16(ref.dequantize(q, s, m, group)))
+    _ok()
+
+
+def _check_attention(cache, lens, new, heads, H, seed, scale=None, hide=None, weights=True,
+                     max_len=None, max_new=None):
+    g = np.random.default_rng(seed + 100)
+    D, group = cache.D, cache.group
+    starts, T = _starts(new), sum(new)
+    scale = D ** -0.5 if scale is None else scale
+    q = ref.bf16(g.standard_normal((T, heads, D)))
+    out, lse, w, reach, span = ref.attention(q, cache, lens, starts, heads, H, scale)
+    width = cache.table.shape[1] * cache.page
+    max_len = max(max(lens), 1) if max_len is None else max_len
+    max_new = max(new) if max_new is None else max_new
+    before = g.random((len(lens), H, width)).astype(np.float32)
+    w_out = torch.full(before.shape, 7.0, device=DEV) if weights else None
+    lse_t = torch.empty(T, heads, device=DEV)
+    qf = torch.zeros(T, heads + 1, D, dtype=torch.bfloat16, device=DEV)
+    qf[:, 1:] = _gpu(q, torch.bfloat16)
+    got = w4.kv4_attention(
+        qf[:, 1:], _gpu(cache.data), _gpu(cache.table), _gpu(np.array(lens, np.int32)),
+        _gpu(starts), max_len, max_new, group=group, scale=scale, lse=lse_t,
+        weights=_gpu(before) if weights else None, weights_out=w_out)
+    _ok()
+    got, lse_g = got.double().cpu().numpy(), lse_t.double().cpu().numpy()
+    E = 2.0 ** -9 * span
+    grow = np.expm1(2 * E)
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2.0 ** -14 + grow[..., None]) * reach
+    err = np.abs(got - out)
+    assert (err <= tol).all(), (err - tol).max()
+    # on average the roundings are far from their bounds
+    assert np.sqrt((err ** 2).mean()) <= 2.0 ** -8 * np.sqrt((reach ** 2).mean()) + 1e-30
+    empty = np.isinf(lse)
+    assert np.array_equal(np.isneginf(lse_g), empty)
+    assert (got[empty] == 0).all()
+    assert (np.abs(lse_g[~empty] - lse[~empty]) <= (E + 2.0 ** -14 * (1 + span))[~empty]).all()
+    if weights:
+        w_g = w_out.double().cpu().numpy()
+        n_max = w.shape[2]
+        for b, n in enumerate(lens):
+            assert (w_g[b, :, n:] == 7.0).all()
+            rows = slice(starts[b], starts[b + 1])
+            gb = (grow[rows].max() if new[b] else 0.0) + 2.0 ** -12
+            d = np.abs(w_g[b, :, :n] - before[b, :, :n] - w[b, :, :n])
+            assert (d <= gb * w[b, :, :n] + 1e-6).all(), d.max()
+        assert n_max
+    return got
+
+
+@pytest.mark.parametrize("D,group,page", SHAPES)
+@pytest.mark.parametrize("heads,H", [(4, 1), (6, 2), (2, 2), (9, 1)])
+@pytest.mark.parametrize("lens", [[1], [17, 0, 64, 129], [700, 3]])
+def test_decode(D, group, page, heads, H, lens):
+    cache, _, _ = _fill(lens, H, D, group, page, 3)
+    _check_attention(cache, lens, [1] * len(lens), heads, H, 3)
+
+
+@pytest.mark.parametrize("D,group,page", SHAPES)
+@pytest.mark.parametrize("heads,H,lens,new", [
+    (4, 2, [5, 70, 40], [5, 3, 0]), (8, 1, [200, 31], [4, 9]), (3, 1, [3, 90], [5, 40]),
+    (4, 1, [150], [150]), (12, 2, [260, 66], [130, 1])])
+def test_several_new_tokens(D, group, page, heads, H, lens, new):
+    cache, _, _ = _fill(lens, H, D, group, page, 4)
+    _check_attention(cache, lens, new, heads, H, 4)
+
+
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+def test_long_sequence_is_split(D, group):
+    lens = [5000, 1, 2047]
+    cache, _, _ = _fill(lens, 1, D, group, 256, 6)
+    _check_attention(cache, lens, [1, 1, 2], 4, 1, 6)
+
+
+@pytest.mark.parametrize("new", [[1], [3], [90]])
+def test_bounds_larger_than_the_lengths(new):
+    lens = [100]
+    cache, _, _ = _fill(lens, 2, 128, 64, 64, 7)
+    _check_attention(cache, lens, new, 4, 2, 7, max_len=128)
+
+
+def test_large_logits():
+    lens, new = [300, 80], [2, 70]
+    cache, _, _ = _fill(lens, 2, 128, 64, 16, 8)
+    _check_attention(cache, lens, new, 4, 2, 8, scale=0.5)
+    _check_attention(cache, lens, new, 4, 2, 8, scale=-0.25)
+
+
+@pytest.mark.parametrize("new", [4, 40])
+def test_hidden_tokens_do_not_matter(new):
+    """Tokens behind a row's position hold infinities and NaN: rows before them are untouched."""
+    D, group, n, H = 128, 64, 80, 2
+    cache, _, _ = _fill([n], H, D, group, 16, 9)
+    bad = np.full(D // group, np.nan), np.full(D // group, np.inf)
+    ones = np.full(D, 15)
+    for h in range(H):
+        cache.put(0, h, n - 1, ones, bad[0], bad[1], ones, bad[1], bad[0])
+    q = torch.randn(new, 4, D, device=DEV).bfloat16()
+    args = (_gpu(cache.table), _gpu(np.array([n], np.int32)), _gpu(_starts([new])))
+    got = w4.kv4_attention(q, _gpu(cache.data), *args, n, new, group=group)
+    lens1, starts1 = _gpu(np.array([n - 1], np.int32)), _gpu(_starts([new - 1]))
+    want = w4.kv4_attention(q[:-1], _gpu(cache.data), args[0], lens1, starts1, n, new - 1,
+                            group=group)
+    assert torch.isfinite(got[:-1].float()).all()
+    assert (got[:-1].float() - want.float()).abs().max() <= 2.0 ** -6
+    _ok()
+
+
+@pytest.mark.parametrize("new", [1, 33])
+def test_repeats_are_equal_and_streams_are_kept(new):
+    lens = [1000, 333]
+    cache, _, _ = _fill(lens, 2, 128, 64, 64, 10)
+    T = 2 * new
+    q = torch.randn(T, 4, 128, device=DEV).bfloat16()
+    data, table = _gpu(cache.data), _gpu(cache.table)
+    lens_t, starts = _gpu(np.array(lens, np.int32)), _gpu(_starts([new, new]))
+    ws = torch.zeros(w4.kv4_attention_workspace_bytes(2, T, new, 1000, 4, 2, 128, 64, True),
+                     dtype=torch.uint8, device=DEV)
+    shape = (2, 2, table.shape[1] * 64)
+    w = torch.zeros(shape, device=DEV)
+
+    def call(stream=None):
+        o = torch.zeros(shape, device=DEV)
+        r = w4.kv4_attention(q, data, table, lens_t, starts, 1000, new, weights=w, weights_out=o,
+                             workspace=ws, stream=stream)
+        return r, o
+
+    first = call()
+    for _ in range(3):
+        again = call()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = call()
+        graph = torch.cuda.CUDAGraph()
+        out = torch.zeros_like(first[0])
+        wo = torch.zeros(shape, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            w4.kv4_attention(q, data, table, lens_t, starts, 1000, new, out=out, weights=w,
+                             weights_out=wo, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(first[0], other[0]) and torch.equal(first[1], other[1])
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(first[0], out) and torch.equal(first[1], wo)
+    _ok()
+
+
+def test_weights_may_be_added_in_place():
+    lens = [130]
+    cache, _, _ = _fill(lens, 1, 64, 64, 16, 11)
+    q = torch.randn(1, 4, 64, device=DEV).bfloat16()
+    args = (q, _gpu(cache.data), _gpu(cache.table), _gpu(np.array(lens, np.int32)),
+            _gpu(_starts([1])), 130, 1)
+    one = torch.zeros(1, 1, 256, device=DEV)
+    w4.kv4_attention(*args, weights_out=one)
+    acc = torch.full_like(one, 2.0)
+    w4.kv4_attention(*args, weights=acc, weights_out=acc)
+    assert torch.equal(acc[..., :130], one[..., :130] + 2.0)
+    assert abs(one.sum().item() - 4.0) < 1e-3   # four heads' probabilities
+
+
+def test_offsets_past_32_bits():
+    """The pages in use lie past 4 GiB of a cache."""
+    D, group, page, H, lens = 128, 64, 64, 2, [100, 70]
+    cache, _, _ = _fill(lens, H, D, group, page, 12)
+    per_page = cache.data[0].size
+    shift = (1 << 32) // per_page + 5
+    big = torch.empty((shift + len(cache.data),) + cache.data.shape[1:], dtype=torch.uint8,
+                      device=DEV)
+    big[shift:] = _gpu(cache.data)
+    table = np.where(cache.table >= 0, cache.table + shift, -1).astype(np.int32)
+    q = torch.randn(41, 4, D, device=DEV).bfloat16()
+    lens_t, starts = _gpu(np.array(lens, np.int32)), _gpu(_starts([1, 40]))
+    for lo, hi, st in ((0, 41, starts), (0, 2, _gpu(_starts([1, 1])))):
+        a = w4.kv4_attention(q[lo:hi], _gpu(cache.data), _gpu(cache.table), lens_t, st, 100, 40
+                             if hi > 2 else 1)
+        b = w4.kv4_attention(q[lo:hi], big, _gpu(table), lens_t, st, 100, 40 if hi > 2 else 1)
+        assert torch.equal(a, b)
+    k = torch.randn(41, H, D, device=DEV).bfloat16()
+    small = _gpu(cache.data)
+    w4.kv4_append(small, _gpu(cache.table), lens_t, starts, k, k)
+    w4.kv4_append(big, _gpu(table), lens_t, starts, k, k)
+    assert torch.equal(big[shift:], small)
+    for x, y in zip(w4.kv4_read(small, _gpu(cache.table), lens_t, starts, 41, D),
+                    w4.kv4_read(big, _gpu(table), lens_t, starts, 41, D)):
+        assert torch.equal(x, y)
+    _ok()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_out_of_range_numbers_are_reported_not_followed(new):
+    D, group, page, n = 128, 64, 16, 100
+    cache, _, _ = _fill([n], 1, D, group, page, 13, stale=0)
+    q = torch.randn(new, 4, D, device=DEV).bfloat16()
+    starts = _gpu(_starts([new]))
+
+    def status_of(table, length, st=starts):
+        w4.kv4_attention(q, _gpu(cache.data), _gpu(table), _gpu(np.array([length], np.int32)), st,
+                         n, new)
+        return w4.w4a16_device_status()
+
+    for bad_page in (-1, len(cache.data), 1 << 30):
+        table = cache.table.copy()
+        table[0, 2] = bad_page
+        assert status_of(table, n) == 8
+    assert status_of(cache.table, n + 1) == 8            # longer than max_len
+    assert status_of(cache.table, -3) == 8
+    assert status_of(cache.table, n, _gpu(np.array([0, new + 7], np.int32))) == 8
+    k = torch.randn(new, 1, D, device=DEV).bfloat16()
+    data = _gpu(cache.data)
+    w4.kv4_append(data, _gpu(cache.table), _gpu(np.array([new - 1], np.int32)), starts, k, k)
+    assert w4.w4a16_device_status() == 8                 # the first token has no position
+    w4.kv4_read(data, _gpu(cache.table), _gpu(np.array([new - 1], np.int32)), starts, new, D)
+    assert w4.w4a16_device_status() == 8
+    assert status_of(cache.table, n) == 0
+
+
+@pytest.mark.parametrize("D,group,page", SHAPES)
+@pytest.mark.parametrize("lens,budget,first,recent", [
+    ([50, 16, 70], 33, 2, 7), ([2000, 40], 100, 0, 0), ([100], 64, 30, 34), ([40, 0], 1, 0, 1),
+    ([1100], 1030, 1, 2)])
+def test_evict(D, group, page, lens, budget, first, recent):
+    H, seed = 2, 14
+    out_width = (budget + page - 1) // page
+    cache, order, at = _fill(lens, H, D, group, page, seed, extra=len(lens) * out_width)
+    out_table = order[at:at + len(lens) * out_width].reshape(len(lens), out_width)
+    g = np.random.default_rng(seed)
+    width = cache.table.shape[1] * page
+    w = (g.random((len(lens), H, width)) ** 4).astype(np.float32)
+    w[:, 0] = np.round(w[:, 0] * 8) / 8          # many ties, exact zeros
+    w[0, 1, min(3, lens[0] - 1)] = np.nan
+    w[0, 1, min(5, lens[0] - 1)] = np.inf
+    kept = ref.evict(w, lens, budget, first, recent)
+    data = _gpu(cache.data)
+    got, new_lens, w_out = w4.kv4_evict(data, _gpu(cache.table), _gpu(np.array(lens, np.int32)),
+                                        _gpu(w), _gpu(out_table), budget, max(lens), D,
+                                        first=first, recent=recent, group=group)
+    _ok()
+    assert np.array_equal(got.cpu().numpy(), kept)
+    assert new_lens.tolist() == [min(n, budget) for n in lens]
+    w_out = w_out.cpu().numpy()
+    want = ref.Cache(cache.data.copy(), out_table, D, group)
+    for b, n in enumerate(lens):
+        for h in range(H):
+            m = min(n, budget)
+            assert np.array_equal(w_out[b, h, :m], w[b, h, kept[b, h, :m]], equal_nan=True)
+            k, v = cache.get(b, h, n)
+            moved = ref.Cache(data.cpu().numpy(), out_table, D, group)
+            k2, v2 = moved.get(b, h, m)
+            assert np.array_equal(k2, k[kept[b, h, :m]]) and np.array_equal(v2, v[kept[b, h, :m]])
+    after = data.cpu().numpy()
+    used = np.zeros(len(after), bool)
+    for b, n in enumerate(lens):
+        used[out_table[b, :(min(n, budget) + page - 1) // page]] = True
+    assert np.array_equal(after[~used], want.data[~used])
+
+
+def test_a_decoding_loop_with_eviction():
+    """Append, attend with weights, evict, go on: every step equals the reference on the same
+    cache bytes."""
+    D, group, page, H, heads, budget = 64, 32, 16, 2, 4, 24
+    g = np.random.default_rng(15)
+    lens, B = [30, 9], 2
+    cache, order, at = _fill([n + 20 for n in lens], H, D, group, page, 15, extra=2 * 2 * 2)
+    data, table = _gpu(cache.data), _gpu(cache.table)
+    spare = order[at:at + 8].reshape(2, 2, 2)
+    weights = torch.zeros(B, H, table.shape[1] * page, device=DEV)
+    starts = _gpu(_starts([1, 1]))
+    for step in range(6):
+        lens = [n + 1 for n in lens]
+        lens_t = _gpu(np.array(lens, np.int32))
+        kv = _gpu(ref.bf16(g.standard_normal((2, 2 * H, D))), torch.bfloat16)
+        w4.kv4_append(data, table, lens_t, starts, kv[:, :H], kv[:, H:], group=group,
+                      weights=weights)
+        q = ref.bf16(g.standard_normal((2, heads, D)))
+        before = weights.double().cpu().numpy()
+        out = w4.kv4_attention(_gpu(q, torch.bfloat16), data, table, lens_t, starts,
+                               table.shape[1] * page, 1, group=group, weights=weights,
+                               weights_out=weights)
+        now = ref.Cache(data.cpu().numpy(), table.cpu().numpy(), D, group)
+        want, _, w, reach, _ = ref.attention(q, now, lens, [0, 1, 2], heads, H, D ** -0.5)
+        assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -6 * reach).all()
+        got = weights.double().cpu().numpy()
+        for b, n in enumerate(lens):
+            assert np.allclose(got[b, :, :n], before[b, :, :n] + w[b, :, :n], rtol=1e-2, atol=1e-5)
+        if step in (2, 4):
+            kept, new_lens, w2 = w4.kv4_evict(
+                data, table, lens_t, weights, _gpu(spare[step // 2 - 1]), budget,
+                table.shape[1] * page, D, first=1, recent=4, group=group)
+            assert np.array_equal(kept.cpu().numpy(),
+                                  ref.evict(weights.cpu().numpy(), lens, budget, 1, 4))
+            wide = torch.zeros(B, H, 2 * page, device=DEV)
+            wide[..., :budget] = w2
+            weights, table = wide, _gpu(spare[step // 2 - 1])
+            lens = new_lens.tolist()
+    _ok()
