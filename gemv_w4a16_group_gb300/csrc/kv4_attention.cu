@@ -26,6 +26,7 @@
 // where they join (max, sum, accumulator) through shared memory. A segment that another CTA
 // shares goes to the workspace in fp32, and the CTA that arrives last joins the parts in order.
 #include "kv4_common.cuh"
+#include "kv4_prompt.h"
 
 namespace w4k {
 namespace {
@@ -183,7 +184,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 
   Cursor cur;
   int64_t seg_base = 0;  // first unit of the current segment
-  int seg_index = 0;     // its counter
   {
     int64_t before = 0;
     int b = 0;
@@ -750,15 +750,26 @@ cudaError_t by_rows(const Kv4AttentionArgs& a, cudaStream_t stream) {
   return rows <= 8 ? run<D, NG, 1>(a, stream) : run<D, NG, 2>(a, stream);
 }
 
+// Rows of a key/value head from which the prompts' path takes over.
+constexpr int64_t kPromptRows = 33;
+
+bool is_prompt(int max_new, int heads, int kv_heads) {
+  return static_cast<int64_t>(max_new) * (heads / kv_heads) >= kPromptRows;
+}
+
 }  // namespace
 
 size_t kv4_attention_workspace(int batch, int tokens, int max_new, int max_len, int heads,
                                int kv_heads, int head_dim, int group, bool weights) {
+  if (is_prompt(max_new, heads, kv_heads))
+    return kv4_prompt_workspace(batch, tokens, max_new, max_len, heads, kv_heads, head_dim, weights);
   return layout(batch, tokens, max_new, max_len, heads, kv_heads, head_dim, weights).total;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttentionArgs& a, int head_dim, int group,
                                  cudaStream_t stream) {
+  if (is_prompt(a.max_new, a.heads, a.c.kv_heads))
+    return launch_kv4_prompt(a, head_dim, group, stream);
   if (head_dim == 128)
     return group == 128 ? by_rows<128, 1>(a, stream)
            : group == 64 ? by_rows<128, 2>(a, stream) : by_rows<128, 4>(a, stream);

@@ -1,0 +1,1155 @@
+// Attention of prompts over the 4-bit key/value cache: the tensor-memory path, for more rows
+// (new token, query head) a key/value head than the few that kv4_attention.cu takes.
+//
+//   S = Q K_hat^T,  P = exp2(scale log2(e) S - m),  O = P V_hat,  out = O / rowsum(P)
+//
+// 4 D operations a visible (row, token) pair and one exponential: the tensor pipe bounds it, the
+// exponentials come close behind.
+//
+// 1. kv4_prompt_images_kernel writes the sequence's keys and values, and the queries, as FP16
+//    tiles in the swizzled order that tcgen05.mma reads: every later load is one contiguous bulk
+//    copy, and a code is widened once instead of once a row tile (a 4096-token prompt has 64 of
+//    them a head). Values come transposed, so that both products read K-major operands, rounded
+//    to FP16 under a power of two a tile (2^-12 of a value, an eighth of the output's rounding).
+//    A key is exact: with c the code less 8, c s has at most 3 + 8 significant bits and is an
+//    FP16 number; what is left, (min + 8 s) times the sum of q over the group, goes through 16
+//    more columns, four a group, as FP16 pairs of high and low parts. Rounded keys (2^-12) put
+//    3e-5 into the accumulated weights, which are fp32.
+// 2. kv4_prompt_kernel, one CTA an SM: 256 rows as two row halves of 128, each with a warpgroup
+//    that owns one row a thread (no shuffles), over tiles of 128 tokens in a ring of four bulk
+//    copies. One thread issues S = Q K^T (tensor memory, fp32) and O += P V with P read back from
+//    tensor memory, the halves in turn, so that one half's softmax runs under the other's
+//    products. The running maximum may lag by 2^8 before O is rescaled: P stays in FP16's range
+//    and the rescale is rare. The (sequence, head, 256-row tile) items, each as many units as it
+//    has visible token tiles, are cut into equal ranges of units, one a CTA; an item that a
+//    boundary cuts is joined from fp32 parts by whoever arrives last, in order.
+// 3. With weights, kv4_prompt_weights_kernel makes S^T = K_hat Q^T from the same tiles, a thread
+//    a token, and sums exp2(S - lse) along the row.
+#include "kv4_common.cuh"
+#include "kv4_prompt.h"
+
+namespace w4k {
+namespace {
+
+constexpr int kTileKeys = 128;
+constexpr int kTileRows = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct KeyMeta {
+  float kf;  // a key's image times this is the key
+  int ev;    // a value's image times 2^ev is the value
+};
+
+struct PromptWs {
+  int64_t* base;      // [batch + 1]: units before a sequence
+  int32_t* pre;       // [batch, row_tiles + 1]: units of a head before a row tile
+  KeyMeta* meta;      // [batch, kv_heads, key_tiles]
+  float* qf;          // [batch, kv_heads, row_tiles]: logit (base 2) per image product, without kf
+  uint8_t* q_img;     // [batch, kv_heads, row_tiles] x 256 (D + 16) FP16
+  uint8_t* kv_img;    // [batch, kv_heads, key_tiles] x (K 128 (D + 16), V^T D 128) FP16
+  uint32_t* counters; // [batch, kv_heads, row_tiles, 2], zero between calls
+  float* parts;       // [2 grid][2 halves] x (D + 2) 128
+  float* lse2;        // [tokens, heads], base 2
+  float* sums;        // [splits, batch, kv_heads, key_tiles 128]
+  int key_tiles, row_tiles, splits;
+};
+
+template <int D>
+struct Img {
+  static constexpr uint32_t kMore = 16 * 2;                      // bytes of the 16 more columns
+  static constexpr uint32_t kKCodes = kTileKeys * D * 2;         // one K tile without them
+  static constexpr uint32_t kTile = kKCodes + kTileKeys * kMore; // with them
+  static constexpr uint32_t kVTile = kTileKeys * D * 2;          // one V^T tile
+  static constexpr uint32_t kPair = kTile + kVTile;
+  static constexpr uint32_t kQCodes = kTileRows * D * 2;
+  static constexpr uint32_t kQ = kQCodes + kTileRows * kMore;
+};
+
+// Units (key tiles) of row tile rt.
+__device__ __forceinline__ int units_of(const Kv4Seq& s, int G, int rt) {
+  const int last = min((rt + 1) * kTileRows, s.m * G) - 1;
+  const int key = s.n - s.m + last / G;
+  return key < 0 ? 1 : key / kTileKeys + 1;
+}
+
+// ---- images ------------------------------------------------------------------------------
+constexpr int kImgThreads = 256;
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* sm) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = sm[0];
+#pragma unroll
+  for (int i = 1; i < kImgThreads / 32; ++i) v = max(v, sm[i]);
+  return v;
+}
+
+// Exponent that brings a largest magnitude (fp32 bits, finite) to [2^14, 2^15).
+__device__ __forceinline__ int up_of(uint32_t bits) {
+  const int ex = static_cast<int>(bits >> 23);
+  return ex == 0 ? 0 : min(max(141 - ex, -126), 126);
+}
+
+// Largest finite magnitude of a group's values, fp32 bits.
+__device__ __forceinline__ uint32_t reach_bits(uint32_t param) {
+  const float s = bf16_lo(param), m = bf16_hi(param);
+  const uint32_t a = __float_as_uint(fabsf(m)), b = __float_as_uint(fabsf(fmaf(15.f, s, m)));
+  return max(a >= 0x7F800000u ? 0u : a, b >= 0x7F800000u ? 0u : b);
+}
+
+// Three of the four more columns of a group: high and low FP16 parts of x.
+__device__ __forceinline__ uint32_t high_low(float x) {
+  const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+  return static_cast<uint32_t>(__half_as_ushort(hi)) |
+         (static_cast<uint32_t>(__half_as_ushort(lo)) << 16);
+}
+
+// 128 tokens of one head.
+template <int D, int NG>
+__device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, int h, int tile) {
+  using R = Kv4Record<D, NG>;
+  __shared__ const uint8_t* rec[8];
+  __shared__ uint32_t kp[8][16 * NG], vp[8][16 * NG];
+  __shared__ uint32_t red[2][kImgThreads / 32];
+  const int tid = threadIdx.x;
+  const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
+  const int key0 = tile * kTileKeys;
+  if (seq.m == 0 || key0 >= seq.n) return;
+  if (tid < 8)
+    rec[tid] = key0 + 16 * tid < seq.n ? kv4_record(a.c, a.c.table, a.c.width, b, h, key0 / 16 + tid,
+                                                    R::kBytes)
+                                       : nullptr;
+  __syncthreads();
+  uint32_t ktop = 0, vtop = 0;
+  for (int x = tid; x < 8 * 16 * NG; x += kImgThreads) {
+    const int j = x / (16 * NG), w = x % (16 * NG);
+    uint32_t k = 0, v = 0;  // tokens past the length become 0
+    if (rec[j] != nullptr && key0 + 16 * j + w % 16 < seq.n) {
+      k = reinterpret_cast<const uint32_t*>(rec[j] + R::kKParams)[w];
+      v = reinterpret_cast<const uint32_t*>(rec[j] + R::kVParams)[w];
+    }
+    kp[j][w] = k;
+    vp[j][w] = v;
+    ktop = max(ktop, reach_bits(k));
+    vtop = max(vtop, reach_bits(v));
+  }
+  ktop = block_max(ktop, red[0]);
+  vtop = block_max(vtop, red[1]);
+  // keys reach [2^7, 2^8): 128 times a minimum + 8 s still is an FP16 number
+  const int kup = max(up_of(ktop) - 7, -126), vup = up_of(vtop);
+  const float kf = pow2f(kup), vf = pow2f(vup);
+  const size_t at = (static_cast<size_t>(b) * a.c.kv_heads + h) * ws.key_tiles + tile;
+  if (tid == 0) ws.meta[at] = KeyMeta{pow2f(-kup), -vup};
+  uint8_t* kimg = ws.kv_img + at * Img<D>::kPair;
+  uint8_t* vimg = kimg + Img<D>::kTile;
+  constexpr int kWords = D / 8;
+  for (int x = tid; x < kTileKeys * kWords; x += kImgThreads) {
+    const int t = x / kWords, w = x % kWords, c = w / R::kBlocks, s = w % R::kBlocks;
+    const int d = 32 * s + 8 * c;
+    uint32_t word = 0;
+    if (rec[t / 16] != nullptr)
+      word = reinterpret_cast<const uint32_t*>(rec[t / 16])[(t % 16) * kWords + w];
+    const uint32_t p = kp[t / 16][16 * (d / R::kGroup) + t % 16];
+    const float sc = bf16_lo(p) * kf;
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      out[i] = f16x2_bits((static_cast<float>((word >> (4 * i)) & 15u) - 8.f) * sc,
+                          (static_cast<float>((word >> (16 + 4 * i)) & 15u) - 8.f) * sc);
+    *reinterpret_cast<uint4*>(kimg + (d / 64) * (kTileKeys * 128) + t * 128 +
+                              (((d % 64) / 8) ^ (t & 7)) * 16) =
+        make_uint4(out[0], out[1], out[2], out[3]);
+  }
+  if (tid < kTileKeys) {
+    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const uint32_t p = kp[tid / 16][16 * g + tid % 16];
+      const uint32_t hl = high_low(fmaf(8.f, bf16_lo(p), bf16_hi(p)) * kf * 128.f);
+      w[2 * g] = (hl & 0xFFFFu) * 0x10001u;  // high, high, low, 0
+      w[2 * g + 1] = hl >> 16;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4*>(kimg + Img<D>::kKCodes + i * (kTileKeys * 16) + tid * 16) =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  // a record's 16 tokens of dims 32 blk + 4 r + 0..3
+  for (int x = tid; x < 8 * 8 * R::kBlocks; x += kImgThreads) {
+    const int j = x / (8 * R::kBlocks), w = x % (8 * R::kBlocks);
+    const int d0 = 32 * (w % R::kBlocks) + 4 * (w / R::kBlocks), g = d0 / R::kGroup;
+    uint32_t word[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      word[p] = rec[j] == nullptr ? 0u
+                                  : reinterpret_cast<const uint32_t*>(rec[j] + R::kV)[p * 8 * R::kBlocks + w];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t out[4][4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t p0 = vp[j][16 * g + 8 * half + 2 * p], p1 = vp[j][16 * g + 8 * half + 2 * p + 1];
+        const float s0 = bf16_lo(p0) * vf, m0 = bf16_hi(p0) * vf;
+        const float s1 = bf16_lo(p1) * vf, m1 = bf16_hi(p1) * vf;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo = fmaf(static_cast<float>((word[4 * half + p] >> (4 * i)) & 15u), s0, m0);
+          float hi = fmaf(static_cast<float>((word[4 * half + p] >> (16 + 4 * i)) & 15u), s1, m1);
+          // P of a row that does not see the token is 0; 0 times a non-finite value is not
+          lo = fabsf(lo) <= 65504.f ? lo : 0.f;
+          hi = fabsf(hi) <= 65504.f ? hi : 0.f;
+          out[i][p] = f16x2_bits(lo, hi);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = d0 + i;
+        *reinterpret_cast<uint4*>(vimg + (j / 4) * (D * 128) + d * 128 +
+                                  (((j % 4) * 2 + half) ^ (d & 7)) * 16) =
+            make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
+      }
+    }
+  }
+}
+
+// 256 rows of one head; the sign of the scale goes into them.
+template <int D, int NG>
+__device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, int h, int rt) {
+  __shared__ uint32_t red[kImgThreads / 32];
+  const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
+  const int G = a.heads / a.c.kv_heads, rows = seq.m * G, row0 = rt * kTileRows;
+  if (row0 >= rows) return;
+  constexpr int kChunks = D / 8, kPer = kTileRows * kChunks / kImgThreads;
+  uint4 v[kPer];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int x = threadIdx.x + i * kImgThreads, row = row0 + x / kChunks;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows)
+      v[i] = __ldg(reinterpret_cast<const uint4*>(
+          a.q + static_cast<int64_t>(seq.s0 + row / G) * a.q_stride + (h * G + row % G) * D +
+          8 * (x % kChunks)));
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
+      top = max(top, max(lo >= 0x7F80u ? 0u : lo, hi >= 0x7F80u ? 0u : hi));
+    }
+  }
+  top = block_max(top, red);
+  const int up = up_of(top << 16);
+  const float f = a.scale < 0.f ? -pow2f(up) : a.scale > 0.f ? pow2f(up) : 0.f;
+  const size_t at = (static_cast<size_t>(b) * a.c.kv_heads + h) * ws.row_tiles + rt;
+  if (threadIdx.x == 0) ws.qf[at] = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e * pow2f(-up);
+  uint8_t* img = ws.q_img + at * Img<D>::kQ;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int x = threadIdx.x + i * kImgThreads, r = x / kChunks, ch = x % kChunks;
+    *reinterpret_cast<uint4*>(img + (ch / 8) * (kTileRows * 128) + r * 128 +
+                              ((ch % 8) ^ (r & 7)) * 16) =
+        make_uint4(f16x2_bits(bf16_lo(v[i].x) * f, bf16_hi(v[i].x) * f),
+                   f16x2_bits(bf16_lo(v[i].y) * f, bf16_hi(v[i].y) * f),
+                   f16x2_bits(bf16_lo(v[i].z) * f, bf16_hi(v[i].z) * f),
+                   f16x2_bits(bf16_lo(v[i].w) * f, bf16_hi(v[i].w) * f));
+    // the group's sum of q over 128, which the keys' columns make up for
+    constexpr int kLanes = kChunks / NG;
+    float sum = ((bf16_lo(v[i].x) + bf16_hi(v[i].x)) + (bf16_lo(v[i].y) + bf16_hi(v[i].y))) +
+                ((bf16_lo(v[i].z) + bf16_hi(v[i].z)) + (bf16_lo(v[i].w) + bf16_hi(v[i].w)));
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (ch % kLanes == 0) {
+      const int g = ch / kLanes;
+      const uint32_t hl = high_low(sum * (f * 0.0078125f));
+      uint8_t* more = img + Img<D>::kQCodes + r * 16;
+      // high, low, high, 0
+      *reinterpret_cast<uint2*>(more + (g / 2) * (kTileRows * 16) + (g % 2) * 8) =
+          make_uint2(hl, hl & 0xFFFFu);
+      if (g == 0)
+        for (int x2 = NG; x2 < 4; ++x2)
+          *reinterpret_cast<uint2*>(more + (x2 / 2) * (kTileRows * 16) + (x2 % 2) * 8) =
+              make_uint2(0u, 0u);
+    }
+  }
+}
+
+// Where every sequence's and row tile's units begin.
+__device__ void plan(const Kv4AttentionArgs& a, const PromptWs& ws) {
+  __shared__ int64_t sum[kImgThreads];
+  const int G = a.heads / a.c.kv_heads;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.c.batch; b0 += kImgThreads) {
+    const int b = b0 + threadIdx.x;
+    int64_t units = 0;
+    if (b < a.c.batch) {
+      const Kv4Seq s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
+      const int tiles = (s.m * G + kTileRows - 1) / kTileRows;
+      int32_t* pre = ws.pre + static_cast<size_t>(b) * (ws.row_tiles + 1);
+      int at = 0;
+      for (int rt = 0; rt <= ws.row_tiles; ++rt) {
+        pre[rt] = at;
+        if (rt < tiles) at += units_of(s, G, rt);
+      }
+      units = static_cast<int64_t>(at) * a.c.kv_heads;
+    }
+    sum[threadIdx.x] = units;
+    __syncthreads();
+    int64_t mine = before, all = 0;
+    for (int i = 0; i < kImgThreads; ++i) {
+      if (i < threadIdx.x) mine += sum[i];
+      all += sum[i];
+    }
+    if (b < a.c.batch) ws.base[b] = mine;
+    before += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) ws.base[a.c.batch] = before;
+}
+
+template <int D, int NG>
+__global__ void __launch_bounds__(kImgThreads)
+    kv4_prompt_images_kernel(const Kv4AttentionArgs a, const PromptWs ws) {
+  pdl_launch_dependents();
+  pdl_wait();
+  int64_t x = blockIdx.x;
+  if (x == 0) {
+    plan(a, ws);
+    return;
+  }
+  --x;
+  const int64_t bh = static_cast<int64_t>(a.c.batch) * a.c.kv_heads;
+  if (x < bh * ws.row_tiles) {
+    const int i = static_cast<int>(x / ws.row_tiles);
+    row_tile<D, NG>(a, ws, i / a.c.kv_heads, i % a.c.kv_heads, static_cast<int>(x % ws.row_tiles));
+    return;
+  }
+  x -= bh * ws.row_tiles;
+  const int i = static_cast<int>(x / ws.key_tiles);
+  key_tile<D, NG>(a, ws, i / a.c.kv_heads, i % a.c.kv_heads, static_cast<int>(x % ws.key_tiles));
+}
+
+// ---- tcgen05 -----------------------------------------------------------------------------
+// D[tmem] (+)= A[smem] B[smem], FP16 in, fp32 sums.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Shared-memory descriptor of 16 K-major columns without swizzle: 8-row pieces of 128 bytes one
+// after the other, the second 8 columns `k_bytes` behind the first.
+__device__ __forceinline__ uint64_t smem_desc_16cols(uint32_t saddr, uint32_t k_bytes) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(k_bytes >> 4) << 16) | (static_cast<uint64_t>(128u >> 4) << 32) |
+         (static_cast<uint64_t>(1u) << 46);
+}
+// Instruction descriptor, kind::f16: fp32 accumulator, FP16 A and B, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (x, y) = (x, y) * a + b
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, s, t;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %3};\n\t"
+      "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, s;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
+constexpr int kRing = 4;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;  // after two warpgroups of row threads
+// Three warpgroups of 168 registers a thread at launch; the row threads hold a row of S, so the
+// third gives up what they take: 2 x 208 + 88 = 3 x 168.
+constexpr int kPromptThreads = 384;
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+}
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+}
+
+template <int D>
+struct Smem {
+  static constexpr uint32_t q_off = 0;
+  static constexpr uint32_t ring_off = Img<D>::kQ;
+  static constexpr uint32_t bar_off = ring_off + kRing * Img<D>::kTile;
+  // full[R], empty[R], q_full, q_empty, s_full[2], p_full[2], o_full[2], wg[2], drain
+  static constexpr uint32_t nbars = 2 * kRing + 11;
+  static constexpr uint32_t misc_off = bar_off + nbars * 8;
+  static constexpr uint32_t total = misc_off + 32;
+  static constexpr uint32_t alloc = total + 1024;
+};
+
+// A segment: the part of one (sequence, head, row tile) in this CTA's range of units.
+struct Segment {
+  int b, h, rt;
+  int tiles;   // units of the item
+  int lo, hi;  // of them in this segment
+  int64_t item_base, left;
+  Kv4Seq s;
+};
+
+__device__ __forceinline__ void enter(Segment& g, const PromptWs& ws, int first) {
+  const int32_t* pre = ws.pre + static_cast<size_t>(g.b) * (ws.row_tiles + 1) + g.rt;
+  g.tiles = pre[1] - pre[0];
+  g.lo = first;
+  g.hi = static_cast<int>(min(static_cast<int64_t>(g.tiles), first + g.left));
+  g.left -= g.hi - g.lo;
+}
+__device__ __forceinline__ int row_tiles_of(const Kv4Seq& s, int G) {
+  return (s.m * G + kTileRows - 1) / kTileRows;
+}
+__device__ __forceinline__ bool advance(Segment& g, const Kv4AttentionArgs& a,
+                                        const PromptWs& ws, int G) {
+  if (g.left <= 0) return false;
+  g.item_base += g.tiles;
+  if (++g.rt >= row_tiles_of(g.s, G)) {
+    g.rt = 0;
+    if (++g.h >= a.c.kv_heads) {
+      g.h = 0;
+      do {
+        if (++g.b >= a.c.batch) return false;
+        g.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, g.b);
+      } while (g.s.m == 0);
+    }
+  }
+  enter(g, ws, 0);
+  return true;
+}
+// First segment of the units [u0, u1).
+__device__ __forceinline__ void locate(Segment& g, const Kv4AttentionArgs& a, const PromptWs& ws,
+                                       int64_t u0, int64_t u1) {
+  int lo = 0, hi = a.c.batch - 1;  // last b with base[b] <= u0
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (ws.base[mid] <= u0)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  g.b = lo;
+  g.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, lo);
+  const int32_t* pre = ws.pre + static_cast<size_t>(lo) * (ws.row_tiles + 1);
+  const int64_t off = u0 - ws.base[lo], per_head = pre[ws.row_tiles];
+  g.h = static_cast<int>(off / per_head);
+  const int in_head = static_cast<int>(off % per_head);
+  lo = 0, hi = ws.row_tiles - 1;  // last rt with pre[rt] <= in_head
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (pre[mid] <= in_head)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  g.rt = lo;
+  g.left = u1 - u0;
+  g.item_base = u0 - (in_head - pre[lo]);
+  enter(g, ws, in_head - pre[lo]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    kv4_prompt_kernel(const Kv4AttentionArgs a, const PromptWs ws) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
+  uint64_t* empty = full + kRing;
+  uint64_t* q_full = empty + kRing;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;  // a half's S is there, and its products before are done
+  uint64_t* p_full = s_full + 2;   // a half's P is there, its S read, its O rescaled
+  uint64_t* o_full = p_full + 2;   // a half's segment is complete
+  uint64_t* wg_bar = o_full + 2;
+  uint64_t* drain = wg_bar + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
+  volatile uint32_t* abort_flag = tmem_holder + 1;
+  volatile uint32_t* arrived = tmem_holder + 2;  // [2]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.heads / a.c.kv_heads;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&wg_bar[i], 128);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  pdl_wait();
+
+  const int64_t total = ws.base[a.c.batch];
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+  const int64_t me = blockIdx.x;
+  Segment g;
+  const bool some = me < ctas;
+  if (some) locate(g, a, ws, total * me / ctas, total * (me + 1) / ctas);
+  uint32_t* status = a.c.status;
+  const uint64_t limit = a.wait_limit_ns;
+  auto item = [&](const Segment& x) {
+    return (static_cast<size_t>(x.b) * a.c.kv_heads + x.h) * ws.row_tiles + x.rt;
+  };
+
+  if (warp >= 8) {
+  give_registers();
+  if (some && warp == kLoadWarp) {
+    if (lane == 0) {
+      int n = 0, segs = 0;  // tiles loaded, segments begun
+      bool ok = true;
+      auto load = [&](const uint8_t* src, uint32_t bytes) {
+        const int s = n % kRing;
+        if (n >= kRing) ok = mbar_wait_bounded(&empty[s], (n / kRing - 1) & 1u, abort_flag, status, limit);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        bulk_load(smem + L::ring_off + s * Img<D>::kTile, src, bytes, &full[s]);
+        ++n;
+      };
+      do {
+        if (segs > 0) ok = mbar_wait_bounded(q_empty, (segs - 1) & 1u, abort_flag, status, limit);
+        if (!ok) break;
+        mbar_arrive_expect_tx(q_full, Img<D>::kQ);
+        bulk_load(smem + L::q_off, ws.q_img + item(g) * Img<D>::kQ, Img<D>::kQ, q_full);
+        ++segs;
+        const uint8_t* kv = ws.kv_img + (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) *
+                                            ws.key_tiles * Img<D>::kPair;
+        for (int i = g.lo; i < g.hi && ok; ++i) {
+          const uint8_t* src = kv + static_cast<size_t>(i) * Img<D>::kPair;
+          load(src, Img<D>::kTile);
+          if (ok) load(src + Img<D>::kTile, Img<D>::kVTile);
+        }
+      } while (ok && advance(g, a, ws, G));
+      if (!ok) {  // copies in flight land before the CTA exits
+        volatile uint32_t no_abort = 0u;
+        for (int i = max(0, n - kRing); i < n; ++i)
+          mbar_wait_bounded(&full[i % kRing], (i / kRing) & 1u, &no_abort, status, limit);
+        if (segs > 0) mbar_wait_bounded(q_full, (segs - 1) & 1u, &no_abort, status, limit);
+      }
+    }
+  } else if (some && warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t s_idesc = idesc_f16_f32(128, kTileKeys), o_idesc = idesc_f16_f32(128, D);
+      const uint32_t q_s = smem_addr(smem + L::q_off), ring = smem_addr(smem + L::ring_off);
+      int n = 0, segs = 0, steps = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && mbar_wait_bounded(bar, parity, abort_flag, status, limit);
+        return ok;
+      };
+      auto s_mma = [&](int half, uint32_t k_s) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ss(tmem + half * 128,
+                    smem_desc_kmajor_sw128(q_s + (kk / 4) * (kTileRows * 128) + half * 16384 +
+                                           (kk % 4) * 32),
+                    smem_desc_kmajor_sw128(k_s + (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32),
+                    s_idesc, kk != 0);
+        tc_mma_ss(tmem + half * 128,
+                  smem_desc_16cols(q_s + Img<D>::kQCodes + half * 2048, kTileRows * 16),
+                  smem_desc_16cols(k_s + Img<D>::kKCodes, kTileKeys * 16), s_idesc, 1u);
+      };
+      auto o_mma = [&](int half, uint32_t v_s, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < kTileKeys / 16; ++kk)
+          tc_mma_a_tmem(tmem + 256 + half * D, tmem + half * 128 + kk * 8,
+                        smem_desc_kmajor_sw128(v_s + (kk / 4) * (D * 128) + (kk % 4) * 32), o_idesc,
+                        !(first && kk == 0));
+      };
+      do {
+        if (!wait(q_full, segs & 1u)) break;
+        ++segs;
+        if (!wait(&full[n % kRing], (n / kRing) & 1u)) break;
+        tc_fence_after_sync();
+        {
+          const uint32_t k_s = ring + (n % kRing) * Img<D>::kTile;
+          s_mma(0, k_s);
+          tc_commit(&s_full[0]);
+          s_mma(1, k_s);
+          tc_commit(&s_full[1]);
+          tc_commit(&empty[n % kRing]);
+          if (g.hi - g.lo == 1) tc_commit(q_empty);
+          ++n;
+        }
+        for (int i = g.lo; i < g.hi && ok; ++i) {
+          const bool more = i + 1 < g.hi;
+          const int v_slot = n % kRing, k_slot = (n + 1) % kRing;
+          if (!wait(&full[v_slot], (n / kRing) & 1u)) break;
+          const uint32_t v_s = ring + v_slot * Img<D>::kTile, k_s = ring + k_slot * Img<D>::kTile;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!wait(&p_full[half], steps & 1u)) break;
+            tc_fence_after_sync();
+            o_mma(half, v_s, i == g.lo);
+            if (half == 1) tc_commit(&empty[v_slot]);
+            if (more) {
+              if (half == 0 && !wait(&full[k_slot], ((n + 1) / kRing) & 1u)) break;
+              s_mma(half, k_s);
+            }
+            tc_commit(more ? &s_full[half] : &o_full[half]);
+            if (more && half == 1) {
+              tc_commit(&empty[k_slot]);
+              if (i + 2 == g.hi) tc_commit(q_empty);
+            }
+          }
+          n += more ? 2 : 1;
+          ++steps;
+        }
+      } while (ok && advance(g, a, ws, G));
+      tc_commit(drain);
+      volatile uint32_t no_abort = 0u;
+      mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
+    }
+  }
+  } else {
+    take_registers();
+    if (some) {
+    const int half = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + half * 128, t_o = tmem + lanes + 256 + half * D;
+    uint32_t s_phase = 0, o_phase = 0, wg_phase = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t& phase) {
+      ok = ok && mbar_wait_bounded(bar, phase & 1u, abort_flag, status, limit);
+      ok = __all_sync(0xffffffffu, ok);
+      ++phase;
+      tc_fence_after_sync();
+      return ok;
+    };
+    auto wg_sync = [&]() {
+      mbar_arrive(&wg_bar[half]);
+      return wait(&wg_bar[half], wg_phase);
+    };
+    do {
+      const Kv4Seq seq = g.s;
+      const int rows = seq.m * G, R = g.rt * kTileRows + half * 128 + row;
+      const int last_key = R < rows ? seq.n - seq.m + R / G : -1;
+      // first key that some row of this half does not see
+      const int first_row = g.rt * kTileRows + half * 128;
+      const int clear = first_row + 127 < rows ? seq.n - seq.m + first_row / G + 1 : 0;
+      const float qf = ws.qf[item(g)];
+      const KeyMeta* meta =
+          ws.meta + (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) * ws.key_tiles;
+      KeyMeta km = meta[g.lo];
+      float m = -INFINITY, l = 0.f;
+      int ev = km.ev;
+      for (int i = g.lo; i < g.hi; ++i) {
+        const KeyMeta now = km;
+        if (i + 1 < g.hi) km = meta[i + 1];
+        const float cf = fmaxf(qf * now.kf, 1e-37f);
+        if (!wait(&s_full[half], s_phase)) break;
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_ld_32cols(t_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
+        tmem_ld_wait();
+        const int see = last_key - i * kTileKeys;  // columns up to this one are visible
+        if ((i + 1) * kTileKeys > clear) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) s[j] = j <= see ? s[j] : -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int j = 4; j < 128; j += 8) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            top[x] = j + 4 + x < 128 ? fmaxf(fmaxf(top[x], s[j + x]), s[j + 4 + x])
+                                     : fmaxf(top[x], s[j + x]);
+        }
+        const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const float m_tile = best == -INFINITY ? -INFINITY : best * cf;
+        float f = 1.f;
+        if (m_tile > m + 8.f) {
+          f = ex2(m - m_tile);
+          m = m_tile;
+          l *= f;
+        }
+        if (now.ev > ev) {
+          f *= exp2f(static_cast<float>(ev - now.ev));
+          ev = now.ev;
+        }
+        if (i > g.lo && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32cols(t_o + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st_32cols(t_o + 32 * c, o);
+          }
+        }
+        // past 2^100 the values are nothing beside those met before, and P is 0
+        const float down = static_cast<float>(min(ev - now.ev, 100));
+        const float bias = -((m == -INFINITY ? 0.f : m) + down);
+        float acc0 = 0.f, acc1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float x = s[64 * c + 2 * j], y = s[64 * c + 2 * j + 1];
+            fma2(x, y, cf, bias);
+            x = ex2(x);
+            y = ex2(y);
+            add2(acc0, acc1, x, y);
+            p[j] = f16x2_bits(x, y);
+          }
+          tmem_st_32cols(t_s + 32 * c, p);
+        }
+        l = fmaf(acc0 + acc1, exp2f(down), l);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[half]);
+      }
+      if (!ok || !wait(&o_full[half], o_phase)) break;
+      // ---- O is complete
+      const float vf = exp2f(static_cast<float>(ev));
+      const bool whole = g.lo == 0 && g.hi == g.tiles;
+      const bool have = R < rows;
+      const int64_t at = have ? static_cast<int64_t>(seq.s0 + R / G) * a.heads + g.h * G + R % G : 0;
+      auto finish = [&](float mm, float ll) {
+        const float lse2 = ll == 0.f ? -INFINITY : mm + log2f(ll);
+        if (a.lse != nullptr) a.lse[at] = lse2 * kLn2;
+        if (ws.lse2 != nullptr) ws.lse2[at] = lse2;
+      };
+      auto store32 = [&](int c, const float* v, float inv) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          w[j] = inv == 0.f ? 0u : bf16x2_bits(v[2 * j] * inv, v[2 * j + 1] * inv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(a.out + at * D + 32 * c + 8 * j) =
+              make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      };
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : vf / l;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld_32cols(t_o + 32 * c, o);
+          tmem_ld_wait();
+          if (have) store32(c, reinterpret_cast<const float*>(o), inv);
+        }
+        if (have) finish(m, l);
+      } else {
+        constexpr size_t kPart = static_cast<size_t>(D + 2) * 128;
+        float* part = ws.parts + ((2 * me + (g.lo == 0 ? 1 : 0)) * 2 + half) * kPart + row;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld_32cols(t_o + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            __stcg(part + (32 * c + j) * 128, __uint_as_float(o[j]) * vf);
+        }
+        __stcg(part + D * 128, m);
+        __stcg(part + (D + 1) * 128, l);
+        const int64_t i0 = ((g.item_base + 1) * ctas - 1) / total;
+        const int64_t i1 = ((g.item_base + g.tiles) * ctas - 1) / total;
+        __threadfence();
+        if (!wg_sync()) break;
+        if (row == 0) {
+          uint32_t* cnt = ws.counters + item(g) * 2 + half;
+          const bool last = atomicAdd(cnt, 1u) == static_cast<uint32_t>(i1 - i0);
+          if (last) *cnt = 0u;
+          arrived[half] = last ? 1u : 0u;
+        }
+        if (!wg_sync()) break;
+        if (arrived[half]) {
+          __threadfence();
+          auto part_of = [&](int64_t i) {
+            return ws.parts + ((2 * i + (i == i0 ? 1 : 0)) * 2 + half) * kPart + row;
+          };
+          float mm = -INFINITY, ll = 0.f;
+          for (int64_t i = i0; i <= i1; ++i) mm = fmaxf(mm, __ldcg(part_of(i) + D * 128));
+          for (int64_t i = i0; i <= i1; ++i) {
+            const float x = __ldcg(part_of(i) + D * 128);
+            if (x != -INFINITY) ll = fmaf(__ldcg(part_of(i) + (D + 1) * 128), exp2f(x - mm), ll);
+          }
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            for (int64_t i = i0; i <= i1; ++i) {
+              const float* src = part_of(i);
+              const float x = __ldcg(src + D * 128);
+              const float w = x == -INFINITY ? 0.f : exp2f(x - mm);
+              if (w != 0.f) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = fmaf(__ldcg(src + (32 * c + j) * 128), w, v[j]);
+              }
+            }
+            if (have) store32(c, v, inv);
+          }
+          if (have) finish(mm, ll);
+        }
+        if (!wg_sync()) break;  // `arrived` is read before it is written again
+      }
+    } while (advance(g, a, ws, G));
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- weights -----------------------------------------------------------------------------
+// A CTA sums one tile of 128 tokens over its share of the row tiles. 8 warps: a thread a token
+// (TMEM lane) and half of a row tile's 256 columns; S^T is double-buffered in tensor memory.
+constexpr int kWeightThreads = 320;
+
+template <int D>
+struct WeightSmem {
+  static constexpr uint32_t k_off = 0;
+  static constexpr uint32_t q_off = Img<D>::kTile;
+  static constexpr uint32_t lse_off = q_off + 2 * Img<D>::kQ;         // [2][256]
+  static constexpr uint32_t sum_off = lse_off + 2 * kTileRows * 4;    // [128]
+  static constexpr uint32_t bar_off = sum_off + 128 * 4;
+  // k_full, q_full[2], q_empty[2], s_full[2], s_empty[2], drain
+  static constexpr uint32_t misc_off = bar_off + 10 * 8;
+  static constexpr uint32_t total = misc_off + 16;
+  static constexpr uint32_t alloc = total + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWeightThreads, 1)
+    kv4_prompt_weights_kernel(const Kv4AttentionArgs a, const PromptWs ws) {
+  using L = WeightSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
+  uint64_t *q_full = k_full + 1, *q_empty = q_full + 2, *s_full = q_empty + 2,
+           *s_empty = s_full + 2, *drain = s_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
+  volatile uint32_t* abort_flag = tmem_holder + 1;
+  float* lse_s = reinterpret_cast<float*>(smem + L::lse_off);
+  float* sum_s = reinterpret_cast<float*>(smem + L::sum_off);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.heads / a.c.kv_heads;
+  if (threadIdx.x == 0) {
+    mbar_init(k_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  pdl_wait();
+
+  // the last token tiles have the fewest rows: first come the ones with most
+  const int tile = blockIdx.x / ws.splits, split = blockIdx.x % ws.splits;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
+  const int key0 = tile * kTileKeys, rows = seq.m * G;
+  const int tiles = (rows + kTileRows - 1) / kTileRows;
+  // the first row that sees key0, and the row tiles from there in `splits` shares
+  const int first = static_cast<int>(
+      max(static_cast<int64_t>(0), static_cast<int64_t>(key0 - (seq.n - seq.m)) * G) / kTileRows);
+  const int count = max(0, tiles - first);
+  const int r0 = first + static_cast<int>(static_cast<int64_t>(count) * split / ws.splits);
+  const int r1 = first + static_cast<int>(static_cast<int64_t>(count) * (split + 1) / ws.splits);
+  const bool some = key0 < seq.n && r0 < r1;
+  const size_t bh = static_cast<size_t>(b) * a.c.kv_heads + h;
+  uint32_t* status = a.c.status;
+  const uint64_t limit = a.wait_limit_ns;
+  if (!some) {
+  } else if (warp == kLoadWarp) {
+    if (lane == 0) {
+      bool ok = true;
+      mbar_arrive_expect_tx(k_full, Img<D>::kTile);
+      bulk_load(smem + L::k_off, ws.kv_img + (bh * ws.key_tiles + tile) * Img<D>::kPair,
+                Img<D>::kTile, k_full);
+      int n = 0;
+      for (int rt = r0; rt < r1; ++rt, ++n) {
+        const int s = n & 1;
+        if (n >= 2) ok = mbar_wait_bounded(&q_empty[s], (n / 2 - 1) & 1u, abort_flag, status, limit);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&q_full[s], Img<D>::kQ);
+        bulk_load(smem + L::q_off + s * Img<D>::kQ, ws.q_img + (bh * ws.row_tiles + rt) * Img<D>::kQ,
+                  Img<D>::kQ, &q_full[s]);
+      }
+      if (!ok) {
+        volatile uint32_t no_abort = 0u;
+        mbar_wait_bounded(k_full, 0u, &no_abort, status, limit);
+        for (int i = max(0, n - 2); i < n; ++i)
+          mbar_wait_bounded(&q_full[i & 1], (i / 2) & 1u, &no_abort, status, limit);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16_f32(128, kTileRows);
+      const uint32_t k_s = smem_addr(smem + L::k_off);
+      bool ok = mbar_wait_bounded(k_full, 0u, abort_flag, status, limit);
+      for (int n = 0; n < r1 - r0 && ok; ++n) {
+        const int s = n & 1;
+        ok = mbar_wait_bounded(&q_full[s], (n / 2) & 1u, abort_flag, status, limit) &&
+             (n < 2 || mbar_wait_bounded(&s_empty[s], (n / 2 - 1) & 1u, abort_flag, status, limit));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t q_s = smem_addr(smem + L::q_off) + s * Img<D>::kQ;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ss(tmem + s * 256,
+                    smem_desc_kmajor_sw128(k_s + (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32),
+                    smem_desc_kmajor_sw128(q_s + (kk / 4) * (kTileRows * 128) + (kk % 4) * 32),
+                    idesc, kk != 0);
+        tc_mma_ss(tmem + s * 256, smem_desc_16cols(k_s + Img<D>::kKCodes, kTileKeys * 16),
+                  smem_desc_16cols(q_s + Img<D>::kQCodes, kTileRows * 16), idesc, 1u);
+        tc_commit(&q_empty[s]);
+        tc_commit(&s_full[s]);
+      }
+      tc_commit(drain);
+      volatile uint32_t no_abort = 0u;
+      mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
+    }
+  } else {
+    const int part = warp >> 2;  // columns 128 part .. 128 part + 127
+    const int key = key0 + (warp & 3) * 32 + lane;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + part * 128;
+    const float kf = ws.meta[bh * ws.key_tiles + tile].kf;
+    float acc = 0.f;
+    bool ok = true;
+    for (int n = 0; n < r1 - r0; ++n) {
+      const int s = n & 1, rt = r0 + n;
+      // this warp's 128 columns' log-sums (rows past the end see nothing); warps of a part
+      // write and read their own copy's quarter, all of it after the barrier below
+      const int x = threadIdx.x;  // 0..255
+      const int R = rt * kTileRows + x;
+      float v = INFINITY;
+      if (R < rows) {
+        v = ws.lse2[static_cast<int64_t>(seq.s0 + R / G) * a.heads + h * G + R % G];
+        if (v == -INFINITY) v = INFINITY;
+      }
+      lse_s[s * kTileRows + x] = v;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      ok = ok && mbar_wait_bounded(&s_full[s], (n / 2) & 1u, abort_flag, status, limit);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after_sync();
+        const float cf = fmaxf(ws.qf[bh * ws.row_tiles + rt] * kf, 1e-37f);
+        // rows before this one do not see the token
+        const int64_t need = static_cast<int64_t>(key - (seq.n - seq.m)) * G;
+        const int hide = static_cast<int>(
+            max(static_cast<int64_t>(0), min(need - rt * kTileRows - part * 128, static_cast<int64_t>(128))));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float q[32];
+          tmem_ld_32cols(t_s + s * 256 + 32 * c, reinterpret_cast<uint32_t*>(q));
+          tmem_ld_wait();
+          const float* lse = lse_s + s * kTileRows + part * 128 + 32 * c;
+          float a0 = 0.f, a1 = 0.f;
+          const bool cut = __any_sync(0xffffffffu, hide > 32 * c);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(lse + j);
+            float p0 = ex2(fmaf(q[j], cf, -z.x)), p1 = ex2(fmaf(q[j + 1], cf, -z.y));
+            float p2 = ex2(fmaf(q[j + 2], cf, -z.z)), p3 = ex2(fmaf(q[j + 3], cf, -z.w));
+            if (cut) {
+              if (32 * c + j < hide) p0 = 0.f;
+              if (32 * c + j + 1 < hide) p1 = 0.f;
+              if (32 * c + j + 2 < hide) p2 = 0.f;
+              if (32 * c + j + 3 < hide) p3 = 0.f;
+            }
+            add2(a0, a1, p0, p1);
+            add2(a0, a1, p2, p3);
+          }
+          acc += a0 + a1;
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[s]);
+      }
+    }
+    if (part == 1) sum_s[threadIdx.x & 127] = acc;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (part == 0 && key < seq.n)
+      ws.sums[((static_cast<size_t>(split) * a.c.batch + b) * a.c.kv_heads + h) * ws.key_tiles *
+                  kTileKeys + key] = acc + sum_s[threadIdx.x];
+  }
+  if (!some && threadIdx.x < 128 && key0 + threadIdx.x < seq.n)
+    ws.sums[((static_cast<size_t>(split) * a.c.batch + b) * a.c.kv_heads + h) * ws.key_tiles *
+                kTileKeys + key0 + threadIdx.x] = 0.f;
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+__global__ void __launch_bounds__(256) kv4_prompt_add_kernel(const Kv4AttentionArgs a,
+                                                             const PromptWs ws) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int key = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
+  if (key >= seq.n) return;
+  const size_t bh = static_cast<size_t>(b) * a.c.kv_heads + h;
+  float acc = 0.f;
+  for (int s = 0; s < ws.splits; ++s)
+    acc += ws.sums[(static_cast<size_t>(s) * a.c.batch * a.c.kv_heads + bh) * ws.key_tiles *
+                       kTileKeys + key];
+  const size_t at = bh * a.weights_stride + key;
+  a.weights_out[at] = (a.weights != nullptr ? a.weights[at] : 0.f) + acc;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Layout {
+  size_t base, pre, meta, qf, q_img, kv_img, counters, parts, lse2, sums, total;
+  int key_tiles, row_tiles, splits;
+};
+
+Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv_heads, int D,
+              bool weights) {
+  Layout l = {};
+  const int G = heads / kv_heads;
+  const size_t bh = static_cast<size_t>(batch) * kv_heads;
+  l.key_tiles = (max_len + kTileKeys - 1) / kTileKeys;
+  l.row_tiles = static_cast<int>((static_cast<int64_t>(max_new) * G + kTileRows - 1) / kTileRows);
+  // row shares of a token tile in the weights' kernel: about four CTAs an SM
+  const int64_t ctas = static_cast<int64_t>(bh) * l.key_tiles;
+  const int64_t want = (4 * static_cast<int64_t>(device_sm_count()) + ctas - 1) / ctas;
+  l.splits = static_cast<int>(want < l.row_tiles ? want : l.row_tiles);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
+  l.counters = take(bh * l.row_tiles * 2 * 4);
+  l.base = take((static_cast<size_t>(batch) + 1) * 8);
+  l.pre = take(static_cast<size_t>(batch) * (l.row_tiles + 1) * 4);
+  l.meta = take(bh * l.key_tiles * sizeof(KeyMeta));
+  l.qf = take(bh * l.row_tiles * 4);
+  l.q_img = take(bh * l.row_tiles * kTileRows * (D + 16) * 2);
+  l.kv_img = take(bh * l.key_tiles * kTileKeys * (2 * D + 16) * 2);
+  l.parts = take(static_cast<size_t>(device_sm_count()) * 4 * (D + 2) * 128 * 4);
+  if (weights) {
+    l.lse2 = take(static_cast<size_t>(tokens) * heads * 4);
+    l.sums = take(static_cast<size_t>(l.splits) * bh * l.key_tiles * kTileKeys * 4);
+  }
+  l.total = at;
+  return l;
+}
+
+template <int D, int NG>
+cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
+  const bool weights = a.weights_out != nullptr;
+  const Layout l = layout(a.c.batch, a.tokens, a.max_new, a.max_len, a.heads, a.c.kv_heads, D,
+                          weights);
+  uint8_t* w = a.workspace;
+  PromptWs ws;
+  ws.base = reinterpret_cast<int64_t*>(w + l.base);
+  ws.pre = reinterpret_cast<int32_t*>(w + l.pre);
+  ws.meta = reinterpret_cast<KeyMeta*>(w + l.meta);
+  ws.qf = reinterpret_cast<float*>(w + l.qf);
+  ws.q_img = w + l.q_img;
+  ws.kv_img = w + l.kv_img;
+  ws.counters = reinterpret_cast<uint32_t*>(w + l.counters);
+  ws.parts = reinterpret_cast<float*>(w + l.parts);
+  ws.lse2 = weights ? reinterpret_cast<float*>(w + l.lse2) : nullptr;
+  ws.sums = reinterpret_cast<float*>(w + l.sums);
+  ws.key_tiles = l.key_tiles;
+  ws.row_tiles = l.row_tiles;
+  ws.splits = l.splits;
+  const int64_t bh = static_cast<int64_t>(a.c.batch) * a.c.kv_heads;
+  const int64_t blocks = 1 + bh * (l.row_tiles + l.key_tiles);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaError_t e = launch_with_pdl(kv4_prompt_images_kernel<D, NG>,
+                                  dim3(static_cast<unsigned>(blocks)), dim3(kImgThreads), 0, stream,
+                                  a, ws);
+  if (e != cudaSuccess) return e;
+  auto kern = kv4_prompt_kernel<D>;
+  e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), Smem<D>::alloc);
+  if (e != cudaSuccess) return e;
+  const int64_t units = bh * l.row_tiles * l.key_tiles;
+  const unsigned grid = static_cast<unsigned>(units < device_sm_count() ? units : device_sm_count());
+  e = launch_with_pdl(kern, dim3(grid), dim3(kPromptThreads), Smem<D>::alloc, stream, a, ws);
+  if (e != cudaSuccess || !weights) return e;
+  auto wkern = kv4_prompt_weights_kernel<D>;
+  e = set_max_dynamic_smem(reinterpret_cast<const void*>(wkern), WeightSmem<D>::alloc);
+  if (e != cudaSuccess) return e;
+  e = launch_with_pdl(wkern, dim3(l.key_tiles * l.splits, a.c.kv_heads, a.c.batch),
+                      dim3(kWeightThreads), WeightSmem<D>::alloc, stream, a, ws);
+  if (e != cudaSuccess) return e;
+  return launch_with_pdl(kv4_prompt_add_kernel,
+                         dim3((a.max_len + 255) / 256, a.c.kv_heads, a.c.batch), dim3(256), 0,
+                         stream, a, ws);
+}
+
+}  // namespace
+
+size_t kv4_prompt_workspace(int batch, int tokens, int max_new, int max_len, int heads,
+                            int kv_heads, int head_dim, bool weights) {
+  return layout(batch, tokens, max_new, max_len, heads, kv_heads, head_dim, weights).total;
+}
+
+cudaError_t launch_kv4_prompt(const Kv4AttentionArgs& a, int head_dim, int group,
+                              cudaStream_t stream) {
+  if (head_dim == 128)
+    return group == 128 ? run<128, 1>(a, stream)
+           : group == 64 ? run<128, 2>(a, stream) : run<128, 4>(a, stream);
+  return group == 64 ? run<64, 1>(a, stream) : run<64, 2>(a, stream);
+}
+
+}  // namespace w4k
