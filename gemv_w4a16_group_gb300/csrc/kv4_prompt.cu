@@ -66,11 +66,15 @@ struct Img {
   static constexpr uint32_t kQ = kQCodes + kTileRows * kMore;
 };
 
-// Units (key tiles) of row tile rt.
+// Units of a row tile: its key tiles, after kItemCost units that stand for the time an item costs
+// beyond them (loading its queries, filling the pipeline, writing its rows). Without them the
+// CTAs that get the short items at the beginning of a causal prompt finish last: a 4096-token
+// prompt (32 heads) took 215 us, half of the CTAs having been done at 153.
+constexpr int kItemCost = 2;
 __device__ __forceinline__ int units_of(const Kv4Seq& s, int G, int rt) {
   const int last = min((rt + 1) * kTileRows, s.m * G) - 1;
   const int key = s.n - s.m + last / G;
-  return key < 0 ? 1 : key / kTileKeys + 1;
+  return kItemCost + (key < 0 ? 1 : key / kTileKeys + 1);
 }
 
 // ---- images ------------------------------------------------------------------------------
@@ -331,22 +335,48 @@ __global__ void __launch_bounds__(kImgThreads)
 }
 
 // ---- tcgen05 -----------------------------------------------------------------------------
+// Operands as the low words of shared-memory descriptors (address and leading offset); the high
+// words are the layout's. Descriptors of neighbouring columns differ by an addition to the low
+// word, so a product costs its issuing thread few instructions: with the descriptors put
+// together anew for each one the issue, not the tensor pipe, set the pace (100 cycles a product
+// of 64).
+constexpr uint32_t kDescSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);  // see smem_desc_kmajor_sw128
+// 16 K-major columns without swizzle: 8-row pieces of 128 bytes one after the other, the second 8
+// columns the leading offset behind the first.
+constexpr uint32_t kDescPlain = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t leading) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
+}
 // D[tmem] (+)= A[smem] B[smem], FP16 in, fp32 sums.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
+template <uint32_t HIGH>
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(HIGH)
       : "memory");
 }
-// Shared-memory descriptor of 16 K-major columns without swizzle: 8-row pieces of 128 bytes one
-// after the other, the second 8 columns `k_bytes` behind the first.
-__device__ __forceinline__ uint64_t smem_desc_16cols(uint32_t saddr, uint32_t k_bytes) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
-         (static_cast<uint64_t>(k_bytes >> 4) << 16) | (static_cast<uint64_t>(128u >> 4) << 32) |
-         (static_cast<uint64_t>(1u) << 46);
+// D[tmem] (+)= A[tmem] B[smem].
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescSw128)
+      : "memory");
+}
+// True in one lane, always the same; the whole warp comes here, so that the values the elected
+// lane issues products with stay uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
 }
 // Instruction descriptor, kind::f16: fp32 accumulator, FP16 A and B, both K-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
@@ -356,6 +386,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 // (x, y) = (x, y) * a + b
@@ -401,26 +436,30 @@ struct Smem {
 // A segment: the part of one (sequence, head, row tile) in this CTA's range of units.
 struct Segment {
   int b, h, rt;
-  int tiles;   // units of the item
-  int lo, hi;  // of them in this segment
+  int units;   // of the item
+  int tiles;   // of them key tiles, the last ones
+  int lo, hi;  // key tiles in this segment; none where the range holds only the item's cost
   int64_t item_base, left;
   Kv4Seq s;
 };
 
 __device__ __forceinline__ void enter(Segment& g, const PromptWs& ws, int first) {
   const int32_t* pre = ws.pre + static_cast<size_t>(g.b) * (ws.row_tiles + 1) + g.rt;
-  g.tiles = pre[1] - pre[0];
-  g.lo = first;
-  g.hi = static_cast<int>(min(static_cast<int64_t>(g.tiles), first + g.left));
-  g.left -= g.hi - g.lo;
+  g.units = pre[1] - pre[0];
+  g.tiles = g.units - kItemCost;
+  const int end = static_cast<int>(min(static_cast<int64_t>(g.units), first + g.left));
+  g.left -= end - first;
+  g.lo = max(0, first - kItemCost);
+  g.hi = max(0, end - kItemCost);
 }
 __device__ __forceinline__ int row_tiles_of(const Kv4Seq& s, int G) {
   return (s.m * G + kTileRows - 1) / kTileRows;
 }
 __device__ __forceinline__ bool advance(Segment& g, const Kv4AttentionArgs& a,
                                         const PromptWs& ws, int G) {
+  do {
   if (g.left <= 0) return false;
-  g.item_base += g.tiles;
+  g.item_base += g.units;
   if (++g.rt >= row_tiles_of(g.s, G)) {
     g.rt = 0;
     if (++g.h >= a.c.kv_heads) {
@@ -432,11 +471,12 @@ __device__ __forceinline__ bool advance(Segment& g, const Kv4AttentionArgs& a,
     }
   }
   enter(g, ws, 0);
+  } while (g.lo >= g.hi);
   return true;
 }
-// First segment of the units [u0, u1).
-__device__ __forceinline__ void locate(Segment& g, const Kv4AttentionArgs& a, const PromptWs& ws,
-                                       int64_t u0, int64_t u1) {
+// First segment with key tiles of the units [u0, u1); false if there is none.
+__device__ __forceinline__ bool locate(Segment& g, const Kv4AttentionArgs& a, const PromptWs& ws,
+                                       int64_t u0, int64_t u1, int G) {
   int lo = 0, hi = a.c.batch - 1;  // last b with base[b] <= u0
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -463,6 +503,7 @@ __device__ __forceinline__ void locate(Segment& g, const Kv4AttentionArgs& a, co
   g.left = u1 - u0;
   g.item_base = u0 - (in_head - pre[lo]);
   enter(g, ws, in_head - pre[lo]);
+  return g.lo < g.hi || advance(g, a, ws, G);
 }
 
 template <int D>
@@ -518,8 +559,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
   const int64_t me = blockIdx.x;
   Segment g;
-  const bool some = me < ctas;
-  if (some) locate(g, a, ws, total * me / ctas, total * (me + 1) / ctas);
+  const bool some =
+      me < ctas && locate(g, a, ws, total * me / ctas, total * (me + 1) / ctas, G);
   uint32_t* status = a.c.status;
   const uint64_t limit = a.wait_limit_ns;
   auto item = [&](const Segment& x) {
@@ -562,78 +603,81 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
   } else if (some && warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t s_idesc = idesc_f16_f32(128, kTileKeys), o_idesc = idesc_f16_f32(128, D);
-      const uint32_t q_s = smem_addr(smem + L::q_off), ring = smem_addr(smem + L::ring_off);
-      int n = 0, segs = 0, steps = 0;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && mbar_wait_bounded(bar, parity, abort_flag, status, limit);
-        return ok;
-      };
-      auto s_mma = [&](int half, uint32_t k_s) {
+    constexpr uint32_t s_idesc = idesc_f16_f32(128, kTileKeys), o_idesc = idesc_f16_f32(128, D);
+    const uint32_t q_s = desc_low(smem_addr(smem + L::q_off), 16);
+    const uint32_t q_more = desc_low(smem_addr(smem + L::q_off) + Img<D>::kQCodes, kTileRows * 16);
+    const uint32_t ring = desc_low(smem_addr(smem + L::ring_off), 16);
+    const uint32_t ring_more =
+        desc_low(smem_addr(smem + L::ring_off) + Img<D>::kKCodes, kTileKeys * 16);
+    int n = 0, segs = 0, steps = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait_bounded(bar, parity, abort_flag, status, limit);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    auto s_mma = [&](int half, int slot) {
+      const uint32_t k_s = ring + slot * (Img<D>::kTile >> 4), q_h = q_s + half * (16384 >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ss(tmem + half * 128,
-                    smem_desc_kmajor_sw128(q_s + (kk / 4) * (kTileRows * 128) + half * 16384 +
-                                           (kk % 4) * 32),
-                    smem_desc_kmajor_sw128(k_s + (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32),
-                    s_idesc, kk != 0);
-        tc_mma_ss(tmem + half * 128,
-                  smem_desc_16cols(q_s + Img<D>::kQCodes + half * 2048, kTileRows * 16),
-                  smem_desc_16cols(k_s + Img<D>::kKCodes, kTileKeys * 16), s_idesc, 1u);
-      };
-      auto o_mma = [&](int half, uint32_t v_s, bool first) {
+      for (int kk = 0; kk < D / 16; ++kk)
+        tc_mma_ss<kDescSw128>(tmem + half * 128,
+                              q_h + (((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4),
+                              k_s + (((kk / 4) * (kTileKeys * 128) + (kk % 4) * 32) >> 4), s_idesc,
+                              kk != 0);
+      tc_mma_ss<kDescPlain>(tmem + half * 128, q_more + half * (2048 >> 4),
+                            ring_more + slot * (Img<D>::kTile >> 4), s_idesc, 1u);
+    };
+    auto o_mma = [&](int half, int slot, bool first) {
+      const uint32_t v_s = ring + slot * (Img<D>::kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          tc_mma_a_tmem(tmem + 256 + half * D, tmem + half * 128 + kk * 8,
-                        smem_desc_kmajor_sw128(v_s + (kk / 4) * (D * 128) + (kk % 4) * 32), o_idesc,
-                        !(first && kk == 0));
-      };
-      do {
-        if (!wait(q_full, segs & 1u)) break;
-        ++segs;
-        if (!wait(&full[n % kRing], (n / kRing) & 1u)) break;
-        tc_fence_after_sync();
-        {
-          const uint32_t k_s = ring + (n % kRing) * Img<D>::kTile;
-          s_mma(0, k_s);
-          tc_commit(&s_full[0]);
-          s_mma(1, k_s);
-          tc_commit(&s_full[1]);
-          tc_commit(&empty[n % kRing]);
-          if (g.hi - g.lo == 1) tc_commit(q_empty);
-          ++n;
-        }
-        for (int i = g.lo; i < g.hi && ok; ++i) {
-          const bool more = i + 1 < g.hi;
-          const int v_slot = n % kRing, k_slot = (n + 1) % kRing;
-          if (!wait(&full[v_slot], (n / kRing) & 1u)) break;
-          const uint32_t v_s = ring + v_slot * Img<D>::kTile, k_s = ring + k_slot * Img<D>::kTile;
+      for (int kk = 0; kk < kTileKeys / 16; ++kk)
+        tc_mma_ts(tmem + 256 + half * D, tmem + half * 128 + kk * 8,
+                  v_s + (((kk / 4) * (D * 128) + (kk % 4) * 32) >> 4), o_idesc,
+                  kk != 0 || !first);
+    };
+    do {
+      if (!wait(q_full, segs & 1u)) break;
+      ++segs;
+      if (!wait(&full[n % kRing], (n / kRing) & 1u)) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
+        s_mma(0, n % kRing);
+        tc_commit(&s_full[0]);
+        s_mma(1, n % kRing);
+        tc_commit(&s_full[1]);
+        tc_commit(&empty[n % kRing]);
+        if (g.hi - g.lo == 1) tc_commit(q_empty);
+      }
+      __syncwarp();
+      ++n;
+      for (int i = g.lo; i < g.hi && ok; ++i) {
+        const bool more = i + 1 < g.hi;
+        const int v_slot = n % kRing, k_slot = (n + 1) % kRing;
+        if (!wait(&full[v_slot], (n / kRing) & 1u)) break;
+        if (more && !wait(&full[k_slot], ((n + 1) / kRing) & 1u)) break;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!wait(&p_full[half], steps & 1u)) break;
-            tc_fence_after_sync();
-            o_mma(half, v_s, i == g.lo);
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(&p_full[half], steps & 1u)) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            o_mma(half, v_slot, i == g.lo);
             if (half == 1) tc_commit(&empty[v_slot]);
-            if (more) {
-              if (half == 0 && !wait(&full[k_slot], ((n + 1) / kRing) & 1u)) break;
-              s_mma(half, k_s);
-            }
+            if (more) s_mma(half, k_slot);
             tc_commit(more ? &s_full[half] : &o_full[half]);
             if (more && half == 1) {
               tc_commit(&empty[k_slot]);
               if (i + 2 == g.hi) tc_commit(q_empty);
             }
           }
-          n += more ? 2 : 1;
-          ++steps;
+          __syncwarp();
         }
-      } while (ok && advance(g, a, ws, G));
-      tc_commit(drain);
-      volatile uint32_t no_abort = 0u;
-      mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
-    }
+        n += more ? 2 : 1;
+        ++steps;
+      }
+    } while (ok && advance(g, a, ws, G));
+    if (elect_one()) tc_commit(drain);
+    volatile uint32_t no_abort = 0u;
+    mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
   }
   } else {
     take_registers();
@@ -682,41 +726,49 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
           for (int j = 0; j < 128; ++j) s[j] = j <= see ? s[j] : -INFINITY;
         }
-        float top[4] = {s[0], s[1], s[2], s[3]};
+        float top[8];
 #pragma unroll
-        for (int j = 4; j < 128; j += 8) {
+        for (int x = 0; x < 8; ++x) top[x] = max3(s[x], s[x + 8], s[x + 16]);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            top[x] = j + 4 + x < 128 ? fmaxf(fmaxf(top[x], s[j + x]), s[j + 4 + x])
-                                     : fmaxf(top[x], s[j + x]);
+        for (int j = 24; j < 120; j += 16) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) top[x] = max3(top[x], s[j + x], s[j + 8 + x]);
         }
-        const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        const float m_tile = best == -INFINITY ? -INFINITY : best * cf;
-        float f = 1.f;
-        if (m_tile > m + 8.f) {
-          f = ex2(m - m_tile);
-          m = m_tile;
-          l *= f;
-        }
-        if (now.ev > ev) {
-          f *= exp2f(static_cast<float>(ev - now.ev));
-          ev = now.ev;
-        }
-        if (i > g.lo && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld_32cols(t_o + 32 * c, o);
-            tmem_ld_wait();
+        for (int x = 0; x < 8; ++x) top[x] = fmaxf(top[x], s[120 + x]);
+        const float best = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]),
+                                fmaxf(top[6], top[7]));
+        // -inf stays -inf: cf is positive
+        const bool raise = best * cf > m + 8.f;
+        float down = 0.f, undo = 1.f;
+        if (__any_sync(0xffffffffu, raise) || now.ev != ev) {
+          float f = 1.f;
+          if (raise) {
+            f = ex2(m - best * cf);
+            m = best * cf;
+            l *= f;
+          }
+          if (now.ev > ev) {
+            f *= exp2f(static_cast<float>(ev - now.ev));
+            ev = now.ev;
+          }
+          // past 2^100 the values are nothing beside those met before, and P is 0
+          down = static_cast<float>(min(ev - now.ev, 100));
+          undo = exp2f(down);
+          if (i > g.lo && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st_32cols(t_o + 32 * c, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld_16cols(t_o + 16 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st_16cols(t_o + 16 * c, o);
+            }
           }
         }
-        // past 2^100 the values are nothing beside those met before, and P is 0
-        const float down = static_cast<float>(min(ev - now.ev, 100));
         const float bias = -((m == -INFINITY ? 0.f : m) + down);
-        float acc0 = 0.f, acc1 = 0.f;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t p[32];
@@ -726,16 +778,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             fma2(x, y, cf, bias);
             x = ex2(x);
             y = ex2(y);
-            add2(acc0, acc1, x, y);
+            add2(acc[2 * (j & 1)], acc[2 * (j & 1) + 1], x, y);
             p[j] = f16x2_bits(x, y);
           }
           tmem_st_32cols(t_s + 32 * c, p);
         }
-        l = fmaf(acc0 + acc1, exp2f(down), l);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[half]);
+        l = fmaf((acc[0] + acc[1]) + (acc[2] + acc[3]), undo, l);
       }
       if (!ok || !wait(&o_full[half], o_phase)) break;
       // ---- O is complete
@@ -770,20 +822,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (have) finish(m, l);
       } else {
         constexpr size_t kPart = static_cast<size_t>(D + 2) * 128;
-        float* part = ws.parts + ((2 * me + (g.lo == 0 ? 1 : 0)) * 2 + half) * kPart + row;
+        float* base = ws.parts + ((2 * me + (g.lo == 0 ? 1 : 0)) * 2 + half) * kPart;
+        float* part = base + 4 * row;
+        float2* ml = reinterpret_cast<float2*>(base + D * 128);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld_32cols(t_o + 32 * c, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            __stcg(part + (32 * c + j) * 128, __uint_as_float(o[j]) * vf);
+          for (int j = 0; j < 32; j += 4)
+            __stcg(reinterpret_cast<float4*>(part) + (8 * c + j / 4) * 128,
+                   make_float4(__uint_as_float(o[j]) * vf, __uint_as_float(o[j + 1]) * vf,
+                               __uint_as_float(o[j + 2]) * vf, __uint_as_float(o[j + 3]) * vf));
         }
-        __stcg(part + D * 128, m);
-        __stcg(part + (D + 1) * 128, l);
-        const int64_t i0 = ((g.item_base + 1) * ctas - 1) / total;
-        const int64_t i1 = ((g.item_base + g.tiles) * ctas - 1) / total;
+        __stcg(ml + row, make_float2(m, l));
+        const int64_t i0 = ((g.item_base + kItemCost + 1) * ctas - 1) / total;
+        const int64_t i1 = ((g.item_base + g.units) * ctas - 1) / total;
         __threadfence();
         if (!wg_sync()) break;
         if (row == 0) {
@@ -796,30 +851,44 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (arrived[half]) {
           __threadfence();
           auto part_of = [&](int64_t i) {
-            return ws.parts + ((2 * i + (i == i0 ? 1 : 0)) * 2 + half) * kPart + row;
+            return ws.parts + ((2 * i + (i == i0 ? 1 : 0)) * 2 + half) * kPart;
+          };
+          auto ml_of = [&](int64_t i) {
+            return __ldcg(reinterpret_cast<const float2*>(part_of(i) + D * 128) + row);
           };
           float mm = -INFINITY, ll = 0.f;
-          for (int64_t i = i0; i <= i1; ++i) mm = fmaxf(mm, __ldcg(part_of(i) + D * 128));
+          for (int64_t i = i0; i <= i1; ++i) mm = fmaxf(mm, ml_of(i).x);
           for (int64_t i = i0; i <= i1; ++i) {
-            const float x = __ldcg(part_of(i) + D * 128);
-            if (x != -INFINITY) ll = fmaf(__ldcg(part_of(i) + (D + 1) * 128), exp2f(x - mm), ll);
+            const float2 x = ml_of(i);
+            if (x.x != -INFINITY) ll = fmaf(x.y, exp2f(x.x - mm), ll);
           }
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float v[32];
+          for (int c = 0; c < D / 64; ++c) {
+            float v[64];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            for (int j = 0; j < 64; ++j) v[j] = 0.f;
             for (int64_t i = i0; i <= i1; ++i) {
-              const float* src = part_of(i);
-              const float x = __ldcg(src + D * 128);
+              const float4* src = reinterpret_cast<const float4*>(part_of(i)) + row;
+              const float x = ml_of(i).x;
               const float w = x == -INFINITY ? 0.f : exp2f(x - mm);
+              float4 t[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) t[j] = __ldcg(src + (16 * c + j) * 128);
               if (w != 0.f) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = fmaf(__ldcg(src + (32 * c + j) * 128), w, v[j]);
+                for (int j = 0; j < 16; ++j) {
+                  v[4 * j] = fmaf(t[j].x, w, v[4 * j]);
+                  v[4 * j + 1] = fmaf(t[j].y, w, v[4 * j + 1]);
+                  v[4 * j + 2] = fmaf(t[j].z, w, v[4 * j + 2]);
+                  v[4 * j + 3] = fmaf(t[j].w, w, v[4 * j + 3]);
+                }
               }
             }
-            if (have) store32(c, v, inv);
+            if (have) {
+              store32(2 * c, v, inv);
+              store32(2 * c + 1, v + 32, inv);
+            }
           }
           if (have) finish(mm, ll);
         }
@@ -934,32 +1003,35 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(128, kTileRows);
-      const uint32_t k_s = smem_addr(smem + L::k_off);
-      bool ok = mbar_wait_bounded(k_full, 0u, abort_flag, status, limit);
-      for (int n = 0; n < r1 - r0 && ok; ++n) {
-        const int s = n & 1;
-        ok = mbar_wait_bounded(&q_full[s], (n / 2) & 1u, abort_flag, status, limit) &&
-             (n < 2 || mbar_wait_bounded(&s_empty[s], (n / 2 - 1) & 1u, abort_flag, status, limit));
-        if (!ok) break;
-        tc_fence_after_sync();
-        const uint32_t q_s = smem_addr(smem + L::q_off) + s * Img<D>::kQ;
+    constexpr uint32_t idesc = idesc_f16_f32(128, kTileRows);
+    const uint32_t k_s = desc_low(smem_addr(smem + L::k_off), 16);
+    const uint32_t k_more = desc_low(smem_addr(smem + L::k_off) + Img<D>::kKCodes, kTileKeys * 16);
+    bool ok = mbar_wait_bounded(k_full, 0u, abort_flag, status, limit);
+    for (int n = 0; n < r1 - r0; ++n) {
+      const int s = n & 1;
+      ok = ok && mbar_wait_bounded(&q_full[s], (n / 2) & 1u, abort_flag, status, limit) &&
+           (n < 2 || mbar_wait_bounded(&s_empty[s], (n / 2 - 1) & 1u, abort_flag, status, limit));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t q_at = smem_addr(smem + L::q_off) + s * Img<D>::kQ;
+      const uint32_t q_s = desc_low(q_at, 16), q_more = desc_low(q_at + Img<D>::kQCodes, kTileRows * 16);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ss(tmem + s * 256,
-                    smem_desc_kmajor_sw128(k_s + (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32),
-                    smem_desc_kmajor_sw128(q_s + (kk / 4) * (kTileRows * 128) + (kk % 4) * 32),
-                    idesc, kk != 0);
-        tc_mma_ss(tmem + s * 256, smem_desc_16cols(k_s + Img<D>::kKCodes, kTileKeys * 16),
-                  smem_desc_16cols(q_s + Img<D>::kQCodes, kTileRows * 16), idesc, 1u);
+          tc_mma_ss<kDescSw128>(tmem + s * 256,
+                                k_s + (((kk / 4) * (kTileKeys * 128) + (kk % 4) * 32) >> 4),
+                                q_s + (((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4), idesc,
+                                kk != 0);
+        tc_mma_ss<kDescPlain>(tmem + s * 256, k_more, q_more, idesc, 1u);
         tc_commit(&q_empty[s]);
         tc_commit(&s_full[s]);
       }
-      tc_commit(drain);
-      volatile uint32_t no_abort = 0u;
-      mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
+      __syncwarp();
     }
+    if (elect_one()) tc_commit(drain);
+    volatile uint32_t no_abort = 0u;
+    mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
   } else {
     const int part = warp >> 2;  // columns 128 part .. 128 part + 127
     const int key = key0 + (warp & 3) * 32 + lane;
