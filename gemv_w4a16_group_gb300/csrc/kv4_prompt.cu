@@ -51,8 +51,12 @@ struct PromptWs {
   uint32_t* counters; // [batch, kv_heads, row_tiles, 2], zero between calls
   float* parts;       // [2 grid][2 halves] x (D + 2) 128
   float* lse2;        // [tokens, heads], base 2
-  float* sums;        // [splits, batch, kv_heads, key_tiles 128]
-  int key_tiles, row_tiles, splits;
+  // with weights, the same for the units of the token tiles (row tiles that see them)
+  int64_t* kbase;     // [batch + 1]
+  int32_t* kpre;      // [batch, key_tiles + 1]
+  uint32_t* kcounters;  // [batch, kv_heads, key_tiles], zero between calls
+  float* sums;        // [2 grid] x 128
+  int key_tiles, row_tiles;
 };
 
 template <int D>
@@ -78,7 +82,7 @@ __device__ __forceinline__ int units_of(const Kv4Seq& s, int G, int rt) {
 }
 
 // ---- images ------------------------------------------------------------------------------
-constexpr int kImgThreads = 256;
+constexpr int kImgThreads = 512;
 
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* sm) {
   v = __reduce_max_sync(0xffffffffu, v);
@@ -110,34 +114,57 @@ __device__ __forceinline__ uint32_t high_low(float x) {
          (static_cast<uint32_t>(__half_as_ushort(lo)) << 16);
 }
 
-// 128 tokens of one head.
+// 128 tokens of one head: their records come into shared memory by bulk copies at once (a load
+// for each word, with the images' stores between them, made every word wait for memory).
 template <int D, int NG>
-__device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, int h, int tile) {
+__device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, int h, int tile,
+                         uint8_t* raw) {
   using R = Kv4Record<D, NG>;
-  __shared__ const uint8_t* rec[8];
-  __shared__ uint32_t kp[8][16 * NG], vp[8][16 * NG];
   __shared__ uint32_t red[2][kImgThreads / 32];
+  __shared__ uint64_t bar;
+  __shared__ uint32_t present;  // bit j: record j is there
+  __shared__ uint32_t abort_flag;
   const int tid = threadIdx.x;
   const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
   const int key0 = tile * kTileKeys;
   if (seq.m == 0 || key0 >= seq.n) return;
-  if (tid < 8)
-    rec[tid] = key0 + 16 * tid < seq.n ? kv4_record(a.c, a.c.table, a.c.width, b, h, key0 / 16 + tid,
-                                                    R::kBytes)
-                                       : nullptr;
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    abort_flag = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const uint8_t* src = nullptr;
+    if (tid < 8 && key0 + 16 * tid < seq.n)
+      src = kv4_record(a.c, a.c.table, a.c.width, b, h, key0 / 16 + tid, R::kBytes);
+    const uint32_t have = __ballot_sync(0xffffffffu, src != nullptr);
+    if (tid == 0) {
+      present = have;
+      mbar_arrive_expect_tx(&bar, __popc(have) * R::kBytes);
+    }
+    __syncwarp();
+    if (src != nullptr) bulk_load(raw + tid * R::kBytes, src, R::kBytes, &bar);
+  }
+  __syncthreads();
+  if (!mbar_wait_bounded(&bar, 0u, &abort_flag, a.c.status, a.wait_limit_ns)) {
+    volatile uint32_t no_abort = 0u;  // the copies land before the block exits
+    mbar_wait_bounded(&bar, 0u, &no_abort, a.c.status, a.wait_limit_ns);
+  }
+  // what is not there, and tokens past the length, become 0
+  for (int x = tid; x < 8 * 16 * NG; x += kImgThreads) {
+    const int j = x / (16 * NG), w = x % (16 * NG);
+    if (!((present >> j) & 1u) || key0 + 16 * j + w % 16 >= seq.n) {
+      reinterpret_cast<uint32_t*>(raw + j * R::kBytes + R::kKParams)[w] = 0u;
+      reinterpret_cast<uint32_t*>(raw + j * R::kBytes + R::kVParams)[w] = 0u;
+    }
+  }
   __syncthreads();
   uint32_t ktop = 0, vtop = 0;
   for (int x = tid; x < 8 * 16 * NG; x += kImgThreads) {
     const int j = x / (16 * NG), w = x % (16 * NG);
-    uint32_t k = 0, v = 0;  // tokens past the length become 0
-    if (rec[j] != nullptr && key0 + 16 * j + w % 16 < seq.n) {
-      k = reinterpret_cast<const uint32_t*>(rec[j] + R::kKParams)[w];
-      v = reinterpret_cast<const uint32_t*>(rec[j] + R::kVParams)[w];
-    }
-    kp[j][w] = k;
-    vp[j][w] = v;
-    ktop = max(ktop, reach_bits(k));
-    vtop = max(vtop, reach_bits(v));
+    ktop = max(ktop, reach_bits(reinterpret_cast<const uint32_t*>(raw + j * R::kBytes + R::kKParams)[w]));
+    vtop = max(vtop, reach_bits(reinterpret_cast<const uint32_t*>(raw + j * R::kBytes + R::kVParams)[w]));
   }
   ktop = block_max(ktop, red[0]);
   vtop = block_max(vtop, red[1]);
@@ -152,10 +179,10 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   for (int x = tid; x < kTileKeys * kWords; x += kImgThreads) {
     const int t = x / kWords, w = x % kWords, c = w / R::kBlocks, s = w % R::kBlocks;
     const int d = 32 * s + 8 * c;
-    uint32_t word = 0;
-    if (rec[t / 16] != nullptr)
-      word = reinterpret_cast<const uint32_t*>(rec[t / 16])[(t % 16) * kWords + w];
-    const uint32_t p = kp[t / 16][16 * (d / R::kGroup) + t % 16];
+    const uint8_t* rec = raw + (t / 16) * R::kBytes;
+    const uint32_t word = reinterpret_cast<const uint32_t*>(rec)[(t % 16) * kWords + w];
+    const uint32_t p =
+        reinterpret_cast<const uint32_t*>(rec + R::kKParams)[16 * (d / R::kGroup) + t % 16];
     const float sc = bf16_lo(p) * kf;
     uint32_t out[4];
 #pragma unroll
@@ -170,7 +197,8 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
     uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const uint32_t p = kp[tid / 16][16 * g + tid % 16];
+      const uint32_t p = reinterpret_cast<const uint32_t*>(
+          raw + (tid / 16) * R::kBytes + R::kKParams)[16 * g + tid % 16];
       const uint32_t hl = high_low(fmaf(8.f, bf16_lo(p), bf16_hi(p)) * kf * 128.f);
       w[2 * g] = (hl & 0xFFFFu) * 0x10001u;  // high, high, low, 0
       w[2 * g + 1] = hl >> 16;
@@ -184,17 +212,17 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   for (int x = tid; x < 8 * 8 * R::kBlocks; x += kImgThreads) {
     const int j = x / (8 * R::kBlocks), w = x % (8 * R::kBlocks);
     const int d0 = 32 * (w % R::kBlocks) + 4 * (w / R::kBlocks), g = d0 / R::kGroup;
+    const uint32_t* v_codes = reinterpret_cast<const uint32_t*>(raw + j * R::kBytes + R::kV);
+    const uint32_t* vp = reinterpret_cast<const uint32_t*>(raw + j * R::kBytes + R::kVParams);
     uint32_t word[8];
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
-      word[p] = rec[j] == nullptr ? 0u
-                                  : reinterpret_cast<const uint32_t*>(rec[j] + R::kV)[p * 8 * R::kBlocks + w];
+    for (int p = 0; p < 8; ++p) word[p] = v_codes[p * 8 * R::kBlocks + w];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t out[4][4];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const uint32_t p0 = vp[j][16 * g + 8 * half + 2 * p], p1 = vp[j][16 * g + 8 * half + 2 * p + 1];
+        const uint32_t p0 = vp[16 * g + 8 * half + 2 * p], p1 = vp[16 * g + 8 * half + 2 * p + 1];
         const float s0 = bf16_lo(p0) * vf, m0 = bf16_hi(p0) * vf;
         const float s1 = bf16_lo(p1) * vf, m1 = bf16_hi(p1) * vf;
 #pragma unroll
@@ -279,50 +307,73 @@ __device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   }
 }
 
+// Row tiles that see a token of key tile kt.
+__device__ __forceinline__ int first_row_tile(const Kv4Seq& s, int G, int kt) {
+  const int64_t row = static_cast<int64_t>(kt * kTileKeys - (s.n - s.m)) * G;
+  return row <= 0 ? 0 : static_cast<int>(row / kTileRows);
+}
+// Units of a token tile in the weights' kernel.
+__device__ __forceinline__ int key_units_of(const Kv4Seq& s, int G, int kt) {
+  return max(1, (s.m * G + kTileRows - 1) / kTileRows - first_row_tile(s, G, kt));
+}
+
 // Where every sequence's and row tile's units begin.
-__device__ void plan(const Kv4AttentionArgs& a, const PromptWs& ws) {
+template <typename F>
+__device__ void plan(const Kv4AttentionArgs& a, int64_t* base, int32_t* pre_all, int width,
+                     F units_of_tile) {
   __shared__ int64_t sum[kImgThreads];
-  const int G = a.heads / a.c.kv_heads;
   int64_t before = 0;
   for (int b0 = 0; b0 < a.c.batch; b0 += kImgThreads) {
     const int b = b0 + threadIdx.x;
     int64_t units = 0;
     if (b < a.c.batch) {
       const Kv4Seq s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
-      const int tiles = (s.m * G + kTileRows - 1) / kTileRows;
-      int32_t* pre = ws.pre + static_cast<size_t>(b) * (ws.row_tiles + 1);
+      int32_t* pre = pre_all + static_cast<size_t>(b) * (width + 1);
       int at = 0;
-      for (int rt = 0; rt <= ws.row_tiles; ++rt) {
-        pre[rt] = at;
-        if (rt < tiles) at += units_of(s, G, rt);
+      for (int t = 0; t <= width; ++t) {
+        pre[t] = at;
+        if (t < width) at += units_of_tile(s, t);
       }
       units = static_cast<int64_t>(at) * a.c.kv_heads;
     }
     sum[threadIdx.x] = units;
     __syncthreads();
     int64_t mine = before, all = 0;
-    for (int i = 0; i < kImgThreads; ++i) {
+    const int count = min(kImgThreads, a.c.batch - b0);
+    for (int i = 0; i < count; ++i) {
       if (i < threadIdx.x) mine += sum[i];
       all += sum[i];
     }
-    if (b < a.c.batch) ws.base[b] = mine;
+    if (b < a.c.batch) base[b] = mine;
     before += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) ws.base[a.c.batch] = before;
+  if (threadIdx.x == 0) base[a.c.batch] = before;
 }
 
 template <int D, int NG>
-__global__ void __launch_bounds__(kImgThreads)
+__global__ void __launch_bounds__(kImgThreads, 2)
     kv4_prompt_images_kernel(const Kv4AttentionArgs a, const PromptWs ws) {
+  __shared__ __align__(128) uint8_t raw[8 * Kv4Record<D, NG>::kBytes];
   pdl_launch_dependents();
   pdl_wait();
   int64_t x = blockIdx.x;
   if (x == 0) {
-    plan(a, ws);
+    const int G = a.heads / a.c.kv_heads;
+    plan(a, ws.base, ws.pre, ws.row_tiles, [&](const Kv4Seq& s, int t) {
+      return t * kTileRows < s.m * G ? units_of(s, G, t) : 0;
+    });
     return;
   }
-  --x;
+  if (x == 1) {
+    if (ws.kbase == nullptr) return;
+    const int G = a.heads / a.c.kv_heads;
+    plan(a, ws.kbase, ws.kpre, ws.key_tiles, [&](const Kv4Seq& s, int t) {
+      return t * kTileKeys < s.n ? key_units_of(s, G, t) : 0;
+    });
+    return;
+  }
+  x -= 2;
   const int64_t bh = static_cast<int64_t>(a.c.batch) * a.c.kv_heads;
   if (x < bh * ws.row_tiles) {
     const int i = static_cast<int>(x / ws.row_tiles);
@@ -331,7 +382,8 @@ __global__ void __launch_bounds__(kImgThreads)
   }
   x -= bh * ws.row_tiles;
   const int i = static_cast<int>(x / ws.key_tiles);
-  key_tile<D, NG>(a, ws, i / a.c.kv_heads, i % a.c.kv_heads, static_cast<int>(x % ws.key_tiles));
+  key_tile<D, NG>(a, ws, i / a.c.kv_heads, i % a.c.kv_heads, static_cast<int>(x % ws.key_tiles),
+                  raw);
 }
 
 // ---- tcgen05 -----------------------------------------------------------------------------
@@ -474,35 +526,32 @@ __device__ __forceinline__ bool advance(Segment& g, const Kv4AttentionArgs& a,
   } while (g.lo >= g.hi);
   return true;
 }
+// Largest i < n with x[i] <= u, x non-decreasing from 0.
+template <typename T>
+__device__ __forceinline__ int last_at_most(const T* x, int n, T u) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (x[mid] <= u)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
 // First segment with key tiles of the units [u0, u1); false if there is none.
 __device__ __forceinline__ bool locate(Segment& g, const Kv4AttentionArgs& a, const PromptWs& ws,
                                        int64_t u0, int64_t u1, int G) {
-  int lo = 0, hi = a.c.batch - 1;  // last b with base[b] <= u0
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (ws.base[mid] <= u0)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  g.b = lo;
-  g.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, lo);
-  const int32_t* pre = ws.pre + static_cast<size_t>(lo) * (ws.row_tiles + 1);
-  const int64_t off = u0 - ws.base[lo], per_head = pre[ws.row_tiles];
+  g.b = last_at_most(ws.base, a.c.batch, u0);
+  g.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, g.b);
+  const int32_t* pre = ws.pre + static_cast<size_t>(g.b) * (ws.row_tiles + 1);
+  const int64_t off = u0 - ws.base[g.b], per_head = pre[ws.row_tiles];
   g.h = static_cast<int>(off / per_head);
   const int in_head = static_cast<int>(off % per_head);
-  lo = 0, hi = ws.row_tiles - 1;  // last rt with pre[rt] <= in_head
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (pre[mid] <= in_head)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  g.rt = lo;
+  g.rt = last_at_most(pre, ws.row_tiles, in_head);
   g.left = u1 - u0;
-  g.item_base = u0 - (in_head - pre[lo]);
-  enter(g, ws, in_head - pre[lo]);
+  g.item_base = u0 - (in_head - pre[g.rt]);
+  enter(g, ws, in_head - pre[g.rt]);
   return g.lo < g.hi || advance(g, a, ws, G);
 }
 
@@ -907,22 +956,71 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 }
 
 // ---- weights -----------------------------------------------------------------------------
-// A CTA sums one tile of 128 tokens over its share of the row tiles. 8 warps: a thread a token
-// (TMEM lane) and half of a row tile's 256 columns; S^T is double-buffered in tensor memory.
+// Units are (row tile, token tile) pairs, token tile by token tile, cut evenly over the CTAs. 8
+// warps: a thread a token (TMEM lane) and half of a row tile's 256 columns; S^T is
+// double-buffered in tensor memory. A token tile that a boundary cuts is joined from its parts
+// (128 sums) by whoever arrives last, in order.
 constexpr int kWeightThreads = 320;
 
 template <int D>
 struct WeightSmem {
   static constexpr uint32_t k_off = 0;
-  static constexpr uint32_t q_off = Img<D>::kTile;
+  static constexpr uint32_t q_off = 2 * Img<D>::kTile;
   static constexpr uint32_t lse_off = q_off + 2 * Img<D>::kQ;         // [2][256]
   static constexpr uint32_t sum_off = lse_off + 2 * kTileRows * 4;    // [128]
   static constexpr uint32_t bar_off = sum_off + 128 * 4;
-  // k_full, q_full[2], q_empty[2], s_full[2], s_empty[2], drain
-  static constexpr uint32_t misc_off = bar_off + 10 * 8;
+  // k_full[2], k_empty[2], q_full[2], q_empty[2], s_full[2], s_empty[2], drain
+  static constexpr uint32_t misc_off = bar_off + 13 * 8;
   static constexpr uint32_t total = misc_off + 16;
   static constexpr uint32_t alloc = total + 1024;
 };
+
+struct KeySegment {
+  int b, h, kt;
+  int units;   // row tiles of the token tile
+  int lo, hi;  // of them in this segment
+  int first;   // first row tile
+  int64_t item_base, left;
+  Kv4Seq s;
+};
+__device__ __forceinline__ void enter(KeySegment& g, const PromptWs& ws, int G, int at) {
+  const int32_t* pre = ws.kpre + static_cast<size_t>(g.b) * (ws.key_tiles + 1) + g.kt;
+  g.units = pre[1] - pre[0];
+  g.first = first_row_tile(g.s, G, g.kt);
+  g.lo = at;
+  g.hi = static_cast<int>(min(static_cast<int64_t>(g.units), at + g.left));
+  g.left -= g.hi - g.lo;
+}
+__device__ __forceinline__ bool advance(KeySegment& g, const Kv4AttentionArgs& a,
+                                        const PromptWs& ws, int G) {
+  if (g.left <= 0) return false;
+  g.item_base += g.units;
+  if (++g.kt * kTileKeys >= g.s.n) {
+    g.kt = 0;
+    if (++g.h >= a.c.kv_heads) {
+      g.h = 0;
+      do {
+        if (++g.b >= a.c.batch) return false;
+        g.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, g.b);
+      } while (g.s.n == 0);
+    }
+  }
+  enter(g, ws, G, 0);
+  return true;
+}
+__device__ __forceinline__ void locate(KeySegment& g, const Kv4AttentionArgs& a,
+                                       const PromptWs& ws, int64_t u0, int64_t u1, int G) {
+  g.b = last_at_most(ws.kbase, a.c.batch, u0);
+  g.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, g.b);
+  const int32_t* pre = ws.kpre + static_cast<size_t>(g.b) * (ws.key_tiles + 1);
+  const int64_t off = u0 - ws.kbase[g.b], per_head = pre[ws.key_tiles];
+  g.h = static_cast<int>(off / per_head);
+  const int in_head = static_cast<int>(off % per_head);
+  g.kt = last_at_most(pre, ws.key_tiles, in_head);
+  g.left = u1 - u0;
+  g.item_base = u0 - (in_head - pre[g.kt]);
+  enter(g, ws, G, in_head - pre[g.kt]);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kWeightThreads, 1)
@@ -932,17 +1030,19 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
-  uint64_t *q_full = k_full + 1, *q_empty = q_full + 2, *s_full = q_empty + 2,
-           *s_empty = s_full + 2, *drain = s_empty + 2;
+  uint64_t *k_empty = k_full + 2, *q_full = k_empty + 2, *q_empty = q_full + 2,
+           *s_full = q_empty + 2, *s_empty = s_full + 2, *drain = s_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile uint32_t* abort_flag = tmem_holder + 1;
+  volatile uint32_t* arrived = tmem_holder + 2;
   float* lse_s = reinterpret_cast<float*>(smem + L::lse_off);
   float* sum_s = reinterpret_cast<float*>(smem + L::sum_off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.heads / a.c.kv_heads;
   if (threadIdx.x == 0) {
-    mbar_init(k_full, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
@@ -963,142 +1063,182 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   if (threadIdx.x == 0) pdl_launch_dependents();
   pdl_wait();
 
-  // the last token tiles have the fewest rows: first come the ones with most
-  const int tile = blockIdx.x / ws.splits, split = blockIdx.x % ws.splits;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
-  const int key0 = tile * kTileKeys, rows = seq.m * G;
-  const int tiles = (rows + kTileRows - 1) / kTileRows;
-  // the first row that sees key0, and the row tiles from there in `splits` shares
-  const int first = static_cast<int>(
-      max(static_cast<int64_t>(0), static_cast<int64_t>(key0 - (seq.n - seq.m)) * G) / kTileRows);
-  const int count = max(0, tiles - first);
-  const int r0 = first + static_cast<int>(static_cast<int64_t>(count) * split / ws.splits);
-  const int r1 = first + static_cast<int>(static_cast<int64_t>(count) * (split + 1) / ws.splits);
-  const bool some = key0 < seq.n && r0 < r1;
-  const size_t bh = static_cast<size_t>(b) * a.c.kv_heads + h;
+  const int64_t total = ws.kbase[a.c.batch];
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+  const int64_t me = blockIdx.x;
+  const bool some = me < ctas;
+  KeySegment g;
+  if (some) locate(g, a, ws, total * me / ctas, total * (me + 1) / ctas, G);
   uint32_t* status = a.c.status;
   const uint64_t limit = a.wait_limit_ns;
+  auto head = [&]() { return static_cast<size_t>(g.b) * a.c.kv_heads + g.h; };
   if (!some) {
   } else if (warp == kLoadWarp) {
     if (lane == 0) {
       bool ok = true;
-      mbar_arrive_expect_tx(k_full, Img<D>::kTile);
-      bulk_load(smem + L::k_off, ws.kv_img + (bh * ws.key_tiles + tile) * Img<D>::kPair,
-                Img<D>::kTile, k_full);
-      int n = 0;
-      for (int rt = r0; rt < r1; ++rt, ++n) {
-        const int s = n & 1;
-        if (n >= 2) ok = mbar_wait_bounded(&q_empty[s], (n / 2 - 1) & 1u, abort_flag, status, limit);
+      int n = 0, segs = 0;
+      do {
+        const int ks = segs & 1;
+        if (segs >= 2) ok = mbar_wait_bounded(&k_empty[ks], (segs / 2 - 1) & 1u, abort_flag, status, limit);
         if (!ok) break;
-        mbar_arrive_expect_tx(&q_full[s], Img<D>::kQ);
-        bulk_load(smem + L::q_off + s * Img<D>::kQ, ws.q_img + (bh * ws.row_tiles + rt) * Img<D>::kQ,
-                  Img<D>::kQ, &q_full[s]);
-      }
-      if (!ok) {
+        mbar_arrive_expect_tx(&k_full[ks], Img<D>::kTile);
+        bulk_load(smem + L::k_off + ks * Img<D>::kTile,
+                  ws.kv_img + (head() * ws.key_tiles + g.kt) * Img<D>::kPair, Img<D>::kTile,
+                  &k_full[ks]);
+        ++segs;
+        for (int i = g.lo; i < g.hi; ++i, ++n) {
+          const int s = n & 1;
+          if (n >= 2) ok = mbar_wait_bounded(&q_empty[s], (n / 2 - 1) & 1u, abort_flag, status, limit);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&q_full[s], Img<D>::kQ);
+          bulk_load(smem + L::q_off + s * Img<D>::kQ,
+                    ws.q_img + (head() * ws.row_tiles + g.first + i) * Img<D>::kQ, Img<D>::kQ,
+                    &q_full[s]);
+        }
+      } while (ok && advance(g, a, ws, G));
+      if (!ok) {  // copies in flight land before the CTA exits
         volatile uint32_t no_abort = 0u;
-        mbar_wait_bounded(k_full, 0u, &no_abort, status, limit);
+        for (int i = max(0, segs - 2); i < segs; ++i)
+          mbar_wait_bounded(&k_full[i & 1], (i / 2) & 1u, &no_abort, status, limit);
         for (int i = max(0, n - 2); i < n; ++i)
           mbar_wait_bounded(&q_full[i & 1], (i / 2) & 1u, &no_abort, status, limit);
       }
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t idesc = idesc_f16_f32(128, kTileRows);
-    const uint32_t k_s = desc_low(smem_addr(smem + L::k_off), 16);
-    const uint32_t k_more = desc_low(smem_addr(smem + L::k_off) + Img<D>::kKCodes, kTileKeys * 16);
-    bool ok = mbar_wait_bounded(k_full, 0u, abort_flag, status, limit);
-    for (int n = 0; n < r1 - r0; ++n) {
-      const int s = n & 1;
-      ok = ok && mbar_wait_bounded(&q_full[s], (n / 2) & 1u, abort_flag, status, limit) &&
-           (n < 2 || mbar_wait_bounded(&s_empty[s], (n / 2 - 1) & 1u, abort_flag, status, limit));
+    bool ok = true;
+    int n = 0, segs = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait_bounded(bar, parity, abort_flag, status, limit);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after_sync();
-      const uint32_t q_at = smem_addr(smem + L::q_off) + s * Img<D>::kQ;
-      const uint32_t q_s = desc_low(q_at, 16), q_more = desc_low(q_at + Img<D>::kQCodes, kTileRows * 16);
-      if (elect_one()) {
+      return ok;
+    };
+    do {
+      const int ks = segs & 1;
+      if (!wait(&k_full[ks], (segs / 2) & 1u)) break;
+      ++segs;
+      const uint32_t k_at = smem_addr(smem + L::k_off) + ks * Img<D>::kTile;
+      const uint32_t k_s = desc_low(k_at, 16), k_more = desc_low(k_at + Img<D>::kKCodes, kTileKeys * 16);
+      for (int i = g.lo; i < g.hi; ++i, ++n) {
+        const int s = n & 1;
+        if (!wait(&q_full[s], (n / 2) & 1u)) break;
+        if (n >= 2 && !wait(&s_empty[s], (n / 2 - 1) & 1u)) break;
+        tc_fence_after_sync();
+        const uint32_t q_at = smem_addr(smem + L::q_off) + s * Img<D>::kQ;
+        const uint32_t q_s = desc_low(q_at, 16), q_more = desc_low(q_at + Img<D>::kQCodes, kTileRows * 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ss<kDescSw128>(tmem + s * 256,
-                                k_s + (((kk / 4) * (kTileKeys * 128) + (kk % 4) * 32) >> 4),
-                                q_s + (((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4), idesc,
-                                kk != 0);
-        tc_mma_ss<kDescPlain>(tmem + s * 256, k_more, q_more, idesc, 1u);
-        tc_commit(&q_empty[s]);
-        tc_commit(&s_full[s]);
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma_ss<kDescSw128>(tmem + s * 256,
+                                  k_s + (((kk / 4) * (kTileKeys * 128) + (kk % 4) * 32) >> 4),
+                                  q_s + (((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4), idesc,
+                                  kk != 0);
+          tc_mma_ss<kDescPlain>(tmem + s * 256, k_more, q_more, idesc, 1u);
+          tc_commit(&q_empty[s]);
+          tc_commit(&s_full[s]);
+          if (i + 1 == g.hi) tc_commit(&k_empty[ks]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-    }
+    } while (ok && advance(g, a, ws, G));
     if (elect_one()) tc_commit(drain);
     volatile uint32_t no_abort = 0u;
     mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
   } else {
     const int part = warp >> 2;  // columns 128 part .. 128 part + 127
-    const int key = key0 + (warp & 3) * 32 + lane;
     const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + part * 128;
-    const float kf = ws.meta[bh * ws.key_tiles + tile].kf;
-    float acc = 0.f;
     bool ok = true;
-    for (int n = 0; n < r1 - r0; ++n) {
-      const int s = n & 1, rt = r0 + n;
-      // this warp's 128 columns' log-sums (rows past the end see nothing); warps of a part
-      // write and read their own copy's quarter, all of it after the barrier below
-      const int x = threadIdx.x;  // 0..255
-      const int R = rt * kTileRows + x;
+    int n = 0;
+    // the log-sum of row `threadIdx.x` of a row tile; rows past the end see nothing
+    auto lse_of = [&](int rt) {
+      const int R = rt * kTileRows + threadIdx.x;
       float v = INFINITY;
-      if (R < rows) {
-        v = ws.lse2[static_cast<int64_t>(seq.s0 + R / G) * a.heads + h * G + R % G];
-        if (v == -INFINITY) v = INFINITY;
-      }
-      lse_s[s * kTileRows + x] = v;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      ok = ok && mbar_wait_bounded(&s_full[s], (n / 2) & 1u, abort_flag, status, limit);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        tc_fence_after_sync();
-        const float cf = fmaxf(ws.qf[bh * ws.row_tiles + rt] * kf, 1e-37f);
-        // rows before this one do not see the token
-        const int64_t need = static_cast<int64_t>(key - (seq.n - seq.m)) * G;
-        const int hide = static_cast<int>(
-            max(static_cast<int64_t>(0), min(need - rt * kTileRows - part * 128, static_cast<int64_t>(128))));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float q[32];
-          tmem_ld_32cols(t_s + s * 256 + 32 * c, reinterpret_cast<uint32_t*>(q));
-          tmem_ld_wait();
-          const float* lse = lse_s + s * kTileRows + part * 128 + 32 * c;
-          float a0 = 0.f, a1 = 0.f;
-          const bool cut = __any_sync(0xffffffffu, hide > 32 * c);
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 z = *reinterpret_cast<const float4*>(lse + j);
-            float p0 = ex2(fmaf(q[j], cf, -z.x)), p1 = ex2(fmaf(q[j + 1], cf, -z.y));
-            float p2 = ex2(fmaf(q[j + 2], cf, -z.z)), p3 = ex2(fmaf(q[j + 3], cf, -z.w));
-            if (cut) {
-              if (32 * c + j < hide) p0 = 0.f;
-              if (32 * c + j + 1 < hide) p1 = 0.f;
-              if (32 * c + j + 2 < hide) p2 = 0.f;
-              if (32 * c + j + 3 < hide) p3 = 0.f;
-            }
-            add2(a0, a1, p0, p1);
-            add2(a0, a1, p2, p3);
-          }
-          acc += a0 + a1;
+      if (R < g.s.m * G)
+        v = ws.lse2[static_cast<int64_t>(g.s.s0 + R / G) * a.heads + g.h * G + R % G];
+      return v == -INFINITY ? INFINITY : v;
+    };
+    do {
+      const int key = g.kt * kTileKeys + (warp & 3) * 32 + lane;
+      const float kf = ws.meta[head() * ws.key_tiles + g.kt].kf;
+      float acc = 0.f;
+      float lse_next = lse_of(g.first + g.lo), qf_next = ws.qf[head() * ws.row_tiles + min(g.first + g.lo, ws.row_tiles - 1)];
+      for (int i = g.lo; i < g.hi; ++i, ++n) {
+        const int s = n & 1, rt = g.first + i;
+        lse_s[s * kTileRows + threadIdx.x] = lse_next;
+        const float cf = fmaxf(qf_next * kf, 1e-37f);
+        if (i + 1 < g.hi) {
+          lse_next = lse_of(rt + 1);
+          qf_next = ws.qf[head() * ws.row_tiles + rt + 1];
         }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        ok = ok && mbar_wait_bounded(&s_full[s], (n / 2) & 1u, abort_flag, status, limit);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        tc_fence_after_sync();
+        // rows before this one do not see the token
+        const int64_t need = static_cast<int64_t>(key - (g.s.n - g.s.m)) * G;
+        const int hide = static_cast<int>(max(
+            static_cast<int64_t>(0),
+            min(need - static_cast<int64_t>(rt) * kTileRows - part * 128, static_cast<int64_t>(128))));
+        float q[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_ld_32cols(t_s + s * 256 + 32 * c, reinterpret_cast<uint32_t*>(q) + 32 * c);
+        tmem_ld_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[s]);
+        const float* lse = lse_s + s * kTileRows + part * 128;
+        float p[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!__any_sync(0xffffffffu, hide > 0)) {
+#pragma unroll
+          for (int j = 0; j < 128; j += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(lse + j);
+            add2(p[0], p[1], ex2(fmaf(q[j], cf, -z.x)), ex2(fmaf(q[j + 1], cf, -z.y)));
+            add2(p[2], p[3], ex2(fmaf(q[j + 2], cf, -z.z)), ex2(fmaf(q[j + 3], cf, -z.w)));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) p[j & 3] += j < hide ? 0.f : ex2(fmaf(q[j], cf, -lse[j]));
+        }
+        acc += (p[0] + p[1]) + (p[2] + p[3]);
       }
-    }
-    if (part == 1) sum_s[threadIdx.x & 127] = acc;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (part == 0 && key < seq.n)
-      ws.sums[((static_cast<size_t>(split) * a.c.batch + b) * a.c.kv_heads + h) * ws.key_tiles *
-                  kTileKeys + key] = acc + sum_s[threadIdx.x];
+      // ---- the two column halves, then the other CTAs' parts
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (part == 1) sum_s[threadIdx.x & 127] = acc;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const size_t at = head() * a.weights_stride + key;
+      const bool have = part == 0 && key < g.s.n;
+      auto store = [&](float x) {
+        if (have) a.weights_out[at] = (a.weights != nullptr ? a.weights[at] : 0.f) + x;
+      };
+      if (part == 0) acc += sum_s[threadIdx.x];
+      if (g.s.m == 0) acc = 0.f;  // no rows: nothing has written these tiles
+      if (g.lo == 0 && g.hi == g.units) {
+        store(acc);
+      } else {
+        if (part == 0) __stcg(ws.sums + (2 * me + (g.lo == 0 ? 1 : 0)) * 128 + threadIdx.x, acc);
+        const int64_t i0 = ((g.item_base + 1) * ctas - 1) / total;
+        const int64_t i1 = ((g.item_base + g.units) * ctas - 1) / total;
+        __threadfence();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x == 0) {
+          uint32_t* cnt = ws.kcounters + head() * ws.key_tiles + g.kt;
+          const bool last = atomicAdd(cnt, 1u) == static_cast<uint32_t>(i1 - i0);
+          if (last) *cnt = 0u;
+          *arrived = last ? 1u : 0u;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (*arrived && part == 0) {
+          __threadfence();
+          float x = 0.f;
+          for (int64_t i = i0; i <= i1; ++i)
+            x += __ldcg(ws.sums + (2 * i + (i == i0 ? 1 : 0)) * 128 + threadIdx.x);
+          store(x);
+        }
+      }
+    } while (advance(g, a, ws, G));
   }
-  if (!some && threadIdx.x < 128 && key0 + threadIdx.x < seq.n)
-    ws.sums[((static_cast<size_t>(split) * a.c.batch + b) * a.c.kv_heads + h) * ws.key_tiles *
-                kTileKeys + key0 + threadIdx.x] = 0.f;
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -1108,27 +1248,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   }
 }
 
-__global__ void __launch_bounds__(256) kv4_prompt_add_kernel(const Kv4AttentionArgs a,
-                                                             const PromptWs ws) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int key = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
-  if (key >= seq.n) return;
-  const size_t bh = static_cast<size_t>(b) * a.c.kv_heads + h;
-  float acc = 0.f;
-  for (int s = 0; s < ws.splits; ++s)
-    acc += ws.sums[(static_cast<size_t>(s) * a.c.batch * a.c.kv_heads + bh) * ws.key_tiles *
-                       kTileKeys + key];
-  const size_t at = bh * a.weights_stride + key;
-  a.weights_out[at] = (a.weights != nullptr ? a.weights[at] : 0.f) + acc;
-}
-
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-  size_t base, pre, meta, qf, q_img, kv_img, counters, parts, lse2, sums, total;
-  int key_tiles, row_tiles, splits;
+  size_t base, pre, meta, qf, q_img, kv_img, counters, parts, lse2, kbase, kpre, kcounters, sums,
+      total;
+  int key_tiles, row_tiles;
 };
 
 Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv_heads, int D,
@@ -1138,10 +1263,6 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   const size_t bh = static_cast<size_t>(batch) * kv_heads;
   l.key_tiles = (max_len + kTileKeys - 1) / kTileKeys;
   l.row_tiles = static_cast<int>((static_cast<int64_t>(max_new) * G + kTileRows - 1) / kTileRows);
-  // row shares of a token tile in the weights' kernel: about four CTAs an SM
-  const int64_t ctas = static_cast<int64_t>(bh) * l.key_tiles;
-  const int64_t want = (4 * static_cast<int64_t>(device_sm_count()) + ctas - 1) / ctas;
-  l.splits = static_cast<int>(want < l.row_tiles ? want : l.row_tiles);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -1149,6 +1270,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
     return here;
   };
   l.counters = take(bh * l.row_tiles * 2 * 4);
+  if (weights) l.kcounters = take(bh * l.key_tiles * 4);
   l.base = take((static_cast<size_t>(batch) + 1) * 8);
   l.pre = take(static_cast<size_t>(batch) * (l.row_tiles + 1) * 4);
   l.meta = take(bh * l.key_tiles * sizeof(KeyMeta));
@@ -1158,7 +1280,9 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   l.parts = take(static_cast<size_t>(device_sm_count()) * 4 * (D + 2) * 128 * 4);
   if (weights) {
     l.lse2 = take(static_cast<size_t>(tokens) * heads * 4);
-    l.sums = take(static_cast<size_t>(l.splits) * bh * l.key_tiles * kTileKeys * 4);
+    l.kbase = take((static_cast<size_t>(batch) + 1) * 8);
+    l.kpre = take(static_cast<size_t>(batch) * (l.key_tiles + 1) * 4);
+    l.sums = take(static_cast<size_t>(device_sm_count()) * 2 * 128 * 4);
   }
   l.total = at;
   return l;
@@ -1180,12 +1304,14 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   ws.counters = reinterpret_cast<uint32_t*>(w + l.counters);
   ws.parts = reinterpret_cast<float*>(w + l.parts);
   ws.lse2 = weights ? reinterpret_cast<float*>(w + l.lse2) : nullptr;
+  ws.kbase = weights ? reinterpret_cast<int64_t*>(w + l.kbase) : nullptr;
+  ws.kpre = reinterpret_cast<int32_t*>(w + l.kpre);
+  ws.kcounters = reinterpret_cast<uint32_t*>(w + l.kcounters);
   ws.sums = reinterpret_cast<float*>(w + l.sums);
   ws.key_tiles = l.key_tiles;
   ws.row_tiles = l.row_tiles;
-  ws.splits = l.splits;
   const int64_t bh = static_cast<int64_t>(a.c.batch) * a.c.kv_heads;
-  const int64_t blocks = 1 + bh * (l.row_tiles + l.key_tiles);
+  const int64_t blocks = 2 + bh * (l.row_tiles + l.key_tiles);
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaError_t e = launch_with_pdl(kv4_prompt_images_kernel<D, NG>,
                                   dim3(static_cast<unsigned>(blocks)), dim3(kImgThreads), 0, stream,
@@ -1201,12 +1327,8 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   auto wkern = kv4_prompt_weights_kernel<D>;
   e = set_max_dynamic_smem(reinterpret_cast<const void*>(wkern), WeightSmem<D>::alloc);
   if (e != cudaSuccess) return e;
-  e = launch_with_pdl(wkern, dim3(l.key_tiles * l.splits, a.c.kv_heads, a.c.batch),
-                      dim3(kWeightThreads), WeightSmem<D>::alloc, stream, a, ws);
-  if (e != cudaSuccess) return e;
-  return launch_with_pdl(kv4_prompt_add_kernel,
-                         dim3((a.max_len + 255) / 256, a.c.kv_heads, a.c.batch), dim3(256), 0,
-                         stream, a, ws);
+  return launch_with_pdl(wkern, dim3(grid), dim3(kWeightThreads), WeightSmem<D>::alloc, stream, a,
+                         ws);
 }
 
 }  // namespace
