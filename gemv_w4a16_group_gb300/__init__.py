@@ -31,6 +31,7 @@ Formats ("Low-Precision Kernels: INT4, INT8 and FP8 Matmuls, Measured", Step 2;
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -144,13 +145,17 @@ _lib = _load()
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream() builds a Stream object: 3 us of a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> int:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
+            and t.is_cuda and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -651,20 +656,31 @@ def _tokens(t: torch.Tensor, name: str):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    tokens, heads, dim = t.shape
+    step, head_step, dim_step = t.stride()
+    if dim_step != 1 or (heads > 1 and head_step != dim):
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with dense heads")
-    dense = t.shape[1] * t.shape[2]
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else dense)
+    return t.data_ptr(), (step if tokens > 1 else heads * dim)
 
 
 def _kv4_weights(t, name: str, batch: int, kv_heads: int):
     if t is None:
         return None, 0
-    if t.dim() != 3 or tuple(t.shape[:2]) != (batch, kv_heads):
+    if t.dim() != 3 or t.shape[0] != batch or t.shape[1] != kv_heads:
         raise ValueError(f"{name} must be [{batch}, {kv_heads}, length]")
     return _dev(t, name, torch.float32), t.shape[2]
+
+
+def _on(stream):
+    """Context in which a result for a call on `stream` is allocated (the caching allocator
+    reuses a freed block in the order of the stream it was allocated on)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext()
 
 
 def kv4_append(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -673,15 +689,16 @@ def kv4_append(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
     """Quantizes k and v (bf16 [tokens, kv_heads, head_dim], tokens may be strided) into the
     cache. ``lens`` counts the new tokens, ``starts`` int32 [batch + 1] are their offsets; the
     entries of the new tokens in ``weights`` (fp32 [batch, kv_heads, length]) become 0."""
-    c = _kv4(cache, table, lens, k.shape[-1], group)
+    tokens, heads, head_dim = k.shape
+    c = _kv4(cache, table, lens, head_dim, group)
     kp, ks = _tokens(k, "k")
     vp, vs = _tokens(v, "v")
-    if k.shape != v.shape or k.shape[1] != c.kv_heads:
+    if k.shape != v.shape or heads != c.kv_heads:
         raise ValueError("k and v must have the same shape and the cache's heads")
     wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
     _check("kv4_append", _lib.kv4_append(
-        c, _dev(starts, "starts", torch.int32, (c.batch + 1,)), kp, ks, vp, vs, k.shape[0], wp,
-        wl, _stream(stream)))
+        c, _dev(starts, "starts", torch.int32, (c.batch + 1,)), kp, ks, vp, vs, tokens, wp, wl,
+        _stream(stream)))
     return cache
 
 
@@ -691,10 +708,12 @@ def kv4_read(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, start
     each sequence as the cache holds them."""
     c = _kv4(cache, table, lens, head_dim, group)
     shape = (tokens, c.kv_heads, head_dim)
-    if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    if k is None or v is None:
+        with _on(stream):
+            if k is None:
+                k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+            if v is None:
+                v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
     _check("kv4_read", _lib.kv4_read(
         c, _dev(starts, "starts", torch.int32, (c.batch + 1,)),
         _dev(k, "k", torch.bfloat16, shape), _dev(v, "v", torch.bfloat16, shape), tokens,
@@ -723,14 +742,13 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
     T, heads, head_dim = q.shape
     c = _kv4(cache, table, lens, head_dim, group)
     qp, qs = _tokens(q, "q")
-    on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_stream(q.device)
     if workspace is None:
-        with torch.cuda.stream(on):
+        with _on(stream):
             workspace = torch.zeros(kv4_attention_workspace_bytes(
                 c.batch, T, max_new, max_len, heads, c.kv_heads, head_dim, group,
                 weights_out is not None), dtype=torch.uint8, device=q.device)
     if out is None:
-        with torch.cuda.stream(on):
+        with _on(stream):
             out = torch.empty((T, heads, head_dim), dtype=torch.bfloat16, device=q.device)
     wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
     op, ol = _kv4_weights(weights_out, "weights_out", c.batch, c.kv_heads)
@@ -755,13 +773,15 @@ def kv4_evict(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weig
     each head move to the pages of ``out_table``."""
     c = _kv4(cache, table, lens, head_dim, group)
     wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
-    if kept is None:
-        kept = torch.empty((c.batch, c.kv_heads, budget), dtype=torch.int32, device=cache.device)
-    if new_lens is None:
-        new_lens = torch.empty((c.batch,), dtype=torch.int32, device=cache.device)
-    if weights_out is None:
-        weights_out = torch.empty((c.batch, c.kv_heads, budget), dtype=torch.float32,
-                                  device=cache.device)
+    if kept is None or new_lens is None or weights_out is None:
+        shape, dev = (c.batch, c.kv_heads, budget), cache.device
+        with _on(stream):
+            if kept is None:
+                kept = torch.empty(shape, dtype=torch.int32, device=dev)
+            if new_lens is None:
+                new_lens = torch.empty(shape[:1], dtype=torch.int32, device=dev)
+            if weights_out is None:
+                weights_out = torch.empty(shape, dtype=torch.float32, device=dev)
     op, ol = _kv4_weights(weights_out, "weights_out", c.batch, c.kv_heads)
     if out_table.dim() != 2 or out_table.shape[0] != c.batch:
         raise ValueError("out_table must be [batch, width]")

@@ -3,17 +3,18 @@
 //   s_ij = scale q_i . k_hat_j (j <= n - m + i),  p = softmax_j(s),  out_i = sum_j p_ij v_hat_j
 //
 // Rows are the (new token, query head) pairs that share a key/value head, 8 NT of them a tile.
-// With c the code less 8 (c - 8 and c are both exact small numbers), s the scale and m the minimum
-// plus 8 s, of a dim's group g,
+// With c the code, s the scale and m the minimum of a dim's group g,
 //   q . k_hat_j = sum_g s_jg (sum_{d in g} q_d c_jd) + m_jg (sum_{d in g} q_d)
 //   sum_j p_j v_hat_jd = sum_j (p_j s_jg) c_jd + sum_j p_j m_jg
-// so the codes go to the tensor pipe as they are, as FP16 pairs (one LOP3 and one HFMA2 a pair),
-// and the scales touch one number a token and group. The codes are centred because the MMA
-// truncates its sums: left as 1024 + c or 128 + c the offset's own sum, hundreds of times the
-// result over a long cache, took 1.2 % of it (131072 tokens). q is FP16 under a power of two a
-// row, exact down to 2^-31 of the row's largest; p s is rounded to FP16 under the largest scale's
-// power of two that the row has met (relative 2^-12; BF16's 2^-9 was twice the output's own
-// rounding error). Sums, maxima and the softmax's statistics are fp32.
+// so the codes go to the tensor pipe as they are, and the scales touch one number a token and
+// group. A code masked out of its word is an FP16 subnormal, c 2^-24 (or c 2^-20 for the nibble
+// above), which the MMA multiplies exactly: five operations for eight codes. (128 + c or 1024 + c
+// needs the offset's sum taken out again; the MMA truncates its sums, and over 131072 tokens the
+// offset, hundreds of times the result, cost 1.2 % of it. Centring the pairs cures that for four
+// more operations.) q is FP16 under a power of two a row, exact down to 2^-27 of the row's
+// largest; p s is rounded to FP16 under the largest scale's power of two that the row has met
+// (relative 2^-12; BF16's 2^-9 was twice the output's own rounding error). Sums, maxima and the
+// softmax's statistics are fp32.
 //
 // What bounds it: the cache is read once (D + 8 D / group bytes a token and head), at 4 heads a
 // key/value head about 8 operations a byte, so the aim is the memory's rate.
@@ -32,8 +33,13 @@ namespace w4k {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kUnit = 64;  // tokens
+constexpr int kUnit = 32;  // tokens
 constexpr int kUnitRecords = kUnit / 16;
+// Units that stand for what an item (sequence, head, row tile) costs beyond its own: loading its
+// queries, joining the warps, writing its rows. They come before its units in the list. Without
+// them the CTA that got the shortest sequences of a ragged batch (0, 1, 17 .. 4096 tokens, 32
+// sequences of 8 heads) took 42 us, its neighbours 10.
+constexpr int kItemCost = 6;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -43,17 +49,18 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   return d;
 }
 
-// FP16 pairs (q - 8, q' - 8) of nibbles i and i + 4, i = 0..3.
-__device__ __forceinline__ void centred_pairs(uint32_t w, uint32_t (&p)[4]) {
-  code_pairs_f16(w, p);  // 1024 + q (even i) and 1024 + 16 q (odd i)
-  const __half2 one = __float2half2_rn(1.f), off = __float2half2_rn(-1032.f);
-  const __half2 frac = __float2half2_rn(0.0625f), off16 = __float2half2_rn(-72.f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __half2 x = *reinterpret_cast<__half2*>(&p[i]);
-    x = i % 2 == 0 ? __hfma2(x, one, off) : __hfma2(x, frac, off16);
-    p[i] = *reinterpret_cast<uint32_t*>(&x);
-  }
+// FP16 pairs of nibbles i and i + 4: q 2^-24 for even i, q 2^-20 for odd i.
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&p)[4]) {
+  p[0] = w & 0x000F000Fu;
+  p[1] = w & 0x00F000F0u;
+  p[2] = (w >> 8) & 0x000F000Fu;
+  p[3] = (w >> 8) & 0x00F000F0u;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <int NB>
@@ -84,7 +91,7 @@ struct Workspace {
 // (its rows are still to be written).
 struct Work {
   Kv4Seq s;
-  int tiles, chunks;
+  int tiles, chunks;  // row tiles, units of each
 };
 template <int ROWS>
 __device__ __forceinline__ Work work_of(const Kv4AttentionArgs& a, int group, int b) {
@@ -99,21 +106,26 @@ __device__ __forceinline__ Work work_of(const Kv4AttentionArgs& a, int group, in
 struct Cursor {
   int b, h, tile;      // segment
   Work w;
-  int lo, hi;          // the segment's units in this CTA's range
-  int64_t left;        // units of the range after this segment's
+  int lo, hi;          // the item's units in this CTA's range
+  uint32_t base;       // the item's first place in the list
+  uint32_t left;       // places of the range after this segment's
 };
 
 template <int ROWS>
 __device__ __forceinline__ void enter(Cursor& c, const Kv4AttentionArgs& a, int first) {
-  c.lo = first;
-  c.hi = static_cast<int>(min(static_cast<int64_t>(c.w.chunks), first + c.left));
-  c.left -= c.hi - c.lo;
+  const int end = static_cast<int>(min(static_cast<uint32_t>(kItemCost + c.w.chunks), first + c.left));
+  c.left -= end - first;
+  c.lo = max(0, first - kItemCost);
+  c.hi = max(0, end - kItemCost);
 }
 
-// Next segment of the range; false at its end.
+// Next segment of the range that has units (the range's end may hold only an item's cost); false
+// at its end. `base` is the item's place in the list.
 template <int ROWS>
 __device__ __forceinline__ bool advance(Cursor& c, const Kv4AttentionArgs& a, int group) {
-  if (c.left <= 0) return false;
+  do {
+  if (c.left == 0) return false;
+  c.base += kItemCost + c.w.chunks;
   if (++c.tile >= c.w.tiles) {
     c.tile = 0;
     if (++c.h >= a.c.kv_heads) {
@@ -125,8 +137,12 @@ __device__ __forceinline__ bool advance(Cursor& c, const Kv4AttentionArgs& a, in
     }
   }
   enter<ROWS>(c, a, 0);
+  } while (c.lo >= c.hi);
   return true;
 }
+
+// Resident CTAs an SM, by registers (168 or 255 a thread).
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 
 template <int D, int NG, int NT, int STAGES>
 struct Shape {
@@ -142,7 +158,7 @@ struct Shape {
 };
 
 template <int D, int NG, int NT, int STAGES, bool LOGITS>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
     kv4_attention_kernel(const Kv4AttentionArgs a, const Workspace ws) {
   using R = Kv4Record<D, NG>;
   using S = Shape<D, NG, NT, STAGES>;
@@ -164,75 +180,88 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   pdl_launch_dependents();
   pdl_wait();
 
-  // This CTA's range of units.
-  int64_t total = 0;
-  for (int base = 0; base < a.c.batch; base += 32) {
-    int64_t u = 0;
-    if (base + lane < a.c.batch) {
-      const Work w = work_of<kRows>(a, G, base + lane);
-      u = static_cast<int64_t>(w.tiles) * w.chunks * a.c.kv_heads;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    total += u;
-  }
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + kWarps - 1) / kWarps);
-  const int64_t me = blockIdx.x;
+  // This CTA's range of units: lane by lane the sequences' units, and among them the range's
+  // beginning.
+  uint32_t total = 0;
+  auto units_of = [&](int b, Work& w) {
+    if (b >= a.c.batch) return 0u;
+    w = work_of<kRows>(a, G, b);
+    return static_cast<uint32_t>(w.tiles) * (kItemCost + w.chunks) * a.c.kv_heads;
+  };
+  Work mine;
+  for (int base = 0; base < a.c.batch; base += 32)
+    total += __reduce_add_sync(0xffffffffu, units_of(base + lane, mine));
+  const uint32_t ctas = min(gridDim.x, (total + kWarps - 1) / kWarps), me = blockIdx.x;
   if (me >= ctas) return;
-  const int64_t u0 = total * me / ctas, u1 = total * (me + 1) / ctas;
-  if (u0 >= u1) return;
+  const Shares shares(total, ctas);
+  const uint32_t u0 = shares.begin(me), u1 = shares.begin(me + 1);
 
   Cursor cur;
-  int64_t seg_base = 0;  // first unit of the current segment
   {
-    int64_t before = 0;
-    int b = 0;
-    for (;; ++b) {
-      const Work w = work_of<kRows>(a, G, b);
-      const int64_t u = static_cast<int64_t>(w.tiles) * w.chunks * a.c.kv_heads;
-      if (u0 < before + u) {
-        cur.w = w;
+    uint32_t before = 0;
+    for (int base = 0;; base += 32) {
+      const uint32_t u = units_of(base + lane, mine);
+      uint32_t upto = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, u0 < before + upto);
+      if (hit != 0) {
+        const int at = __ffs(hit) - 1;
+        before += __shfl_sync(0xffffffffu, upto - u, at);
+        cur.b = base + at;
+        cur.w.s.n = __shfl_sync(0xffffffffu, mine.s.n, at);
+        cur.w.s.m = __shfl_sync(0xffffffffu, mine.s.m, at);
+        cur.w.s.s0 = __shfl_sync(0xffffffffu, mine.s.s0, at);
+        cur.w.tiles = __shfl_sync(0xffffffffu, mine.tiles, at);
+        cur.w.chunks = __shfl_sync(0xffffffffu, mine.chunks, at);
         break;
       }
-      before += u;
+      before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    const int64_t seg = (u0 - before) / cur.w.chunks;
-    cur.b = b;
+    const uint32_t per = kItemCost + cur.w.chunks, seg = (u0 - before) / per;
     cur.h = static_cast<int>(seg / cur.w.tiles);
     cur.tile = static_cast<int>(seg % cur.w.tiles);
     cur.left = u1 - u0;
-    seg_base = before + seg * cur.w.chunks;
-    enter<kRows>(cur, a, static_cast<int>(u0 - seg_base));
+    cur.base = before + seg * per;
+    enter<kRows>(cur, a, static_cast<int>(u0 - cur.base));
+    if (cur.lo >= cur.hi && !advance<kRows>(cur, a, G)) return;
   }
 
-  // Ring: this warp's units in order, STAGES - 1 ahead of the one it computes on.
+  // Ring: this warp's units in order, STAGES - 1 ahead of the one it computes on. A unit's page
+  // numbers are looked up a unit before its copies are issued.
   const uint32_t ring = smem_addr(smem) + warp * STAGES * S::stage_bytes;
   uint64_t* full = bars + warp * STAGES;
+  const int run = min(1 << (a.c.page_shift - 4), kUnitRecords);  // records a copy, in one page
   Cursor pre = cur;
-  int pre_unit = cur.lo + warp;
+  int pre_unit = cur.lo + warp, pre_records = 0, pre_page = 0;
   bool pre_more = true;
   int filled = 0, used = 0;  // units loaded, units computed
   bool ok = true;
-  auto fill = [&]() {
+  auto look = [&]() {
     while (pre_more && pre_unit >= pre.hi) {
       pre_more = advance<kRows>(pre, a, G);
       pre_unit = pre.lo + warp;
     }
+    if (!pre_more) return;
+    pre_records = min(kUnitRecords, (pre.w.s.n + 15) / 16 - pre_unit * kUnitRecords);
+    if (lane < pre_records && lane % run == 0)
+      pre_page = a.c.table[static_cast<size_t>(pre.b) * a.c.width +
+                           ((pre_unit * kUnitRecords + lane) >> (a.c.page_shift - 4))];
+  };
+  auto fill = [&]() {
     if (!pre_more || !ok) return;
     const int stage = filled % STAGES;
-    const int records = min(kUnitRecords, (pre.w.s.n + 15) / 16 - pre_unit * kUnitRecords);
-    // one copy a run of records within a page; lane i looks the run of record i up
-    const int per_page = 1 << (a.c.page_shift - 4);
-    const int run = min(per_page, kUnitRecords);
+    const bool mine = lane < pre_records && lane % run == 0;
     const uint8_t* src = nullptr;
-    if (lane < records && lane % run == 0)
-      src = kv4_record(a.c, a.c.table, a.c.width, pre.b, pre.h, pre_unit * kUnitRecords + lane,
-                       R::kBytes);
-    const uint32_t bytes = src == nullptr ? 0u : min(run, records - lane) * R::kBytes;
-    uint32_t sum = bytes;
-#pragma unroll
-    for (int o = 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncwarp();
+    if (mine)
+      src = kv4_in_page(a.c, pre_page, pre.h, pre_unit * kUnitRecords + lane, R::kBytes);
+    uint32_t sum = pre_records * R::kBytes;
+    const uint32_t bytes = src == nullptr ? 0u : min(run, pre_records - lane) * R::kBytes;
+    if (__any_sync(0xffffffffu, mine && src == nullptr))
+      sum = __reduce_add_sync(0xffffffffu, bytes);
     if (lane == 0) mbar_arrive_expect_tx(&full[stage], sum);
     __syncwarp();
     if (src != nullptr)
@@ -240,11 +269,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 &full[stage]);
     ++filled;
     pre_unit += kWarps;
+    look();
   };
+  look();
 #pragma unroll 1
   for (int i = 0; i < STAGES - 1; ++i) fill();
 
-  const float scale2 = a.scale * kLog2e;
+  const float scale2 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e;
   for (;;) {
     // ---- one segment
     const Kv4Seq seq = cur.w.s;
@@ -252,7 +283,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     const int rows = min(kRows, rows_all - row0);
     uint32_t q[NT][NB][4];   // FP16 under the row's power of two
     float sq[NT][NG][2];     // sums of q over a group's dims, rows 2c, 2c + 1
-    float unscale[NT][2];    // scale log2(e) / power of two of rows 2c, 2c + 1
+    float unscale[NT][2];    // makes a sum of products of rows 2c, 2c + 1 a logit (base 2)
     int last_key[NT][2];     // last visible key of rows 2c, 2c + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -275,26 +306,31 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       // 2^e brings the row's largest to [2^14, 2^15)
       const int ex = static_cast<int>(top >> 7);
       const int up = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -126), 126);
-      const float f = pow2f(up);
+      // pairs 1 and 3 meet codes times 16
+      const float f = a.scale < 0.f ? -pow2f(up) : a.scale > 0.f ? pow2f(up) : 0.f;
+      const float f16 = f * 0.0625f;
 #pragma unroll
       for (int s = 0; s < NB; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          q[nt][s][i] = f16x2_bits(bf16_lo(q[nt][s][i]) * f, bf16_hi(q[nt][s][i]) * f);
+          q[nt][s][i] = f16x2_bits(bf16_lo(q[nt][s][i]) * (i % 2 ? f16 : f),
+                                   bf16_hi(q[nt][s][i]) * (i % 2 ? f16 : f));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int rr = nt * 8 + 2 * c + i;
         last_key[nt][i] = rr < rows ? seq.n - seq.m + (row0 + rr) / G : -1;
-        unscale[nt][i] = scale2 * pow2f(-__shfl_sync(0xffffffffu, up, (2 * c + i) * 4));
+        // products are codes' 2^24 too small; the sums below carry the same factor
+        unscale[nt][i] = fmaxf(
+            scale2 * 16777216.f * pow2f(-__shfl_sync(0xffffffffu, up, (2 * c + i) * 4)), 1e-37f);
       }
-      constexpr uint32_t ones = 0x3C003C00u;
+      constexpr uint32_t one = 0x00010001u, one16 = 0x00100010u;  // code 1
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = g * NB / NG; s < (g + 1) * NB / NG; ++s) {
-          mma_f16_16816(acc, ones, ones, ones, ones, q[nt][s][0], q[nt][s][1]);
-          mma_f16_16816(acc, ones, ones, ones, ones, q[nt][s][2], q[nt][s][3]);
+          mma_f16_16816(acc, one, one, one16, one16, q[nt][s][0], q[nt][s][1]);
+          mma_f16_16816(acc, one, one, one16, one16, q[nt][s][2], q[nt][s][3]);
         }
         sq[nt][g][0] = acc[0];
         sq[nt][g][1] = acc[1];
@@ -336,7 +372,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       const int key0 = unit * kUnit;
       const int records = min(kUnitRecords, (seq.n - key0 + 15) / 16);
       const bool masked = key0 + kUnit > clear;
-      // ---- logits, base 2
+      // ---- logits, times 1 / unscale
       float s[kUnitRecords][NT][4];
 #pragma unroll
       for (int j = 0; j < kUnitRecords; ++j) {
@@ -355,8 +391,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         for (int g = 0; g < NG; ++g) {
           const uint32_t p0 = lds32(rec + R::kKParams + (16 * g + r) * 4);
           const uint32_t p1 = lds32(rec + R::kKParams + (16 * g + r + 8) * 4);
-          const float s0 = bf16_lo(p0), s1 = bf16_lo(p1);
-          const float m0 = fmaf(8.f, s0, bf16_hi(p0)), m1 = fmaf(8.f, s1, bf16_hi(p1));
+          const float s0 = bf16_lo(p0), s1 = bf16_lo(p1), m0 = bf16_hi(p0), m1 = bf16_hi(p1);
           float acc[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -365,8 +400,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
           for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
             uint32_t k0[4], k1[4];
-            centred_pairs(w0[x], k0);
-            centred_pairs(w1[x], k1);
+            code_pairs(w0[x], k0);
+            code_pairs(w1[x], k1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_f16_16816(acc[nt], k0[0], k1[0], k0[1], k1[1], q[nt][x][0], q[nt][x][1]);
@@ -377,14 +412,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float t = fmaf(i < 2 ? s0 : s1, acc[nt][i], (i < 2 ? m0 : m1) * sq[nt][g][i & 1]);
-              s[j][nt][i] = g == 0 ? t : s[j][nt][i] + t;
+              const float m = i < 2 ? m0 : m1, sum_q = sq[nt][g][i & 1];
+              s[j][nt][i] = fmaf(i < 2 ? s0 : s1, acc[nt][i],
+                                 g == 0 ? m * sum_q : fmaf(m, sum_q, s[j][nt][i]));
             }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[j][nt][i] *= unscale[nt][i & 1];
         if (masked) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -402,7 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
               const int key = key0 + 16 * j + r + (i >= 2 ? 8 : 0);
               if (rr < rows && key < seq.n)
                 ws.logits[((static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) * a.max_new * G +
-                           row0 + rr) * ws.row_len + key] = s[j][nt][i];
+                           row0 + rr) * ws.row_len + key] = s[j][nt][i] * unscale[nt][i & 1];
             }
         }
       }
@@ -456,10 +488,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          const float now = fmaxf(mx[nt][i], v);
+          const float now = fmaxf(mx[nt][i], v * unscale[nt][i]);
           const int ev_now = max(ev[nt][i], unit_ev[nt][i]);
-          alpha[nt][i] = now == -INFINITY ? 1.f : exp2f(mx[nt][i] - now);
-          beta[nt][i] = alpha[nt][i] * exp2f(static_cast<float>(ev[nt][i] - ev_now));
+          alpha[nt][i] = now == -INFINITY ? 1.f : ex2(mx[nt][i] - now);
+          beta[nt][i] = alpha[nt][i] * ex2(static_cast<float>(ev[nt][i] - ev_now));
           grow |= now > mx[nt][i] || ev_now > ev[nt][i];
           mx[nt][i] = now;
           ev[nt][i] = ev_now;
@@ -482,11 +514,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
               }
           }
       }
-      float down[NT][2];  // 2^-ev
+      float down[NT][2], top[NT][2];  // 2^-ev; the maximum, 0 while nothing is visible
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) down[nt][i] = pow2f(127 - min(ev[nt][i], 250));
+        for (int i = 0; i < 2; ++i) {
+          down[nt][i] = pow2f(127 - min(ev[nt][i], 250));
+          top[nt][i] = mx[nt][i] == -INFINITY ? 0.f : mx[nt][i];
+        }
       // ---- P V
 #pragma unroll
       for (int j = 0; j < kUnitRecords; ++j) {
@@ -495,45 +530,47 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         uint32_t w0[NB], w1[NB];
         load_words<NB>(rec + R::kV + ((c * 8 + r) * NB) * 4, w0);
         load_words<NB>(rec + R::kV + (((c + 4) * 8 + r) * NB) * 4, w1);
-        float p[NT][4];
+        float p[NT][4], pd[NT][4];  // p, and p under the scales' power of two
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float m = mx[nt][i & 1];
-            p[nt][i] = m == -INFINITY ? 0.f : exp2f(s[j][nt][i] - m);
+            p[nt][i] = ex2(fmaf(s[j][nt][i], unscale[nt][i & 1], -top[nt][i & 1]));
             sum[nt][i & 1] += p[nt][i];
+            pd[nt][i] = p[nt][i] * down[nt][i & 1];
           }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const uint32_t p0 = lds32(rec + R::kVParams + (16 * g + r) * 4);
           const uint32_t p1 = lds32(rec + R::kVParams + (16 * g + r + 8) * 4);
-          const float s0 = bf16_lo(p0), s1 = bf16_lo(p1);
-          const float m0 = fmaf(8.f, s0, bf16_hi(p0)), m1 = fmaf(8.f, s1, bf16_hi(p1));
+          const float s0 = bf16_lo(p0), s1 = bf16_lo(p1), m0 = bf16_hi(p0), m1 = bf16_hi(p1);
           uint32_t b0[NT], b1[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float x[4], y[4];
+            float x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[i] = p[nt][i] * ((i < 2 ? s0 : s1) * down[nt][i & 1]);
-              y[i] = p[nt][i] * (i < 2 ? m0 : m1);
-            }
-            if (masked) {  // a hidden token's parameters may hold anything, NaN included
+            for (int i = 0; i < 4; ++i) x[i] = pd[nt][i] * (i < 2 ? s0 : s1);
+            if (!masked) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (s[j][nt][i] == -INFINITY) x[i] = y[i] = 0.f;
+                corr[nt][g][i & 1] = fmaf(p[nt][i], i < 2 ? m0 : m1, corr[nt][g][i & 1]);
+            } else {  // a hidden token's parameters may hold anything, NaN included
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (s[j][nt][i] == -INFINITY)
+                  x[i] = 0.f;
+                else
+                  corr[nt][g][i & 1] = fmaf(p[nt][i], i < 2 ? m0 : m1, corr[nt][g][i & 1]);
+              }
             }
-            corr[nt][g][0] += y[0] + y[2];
-            corr[nt][g][1] += y[1] + y[3];
             b0[nt] = movmatrix_trans(f16x2_bits(x[0], x[1]));
             b1[nt] = movmatrix_trans(f16x2_bits(x[2], x[3]));
           }
 #pragma unroll
           for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
             uint32_t v0[4], v1[4];
-            centred_pairs(w0[x], v0);
-            centred_pairs(w1[x], v1);
+            code_pairs(w0[x], v0);
+            code_pairs(w1[x], v1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_f16_16816(o[nt][x][0], v0[0], v0[1], v1[0], v1[1], b0[nt], b1[nt]);
@@ -565,15 +602,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
         for (int x = 0; x < NB; ++x) {
           const float k = corr[nt][x / (NB / NG)][i];
-          const float f = pow2f(min(ev[nt][i], 250) - 127);
+          // sums of codes' 2^-24 (2^-20 for odd dims) under 2^-ev
+          const float f = pow2f(min(ev[nt][i], 250) - 127) * 16777216.f, f16 = f * 0.0625f;
           *reinterpret_cast<float4*>(sm_o + (warp * kRows + row) * D + 32 * x + 4 * r) =
-              make_float4(fmaf(o[nt][x][0][i], f, k), fmaf(o[nt][x][0][i + 2], f, k),
-                          fmaf(o[nt][x][1][i], f, k), fmaf(o[nt][x][1][i + 2], f, k));
+              make_float4(fmaf(o[nt][x][0][i], f, k), fmaf(o[nt][x][0][i + 2], f16, k),
+                          fmaf(o[nt][x][1][i], f, k), fmaf(o[nt][x][1][i + 2], f16, k));
         }
       }
     __syncthreads();
     const bool whole = cur.lo == 0 && cur.hi == cur.w.chunks;
-    float* part = ws.parts + (2 * me + (cur.lo == 0 ? 1 : 0)) * S::part_floats;
+    auto part_of = [&](uint32_t cta, bool first) {
+      return ws.parts + static_cast<size_t>(2 * cta + (first ? 1 : 0)) * S::part_floats;
+    };
+    float* part = part_of(me, cur.lo == 0);
     // (value, max, sum) of a row's dims 4 e .. 4 e + 3 -> output
     auto store = [&](int row, int e, float4 v, float m, float l) {
       const int rr = row0 + row;
@@ -616,44 +657,66 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
     if (!whole) {
       // CTAs i0 .. i1 share the segment; the one that arrives last joins their parts in order.
-      const int64_t i0 = ((seg_base + 1) * ctas - 1) / total;
-      const int64_t i1 = ((seg_base + cur.w.chunks) * ctas - 1) / total;
+      const uint32_t first_unit = cur.base + kItemCost;
+      const uint32_t i0 = shares.of(first_unit), i1 = shares.of(first_unit + cur.w.chunks - 1);
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
         uint32_t* cnt = ws.counters + (static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) *
                                           ((a.max_new * G + kRows - 1) / kRows) + cur.tile;
-        const uint32_t n = atomicAdd(cnt, 1u);
-        const bool last = n == static_cast<uint32_t>(i1 - i0);
+        const bool last = atomicAdd(cnt, 1u) == i1 - i0;
         if (last) *cnt = 0u;
         *arrived = last ? 1u : 0u;
       }
       __syncthreads();
       if (*arrived) {
         __threadfence();
-        for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
-          const int row = x / (D / 4), e = x % (D / 4);
+        // D / 4 lanes take a row, 4 dims each; together they read the parts' (max, sum), a lane
+        // a part, and then each its dims of the parts, eight at a time.
+        constexpr int kLanes = D / 4;
+        const int e = threadIdx.x % kLanes;
+        const int count = static_cast<int>(i1 - i0) + 1;
+        for (int row = threadIdx.x / kLanes; row < (rows + 1) / 2 * 2; row += kWarps * 32 / kLanes) {
+          auto ml_of = [&](int i) {
+            return row < rows && i < count
+                       ? __ldcg(reinterpret_cast<const float2*>(part_of(i0 + i, i == 0) + kRows * D +
+                                                                2 * row))
+                       : make_float2(-INFINITY, 0.f);
+          };
           float m = -INFINITY;
-          for (int64_t i = i0; i <= i1; ++i)
-            m = fmaxf(m, __ldcg(ws.parts + (2 * i + (i == i0 ? 1 : 0)) * S::part_floats +
-                                kRows * D + 2 * row));
+          for (int i = e; i < (count + kLanes - 1) / kLanes * kLanes; i += kLanes)
+            m = fmaxf(m, ml_of(i).x);
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           float l = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int64_t i = i0; i <= i1; ++i) {
-            const float* src = ws.parts + (2 * i + (i == i0 ? 1 : 0)) * S::part_floats;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + kRows * D + 2 * row));
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(src + row * D + 4 * e));
-            if (ml.x == -INFINITY) continue;
-            const float f = exp2f(ml.x - m);
-            l = fmaf(ml.y, f, l);
-            v.x = fmaf(t.x, f, v.x), v.y = fmaf(t.y, f, v.y);
-            v.z = fmaf(t.z, f, v.z), v.w = fmaf(t.w, f, v.w);
+          for (int base = 0; base < count; base += kLanes) {
+            const float2 ml = ml_of(base + e);
+            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+            const float wl = w * ml.y;
+            for (int j = 0; j < min(kLanes, count - base); j += 8) {
+              float4 t[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                t[x] = row < rows && base + j + x < count
+                           ? __ldcg(reinterpret_cast<const float4*>(
+                                 part_of(i0 + base + j + x, base + j + x == 0) + row * D + 4 * e))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const float f = __shfl_sync(0xffffffffu, w, j + x, kLanes);
+                l += __shfl_sync(0xffffffffu, wl, j + x, kLanes);
+                if (f != 0.f) {
+                  v.x = fmaf(t[x].x, f, v.x), v.y = fmaf(t[x].y, f, v.y);
+                  v.z = fmaf(t[x].z, f, v.z), v.w = fmaf(t[x].w, f, v.w);
+                }
+              }
+            }
           }
-          store(row, e, v, m, l);
+          if (row < rows) store(row, e, v, m, l);
         }
       }
     }
-    seg_base += cur.w.chunks;
     if (!advance<kRows>(cur, a, G)) break;
     __syncthreads();  // the join's reads of shared memory before the next segment's writes
   }
@@ -667,45 +730,72 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 }
 
 // weights_out[b, h, j] = weights[b, h, j] + sum over rows of exp2(logit - lse2), in row order.
+// A thread takes four tokens 256 apart, four rows of each at a time: sixteen loads on their way.
+constexpr int kWeightRows = 32;  // rows a head has at most on this path
 __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttentionArgs a,
                                                           const Workspace ws) {
+  __shared__ float lse[kWeightRows];
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.z, h = blockIdx.y, G = a.heads / a.c.kv_heads;
   const Kv4Seq s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
-  const int key = blockIdx.x * 256 + threadIdx.x;
-  if (key >= s.n) return;
-  const float* x = ws.logits + (static_cast<size_t>(b) * a.c.kv_heads + h) * a.max_new * G *
-                                   ws.row_len + key;
-  const size_t at = (static_cast<size_t>(b) * a.c.kv_heads + h) * a.weights_stride + key;
-  float acc = 0.f;
-  for (int row = 0; row < s.m * G; ++row) {
-    const float l = ws.lse2[static_cast<int64_t>(s.s0 + row / G) * a.heads + h * G + row % G];
-    if (l != -INFINITY) acc += exp2f(x[static_cast<size_t>(row) * ws.row_len] - l);
+  const int key0 = blockIdx.x * 1024 + threadIdx.x;
+  if (blockIdx.x * 1024 >= s.n) return;
+  const int rows = s.m * G;
+  if (threadIdx.x < kWeightRows) {
+    float v = INFINITY;
+    if (threadIdx.x < rows)
+      v = ws.lse2[static_cast<int64_t>(s.s0 + threadIdx.x / G) * a.heads + h * G + threadIdx.x % G];
+    lse[threadIdx.x] = v == -INFINITY ? INFINITY : v;  // such a row adds nothing
   }
-  a.weights_out[at] = (a.weights != nullptr ? a.weights[at] : 0.f) + acc;
+  __syncthreads();
+  const size_t bh = static_cast<size_t>(b) * a.c.kv_heads + h;
+  const float* x = ws.logits + bh * a.max_new * G * ws.row_len + key0;
+  const size_t at = bh * a.weights_stride + key0;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    if (a.weights != nullptr && key0 + 256 * t < s.n) w[t] = a.weights[at + 256 * t];
+  for (int row = 0; row < rows; row += 4) {
+    float v[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        v[r][t] = row + r < rows && key0 + 256 * t < s.n
+                      ? x[static_cast<size_t>(row + r) * ws.row_len + 256 * t]
+                      : -INFINITY;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] += ex2(v[r][t] - lse[row + r]);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    if (key0 + 256 * t < s.n) a.weights_out[at + 256 * t] = w[t] + acc[t];
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-constexpr int kMaxTiles = 2;  // n8 tiles a row tile has at most
+// n8 tiles of a row tile
+int row_blocks(int max_new, int G) { return max_new * G <= 8 ? 1 : 2; }
 
 struct Layout {
   size_t counters, lse2, logits, parts, total;
   int row_len;
 };
-int grid_limit() { return 2 * device_sm_count(); }
+int grid_limit(int nt) { return ctas_per_sm(nt) * device_sm_count(); }
 
 Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv_heads, int D,
               bool weights) {
   Layout l;
-  const int G = heads / kv_heads;
+  const int G = heads / kv_heads, nt = row_blocks(max_new, G);
   l.row_len = (max_len + 3) / 4 * 4;
   size_t at = 0;
   l.counters = at;
   at += round256(static_cast<size_t>(batch) * kv_heads * ((static_cast<size_t>(max_new) * G + 7) / 8) * 4);
   l.parts = at;
-  at += round256(static_cast<size_t>(2) * grid_limit() * kMaxTiles * 8 * (D + 2) * 4);
+  at += round256(static_cast<size_t>(2) * grid_limit(nt) * nt * 8 * (D + 2) * 4);
   l.lse2 = at;
   if (weights) at += round256(static_cast<size_t>(tokens) * heads * 4);
   l.logits = at;
@@ -717,7 +807,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
 
 template <int D, int NG, int NT>
 cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
-  constexpr int kStages = 2;
+  constexpr int kStages = 3;
   using S = Shape<D, NG, NT, kStages>;
   const Layout l = layout(a.c.batch, a.tokens, a.max_new, a.max_len, a.heads, a.c.kv_heads, D,
                           a.weights_out != nullptr);
@@ -734,24 +824,24 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   const int G = a.heads / a.c.kv_heads;
   const int64_t tiles = (static_cast<int64_t>(a.max_new) * G + S::kRows - 1) / S::kRows;
   const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.kv_heads * tiles *
-                        ((a.max_len + kUnit - 1) / kUnit + 1);
+                        (kItemCost + (a.max_len + kUnit - 1) / kUnit);
+  if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int64_t want = (units + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(want < grid_limit() ? want : grid_limit());
+  const unsigned grid = static_cast<unsigned>(want < grid_limit(NT) ? want : grid_limit(NT));
   e = launch_with_pdl(kern, dim3(grid), dim3(kWarps * 32), S::total, stream, a, ws);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
   return launch_with_pdl(kv4_weights_kernel,
-                         dim3((a.max_len + 255) / 256, a.c.kv_heads, a.c.batch), dim3(256), 0,
+                         dim3((a.max_len + 1023) / 1024, a.c.kv_heads, a.c.batch), dim3(256), 0,
                          stream, a, ws);
 }
 
 template <int D, int NG>
 cudaError_t by_rows(const Kv4AttentionArgs& a, cudaStream_t stream) {
-  const int rows = a.max_new * (a.heads / a.c.kv_heads);
-  return rows <= 8 ? run<D, NG, 1>(a, stream) : run<D, NG, 2>(a, stream);
+  return row_blocks(a.max_new, a.heads / a.c.kv_heads) == 1 ? run<D, NG, 1>(a, stream) : run<D, NG, 2>(a, stream);
 }
 
 // Rows of a key/value head from which the prompts' path takes over.
-constexpr int64_t kPromptRows = 33;
+constexpr int64_t kPromptRows = kWeightRows + 1;
 
 bool is_prompt(int max_new, int heads, int kv_heads) {
   return static_cast<int64_t>(max_new) * (heads / kv_heads) >= kPromptRows;

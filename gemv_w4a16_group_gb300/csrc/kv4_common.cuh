@@ -54,20 +54,37 @@ __device__ __forceinline__ Kv4Seq kv4_sequence(const Kv4View& c, const int32_t* 
   return s;
 }
 
-// First byte of record `rec` (of the sequence) of head h; nullptr for a page number outside the
-// cache, which is reported.
-__device__ __forceinline__ uint8_t* kv4_record(const Kv4View& c, const int32_t* table, int width,
-                                               int b, int h, int rec, uint32_t record_bytes) {
-  const int shift = c.page_shift - 4;
-  const int page = table[static_cast<size_t>(b) * width + (rec >> shift)];
+// First byte of record `rec` (of the sequence) of head h in page `page`, its table's entry for the
+// record; nullptr for a page number outside the cache, which is reported.
+__device__ __forceinline__ uint8_t* kv4_in_page(const Kv4View& c, int page, int h, int rec,
+                                                uint32_t record_bytes) {
   if (page < 0 || page >= c.pages) {
     atomicOr(c.status, kStatusIndex);
     return nullptr;
   }
+  const int shift = c.page_shift - 4;
   const size_t r = ((static_cast<size_t>(page) * c.kv_heads + h) << shift) +
                    (rec & ((1 << shift) - 1));
   return c.data + r * record_bytes;
 }
+__device__ __forceinline__ uint8_t* kv4_record(const Kv4View& c, const int32_t* table, int width,
+                                               int b, int h, int rec, uint32_t record_bytes) {
+  return kv4_in_page(c, table[static_cast<size_t>(b) * width + (rec >> (c.page_shift - 4))], h, rec,
+                     record_bytes);
+}
+
+// n units in equal consecutive shares of `ctas` CTAs.
+struct Shares {
+  uint32_t each, more;  // the first `more` CTAs have each + 1
+  __device__ __forceinline__ Shares(uint32_t n, uint32_t ctas) : each(n / ctas), more(n % ctas) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
+    return cta * each + min(cta, more);
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t unit) const {  // the CTA that has a unit
+    const uint32_t big = more * (each + 1);
+    return unit < big ? unit / (each + 1) : more + (unit - big) / each;
+  }
+};
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }

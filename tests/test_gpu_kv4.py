@@ -186,6 +186,13 @@ def test_large_logits():
     _check_attention(cache, lens, new, 4, 2, 8, scale=-0.25)
 
 
+@pytest.mark.parametrize("new", [[1, 2], [2, 70]])
+def test_scale_zero_averages(new):
+    lens = [300, 80]
+    cache, _, _ = _fill(lens, 2, 128, 64, 16, 8)
+    _check_attention(cache, lens, new, 4, 2, 8, scale=0.0)
+
+
 @pytest.mark.parametrize("new", [4, 40])
 def test_hidden_tokens_do_not_matter(new):
     """Tokens behind a row's position hold infinities and NaN: rows before them are untouched."""
