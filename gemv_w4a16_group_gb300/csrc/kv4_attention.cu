@@ -19,33 +19,42 @@
 // What bounds it: the cache is read once (D + 8 D / group bytes a token and head), at 4 heads a
 // key/value head about 8 operations a byte, so the aim is the memory's rate.
 //
-// Work split. A unit is 64 tokens of one (sequence, head, row tile); the units of all sequences
+// Work split. A unit is 32 tokens of one (sequence, head, row tile); the units of all sequences
 // in order are cut into equal ranges, one a CTA, from the lengths on the device: ragged batches
 // and one long sequence use the whole GPU alike, and a bound on the length costs nothing. Within
-// a range the CTA's warps take units in turn, each with its own ring of bulk copies and no
-// barrier but at the end of a segment (the part of one sequence, head and tile in the range),
-// where they join (max, sum, accumulator) through shared memory. A segment that another CTA
-// shares goes to the workspace in fp32, and the CTA that arrives last joins the parts in order.
+// a range the computing warps take units in turn, each from its own ring of two bulk copies that
+// one more warp keeps filled; there is no barrier but at a segment (the part of one sequence, head and
+// tile in the range), whose rows one warp prepares and whose end joins the warps' (max, sum,
+// accumulator) through shared memory. A segment that another CTA shares goes to the workspace in
+// fp32, and the CTA that arrives last joins the parts in order. (Copies issued by the computing
+// warps themselves, with a page looked up for each, cost them registers and a sixth of their
+// instructions.)
+#include <type_traits>
+
 #include "kv4_common.cuh"
 #include "kv4_prompt.h"
 
 namespace w4k {
 namespace {
 
-constexpr int kWarps = 4;
+// Computing warps of a CTA and resident CTAs an SM, by the n8 tiles of rows a warp holds: one
+// needs 128 registers a thread (2 CTAs of 8 warps), two 168 (one of 12).
+constexpr int computing_warps(int nt) { return nt == 1 ? 7 : 11; }
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
+constexpr int kStages = 2;
 constexpr int kUnit = 32;  // tokens
 constexpr int kUnitRecords = kUnit / 16;
 // Units that stand for what an item (sequence, head, row tile) costs beyond its own: loading its
 // queries, joining the warps, writing its rows. They come before its units in the list. Without
 // them the CTA that got the shortest sequences of a ragged batch (0, 1, 17 .. 4096 tokens, 32
 // sequences of 8 heads) took 42 us, its neighbours 10.
-constexpr int kItemCost = 6;
+constexpr int kItemCost = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -61,6 +70,15 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// D(16x8) = A(16x16) B(16x8), FP16 in, fp32 out.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 template <int NB>
@@ -79,8 +97,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
+// Barrier of the computing warps.
+template <int WARPS>
+__device__ __forceinline__ void join_warps() {
+  asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+}
+
 struct Workspace {
-  uint32_t* counters;  // one a segment, zero between calls
+  uint32_t* counters;  // one an item, zero between calls
   float* lse2;         // [tokens, heads], base 2
   float* logits;       // [batch, kv_heads, max_new G, row_len], base 2 (weights only)
   float* parts;        // [2 grid] x (8 NT rows x D + 16 NT)
@@ -102,17 +126,16 @@ __device__ __forceinline__ Work work_of(const Kv4AttentionArgs& a, int group, in
   return w;
 }
 
-// Position in the list of units. A warp walks units w, w + kWarps, ... of each segment.
+// An item and its units in this CTA's range, a segment.
 struct Cursor {
-  int b, h, tile;      // segment
+  int b, h, tile;
   Work w;
-  int lo, hi;          // the item's units in this CTA's range
-  uint32_t base;       // the item's first place in the list
-  uint32_t left;       // places of the range after this segment's
+  int lo, hi;
+  uint32_t base;  // the item's first place in the list
+  uint32_t left;  // places of the range after this segment's
 };
 
-template <int ROWS>
-__device__ __forceinline__ void enter(Cursor& c, const Kv4AttentionArgs& a, int first) {
+__device__ __forceinline__ void enter(Cursor& c, int first) {
   const int end = static_cast<int>(min(static_cast<uint32_t>(kItemCost + c.w.chunks), first + c.left));
   c.left -= end - first;
   c.lo = max(0, first - kItemCost);
@@ -120,61 +143,62 @@ __device__ __forceinline__ void enter(Cursor& c, const Kv4AttentionArgs& a, int 
 }
 
 // Next segment of the range that has units (the range's end may hold only an item's cost); false
-// at its end. `base` is the item's place in the list.
+// at its end.
 template <int ROWS>
 __device__ __forceinline__ bool advance(Cursor& c, const Kv4AttentionArgs& a, int group) {
   do {
-  if (c.left == 0) return false;
-  c.base += kItemCost + c.w.chunks;
-  if (++c.tile >= c.w.tiles) {
-    c.tile = 0;
-    if (++c.h >= a.c.kv_heads) {
-      c.h = 0;
-      do {
-        if (++c.b >= a.c.batch) return false;
-        c.w = work_of<ROWS>(a, group, c.b);
-      } while (c.w.tiles == 0);
+    if (c.left == 0) return false;
+    c.base += kItemCost + c.w.chunks;
+    if (++c.tile >= c.w.tiles) {
+      c.tile = 0;
+      if (++c.h >= a.c.kv_heads) {
+        c.h = 0;
+        do {
+          if (++c.b >= a.c.batch) return false;
+          c.w = work_of<ROWS>(a, group, c.b);
+        } while (c.w.tiles == 0);
+      }
     }
-  }
-  enter<ROWS>(c, a, 0);
+    enter(c, 0);
   } while (c.lo >= c.hi);
   return true;
 }
 
-// Resident CTAs an SM, by registers (168 or 255 a thread).
-constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
-
-template <int D, int NG, int NT, int STAGES>
+template <int D, int NG, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
+  static constexpr int kWarps = computing_warps(NT);
+  static constexpr int kLower = (kWarps + 1) / 2;  // accumulators in shared memory at a time
   static constexpr uint32_t stage_bytes = kUnitRecords * Kv4Record<D, NG>::kBytes;
-  static constexpr uint32_t ring_bytes = kWarps * STAGES * stage_bytes;
-  static constexpr uint32_t o_off = ring_bytes;                            // [warp][row][D]
-  static constexpr uint32_t ml_off = o_off + kWarps * kRows * D * 4;       // [warp][row] (m, l)
-  static constexpr uint32_t bar_off = ml_off + kWarps * kRows * 8;
-  static constexpr uint32_t misc_off = bar_off + kWarps * STAGES * 8;
+  static constexpr uint32_t q_off = kWarps * kStages * stage_bytes;  // [nt][D / 32][lane] 16 bytes
+  static constexpr uint32_t o_off = q_off + NT * (D / 32) * 512;     // [kLower][row][D]
+  static constexpr uint32_t ml_off = o_off + kLower * kRows * D * 4;  // [warp][row] (m, l)
+  static constexpr uint32_t row_off = ml_off + kWarps * kRows * 8;   // [row] (sums of q, unscale)
+  static constexpr uint32_t bar_off = row_off + kRows * (NG + 1) * 4;
+  static constexpr uint32_t misc_off = bar_off + 2 * kWarps * kStages * 8;
   static constexpr uint32_t total = misc_off + 16;
   static constexpr int part_floats = kRows * D + 2 * kRows;
 };
 
-template <int D, int NG, int NT, int STAGES, bool LOGITS>
-__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
+template <int D, int NG, int NT, bool LOGITS>
+__global__ void __launch_bounds__((computing_warps(NT) + 1) * 32, ctas_per_sm(NT))
     kv4_attention_kernel(const Kv4AttentionArgs a, const Workspace ws) {
   using R = Kv4Record<D, NG>;
-  using S = Shape<D, NG, NT, STAGES>;
-  constexpr int NB = R::kBlocks, kRows = S::kRows;
+  using S = Shape<D, NG, NT>;
+  constexpr int NB = R::kBlocks, kRows = S::kRows, kWarps = S::kWarps, kLower = S::kLower;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::bar_off);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bar_off);  // [warp][stage]
+  uint64_t* empty = full + kWarps * kStages;
   volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + S::misc_off);
   volatile uint32_t* arrived = abort_flag + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = lane >> 2, c = lane & 3;
   const int G = a.heads / a.c.kv_heads;
 
-  if (threadIdx.x < kWarps * STAGES) mbar_init(&bars[threadIdx.x], 1);
-  if (threadIdx.x == 0) {
-    *abort_flag = 0u;
-    fence_barrier_init();
+  if (threadIdx.x < 2 * kWarps * kStages) mbar_init(&full[threadIdx.x], 1);
+  if (threadIdx.x == 0) *abort_flag = 0u;
+  if (warp == 0) {
+    __syncwarp();
+    if (lane == 0) fence_barrier_init();
   }
   __syncthreads();
   pdl_launch_dependents();
@@ -183,24 +207,24 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
   // This CTA's range of units: lane by lane the sequences' units, and among them the range's
   // beginning.
   uint32_t total = 0;
-  auto units_of = [&](int b, Work& w) {
-    if (b >= a.c.batch) return 0u;
-    w = work_of<kRows>(a, G, b);
-    return static_cast<uint32_t>(w.tiles) * (kItemCost + w.chunks) * a.c.kv_heads;
-  };
   Work mine;
+  auto units_of = [&](int b) {
+    if (b >= a.c.batch) return 0u;
+    mine = work_of<kRows>(a, G, b);
+    return static_cast<uint32_t>(mine.tiles) * (kItemCost + mine.chunks) * a.c.kv_heads;
+  };
   for (int base = 0; base < a.c.batch; base += 32)
-    total += __reduce_add_sync(0xffffffffu, units_of(base + lane, mine));
+    total += __reduce_add_sync(0xffffffffu, units_of(base + lane));
   const uint32_t ctas = min(gridDim.x, (total + kWarps - 1) / kWarps), me = blockIdx.x;
   if (me >= ctas) return;
   const Shares shares(total, ctas);
-  const uint32_t u0 = shares.begin(me), u1 = shares.begin(me + 1);
+  const uint32_t u0 = shares.begin(me);
 
   Cursor cur;
   {
     uint32_t before = 0;
     for (int base = 0;; base += 32) {
-      const uint32_t u = units_of(base + lane, mine);
+      const uint32_t u = units_of(base + lane);
       uint32_t upto = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -224,159 +248,197 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
     const uint32_t per = kItemCost + cur.w.chunks, seg = (u0 - before) / per;
     cur.h = static_cast<int>(seg / cur.w.tiles);
     cur.tile = static_cast<int>(seg % cur.w.tiles);
-    cur.left = u1 - u0;
+    cur.left = shares.begin(me + 1) - u0;
     cur.base = before + seg * per;
-    enter<kRows>(cur, a, static_cast<int>(u0 - cur.base));
+    enter(cur, static_cast<int>(u0 - cur.base));
     if (cur.lo >= cur.hi && !advance<kRows>(cur, a, G)) return;
   }
 
-  // Ring: this warp's units in order, STAGES - 1 ahead of the one it computes on. A unit's page
-  // numbers are looked up a unit before its copies are issued.
-  const uint32_t ring = smem_addr(smem) + warp * STAGES * S::stage_bytes;
-  uint64_t* full = bars + warp * STAGES;
-  const int run = min(1 << (a.c.page_shift - 4), kUnitRecords);  // records a copy, in one page
-  Cursor pre = cur;
-  int pre_unit = cur.lo + warp, pre_records = 0, pre_page = 0;
-  bool pre_more = true;
-  int filled = 0, used = 0;  // units loaded, units computed
-  bool ok = true;
-  auto look = [&]() {
-    while (pre_more && pre_unit >= pre.hi) {
-      pre_more = advance<kRows>(pre, a, G);
-      pre_unit = pre.lo + warp;
-    }
-    if (!pre_more) return;
-    pre_records = min(kUnitRecords, (pre.w.s.n + 15) / 16 - pre_unit * kUnitRecords);
-    if (lane < pre_records && lane % run == 0)
-      pre_page = a.c.table[static_cast<size_t>(pre.b) * a.c.width +
-                           ((pre_unit * kUnitRecords + lane) >> (a.c.page_shift - 4))];
-  };
-  auto fill = [&]() {
-    if (!pre_more || !ok) return;
-    const int stage = filled % STAGES;
-    const bool mine = lane < pre_records && lane % run == 0;
-    const uint8_t* src = nullptr;
-    if (mine)
-      src = kv4_in_page(a.c, pre_page, pre.h, pre_unit * kUnitRecords + lane, R::kBytes);
-    uint32_t sum = pre_records * R::kBytes;
-    const uint32_t bytes = src == nullptr ? 0u : min(run, pre_records - lane) * R::kBytes;
-    if (__any_sync(0xffffffffu, mine && src == nullptr))
-      sum = __reduce_add_sync(0xffffffffu, bytes);
-    if (lane == 0) mbar_arrive_expect_tx(&full[stage], sum);
-    __syncwarp();
-    if (src != nullptr)
-      bulk_load(smem + (warp * STAGES + stage) * S::stage_bytes + lane * R::kBytes, src, bytes,
-                &full[stage]);
-    ++filled;
-    pre_unit += kWarps;
-    look();
-  };
-  look();
-#pragma unroll 1
-  for (int i = 0; i < STAGES - 1; ++i) fill();
-
-  const float scale2 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e;
-  for (;;) {
-    // ---- one segment
-    const Kv4Seq seq = cur.w.s;
-    const int rows_all = seq.m * G, row0 = cur.tile * kRows;
-    const int rows = min(kRows, rows_all - row0);
-    uint32_t q[NT][NB][4];   // FP16 under the row's power of two
-    float sq[NT][NG][2];     // sums of q over a group's dims, rows 2c, 2c + 1
-    float unscale[NT][2];    // makes a sum of products of rows 2c, 2c + 1 a logit (base 2)
-    int last_key[NT][2];     // last visible key of rows 2c, 2c + 1
+  if (warp == kWarps) {
+    // ---- the copies: lane w keeps warp w's ring filled, on its own way through the segments. The
+    // lanes poll together (a lane that blocked would hold up the others), and each has loaded its
+    // next unit's page numbers long before it needs them.
+    if (lane >= kWarps) return;
+    constexpr uint32_t kLanes = (1u << kWarps) - 1u;
+    const int shift = a.c.page_shift - 4;
+    Cursor at = cur;
+    int unit = at.lo + lane, records = 0, given = 0;
+    int page[kUnitRecords] = {};
+    bool more = true;
+    auto look = [&]() {
+      while (more && unit >= at.hi) {
+        more = advance<kRows>(at, a, G);
+        unit = at.lo + lane;
+      }
+      if (!more) return;
+      records = min(kUnitRecords, (at.w.s.n + 15) / 16 - unit * kUnitRecords);
+      const int32_t* table = a.c.table + static_cast<size_t>(at.b) * a.c.width;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + nt * 8 + r;
-      const bool have = nt * 8 + r < rows;
+      for (int j = 0; j < kUnitRecords; ++j)
+        if (j < records) page[j] = table[(unit * kUnitRecords + j) >> shift];
+    };
+    look();
+    uint64_t since = 0;  // when polling began to no avail
+    bool ok = true;
+    while (__any_sync(kLanes, more)) {
+      const int stage = lane * kStages + given % kStages;
+      const bool free = more && (given < kStages ||
+                                 mbar_test(&empty[stage], (given / kStages - 1) & 1u));
+      if (free) {
+        const uint8_t* src[kUnitRecords];
+        uint32_t sum = 0;
+#pragma unroll
+        for (int j = 0; j < kUnitRecords; ++j) {
+          src[j] = j < records ? kv4_in_page(a.c, page[j], at.h, unit * kUnitRecords + j, R::kBytes)
+                               : nullptr;
+          if (src[j] != nullptr) sum += R::kBytes;
+        }
+        mbar_arrive_expect_tx(&full[stage], sum);
+        uint8_t* dst = smem + stage * S::stage_bytes;
+        if (shift > 0 && sum == kUnitRecords * R::kBytes) {
+          bulk_load(dst, src[0], kUnitRecords * R::kBytes, &full[stage]);  // one page
+        } else {
+#pragma unroll
+          for (int j = 0; j < kUnitRecords; ++j)
+            if (src[j] != nullptr) bulk_load(dst + j * R::kBytes, src[j], R::kBytes, &full[stage]);
+        }
+        ++given;
+        unit += kWarps;
+        look();
+      }
+      if (__any_sync(kLanes, free)) {
+        since = 0;
+        continue;
+      }
+      const uint64_t now = global_timer_ns();
+      if (since == 0) since = now;
+      if (__any_sync(kLanes, *abort_flag != 0u || now - since > a.wait_limit_ns)) {
+        ok = false;
+        *abort_flag = 1u;
+        if (lane == 0) atomicOr(a.c.status, kStatusTimeout);
+        break;
+      }
+      __nanosleep(32);
+    }
+    if (!ok) {  // copies in flight land before the CTA exits
+      volatile uint32_t no_abort = 0u;
+      for (int i = max(0, given - kStages); i < given; ++i)
+        mbar_wait_bounded(&full[lane * kStages + i % kStages], (i / kStages) & 1u, &no_abort,
+                          a.c.status, a.wait_limit_ns);
+    }
+    return;
+  }
+
+  const int r = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_addr(smem) + warp * kStages * S::stage_bytes;
+  const uint32_t q_s = smem_addr(smem) + S::q_off + lane * 16;
+  float* sm_o = reinterpret_cast<float*>(smem + S::o_off);
+  float2* sm_ml = reinterpret_cast<float2*>(smem + S::ml_off);
+  float* sm_row = reinterpret_cast<float*>(smem + S::row_off);  // [NG + 1][row]
+  // its sign, or a zero, goes into q: hidden logits are -inf times this
+  const float scale2 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e;
+  int used = 0;
+  bool ok = true;
+  for (;;) {
+    const Kv4Seq seq = cur.w.s;
+    const int row0 = cur.tile * kRows, rows = min(kRows, seq.m * G - row0);
+    // ---- a warp an n8 tile brings the queries into FP16 fragments under a power of two a row
+    if (warp < NT) {
+      const int row = row0 + warp * 8 + r;
+      const bool have = warp * 8 + r < rows;
       const uint16_t* src = a.q + static_cast<int64_t>(seq.s0 + (have ? row / G : 0)) * a.q_stride +
                             (cur.h * G + (have ? row % G : 0)) * D + 8 * c;
+      uint4 v[NB];
       uint32_t top = 0;  // largest magnitude of the row, BF16 bits
 #pragma unroll
-      for (int s = 0; s < NB; ++s) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (have) v = __ldg(reinterpret_cast<const uint4*>(src + 32 * s));
-        q[nt][s][0] = v.x, q[nt][s][1] = v.y, q[nt][s][2] = v.z, q[nt][s][3] = v.w;
+      for (int x = 0; x < NB; ++x) {
+        v[x] = make_uint4(0, 0, 0, 0);
+        if (have) v[x] = __ldg(reinterpret_cast<const uint4*>(src + 32 * x));
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          top = max(top, max(q[nt][s][i] & 0x7FFFu, (q[nt][s][i] >> 16) & 0x7FFFu));
+      for (int x = 0; x < NB; ++x) {
+        const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^e brings the row's largest to [2^14, 2^15)
+      // 2^up brings the row's largest to [2^14, 2^15)
       const int ex = static_cast<int>(top >> 7);
       const int up = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -126), 126);
-      // pairs 1 and 3 meet codes times 16
       const float f = a.scale < 0.f ? -pow2f(up) : a.scale > 0.f ? pow2f(up) : 0.f;
-      const float f16 = f * 0.0625f;
+      const float f16 = f * 0.0625f;  // pairs 1 and 3 meet codes times 16
 #pragma unroll
-      for (int s = 0; s < NB; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          q[nt][s][i] = f16x2_bits(bf16_lo(q[nt][s][i]) * (i % 2 ? f16 : f),
-                                   bf16_hi(q[nt][s][i]) * (i % 2 ? f16 : f));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = nt * 8 + 2 * c + i;
-        last_key[nt][i] = rr < rows ? seq.n - seq.m + (row0 + rr) / G : -1;
-        // products are codes' 2^24 too small; the sums below carry the same factor
-        unscale[nt][i] = fmaxf(
-            scale2 * 16777216.f * pow2f(-__shfl_sync(0xffffffffu, up, (2 * c + i) * 4)), 1e-37f);
+      for (int x = 0; x < NB; ++x) {
+        const uint4 h = make_uint4(f16x2_bits(bf16_lo(v[x].x) * f, bf16_hi(v[x].x) * f),
+                                   f16x2_bits(bf16_lo(v[x].y) * f16, bf16_hi(v[x].y) * f16),
+                                   f16x2_bits(bf16_lo(v[x].z) * f, bf16_hi(v[x].z) * f),
+                                   f16x2_bits(bf16_lo(v[x].w) * f16, bf16_hi(v[x].w) * f16));
+        *reinterpret_cast<uint4*>(smem + S::q_off + ((warp * NB + x) * 32 + lane) * 16) = h;
+        v[x] = h;
       }
-      constexpr uint32_t one = 0x00010001u, one16 = 0x00100010u;  // code 1
+      // sums of q over a group's dims, as codes 1 would give them: column n of the product
+      constexpr uint32_t one = 0x00010001u, one16 = 0x00100010u;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4];
 #pragma unroll
-        for (int s = g * NB / NG; s < (g + 1) * NB / NG; ++s) {
-          mma_f16_16816(acc, one, one, one16, one16, q[nt][s][0], q[nt][s][1]);
-          mma_f16_16816(acc, one, one, one16, one16, q[nt][s][2], q[nt][s][3]);
+        for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
+          if (x == g * NB / NG)
+            mma_f16_first(acc, one, one, one16, one16, v[x].x, v[x].y);
+          else
+            mma_f16_16816(acc, one, one, one16, one16, v[x].x, v[x].y);
+          mma_f16_16816(acc, one, one, one16, one16, v[x].z, v[x].w);
         }
-        sq[nt][g][0] = acc[0];
-        sq[nt][g][1] = acc[1];
+        if (r == 0) {
+          sm_row[g * kRows + warp * 8 + 2 * c] = acc[0];
+          sm_row[g * kRows + warp * 8 + 2 * c + 1] = acc[1];
+        }
       }
+      // products are codes' 2^24 too small, as the sums are
+      if (c == 0)
+        sm_row[NG * kRows + warp * 8 + r] = fmaxf(scale2 * 16777216.f * pow2f(-up), 1e-37f);
     }
+    join_warps<kWarps>();
+    float sq[NT][NG][2], unscale[NT][2];  // of rows 2c, 2c + 1
     float o[NT][NB][2][4], corr[NT][NG][2], mx[NT][2], sum[NT][2];
-    int ev[NT][2];  // exponent field of the largest V scale that rows 2c, 2c + 1 have met
+    int ev[NT][2];         // exponent field of the largest V scale that the rows have met
+    float down[NT][2];     // 2^-ev
+    float cap = -1.f;      // V scales up to this may come under every row's 2^-ev
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = nt * 8 + 2 * c + i;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          sq[nt][g][i] = sm_row[g * kRows + row];
+          corr[nt][g][i] = 0.f;
+        }
+        unscale[nt][i] = sm_row[NG * kRows + row];
+        mx[nt][i] = -INFINITY;
+        sum[nt][i] = 0.f;
+        ev[nt][i] = 0;
+        down[nt][i] = 0.f;
+      }
 #pragma unroll
       for (int x = 0; x < NB; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int z = 0; z < 4; ++z) o[nt][x][y][z] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[nt][i] = -INFINITY;
-        sum[nt][i] = 0.f;
-        ev[nt][i] = 0;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) corr[nt][g][i] = 0.f;
-      }
     }
     // first key that some row of the tile does not see
     const int clear = rows > 0 ? seq.n - seq.m + row0 / G + 1 : 0;
 
-#pragma unroll 1
-    for (int unit = cur.lo + warp; unit < cur.hi; unit += kWarps) {
-      fill();
-      const int stage = used % STAGES;
-      if (ok)
-        ok = mbar_wait_bounded(&full[stage], (used / STAGES) & 1u, abort_flag, a.c.status,
-                               a.wait_limit_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      ++used;
-      if (!ok) continue;
-      const uint32_t base = ring + stage * S::stage_bytes;
-      const int key0 = unit * kUnit;
-      const int records = min(kUnitRecords, (seq.n - key0 + 15) / 16);
-      const bool masked = key0 + kUnit > clear;
+    auto compute = [&](auto mask, uint32_t base, int key0) {
+      constexpr bool kMasked = decltype(mask)::value;
+      const int records = kMasked ? min(kUnitRecords, (seq.n - key0 + 15) / 16) : kUnitRecords;
       // ---- logits, times 1 / unscale
       float s[kUnitRecords][NT][4];
 #pragma unroll
       for (int j = 0; j < kUnitRecords; ++j) {
-        if (j >= records) {
+        if (kMasked && j >= records) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -391,12 +453,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
         for (int g = 0; g < NG; ++g) {
           const uint32_t p0 = lds32(rec + R::kKParams + (16 * g + r) * 4);
           const uint32_t p1 = lds32(rec + R::kKParams + (16 * g + r + 8) * 4);
-          const float s0 = bf16_lo(p0), s1 = bf16_lo(p1), m0 = bf16_hi(p0), m1 = bf16_hi(p1);
           float acc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
 #pragma unroll
           for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
             uint32_t k0[4], k1[4];
@@ -404,10 +461,15 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             code_pairs(w1[x], k1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_f16_16816(acc[nt], k0[0], k1[0], k0[1], k1[1], q[nt][x][0], q[nt][x][1]);
-              mma_f16_16816(acc[nt], k0[2], k1[2], k0[3], k1[3], q[nt][x][2], q[nt][x][3]);
+              const uint4 q = lds128(q_s + (nt * NB + x) * 512);
+              if (x == g * NB / NG)
+                mma_f16_first(acc[nt], k0[0], k1[0], k0[1], k1[1], q.x, q.y);
+              else
+                mma_f16_16816(acc[nt], k0[0], k1[0], k0[1], k1[1], q.x, q.y);
+              mma_f16_16816(acc[nt], k0[2], k1[2], k0[3], k1[3], q.z, q.w);
             }
           }
+          const float s0 = bf16_lo(p0), s1 = bf16_lo(p1), m0 = bf16_hi(p0), m1 = bf16_hi(p1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -417,115 +479,116 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
                                  g == 0 ? m * sum_q : fmaf(m, sum_q, s[j][nt][i]));
             }
         }
-        if (masked) {
+        if constexpr (kMasked) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (key0 + 16 * j + r + (i >= 2 ? 8 : 0) > last_key[nt][i & 1])
-                s[j][nt][i] = -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+              const int row = nt * 8 + 2 * c + (i & 1);
+              const int last = row < rows ? seq.n - seq.m + (row0 + row) / G : -1;
+              if (key0 + 16 * j + r + (i >= 2 ? 8 : 0) > last) s[j][nt][i] = -INFINITY;
+            }
         }
         if constexpr (LOGITS) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int rr = nt * 8 + 2 * c + (i & 1);
+              const int row = nt * 8 + 2 * c + (i & 1);
               const int key = key0 + 16 * j + r + (i >= 2 ? 8 : 0);
-              if (rr < rows && key < seq.n)
+              if (row < rows && key < seq.n)
                 ws.logits[((static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) * a.max_new * G +
-                           row0 + rr) * ws.row_len + key] = s[j][nt][i] * unscale[nt][i & 1];
+                           row0 + row) * ws.row_len + key] = s[j][nt][i] * unscale[nt][i & 1];
             }
         }
       }
-      // ---- running maximum, and the largest V scale's exponent among the visible tokens
-      int unit_ev[NT][2];
-      if (!masked) {
-        uint32_t top = 0;
+      // ---- running maximum, and the largest V scale's exponent among the visible tokens. Both
+      // may lag, by 2^8 and 2^6: p times a scale stays an FP16 number, and most units need
+      // neither the reductions over the warp nor a rescale.
+      constexpr int kScales = kUnitRecords * NG * 16;
+      auto scale_bits = [&](int x) {
+        return lds32(base + (x / (16 * NG)) * R::kBytes + R::kVParams + (x % (16 * NG)) * 4) &
+               0xFFFFu;
+      };
+      bool fits = !kMasked;
+      if constexpr (!kMasked) {
 #pragma unroll
-        for (int x = lane; x < kUnitRecords * NG * 16; x += 32) {
-          const uint32_t sc = lds32(base + (x / (16 * NG)) * R::kBytes + R::kVParams +
-                                    (x % (16 * NG)) * 4) & 0xFFFFu;
-          top = max(top, sc >= 0x7F80u ? 0u : sc);
-        }
-        top = __reduce_max_sync(0xffffffffu, top) >> 7;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) unit_ev[nt][0] = unit_ev[nt][1] = static_cast<int>(top);
-      } else {
+        for (int x = 0; x < kScales; x += 32)
+          fits = fits && __uint_as_float(scale_bits(x + lane) << 16) <= cap;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            uint32_t top = 0;
+            float v = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
 #pragma unroll
-            for (int j = 0; j < kUnitRecords; ++j) {
-              if (j >= records) continue;
-#pragma unroll
-              for (int g = 0; g < NG; ++g)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  const uint32_t sc = lds32(base + j * R::kBytes + R::kVParams +
-                                            (16 * g + r + 8 * half) * 4) & 0xFFFFu;
-                  if (s[j][nt][i + 2 * half] != -INFINITY && sc < 0x7F80u) top = max(top, sc);
-                }
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            unit_ev[nt][i] = static_cast<int>(top >> 7);
+            for (int j = 1; j < kUnitRecords; ++j)
+              v = fmaxf(v, fmaxf(s[j][nt][i], s[j][nt][i + 2]));
+            fits = fits && v * unscale[nt][i] <= mx[nt][i] + 8.f;
           }
       }
-      bool grow = false;
-      float alpha[NT][2], beta[NT][2];
+      if (kMasked || !__all_sync(0xffffffffu, fits)) {
+        uint32_t unit_top = 0;  // of all the unit's scales
+        if constexpr (!kMasked) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float v = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
-#pragma unroll
-          for (int j = 1; j < kUnitRecords; ++j)
-            v = fmaxf(v, fmaxf(s[j][nt][i], s[j][nt][i + 2]));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          const float now = fmaxf(mx[nt][i], v * unscale[nt][i]);
-          const int ev_now = max(ev[nt][i], unit_ev[nt][i]);
-          alpha[nt][i] = now == -INFINITY ? 1.f : ex2(mx[nt][i] - now);
-          beta[nt][i] = alpha[nt][i] * ex2(static_cast<float>(ev[nt][i] - ev_now));
-          grow |= now > mx[nt][i] || ev_now > ev[nt][i];
-          mx[nt][i] = now;
-          ev[nt][i] = ev_now;
+          for (int x = 0; x < kScales; x += 32) {
+            const uint32_t sc = scale_bits(x + lane);
+            unit_top = max(unit_top, sc >= 0x7F80u ? 0u : sc);
+          }
+          unit_top = __reduce_max_sync(0xffffffffu, unit_top);
         }
-      if (__any_sync(0xffffffffu, grow)) {
+        int least = 255;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float f = alpha[nt][i];
-            sum[nt][i] *= f;
+            uint32_t top = unit_top;
+            if constexpr (kMasked) {
 #pragma unroll
-            for (int g = 0; g < NG; ++g) corr[nt][g][i] *= f;
+              for (int j = 0; j < kUnitRecords; ++j)
+#pragma unroll
+                for (int x = 0; x < 2 * NG; ++x) {
+                  if (j >= records || s[j][nt][i + 2 * (x & 1)] == -INFINITY) continue;
+                  const uint32_t sc = lds32(base + j * R::kBytes + R::kVParams +
+                                            (16 * (x / 2) + r + 8 * (x & 1)) * 4) & 0xFFFFu;
+                  if (sc < 0x7F80u) top = max(top, sc);
+                }
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            }
+            float v = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
+#pragma unroll
+            for (int j = 1; j < kUnitRecords; ++j)
+              v = fmaxf(v, fmaxf(s[j][nt][i], s[j][nt][i + 2]));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float now = fmaxf(mx[nt][i], v * unscale[nt][i]);
+            const int ev_now = max(ev[nt][i], static_cast<int>(top >> 7));
+            const float alpha = now == -INFINITY ? 1.f : ex2(mx[nt][i] - now);
+            const float beta = alpha * ex2(static_cast<float>(ev[nt][i] - ev_now));
+            mx[nt][i] = now;
+            ev[nt][i] = ev_now;
+            down[nt][i] = pow2f(127 - min(ev_now, 250));
+            least = min(least, ev_now);
+            sum[nt][i] *= alpha;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) corr[nt][g][i] *= alpha;
 #pragma unroll
             for (int x = 0; x < NB; ++x)
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                o[nt][x][y][i] *= beta[nt][i];
-                o[nt][x][y][i + 2] *= beta[nt][i];
+                o[nt][x][y][i] *= beta;
+                o[nt][x][y][i + 2] *= beta;
               }
           }
+        least = __reduce_min_sync(0xffffffffu, least);
+        cap = pow2f(min(least - 121, 127));
       }
-      float down[NT][2], top[NT][2];  // 2^-ev; the maximum, 0 while nothing is visible
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          down[nt][i] = pow2f(127 - min(ev[nt][i], 250));
-          top[nt][i] = mx[nt][i] == -INFINITY ? 0.f : mx[nt][i];
-        }
       // ---- P V
 #pragma unroll
       for (int j = 0; j < kUnitRecords; ++j) {
-        if (j >= records) continue;
+        if (kMasked && j >= records) continue;
         const uint32_t rec = base + j * R::kBytes;
         uint32_t w0[NB], w1[NB];
         load_words<NB>(rec + R::kV + ((c * 8 + r) * NB) * 4, w0);
@@ -535,7 +598,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            p[nt][i] = ex2(fmaf(s[j][nt][i], unscale[nt][i & 1], -top[nt][i & 1]));
+            const float m = mx[nt][i & 1];
+            p[nt][i] = ex2(fmaf(s[j][nt][i], unscale[nt][i & 1],
+                                kMasked && m == -INFINITY ? 0.f : -m));
             sum[nt][i & 1] += p[nt][i];
             pd[nt][i] = p[nt][i] * down[nt][i & 1];
           }
@@ -550,7 +615,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             float x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = pd[nt][i] * (i < 2 ? s0 : s1);
-            if (!masked) {
+            if constexpr (!kMasked) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 corr[nt][g][i & 1] = fmaf(p[nt][i], i < 2 ? m0 : m1, corr[nt][g][i & 1]);
@@ -579,12 +644,31 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
           }
         }
       }
-      __syncwarp();  // every lane is done with the stage before it is filled again
+    };
+
+#pragma unroll 1
+    for (int unit = cur.lo + warp; unit < cur.hi; unit += kWarps) {
+      const int stage = used % kStages;
+      if (ok)
+        ok = mbar_wait_bounded(&full[warp * kStages + stage], (used / kStages) & 1u, abort_flag,
+                               a.c.status, a.wait_limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      ++used;
+      if (!ok) continue;
+      const uint32_t base = ring + stage * S::stage_bytes;
+      const int key0 = unit * kUnit;
+      const bool masked = key0 + kUnit > clear;
+      // two bodies: the one that every unit but a sequence's last takes has no branches
+      if (masked)
+        compute(std::true_type(), base, key0);
+      else
+        compute(std::false_type(), base, key0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[warp * kStages + stage]);
     }
 
-    // ---- join the warps
-    float* sm_o = reinterpret_cast<float*>(smem + S::o_off);
-    float2* sm_ml = reinterpret_cast<float2*>(smem + S::ml_off);
+    // ---- join the warps: every warp under the rows' common maximum, the upper half's
+    // accumulators onto the lower half's, then those.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -597,19 +681,42 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
 #pragma unroll
           for (int d = 4; d <= 16; d <<= 1)
             corr[nt][g][i] += __shfl_xor_sync(0xffffffffu, corr[nt][g][i], d);
-        const int row = nt * 8 + 2 * c + i;
-        if (r == 0) sm_ml[warp * kRows + row] = make_float2(mx[nt][i], l);
-#pragma unroll
-        for (int x = 0; x < NB; ++x) {
-          const float k = corr[nt][x / (NB / NG)][i];
-          // sums of codes' 2^-24 (2^-20 for odd dims) under 2^-ev
-          const float f = pow2f(min(ev[nt][i], 250) - 127) * 16777216.f, f16 = f * 0.0625f;
-          *reinterpret_cast<float4*>(sm_o + (warp * kRows + row) * D + 32 * x + 4 * r) =
-              make_float4(fmaf(o[nt][x][0][i], f, k), fmaf(o[nt][x][0][i + 2], f16, k),
-                          fmaf(o[nt][x][1][i], f, k), fmaf(o[nt][x][1][i + 2], f16, k));
-        }
+        if (r == 0) sm_ml[warp * kRows + nt * 8 + 2 * c + i] = make_float2(mx[nt][i], l);
       }
-    __syncthreads();
+    join_warps<kWarps>();
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      if ((warp < kLower) == (pass == 1)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = nt * 8 + 2 * c + i;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_ml[w * kRows + row].x);
+            const float w = mx[nt][i] == -INFINITY ? 0.f : ex2(mx[nt][i] - m);
+            // sums of codes' 2^-24 (2^-20 for odd dims) under 2^-ev
+            const float f = pow2f(min(ev[nt][i], 250) - 127) * 16777216.f, f16 = f * 0.0625f;
+#pragma unroll
+            for (int x = 0; x < NB; ++x) {
+              const float k = corr[nt][x / (NB / NG)][i];
+              float4 v = make_float4(fmaf(o[nt][x][0][i], f, k), fmaf(o[nt][x][0][i + 2], f16, k),
+                                     fmaf(o[nt][x][1][i], f, k), fmaf(o[nt][x][1][i + 2], f16, k));
+              v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                           : make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+              float4* at = reinterpret_cast<float4*>(
+                  sm_o + ((warp % kLower) * kRows + row) * D + 32 * x + 4 * r);
+              if (pass == 1 && warp + kLower < kWarps) {
+                const float4 t = *at;
+                v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+              }
+              *at = v;
+            }
+          }
+      }
+      join_warps<kWarps>();
+    }
     const bool whole = cur.lo == 0 && cur.hi == cur.w.chunks;
     auto part_of = [&](uint32_t cta, bool first) {
       return ws.parts + static_cast<size_t>(2 * cta + (first ? 1 : 0)) * S::part_floats;
@@ -631,22 +738,19 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
     };
     for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
       const int row = x / (D / 4), e = x % (D / 4);
-      float m = -INFINITY;
+      float m = -INFINITY, l = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_ml[w * kRows + row].x);
-      float l = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = sm_ml[w * kRows + row];
-        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-        const float4 t =
-            *reinterpret_cast<const float4*>(sm_o + (w * kRows + row) * D + 4 * e);
-        if (f != 0.f) {
-          l = fmaf(ml.y, f, l);
-          v.x = fmaf(t.x, f, v.x), v.y = fmaf(t.y, f, v.y);
-          v.z = fmaf(t.z, f, v.z), v.w = fmaf(t.w, f, v.w);
-        }
+        if (ml.x != -INFINITY) l = fmaf(ml.y, ex2(ml.x - m), l);
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kLower; ++w) {
+        const float4 t = *reinterpret_cast<const float4*>(sm_o + (w * kRows + row) * D + 4 * e);
+        v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
       }
       if (whole) {
         store(row, e, v, m, l);
@@ -656,11 +760,11 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
       }
     }
     if (!whole) {
-      // CTAs i0 .. i1 share the segment; the one that arrives last joins their parts in order.
+      // CTAs i0 .. i1 share the item; the one that arrives last joins their parts in order.
       const uint32_t first_unit = cur.base + kItemCost;
       const uint32_t i0 = shares.of(first_unit), i1 = shares.of(first_unit + cur.w.chunks - 1);
       __threadfence();
-      __syncthreads();
+      join_warps<kWarps>();
       if (threadIdx.x == 0) {
         uint32_t* cnt = ws.counters + (static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) *
                                           ((a.max_new * G + kRows - 1) / kRows) + cur.tile;
@@ -668,7 +772,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
         if (last) *cnt = 0u;
         *arrived = last ? 1u : 0u;
       }
-      __syncthreads();
+      join_warps<kWarps>();
       if (*arrived) {
         __threadfence();
         // D / 4 lanes take a row, 4 dims each; together they read the parts' (max, sum), a lane
@@ -687,7 +791,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
           for (int i = e; i < (count + kLanes - 1) / kLanes * kLanes; i += kLanes)
             m = fmaxf(m, ml_of(i).x);
 #pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          for (int o2 = kLanes / 2; o2 > 0; o2 >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o2));
           float l = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int base = 0; base < count; base += kLanes) {
@@ -718,14 +823,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
       }
     }
     if (!advance<kRows>(cur, a, G)) break;
-    __syncthreads();  // the join's reads of shared memory before the next segment's writes
-  }
-  // A warp that gave up lets its copies in flight land before the CTA exits.
-  if (!ok) {
-    volatile uint32_t no_abort = 0u;
-    for (int i = max(0, filled - STAGES); i < filled; ++i)
-      mbar_wait_bounded(&full[i % STAGES], (i / STAGES) & 1u, &no_abort, a.c.status,
-                        a.wait_limit_ns);
+    join_warps<kWarps>();  // the join's reads of shared memory before the next segment's writes
   }
 }
 
@@ -807,8 +905,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
 
 template <int D, int NG, int NT>
 cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
-  constexpr int kStages = 3;
-  using S = Shape<D, NG, NT, kStages>;
+  using S = Shape<D, NG, NT>;
   const Layout l = layout(a.c.batch, a.tokens, a.max_new, a.max_len, a.heads, a.c.kv_heads, D,
                           a.weights_out != nullptr);
   Workspace ws;
@@ -817,8 +914,8 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   ws.logits = reinterpret_cast<float*>(a.workspace + l.logits);
   ws.parts = reinterpret_cast<float*>(a.workspace + l.parts);
   ws.row_len = l.row_len;
-  auto kern = a.weights_out != nullptr ? kv4_attention_kernel<D, NG, NT, kStages, true>
-                                       : kv4_attention_kernel<D, NG, NT, kStages, false>;
+  auto kern = a.weights_out != nullptr ? kv4_attention_kernel<D, NG, NT, true>
+                                       : kv4_attention_kernel<D, NG, NT, false>;
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), S::total);
   if (e != cudaSuccess) return e;
   const int G = a.heads / a.c.kv_heads;
@@ -826,9 +923,9 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.kv_heads * tiles *
                         (kItemCost + (a.max_len + kUnit - 1) / kUnit);
   if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const int64_t want = (units + kWarps - 1) / kWarps;
+  const int64_t want = (units + S::kWarps - 1) / S::kWarps;
   const unsigned grid = static_cast<unsigned>(want < grid_limit(NT) ? want : grid_limit(NT));
-  e = launch_with_pdl(kern, dim3(grid), dim3(kWarps * 32), S::total, stream, a, ws);
+  e = launch_with_pdl(kern, dim3(grid), dim3((S::kWarps + 1) * 32), S::total, stream, a, ws);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
   return launch_with_pdl(kv4_weights_kernel,
                          dim3((a.max_len + 1023) / 1024, a.c.kv_heads, a.c.batch), dim3(256), 0,
