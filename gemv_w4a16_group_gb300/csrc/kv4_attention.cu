@@ -22,7 +22,7 @@
 // Work split. A unit is 32 tokens of one (sequence, head, row tile); the units of all sequences
 // in order are cut into equal ranges, one a CTA, from the lengths on the device: ragged batches
 // and one long sequence use the whole GPU alike, and a bound on the length costs nothing. Within
-// a range the computing warps take units in turn, each from its own ring of two bulk copies that
+// a range the computing warps take units in turn, each from its own ring of bulk copies that
 // one more warp keeps filled; there is no barrier but at a segment (the part of one sequence, head and
 // tile in the range), whose rows one warp prepares and whose end joins the warps' (max, sum,
 // accumulator) through shared memory. A segment that another CTA shares goes to the workspace in
@@ -37,11 +37,12 @@
 namespace w4k {
 namespace {
 
-// Computing warps of a CTA and resident CTAs an SM, by the n8 tiles of rows a warp holds: one
-// needs 128 registers a thread (2 CTAs of 8 warps), two 168 (one of 12).
-constexpr int computing_warps(int nt) { return nt == 1 ? 7 : 11; }
+// Computing warps of a CTA (with the copies' warp eight) and resident CTAs an SM, by the n8 tiles
+// of rows a warp holds: one needs 128 registers a thread, two all 255.
+constexpr int kWarps = 7;
 constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
-constexpr int kStages = 2;
+// Copies a warp has on their way or at hand: what two CTAs' shared memory holds.
+constexpr int ring_stages(int d, int ng) { return d == 128 && ng == 4 ? 2 : 3; }
 constexpr int kUnit = 32;  // tokens
 constexpr int kUnitRecords = kUnit / 16;
 // Units that stand for what an item (sequence, head, row tile) costs beyond its own: loading its
@@ -98,9 +99,8 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 }
 
 // Barrier of the computing warps.
-template <int WARPS>
 __device__ __forceinline__ void join_warps() {
-  asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
 }
 
 struct Workspace {
@@ -167,25 +167,28 @@ __device__ __forceinline__ bool advance(Cursor& c, const Kv4AttentionArgs& a, in
 template <int D, int NG, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = computing_warps(NT);
+  static constexpr int kStages = ring_stages(D, NG);
   static constexpr int kLower = (kWarps + 1) / 2;  // accumulators in shared memory at a time
   static constexpr uint32_t stage_bytes = kUnitRecords * Kv4Record<D, NG>::kBytes;
-  static constexpr uint32_t q_off = kWarps * kStages * stage_bytes;  // [nt][D / 32][lane] 16 bytes
-  static constexpr uint32_t o_off = q_off + NT * (D / 32) * 512;     // [kLower][row][D]
+  // the queries, [nt][D / 32][lane] 16 bytes, until the warps join; then accumulators,
+  // [kLower][row][D]
+  static constexpr uint32_t q_off = kWarps * kStages * stage_bytes;
+  static constexpr uint32_t o_off = q_off;
   static constexpr uint32_t ml_off = o_off + kLower * kRows * D * 4;  // [warp][row] (m, l)
   static constexpr uint32_t row_off = ml_off + kWarps * kRows * 8;   // [row] (sums of q, unscale)
   static constexpr uint32_t bar_off = row_off + kRows * (NG + 1) * 4;
   static constexpr uint32_t misc_off = bar_off + 2 * kWarps * kStages * 8;
   static constexpr uint32_t total = misc_off + 16;
   static constexpr int part_floats = kRows * D + 2 * kRows;
+  static_assert(total <= (ctas_per_sm(NT) == 2 ? 113u : 227u) * 1024u, "shared memory");
 };
 
 template <int D, int NG, int NT, bool LOGITS>
-__global__ void __launch_bounds__((computing_warps(NT) + 1) * 32, ctas_per_sm(NT))
+__global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(NT))
     kv4_attention_kernel(const Kv4AttentionArgs a, const Workspace ws) {
   using R = Kv4Record<D, NG>;
   using S = Shape<D, NG, NT>;
-  constexpr int NB = R::kBlocks, kRows = S::kRows, kWarps = S::kWarps, kLower = S::kLower;
+  constexpr int NB = R::kBlocks, kRows = S::kRows, kLower = S::kLower, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bar_off);  // [warp][stage]
   uint64_t* empty = full + kWarps * kStages;
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__((computing_warps(NT) + 1) * 32, ctas_per_sm(NT
       if (c == 0)
         sm_row[NG * kRows + warp * 8 + r] = fmaxf(scale2 * 16777216.f * pow2f(-up), 1e-37f);
     }
-    join_warps<kWarps>();
+    join_warps();
     float sq[NT][NG][2], unscale[NT][2];  // of rows 2c, 2c + 1
     float o[NT][NB][2][4], corr[NT][NG][2], mx[NT][2], sum[NT][2];
     int ev[NT][2];         // exponent field of the largest V scale that the rows have met
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__((computing_warps(NT) + 1) * 32, ctas_per_sm(NT
             corr[nt][g][i] += __shfl_xor_sync(0xffffffffu, corr[nt][g][i], d);
         if (r == 0) sm_ml[warp * kRows + nt * 8 + 2 * c + i] = make_float2(mx[nt][i], l);
       }
-    join_warps<kWarps>();
+    join_warps();
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
       if ((warp < kLower) == (pass == 1)) {
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__((computing_warps(NT) + 1) * 32, ctas_per_sm(NT
             }
           }
       }
-      join_warps<kWarps>();
+      join_warps();
     }
     const bool whole = cur.lo == 0 && cur.hi == cur.w.chunks;
     auto part_of = [&](uint32_t cta, bool first) {
@@ -764,7 +767,7 @@ __global__ void __launch_bounds__((computing_warps(NT) + 1) * 32, ctas_per_sm(NT
       const uint32_t first_unit = cur.base + kItemCost;
       const uint32_t i0 = shares.of(first_unit), i1 = shares.of(first_unit + cur.w.chunks - 1);
       __threadfence();
-      join_warps<kWarps>();
+      join_warps();
       if (threadIdx.x == 0) {
         uint32_t* cnt = ws.counters + (static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) *
                                           ((a.max_new * G + kRows - 1) / kRows) + cur.tile;
@@ -772,7 +775,7 @@ __global__ void __launch_bounds__((computing_warps(NT) + 1) * 32, ctas_per_sm(NT
         if (last) *cnt = 0u;
         *arrived = last ? 1u : 0u;
       }
-      join_warps<kWarps>();
+      join_warps();
       if (*arrived) {
         __threadfence();
         // D / 4 lanes take a row, 4 dims each; together they read the parts' (max, sum), a lane
@@ -823,7 +826,7 @@ __global__ void __launch_bounds__((computing_warps(NT) + 1) * 32, ctas_per_sm(NT
       }
     }
     if (!advance<kRows>(cur, a, G)) break;
-    join_warps<kWarps>();  // the join's reads of shared memory before the next segment's writes
+    join_warps();  // the join's reads of shared memory before the next segment's writes
   }
 }
 
@@ -923,9 +926,9 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.kv_heads * tiles *
                         (kItemCost + (a.max_len + kUnit - 1) / kUnit);
   if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const int64_t want = (units + S::kWarps - 1) / S::kWarps;
+  const int64_t want = (units + kWarps - 1) / kWarps;
   const unsigned grid = static_cast<unsigned>(want < grid_limit(NT) ? want : grid_limit(NT));
-  e = launch_with_pdl(kern, dim3(grid), dim3((S::kWarps + 1) * 32), S::total, stream, a, ws);
+  e = launch_with_pdl(kern, dim3(grid), dim3((kWarps + 1) * 32), S::total, stream, a, ws);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
   return launch_with_pdl(kv4_weights_kernel,
                          dim3((a.max_len + 1023) / 1024, a.c.kv_heads, a.c.batch), dim3(256), 0,
