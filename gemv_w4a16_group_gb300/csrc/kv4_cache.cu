@@ -2,20 +2,76 @@
 //
 // Both move every value once and compute a handful of operations on it, so memory bounds them:
 // an append reads 4 bytes and writes 1 + 8 / group bytes for a dim's key and value, a read the
-// other way round.
+// other way round. A block takes 64 tokens of one head. Where each of them lies (its sequence,
+// page and row, three loads that wait for one another) is found once, by a thread a token; then
+// D / 8 lanes take a token, with all of a thread's loads on their way before the first is used.
 #include "kv4_common.cuh"
 
 namespace w4k {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTokens = 64;
+constexpr int kStarts = 1024;  // offsets kept in shared memory
+
+struct Places {
+  int32_t starts[kStarts + 1];
+  uint8_t* rec[kTokens];  // the token's record; nullptr if it has none
+  int row[kTokens];
+  float* weight[kTokens];  // its accumulated weight, or nullptr
+};
+
+// Threads 0 .. kTokens - 1 find tokens t0 .. (of `tokens`) of head h.
+__device__ __forceinline__ void find(Places& p, const Kv4View& c, const int32_t* starts, int tokens,
+                                     int t0, int h, uint32_t record_bytes, float* weights,
+                                     int weights_stride) {
+  const bool cached = c.batch <= kStarts;
+  if (cached)
+    for (int i = threadIdx.x; i <= c.batch; i += kThreads) p.starts[i] = starts[i];
+  __syncthreads();
+  if (threadIdx.x < kTokens) {
+    const int t = t0 + threadIdx.x;
+    uint8_t* rec = nullptr;
+    float* weight = nullptr;
+    int row = 0;
+    if (t < tokens) {
+      const int32_t* s = cached ? p.starts : starts;
+      int lo = 0, hi = c.batch;  // the first b whose end lies behind t
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (s[mid + 1] <= t)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      bool known = lo < c.batch && s[lo] <= t;
+      if (known) {
+        const Kv4Seq seq = kv4_sequence(c, starts, tokens, tokens, 0x7fffffff, lo);
+        const int pos = seq.n - seq.m + (t - seq.s0);
+        known = t >= seq.s0 && t < seq.s0 + seq.m && pos >= 0;
+        if (known) {
+          rec = kv4_record(c, c.table, c.width, lo, h, pos >> 4, record_bytes);
+          row = pos & 15;
+          if (weights != nullptr)
+            weight = weights + (static_cast<size_t>(lo) * c.kv_heads + h) * weights_stride + pos;
+        }
+      }
+      if (!known) atomicOr(c.status, kStatusIndex);
+    }
+    p.rec[threadIdx.x] = rec;
+    p.row[threadIdx.x] = row;
+    p.weight[threadIdx.x] = weight;
+  }
+  __syncthreads();
+}
 
 // Eight values of one group of `lanes` neighbouring lanes x 8 -> codes and the group's
-// scale | minimum word.
+// scale | minimum word. The code is rint((x - m) / s) of the fp32 quotient; a product with 1 / s is
+// within 1e-5 of it and has the same code unless it lies that near to a tie.
 __device__ __forceinline__ void quantize8(const uint4& x, int lanes, uint32_t (&q)[8],
                                           uint32_t& param) {
-  float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
-                bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
+  const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
+                      bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
   float mx = f[0], mn = f[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
@@ -28,157 +84,166 @@ __device__ __forceinline__ void quantize8(const uint4& x, int lanes, uint32_t (&
   }
   const uint32_t sb = __bfloat16_as_ushort(__float2bfloat16_rn((mx - mn) / 15.0f));
   const uint32_t mb = __bfloat16_as_ushort(__float2bfloat16_rn(mn));
+  param = sb | (mb << 16);
   const float s = bf16_bits_to_f32(sb), m = bf16_bits_to_f32(mb);
+  if (s == 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = 0u;
+    return;
+  }
+  const float inv = 1.0f / s;
+  const float magic = 12582912.0f;  // adding it rounds to a whole number, half to even
+  bool ties = !(inv <= 3e38f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float r = s == 0.0f ? 0.0f : rintf((f[i] - m) / s);
-    q[i] = static_cast<uint32_t>(fminf(fmaxf(r, 0.0f), 15.0f));
+    const float t = fminf(fmaxf((f[i] - m) * inv, 0.0f), 15.0f);
+    const float n = t + magic;
+    q[i] = __float_as_uint(n) & 15u;
+    ties = ties || fabsf(t - (n - magic)) > 0.4999f;
   }
-  param = sb | (mb << 16);
+  if (ties) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      q[i] = __float_as_uint(fminf(fmaxf((f[i] - m) / s, 0.0f), 15.0f) + magic) & 15u;
+  }
 }
 
-// D / 8 neighbouring lanes take one token of one head, 8 dims each.
+// D / 8 neighbouring lanes take one token, 8 dims each.
 template <int D, int NG>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   using R = Kv4Record<D, NG>;
-  constexpr int kLanes = D / 8, kItems = kThreads / kLanes;
+  constexpr int kLanes = D / 8, kAtOnce = kThreads / kLanes, kRounds = kTokens / kAtOnce;
+  __shared__ Places p;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t items = static_cast<int64_t>(a.tokens) * a.c.kv_heads;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + threadIdx.x / kLanes;
-  const int j = threadIdx.x % kLanes;
-  const int64_t it = item < items ? item : items - 1;
-  const int t = static_cast<int>(it / a.c.kv_heads), h = static_cast<int>(it % a.c.kv_heads);
-  // the sequence of this lane's token: starts has batch + 1 non-decreasing entries
-  int lo = 0, hi = a.c.batch;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (a.starts[mid + 1] <= t)
-      lo = mid + 1;
-    else
-      hi = mid;
+  const int t0 = blockIdx.x * kTokens, h = blockIdx.y;
+  const int j = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+  uint4 k[kRounds], v[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int t = t0 + first + i * kAtOnce;
+    k[i] = v[i] = make_uint4(0, 0, 0, 0);
+    if (t < a.tokens) {
+      k[i] = __ldg(reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + 8 * j));
+      v[i] = __ldg(reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + 8 * j));
+    }
   }
-  const int b = min(lo, a.c.batch - 1);
-  const Kv4Seq s = kv4_sequence(a.c, a.starts, a.tokens, a.tokens, 0x7fffffff, b);
-  const int pos = s.n - s.m + (t - s.s0);
-  uint32_t kq[8], vq[8], kp, vp;
-  quantize8(*reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + 8 * j), R::kGroup / 8,
-            kq, kp);
-  quantize8(*reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + 8 * j), R::kGroup / 8,
-            vq, vp);
-  if (item >= items) return;
-  if (lo >= a.c.batch || t < s.s0 || t >= s.s0 + s.m || pos < 0) {
-    atomicOr(a.c.status, kStatusIndex);
-    return;
-  }
-  uint8_t* rec = kv4_record(a.c, a.c.table, a.c.width, b, h, pos >> 4, R::kBytes);
-  if (rec == nullptr) return;
-  const int row = pos & 15;
+  find(p, a.c, a.starts, a.tokens, t0, h, R::kBytes, a.weights, a.weights_stride);
   const int blk = j / 4, c = j % 4;  // dims 8 j = 32 blk + 8 c
-  uint32_t kw = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) kw |= kq[e] << (4 * (e / 2) + 16 * (e % 2));
-  reinterpret_cast<uint32_t*>(rec)[(row * 4 + c) * R::kBlocks + blk] = kw;
-  uint16_t* vh = reinterpret_cast<uint16_t*>(rec + R::kV);
+  for (int i = 0; i < kRounds; ++i) {
+    const int at = first + i * kAtOnce;
+    if (__all_sync(0xffffffffu, t0 + at >= a.tokens)) break;
+    uint32_t kq[8], vq[8], kp, vp;
+    quantize8(k[i], R::kGroup / 8, kq, kp);
+    quantize8(v[i], R::kGroup / 8, vq, vp);
+    uint32_t kw = 0, vw[2] = {0, 0};
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const uint32_t w = vq[4 * u] | (vq[4 * u + 1] << 4) | (vq[4 * u + 2] << 8) |
-                       (vq[4 * u + 3] << 12);
-    vh[2 * (((row / 2) * 8 + 2 * c + u) * R::kBlocks + blk) + row % 2] = static_cast<uint16_t>(w);
+    for (int e = 0; e < 8; ++e) {
+      kw |= kq[e] << (4 * (e / 2) + 16 * (e % 2));
+      vw[e / 4] |= vq[e] << (4 * (e % 4));
+    }
+    uint8_t* rec = p.rec[at];
+    const int row = p.row[at];
+    // the token of the other half of a V word, if a lane of this warp has it
+    const int other = at ^ 1;
+    const bool pair = rec != nullptr && p.rec[other] == rec && (p.row[other] ^ row) == 1 &&
+                      row % 2 == at % 2 && 32 % (2 * kLanes) == 0;
+    const uint32_t out = __shfl_xor_sync(0xffffffffu, row % 2 == 0 ? vw[1] : vw[0], kLanes);
+    if (rec == nullptr) continue;
+    reinterpret_cast<uint32_t*>(rec)[(row * 4 + c) * R::kBlocks + blk] = kw;
+    uint32_t* words = reinterpret_cast<uint32_t*>(rec + R::kV) +
+                      ((row / 2) * 8 + 2 * c) * R::kBlocks + blk;
+    if (pair) {
+      // the even token's lane writes the first word of the two, the odd one's the second
+      if (row % 2 == 0)
+        words[0] = vw[0] | (out << 16);
+      else
+        words[R::kBlocks] = out | (vw[1] << 16);
+    } else {
+      reinterpret_cast<uint16_t*>(words)[row % 2] = static_cast<uint16_t>(vw[0]);
+      reinterpret_cast<uint16_t*>(words + R::kBlocks)[row % 2] = static_cast<uint16_t>(vw[1]);
+    }
+    if (j % (R::kGroup / 8) == 0) {
+      const int g = 8 * j / R::kGroup;
+      reinterpret_cast<uint32_t*>(rec + R::kKParams)[16 * g + row] = kp;
+      reinterpret_cast<uint32_t*>(rec + R::kVParams)[16 * g + row] = vp;
+    }
+    if (j == 0 && p.weight[at] != nullptr) *p.weight[at] = 0.0f;
   }
-  if (j % (R::kGroup / 8) == 0) {
-    const int g = 8 * j / R::kGroup;
-    reinterpret_cast<uint32_t*>(rec + R::kKParams)[16 * g + row] = kp;
-    reinterpret_cast<uint32_t*>(rec + R::kVParams)[16 * g + row] = vp;
-  }
-  if (j == 0 && a.weights != nullptr)
-    a.weights[(static_cast<size_t>(b) * a.c.kv_heads + h) * a.weights_stride + pos] = 0.0f;
 }
 
 template <int D, int NG>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4ReadArgs a) {
   using R = Kv4Record<D, NG>;
-  constexpr int kLanes = D / 8, kItems = kThreads / kLanes;
+  constexpr int kLanes = D / 8, kAtOnce = kThreads / kLanes, kRounds = kTokens / kAtOnce;
+  __shared__ Places p;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t items = static_cast<int64_t>(a.tokens) * a.c.kv_heads;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + threadIdx.x / kLanes;
-  const int j = threadIdx.x % kLanes;
-  if (item >= items) return;
-  const int t = static_cast<int>(item / a.c.kv_heads), h = static_cast<int>(item % a.c.kv_heads);
-  int lo = 0, hi = a.c.batch;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (a.starts[mid + 1] <= t)
-      lo = mid + 1;
-    else
-      hi = mid;
+  const int t0 = blockIdx.x * kTokens, h = blockIdx.y;
+  find(p, a.c, a.starts, a.tokens, t0, h, R::kBytes, nullptr, 0);
+  const int j = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+  const int blk = j / 4, c = j % 4, g = 8 * j / R::kGroup;
+  uint32_t kw[kRounds], vw[kRounds][2], kp[kRounds], vp[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const uint8_t* rec = p.rec[first + i * kAtOnce];
+    const int row = p.row[first + i * kAtOnce];
+    kw[i] = vw[i][0] = vw[i][1] = kp[i] = vp[i] = 0u;
+    if (rec == nullptr) continue;
+    kw[i] = reinterpret_cast<const uint32_t*>(rec)[(row * 4 + c) * R::kBlocks + blk];
+    kp[i] = reinterpret_cast<const uint32_t*>(rec + R::kKParams)[16 * g + row];
+    vp[i] = reinterpret_cast<const uint32_t*>(rec + R::kVParams)[16 * g + row];
+    const uint16_t* half = reinterpret_cast<const uint16_t*>(rec + R::kV);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      vw[i][u] = half[2 * (((row / 2) * 8 + 2 * c + u) * R::kBlocks + blk) + row % 2];
   }
-  const int b = min(lo, a.c.batch - 1);
-  const Kv4Seq s = kv4_sequence(a.c, a.starts, a.tokens, a.tokens, 0x7fffffff, b);
-  const int pos = s.n - s.m + (t - s.s0);
-  uint8_t* rec = nullptr;
-  if (lo >= a.c.batch || t < s.s0 || t >= s.s0 + s.m || pos < 0)
-    atomicOr(a.c.status, kStatusIndex);
-  else
-    rec = kv4_record(a.c, a.c.table, a.c.width, b, h, pos >> 4, R::kBytes);
-  uint32_t ko[4] = {0, 0, 0, 0}, vo[4] = {0, 0, 0, 0};
-  if (rec != nullptr) {
-    const int row = pos & 15, blk = j / 4, c = j % 4, g = 8 * j / R::kGroup;
-    const uint32_t kw = reinterpret_cast<const uint32_t*>(rec)[(row * 4 + c) * R::kBlocks + blk];
-    const uint32_t kp = reinterpret_cast<const uint32_t*>(rec + R::kKParams)[16 * g + row];
-    const uint32_t vp = reinterpret_cast<const uint32_t*>(rec + R::kVParams)[16 * g + row];
-    const uint16_t* vh = reinterpret_cast<const uint16_t*>(rec + R::kV);
-    const float ks = bf16_lo(kp), km = bf16_hi(kp), vs = bf16_lo(vp), vm = bf16_hi(vp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ko[i] = bf16x2_bits(fmaf(static_cast<float>((kw >> (4 * i)) & 15u), ks, km),
-                          fmaf(static_cast<float>((kw >> (16 + 4 * i)) & 15u), ks, km));
+  for (int i = 0; i < kRounds; ++i) {
+    const int t = t0 + first + i * kAtOnce;
+    if (t >= a.tokens) break;
+    const float ks = bf16_lo(kp[i]), km = bf16_hi(kp[i]), vs = bf16_lo(vp[i]), vm = bf16_hi(vp[i]);
+    uint32_t ko[4], vo[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t w = vh[2 * (((row / 2) * 8 + 2 * c + u) * R::kBlocks + blk) + row % 2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        vo[2 * u + i] = bf16x2_bits(fmaf(static_cast<float>((w >> (8 * i)) & 15u), vs, vm),
-                                    fmaf(static_cast<float>((w >> (8 * i + 4)) & 15u), vs, vm));
+    for (int e = 0; e < 4; ++e) {
+      ko[e] = bf16x2_bits(fmaf(static_cast<float>((kw[i] >> (4 * e)) & 15u), ks, km),
+                          fmaf(static_cast<float>((kw[i] >> (16 + 4 * e)) & 15u), ks, km));
+      const uint32_t w = vw[i][e / 2] >> (8 * (e % 2));
+      vo[e] = bf16x2_bits(fmaf(static_cast<float>(w & 15u), vs, vm),
+                          fmaf(static_cast<float>((w >> 4) & 15u), vs, vm));
     }
+    const size_t at = (static_cast<size_t>(t) * a.c.kv_heads + h) * D + 8 * j;
+    *reinterpret_cast<uint4*>(a.k + at) = make_uint4(ko[0], ko[1], ko[2], ko[3]);
+    *reinterpret_cast<uint4*>(a.v + at) = make_uint4(vo[0], vo[1], vo[2], vo[3]);
   }
-  const size_t at = static_cast<size_t>(item) * D + 8 * j;
-  *reinterpret_cast<uint4*>(a.k + at) = make_uint4(ko[0], ko[1], ko[2], ko[3]);
-  *reinterpret_cast<uint4*>(a.v + at) = make_uint4(vo[0], vo[1], vo[2], vo[3]);
 }
 
-template <int D, int NG>
-cudaError_t append(const Kv4AppendArgs& a, cudaStream_t stream) {
-  const int64_t per = kThreads / (D / 8);
-  const int64_t items = static_cast<int64_t>(a.tokens) * a.c.kv_heads;
-  return launch_with_pdl(kv4_append_kernel<D, NG>, dim3(static_cast<unsigned>((items + per - 1) / per)),
-                         dim3(kThreads), 0, stream, a);
-}
-
-template <int D, int NG>
-cudaError_t read(const Kv4ReadArgs& a, cudaStream_t stream) {
-  const int64_t per = kThreads / (D / 8);
-  const int64_t items = static_cast<int64_t>(a.tokens) * a.c.kv_heads;
-  return launch_with_pdl(kv4_read_kernel<D, NG>, dim3(static_cast<unsigned>((items + per - 1) / per)),
-                         dim3(kThreads), 0, stream, a);
+dim3 grid_of(int tokens, int kv_heads) {
+  return dim3((tokens + kTokens - 1) / kTokens, kv_heads);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int head_dim, int group,
                               cudaStream_t stream) {
+  auto run = [&](auto kern) {
+    return launch_with_pdl(kern, grid_of(a.tokens, a.c.kv_heads), dim3(kThreads), 0, stream, a);
+  };
   if (head_dim == 128)
-    return group == 128 ? append<128, 1>(a, stream)
-           : group == 64 ? append<128, 2>(a, stream) : append<128, 4>(a, stream);
-  return group == 64 ? append<64, 1>(a, stream) : append<64, 2>(a, stream);
+    return group == 128 ? run(kv4_append_kernel<128, 1>)
+           : group == 64 ? run(kv4_append_kernel<128, 2>) : run(kv4_append_kernel<128, 4>);
+  return group == 64 ? run(kv4_append_kernel<64, 1>) : run(kv4_append_kernel<64, 2>);
 }
 
 cudaError_t launch_kv4_read(const Kv4ReadArgs& a, int head_dim, int group, cudaStream_t stream) {
+  auto run = [&](auto kern) {
+    return launch_with_pdl(kern, grid_of(a.tokens, a.c.kv_heads), dim3(kThreads), 0, stream, a);
+  };
   if (head_dim == 128)
-    return group == 128 ? read<128, 1>(a, stream)
-           : group == 64 ? read<128, 2>(a, stream) : read<128, 4>(a, stream);
-  return group == 64 ? read<64, 1>(a, stream) : read<64, 2>(a, stream);
+    return group == 128 ? run(kv4_read_kernel<128, 1>)
+           : group == 64 ? run(kv4_read_kernel<128, 2>) : run(kv4_read_kernel<128, 4>);
+  return group == 64 ? run(kv4_read_kernel<64, 1>) : run(kv4_read_kernel<64, 2>);
 }
 
 }  // namespace w4k

@@ -18,16 +18,160 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA a (head, sequence): the smallest kept key by four 8-bit radix passes, then the kept
-// indices by a running count over the tokens in order.
-__global__ void __launch_bounds__(kSelectThreads) kv4_select_kernel(const Kv4EvictArgs a) {
+// One CTA a (head, sequence): the smallest kept key, then the kept indices by counts over the
+// tokens in order. Up to kHeld tokens that may go stay in registers, 16 a thread, and the key is
+// found two bits at a time by counting the keys at three candidates (16 rounds of one barrier:
+// 2 us for 8192 tokens; a histogram of key bytes meets itself in the few bins that steep weights
+// fill, 20 us). More tokens than that take four passes of such a histogram.
+constexpr int kHeld = 16;
+
+struct Select {
+  const float* w;
+  float* w_out;
+  int32_t* kept;
+  int lo, hi, k;  // of the tokens lo .. hi - 1, k stay
+};
+
+__device__ __forceinline__ void select_held(const Select& q) {
+  __shared__ uint32_t counts[2][32];
+  __shared__ uint32_t before[kHeld * 32];  // tokens above (low half) and at the key, per warp
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rounds = (q.hi - q.lo + kSelectThreads - 1) / kSelectThreads;
+  float x[kHeld];
+  uint32_t key[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const int i = q.lo + tid + j * kSelectThreads;
+    x[j] = i < q.hi ? q.w[i] : 0.f;
+    key[j] = i < q.hi ? order_key(x[j]) : 0u;
+  }
+  // tokens that are not there have key 0 and never count: candidates are above it
+  uint32_t at = 0;
+  const uint32_t need = static_cast<uint32_t>(q.k);
+  for (int shift = 30, turn = 0; shift >= 0; shift -= 2, turn ^= 1) {
+    uint32_t c = 0;  // three counts of ten bits: a warp has 512 keys
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (j >= rounds) break;
+#pragma unroll
+      for (uint32_t b = 1; b < 4; ++b) c += key[j] >= (at | (b << shift)) ? 1u << (10 * (b - 1)) : 0u;
+    }
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) counts[turn][warp] = c;
+    __syncthreads();
+    c = counts[turn][lane];
+    uint32_t bits = 0;
+#pragma unroll
+    for (uint32_t b = 1; b < 4; ++b)
+      if (__reduce_add_sync(0xffffffffu, (c >> (10 * (b - 1))) & 1023u) >= need) bits = b;
+    at |= bits << shift;
+  }
+  // counts above and at the key, warp by warp in the tokens' order
+  uint32_t above[kHeld], equal[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    if (j >= rounds) break;
+    const bool there = q.lo + tid + j * kSelectThreads < q.hi;
+    above[j] = __ballot_sync(0xffffffffu, there && key[j] > at);
+    equal[j] = __ballot_sync(0xffffffffu, there && key[j] == at);
+    if (lane == 0) before[j * 32 + warp] = __popc(above[j]) | (__popc(equal[j]) << 16);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t base = 0;
+    for (int j = 0; j < rounds; ++j) {
+      const uint32_t mine = before[j * 32 + lane];
+      uint32_t upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      before[j * 32 + lane] = base + upto - mine;
+      base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) counts[0][0] = base & 0xFFFFu;  // all above
+  }
+  __syncthreads();
+  const uint32_t ties = need - counts[0][0];  // of the tokens at the key, the first ones stay
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    if (j >= rounds) break;
+    const uint32_t b = before[j * 32 + warp];
+    const uint32_t g = (b & 0xFFFFu) + __popc(above[j] & below);
+    const uint32_t e = (b >> 16) + __popc(equal[j] & below);
+    const bool is_above = (above[j] >> lane) & 1u, is_equal = (equal[j] >> lane) & 1u;
+    if (is_above || (is_equal && e < ties)) {
+      const uint32_t to = q.lo + g + min(e, ties);
+      q.kept[to] = q.lo + tid + j * kSelectThreads;
+      q.w_out[to] = x[j];
+    }
+  }
+}
+
+__device__ __forceinline__ void select_long(const Select& q) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t warp_gt[32], warp_eq[32];
   __shared__ uint32_t s_prefix, s_need;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    s_prefix = 0u;
+    s_need = static_cast<uint32_t>(q.k);
+  }
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < 256) hist[tid] = 0u;
+    __syncthreads();
+    const uint32_t prefix = s_prefix;
+    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    for (int i = q.lo + tid; i < q.hi; i += kSelectThreads) {
+      const uint32_t key = order_key(q.w[i]);
+      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t need = s_need;
+      int bin = 255;
+      while (bin > 0 && hist[bin] < need) need -= hist[bin--];
+      s_need = need;
+      s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
+    }
+    __syncthreads();
+  }
+  const uint32_t threshold = s_prefix, need = s_need;  // need of the keys equal to it stay
+  uint32_t gt_before = 0, eq_before = 0;
+  for (int base = q.lo; base < q.hi; base += kSelectThreads) {
+    const int i = base + tid;
+    const float x = i < q.hi ? q.w[i] : 0.f;
+    const uint32_t key = order_key(x);
+    const bool gt = i < q.hi && key > threshold, eq = i < q.hi && key == threshold;
+    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) {
+      warp_gt[warp] = __popc(bg);
+      warp_eq[warp] = __popc(be);
+    }
+    __syncthreads();
+    const uint32_t g_lane = warp_gt[lane], e_lane = warp_eq[lane];
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t g = gt_before + __reduce_add_sync(0xffffffffu, lane < warp ? g_lane : 0u) +
+                       __popc(bg & below);
+    const uint32_t e = eq_before + __reduce_add_sync(0xffffffffu, lane < warp ? e_lane : 0u) +
+                       __popc(be & below);
+    if (gt || (eq && e < need)) {
+      const uint32_t at = q.lo + g + min(e, need);
+      q.kept[at] = i;
+      q.w_out[at] = x;
+    }
+    gt_before += __reduce_add_sync(0xffffffffu, g_lane);
+    eq_before += __reduce_add_sync(0xffffffffu, e_lane);
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kSelectThreads) kv4_select_kernel(const Kv4EvictArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
   const int len = a.c.lens[b];
   const int n = min(max(len, 0), min(a.max_len, a.c.width << a.c.page_shift));
   if (n != len && tid == 0) atomicOr(a.c.status, kStatusIndex);
@@ -45,123 +189,111 @@ __global__ void __launch_bounds__(kSelectThreads) kv4_select_kernel(const Kv4Evi
     }
     return;
   }
-  const int lo = a.first, hi = n - a.recent, k = a.budget - a.first - a.recent;
-  for (int i = tid; i < lo; i += kSelectThreads) {
+  const Select q = {w, w_out, kept, a.first, n - a.recent, a.budget - a.first - a.recent};
+  for (int i = tid; i < q.lo; i += kSelectThreads) {
     kept[i] = i;
     w_out[i] = w[i];
   }
   for (int i = tid; i < a.recent; i += kSelectThreads) {
-    kept[lo + k + i] = hi + i;
-    w_out[lo + k + i] = w[hi + i];
+    kept[q.lo + q.k + i] = q.hi + i;
+    w_out[q.lo + q.k + i] = w[q.hi + i];
   }
-  if (k == 0) return;
-  if (tid == 0) {
-    s_prefix = 0u;
-    s_need = static_cast<uint32_t>(k);
-  }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0u;
-    __syncthreads();
-    const uint32_t prefix = s_prefix;
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int i = lo + tid; i < hi; i += kSelectThreads) {
-      const uint32_t key = order_key(w[i]);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t need = s_need;
-      int bin = 255;
-      while (bin > 0 && hist[bin] < need) need -= hist[bin--];
-      s_need = need;
-      s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-    }
-    __syncthreads();
-  }
-  const uint32_t threshold = s_prefix, need = s_need;  // need of the keys equal to it stay
-  uint32_t gt_before = 0, eq_before = 0;
-  for (int base = lo; base < hi; base += kSelectThreads) {
-    const int i = base + tid;
-    const float x = i < hi ? w[i] : 0.f;
-    const uint32_t key = order_key(x);
-    const bool gt = i < hi && key > threshold, eq = i < hi && key == threshold;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      warp_gt[warp] = __popc(bg);
-      warp_eq[warp] = __popc(be);
-    }
-    __syncthreads();
-    uint32_t g = 0, e = 0, g_all = 0, e_all = 0;
-    for (int x2 = 0; x2 < kSelectThreads / 32; ++x2) {
-      if (x2 < warp) {
-        g += warp_gt[x2];
-        e += warp_eq[x2];
-      }
-      g_all += warp_gt[x2];
-      e_all += warp_eq[x2];
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    g += gt_before + __popc(bg & below);
-    e += eq_before + __popc(be & below);
-    if (gt || (eq && e < need)) {
-      const uint32_t at = lo + g + min(e, need);
-      kept[at] = i;
-      w_out[at] = x;
-    }
-    gt_before += g_all;
-    eq_before += e_all;
-    __syncthreads();
-  }
+  if (q.k == 0) return;
+  if (q.hi - q.lo <= kHeld * kSelectThreads)
+    select_held(q);
+  else
+    select_long(q);
 }
 
-constexpr int kMoveThreads = 128;
+// A CTA four destination records of a head, all of a thread's loads before its first store.
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRecords = 4;
+constexpr int kMoveTokens = 16 * kMoveRecords;
 
-// One CTA a destination record.
 template <int D, int NG>
 __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(const Kv4EvictArgs a) {
   using R = Kv4Record<D, NG>;
-  __shared__ const uint8_t* src[16];
-  __shared__ int row[16];
+  __shared__ const uint8_t* src[kMoveTokens];
+  __shared__ int row[kMoveTokens];
+  __shared__ uint8_t* dst[kMoveRecords];
   pdl_launch_dependents();
   pdl_wait();
-  const int rec = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int n = min(max(a.c.lens[b], 0), min(a.max_len, a.c.width << a.c.page_shift));
-  const int m = min(n, a.budget);
-  const int count = min(16, m - 16 * rec);
-  if (count <= 0) return;
-  if (tid < 16) {
-    const uint8_t* p = nullptr;
-    int i = 0;
-    if (tid < count) {
-      i = a.kept[(static_cast<size_t>(b) * a.c.kv_heads + h) * a.budget + 16 * rec + tid];
-      p = kv4_record(a.c, a.c.table, a.c.width, b, h, i >> 4, R::kBytes);
-    }
-    src[tid] = p;
+  const int rec0 = blockIdx.x * kMoveRecords, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  if (tid < kMoveTokens) {
+    const int to = 16 * rec0 + tid;
+    // -1 past the kept ones
+    const int i = to < a.budget
+                      ? a.kept[(static_cast<size_t>(b) * a.c.kv_heads + h) * a.budget + to]
+                      : -1;
+    src[tid] = i < 0 ? nullptr : kv4_record(a.c, a.c.table, a.c.width, b, h, i >> 4, R::kBytes);
     row[tid] = i & 15;
+    if (tid % 16 == 0)
+      dst[tid / 16] = i < 0 ? nullptr
+                            : kv4_record(a.c, a.out_table, a.out_width, b, h, rec0 + tid / 16, R::kBytes);
   }
-  uint8_t* dst = kv4_record(a.c, a.out_table, a.out_width, b, h, rec, R::kBytes);
   __syncthreads();
-  if (dst == nullptr) return;
-  constexpr int kKWords = 4 * R::kBlocks;
-  for (int x = tid; x < 16 * kKWords; x += kMoveThreads) {
-    const int t = x / kKWords, w = x % kKWords;
-    if (src[t] != nullptr)
-      reinterpret_cast<uint32_t*>(dst)[x] =
-          reinterpret_cast<const uint32_t*>(src[t])[row[t] * kKWords + w];
+  constexpr int kWords = D / 8;  // 32-bit words of a token's K codes; V: 16-bit pieces, twice them
+  constexpr int kPer = kMoveTokens * kWords / kMoveThreads;
+  constexpr int kParams = kMoveTokens * 2 * NG / kMoveThreads;  // per thread, rounded up below
+  uint32_t k[kPer], v[kPer], p[kParams + 1];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int x = tid + i * kMoveThreads, t = x / kWords, w = x % kWords;
+    k[i] = src[t] == nullptr
+               ? 0u
+               : __ldg(reinterpret_cast<const uint32_t*>(src[t]) + row[t] * kWords + w);
   }
-  constexpr int kVHalves = D / 4;  // 16-bit pieces of a token
-  for (int x = tid; x < 16 * kVHalves; x += kMoveThreads) {
-    const int pair = x / (2 * kVHalves), w = (x / 2) % kVHalves, t = 2 * pair + x % 2;
-    if (src[t] != nullptr)
-      reinterpret_cast<uint16_t*>(dst + R::kV)[x] = reinterpret_cast<const uint16_t*>(
-          src[t] + R::kV)[((row[t] / 2) * kVHalves + w) * 2 + row[t] % 2];
+  // word w of a pair of tokens, a half from each
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int x = tid + i * kMoveThreads, t = x / (2 * kWords) * 2, w = x % (2 * kWords);
+    uint32_t half[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      half[u] = src[t + u] == nullptr
+                    ? 0u
+                    : __ldg(reinterpret_cast<const uint16_t*>(src[t + u] + R::kV) +
+                            ((row[t + u] / 2) * 2 * kWords + w) * 2 + row[t + u] % 2);
+    v[i] = half[0] | (half[1] << 16);
   }
-  for (int x = tid; x < 2 * 16 * NG; x += kMoveThreads) {
-    const int t = x % 16, g = (x / 16) % NG;
-    const uint32_t off = x / 16 < NG ? R::kKParams : R::kVParams;
+#pragma unroll
+  for (int i = 0; i <= kParams; ++i) {
+    const int x = tid + i * kMoveThreads;
+    p[i] = 0u;
+    if (x >= kMoveTokens * 2 * NG) break;
+    const int t = x / (32 * NG) * 16 + x % 16, g = x / 16 % (2 * NG);
     if (src[t] != nullptr)
-      reinterpret_cast<uint32_t*>(dst + off)[16 * g + t] =
-          reinterpret_cast<const uint32_t*>(src[t] + off)[16 * g + row[t]];
+      p[i] = __ldg(reinterpret_cast<const uint32_t*>(
+                       src[t] + (g < NG ? R::kKParams : R::kVParams)) +
+                   16 * (g % NG) + row[t]);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int x = tid + i * kMoveThreads, t = x / kWords;
+    if (src[t] != nullptr && dst[t / 16] != nullptr)
+      reinterpret_cast<uint32_t*>(dst[t / 16])[x % (16 * kWords)] = k[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int x = tid + i * kMoveThreads, t = x / (2 * kWords) * 2;
+    uint8_t* d = dst[t / 16];
+    if (d == nullptr) continue;
+    uint32_t* to = reinterpret_cast<uint32_t*>(d + R::kV) + x % (16 * kWords);
+    if (src[t] != nullptr && src[t + 1] != nullptr)
+      *to = v[i];
+    else if (src[t] != nullptr)
+      *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(v[i]);
+    else if (src[t + 1] != nullptr)
+      reinterpret_cast<uint16_t*>(to)[1] = static_cast<uint16_t>(v[i] >> 16);
+  }
+#pragma unroll
+  for (int i = 0; i <= kParams; ++i) {
+    const int x = tid + i * kMoveThreads;
+    if (x >= kMoveTokens * 2 * NG) break;
+    const int t = x / (32 * NG) * 16 + x % 16, g = x / 16 % (2 * NG);
+    if (src[t] != nullptr && dst[t / 16] != nullptr)
+      reinterpret_cast<uint32_t*>(dst[t / 16] + (g < NG ? R::kKParams : R::kVParams))[16 * (g % NG) +
+                                                                                     t % 16] = p[i];
   }
 }
 
@@ -171,8 +303,8 @@ cudaError_t run(const Kv4EvictArgs& a, cudaStream_t stream) {
                                   dim3(kSelectThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
   return launch_with_pdl(kv4_move_kernel<D, NG>,
-                         dim3((a.budget + 15) / 16, a.c.kv_heads, a.c.batch), dim3(kMoveThreads),
-                         0, stream, a);
+                         dim3((a.budget + kMoveTokens - 1) / kMoveTokens, a.c.kv_heads, a.c.batch),
+                         dim3(kMoveThreads), 0, stream, a);
 }
 
 }  // namespace

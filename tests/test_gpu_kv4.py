@@ -331,6 +331,16 @@ def test_out_of_range_numbers_are_reported_not_followed(new):
     ([50, 16, 70], 33, 2, 7), ([2000, 40], 100, 0, 0), ([100], 64, 30, 34), ([40, 0], 1, 0, 1),
     ([1100], 1030, 1, 2)])
 def test_evict(D, group, page, lens, budget, first, recent):
+    _check_evict(D, group, page, lens, budget, first, recent)
+
+
+@pytest.mark.parametrize("budget,first,recent", [(300, 4, 50), (17000, 0, 1)])
+def test_evict_from_a_long_cache(budget, first, recent):
+    """More tokens that may go than a block holds in registers (16384)."""
+    _check_evict(64, 64, 256, [17500, 16500], budget, first, recent)
+
+
+def _check_evict(D, group, page, lens, budget, first, recent):
     H, seed = 2, 14
     out_width = (budget + page - 1) // page
     cache, order, at = _fill(lens, H, D, group, page, seed, extra=len(lens) * out_width)
@@ -350,20 +360,19 @@ def test_evict(D, group, page, lens, budget, first, recent):
     assert np.array_equal(got.cpu().numpy(), kept)
     assert new_lens.tolist() == [min(n, budget) for n in lens]
     w_out = w_out.cpu().numpy()
-    want = ref.Cache(cache.data.copy(), out_table, D, group)
+    moved = ref.Cache(data.cpu().numpy(), out_table, D, group)
     for b, n in enumerate(lens):
         for h in range(H):
             m = min(n, budget)
             assert np.array_equal(w_out[b, h, :m], w[b, h, kept[b, h, :m]], equal_nan=True)
             k, v = cache.get(b, h, n)
-            moved = ref.Cache(data.cpu().numpy(), out_table, D, group)
             k2, v2 = moved.get(b, h, m)
             assert np.array_equal(k2, k[kept[b, h, :m]]) and np.array_equal(v2, v[kept[b, h, :m]])
-    after = data.cpu().numpy()
+    after = moved.data
     used = np.zeros(len(after), bool)
     for b, n in enumerate(lens):
         used[out_table[b, :(min(n, budget) + page - 1) // page]] = True
-    assert np.array_equal(after[~used], want.data[~used])
+    assert np.array_equal(after[~used], cache.data[~used])
 
 
 def test_a_decoding_loop_with_eviction():
