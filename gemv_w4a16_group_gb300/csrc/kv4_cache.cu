@@ -2,7 +2,7 @@
 //
 // Both move every value once and compute a handful of operations on it, so memory bounds them:
 // an append reads 4 bytes and writes 1 + 8 / group bytes for a dim's key and value, a read the
-// other way round. A block takes 64 tokens of one head. Where each of them lies (its sequence,
+// other way round. A block takes 32 tokens of one head. Where each of them lies (its sequence,
 // page and row, three loads that wait for one another) is found once, by a thread a token; then
 // D / 8 lanes take a token, with all of a thread's loads on their way before the first is used.
 #include "kv4_common.cuh"
@@ -11,11 +11,11 @@ namespace w4k {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 64;
-constexpr int kStarts = 1024;  // offsets kept in shared memory
+constexpr int kTokens = 32;
+constexpr int kStarts = 512;  // sequences whose offsets and lengths are kept in shared memory
 
 struct Places {
-  int32_t starts[kStarts + 1];
+  int32_t starts[kStarts + 1], lens[kStarts];
   uint8_t* rec[kTokens];  // the token's record; nullptr if it has none
   int row[kTokens];
   float* weight[kTokens];  // its accumulated weight, or nullptr
@@ -27,7 +27,10 @@ __device__ __forceinline__ void find(Places& p, const Kv4View& c, const int32_t*
                                      int weights_stride) {
   const bool cached = c.batch <= kStarts;
   if (cached)
-    for (int i = threadIdx.x; i <= c.batch; i += kThreads) p.starts[i] = starts[i];
+    for (int i = threadIdx.x; i <= c.batch; i += kThreads) {
+      p.starts[i] = starts[i];
+      if (i < c.batch) p.lens[i] = c.lens[i];
+    }
   __syncthreads();
   if (threadIdx.x < kTokens) {
     const int t = t0 + threadIdx.x;
@@ -46,7 +49,8 @@ __device__ __forceinline__ void find(Places& p, const Kv4View& c, const int32_t*
       }
       bool known = lo < c.batch && s[lo] <= t;
       if (known) {
-        const Kv4Seq seq = kv4_sequence(c, starts, tokens, tokens, 0x7fffffff, lo);
+        const Kv4Seq seq = kv4_clamped(c, cached ? p.lens[lo] : c.lens[lo], s[lo], s[lo + 1], tokens,
+                                       tokens, 0x7fffffff);
         const int pos = seq.n - seq.m + (t - seq.s0);
         known = t >= seq.s0 && t < seq.s0 + seq.m && pos >= 0;
         if (known) {
@@ -65,19 +69,31 @@ __device__ __forceinline__ void find(Places& p, const Kv4View& c, const int32_t*
   __syncthreads();
 }
 
-// Eight values of one group of `lanes` neighbouring lanes x 8 -> codes and the group's
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Four codes, whole numbers 0..15 as floats, in the nibbles of 16 bits: exact sums under 2^23.
+__device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) {
+  return __float_as_uint(fmaf(fmaf(d, 16.f, c), 256.f, fmaf(b, 16.f, a + 8388608.f)));
+}
+
+// Eight values of one group of `lanes` neighbouring lanes x 8 -> codes (as floats) and the group's
 // scale | minimum word. The code is rint((x - m) / s) of the fp32 quotient; a product with 1 / s is
 // within 1e-5 of it and has the same code unless it lies that near to a tie.
-__device__ __forceinline__ void quantize8(const uint4& x, int lanes, uint32_t (&q)[8],
+__device__ __forceinline__ void quantize8(const uint4& x, int lanes, float (&q)[8],
                                           uint32_t& param) {
   const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
                       bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
-  float mx = f[0], mn = f[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    mx = fmaxf(mx, f[i]);
-    mn = fminf(mn, f[i]);
-  }
+  float mx = max3(max3(f[0], f[1], f[2]), max3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+  float mn = min3(min3(f[0], f[1], f[2]), min3(f[3], f[4], f[5]), fminf(f[6], f[7]));
   for (int o = 1; o < lanes; o <<= 1) {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -86,25 +102,24 @@ __device__ __forceinline__ void quantize8(const uint4& x, int lanes, uint32_t (&
   const uint32_t mb = __bfloat16_as_ushort(__float2bfloat16_rn(mn));
   param = sb | (mb << 16);
   const float s = bf16_bits_to_f32(sb), m = bf16_bits_to_f32(mb);
-  if (s == 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = 0u;
-    return;
-  }
-  const float inv = 1.0f / s;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  if (s == 0.0f) inv = 0.0f;  // codes 0
   const float magic = 12582912.0f;  // adding it rounds to a whole number, half to even
-  bool ties = !(inv <= 3e38f);
+  // tiny and huge scales go the exact way
+  float far = s == 0.0f || (s > 1e-30f && s < 1e30f) ? 0.f : 1.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = fminf(fmaxf((f[i] - m) * inv, 0.0f), 15.0f);
-    const float n = t + magic;
-    q[i] = __float_as_uint(n) & 15u;
-    ties = ties || fabsf(t - (n - magic)) > 0.4999f;
+    const float t = __saturatef((f[i] - m) * (inv * (1.0f / 15.0f)));  // of 15
+    q[i] = fmaf(t, 15.0f, magic) - magic;
+    far = fmaxf(far, fabsf(fmaf(t, 15.0f, -q[i])));
   }
-  if (ties) {
+  if (far > 0.4999f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      q[i] = __float_as_uint(fminf(fmaxf((f[i] - m) / s, 0.0f), 15.0f) + magic) & 15u;
+    for (int i = 0; i < 8; ++i) {
+      const float r = fminf(fmaxf((f[i] - m) / s, 0.0f), 15.0f) + magic;
+      q[i] = r - magic;
+    }
   }
 }
 
@@ -134,15 +149,15 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArg
   for (int i = 0; i < kRounds; ++i) {
     const int at = first + i * kAtOnce;
     if (__all_sync(0xffffffffu, t0 + at >= a.tokens)) break;
-    uint32_t kq[8], vq[8], kp, vp;
+    float kq[8], vq[8];
+    uint32_t kp, vp;
     quantize8(k[i], R::kGroup / 8, kq, kp);
     quantize8(v[i], R::kGroup / 8, vq, vp);
-    uint32_t kw = 0, vw[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      kw |= kq[e] << (4 * (e / 2) + 16 * (e % 2));
-      vw[e / 4] |= vq[e] << (4 * (e % 4));
-    }
+    // even dims in the low half's nibbles, odd ones in the high half's
+    const uint32_t kw = __byte_perm(nibbles(kq[0], kq[2], kq[4], kq[6]),
+                                    nibbles(kq[1], kq[3], kq[5], kq[7]), 0x5410);
+    const uint32_t vw[2] = {nibbles(vq[0], vq[1], vq[2], vq[3]) & 0xFFFFu,
+                            nibbles(vq[4], vq[5], vq[6], vq[7]) & 0xFFFFu};
     uint8_t* rec = p.rec[at];
     const int row = p.row[at];
     // the token of the other half of a V word, if a lane of this warp has it

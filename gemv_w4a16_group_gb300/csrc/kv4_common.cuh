@@ -42,9 +42,8 @@ struct Kv4Record {
 struct Kv4Seq {
   int n, m, s0;
 };
-__device__ __forceinline__ Kv4Seq kv4_sequence(const Kv4View& c, const int32_t* starts, int tokens,
-                                               int max_new, int max_len, int b) {
-  const int len = c.lens[b], a = starts[b], e = starts[b + 1];
+__device__ __forceinline__ Kv4Seq kv4_clamped(const Kv4View& c, int len, int a, int e, int tokens,
+                                              int max_new, int max_len) {
   Kv4Seq s;
   s.n = min(max(len, 0), min(max_len, c.width << c.page_shift));
   s.s0 = min(max(a, 0), tokens);
@@ -52,6 +51,11 @@ __device__ __forceinline__ Kv4Seq kv4_sequence(const Kv4View& c, const int32_t* 
   s.m = min(end - s.s0, max_new);
   if (s.n != len || s.s0 != a || s.s0 + s.m != e) atomicOr(c.status, kStatusIndex);
   return s;
+}
+
+__device__ __forceinline__ Kv4Seq kv4_sequence(const Kv4View& c, const int32_t* starts, int tokens,
+                                               int max_new, int max_len, int b) {
+  return kv4_clamped(c, c.lens[b], starts[b], starts[b + 1], tokens, max_new, max_len);
 }
 
 // First byte of record `rec` (of the sequence) of head h in page `page`, its table's entry for the
@@ -93,20 +97,6 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// Sequence that owns token t: the number of b in 1..batch with starts[b] <= t. All lanes of a
-// warp call with the same t.
-__device__ __forceinline__ int kv4_sequence_of(const int32_t* starts, int batch, int t) {
-  const int lane = threadIdx.x & 31;
-  int b = 0;
-  for (int base = 1; base <= batch; base += 32) {
-    const bool below = base + lane <= batch && starts[base + lane] <= t;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, below));
-    b += cnt;
-    if (cnt < 32) break;
-  }
-  return b;
 }
 
 }  // namespace w4k
