@@ -2,7 +2,7 @@
 //
 // Both move every value once and compute a handful of operations on it, so memory bounds them:
 // an append reads 4 bytes and writes 1 + 8 / group bytes for a dim's key and value, a read the
-// other way round. A block takes 32 tokens of one head. Where each of them lies (its sequence,
+// other way round. A block takes 64 tokens of one head. Where each of them lies (its sequence,
 // page and row, three loads that wait for one another) is found once, by a thread a token; then
 // D / 8 lanes take a token, with all of a thread's loads on their way before the first is used.
 #include "kv4_common.cuh"
@@ -11,7 +11,7 @@ namespace w4k {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 32;
+constexpr int kTokens = 64;
 constexpr int kStarts = 512;  // sequences whose offsets and lengths are kept in shared memory
 
 struct Places {
@@ -80,12 +80,16 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return y;
 }
 
-// Four codes, whole numbers 0..15 as floats, in the nibbles of 16 bits: exact sums under 2^23.
+// Adding this rounds a float to a whole number, half to even, and leaves it in the low bits.
+constexpr float kMagic = 12582912.0f;
+
+// The nibbles of four such sums in the low 16 bits (the sums' other bits are above them).
 __device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) {
-  return __float_as_uint(fmaf(fmaf(d, 16.f, c), 256.f, fmaf(b, 16.f, a + 8388608.f)));
+  return ((__float_as_uint(d) * 16u + __float_as_uint(c)) * 16u + __float_as_uint(b)) * 16u +
+         __float_as_uint(a);
 }
 
-// Eight values of one group of `lanes` neighbouring lanes x 8 -> codes (as floats) and the group's
+// Eight values of one group of `lanes` neighbouring lanes x 8 -> codes (plus kMagic) and the group's
 // scale | minimum word. The code is rint((x - m) / s) of the fp32 quotient; a product with 1 / s is
 // within 1e-5 of it and has the same code unless it lies that near to a tie.
 __device__ __forceinline__ void quantize8(const uint4& x, int lanes, float (&q)[8],
@@ -105,27 +109,23 @@ __device__ __forceinline__ void quantize8(const uint4& x, int lanes, float (&q)[
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   if (s == 0.0f) inv = 0.0f;  // codes 0
-  const float magic = 12582912.0f;  // adding it rounds to a whole number, half to even
   // tiny and huge scales go the exact way
   float far = s == 0.0f || (s > 1e-30f && s < 1e30f) ? 0.f : 1.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float t = __saturatef((f[i] - m) * (inv * (1.0f / 15.0f)));  // of 15
-    q[i] = fmaf(t, 15.0f, magic) - magic;
-    far = fmaxf(far, fabsf(fmaf(t, 15.0f, -q[i])));
+    q[i] = fmaf(t, 15.0f, kMagic);
+    far = fmaxf(far, fabsf(fmaf(t, 15.0f, kMagic - q[i])));
   }
   if (far > 0.4999f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float r = fminf(fmaxf((f[i] - m) / s, 0.0f), 15.0f) + magic;
-      q[i] = r - magic;
-    }
+    for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf((f[i] - m) / s, 0.0f), 15.0f) + kMagic;
   }
 }
 
 // D / 8 neighbouring lanes take one token, 8 dims each.
 template <int D, int NG>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(const Kv4AppendArgs a) {
   using R = Kv4Record<D, NG>;
   constexpr int kLanes = D / 8, kAtOnce = kThreads / kLanes, kRounds = kTokens / kAtOnce;
   __shared__ Places p;
