@@ -37,10 +37,10 @@
 namespace w4k {
 namespace {
 
-// Computing warps of a CTA (with the copies' warp eight) and resident CTAs an SM, by the n8 tiles
-// of rows a warp holds: one needs 128 registers a thread, two all 255.
+// Computing warps of a CTA (with the copies' warp eight) and resident CTAs an SM, by what the
+// accumulators of nt n8 tiles of rows leave of the registers: 128 a thread or all 255.
 constexpr int kWarps = 7;
-constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
+constexpr int ctas_per_sm(int d, int nt) { return d * nt <= 128 ? 2 : 1; }
 // Copies a warp has on their way or at hand: what two CTAs' shared memory holds.
 constexpr int ring_stages(int d, int ng) { return d == 128 && ng == 4 ? 2 : 3; }
 constexpr int kUnit = 32;  // tokens
@@ -180,11 +180,11 @@ struct Shape {
   static constexpr uint32_t misc_off = bar_off + 2 * kWarps * kStages * 8;
   static constexpr uint32_t total = misc_off + 16;
   static constexpr int part_floats = kRows * D + 2 * kRows;
-  static_assert(total <= (ctas_per_sm(NT) == 2 ? 113u : 227u) * 1024u, "shared memory");
+  static_assert(total <= (ctas_per_sm(D, NT) == 2 ? 113u : 227u) * 1024u, "shared memory");
 };
 
 template <int D, int NG, int NT, bool LOGITS>
-__global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(NT))
+__global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
     kv4_attention_kernel(const Kv4AttentionArgs a, const Workspace ws) {
   using R = Kv4Record<D, NG>;
   using S = Shape<D, NG, NT>;
@@ -766,18 +766,18 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(NT))
       // CTAs i0 .. i1 share the item; the one that arrives last joins their parts in order.
       const uint32_t first_unit = cur.base + kItemCost;
       const uint32_t i0 = shares.of(first_unit), i1 = shares.of(first_unit + cur.w.chunks - 1);
-      __threadfence();
       join_warps();
       if (threadIdx.x == 0) {
+        __threadfence();  // the CTA's writes, which the barrier has ordered before this
         uint32_t* cnt = ws.counters + (static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) *
                                           ((a.max_new * G + kRows - 1) / kRows) + cur.tile;
         const bool last = atomicAdd(cnt, 1u) == i1 - i0;
         if (last) *cnt = 0u;
+        __threadfence();
         *arrived = last ? 1u : 0u;
       }
       join_warps();
       if (*arrived) {
-        __threadfence();
         // D / 4 lanes take a row, 4 dims each; together they read the parts' (max, sum), a lane
         // a part, and then each its dims of the parts, eight at a time.
         constexpr int kLanes = D / 4;
@@ -832,10 +832,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(NT))
 
 // weights_out[b, h, j] = weights[b, h, j] + sum over rows of exp2(logit - lse2), in row order.
 // A thread takes four tokens 256 apart, four rows of each at a time: sixteen loads on their way.
-constexpr int kWeightRows = 32;  // rows a head has at most on this path
+constexpr int kFewRows = 96;  // rows a key/value head has at most on this path
 __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttentionArgs a,
                                                           const Workspace ws) {
-  __shared__ float lse[kWeightRows];
+  __shared__ float lse[kFewRows];
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.z, h = blockIdx.y, G = a.heads / a.c.kv_heads;
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttentionArgs
   const int key0 = blockIdx.x * 1024 + threadIdx.x;
   if (blockIdx.x * 1024 >= s.n) return;
   const int rows = s.m * G;
-  if (threadIdx.x < kWeightRows) {
+  if (threadIdx.x < kFewRows) {
     float v = INFINITY;
     if (threadIdx.x < rows)
       v = ws.lse2[static_cast<int64_t>(s.s0 + threadIdx.x / G) * a.heads + h * G + threadIdx.x % G];
@@ -878,14 +878,15 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttentionArgs
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-// n8 tiles of a row tile
+// n8 tiles of a row tile. More than two are slower than several row tiles of two: head size 64,
+// 36 rows in three tiles 12.9 us (one sequence of 2048), 32 rows in one of four 18.0 us.
 int row_blocks(int max_new, int G) { return max_new * G <= 8 ? 1 : 2; }
 
 struct Layout {
   size_t counters, lse2, logits, parts, total;
   int row_len;
 };
-int grid_limit(int nt) { return ctas_per_sm(nt) * device_sm_count(); }
+int grid_limit(int d, int nt) { return ctas_per_sm(d, nt) * device_sm_count(); }
 
 Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv_heads, int D,
               bool weights) {
@@ -896,7 +897,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   l.counters = at;
   at += round256(static_cast<size_t>(batch) * kv_heads * ((static_cast<size_t>(max_new) * G + 7) / 8) * 4);
   l.parts = at;
-  at += round256(static_cast<size_t>(2) * grid_limit(nt) * nt * 8 * (D + 2) * 4);
+  at += round256(static_cast<size_t>(2) * grid_limit(D, nt) * nt * 8 * (D + 2) * 4);
   l.lse2 = at;
   if (weights) at += round256(static_cast<size_t>(tokens) * heads * 4);
   l.logits = at;
@@ -927,7 +928,7 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
                         (kItemCost + (a.max_len + kUnit - 1) / kUnit);
   if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int64_t want = (units + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(want < grid_limit(NT) ? want : grid_limit(NT));
+  const unsigned grid = static_cast<unsigned>(want < grid_limit(D, NT) ? want : grid_limit(D, NT));
   e = launch_with_pdl(kern, dim3(grid), dim3((kWarps + 1) * 32), S::total, stream, a, ws);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
   return launch_with_pdl(kv4_weights_kernel,
@@ -937,14 +938,16 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
 
 template <int D, int NG>
 cudaError_t by_rows(const Kv4AttentionArgs& a, cudaStream_t stream) {
-  return row_blocks(a.max_new, a.heads / a.c.kv_heads) == 1 ? run<D, NG, 1>(a, stream) : run<D, NG, 2>(a, stream);
+  return row_blocks(a.max_new, a.heads / a.c.kv_heads) == 1 ? run<D, NG, 1>(a, stream)
+                                                            : run<D, NG, 2>(a, stream);
 }
 
-// Rows of a key/value head from which the prompts' path takes over.
-constexpr int64_t kPromptRows = kWeightRows + 1;
-
+// Above kFewRows the prompts' path takes over. It widens the whole cache to FP16 tiles first and
+// pads the rows to 128; here every 16 rows read the cache's codes again. 32 query heads on 8, us
+// at 32 / 36 rows (8 / 9 new tokens) with this path up to 32: 47 / 105 for 16 sequences of 2048,
+// 102 / 309 for 16 of 8192, 30 / 79 for one of 16384; a 16-row tile more costs 20, 50 and 13.
 bool is_prompt(int max_new, int heads, int kv_heads) {
-  return static_cast<int64_t>(max_new) * (heads / kv_heads) >= kPromptRows;
+  return static_cast<int64_t>(max_new) * (heads / kv_heads) > kFewRows;
 }
 
 }  // namespace

@@ -59,7 +59,7 @@ constexpr int kOrdered = 512;
 struct PromptWs {
   Plan* plan;         // [2]: of the row tiles, of the weights' key tiles
   Start* starts;      // [2][grid]
-  int2* order;        // [kOrdered]: (sequence, row tile), longest first
+  Start* order;       // [kOrdered]: row tiles, longest first (b, tile, units and s)
   uint32_t* base;     // [batch + 1]: units before a sequence
   int32_t* pre;       // [batch, row_tiles + 1]: units of a head before a row tile
   KeyMeta* meta;      // [batch, kv_heads, key_tiles]
@@ -442,7 +442,12 @@ __device__ void deal(const Kv4AttentionArgs& a, const PromptWs& ws) {
     if (units[i] == 0) continue;
     int rank = 0;
     for (int j = 0; j < n; ++j) rank += units[j] > units[i] || (units[j] == units[i] && j < i);
-    ws.order[rank] = make_int2(i / ws.row_tiles, i % ws.row_tiles);
+    Start x = {};
+    x.b = i / ws.row_tiles;
+    x.tile = i % ws.row_tiles;
+    x.units = units[i];
+    x.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, x.b);
+    ws.order[rank] = x;
   }
   if (threadIdx.x == 0) ws.plan->dealt = count * a.c.kv_heads;
 }
@@ -582,6 +587,11 @@ struct Smem {
 };
 
 // A segment: the part of one (sequence, head, row tile) in this CTA's range of units.
+// Halves of a row tile that have rows.
+__device__ __forceinline__ int halves_of(const Kv4Seq& s, int G, int rt) {
+  return s.m * G - rt * kTileRows > 128 ? 2 : 1;
+}
+
 struct Segment {
   int b, h, rt;
   int units;   // of the item
@@ -606,12 +616,12 @@ __device__ __forceinline__ bool advance(Segment& g, const Kv4AttentionArgs& a, c
     const uint32_t i = g.turn * ctas + (g.turn % 2 == 0 ? blockIdx.x : ctas - 1 - blockIdx.x);
     if (i >= g.dealt) return false;
     ++g.turn;
-    const int2 x = ws.order[i / a.c.kv_heads];
-    g.b = x.x;
-    g.rt = x.y;
+    const Start x = ws.order[i / a.c.kv_heads];
+    g.b = x.b;
+    g.rt = x.tile;
     g.h = i % a.c.kv_heads;
-    g.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, g.b);
-    g.units = units_of(g.s, G, g.rt);
+    g.s = x.s;
+    g.units = x.units;
     g.tiles = g.hi = g.units - kItemCost;
     g.lo = 0;
     return true;
@@ -635,11 +645,10 @@ __device__ __forceinline__ bool advance(Segment& g, const Kv4AttentionArgs& a, c
 }
 // This CTA's first segment; false if it has none.
 __device__ __forceinline__ bool begin(Segment& g, const Kv4AttentionArgs& a, const PromptWs& ws,
-                                      const Plan& plan, int G) {
+                                      const Plan& plan, const Start& x, int G) {
   g.dealt = plan.dealt;
   g.turn = 0;
   if (g.dealt != 0) return advance(g, a, ws, plan.ctas, G);
-  const Start x = ws.starts[blockIdx.x];
   g.b = x.b;
   g.h = x.h;
   g.rt = x.tile;
@@ -701,8 +710,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   const Plan plan = ws.plan[0];
   const uint32_t me = blockIdx.x;
+  const Start start = ws.starts[me];  // not written past plan.ctas, and not used there
   Segment g;
-  const bool some = me < plan.ctas && begin(g, a, ws, plan, G);
+  const bool some = me < plan.ctas && begin(g, a, ws, plan, start, G);
   uint32_t* status = a.c.status;
   const uint64_t limit = a.wait_limit_ns;
   auto item = [&](const Segment& x) {
@@ -751,7 +761,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t ring = desc_low(smem_addr(smem + L::ring_off), 16);
     const uint32_t ring_more =
         desc_low(smem_addr(smem + L::ring_off) + Img<D>::kKCodes, kTileKeys * 16);
-    int n = 0, segs = 0, steps = 0;
+    int n = 0, segs = 0, steps = 0, steps_1 = 0;  // tiles of all halves, of second halves
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && mbar_wait_bounded(bar, parity, abort_flag, status, limit);
@@ -782,11 +792,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       ++segs;
       if (!wait(&full[n % kRing], (n / kRing) & 1u)) break;
       tc_fence_after_sync();
+      const int halves = halves_of(g.s, G, g.rt);
       if (elect_one()) {
         s_mma(0, n % kRing);
         tc_commit(&s_full[0]);
-        s_mma(1, n % kRing);
-        tc_commit(&s_full[1]);
+        if (halves == 2) {
+          s_mma(1, n % kRing);
+          tc_commit(&s_full[1]);
+        }
         tc_commit(&empty[n % kRing]);
         if (g.hi - g.lo == 1) tc_commit(q_empty);
       }
@@ -799,14 +812,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (more && !wait(&full[k_slot], ((n + 1) / kRing) & 1u)) break;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!wait(&p_full[half], steps & 1u)) break;
+          if (half >= halves) break;
+          const bool last = half + 1 == halves;
+          if (!wait(&p_full[half], (half == 0 ? steps : steps_1) & 1u)) break;
           tc_fence_after_sync();
           if (elect_one()) {
             o_mma(half, v_slot, i == g.lo);
-            if (half == 1) tc_commit(&empty[v_slot]);
+            if (last) tc_commit(&empty[v_slot]);
             if (more) s_mma(half, k_slot);
             tc_commit(more ? &s_full[half] : &o_full[half]);
-            if (more && half == 1) {
+            if (more && last) {
               tc_commit(&empty[k_slot]);
               if (i + 2 == g.hi) tc_commit(q_empty);
             }
@@ -815,6 +830,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         n += more ? 2 : 1;
         ++steps;
+        if (halves == 2) ++steps_1;
       }
     } while (ok && advance(g, a, ws, plan.ctas, G));
     if (elect_one()) tc_commit(drain);
@@ -842,6 +858,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     };
     do {
       const Kv4Seq seq = g.s;
+      if (half >= halves_of(seq, G, g.rt)) continue;
       const int rows = seq.m * G, R = g.rt * kTileRows + half * 128 + row;
       const int last_key = R < rows ? seq.n - seq.m + R / G : -1;
       // first key that some row of this half does not see
@@ -982,28 +999,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const Shares shares(plan.total, plan.ctas);
         const uint32_t i0 = shares.of(g.item_base + kItemCost);
         const uint32_t i1 = shares.of(g.item_base + g.units - 1);
-        __threadfence();
         if (!wg_sync()) break;
         if (row == 0) {
+          __threadfence();  // the half's writes, which the barrier has ordered before this
           uint32_t* cnt = ws.counters + item(g) * 2 + half;
-          const bool last = atomicAdd(cnt, 1u) == static_cast<uint32_t>(i1 - i0);
+          const bool last = atomicAdd(cnt, 1u) == i1 - i0;
           if (last) *cnt = 0u;
+          __threadfence();
           arrived[half] = last ? 1u : 0u;
         }
         if (!wg_sync()) break;
         if (arrived[half]) {
-          __threadfence();
+          // the parts in the CTAs' order; this one's is still in tensor memory
           auto part_of = [&](uint32_t i) {
             return ws.parts + ((2 * i + (i == i0 ? 1 : 0)) * 2 + half) * kPart;
           };
           auto ml_of = [&](uint32_t i) {
-            return __ldcg(reinterpret_cast<const float2*>(part_of(i) + D * 128) + row);
+            return i == me ? make_float2(m, l)
+                           : __ldcg(reinterpret_cast<const float2*>(part_of(i) + D * 128) + row);
           };
           float mm = -INFINITY, ll = 0.f;
-          for (uint32_t i = i0; i <= i1; ++i) mm = fmaxf(mm, ml_of(i).x);
-          for (uint32_t i = i0; i <= i1; ++i) {
-            const float2 x = ml_of(i);
-            if (x.x != -INFINITY) ll = fmaf(x.y, exp2f(x.x - mm), ll);
+          for (uint32_t i = i0; i <= i1; i += 4) {
+            float2 x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[j] = i + j <= i1 ? ml_of(i + j) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (x[j].x == -INFINITY) continue;
+              const float top = fmaxf(mm, x[j].x);
+              ll = fmaf(ll, ex2(mm - top), x[j].y * ex2(x[j].x - top));
+              mm = top;
+            }
           }
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll 1
@@ -1012,9 +1039,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
             for (int j = 0; j < 64; ++j) v[j] = 0.f;
             for (uint32_t i = i0; i <= i1; ++i) {
+              const float x = ml_of(i).x, w = x == -INFINITY ? 0.f : ex2(x - mm);
+              if (i == me) {
+                const float wv = w * vf;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  uint32_t o[16];
+                  tmem_ld_16cols(t_o + 64 * c + 16 * z, o);
+                  tmem_ld_wait();
+                  if (w != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                      v[16 * z + j] = fmaf(__uint_as_float(o[j]), wv, v[16 * z + j]);
+                  }
+                }
+                continue;
+              }
               const float4* src = reinterpret_cast<const float4*>(part_of(i)) + row;
-              const float x = ml_of(i).x;
-              const float w = x == -INFINITY ? 0.f : exp2f(x - mm);
               float4 t[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) t[j] = __ldcg(src + (16 * c + j) * 128);
@@ -1054,7 +1095,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 // warps: a thread a token (TMEM lane) and half of a row tile's 256 columns; S^T is
 // double-buffered in tensor memory. A token tile that a boundary cuts is joined from its parts
 // (128 sums) by whoever arrives last, in order.
-constexpr int kWeightThreads = 320;
+constexpr int kSumWarps = 8;
+constexpr int kSumThreads = kSumWarps * 32;
+constexpr int kWeightThreads = kSumThreads + 64;
 
 template <int D>
 struct WeightSmem {
@@ -1068,6 +1111,10 @@ struct WeightSmem {
   static constexpr uint32_t total = misc_off + 16;
   static constexpr uint32_t alloc = total + 1024;
 };
+
+__device__ __forceinline__ void sum_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSumThreads) : "memory");
+}
 
 struct KeySegment {
   int b, h, kt;
@@ -1125,13 +1172,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 8);
+      mbar_init(&s_empty[i], kSumWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0u;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kSumWarps + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -1160,7 +1207,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   const uint64_t limit = a.wait_limit_ns;
   auto head = [&]() { return static_cast<size_t>(g.b) * a.c.kv_heads + g.h; };
   if (!some) {
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kSumWarps) {
     if (lane == 0) {
       bool ok = true;
       int n = 0, segs = 0;
@@ -1191,7 +1238,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           mbar_wait_bounded(&q_full[i & 1], (i / 2) & 1u, &no_abort, status, limit);
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kSumWarps + 1) {
     constexpr uint32_t idesc = idesc_f16_f32(128, kTileRows);
     bool ok = true;
     int n = 0, segs = 0;
@@ -1257,7 +1304,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           lse_next = lse_of(rt + 1);
           qf_next = ws.qf[head() * ws.row_tiles + rt + 1];
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        sum_sync();
         ok = ok && mbar_wait_bounded(&s_full[s], (n / 2) & 1u, abort_flag, status, limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
@@ -1297,9 +1344,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         acc += (p[0] + p[1]) + (p[2] + p[3]);
       }
       // ---- the two column halves, then the other CTAs' parts
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (part == 1) sum_s[threadIdx.x & 127] = acc;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      sum_sync();
+      if (part == 1) sum_s[threadIdx.x - 128] = acc;
+      sum_sync();
       const size_t at = head() * a.weights_stride + key;
       const bool have = part == 0 && key < g.s.n;
       auto store = [&](float x) {
@@ -1313,17 +1360,17 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         if (part == 0) __stcg(ws.sums + (2 * me + (g.lo == 0 ? 1 : 0)) * 128 + threadIdx.x, acc);
         const Shares shares(plan.total, plan.ctas);
         const uint32_t i0 = shares.of(g.item_base), i1 = shares.of(g.item_base + g.units - 1);
-        __threadfence();
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        sum_sync();
         if (threadIdx.x == 0) {
+          __threadfence();
           uint32_t* cnt = ws.kcounters + head() * ws.key_tiles + g.kt;
           const bool last = atomicAdd(cnt, 1u) == static_cast<uint32_t>(i1 - i0);
           if (last) *cnt = 0u;
+          __threadfence();
           *arrived = last ? 1u : 0u;
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        sum_sync();
         if (*arrived && part == 0) {
-          __threadfence();
           float x = 0.f;
           for (uint32_t i = i0; i <= i1; ++i)
             x += __ldcg(ws.sums + (2 * i + (i == i0 ? 1 : 0)) * 128 + threadIdx.x);
@@ -1335,7 +1382,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kSumWarps + 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
@@ -1366,7 +1413,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   if (weights) l.kcounters = take(bh * l.key_tiles * 4);
   l.plan = take(2 * sizeof(Plan));
   l.starts = take(2 * static_cast<size_t>(device_sm_count()) * sizeof(Start));
-  l.order = take(kOrdered * sizeof(int2));
+  l.order = take(kOrdered * sizeof(Start));
   l.base = take((static_cast<size_t>(batch) + 1) * 4);
   l.pre = take(static_cast<size_t>(batch) * (l.row_tiles + 1) * 4);
   l.meta = take(bh * l.key_tiles * sizeof(KeyMeta));
@@ -1393,7 +1440,7 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   PromptWs ws;
   ws.plan = reinterpret_cast<Plan*>(w + l.plan);
   ws.starts = reinterpret_cast<Start*>(w + l.starts);
-  ws.order = reinterpret_cast<int2*>(w + l.order);
+  ws.order = reinterpret_cast<Start*>(w + l.order);
   ws.base = reinterpret_cast<uint32_t*>(w + l.base);
   ws.pre = reinterpret_cast<int32_t*>(w + l.pre);
   ws.meta = reinterpret_cast<KeyMeta*>(w + l.meta);
