@@ -7,14 +7,14 @@
 //   q . k_hat_j = sum_g s_jg (sum_{d in g} q_d c_jd) + m_jg (sum_{d in g} q_d)
 //   sum_j p_j v_hat_jd = sum_j (p_j s_jg) c_jd + sum_j p_j m_jg
 // so the codes go to the tensor pipe as they are, and the scales touch one number a token and
-// group. A code masked out of its word is an FP16 subnormal, c 2^-24 (or c 2^-20 for the nibble
-// above), which the MMA multiplies exactly: five operations for eight codes. (128 + c or 1024 + c
-// needs the offset's sum taken out again; the MMA truncates its sums, and over 131072 tokens the
-// offset, hundreds of times the result, cost 1.2 % of it. Centring the pairs cures that for four
-// more operations.) q is FP16 under a power of two a row, exact down to 2^-27 of the row's
-// largest; p s is rounded to FP16 under the largest scale's power of two that the row has met
-// (relative 2^-12; BF16's 2^-9 was twice the output's own rounding error). Sums, maxima and the
-// softmax's statistics are fp32.
+// group. A code masked out of its word is an FP16 subnormal, a power of two times the code, which
+// the MMA multiplies exactly: five or six operations for eight codes. (128 + c or 1024 + c needs
+// the offset's sum taken out again; the MMA truncates its sums, and over 131072 tokens the offset,
+// hundreds of times the result, cost 1.2 % of it. Centring the pairs cures that for four more
+// operations.) q is FP16 under a power of two a row, exact down to 2^-27 of the row's largest; p s
+// is rounded to FP16 under the largest scale's power of two that the row has met (relative 2^-12;
+// BF16's 2^-9 was twice the output's own rounding error). Sums, maxima and the softmax's
+// statistics are fp32.
 //
 // What bounds it: the cache is read once (D + 8 D / group bytes a token and head), at 4 heads a
 // key/value head about 8 operations a byte, so the aim is the memory's rate.
@@ -59,12 +59,23 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   return d;
 }
 
-// FP16 pairs of nibbles i and i + 4: q 2^-24 for even i, q 2^-20 for odd i.
-__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&p)[4]) {
+// FP16 pairs of nibbles i and i + 4. The MMA lines its products up by their operands' exponent
+// fields, so the zeros above a subnormal's bits are bits lost of the sum: the higher a code lies in
+// the mantissa the better.
+// Keys: q 2^-22 for even i, q 2^-18 for odd i (with q 2^-24 and q 2^-20, one shift less, the
+// log-sums were off by 1e-6 of themselves, now by 1e-7).
+__device__ __forceinline__ void key_pairs(uint32_t w, uint32_t (&p)[4]) {
+  p[0] = (w << 2) & 0x003C003Cu;
+  p[1] = (w << 2) & 0x03C003C0u;
+  p[2] = (w >> 6) & 0x003C003Cu;
+  p[3] = (w >> 6) & 0x03C003C0u;
+}
+// Values, where the output's rounding hides it: q 2^-24, 2^-20, 2^-22, 2^-18.
+__device__ __forceinline__ void value_pairs(uint32_t w, uint32_t (&p)[4]) {
   p[0] = w & 0x000F000Fu;
   p[1] = w & 0x00F000F0u;
-  p[2] = (w >> 8) & 0x000F000Fu;
-  p[3] = (w >> 8) & 0x00F000F0u;
+  p[2] = (w >> 6) & 0x003C003Cu;
+  p[3] = (w >> 6) & 0x03C003C0u;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -381,7 +392,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
         v[x] = h;
       }
       // sums of q over a group's dims, as codes 1 would give them: column n of the product
-      constexpr uint32_t one = 0x00010001u, one16 = 0x00100010u;
+      constexpr uint32_t one = 0x00040004u, one16 = 0x00400040u;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float acc[4];
@@ -398,9 +409,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
           sm_row[g * kRows + warp * 8 + 2 * c + 1] = acc[1];
         }
       }
-      // products are codes' 2^24 too small, as the sums are
+      // products are codes' 2^22 too small, as the sums are
       if (c == 0)
-        sm_row[NG * kRows + warp * 8 + r] = fmaxf(scale2 * 16777216.f * pow2f(-up), 1e-37f);
+        sm_row[NG * kRows + warp * 8 + r] = fmaxf(scale2 * 4194304.f * pow2f(-up), 1e-37f);
     }
     join_warps();
     float sq[NT][NG][2], unscale[NT][2];  // of rows 2c, 2c + 1
@@ -460,8 +471,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
 #pragma unroll
           for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
             uint32_t k0[4], k1[4];
-            code_pairs(w0[x], k0);
-            code_pairs(w1[x], k1);
+            key_pairs(w0[x], k0);
+            key_pairs(w1[x], k1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint4 q = lds128(q_s + (nt * NB + x) * 512);
@@ -637,8 +648,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
 #pragma unroll
           for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
             uint32_t v0[4], v1[4];
-            code_pairs(w0[x], v0);
-            code_pairs(w1[x], v1);
+            value_pairs(w0[x], v0);
+            value_pairs(w1[x], v1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_f16_16816(o[nt][x][0], v0[0], v0[1], v1[0], v1[1], b0[nt], b1[nt]);
@@ -699,13 +710,15 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_ml[w * kRows + row].x);
             const float w = mx[nt][i] == -INFINITY ? 0.f : ex2(mx[nt][i] - m);
-            // sums of codes' 2^-24 (2^-20 for odd dims) under 2^-ev
-            const float f = pow2f(min(ev[nt][i], 250) - 127) * 16777216.f, f16 = f * 0.0625f;
+            // sums of codes' 2^-24, 2^-20, 2^-22, 2^-18 by dims, under 2^-ev
+            const float f = pow2f(min(ev[nt][i], 250) - 127) * 16777216.f;
 #pragma unroll
             for (int x = 0; x < NB; ++x) {
               const float k = corr[nt][x / (NB / NG)][i];
-              float4 v = make_float4(fmaf(o[nt][x][0][i], f, k), fmaf(o[nt][x][0][i + 2], f16, k),
-                                     fmaf(o[nt][x][1][i], f, k), fmaf(o[nt][x][1][i + 2], f16, k));
+              float4 v = make_float4(fmaf(o[nt][x][0][i], f, k),
+                                     fmaf(o[nt][x][0][i + 2], f * 0.0625f, k),
+                                     fmaf(o[nt][x][1][i], f * 0.25f, k),
+                                     fmaf(o[nt][x][1][i + 2], f * 0.015625f, k));
               v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                            : make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
               float4* at = reinterpret_cast<float4*>(

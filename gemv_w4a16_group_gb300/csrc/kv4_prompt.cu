@@ -66,13 +66,13 @@ struct PromptWs {
   float* qf;          // [batch, kv_heads, row_tiles]: logit (base 2) per image product, without kf
   uint8_t* q_img;     // [batch, kv_heads, row_tiles] x 256 (D + 16) FP16
   uint8_t* kv_img;    // [batch, kv_heads, key_tiles] x (K 128 (D + 16), V^T D 128) FP16
-  uint32_t* counters; // [batch, kv_heads, row_tiles, 2], zero between calls
+  uint32_t* counters; // [batch, kv_heads, row_tiles, 2], zeroed beside the images
   float* parts;       // [2 grid][2 halves] x (D + 2) 128
   float* lse2;        // [tokens, heads], base 2
   // with weights, the same for the units of the token tiles (row tiles that see them)
   uint32_t* kbase;    // [batch + 1]
   int32_t* kpre;      // [batch, key_tiles + 1]
-  uint32_t* kcounters;  // [batch, kv_heads, key_tiles], zero between calls
+  uint32_t* kcounters;  // [batch, kv_heads, key_tiles], zeroed beside the images
   float* sums;        // [2 grid] x 128
   int key_tiles, row_tiles, grid;
 };
@@ -145,6 +145,8 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   const int tid = threadIdx.x;
   const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
   const int key0 = tile * kTileKeys;
+  const size_t at = (static_cast<size_t>(b) * a.c.kv_heads + h) * ws.key_tiles + tile;
+  if (tid == 0 && ws.kbase != nullptr) ws.kcounters[at] = 0u;
   if (seq.m == 0 || key0 >= seq.n) return;
   if (tid == 0) {
     mbar_init(&bar, 1);
@@ -189,7 +191,6 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   // keys reach [2^7, 2^8): 128 times a minimum + 8 s still is an FP16 number
   const int kup = max(up_of(ktop) - 7, -126), vup = up_of(vtop);
   const float kf = pow2f(kup), vf = pow2f(vup);
-  const size_t at = (static_cast<size_t>(b) * a.c.kv_heads + h) * ws.key_tiles + tile;
   if (tid == 0) ws.meta[at] = KeyMeta{pow2f(-kup), -vup};
   uint8_t* kimg = ws.kv_img + at * Img<D>::kPair;
   uint8_t* vimg = kimg + Img<D>::kTile;
@@ -270,6 +271,8 @@ __device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   __shared__ uint32_t red[kImgThreads / 32];
   const Kv4Seq seq = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
   const int G = a.heads / a.c.kv_heads, rows = seq.m * G, row0 = rt * kTileRows;
+  const size_t at = (static_cast<size_t>(b) * a.c.kv_heads + h) * ws.row_tiles + rt;
+  if (threadIdx.x < 2) ws.counters[2 * at + threadIdx.x] = 0u;
   if (row0 >= rows) return;
   constexpr int kChunks = D / 8, kPer = kTileRows * kChunks / kImgThreads;
   uint4 v[kPer];
@@ -292,7 +295,6 @@ __device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   top = block_max(top, red);
   const int up = up_of(top << 16);
   const float f = a.scale < 0.f ? -pow2f(up) : a.scale > 0.f ? pow2f(up) : 0.f;
-  const size_t at = (static_cast<size_t>(b) * a.c.kv_heads + h) * ws.row_tiles + rt;
   if (threadIdx.x == 0) ws.qf[at] = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e * pow2f(-up);
   uint8_t* img = ws.q_img + at * Img<D>::kQ;
 #pragma unroll

@@ -465,13 +465,17 @@ w4a16_status kv4_read(const kv4_cache* cache, const int32_t* starts, uint16_t* k
  *   max_new, max_len  upper bounds, known on the host, of a sequence's new tokens and length; they
  *           size the launch, while the work is that of the real lengths.
  * A row that sees no token (an empty sequence) gives out = 0 and lse = -inf. Tokens that a row
- * does not see do not touch it, whatever they hold. Sums, the softmax's maxima and sums, lse and
- * weights are fp32; codes and probabilities meet as BF16 products with fp32 sums. Results do not
- * depend on timing (no floating-point atomics).
+ * does not see do not touch it, whatever they hold. Products are FP16 with fp32 sums: codes are
+ * exact in them, probabilities (and, from 97 rows a key/value head on, values) rounded to 2^-12 of
+ * themselves; maxima, sums, lse and weights are fp32. out is within about a rounding to BF16 of the
+ * exact result, lse and weights within 1e-6. Results do not depend on timing (no floating-point
+ * atomics). Values must be finite where a row sees them.
+ * Up to 96 rows (max_new * heads / kv_heads) the cache is read in place; above that it is widened
+ * into the workspace first (4 bytes a key/value pair of dims, 16-bit tiles for tcgen05.mma).
  * Workspace: kv4_attention_workspace_bytes() bytes, 16-byte aligned, zero-filled before its first
  * use (the kernels leave its counters zero) and not shared by calls that may run concurrently;
- * W4A16_ERR_WORKSPACE if NULL or smaller. Calls of other shapes may use the same buffer only
- * after it has been zero-filled again.
+ * W4A16_ERR_WORKSPACE if NULL or smaller. Calls that differ in tokens, max_len and the lengths
+ * themselves may share one; others need one of their own, or it zero-filled again.
  */
 size_t kv4_attention_workspace_bytes(int batch, int tokens, int max_new, int max_len, int heads,
                                      int kv_heads, int head_dim, int group, int with_weights);

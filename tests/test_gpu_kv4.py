@@ -172,6 +172,36 @@ def test_long_sequence_is_split(D, group):
     _check_attention(cache, lens, [1, 1, 2], 4, 1, 6)
 
 
+@pytest.mark.parametrize("heads,H,lens,new", [
+    # whole items dealt out over the GPU, and items cut between several CTAs
+    (32, 8, [600] * 7 + [1], [600] * 7 + [1]), (8, 2, [3000, 200], [100, 200])])
+def test_prompts_over_the_whole_gpu(heads, H, lens, new):
+    cache, _, _ = _fill(lens, H, 64, 64, 128, 16)
+    _check_attention(cache, lens, new, heads, H, 16)
+
+
+def test_one_workspace_for_changing_lengths():
+    """A workspace serves calls that differ in tokens and lengths; each equals a fresh one's."""
+    lens, B, H, heads, D = [300, 70, 129], 3, 2, 4, 128
+    cache, _, _ = _fill(lens, H, D, 64, 64, 17)
+    data, table = _gpu(cache.data), _gpu(cache.table)
+    for max_new in (1, 60):
+        ws = torch.zeros(w4.kv4_attention_workspace_bytes(B, B * max_new, max_new, 300, heads, H, D,
+                                                          64, True), dtype=torch.uint8, device=DEV)
+        for cut in (0, 30, 5):
+            now = [n - cut for n in lens]
+            new = [max(1, max_new - cut)] * B
+            lens_t, starts = _gpu(np.array(now, np.int32)), _gpu(_starts(new))
+            q = torch.randn(sum(new), heads, D, device=DEV).bfloat16()
+            res = []
+            for workspace in (ws, None):
+                w = torch.zeros(B, H, 320, device=DEV)
+                res.append((w4.kv4_attention(q, data, table, lens_t, starts, max(now), max_new,
+                                             weights_out=w, workspace=workspace), w))
+            assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+    _ok()
+
+
 @pytest.mark.parametrize("new", [[1], [3], [90]])
 def test_bounds_larger_than_the_lengths(new):
     lens = [100]
@@ -193,7 +223,7 @@ def test_scale_zero_averages(new):
     _check_attention(cache, lens, new, 4, 2, 8, scale=0.0)
 
 
-@pytest.mark.parametrize("new", [4, 40])
+@pytest.mark.parametrize("new", [4, 40, 60])
 def test_hidden_tokens_do_not_matter(new):
     """Tokens behind a row's position hold infinities and NaN: rows before them are untouched."""
     D, group, n, H = 128, 64, 80, 2
@@ -213,7 +243,7 @@ def test_hidden_tokens_do_not_matter(new):
     _ok()
 
 
-@pytest.mark.parametrize("new", [1, 33])
+@pytest.mark.parametrize("new", [1, 33, 70])
 def test_repeats_are_equal_and_streams_are_kept(new):
     lens = [1000, 333]
     cache, _, _ = _fill(lens, 2, 128, 64, 64, 10)
@@ -280,12 +310,12 @@ def test_offsets_past_32_bits():
                       device=DEV)
     big[shift:] = _gpu(cache.data)
     table = np.where(cache.table >= 0, cache.table + shift, -1).astype(np.int32)
-    q = torch.randn(41, 4, D, device=DEV).bfloat16()
     lens_t, starts = _gpu(np.array(lens, np.int32)), _gpu(_starts([1, 40]))
-    for lo, hi, st in ((0, 41, starts), (0, 2, _gpu(_starts([1, 1])))):
-        a = w4.kv4_attention(q[lo:hi], _gpu(cache.data), _gpu(cache.table), lens_t, st, 100, 40
-                             if hi > 2 else 1)
-        b = w4.kv4_attention(q[lo:hi], big, _gpu(table), lens_t, st, 100, 40 if hi > 2 else 1)
+    for new in ([1, 40], [1, 1], [1, 65]):
+        st, n = _gpu(_starts(new)), sum(new)
+        q = torch.randn(n, 4, D, device=DEV).bfloat16()
+        a = w4.kv4_attention(q, _gpu(cache.data), _gpu(cache.table), lens_t, st, 100, max(new))
+        b = w4.kv4_attention(q, big, _gpu(table), lens_t, st, 100, max(new))
         assert torch.equal(a, b)
     k = torch.randn(41, H, D, device=DEV).bfloat16()
     small = _gpu(cache.data)
@@ -298,7 +328,7 @@ def test_offsets_past_32_bits():
     _ok()
 
 
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 10, 40])
 def test_out_of_range_numbers_are_reported_not_followed(new):
     D, group, page, n = 128, 64, 16, 100
     cache, _, _ = _fill([n], 1, D, group, page, 13, stale=0)
