@@ -444,3 +444,20 @@ def test_a_decoding_loop_with_eviction():
             weights, table = wide, _gpu(spare[step // 2 - 1])
             lens = new_lens.tolist()
     _ok()
+
+
+def test_the_example_runs_the_operators_together():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "kv4_decode.py")
+    spec = importlib.util.spec_from_file_location("kv4_decode", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    got = mod.main(steps=3, budget=100, lengths=(300, 90))
+    assert got["kept a head"] == [100, 90] and got["lengths now"] == [104, 94]
+    assert got["status"] == 0
+    # k and v read back in BF16 (2^-9 of themselves) against the exact codes: logits move by up to
+    # 2^-9 sum |q k| scale, here 0.02; values by 2^-9; out is rounded to 2^-9
+    assert got["largest relative error of a head"] < 0.05
