@@ -10,7 +10,7 @@
 //    tiles in the swizzled order that tcgen05.mma reads: every later load is one contiguous bulk
 //    copy, and a code is widened once instead of once a row tile (a 4096-token prompt has 64 of
 //    them a head). Values come transposed, so that both products read K-major operands, rounded
-//    to FP16 under a power of two a tile (2^-12 of a value, an eighth of the output's rounding).
+//    to FP16 under a power of two a tile (2^-11 of a value, a quarter of the output's rounding).
 //    A key is exact: with c the code less 8, c s has at most 3 + 8 significant bits and is an
 //    FP16 number; what is left, (min + 8 s) times the sum of q over the group, goes through 16
 //    more columns, four a group, as FP16 pairs of high and low parts. Rounded keys (2^-12) put
@@ -125,6 +125,25 @@ __device__ __forceinline__ uint32_t reach_bits(uint32_t param) {
   return max(a >= 0x7F800000u ? 0u : a, b >= 0x7F800000u ? 0u : b);
 }
 
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// FP16 pairs (q - 8, q' - 8) of nibbles i and i + 4, exact.
+__device__ __forceinline__ void centred_pairs(uint32_t w, uint32_t (&p)[4]) {
+  code_pairs_f16(w, p);  // 1024 + q (even i) and 1024 + 16 q (odd i)
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    p[i] = i % 2 == 0 ? fma_f16x2(p[i], 0x3C003C00u, 0xE408E408u)   // x - 1032
+                      : fma_f16x2(p[i], 0x2C002C00u, 0xD480D480u);  // x / 16 - 72
+}
+
 // Three of the four more columns of a group: high and low FP16 parts of x.
 __device__ __forceinline__ uint32_t high_low(float x) {
   const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
@@ -202,12 +221,11 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
     const uint32_t word = reinterpret_cast<const uint32_t*>(rec)[(t % 16) * kWords + w];
     const uint32_t p =
         reinterpret_cast<const uint32_t*>(rec + R::kKParams)[16 * (d / R::kGroup) + t % 16];
-    const float sc = bf16_lo(p) * kf;
+    const uint32_t sc = f16x2_bits(bf16_lo(p) * kf, bf16_lo(p) * kf);
     uint32_t out[4];
+    centred_pairs(word, out);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      out[i] = f16x2_bits((static_cast<float>((word >> (4 * i)) & 15u) - 8.f) * sc,
-                          (static_cast<float>((word >> (16 + 4 * i)) & 15u) - 8.f) * sc);
+    for (int i = 0; i < 4; ++i) out[i] = mul_f16x2(out[i], sc);
     *reinterpret_cast<uint4*>(kimg + (d / 64) * (kTileKeys * 128) + t * 128 +
                               (((d % 64) / 8) ^ (t & 7)) * 16) =
         make_uint4(out[0], out[1], out[2], out[3]);
@@ -227,40 +245,34 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
       *reinterpret_cast<uint4*>(kimg + Img<D>::kKCodes + i * (kTileKeys * 16) + tid * 16) =
           make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   }
-  // a record's 16 tokens of dims 32 blk + 4 r + 0..3
-  for (int x = tid; x < 8 * 8 * R::kBlocks; x += kImgThreads) {
-    const int j = x / (8 * R::kBlocks), w = x % (8 * R::kBlocks);
+  // eight of a record's tokens, dims 32 blk + 4 r + 0..3
+  for (int x = tid; x < 8 * 8 * R::kBlocks * 2; x += kImgThreads) {
+    const int w = x % (8 * R::kBlocks), half = x / (8 * R::kBlocks) % 2, j = x / (16 * R::kBlocks);
     const int d0 = 32 * (w % R::kBlocks) + 4 * (w / R::kBlocks), g = d0 / R::kGroup;
-    const uint32_t* v_codes = reinterpret_cast<const uint32_t*>(raw + j * R::kBytes + R::kV);
-    const uint32_t* vp = reinterpret_cast<const uint32_t*>(raw + j * R::kBytes + R::kVParams);
-    uint32_t word[8];
+    const uint8_t* rec = raw + j * R::kBytes;
+    const uint2* params = reinterpret_cast<const uint2*>(rec + R::kVParams) + 8 * g + 4 * half;
+    uint32_t out[4][4];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) word[p] = v_codes[p * 8 * R::kBlocks + w];
+    for (int p = 0; p < 4; ++p) {
+      const uint2 two = params[p];
+      uint32_t code[4];
+      centred_pairs(reinterpret_cast<const uint32_t*>(rec + R::kV)[(4 * half + p) * 8 * R::kBlocks + w],
+                    code);
+      // P of a row that does not see a token is 0; 0 times a value that is not finite is not
+      auto param = [&](float v) { return fabsf(v) <= 65504.f ? v : 0.f; };
+      const float s0 = bf16_lo(two.x) * vf, s1 = bf16_lo(two.y) * vf;
+      const uint32_t sc = f16x2_bits(param(s0), param(s1));
+      const uint32_t mn = f16x2_bits(param(fmaf(8.f, s0, bf16_hi(two.x) * vf)),
+                                     param(fmaf(8.f, s1, bf16_hi(two.y) * vf)));
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t out[4][4];
+      for (int i = 0; i < 4; ++i) out[i][p] = fma_f16x2(code[i], sc, mn);
+    }
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t p0 = vp[16 * g + 8 * half + 2 * p], p1 = vp[16 * g + 8 * half + 2 * p + 1];
-        const float s0 = bf16_lo(p0) * vf, m0 = bf16_hi(p0) * vf;
-        const float s1 = bf16_lo(p1) * vf, m1 = bf16_hi(p1) * vf;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float lo = fmaf(static_cast<float>((word[4 * half + p] >> (4 * i)) & 15u), s0, m0);
-          float hi = fmaf(static_cast<float>((word[4 * half + p] >> (16 + 4 * i)) & 15u), s1, m1);
-          // P of a row that does not see the token is 0; 0 times a non-finite value is not
-          lo = fabsf(lo) <= 65504.f ? lo : 0.f;
-          hi = fabsf(hi) <= 65504.f ? hi : 0.f;
-          out[i][p] = f16x2_bits(lo, hi);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = d0 + i;
-        *reinterpret_cast<uint4*>(vimg + (j / 4) * (D * 128) + d * 128 +
-                                  (((j % 4) * 2 + half) ^ (d & 7)) * 16) =
-            make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int d = d0 + i;
+      *reinterpret_cast<uint4*>(vimg + (j / 4) * (D * 128) + d * 128 +
+                                (((j % 4) * 2 + half) ^ (d & 7)) * 16) =
+          make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
     }
   }
 }
