@@ -31,7 +31,6 @@ Formats ("Low-Precision Kernels: INT4, INT8 and FP8 Matmuls, Measured", Step 2;
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -675,12 +674,13 @@ def _kv4_weights(t, name: str, batch: int, kv_heads: int):
     return _dev(t, name, torch.float32), t.shape[2]
 
 
-def _on(stream):
-    """Context in which a result for a call on `stream` is allocated (the caching allocator
-    reuses a freed block in the order of the stream it was allocated on)."""
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A result for a call on `stream`, allocated on it (the caching allocator reuses a freed
+    block in the order of the stream it was allocated on)."""
     if isinstance(stream, torch.cuda.Stream):
-        return torch.cuda.stream(stream)
-    return contextlib.nullcontext()
+        with torch.cuda.stream(stream):
+            return like.new_empty(shape, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def kv4_append(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -708,12 +708,10 @@ def kv4_read(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, start
     each sequence as the cache holds them."""
     c = _kv4(cache, table, lens, head_dim, group)
     shape = (tokens, c.kv_heads, head_dim)
-    if k is None or v is None:
-        with _on(stream):
-            if k is None:
-                k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-            if v is None:
-                v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    if k is None:
+        k = _new(cache, shape, torch.bfloat16, stream)
+    if v is None:
+        v = _new(cache, shape, torch.bfloat16, stream)
     _check("kv4_read", _lib.kv4_read(
         c, _dev(starts, "starts", torch.int32, (c.batch + 1,)),
         _dev(k, "k", torch.bfloat16, shape), _dev(v, "v", torch.bfloat16, shape), tokens,
@@ -743,13 +741,16 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
     c = _kv4(cache, table, lens, head_dim, group)
     qp, qs = _tokens(q, "q")
     if workspace is None:
-        with _on(stream):
-            workspace = torch.zeros(kv4_attention_workspace_bytes(
-                c.batch, T, max_new, max_len, heads, c.kv_heads, head_dim, group,
-                weights_out is not None), dtype=torch.uint8, device=q.device)
+        workspace = _new(q, kv4_attention_workspace_bytes(
+            c.batch, T, max_new, max_len, heads, c.kv_heads, head_dim, group,
+            weights_out is not None), torch.uint8, stream)
+        if isinstance(stream, torch.cuda.Stream):
+            with torch.cuda.stream(stream):
+                workspace.zero_()
+        else:
+            workspace.zero_()
     if out is None:
-        with _on(stream):
-            out = torch.empty((T, heads, head_dim), dtype=torch.bfloat16, device=q.device)
+        out = _new(q, (T, heads, head_dim), torch.bfloat16, stream)
     wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
     op, ol = _kv4_weights(weights_out, "weights_out", c.batch, c.kv_heads)
     if weights is not None and wl != ol:
@@ -773,15 +774,13 @@ def kv4_evict(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weig
     each head move to the pages of ``out_table``."""
     c = _kv4(cache, table, lens, head_dim, group)
     wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
-    if kept is None or new_lens is None or weights_out is None:
-        shape, dev = (c.batch, c.kv_heads, budget), cache.device
-        with _on(stream):
-            if kept is None:
-                kept = torch.empty(shape, dtype=torch.int32, device=dev)
-            if new_lens is None:
-                new_lens = torch.empty(shape[:1], dtype=torch.int32, device=dev)
-            if weights_out is None:
-                weights_out = torch.empty(shape, dtype=torch.float32, device=dev)
+    shape = (c.batch, c.kv_heads, budget)
+    if kept is None:
+        kept = _new(cache, shape, torch.int32, stream)
+    if new_lens is None:
+        new_lens = _new(cache, shape[:1], torch.int32, stream)
+    if weights_out is None:
+        weights_out = _new(cache, shape, torch.float32, stream)
     op, ol = _kv4_weights(weights_out, "weights_out", c.batch, c.kv_heads)
     if out_table.dim() != 2 or out_table.shape[0] != c.batch:
         raise ValueError("out_table must be [batch, width]")

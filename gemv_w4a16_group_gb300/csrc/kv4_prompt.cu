@@ -287,46 +287,66 @@ __device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   if (threadIdx.x < 2) ws.counters[2 * at + threadIdx.x] = 0u;
   if (row0 >= rows) return;
   constexpr int kChunks = D / 8, kPer = kTileRows * kChunks / kImgThreads;
+  constexpr int kStep = kImgThreads / kChunks;  // rows between a thread's chunks
+  const int ch = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
+  // (token, head) of the thread's rows, one division for all of them
+  int token = (row0 + r0) / G, head = (row0 + r0) % G;
+  const int token_step = kStep / G, head_step = kStep % G;
   uint4 v[kPer];
-  uint32_t top = 0;
+  uint32_t tops = 0;  // largest magnitudes of even and odd dims, BF16 bits
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int x = threadIdx.x + i * kImgThreads, row = row0 + x / kChunks;
     v[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows)
+    if (row0 + r0 + i * kStep < rows)
       v[i] = __ldg(reinterpret_cast<const uint4*>(
-          a.q + static_cast<int64_t>(seq.s0 + row / G) * a.q_stride + (h * G + row % G) * D +
-          8 * (x % kChunks)));
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
-      top = max(top, max(lo >= 0x7F80u ? 0u : lo, hi >= 0x7F80u ? 0u : hi));
+          a.q + static_cast<int64_t>(seq.s0 + token) * a.q_stride + (h * G + head) * D + 8 * ch));
+    token += token_step;
+    head += head_step;
+    if (head >= G) {
+      head -= G;
+      ++token;
     }
   }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    tops = __vmaxu2(__vmaxu2(__vmaxu2(tops, v[i].x & 0x7FFF7FFFu), v[i].y & 0x7FFF7FFFu),
+                    __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+  uint32_t top = max(tops & 0xFFFFu, tops >> 16);
   top = block_max(top, red);
+  if (top >= 0x7F80u) {  // infinities or NaN: the largest of the others
+    top = 0;
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = (w[j / 2] >> (16 * (j % 2))) & 0x7FFFu;
+        if (x < 0x7F80u) top = max(top, x);
+      }
+    }
+    __syncthreads();
+    top = block_max(top, red);
+  }
   const int up = up_of(top << 16);
   const float f = a.scale < 0.f ? -pow2f(up) : a.scale > 0.f ? pow2f(up) : 0.f;
   if (threadIdx.x == 0) ws.qf[at] = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e * pow2f(-up);
   uint8_t* img = ws.q_img + at * Img<D>::kQ;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int x = threadIdx.x + i * kImgThreads, r = x / kChunks, ch = x % kChunks;
+    const int r = r0 + i * kStep;
+    const float q[8] = {bf16_lo(v[i].x) * f, bf16_hi(v[i].x) * f, bf16_lo(v[i].y) * f,
+                        bf16_hi(v[i].y) * f, bf16_lo(v[i].z) * f, bf16_hi(v[i].z) * f,
+                        bf16_lo(v[i].w) * f, bf16_hi(v[i].w) * f};
     *reinterpret_cast<uint4*>(img + (ch / 8) * (kTileRows * 128) + r * 128 +
                               ((ch % 8) ^ (r & 7)) * 16) =
-        make_uint4(f16x2_bits(bf16_lo(v[i].x) * f, bf16_hi(v[i].x) * f),
-                   f16x2_bits(bf16_lo(v[i].y) * f, bf16_hi(v[i].y) * f),
-                   f16x2_bits(bf16_lo(v[i].z) * f, bf16_hi(v[i].z) * f),
-                   f16x2_bits(bf16_lo(v[i].w) * f, bf16_hi(v[i].w) * f));
+        make_uint4(f16x2_bits(q[0], q[1]), f16x2_bits(q[2], q[3]), f16x2_bits(q[4], q[5]),
+                   f16x2_bits(q[6], q[7]));
     // the group's sum of q over 128, which the keys' columns make up for
     constexpr int kLanes = kChunks / NG;
-    float sum = ((bf16_lo(v[i].x) + bf16_hi(v[i].x)) + (bf16_lo(v[i].y) + bf16_hi(v[i].y))) +
-                ((bf16_lo(v[i].z) + bf16_hi(v[i].z)) + (bf16_lo(v[i].w) + bf16_hi(v[i].w)));
+    float sum = ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (ch % kLanes == 0) {
       const int g = ch / kLanes;
-      const uint32_t hl = high_low(sum * (f * 0.0078125f));
+      const uint32_t hl = high_low(sum * 0.0078125f);
       uint8_t* more = img + Img<D>::kQCodes + r * 16;
       // high, low, high, 0
       *reinterpret_cast<uint2*>(more + (g / 2) * (kTileRows * 16) + (g % 2) * 8) =
@@ -375,48 +395,58 @@ __device__ __forceinline__ uint32_t scan_add(uint32_t u) {  // inclusive, over t
 }
 
 // Tables of units_of_tile(sequence, tile), a warp a sequence, and where each CTA of an equal cut
-// begins: the kernels would need five loads one after the other to find it.
+// begins: the kernels would need five loads one after the other to find it. The searches go through
+// a copy of the tables in shared memory (`room` words at sm) where they fit.
 template <typename F>
 __device__ void plan(const Kv4AttentionArgs& a, Plan* out, Start* starts, int grid, uint32_t* base,
-                     int32_t* pre_all, int width, F units_of_tile) {
+                     int32_t* pre_all, int width, int32_t* sm, int room, F units_of_tile) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool fits = static_cast<int64_t>(a.c.batch) * (width + 2) + 1 <= room;
+  int32_t* sm_pre = sm;
+  uint32_t* sm_base = reinterpret_cast<uint32_t*>(sm + a.c.batch * (width + 1));
   for (int b = warp; b < a.c.batch; b += kImgThreads / 32) {
     const Kv4Seq s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, b);
-    int32_t* pre = pre_all + static_cast<size_t>(b) * (width + 1);
+    const size_t row = static_cast<size_t>(b) * (width + 1);
     uint32_t at = 0;
-    for (int t0 = 0; t0 < width; t0 += 32) {
+    for (int t0 = 0; t0 <= width; t0 += 32) {
       const uint32_t u = t0 + lane < width ? units_of_tile(s, t0 + lane) : 0;
       const uint32_t upto = scan_add(u);
-      if (t0 + lane < width) pre[t0 + lane] = at + upto - u;
+      if (t0 + lane <= width) {
+        pre_all[row + t0 + lane] = at + upto - u;
+        if (fits) sm_pre[row + t0 + lane] = at + upto - u;
+      }
       at += __shfl_sync(0xffffffffu, upto, 31);
     }
     if (lane == 0) {
-      pre[width] = at;
       base[b] = at * a.c.kv_heads;
+      if (fits) sm_base[b] = at * a.c.kv_heads;
     }
   }
   __syncthreads();
+  const int32_t* pre_tab = fits ? sm_pre : pre_all;
+  uint32_t* base_tab = fits ? sm_base : base;
   if (warp == 0) {
     uint32_t at = 0;
     for (int b0 = 0; b0 < a.c.batch; b0 += 32) {
-      const uint32_t u = b0 + lane < a.c.batch ? base[b0 + lane] : 0;
+      const uint32_t u = b0 + lane < a.c.batch ? base_tab[b0 + lane] : 0;
       const uint32_t upto = scan_add(u);
-      if (b0 + lane < a.c.batch) base[b0 + lane] = at + upto - u;
+      if (b0 + lane < a.c.batch) base_tab[b0 + lane] = at + upto - u;
       at += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 0) base[a.c.batch] = at;
+    if (lane == 0) base_tab[a.c.batch] = at;
   }
   __syncthreads();
-  const uint32_t total = base[a.c.batch], ctas = min(static_cast<uint32_t>(grid), total);
+  const uint32_t total = base_tab[a.c.batch], ctas = min(static_cast<uint32_t>(grid), total);
   if (threadIdx.x == 0) *out = Plan{total, ctas, 0};
   if (total == 0) return;
   const Shares shares(total, ctas);
   for (uint32_t i = threadIdx.x; i < ctas; i += kImgThreads) {
     const uint32_t u0 = shares.begin(i);
     Start x;
-    x.b = last_at_most(base, a.c.batch, u0);
-    const int32_t* pre = pre_all + static_cast<size_t>(x.b) * (width + 1);
-    const uint32_t off = u0 - base[x.b], per_head = pre[width];
+    x.b = last_at_most(base_tab, a.c.batch, u0);
+    x.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, x.b);
+    const int32_t* pre = pre_tab + static_cast<size_t>(x.b) * (width + 1);
+    const uint32_t off = u0 - base_tab[x.b], per_head = pre[width];
     x.h = static_cast<int>(off / per_head);
     const int in_head = static_cast<int>(off % per_head);
     x.tile = last_at_most(pre, width, in_head);
@@ -424,7 +454,6 @@ __device__ void plan(const Kv4AttentionArgs& a, Plan* out, Start* starts, int gr
     x.units = pre[x.tile + 1] - pre[x.tile];
     x.item_base = u0 - x.before;
     x.left = shares.begin(i + 1) - u0;
-    x.s = kv4_sequence(a.c, a.starts, a.tokens, a.max_new, a.max_len, x.b);
     starts[i] = x;
   }
 }
@@ -476,6 +505,7 @@ __global__ void __launch_bounds__(kImgThreads, 2)
   if (x == 0) {
     const int G = a.heads / a.c.kv_heads;
     plan(a, ws.plan, ws.starts, ws.grid, ws.base, ws.pre, ws.row_tiles,
+         reinterpret_cast<int32_t*>(raw), static_cast<int>(sizeof(raw) / 4),
          [&](const Kv4Seq& s, int t) { return t * kTileRows < s.m * G ? units_of(s, G, t) : 0; });
     __syncthreads();
     deal(a, ws);
@@ -485,6 +515,7 @@ __global__ void __launch_bounds__(kImgThreads, 2)
     if (ws.kbase == nullptr) return;
     const int G = a.heads / a.c.kv_heads;
     plan(a, ws.plan + 1, ws.starts + ws.grid, ws.grid, ws.kbase, ws.kpre, ws.key_tiles,
+         reinterpret_cast<int32_t*>(raw), static_cast<int>(sizeof(raw) / 4),
          [&](const Kv4Seq& s, int t) { return t * kTileKeys < s.n ? key_units_of(s, G, t) : 0; });
     return;
   }
@@ -1055,7 +1086,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (uint32_t i = i0; i <= i1; ++i) {
               const float x = ml_of(i).x, w = x == -INFINITY ? 0.f : ex2(x - mm);
               if (i == me) {
-                const float wv = w * vf;
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                   uint32_t o[16];
@@ -1064,7 +1094,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                   if (w != 0.f) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                      v[16 * z + j] = fmaf(__uint_as_float(o[j]), wv, v[16 * z + j]);
+                      v[16 * z + j] = fmaf(__uint_as_float(o[j]) * vf, w, v[16 * z + j]);
                   }
                 }
                 continue;
