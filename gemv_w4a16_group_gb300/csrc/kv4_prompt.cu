@@ -765,364 +765,364 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   };
 
   if (warp >= 8) {
-  give_registers();
-  if (some && warp == kLoadWarp) {
-    if (lane == 0) {
-      int n = 0, segs = 0;  // tiles loaded, segments begun
+    give_registers();
+    if (some && warp == kLoadWarp) {
+      if (lane == 0) {
+        int n = 0, segs = 0;  // tiles loaded, segments begun
+        bool ok = true;
+        auto load = [&](const uint8_t* src, uint32_t bytes) {
+          const int s = n % kRing;
+          if (n >= kRing) ok = mbar_wait_bounded(&empty[s], (n / kRing - 1) & 1u, abort_flag, status, limit);
+          if (!ok) return;
+          mbar_arrive_expect_tx(&full[s], bytes);
+          bulk_load(smem + L::ring_off + s * Img<D>::kTile, src, bytes, &full[s]);
+          ++n;
+        };
+        do {
+          if (segs > 0) ok = mbar_wait_bounded(q_empty, (segs - 1) & 1u, abort_flag, status, limit);
+          if (!ok) break;
+          mbar_arrive_expect_tx(q_full, Img<D>::kQ);
+          bulk_load(smem + L::q_off, ws.q_img + item(g) * Img<D>::kQ, Img<D>::kQ, q_full);
+          ++segs;
+          const uint8_t* kv = ws.kv_img + (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) *
+                                              ws.key_tiles * Img<D>::kPair;
+          for (int i = g.lo; i < g.hi && ok; ++i) {
+            const uint8_t* src = kv + static_cast<size_t>(i) * Img<D>::kPair;
+            load(src, Img<D>::kTile);
+            if (ok) load(src + Img<D>::kTile, Img<D>::kVTile);
+          }
+        } while (ok && advance(g, a, ws, plan.ctas, G));
+        if (!ok) {  // copies in flight land before the CTA exits
+          volatile uint32_t no_abort = 0u;
+          for (int i = max(0, n - kRing); i < n; ++i)
+            mbar_wait_bounded(&full[i % kRing], (i / kRing) & 1u, &no_abort, status, limit);
+          if (segs > 0) mbar_wait_bounded(q_full, (segs - 1) & 1u, &no_abort, status, limit);
+        }
+      }
+    } else if (some && warp == kMmaWarp) {
+      constexpr uint32_t s_idesc = idesc_f16_f32(128, kTileKeys), o_idesc = idesc_f16_f32(128, D);
+      const uint32_t q_s = desc_low(smem_addr(smem + L::q_off), 16);
+      const uint32_t q_more = desc_low(smem_addr(smem + L::q_off) + Img<D>::kQCodes, kTileRows * 16);
+      const uint32_t ring = desc_low(smem_addr(smem + L::ring_off), 16);
+      const uint32_t ring_more =
+          desc_low(smem_addr(smem + L::ring_off) + Img<D>::kKCodes, kTileKeys * 16);
+      int n = 0, segs = 0, steps = 0, steps_1 = 0;  // tiles of all halves, of second halves
       bool ok = true;
-      auto load = [&](const uint8_t* src, uint32_t bytes) {
-        const int s = n % kRing;
-        if (n >= kRing) ok = mbar_wait_bounded(&empty[s], (n / kRing - 1) & 1u, abort_flag, status, limit);
-        if (!ok) return;
-        mbar_arrive_expect_tx(&full[s], bytes);
-        bulk_load(smem + L::ring_off + s * Img<D>::kTile, src, bytes, &full[s]);
-        ++n;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && mbar_wait_bounded(bar, parity, abort_flag, status, limit);
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+      };
+      auto s_mma = [&](int half, int slot) {
+        const uint32_t k_s = ring + slot * (Img<D>::kTile >> 4), q_h = q_s + half * (16384 >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ss<kDescSw128>(tmem + half * 128,
+                                q_h + (((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4),
+                                k_s + (((kk / 4) * (kTileKeys * 128) + (kk % 4) * 32) >> 4), s_idesc,
+                                kk != 0);
+        tc_mma_ss<kDescPlain>(tmem + half * 128, q_more + half * (2048 >> 4),
+                              ring_more + slot * (Img<D>::kTile >> 4), s_idesc, 1u);
+      };
+      auto o_mma = [&](int half, int slot, bool first) {
+        const uint32_t v_s = ring + slot * (Img<D>::kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kTileKeys / 16; ++kk)
+          tc_mma_ts(tmem + 256 + half * D, tmem + half * 128 + kk * 8,
+                    v_s + (((kk / 4) * (D * 128) + (kk % 4) * 32) >> 4), o_idesc,
+                    kk != 0 || !first);
       };
       do {
-        if (segs > 0) ok = mbar_wait_bounded(q_empty, (segs - 1) & 1u, abort_flag, status, limit);
-        if (!ok) break;
-        mbar_arrive_expect_tx(q_full, Img<D>::kQ);
-        bulk_load(smem + L::q_off, ws.q_img + item(g) * Img<D>::kQ, Img<D>::kQ, q_full);
+        if (!wait(q_full, segs & 1u)) break;
         ++segs;
-        const uint8_t* kv = ws.kv_img + (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) *
-                                            ws.key_tiles * Img<D>::kPair;
+        if (!wait(&full[n % kRing], (n / kRing) & 1u)) break;
+        tc_fence_after_sync();
+        const int halves = halves_of(g.s, G, g.rt);
+        if (elect_one()) {
+          s_mma(0, n % kRing);
+          tc_commit(&s_full[0]);
+          if (halves == 2) {
+            s_mma(1, n % kRing);
+            tc_commit(&s_full[1]);
+          }
+          tc_commit(&empty[n % kRing]);
+          if (g.hi - g.lo == 1) tc_commit(q_empty);
+        }
+        __syncwarp();
+        ++n;
         for (int i = g.lo; i < g.hi && ok; ++i) {
-          const uint8_t* src = kv + static_cast<size_t>(i) * Img<D>::kPair;
-          load(src, Img<D>::kTile);
-          if (ok) load(src + Img<D>::kTile, Img<D>::kVTile);
+          const bool more = i + 1 < g.hi;
+          const int v_slot = n % kRing, k_slot = (n + 1) % kRing;
+          if (!wait(&full[v_slot], (n / kRing) & 1u)) break;
+          if (more && !wait(&full[k_slot], ((n + 1) / kRing) & 1u)) break;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (half >= halves) break;
+            const bool last = half + 1 == halves;
+            if (!wait(&p_full[half], (half == 0 ? steps : steps_1) & 1u)) break;
+            tc_fence_after_sync();
+            if (elect_one()) {
+              o_mma(half, v_slot, i == g.lo);
+              if (last) tc_commit(&empty[v_slot]);
+              if (more) s_mma(half, k_slot);
+              tc_commit(more ? &s_full[half] : &o_full[half]);
+              if (more && last) {
+                tc_commit(&empty[k_slot]);
+                if (i + 2 == g.hi) tc_commit(q_empty);
+              }
+            }
+            __syncwarp();
+          }
+          n += more ? 2 : 1;
+          ++steps;
+          if (halves == 2) ++steps_1;
         }
       } while (ok && advance(g, a, ws, plan.ctas, G));
-      if (!ok) {  // copies in flight land before the CTA exits
-        volatile uint32_t no_abort = 0u;
-        for (int i = max(0, n - kRing); i < n; ++i)
-          mbar_wait_bounded(&full[i % kRing], (i / kRing) & 1u, &no_abort, status, limit);
-        if (segs > 0) mbar_wait_bounded(q_full, (segs - 1) & 1u, &no_abort, status, limit);
-      }
+      if (elect_one()) tc_commit(drain);
+      volatile uint32_t no_abort = 0u;
+      mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
     }
-  } else if (some && warp == kMmaWarp) {
-    constexpr uint32_t s_idesc = idesc_f16_f32(128, kTileKeys), o_idesc = idesc_f16_f32(128, D);
-    const uint32_t q_s = desc_low(smem_addr(smem + L::q_off), 16);
-    const uint32_t q_more = desc_low(smem_addr(smem + L::q_off) + Img<D>::kQCodes, kTileRows * 16);
-    const uint32_t ring = desc_low(smem_addr(smem + L::ring_off), 16);
-    const uint32_t ring_more =
-        desc_low(smem_addr(smem + L::ring_off) + Img<D>::kKCodes, kTileKeys * 16);
-    int n = 0, segs = 0, steps = 0, steps_1 = 0;  // tiles of all halves, of second halves
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && mbar_wait_bounded(bar, parity, abort_flag, status, limit);
-      ok = __all_sync(0xffffffffu, ok);
-      return ok;
-    };
-    auto s_mma = [&](int half, int slot) {
-      const uint32_t k_s = ring + slot * (Img<D>::kTile >> 4), q_h = q_s + half * (16384 >> 4);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        tc_mma_ss<kDescSw128>(tmem + half * 128,
-                              q_h + (((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4),
-                              k_s + (((kk / 4) * (kTileKeys * 128) + (kk % 4) * 32) >> 4), s_idesc,
-                              kk != 0);
-      tc_mma_ss<kDescPlain>(tmem + half * 128, q_more + half * (2048 >> 4),
-                            ring_more + slot * (Img<D>::kTile >> 4), s_idesc, 1u);
-    };
-    auto o_mma = [&](int half, int slot, bool first) {
-      const uint32_t v_s = ring + slot * (Img<D>::kTile >> 4);
-#pragma unroll
-      for (int kk = 0; kk < kTileKeys / 16; ++kk)
-        tc_mma_ts(tmem + 256 + half * D, tmem + half * 128 + kk * 8,
-                  v_s + (((kk / 4) * (D * 128) + (kk % 4) * 32) >> 4), o_idesc,
-                  kk != 0 || !first);
-    };
-    do {
-      if (!wait(q_full, segs & 1u)) break;
-      ++segs;
-      if (!wait(&full[n % kRing], (n / kRing) & 1u)) break;
-      tc_fence_after_sync();
-      const int halves = halves_of(g.s, G, g.rt);
-      if (elect_one()) {
-        s_mma(0, n % kRing);
-        tc_commit(&s_full[0]);
-        if (halves == 2) {
-          s_mma(1, n % kRing);
-          tc_commit(&s_full[1]);
-        }
-        tc_commit(&empty[n % kRing]);
-        if (g.hi - g.lo == 1) tc_commit(q_empty);
-      }
-      __syncwarp();
-      ++n;
-      for (int i = g.lo; i < g.hi && ok; ++i) {
-        const bool more = i + 1 < g.hi;
-        const int v_slot = n % kRing, k_slot = (n + 1) % kRing;
-        if (!wait(&full[v_slot], (n / kRing) & 1u)) break;
-        if (more && !wait(&full[k_slot], ((n + 1) / kRing) & 1u)) break;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half >= halves) break;
-          const bool last = half + 1 == halves;
-          if (!wait(&p_full[half], (half == 0 ? steps : steps_1) & 1u)) break;
-          tc_fence_after_sync();
-          if (elect_one()) {
-            o_mma(half, v_slot, i == g.lo);
-            if (last) tc_commit(&empty[v_slot]);
-            if (more) s_mma(half, k_slot);
-            tc_commit(more ? &s_full[half] : &o_full[half]);
-            if (more && last) {
-              tc_commit(&empty[k_slot]);
-              if (i + 2 == g.hi) tc_commit(q_empty);
-            }
-          }
-          __syncwarp();
-        }
-        n += more ? 2 : 1;
-        ++steps;
-        if (halves == 2) ++steps_1;
-      }
-    } while (ok && advance(g, a, ws, plan.ctas, G));
-    if (elect_one()) tc_commit(drain);
-    volatile uint32_t no_abort = 0u;
-    mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
-  }
   } else {
     take_registers();
     if (some) {
-    const int half = warp >> 2, row = threadIdx.x & 127;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + half * 128, t_o = tmem + lanes + 256 + half * D;
-    uint32_t s_phase = 0, o_phase = 0, wg_phase = 0;
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t& phase) {
-      ok = ok && mbar_wait_bounded(bar, phase & 1u, abort_flag, status, limit);
-      ok = __all_sync(0xffffffffu, ok);
-      ++phase;
-      tc_fence_after_sync();
-      return ok;
-    };
-    auto wg_sync = [&]() {
-      mbar_arrive(&wg_bar[half]);
-      return wait(&wg_bar[half], wg_phase);
-    };
-    do {
-      const Kv4Seq seq = g.s;
-      if (half >= halves_of(seq, G, g.rt)) continue;
-      const int rows = seq.m * G, R = g.rt * kTileRows + half * 128 + row;
-      const int last_key = R < rows ? seq.n - seq.m + R / G : -1;
-      // first key that some row of this half does not see
-      const int first_row = g.rt * kTileRows + half * 128;
-      const int clear = first_row + 127 < rows ? seq.n - seq.m + first_row / G + 1 : 0;
-      const float qf = ws.qf[item(g)];
-      const KeyMeta* meta =
-          ws.meta + (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) * ws.key_tiles;
-      KeyMeta km = meta[g.lo];
-      float m = -INFINITY, l = 0.f;
-      int ev = km.ev;
-      for (int i = g.lo; i < g.hi; ++i) {
-        const KeyMeta now = km;
-        if (i + 1 < g.hi) km = meta[i + 1];
-        const float cf = fmaxf(qf * now.kf, 1e-37f);
-        if (!wait(&s_full[half], s_phase)) break;
-        float s[128];
+      const int half = warp >> 2, row = threadIdx.x & 127;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t t_s = tmem + lanes + half * 128, t_o = tmem + lanes + 256 + half * D;
+      uint32_t s_phase = 0, o_phase = 0, wg_phase = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t& phase) {
+        ok = ok && mbar_wait_bounded(bar, phase & 1u, abort_flag, status, limit);
+        ok = __all_sync(0xffffffffu, ok);
+        ++phase;
+        tc_fence_after_sync();
+        return ok;
+      };
+      auto wg_sync = [&]() {
+        mbar_arrive(&wg_bar[half]);
+        return wait(&wg_bar[half], wg_phase);
+      };
+      do {
+        const Kv4Seq seq = g.s;
+        if (half >= halves_of(seq, G, g.rt)) continue;
+        const int rows = seq.m * G, R = g.rt * kTileRows + half * 128 + row;
+        const int last_key = R < rows ? seq.n - seq.m + R / G : -1;
+        // first key that some row of this half does not see
+        const int first_row = g.rt * kTileRows + half * 128;
+        const int clear = first_row + 127 < rows ? seq.n - seq.m + first_row / G + 1 : 0;
+        const float qf = ws.qf[item(g)];
+        const KeyMeta* meta =
+            ws.meta + (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) * ws.key_tiles;
+        KeyMeta km = meta[g.lo];
+        float m = -INFINITY, l = 0.f;
+        int ev = km.ev;
+        for (int i = g.lo; i < g.hi; ++i) {
+          const KeyMeta now = km;
+          if (i + 1 < g.hi) km = meta[i + 1];
+          const float cf = fmaxf(qf * now.kf, 1e-37f);
+          if (!wait(&s_full[half], s_phase)) break;
+          float s[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld_32cols(t_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
-        tmem_ld_wait();
-        const int see = last_key - i * kTileKeys;  // columns up to this one are visible
-        if ((i + 1) * kTileKeys > clear) {
+          for (int c = 0; c < 4; ++c)
+            tmem_ld_32cols(t_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
+          tmem_ld_wait();
+          const int see = last_key - i * kTileKeys;  // columns up to this one are visible
+          if ((i + 1) * kTileKeys > clear) {
 #pragma unroll
-          for (int j = 0; j < 128; ++j) s[j] = j <= see ? s[j] : -INFINITY;
-        }
-        float top[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) top[x] = max3(s[x], s[x + 8], s[x + 16]);
-#pragma unroll
-        for (int j = 24; j < 120; j += 16) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) top[x] = max3(top[x], s[j + x], s[j + 8 + x]);
-        }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) top[x] = fmaxf(top[x], s[120 + x]);
-        const float best = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]),
-                                fmaxf(top[6], top[7]));
-        // -inf stays -inf: cf is positive
-        const bool raise = best * cf > m + 8.f;
-        float down = 0.f, undo = 1.f;
-        if (__any_sync(0xffffffffu, raise) || now.ev != ev) {
-          float f = 1.f;
-          if (raise) {
-            f = ex2(m - best * cf);
-            m = best * cf;
-            l *= f;
+            for (int j = 0; j < 128; ++j) s[j] = j <= see ? s[j] : -INFINITY;
           }
-          if (now.ev > ev) {
-            f *= exp2f(static_cast<float>(ev - now.ev));
-            ev = now.ev;
+          float top[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) top[x] = max3(s[x], s[x + 8], s[x + 16]);
+#pragma unroll
+          for (int j = 24; j < 120; j += 16) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) top[x] = max3(top[x], s[j + x], s[j + 8 + x]);
           }
-          // past 2^100 the values are nothing beside those met before, and P is 0
-          down = static_cast<float>(min(ev - now.ev, 100));
-          undo = exp2f(down);
-          if (i > g.lo && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld_16cols(t_o + 16 * c, o);
-              tmem_ld_wait();
+          for (int x = 0; x < 8; ++x) top[x] = fmaxf(top[x], s[120 + x]);
+          const float best = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]),
+                                  fmaxf(top[6], top[7]));
+          // -inf stays -inf: cf is positive
+          const bool raise = best * cf > m + 8.f;
+          float down = 0.f, undo = 1.f;
+          if (__any_sync(0xffffffffu, raise) || now.ev != ev) {
+            float f = 1.f;
+            if (raise) {
+              f = ex2(m - best * cf);
+              m = best * cf;
+              l *= f;
+            }
+            if (now.ev > ev) {
+              f *= exp2f(static_cast<float>(ev - now.ev));
+              ev = now.ev;
+            }
+            // past 2^100 the values are nothing beside those met before, and P is 0
+            down = static_cast<float>(min(ev - now.ev, 100));
+            undo = exp2f(down);
+            if (i > g.lo && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st_16cols(t_o + 16 * c, o);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld_16cols(t_o + 16 * c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st_16cols(t_o + 16 * c, o);
+              }
             }
           }
-        }
-        const float bias = -((m == -INFINITY ? 0.f : m) + down);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          const float bias = -((m == -INFINITY ? 0.f : m) + down);
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[32];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float x = s[64 * c + 2 * j], y = s[64 * c + 2 * j + 1];
-            fma2(x, y, cf, bias);
-            x = ex2(x);
-            y = ex2(y);
-            add2(acc[2 * (j & 1)], acc[2 * (j & 1) + 1], x, y);
-            p[j] = f16x2_bits(x, y);
-          }
-          tmem_st_32cols(t_s + 32 * c, p);
-        }
-        tmem_st_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[half]);
-        l = fmaf((acc[0] + acc[1]) + (acc[2] + acc[3]), undo, l);
-      }
-      if (!ok || !wait(&o_full[half], o_phase)) break;
-      // ---- O is complete
-      const float vf = exp2f(static_cast<float>(ev));
-      const bool whole = g.lo == 0 && g.hi == g.tiles;
-      const bool have = R < rows;
-      const int64_t at = have ? static_cast<int64_t>(seq.s0 + R / G) * a.heads + g.h * G + R % G : 0;
-      auto finish = [&](float mm, float ll) {
-        const float lse2 = ll == 0.f ? -INFINITY : mm + log2f(ll);
-        if (a.lse != nullptr) a.lse[at] = lse2 * kLn2;
-        if (ws.lse2 != nullptr) ws.lse2[at] = lse2;
-      };
-      auto store32 = [&](int c, const float* v, float inv) {
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          w[j] = inv == 0.f ? 0u : bf16x2_bits(v[2 * j] * inv, v[2 * j + 1] * inv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(a.out + at * D + 32 * c + 8 * j) =
-              make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-      };
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : vf / l;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld_32cols(t_o + 32 * c, o);
-          tmem_ld_wait();
-          if (have) store32(c, reinterpret_cast<const float*>(o), inv);
-        }
-        if (have) finish(m, l);
-      } else {
-        constexpr size_t kPart = static_cast<size_t>(D + 2) * 128;
-        float* base = ws.parts + ((2 * me + (g.lo == 0 ? 1 : 0)) * 2 + half) * kPart;
-        float* part = base + 4 * row;
-        float2* ml = reinterpret_cast<float2*>(base + D * 128);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld_32cols(t_o + 32 * c, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            __stcg(reinterpret_cast<float4*>(part) + (8 * c + j / 4) * 128,
-                   make_float4(__uint_as_float(o[j]) * vf, __uint_as_float(o[j + 1]) * vf,
-                               __uint_as_float(o[j + 2]) * vf, __uint_as_float(o[j + 3]) * vf));
-        }
-        __stcg(ml + row, make_float2(m, l));
-        const Shares shares(plan.total, plan.ctas);
-        const uint32_t i0 = shares.of(g.item_base + kItemCost);
-        const uint32_t i1 = shares.of(g.item_base + g.units - 1);
-        if (!wg_sync()) break;
-        if (row == 0) {
-          __threadfence();  // the half's writes, which the barrier has ordered before this
-          uint32_t* cnt = ws.counters + item(g) * 2 + half;
-          const bool last = atomicAdd(cnt, 1u) == i1 - i0;
-          if (last) *cnt = 0u;
-          __threadfence();
-          arrived[half] = last ? 1u : 0u;
-        }
-        if (!wg_sync()) break;
-        if (arrived[half]) {
-          // the parts in the CTAs' order; this one's is still in tensor memory
-          auto part_of = [&](uint32_t i) {
-            return ws.parts + ((2 * i + (i == i0 ? 1 : 0)) * 2 + half) * kPart;
-          };
-          auto ml_of = [&](uint32_t i) {
-            return i == me ? make_float2(m, l)
-                           : __ldcg(reinterpret_cast<const float2*>(part_of(i) + D * 128) + row);
-          };
-          float mm = -INFINITY, ll = 0.f;
-          for (uint32_t i = i0; i <= i1; i += 4) {
-            float2 x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              x[j] = i + j <= i1 ? ml_of(i + j) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (x[j].x == -INFINITY) continue;
-              const float top = fmaxf(mm, x[j].x);
-              ll = fmaf(ll, ex2(mm - top), x[j].y * ex2(x[j].x - top));
-              mm = top;
+            for (int j = 0; j < 32; ++j) {
+              float x = s[64 * c + 2 * j], y = s[64 * c + 2 * j + 1];
+              fma2(x, y, cf, bias);
+              x = ex2(x);
+              y = ex2(y);
+              add2(acc[2 * (j & 1)], acc[2 * (j & 1) + 1], x, y);
+              p[j] = f16x2_bits(x, y);
             }
+            tmem_st_32cols(t_s + 32 * c, p);
           }
-          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[half]);
+          l = fmaf((acc[0] + acc[1]) + (acc[2] + acc[3]), undo, l);
+        }
+        if (!ok || !wait(&o_full[half], o_phase)) break;
+        // ---- O is complete
+        const float vf = exp2f(static_cast<float>(ev));
+        const bool whole = g.lo == 0 && g.hi == g.tiles;
+        const bool have = R < rows;
+        const int64_t at = have ? static_cast<int64_t>(seq.s0 + R / G) * a.heads + g.h * G + R % G : 0;
+        auto finish = [&](float mm, float ll) {
+          const float lse2 = ll == 0.f ? -INFINITY : mm + log2f(ll);
+          if (a.lse != nullptr) a.lse[at] = lse2 * kLn2;
+          if (ws.lse2 != nullptr) ws.lse2[at] = lse2;
+        };
+        auto store32 = [&](int c, const float* v, float inv) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = inv == 0.f ? 0u : bf16x2_bits(v[2 * j] * inv, v[2 * j + 1] * inv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(a.out + at * D + 32 * c + 8 * j) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        };
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : vf / l;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32cols(t_o + 32 * c, o);
+            tmem_ld_wait();
+            if (have) store32(c, reinterpret_cast<const float*>(o), inv);
+          }
+          if (have) finish(m, l);
+        } else {
+          constexpr size_t kPart = static_cast<size_t>(D + 2) * 128;
+          float* base = ws.parts + ((2 * me + (g.lo == 0 ? 1 : 0)) * 2 + half) * kPart;
+          float* part = base + 4 * row;
+          float2* ml = reinterpret_cast<float2*>(base + D * 128);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32cols(t_o + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              __stcg(reinterpret_cast<float4*>(part) + (8 * c + j / 4) * 128,
+                     make_float4(__uint_as_float(o[j]) * vf, __uint_as_float(o[j + 1]) * vf,
+                                 __uint_as_float(o[j + 2]) * vf, __uint_as_float(o[j + 3]) * vf));
+          }
+          __stcg(ml + row, make_float2(m, l));
+          const Shares shares(plan.total, plan.ctas);
+          const uint32_t i0 = shares.of(g.item_base + kItemCost);
+          const uint32_t i1 = shares.of(g.item_base + g.units - 1);
+          if (!wg_sync()) break;
+          if (row == 0) {
+            __threadfence();  // the half's writes, which the barrier has ordered before this
+            uint32_t* cnt = ws.counters + item(g) * 2 + half;
+            const bool last = atomicAdd(cnt, 1u) == i1 - i0;
+            if (last) *cnt = 0u;
+            __threadfence();
+            arrived[half] = last ? 1u : 0u;
+          }
+          if (!wg_sync()) break;
+          if (arrived[half]) {
+            // the parts in the CTAs' order; this one's is still in tensor memory
+            auto part_of = [&](uint32_t i) {
+              return ws.parts + ((2 * i + (i == i0 ? 1 : 0)) * 2 + half) * kPart;
+            };
+            auto ml_of = [&](uint32_t i) {
+              return i == me ? make_float2(m, l)
+                             : __ldcg(reinterpret_cast<const float2*>(part_of(i) + D * 128) + row);
+            };
+            float mm = -INFINITY, ll = 0.f;
+            for (uint32_t i = i0; i <= i1; i += 4) {
+              float2 x[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                x[j] = i + j <= i1 ? ml_of(i + j) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (x[j].x == -INFINITY) continue;
+                const float top = fmaxf(mm, x[j].x);
+                ll = fmaf(ll, ex2(mm - top), x[j].y * ex2(x[j].x - top));
+                mm = top;
+              }
+            }
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            float v[64];
+            for (int c = 0; c < D / 64; ++c) {
+              float v[64];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] = 0.f;
-            for (uint32_t i = i0; i <= i1; ++i) {
-              const float x = ml_of(i).x, w = x == -INFINITY ? 0.f : ex2(x - mm);
-              if (i == me) {
+              for (int j = 0; j < 64; ++j) v[j] = 0.f;
+              for (uint32_t i = i0; i <= i1; ++i) {
+                const float x = ml_of(i).x, w = x == -INFINITY ? 0.f : ex2(x - mm);
+                if (i == me) {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  uint32_t o[16];
-                  tmem_ld_16cols(t_o + 64 * c + 16 * z, o);
-                  tmem_ld_wait();
-                  if (w != 0.f) {
+                  for (int z = 0; z < 4; ++z) {
+                    uint32_t o[16];
+                    tmem_ld_16cols(t_o + 64 * c + 16 * z, o);
+                    tmem_ld_wait();
+                    if (w != 0.f) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                      v[16 * z + j] = fmaf(__uint_as_float(o[j]) * vf, w, v[16 * z + j]);
+                      for (int j = 0; j < 16; ++j)
+                        v[16 * z + j] = fmaf(__uint_as_float(o[j]) * vf, w, v[16 * z + j]);
+                    }
+                  }
+                  continue;
+                }
+                const float4* src = reinterpret_cast<const float4*>(part_of(i)) + row;
+                float4 t[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) t[j] = __ldcg(src + (16 * c + j) * 128);
+                if (w != 0.f) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    v[4 * j] = fmaf(t[j].x, w, v[4 * j]);
+                    v[4 * j + 1] = fmaf(t[j].y, w, v[4 * j + 1]);
+                    v[4 * j + 2] = fmaf(t[j].z, w, v[4 * j + 2]);
+                    v[4 * j + 3] = fmaf(t[j].w, w, v[4 * j + 3]);
                   }
                 }
-                continue;
               }
-              const float4* src = reinterpret_cast<const float4*>(part_of(i)) + row;
-              float4 t[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) t[j] = __ldcg(src + (16 * c + j) * 128);
-              if (w != 0.f) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  v[4 * j] = fmaf(t[j].x, w, v[4 * j]);
-                  v[4 * j + 1] = fmaf(t[j].y, w, v[4 * j + 1]);
-                  v[4 * j + 2] = fmaf(t[j].z, w, v[4 * j + 2]);
-                  v[4 * j + 3] = fmaf(t[j].w, w, v[4 * j + 3]);
-                }
+              if (have) {
+                store32(2 * c, v, inv);
+                store32(2 * c + 1, v + 32, inv);
               }
             }
-            if (have) {
-              store32(2 * c, v, inv);
-              store32(2 * c + 1, v + 32, inv);
-            }
+            if (have) finish(mm, ll);
           }
-          if (have) finish(mm, ll);
+          if (!wg_sync()) break;  // `arrived` is read before it is written again
         }
-        if (!wg_sync()) break;  // `arrived` is read before it is written again
-      }
-    } while (advance(g, a, ws, plan.ctas, G));
+      } while (advance(g, a, ws, plan.ctas, G));
     }
   }
   __syncwarp();
