@@ -175,7 +175,10 @@ __device__ __forceinline__ bool advance(Cursor& c, const Kv4AttentionArgs& a, in
   return true;
 }
 
-template <int D, int NG, int NT>
+// PACK: up to four rows stand in columns 0..3 for a unit's first record and again in 4..7 for its
+// second, so that one accumulator holds the logits of both and every lane's share of the softmax
+// is of use (otherwise half of the columns pad the tile).
+template <int D, int NG, int NT, bool PACK>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStages = ring_stages(D, NG);
@@ -194,11 +197,12 @@ struct Shape {
   static_assert(total <= (ctas_per_sm(D, NT) == 2 ? 113u : 227u) * 1024u, "shared memory");
 };
 
-template <int D, int NG, int NT, bool LOGITS>
+template <int D, int NG, int NT, bool PACK, bool LOGITS>
 __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
     kv4_attention_kernel(const Kv4AttentionArgs a, const Workspace ws) {
   using R = Kv4Record<D, NG>;
-  using S = Shape<D, NG, NT>;
+  using S = Shape<D, NG, NT, PACK>;
+  static_assert(!PACK || (NT == 1 && kUnitRecords == 2), "two records, eight columns");
   constexpr int NB = R::kBlocks, kRows = S::kRows, kLower = S::kLower, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bar_off);  // [warp][stage]
@@ -358,8 +362,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
     const int row0 = cur.tile * kRows, rows = min(kRows, seq.m * G - row0);
     // ---- a warp an n8 tile brings the queries into FP16 fragments under a power of two a row
     if (warp < NT) {
-      const int row = row0 + warp * 8 + r;
-      const bool have = warp * 8 + r < rows;
+      const int row = row0 + warp * 8 + (PACK ? r & 3 : r);
+      const bool have = row - row0 < rows;
       const uint16_t* src = a.q + static_cast<int64_t>(seq.s0 + (have ? row / G : 0)) * a.q_stride +
                             (cur.h * G + (have ? row % G : 0)) * D + 8 * c;
       uint4 v[NB];
@@ -388,7 +392,14 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
                                    f16x2_bits(bf16_lo(v[x].y) * f16, bf16_hi(v[x].y) * f16),
                                    f16x2_bits(bf16_lo(v[x].z) * f, bf16_hi(v[x].z) * f),
                                    f16x2_bits(bf16_lo(v[x].w) * f16, bf16_hi(v[x].w) * f16));
-        *reinterpret_cast<uint4*>(smem + S::q_off + ((warp * NB + x) * 32 + lane) * 16) = h;
+        uint4* to = reinterpret_cast<uint4*>(smem + S::q_off + ((warp * NB + x) * 32 + lane) * 16);
+        if constexpr (PACK) {
+          const uint4 none = make_uint4(0, 0, 0, 0);
+          to[0] = r < 4 ? h : none;
+          to[NB * 32] = r < 4 ? none : h;
+        } else {
+          *to = h;
+        }
         v[x] = h;
       }
       // sums of q over a group's dims, as codes 1 would give them: column n of the product
@@ -448,72 +459,105 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
     auto compute = [&](auto mask, uint32_t base, int key0) {
       constexpr bool kMasked = decltype(mask)::value;
       const int records = kMasked ? min(kUnitRecords, (seq.n - key0 + 15) / 16) : kUnitRecords;
-      // ---- logits, times 1 / unscale
-      float s[kUnitRecords][NT][4];
+      // ---- logits, times 1 / unscale. Set j holds record j's tokens (packed: a lane's own record's)
+      constexpr int kSets = PACK ? 1 : kUnitRecords;
+      const int half = c >> 1;  // packed: this lane's record
+      float s[kSets][NT][4];
+      auto fold = [&](int j, int g, uint32_t p0, uint32_t p1, const float (&acc)[NT][4]) {
+        const float s0 = bf16_lo(p0), s1 = bf16_lo(p1), m0 = bf16_hi(p0), m1 = bf16_hi(p1);
 #pragma unroll
-      for (int j = 0; j < kUnitRecords; ++j) {
-        if (kMasked && j >= records) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][nt][i] = -INFINITY;
-          continue;
-        }
-        const uint32_t rec = base + j * R::kBytes;
-        uint32_t w0[NB], w1[NB];
-        load_words<NB>(rec + ((r * 4 + c) * NB) * 4, w0);
-        load_words<NB>(rec + (((r + 8) * 4 + c) * NB) * 4, w1);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const uint32_t p0 = lds32(rec + R::kKParams + (16 * g + r) * 4);
-          const uint32_t p1 = lds32(rec + R::kKParams + (16 * g + r + 8) * 4);
-          float acc[NT][4];
-#pragma unroll
-          for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
-            uint32_t k0[4], k1[4];
-            key_pairs(w0[x], k0);
-            key_pairs(w1[x], k1);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint4 q = lds128(q_s + (nt * NB + x) * 512);
-              if (x == g * NB / NG)
-                mma_f16_first(acc[nt], k0[0], k1[0], k0[1], k1[1], q.x, q.y);
-              else
-                mma_f16_16816(acc[nt], k0[0], k1[0], k0[1], k1[1], q.x, q.y);
-              mma_f16_16816(acc[nt], k0[2], k1[2], k0[3], k1[3], q.z, q.w);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float m = i < 2 ? m0 : m1, sum_q = sq[nt][g][i & 1];
+            s[j][nt][i] = fmaf(i < 2 ? s0 : s1, acc[nt][i],
+                               g == 0 ? m * sum_q : fmaf(m, sum_q, s[j][nt][i]));
           }
-          const float s0 = bf16_lo(p0), s1 = bf16_lo(p1), m0 = bf16_hi(p0), m1 = bf16_hi(p1);
+      };
+      auto hide_and_keep = [&](int j) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float m = i < 2 ? m0 : m1, sum_q = sq[nt][g][i & 1];
-              s[j][nt][i] = fmaf(i < 2 ? s0 : s1, acc[nt][i],
-                                 g == 0 ? m * sum_q : fmaf(m, sum_q, s[j][nt][i]));
+          for (int i = 0; i < 4; ++i) {
+            const int row = PACK ? 2 * (c & 1) + (i & 1) : nt * 8 + 2 * c + (i & 1);
+            const int key = key0 + 16 * (PACK ? half : j) + r + (i >= 2 ? 8 : 0);
+            if constexpr (kMasked) {
+              if (key > (row < rows ? seq.n - seq.m + (row0 + row) / G : -1))
+                s[j][nt][i] = -INFINITY;
             }
-        }
-        if constexpr (kMasked) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = nt * 8 + 2 * c + (i & 1);
-              const int last = row < rows ? seq.n - seq.m + (row0 + row) / G : -1;
-              if (key0 + 16 * j + r + (i >= 2 ? 8 : 0) > last) s[j][nt][i] = -INFINITY;
-            }
-        }
-        if constexpr (LOGITS) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = nt * 8 + 2 * c + (i & 1);
-              const int key = key0 + 16 * j + r + (i >= 2 ? 8 : 0);
+            if constexpr (LOGITS) {
               if (row < rows && key < seq.n)
                 ws.logits[((static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) * a.max_new * G +
                            row0 + row) * ws.row_len + key] = s[j][nt][i] * unscale[nt][i & 1];
             }
+          }
+      };
+      if constexpr (PACK) {
+        uint32_t w0[kUnitRecords][NB], w1[kUnitRecords][NB];
+#pragma unroll
+        for (int j = 0; j < kUnitRecords; ++j) {
+          load_words<NB>(base + j * R::kBytes + ((r * 4 + c) * NB) * 4, w0[j]);
+          load_words<NB>(base + j * R::kBytes + (((r + 8) * 4 + c) * NB) * 4, w1[j]);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t at = base + half * R::kBytes + R::kKParams + (16 * g + r) * 4;
+          const uint32_t p0 = lds32(at), p1 = lds32(at + 32);
+          float acc[NT][4];
+#pragma unroll
+          for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x)
+#pragma unroll
+            for (int j = 0; j < kUnitRecords; ++j) {
+              uint32_t k0[4], k1[4];
+              key_pairs(w0[j][x], k0);
+              key_pairs(w1[j][x], k1);
+              const uint4 q = lds128(q_s + (j * NB + x) * 512);
+              if (x == g * NB / NG && j == 0)
+                mma_f16_first(acc[0], k0[0], k1[0], k0[1], k1[1], q.x, q.y);
+              else
+                mma_f16_16816(acc[0], k0[0], k1[0], k0[1], k1[1], q.x, q.y);
+              mma_f16_16816(acc[0], k0[2], k1[2], k0[3], k1[3], q.z, q.w);
+            }
+          fold(0, g, p0, p1, acc);
+        }
+        hide_and_keep(0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kUnitRecords; ++j) {
+          if (kMasked && j >= records) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[j][nt][i] = -INFINITY;
+            continue;
+          }
+          const uint32_t rec = base + j * R::kBytes;
+          uint32_t w0[NB], w1[NB];
+          load_words<NB>(rec + ((r * 4 + c) * NB) * 4, w0);
+          load_words<NB>(rec + (((r + 8) * 4 + c) * NB) * 4, w1);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const uint32_t p0 = lds32(rec + R::kKParams + (16 * g + r) * 4);
+            const uint32_t p1 = lds32(rec + R::kKParams + (16 * g + r + 8) * 4);
+            float acc[NT][4];
+#pragma unroll
+            for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
+              uint32_t k0[4], k1[4];
+              key_pairs(w0[x], k0);
+              key_pairs(w1[x], k1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint4 q = lds128(q_s + (nt * NB + x) * 512);
+                if (x == g * NB / NG)
+                  mma_f16_first(acc[nt], k0[0], k1[0], k0[1], k1[1], q.x, q.y);
+                else
+                  mma_f16_16816(acc[nt], k0[0], k1[0], k0[1], k1[1], q.x, q.y);
+                mma_f16_16816(acc[nt], k0[2], k1[2], k0[3], k1[3], q.z, q.w);
+              }
+            }
+            fold(j, g, p0, p1, acc);
+          }
+          hide_and_keep(j);
         }
       }
       // ---- running maximum, and the largest V scale's exponent among the visible tokens. Both
@@ -535,7 +579,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
           for (int i = 0; i < 2; ++i) {
             float v = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
 #pragma unroll
-            for (int j = 1; j < kUnitRecords; ++j)
+            for (int j = 1; j < kSets; ++j)
               v = fmaxf(v, fmaxf(s[j][nt][i], s[j][nt][i + 2]));
             fits = fits && v * unscale[nt][i] <= mx[nt][i] + 8.f;
           }
@@ -558,11 +602,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
             uint32_t top = unit_top;
             if constexpr (kMasked) {
 #pragma unroll
-              for (int j = 0; j < kUnitRecords; ++j)
+              for (int j = 0; j < kSets; ++j)
 #pragma unroll
                 for (int x = 0; x < 2 * NG; ++x) {
-                  if (j >= records || s[j][nt][i + 2 * (x & 1)] == -INFINITY) continue;
-                  const uint32_t sc = lds32(base + j * R::kBytes + R::kVParams +
+                  if (s[j][nt][i + 2 * (x & 1)] == -INFINITY) continue;
+                  const uint32_t sc = lds32(base + (PACK ? half : j) * R::kBytes + R::kVParams +
                                             (16 * (x / 2) + r + 8 * (x & 1)) * 4) & 0xFFFFu;
                   if (sc < 0x7F80u) top = max(top, sc);
                 }
@@ -572,11 +616,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
             }
             float v = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
 #pragma unroll
-            for (int j = 1; j < kUnitRecords; ++j)
+            for (int j = 1; j < kSets; ++j)
               v = fmaxf(v, fmaxf(s[j][nt][i], s[j][nt][i + 2]));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            if constexpr (PACK) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
             const float now = fmaxf(mx[nt][i], v * unscale[nt][i]);
             const int ev_now = max(ev[nt][i], static_cast<int>(top >> 7));
             const float alpha = now == -INFINITY ? 1.f : ex2(mx[nt][i] - now);
@@ -600,14 +645,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
         cap = pow2f(min(least - 121, 127));
       }
       // ---- P V
-#pragma unroll
-      for (int j = 0; j < kUnitRecords; ++j) {
-        if (kMasked && j >= records) continue;
-        const uint32_t rec = base + j * R::kBytes;
-        uint32_t w0[NB], w1[NB];
-        load_words<NB>(rec + R::kV + ((c * 8 + r) * NB) * 4, w0);
-        load_words<NB>(rec + R::kV + (((c + 4) * 8 + r) * NB) * 4, w1);
-        float p[NT][4], pd[NT][4];  // p, and p under the scales' power of two
+      auto probabilities = [&](int j, float (&p)[NT][4], float (&pd)[NT][4]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -618,42 +656,81 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
             sum[nt][i & 1] += p[nt][i];
             pd[nt][i] = p[nt][i] * down[nt][i & 1];
           }
+      };
+      // P of set j times group g's scales (parameters p0, p1), as the products' second operand
+      auto scaled = [&](int j, int g, uint32_t p0, uint32_t p1, const float (&p)[NT][4],
+                        const float (&pd)[NT][4], uint32_t (&b0)[NT], uint32_t (&b1)[NT]) {
+        const float s0 = bf16_lo(p0), s1 = bf16_lo(p1), m0 = bf16_hi(p0), m1 = bf16_hi(p1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = pd[nt][i] * (i < 2 ? s0 : s1);
+            // a hidden token's parameters may hold anything, NaN included
+            if (kMasked && s[j][nt][i] == -INFINITY)
+              x[i] = 0.f;
+            else
+              corr[nt][g][i & 1] = fmaf(p[nt][i], i < 2 ? m0 : m1, corr[nt][g][i & 1]);
+          }
+          b0[nt] = movmatrix_trans(f16x2_bits(x[0], x[1]));
+          b1[nt] = movmatrix_trans(f16x2_bits(x[2], x[3]));
+        }
+      };
+      if constexpr (PACK) {
+        float p[NT][4], pd[NT][4];
+        probabilities(0, p, pd);
+        uint32_t w0[kUnitRecords][NB], w1[kUnitRecords][NB];
+#pragma unroll
+        for (int j = 0; j < kUnitRecords; ++j) {
+          load_words<NB>(base + j * R::kBytes + R::kV + ((c * 8 + r) * NB) * 4, w0[j]);
+          load_words<NB>(base + j * R::kBytes + R::kV + (((c + 4) * 8 + r) * NB) * 4, w1[j]);
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const uint32_t p0 = lds32(rec + R::kVParams + (16 * g + r) * 4);
-          const uint32_t p1 = lds32(rec + R::kVParams + (16 * g + r + 8) * 4);
-          const float s0 = bf16_lo(p0), s1 = bf16_lo(p1), m0 = bf16_hi(p0), m1 = bf16_hi(p1);
+          const uint32_t at = base + half * R::kBytes + R::kVParams + (16 * g + r) * 4;
           uint32_t b0[NT], b1[NT];
+          scaled(0, g, lds32(at), lds32(at + 32), p, pd, b0, b1);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float x[4];
+          for (int j = 0; j < kUnitRecords; ++j) {
+            // a lane holds a column: the other record's are no part of this one's product
+            const bool on = (r >= 4) == (j == 1);
+            const uint32_t c0 = on ? b0[0] : 0u, c1 = on ? b1[0] : 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = pd[nt][i] * (i < 2 ? s0 : s1);
-            if constexpr (!kMasked) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                corr[nt][g][i & 1] = fmaf(p[nt][i], i < 2 ? m0 : m1, corr[nt][g][i & 1]);
-            } else {  // a hidden token's parameters may hold anything, NaN included
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (s[j][nt][i] == -INFINITY)
-                  x[i] = 0.f;
-                else
-                  corr[nt][g][i & 1] = fmaf(p[nt][i], i < 2 ? m0 : m1, corr[nt][g][i & 1]);
-              }
+            for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
+              uint32_t v0[4], v1[4];
+              value_pairs(w0[j][x], v0);
+              value_pairs(w1[j][x], v1);
+              mma_f16_16816(o[0][x][0], v0[0], v0[1], v1[0], v1[1], c0, c1);
+              mma_f16_16816(o[0][x][1], v0[2], v0[3], v1[2], v1[3], c0, c1);
             }
-            b0[nt] = movmatrix_trans(f16x2_bits(x[0], x[1]));
-            b1[nt] = movmatrix_trans(f16x2_bits(x[2], x[3]));
           }
+        }
+      } else {
 #pragma unroll
-          for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
-            uint32_t v0[4], v1[4];
-            value_pairs(w0[x], v0);
-            value_pairs(w1[x], v1);
+        for (int j = 0; j < kUnitRecords; ++j) {
+          if (kMasked && j >= records) continue;
+          const uint32_t rec = base + j * R::kBytes;
+          uint32_t w0[NB], w1[NB];
+          load_words<NB>(rec + R::kV + ((c * 8 + r) * NB) * 4, w0);
+          load_words<NB>(rec + R::kV + (((c + 4) * 8 + r) * NB) * 4, w1);
+          float p[NT][4], pd[NT][4];
+          probabilities(j, p, pd);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16_16816(o[nt][x][0], v0[0], v0[1], v1[0], v1[1], b0[nt], b1[nt]);
-              mma_f16_16816(o[nt][x][1], v0[2], v0[3], v1[2], v1[3], b0[nt], b1[nt]);
+          for (int g = 0; g < NG; ++g) {
+            const uint32_t at = rec + R::kVParams + (16 * g + r) * 4;
+            uint32_t b0[NT], b1[NT];
+            scaled(j, g, lds32(at), lds32(at + 32), p, pd, b0, b1);
+#pragma unroll
+            for (int x = g * NB / NG; x < (g + 1) * NB / NG; ++x) {
+              uint32_t v0[4], v1[4];
+              value_pairs(w0[x], v0);
+              value_pairs(w1[x], v1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_f16_16816(o[nt][x][0], v0[0], v0[1], v1[0], v1[1], b0[nt], b1[nt]);
+                mma_f16_16816(o[nt][x][1], v0[2], v0[3], v1[2], v1[3], b0[nt], b1[nt]);
+              }
             }
           }
         }
@@ -760,13 +837,19 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = sm_ml[w * kRows + row];
-        if (ml.x != -INFINITY) l = fmaf(ml.y, ex2(ml.x - m), l);
+        if (ml.x != -INFINITY)
+          l = fmaf(PACK ? ml.y + sm_ml[w * kRows + row + 4].y : ml.y, ex2(ml.x - m), l);
       }
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kLower; ++w) {
         const float4 t = *reinterpret_cast<const float4*>(sm_o + (w * kRows + row) * D + 4 * e);
         v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+        if constexpr (PACK) {
+          const float4 z =
+              *reinterpret_cast<const float4*>(sm_o + (w * kRows + row + 4) * D + 4 * e);
+          v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
+        }
       }
       if (whole) {
         store(row, e, v, m, l);
@@ -920,9 +1003,9 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   return l;
 }
 
-template <int D, int NG, int NT>
+template <int D, int NG, int NT, bool PACK>
 cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
-  using S = Shape<D, NG, NT>;
+  using S = Shape<D, NG, NT, PACK>;
   const Layout l = layout(a.c.batch, a.tokens, a.max_new, a.max_len, a.heads, a.c.kv_heads, D,
                           a.weights_out != nullptr);
   Workspace ws;
@@ -931,8 +1014,8 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   ws.logits = reinterpret_cast<float*>(a.workspace + l.logits);
   ws.parts = reinterpret_cast<float*>(a.workspace + l.parts);
   ws.row_len = l.row_len;
-  auto kern = a.weights_out != nullptr ? kv4_attention_kernel<D, NG, NT, true>
-                                       : kv4_attention_kernel<D, NG, NT, false>;
+  auto kern = a.weights_out != nullptr ? kv4_attention_kernel<D, NG, NT, PACK, true>
+                                       : kv4_attention_kernel<D, NG, NT, PACK, false>;
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), S::total);
   if (e != cudaSuccess) return e;
   const int G = a.heads / a.c.kv_heads;
@@ -951,8 +1034,9 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
 
 template <int D, int NG>
 cudaError_t by_rows(const Kv4AttentionArgs& a, cudaStream_t stream) {
-  return row_blocks(a.max_new, a.heads / a.c.kv_heads) == 1 ? run<D, NG, 1>(a, stream)
-                                                            : run<D, NG, 2>(a, stream);
+  const int G = a.heads / a.c.kv_heads;
+  if (row_blocks(a.max_new, G) == 2) return run<D, NG, 2, false>(a, stream);
+  return a.max_new * G <= 4 ? run<D, NG, 1, true>(a, stream) : run<D, NG, 1, false>(a, stream);
 }
 
 // Above kFewRows the prompts' path takes over. It widens the whole cache to FP16 tiles first and
