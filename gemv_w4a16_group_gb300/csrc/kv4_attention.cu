@@ -23,8 +23,8 @@
 // in order are cut into equal ranges, one a CTA, from the lengths on the device: ragged batches
 // and one long sequence use the whole GPU alike, and a bound on the length costs nothing. Within
 // a range the computing warps take units in turn, each from its own ring of bulk copies that
-// one more warp keeps filled; there is no barrier but at a segment (the part of one sequence, head and
-// tile in the range), whose rows one warp prepares and whose end joins the warps' (max, sum,
+// one more warp keeps filled; there is no barrier but at a segment (the part of one sequence, head
+// and tile in the range), whose rows one warp prepares and whose end joins the warps' (max, sum,
 // accumulator) through shared memory. A segment that another CTA shares goes to the workspace in
 // fp32, and the CTA that arrives last joins the parts in order. (Copies issued by the computing
 // warps themselves, with a page looked up for each, cost them registers and a sixth of their

@@ -68,7 +68,8 @@ struct PromptWs {
   uint8_t* kv_img;    // [batch, kv_heads, key_tiles] x (K 128 (D + 16), V^T D 128) FP16
   uint32_t* counters; // [batch, kv_heads, row_tiles, 2], zeroed beside the images
   float* parts;       // [2 grid][2 halves] x (D + 2) 128
-  float* lse2;        // [tokens, heads], base 2
+  // [batch, kv_heads, row_tiles, 256] less the log-sums, base 2; -inf for a row that sees nothing
+  float* lse2;
   // with weights, the same for the units of the token tiles (row tiles that see them)
   uint32_t* kbase;    // [batch + 1]
   int32_t* kpre;      // [batch, key_tiles + 1]
@@ -202,8 +203,9 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   uint32_t ktop = 0, vtop = 0;
   for (int x = tid; x < 8 * 16 * NG; x += kImgThreads) {
     const int j = x / (16 * NG), w = x % (16 * NG);
-    ktop = max(ktop, reach_bits(reinterpret_cast<const uint32_t*>(raw + j * R::kBytes + R::kKParams)[w]));
-    vtop = max(vtop, reach_bits(reinterpret_cast<const uint32_t*>(raw + j * R::kBytes + R::kVParams)[w]));
+    const uint8_t* rec = raw + j * R::kBytes;
+    ktop = max(ktop, reach_bits(reinterpret_cast<const uint32_t*>(rec + R::kKParams)[w]));
+    vtop = max(vtop, reach_bits(reinterpret_cast<const uint32_t*>(rec + R::kVParams)[w]));
   }
   ktop = block_max(ktop, red[0]);
   vtop = block_max(vtop, red[1]);
@@ -599,6 +601,14 @@ __device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
+// (x, y) = (x, y) * a + (b, c)
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float c) {
+  asm("{\n\t.reg .b64 v, s, t;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %4};\n\t"
+      "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c));
+}
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
   asm("{\n\t.reg .b64 v, s;\n\t"
       "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
@@ -772,7 +782,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         bool ok = true;
         auto load = [&](const uint8_t* src, uint32_t bytes) {
           const int s = n % kRing;
-          if (n >= kRing) ok = mbar_wait_bounded(&empty[s], (n / kRing - 1) & 1u, abort_flag, status, limit);
+          if (n >= kRing)
+            ok = mbar_wait_bounded(&empty[s], (n / kRing - 1) & 1u, abort_flag, status, limit);
           if (!ok) return;
           mbar_arrive_expect_tx(&full[s], bytes);
           bulk_load(smem + L::ring_off + s * Img<D>::kTile, src, bytes, &full[s]);
@@ -903,7 +914,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       };
       do {
         const Kv4Seq seq = g.s;
-        if (half >= halves_of(seq, G, g.rt)) continue;
+        if (half >= halves_of(seq, G, g.rt)) {
+          if (ws.lse2 != nullptr) ws.lse2[item(g) * kTileRows + 128 + row] = -INFINITY;
+          continue;
+        }
         const int rows = seq.m * G, R = g.rt * kTileRows + half * 128 + row;
         const int last_key = R < rows ? seq.n - seq.m + R / G : -1;
         // first key that some row of this half does not see
@@ -1001,8 +1015,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int64_t at = have ? static_cast<int64_t>(seq.s0 + R / G) * a.heads + g.h * G + R % G : 0;
         auto finish = [&](float mm, float ll) {
           const float lse2 = ll == 0.f ? -INFINITY : mm + log2f(ll);
-          if (a.lse != nullptr) a.lse[at] = lse2 * kLn2;
-          if (ws.lse2 != nullptr) ws.lse2[at] = lse2;
+          if (have && a.lse != nullptr) a.lse[at] = lse2 * kLn2;
+          if (ws.lse2 != nullptr)
+            ws.lse2[item(g) * kTileRows + half * 128 + row] =
+                have && lse2 != -INFINITY ? -lse2 : -INFINITY;
         };
         auto store32 = [&](int c, const float* v, float inv) {
           uint32_t w[16];
@@ -1023,7 +1039,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tmem_ld_wait();
             if (have) store32(c, reinterpret_cast<const float*>(o), inv);
           }
-          if (have) finish(m, l);
+          finish(m, l);
         } else {
           constexpr size_t kPart = static_cast<size_t>(D + 2) * 128;
           float* base = ws.parts + ((2 * me + (g.lo == 0 ? 1 : 0)) * 2 + half) * kPart;
@@ -1118,7 +1134,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 store32(2 * c + 1, v + 32, inv);
               }
             }
-            if (have) finish(mm, ll);
+            finish(mm, ll);
           }
           if (!wg_sync()) break;  // `arrived` is read before it is written again
         }
@@ -1135,11 +1151,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 }
 
 // ---- weights -----------------------------------------------------------------------------
-// Units are (row tile, token tile) pairs, token tile by token tile, cut evenly over the CTAs. 8
-// warps: a thread a token (TMEM lane) and half of a row tile's 256 columns; S^T is
-// double-buffered in tensor memory. A token tile that a boundary cuts is joined from its parts
-// (128 sums) by whoever arrives last, in order.
-constexpr int kSumWarps = 8;
+// Units are (row tile, token tile) pairs, token tile by token tile, cut evenly over the CTAs. 16
+// warps: a thread a token (TMEM lane) and a quarter of a row tile's 256 columns; S^T is
+// double-buffered in tensor memory, and a row tile's log-sums come as one more bulk copy. A token
+// tile that a boundary cuts is joined from its parts (128 sums) by whoever arrives last, in order.
+//
+// A unit's products take 1490 cycles, with its 75 KB of loads 1750, a thread's way through 64
+// exponentials and sums 2300 (1.2 us a unit: 78 us for a prompt of 4096 tokens of 32 heads on 8,
+// 262 us for 8192). Eight warps of 128 columns each took 84 and 286 us, with a barrier a unit and
+// the log-sums fetched by each thread 107 and 380; the next columns' load ahead of the sums spills
+// at sixteen warps.
+constexpr int kSumWarps = 16;
+constexpr int kSumParts = kSumWarps / 4;
+constexpr int kSumCols = kTileRows / kSumParts;
+// The log-sums' ring. Unit n's are written once unit n - 2's products are made; those waited until
+// every warp had read unit n - 4's, so unit n - 8's are done with.
+constexpr int kLseRing = 8;
 constexpr int kSumThreads = kSumWarps * 32;
 constexpr int kWeightThreads = kSumThreads + 64;
 
@@ -1147,11 +1174,11 @@ template <int D>
 struct WeightSmem {
   static constexpr uint32_t k_off = 0;
   static constexpr uint32_t q_off = 2 * Img<D>::kTile;
-  static constexpr uint32_t lse_off = q_off + 2 * Img<D>::kQ;         // [2][256]
-  static constexpr uint32_t sum_off = lse_off + 2 * kTileRows * 4;    // [128]
-  static constexpr uint32_t bar_off = sum_off + 128 * 4;
-  // k_full[2], k_empty[2], q_full[2], q_empty[2], s_full[2], s_empty[2], drain
-  static constexpr uint32_t misc_off = bar_off + 13 * 8;
+  static constexpr uint32_t lse_off = q_off + 2 * Img<D>::kQ;         // [kLseRing][256]
+  static constexpr uint32_t sum_off = lse_off + kLseRing * kTileRows * 4;  // [parts - 1][128]
+  static constexpr uint32_t bar_off = sum_off + (kSumParts - 1) * 128 * 4;
+  // k_full[2], k_empty[2], q_full[2], q_empty[2], s_full[2], s_empty[2], lse_full[8], drain
+  static constexpr uint32_t misc_off = bar_off + (13 + kLseRing) * 8;
   static constexpr uint32_t total = misc_off + 16;
   static constexpr uint32_t alloc = total + 1024;
 };
@@ -1201,7 +1228,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
   uint64_t *k_empty = k_full + 2, *q_full = k_empty + 2, *q_empty = q_full + 2,
-           *s_full = q_empty + 2, *s_empty = s_full + 2, *drain = s_empty + 2;
+           *s_full = q_empty + 2, *s_empty = s_full + 2, *lse_full = s_empty + 2,
+           *drain = lse_full + kLseRing;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile uint32_t* abort_flag = tmem_holder + 1;
   volatile uint32_t* arrived = tmem_holder + 2;
@@ -1218,6 +1246,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], kSumWarps);
     }
+    for (int i = 0; i < kLseRing; ++i) mbar_init(&lse_full[i], 1);
     mbar_init(drain, 1);
     *abort_flag = 0u;
     fence_barrier_init();
@@ -1257,7 +1286,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       int n = 0, segs = 0;
       do {
         const int ks = segs & 1;
-        if (segs >= 2) ok = mbar_wait_bounded(&k_empty[ks], (segs / 2 - 1) & 1u, abort_flag, status, limit);
+        if (segs >= 2)
+          ok = mbar_wait_bounded(&k_empty[ks], (segs / 2 - 1) & 1u, abort_flag, status, limit);
         if (!ok) break;
         mbar_arrive_expect_tx(&k_full[ks], Img<D>::kTile);
         bulk_load(smem + L::k_off + ks * Img<D>::kTile,
@@ -1268,10 +1298,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           const int s = n & 1;
           if (n >= 2) ok = mbar_wait_bounded(&q_empty[s], (n / 2 - 1) & 1u, abort_flag, status, limit);
           if (!ok) break;
+          const size_t tile = head() * ws.row_tiles + g.first + i;
+          const int z = n % kLseRing;
+          mbar_arrive_expect_tx(&lse_full[z], kTileRows * 4);
+          bulk_load(lse_s + z * kTileRows, ws.lse2 + tile * kTileRows, kTileRows * 4, &lse_full[z]);
           mbar_arrive_expect_tx(&q_full[s], Img<D>::kQ);
           bulk_load(smem + L::q_off + s * Img<D>::kQ,
-                    ws.q_img + (head() * ws.row_tiles + g.first + i) * Img<D>::kQ, Img<D>::kQ,
-                    &q_full[s]);
+                    ws.q_img + tile * Img<D>::kQ, Img<D>::kQ, &q_full[s]);
         }
       } while (ok && advance(g, a, G));
       if (!ok) {  // copies in flight land before the CTA exits
@@ -1280,6 +1313,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           mbar_wait_bounded(&k_full[i & 1], (i / 2) & 1u, &no_abort, status, limit);
         for (int i = max(0, n - 2); i < n; ++i)
           mbar_wait_bounded(&q_full[i & 1], (i / 2) & 1u, &no_abort, status, limit);
+        for (int i = max(0, n - kLseRing); i < n; ++i)
+          mbar_wait_bounded(&lse_full[i % kLseRing], (i / kLseRing) & 1u, &no_abort, status, limit);
       }
     }
   } else if (warp == kSumWarps + 1) {
@@ -1323,80 +1358,78 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     volatile uint32_t no_abort = 0u;
     mbar_wait_bounded(drain, 0u, &no_abort, status, limit);
   } else {
-    const int part = warp >> 2;  // columns 128 part .. 128 part + 127
-    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + part * 128;
+    const int part = warp >> 2;  // columns kSumCols part ..
+    const uint32_t t_s =
+        tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + part * kSumCols;
     bool ok = true;
     int n = 0;
-    // the log-sum of row `threadIdx.x` of a row tile; rows past the end see nothing
-    auto lse_of = [&](int rt) {
-      const int R = rt * kTileRows + threadIdx.x;
-      float v = INFINITY;
-      if (R < g.s.m * G)
-        v = ws.lse2[static_cast<int64_t>(g.s.s0 + R / G) * a.heads + g.h * G + R % G];
-      return v == -INFINITY ? INFINITY : v;
-    };
     do {
       const int key = g.kt * kTileKeys + (warp & 3) * 32 + lane;
       const float kf = ws.meta[head() * ws.key_tiles + g.kt].kf;
       float acc = 0.f;
-      float lse_next = lse_of(g.first + g.lo), qf_next = ws.qf[head() * ws.row_tiles + min(g.first + g.lo, ws.row_tiles - 1)];
+      auto qf_of = [&](int i) { return ws.qf[head() * ws.row_tiles + g.first + i]; };
+      // rows that do not see the lane's token, and the first tile whose rows see all of them
+      const int64_t need = static_cast<int64_t>(key - (g.s.n - g.s.m)) * G;
+      const int64_t last =
+          static_cast<int64_t>(g.kt * kTileKeys + kTileKeys - 1 - (g.s.n - g.s.m)) * G;
+      const int clear =
+          static_cast<int>(max(static_cast<int64_t>(0), (last + kTileRows - 1) / kTileRows));
+      float qf_next = g.lo < g.hi ? qf_of(g.lo) : 0.f;
       for (int i = g.lo; i < g.hi; ++i, ++n) {
         const int s = n & 1, rt = g.first + i;
-        lse_s[s * kTileRows + threadIdx.x] = lse_next;
         const float cf = fmaxf(qf_next * kf, 1e-37f);
-        if (i + 1 < g.hi) {
-          lse_next = lse_of(rt + 1);
-          qf_next = ws.qf[head() * ws.row_tiles + rt + 1];
-        }
-        sum_sync();
-        ok = ok && mbar_wait_bounded(&s_full[s], (n / 2) & 1u, abort_flag, status, limit);
+        if (i + 1 < g.hi) qf_next = qf_of(i + 1);
+        ok = ok && mbar_wait_bounded(&lse_full[n % kLseRing], (n / kLseRing) & 1u, abort_flag,
+                                     status, limit) &&
+             mbar_wait_bounded(&s_full[s], (n / 2) & 1u, abort_flag, status, limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         tc_fence_after_sync();
-        // rows before this one do not see the token
-        const int64_t need = static_cast<int64_t>(key - (g.s.n - g.s.m)) * G;
-        const int hide = static_cast<int>(max(
-            static_cast<int64_t>(0),
-            min(need - static_cast<int64_t>(rt) * kTileRows - part * 128, static_cast<int64_t>(128))));
-        const bool cut = __any_sync(0xffffffffu, hide > 0);
-        const float* lse = lse_s + s * kTileRows + part * 128;
+        const float* lse = lse_s + (n % kLseRing) * kTileRows + part * kSumCols;
         float p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 128; c += 64) {
-          float q[64];
-          tmem_ld_32cols(t_s + s * 256 + c, reinterpret_cast<uint32_t*>(q));
-          tmem_ld_32cols(t_s + s * 256 + c + 32, reinterpret_cast<uint32_t*>(q) + 32);
+        for (int c = 0; c < kSumCols; c += 32) {
+          float x[32];
+          tmem_ld_32cols(t_s + s * 256 + c, reinterpret_cast<uint32_t*>(x));
           tmem_ld_wait();
-          if (c == 64) {
+          if (c + 32 == kSumCols) {
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[s]);
           }
-          if (!cut) {
+          if (rt >= clear) {
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
+            for (int j = 0; j < 32; j += 4) {
               const float4 z = *reinterpret_cast<const float4*>(lse + c + j);
-              add2(p[0], p[1], ex2(fmaf(q[j], cf, -z.x)), ex2(fmaf(q[j + 1], cf, -z.y)));
-              add2(p[2], p[3], ex2(fmaf(q[j + 2], cf, -z.z)), ex2(fmaf(q[j + 3], cf, -z.w)));
+              fma2(x[j], x[j + 1], cf, z.x, z.y);
+              fma2(x[j + 2], x[j + 3], cf, z.z, z.w);
+              add2(p[0], p[1], ex2(x[j]), ex2(x[j + 1]));
+              add2(p[2], p[3], ex2(x[j + 2]), ex2(x[j + 3]));
             }
           } else {
+            const int64_t first = need - static_cast<int64_t>(rt) * kTileRows - part * kSumCols - c;
+            const int hide =
+                static_cast<int>(max(static_cast<int64_t>(0), min(first, static_cast<int64_t>(32))));
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              p[j & 3] += c + j < hide ? 0.f : ex2(fmaf(q[j], cf, -lse[c + j]));
+            for (int j = 0; j < 32; ++j)
+              p[j & 3] += j < hide ? 0.f : ex2(fmaf(x[j], cf, lse[c + j]));
           }
         }
         acc += (p[0] + p[1]) + (p[2] + p[3]);
       }
-      // ---- the two column halves, then the other CTAs' parts
+      // ---- the columns' parts, then the other CTAs'
       sum_sync();
-      if (part == 1) sum_s[threadIdx.x - 128] = acc;
+      if (part != 0) sum_s[threadIdx.x - 128] = acc;
       sum_sync();
       const size_t at = head() * a.weights_stride + key;
       const bool have = part == 0 && key < g.s.n;
       auto store = [&](float x) {
         if (have) a.weights_out[at] = (a.weights != nullptr ? a.weights[at] : 0.f) + x;
       };
-      if (part == 0) acc += sum_s[threadIdx.x];
+      if (part == 0) {
+#pragma unroll
+        for (int x = 0; x < kSumParts - 1; ++x) acc += sum_s[128 * x + threadIdx.x];
+      }
       if (g.s.m == 0) acc = 0.f;  // no rows: nothing has written these tiles
       if (g.lo == 0 && g.hi == g.units) {
         store(acc);
@@ -1466,7 +1499,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   l.kv_img = take(bh * l.key_tiles * kTileKeys * (2 * D + 16) * 2);
   l.parts = take(static_cast<size_t>(device_sm_count()) * 4 * (D + 2) * 128 * 4);
   if (weights) {
-    l.lse2 = take(static_cast<size_t>(tokens) * heads * 4);
+    l.lse2 = take(bh * l.row_tiles * kTileRows * 4);
     l.kbase = take((static_cast<size_t>(batch) + 1) * 4);
     l.kpre = take(static_cast<size_t>(batch) * (l.key_tiles + 1) * 4);
     l.sums = take(static_cast<size_t>(device_sm_count()) * 2 * 128 * 4);
