@@ -11,18 +11,22 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 
-// Orders as the number does; NaN is the lowest.
+// Orders as the number does (-0 as 0); NaN is the lowest.
 __device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(x + 0.f);
   if (x != x) return 0u;
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
 // One CTA a (head, sequence): the smallest kept key, then the kept indices by counts over the
-// tokens in order. Up to kHeld tokens that may go stay in registers, 16 a thread, and the key is
-// found two bits at a time by counting the keys at three candidates (16 rounds of one barrier:
-// 2 us for 8192 tokens; a histogram of key bytes meets itself in the few bins that steep weights
-// fill, 20 us). More tokens than that take four passes of such a histogram.
+// tokens in order. Up to kHeld tokens a thread that may go stay in registers; more are read again
+// from memory in every pass.
+//
+// The key is found by histograms of 1024 equal bins over the range that is left, from the lowest
+// to the highest key at first, until one bin's keys all stay or a bin is one key: two passes as a
+// rule, four at most. A selection from 8192 tokens takes 10 us, launch included, whether the weights
+// are uniform, steep or mostly equal. (Counting the keys at three candidates, two bits at a time,
+// took 17; histograms of the keys' bytes, whose few used bins all keys meet in, 28.)
 constexpr int kHeld = 16;
 
 struct Select {
@@ -32,68 +36,114 @@ struct Select {
   int lo, hi, k;  // of the tokens lo .. hi - 1, k stay
 };
 
+// Tokens with a key above `at` stay, with `all` those at it too, otherwise the first `ties` of
+// those.
+struct Cut {
+  uint32_t at, ties;
+  bool all;
+};
+
+// Inclusive sum over the lanes.
+__device__ __forceinline__ uint32_t scan(uint32_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// each(f) calls f with the keys of the thread's tokens, k >= 1 of all threads' stay.
+template <typename EACH>
+__device__ __forceinline__ Cut find_cut(uint32_t k, EACH each) {
+  __shared__ uint32_t hist[kSelectThreads];
+  __shared__ uint32_t warps[2][32];
+  __shared__ uint32_t found[3];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  each([&](uint32_t key) {
+    lo = min(lo, key);
+    hi = max(hi, key);
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    warps[0][warp] = lo;
+    warps[1][warp] = hi;
+  }
+  hist[tid] = 0u;
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, warps[0][lane]);
+  hi = __reduce_max_sync(0xffffffffu, warps[1][lane]);
+  for (uint32_t need = k;;) {
+    const uint32_t span = hi - lo;
+    const int shift = span < kSelectThreads ? 0 : 22 - __clz(span);
+    each([&](uint32_t key) {
+      if (key - lo <= span) atomicAdd(&hist[(key - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // from the highest bin down
+    const uint32_t bin = kSelectThreads - 1 - tid, count = hist[bin];
+    uint32_t upto = scan(count, lane);
+    if (lane == 31) warps[0][warp] = upto;
+    __syncthreads();
+    upto += __reduce_add_sync(0xffffffffu, lane < warp ? warps[0][lane] : 0u);
+    if (upto >= need && upto - count < need) {
+      found[0] = bin;
+      found[1] = upto - count;
+      found[2] = count;
+    }
+    hist[bin] = 0u;
+    __syncthreads();
+    need -= found[1];
+    lo += found[0] << shift;
+    hi = min(hi, lo + (1u << shift) - 1u);
+    if (found[2] == need) return {lo, 0u, true};
+    if (shift == 0) return {lo, need, false};
+  }
+}
+
 __device__ __forceinline__ void select_held(const Select& q) {
-  __shared__ uint32_t counts[2][32];
   __shared__ uint32_t before[kHeld * 32];  // tokens above (low half) and at the key, per warp
+  __shared__ uint32_t warps[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rounds = (q.hi - q.lo + kSelectThreads - 1) / kSelectThreads;
   float x[kHeld];
-  uint32_t key[kHeld];
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
     const int i = q.lo + tid + j * kSelectThreads;
     x[j] = i < q.hi ? q.w[i] : 0.f;
-    key[j] = i < q.hi ? order_key(x[j]) : 0u;
   }
-  // tokens that are not there have key 0 and never count: candidates are above it
-  uint32_t at = 0;
-  const uint32_t need = static_cast<uint32_t>(q.k);
-  for (int shift = 30, turn = 0; shift >= 0; shift -= 2, turn ^= 1) {
-    uint32_t c = 0;  // three counts of ten bits: a warp has 512 keys
+  const Cut cut = find_cut(static_cast<uint32_t>(q.k), [&](auto f) {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
       if (j >= rounds) break;
-#pragma unroll
-      for (uint32_t b = 1; b < 4; ++b) c += key[j] >= (at | (b << shift)) ? 1u << (10 * (b - 1)) : 0u;
+      if (q.lo + tid + j * kSelectThreads < q.hi) f(order_key(x[j]));
     }
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) counts[turn][warp] = c;
-    __syncthreads();
-    c = counts[turn][lane];
-    uint32_t bits = 0;
-#pragma unroll
-    for (uint32_t b = 1; b < 4; ++b)
-      if (__reduce_add_sync(0xffffffffu, (c >> (10 * (b - 1))) & 1023u) >= need) bits = b;
-    at |= bits << shift;
-  }
+  });
   // counts above and at the key, warp by warp in the tokens' order
   uint32_t above[kHeld], equal[kHeld];
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
     if (j >= rounds) break;
     const bool there = q.lo + tid + j * kSelectThreads < q.hi;
-    above[j] = __ballot_sync(0xffffffffu, there && key[j] > at);
-    equal[j] = __ballot_sync(0xffffffffu, there && key[j] == at);
+    const uint32_t key = order_key(x[j]);
+    const bool at = there && key == cut.at;
+    above[j] = __ballot_sync(0xffffffffu, (there && key > cut.at) || (at && cut.all));
+    equal[j] = __ballot_sync(0xffffffffu, at && !cut.all);
     if (lane == 0) before[j * 32 + warp] = __popc(above[j]) | (__popc(equal[j]) << 16);
   }
   __syncthreads();
-  if (warp == 0) {
-    uint32_t base = 0;
-    for (int j = 0; j < rounds; ++j) {
-      const uint32_t mine = before[j * 32 + lane];
-      uint32_t upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      before[j * 32 + lane] = base + upto - mine;
-      base += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) counts[0][0] = base & 0xFFFFu;  // all above
+  uint32_t mine = 0u, upto = 0u;
+  if (warp < kHeld) {
+    if (warp < rounds) mine = before[tid];
+    upto = scan(mine, lane);
+    if (lane == 31) warps[warp] = upto;
   }
   __syncthreads();
-  const uint32_t ties = need - counts[0][0];  // of the tokens at the key, the first ones stay
+  if (warp < rounds)
+    before[tid] = upto - mine + __reduce_add_sync(0xffffffffu, lane < warp ? warps[lane] : 0u);
+  __syncthreads();
   const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
@@ -102,8 +152,8 @@ __device__ __forceinline__ void select_held(const Select& q) {
     const uint32_t g = (b & 0xFFFFu) + __popc(above[j] & below);
     const uint32_t e = (b >> 16) + __popc(equal[j] & below);
     const bool is_above = (above[j] >> lane) & 1u, is_equal = (equal[j] >> lane) & 1u;
-    if (is_above || (is_equal && e < ties)) {
-      const uint32_t to = q.lo + g + min(e, ties);
+    if (is_above || (is_equal && e < cut.ties)) {
+      const uint32_t to = q.lo + g + min(e, cut.ties);
       q.kept[to] = q.lo + tid + j * kSelectThreads;
       q.w_out[to] = x[j];
     }
@@ -111,40 +161,18 @@ __device__ __forceinline__ void select_held(const Select& q) {
 }
 
 __device__ __forceinline__ void select_long(const Select& q) {
-  __shared__ uint32_t hist[256];
   __shared__ uint32_t warp_gt[32], warp_eq[32];
-  __shared__ uint32_t s_prefix, s_need;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    s_prefix = 0u;
-    s_need = static_cast<uint32_t>(q.k);
-  }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0u;
-    __syncthreads();
-    const uint32_t prefix = s_prefix;
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int i = q.lo + tid; i < q.hi; i += kSelectThreads) {
-      const uint32_t key = order_key(q.w[i]);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t need = s_need;
-      int bin = 255;
-      while (bin > 0 && hist[bin] < need) need -= hist[bin--];
-      s_need = need;
-      s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-    }
-    __syncthreads();
-  }
-  const uint32_t threshold = s_prefix, need = s_need;  // need of the keys equal to it stay
+  const Cut cut = find_cut(static_cast<uint32_t>(q.k), [&](auto f) {
+    for (int i = q.lo + tid; i < q.hi; i += kSelectThreads) f(order_key(q.w[i]));
+  });
   uint32_t gt_before = 0, eq_before = 0;
   for (int base = q.lo; base < q.hi; base += kSelectThreads) {
     const int i = base + tid;
     const float x = i < q.hi ? q.w[i] : 0.f;
     const uint32_t key = order_key(x);
-    const bool gt = i < q.hi && key > threshold, eq = i < q.hi && key == threshold;
+    const bool at = i < q.hi && key == cut.at;
+    const bool gt = (i < q.hi && key > cut.at) || (at && cut.all), eq = at && !cut.all;
     const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
     if (lane == 0) {
       warp_gt[warp] = __popc(bg);
@@ -157,10 +185,10 @@ __device__ __forceinline__ void select_long(const Select& q) {
                        __popc(bg & below);
     const uint32_t e = eq_before + __reduce_add_sync(0xffffffffu, lane < warp ? e_lane : 0u) +
                        __popc(be & below);
-    if (gt || (eq && e < need)) {
-      const uint32_t at = q.lo + g + min(e, need);
-      q.kept[at] = i;
-      q.w_out[at] = x;
+    if (gt || (eq && e < cut.ties)) {
+      const uint32_t to = q.lo + g + min(e, cut.ties);
+      q.kept[to] = i;
+      q.w_out[to] = x;
     }
     gt_before += __reduce_add_sync(0xffffffffu, g_lane);
     eq_before += __reduce_add_sync(0xffffffffu, e_lane);

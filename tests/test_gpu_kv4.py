@@ -370,6 +370,32 @@ def test_evict_from_a_long_cache(budget, first, recent):
     _check_evict(64, 64, 256, [17500, 16500], budget, first, recent)
 
 
+def _signed(g, n):
+    return np.where(np.arange(n) % 3 == 0, -0.0, g.integers(-2, 3, n) * 0.25)
+
+
+@pytest.mark.parametrize("n,budget", [(1100, 70), (1025, 1023), (16384, 900), (20000, 3)])
+@pytest.mark.parametrize("draw", [
+    lambda g, n: np.zeros(n), lambda g, n: np.exp(-80 * g.random(n)), _signed,
+    lambda g, n: np.full(n, np.inf), lambda g, n: np.full(n, np.nan),
+    lambda g, n: g.integers(0, 2, n) * 3e38, lambda g, n: g.integers(0, 1000, n) * 1e-42,
+    lambda g, n: 1 + np.arange(n) * 2.0 ** -23, lambda g, n: -g.random(n)])
+def test_evict_selects_from_any_weights(draw, n, budget):
+    g = np.random.default_rng(31)
+    w = draw(g, n).astype(np.float32)[None, None]
+    pages, page = (n + 255) // 256, 256
+    data = torch.zeros(pages + (budget + 255) // 256, 1, page // 16, ref.record_bytes(64, 64),
+                       dtype=torch.uint8, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    out_table = torch.arange(pages, len(data), dtype=torch.int32, device="cuda")[None]
+    got, _, w_out = w4.kv4_evict(data, table, _gpu(np.array([n], np.int32)), _gpu(w), out_table,
+                                 budget, n, 64, first=1, recent=1, group=64)
+    _ok()
+    kept = ref.evict(w, [n], budget, 1, 1)
+    assert np.array_equal(got.cpu().numpy(), kept)
+    assert np.array_equal(w_out.cpu().numpy()[0, 0, :budget], w[0, 0, kept[0, 0]], equal_nan=True)
+
+
 def _check_evict(D, group, page, lens, budget, first, recent):
     H, seed = 2, 14
     out_width = (budget + page - 1) // page
