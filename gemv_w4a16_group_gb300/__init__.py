@@ -33,6 +33,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -65,10 +66,9 @@ class W4A16Error(RuntimeError):
         self.status = status
 
 
-class _Kv4Cache(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
-    _fields_ += [(n, ctypes.c_int32) for n in ("pages", "kv_heads", "head_dim", "group",
-                                               "page_size", "batch", "table_width")]
+# kv4_cache: data, table, lens; pages, kv_heads, head_dim, group, page_size, batch, table_width (a
+# ctypes.Structure takes five times as long to fill)
+_kv4_struct = struct.Struct("PPP7i").pack
 
 
 def library_path() -> str:
@@ -82,7 +82,7 @@ def _load():
             "`python -m gemv_w4a16_group_gb300.build` on a machine with nvcc")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, S, U32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint32
-    L, F, C = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(_Kv4Cache)
+    L, F, C = ctypes.c_int64, ctypes.c_float, ctypes.c_char_p
     sigs = {
         "w4a16_quantize": [P, I, I, I, P, P, P, P],
         "w4a16_pack": [P, I, I, P, P],
@@ -637,6 +637,7 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, gro
 
 
 def _kv4(cache, table, lens, head_dim: int, group: int):
+    """(kv4_cache struct, batch, kv_heads)"""
     if cache.dim() != 4 or table.dim() != 2:
         raise ValueError("cache must have 4 dims (see kv4_cache) and table 2")
     pages, kv_heads, records, nbytes = cache.shape
@@ -644,9 +645,10 @@ def _kv4(cache, table, lens, head_dim: int, group: int):
         raise ValueError(f"cache has records of {nbytes} bytes, not those of head_dim {head_dim} "
                          f"in groups of {group}")
     batch, width = table.shape
-    return _Kv4Cache(_dev(cache, "cache", torch.uint8), _dev(table, "table", torch.int32),
-                     _dev(lens, "lens", torch.int32, (batch,)), pages, kv_heads, head_dim, group,
-                     16 * records, batch, width)
+    c = _kv4_struct(_dev(cache, "cache", torch.uint8), _dev(table, "table", torch.int32),
+                    _dev(lens, "lens", torch.int32, (batch,)), pages, kv_heads, head_dim, group,
+                    16 * records, batch, width)
+    return c, batch, kv_heads
 
 
 def _tokens(t: torch.Tensor, name: str):
@@ -690,14 +692,14 @@ def kv4_append(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
     cache. ``lens`` counts the new tokens, ``starts`` int32 [batch + 1] are their offsets; the
     entries of the new tokens in ``weights`` (fp32 [batch, kv_heads, length]) become 0."""
     tokens, heads, head_dim = k.shape
-    c = _kv4(cache, table, lens, head_dim, group)
+    c, batch, kv_heads = _kv4(cache, table, lens, head_dim, group)
     kp, ks = _tokens(k, "k")
     vp, vs = _tokens(v, "v")
-    if k.shape != v.shape or heads != c.kv_heads:
+    if k.shape != v.shape or heads != kv_heads:
         raise ValueError("k and v must have the same shape and the cache's heads")
-    wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
+    wp, wl = _kv4_weights(weights, "weights", batch, kv_heads)
     _check("kv4_append", _lib.kv4_append(
-        c, _dev(starts, "starts", torch.int32, (c.batch + 1,)), kp, ks, vp, vs, tokens, wp, wl,
+        c, _dev(starts, "starts", torch.int32, (batch + 1,)), kp, ks, vp, vs, tokens, wp, wl,
         _stream(stream)))
     return cache
 
@@ -706,14 +708,14 @@ def kv4_read(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, start
              tokens: int, head_dim: int, group: int = 64, k=None, v=None, stream=None):
     """(k, v) bf16 [tokens, kv_heads, head_dim]: the last starts[b + 1] - starts[b] tokens of
     each sequence as the cache holds them."""
-    c = _kv4(cache, table, lens, head_dim, group)
-    shape = (tokens, c.kv_heads, head_dim)
+    c, batch, kv_heads = _kv4(cache, table, lens, head_dim, group)
+    shape = (tokens, kv_heads, head_dim)
     if k is None:
         k = _new(cache, shape, torch.bfloat16, stream)
     if v is None:
         v = _new(cache, shape, torch.bfloat16, stream)
     _check("kv4_read", _lib.kv4_read(
-        c, _dev(starts, "starts", torch.int32, (c.batch + 1,)),
+        c, _dev(starts, "starts", torch.int32, (batch + 1,)),
         _dev(k, "k", torch.bfloat16, shape), _dev(v, "v", torch.bfloat16, shape), tokens,
         _stream(stream)))
     return k, v
@@ -738,11 +740,11 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
     Without a ``workspace`` (kv4_attention_workspace_bytes, zero-filled once) one is allocated
     and zero-filled for the call."""
     T, heads, head_dim = q.shape
-    c = _kv4(cache, table, lens, head_dim, group)
+    c, batch, kv_heads = _kv4(cache, table, lens, head_dim, group)
     qp, qs = _tokens(q, "q")
     if workspace is None:
         workspace = _new(q, kv4_attention_workspace_bytes(
-            c.batch, T, max_new, max_len, heads, c.kv_heads, head_dim, group,
+            batch, T, max_new, max_len, heads, kv_heads, head_dim, group,
             weights_out is not None), torch.uint8, stream)
         if isinstance(stream, torch.cuda.Stream):
             with torch.cuda.stream(stream):
@@ -751,14 +753,14 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
             workspace.zero_()
     if out is None:
         out = _new(q, (T, heads, head_dim), torch.bfloat16, stream)
-    wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
-    op, ol = _kv4_weights(weights_out, "weights_out", c.batch, c.kv_heads)
+    wp, wl = _kv4_weights(weights, "weights", batch, kv_heads)
+    op, ol = _kv4_weights(weights_out, "weights_out", batch, kv_heads)
     if weights is not None and wl != ol:
         raise ValueError("weights and weights_out must have the same shape")
     lp = None if lse is None else _dev(lse, "lse", torch.float32, (T, heads))
     ws_ptr, ws_bytes = _workspace(workspace)
     _check("kv4_attention", _lib.kv4_attention(
-        c, _dev(starts, "starts", torch.int32, (c.batch + 1,)), qp, qs,
+        c, _dev(starts, "starts", torch.int32, (batch + 1,)), qp, qs,
         _dev(out, "out", torch.bfloat16, (T, heads, head_dim)), lp, T, heads, max_new, max_len,
         head_dim ** -0.5 if scale is None else scale, wp, op, ol, ws_ptr, ws_bytes,
         _stream(stream)))
@@ -772,20 +774,20 @@ def kv4_evict(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weig
     """(kept int32 [batch, kv_heads, budget], new_lens int32 [batch], weights_out fp32
     [batch, kv_heads, >= budget]): the first, the last ``recent`` and the heaviest other tokens of
     each head move to the pages of ``out_table``."""
-    c = _kv4(cache, table, lens, head_dim, group)
-    wp, wl = _kv4_weights(weights, "weights", c.batch, c.kv_heads)
-    shape = (c.batch, c.kv_heads, budget)
+    c, batch, kv_heads = _kv4(cache, table, lens, head_dim, group)
+    wp, wl = _kv4_weights(weights, "weights", batch, kv_heads)
+    shape = (batch, kv_heads, budget)
     if kept is None:
         kept = _new(cache, shape, torch.int32, stream)
     if new_lens is None:
         new_lens = _new(cache, shape[:1], torch.int32, stream)
     if weights_out is None:
         weights_out = _new(cache, shape, torch.float32, stream)
-    op, ol = _kv4_weights(weights_out, "weights_out", c.batch, c.kv_heads)
-    if out_table.dim() != 2 or out_table.shape[0] != c.batch:
+    op, ol = _kv4_weights(weights_out, "weights_out", batch, kv_heads)
+    if out_table.dim() != 2 or out_table.shape[0] != batch:
         raise ValueError("out_table must be [batch, width]")
     _check("kv4_evict", _lib.kv4_evict(
         c, _dev(out_table, "out_table", torch.int32), out_table.shape[1], wp, wl, budget, first,
-        recent, max_len, _dev(kept, "kept", torch.int32, (c.batch, c.kv_heads, budget)),
-        _dev(new_lens, "new_lens", torch.int32, (c.batch,)), op, ol, _stream(stream)))
+        recent, max_len, _dev(kept, "kept", torch.int32, (batch, kv_heads, budget)),
+        _dev(new_lens, "new_lens", torch.int32, (batch,)), op, ol, _stream(stream)))
     return kept, new_lens, weights_out
