@@ -69,14 +69,33 @@ __device__ __forceinline__ void find(Places& p, const Kv4View& c, const int32_t*
   __syncthreads();
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+// Pairs of BF16; a NaN gives way to a number, and -0 is below 0.
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
   return y;
 }
-__device__ __forceinline__ float min3(float a, float b, float c) {
+__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+// (x, y) += a and (x, y) *= a, and |x| or the largest so far; a NaN stays.
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a) {
+  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\t"
+      "mul.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a));
+}
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
   float y;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -89,19 +108,20 @@ __device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) 
          __float_as_uint(a);
 }
 
-// Eight values of one group of `lanes` neighbouring lanes x 8 -> codes (plus kMagic) and the group's
-// scale | minimum word. The code is rint((x - m) / s) of the fp32 quotient; a product with 1 / s is
-// within 1e-5 of it and has the same code unless it lies that near to a tie.
+// Eight values of one group of `lanes` neighbouring lanes x 8 -> codes (plus kMagic) and the
+// group's scale | minimum word. The code is rint((x - m) / s) of the fp32 quotient; a product with
+// 1 / s is within 5e-6 of it and has the same code unless it lies that near to a tie. The quotient
+// needs no clamp: the minimum is exact, so it is 0 or more, and the scale's rounding leaves it
+// below 15.07.
 __device__ __forceinline__ void quantize8(const uint4& x, int lanes, float (&q)[8],
                                           uint32_t& param) {
-  const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
-                      bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
-  float mx = max3(max3(f[0], f[1], f[2]), max3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
-  float mn = min3(min3(f[0], f[1], f[2]), min3(f[3], f[4], f[5]), fminf(f[6], f[7]));
-  for (int o = 1; o < lanes; o <<= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-  }
+  const uint32_t top = max_pair(max_pair(x.x, x.y), max_pair(x.z, x.w));
+  const uint32_t low = min_pair(min_pair(x.x, x.y), min_pair(x.z, x.w)) ^ 0x80008000u;
+  // (maximum, less the minimum): one exchange for both
+  uint32_t ends = max_pair(__byte_perm(top, low, 0x5410), __byte_perm(top, low, 0x7632));
+  for (int o = 1; o < lanes; o <<= 1)
+    ends = max_pair(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+  const float mx = bf16_lo(ends), mn = -bf16_hi(ends);
   const uint32_t sb = __bfloat16_as_ushort(__float2bfloat16_rn((mx - mn) / 15.0f));
   const uint32_t mb = __bfloat16_as_ushort(__float2bfloat16_rn(mn));
   param = sb | (mb << 16);
@@ -109,15 +129,24 @@ __device__ __forceinline__ void quantize8(const uint4& x, int lanes, float (&q)[
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   if (s == 0.0f) inv = 0.0f;  // codes 0
-  // tiny and huge scales go the exact way
+  const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
+                      bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
+  // distance from the code; tiny and huge scales go the exact way
   float far = s == 0.0f || (s > 1e-30f && s < 1e30f) ? 0.f : 1.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __saturatef((f[i] - m) * (inv * (1.0f / 15.0f)));  // of 15
-    q[i] = fmaf(t, 15.0f, kMagic);
-    far = fmaxf(far, fabsf(fmaf(t, 15.0f, kMagic - q[i])));
+  for (int i = 0; i < 8; i += 2) {
+    float t0 = f[i], t1 = f[i + 1];
+    add2(t0, t1, -m, -m);
+    mul2(t0, t1, inv);
+    q[i] = t0;
+    q[i + 1] = t1;
+    add2(q[i], q[i + 1], kMagic, kMagic);
+    float c0 = q[i], c1 = q[i + 1];
+    add2(c0, c1, -kMagic, -kMagic);
+    add2(t0, t1, -c0, -c1);
+    far = max_abs(far, t0, t1);
   }
-  if (far > 0.4999f) {
+  if (!(far <= 0.49998f)) {  // also for a NaN: code 0
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf((f[i] - m) / s, 0.0f), 15.0f) + kMagic;
   }
