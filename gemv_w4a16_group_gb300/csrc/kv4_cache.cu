@@ -5,6 +5,11 @@
 // other way round. A block takes 64 tokens of one head. Where each of them lies (its sequence,
 // page and row, three loads that wait for one another) is found once, by a thread a token; then
 // D / 8 lanes take a token, with all of a thread's loads on their way before the first is used.
+//
+// 6571 tokens of 8 heads of 128 (34 MB): append 17.5 us, read 8.9 us, launches included (4.7 and 4 us
+// for one token). The read is bound by memory; the append by its instructions, 21 a value at first
+// and a dozen with the extremes and codes in pairs (19.5 us). 32 tokens a block, or more blocks an
+// SM at fewer registers, are within 3 % of this.
 #include "kv4_common.cuh"
 
 namespace w4k {

@@ -165,6 +165,16 @@ def test_several_new_tokens(D, group, page, heads, H, lens, new):
     _check_attention(cache, lens, new, heads, H, 4)
 
 
+@pytest.mark.parametrize("D,group,page", SHAPES)
+@pytest.mark.parametrize("heads,H,lens,new", [
+    # a few rows a key/value head, some of which do not see the last tokens of a record or its half
+    (2, 1, [90, 33, 18, 1], [2, 1, 2, 1]), (1, 1, [40, 17, 100, 16], [4, 3, 1, 2]),
+    (2, 2, [65, 16, 3000], [3, 4, 4]), (3, 3, [48, 32, 0], [4, 4, 0]), (3, 1, [47, 2], [1, 1])])
+def test_up_to_four_rows(D, group, page, heads, H, lens, new):
+    cache, _, _ = _fill(lens, H, D, group, page, 21)
+    _check_attention(cache, lens, new, heads, H, 21)
+
+
 @pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
 def test_long_sequence_is_split(D, group):
     lens = [5000, 1, 2047]
