@@ -638,13 +638,14 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, gro
 
 def _kv4(cache, table, lens, head_dim: int, group: int):
     """(kv4_cache struct, batch, kv_heads)"""
-    if cache.dim() != 4 or table.dim() != 2:
+    at, to = cache.shape, table.shape
+    if len(at) != 4 or len(to) != 2:
         raise ValueError("cache must have 4 dims (see kv4_cache) and table 2")
-    pages, kv_heads, records, nbytes = cache.shape
+    pages, kv_heads, records, nbytes = at
     if group > 0 and nbytes != 16 * (head_dim + 8 * (head_dim // group)):
         raise ValueError(f"cache has records of {nbytes} bytes, not those of head_dim {head_dim} "
                          f"in groups of {group}")
-    batch, width = table.shape
+    batch, width = to
     c = _kv4_struct(_dev(cache, "cache", torch.uint8), _dev(table, "table", torch.int32),
                     _dev(lens, "lens", torch.int32, (batch,)), pages, kv_heads, head_dim, group,
                     16 * records, batch, width)
@@ -671,9 +672,10 @@ def _tokens(t: torch.Tensor, name: str):
 def _kv4_weights(t, name: str, batch: int, kv_heads: int):
     if t is None:
         return None, 0
-    if t.dim() != 3 or t.shape[0] != batch or t.shape[1] != kv_heads:
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != batch or shape[1] != kv_heads:
         raise ValueError(f"{name} must be [{batch}, {kv_heads}, length]")
-    return _dev(t, name, torch.float32), t.shape[2]
+    return _dev(t, name, torch.float32), shape[2]
 
 
 def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
@@ -681,8 +683,16 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     block in the order of the stream it was allocated on)."""
     if isinstance(stream, torch.cuda.Stream):
         with torch.cuda.stream(stream):
-            return like.new_empty(shape, dtype=dtype)
-    return like.new_empty(shape, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=like.device)
+    return torch.empty(shape, dtype=dtype, device=like.device)  # half of new_empty's time
+
+
+def _result(t, name: str, like: torch.Tensor, shape, dtype, stream):
+    """(t, its address), with a new t for None."""
+    if t is None:
+        t = _new(like, shape, dtype, stream)
+        return t, t.data_ptr()
+    return t, _dev(t, name, dtype, shape)
 
 
 def kv4_append(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -710,14 +720,10 @@ def kv4_read(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, start
     each sequence as the cache holds them."""
     c, batch, kv_heads = _kv4(cache, table, lens, head_dim, group)
     shape = (tokens, kv_heads, head_dim)
-    if k is None:
-        k = _new(cache, shape, torch.bfloat16, stream)
-    if v is None:
-        v = _new(cache, shape, torch.bfloat16, stream)
+    k, kp = _result(k, "k", cache, shape, torch.bfloat16, stream)
+    v, vp = _result(v, "v", cache, shape, torch.bfloat16, stream)
     _check("kv4_read", _lib.kv4_read(
-        c, _dev(starts, "starts", torch.int32, (batch + 1,)),
-        _dev(k, "k", torch.bfloat16, shape), _dev(v, "v", torch.bfloat16, shape), tokens,
-        _stream(stream)))
+        c, _dev(starts, "starts", torch.int32, (batch + 1,)), kp, vp, tokens, _stream(stream)))
     return k, v
 
 
@@ -751,8 +757,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
                 workspace.zero_()
         else:
             workspace.zero_()
-    if out is None:
-        out = _new(q, (T, heads, head_dim), torch.bfloat16, stream)
+    out, out_p = _result(out, "out", q, (T, heads, head_dim), torch.bfloat16, stream)
     wp, wl = _kv4_weights(weights, "weights", batch, kv_heads)
     op, ol = _kv4_weights(weights_out, "weights_out", batch, kv_heads)
     if weights is not None and wl != ol:
@@ -761,7 +766,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
     ws_ptr, ws_bytes = _workspace(workspace)
     _check("kv4_attention", _lib.kv4_attention(
         c, _dev(starts, "starts", torch.int32, (batch + 1,)), qp, qs,
-        _dev(out, "out", torch.bfloat16, (T, heads, head_dim)), lp, T, heads, max_new, max_len,
+        out_p, lp, T, heads, max_new, max_len,
         head_dim ** -0.5 if scale is None else scale, wp, op, ol, ws_ptr, ws_bytes,
         _stream(stream)))
     return out
@@ -777,10 +782,8 @@ def kv4_evict(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weig
     c, batch, kv_heads = _kv4(cache, table, lens, head_dim, group)
     wp, wl = _kv4_weights(weights, "weights", batch, kv_heads)
     shape = (batch, kv_heads, budget)
-    if kept is None:
-        kept = _new(cache, shape, torch.int32, stream)
-    if new_lens is None:
-        new_lens = _new(cache, shape[:1], torch.int32, stream)
+    kept, kept_p = _result(kept, "kept", cache, shape, torch.int32, stream)
+    new_lens, new_p = _result(new_lens, "new_lens", cache, shape[:1], torch.int32, stream)
     if weights_out is None:
         weights_out = _new(cache, shape, torch.float32, stream)
     op, ol = _kv4_weights(weights_out, "weights_out", batch, kv_heads)
@@ -788,6 +791,5 @@ def kv4_evict(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weig
         raise ValueError("out_table must be [batch, width]")
     _check("kv4_evict", _lib.kv4_evict(
         c, _dev(out_table, "out_table", torch.int32), out_table.shape[1], wp, wl, budget, first,
-        recent, max_len, _dev(kept, "kept", torch.int32, (batch, kv_heads, budget)),
-        _dev(new_lens, "new_lens", torch.int32, (batch,)), op, ol, _stream(stream)))
+        recent, max_len, kept_p, new_p, op, ol, _stream(stream)))
     return kept, new_lens, weights_out
