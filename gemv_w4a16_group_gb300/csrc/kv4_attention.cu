@@ -18,11 +18,11 @@
 //
 // What bounds it: the cache is read once (D + 8 D / group bytes a token and head), at 4 heads a
 // key/value head about 8 operations a byte, so the aim is the memory's rate. 64 sequences of 8192
-// tokens, 32 heads on 8 of 128: 604 MB of cache and 67 MB of logits in 118 us, 5.7 TB/s (0.84 of a
-// copy's rate), the weights' kernel 18.7 us more; one of 131072 tokens 34.7 us, 4.1 TB/s, of which
-// some 8 us are the launch, the first copies and the join. Without the logits issue slots (45 % of
-// cycles), ALU (46 %) and DRAM (55 %) are all half busy: latency between the few warps that the
-// accumulators leave room for.
+// tokens, 32 heads on 8 of 128: 604 MB of cache in 105 us, 5.8 TB/s (0.85 of a copy's rate), with
+// weights 67 MB of logits more and read again, 132 us; one of 131072 tokens 32.8 us, 4.3 TB/s, of
+// which some 8 us are the launch, the first copies and the join. Issue slots (45 % of cycles), ALU
+// (46 %) and DRAM (55 %) are all half busy in 24 sequences of 8192: latency between the few warps
+// that the accumulators leave room for.
 //
 // Work split. A unit is 32 tokens of one (sequence, head, row tile); the units of all sequences
 // in order are cut into equal ranges, one a CTA, from the lengths on the device: ragged batches
@@ -117,6 +117,18 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 // Barrier of the computing warps.
 __device__ __forceinline__ void join_warps() {
   asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+}
+
+// bulk_load of bytes that the call reads once and that leave L2 first: the logits stay (64 sequences
+// of 8192 with weights 137.5 -> 132 us, 16 of them 48 -> 43; without weights 107.8 -> 105). A cache
+// that fits L2 and is read again at once is the other side: 4 sequences of 8192 17.7 -> 18.2 us.
+__device__ __forceinline__ void bulk_load_once(void* smem_dst, const void* gsrc, uint32_t bytes,
+                                               uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
 }
 
 struct Workspace {
@@ -302,6 +314,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
         if (j < records) page[j] = table[(unit * kUnitRecords + j) >> shift];
     };
     look();
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     uint64_t since = 0;  // when polling began to no avail
     bool ok = true;
     while (__any_sync(kLanes, more)) {
@@ -320,11 +334,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
         mbar_arrive_expect_tx(&full[stage], sum);
         uint8_t* dst = smem + stage * S::stage_bytes;
         if (shift > 0 && sum == kUnitRecords * R::kBytes) {
-          bulk_load(dst, src[0], kUnitRecords * R::kBytes, &full[stage]);  // one page
+          bulk_load_once(dst, src[0], kUnitRecords * R::kBytes, &full[stage], policy);  // one page
         } else {
 #pragma unroll
           for (int j = 0; j < kUnitRecords; ++j)
-            if (src[j] != nullptr) bulk_load(dst + j * R::kBytes, src[j], R::kBytes, &full[stage]);
+            if (src[j] != nullptr)
+              bulk_load_once(dst + j * R::kBytes, src[j], R::kBytes, &full[stage], policy);
         }
         ++given;
         unit += kWarps;
