@@ -190,6 +190,16 @@ def test_prompts_over_the_whole_gpu(heads, H, lens, new):
     _check_attention(cache, lens, new, heads, H, 16)
 
 
+@pytest.mark.parametrize("D,group", [(128, 128), (64, 32)])
+@pytest.mark.parametrize("heads,H,lens,new", [
+    # sequences beside a prompt that bring no token, hold none, or end in a tile's first row
+    (8, 2, [300, 70, 0, 40], [200, 0, 0, 1]), (4, 1, [257, 0, 129], [129, 0, 128]),
+    (3, 1, [43, 700], [43, 0])])
+def test_prompts_beside_idle_sequences(D, group, heads, H, lens, new):
+    cache, _, _ = _fill(lens, H, D, group, 64, 23)
+    _check_attention(cache, lens, new, heads, H, 23)
+
+
 def test_one_workspace_for_changing_lengths():
     """A workspace serves calls that differ in tokens and lengths; each equals a fresh one's."""
     lens, B, H, heads, D = [300, 70, 129], 3, 2, 4, 128
