@@ -201,6 +201,7 @@ struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStages = ring_stages(D, NG);
   static constexpr int kLower = (kWarps + 1) / 2;  // accumulators in shared memory at a time
+  static_assert(!PACK || kWarps * 4 <= kLower * kRows, "packed: all warps' four rows");
   static constexpr uint32_t stage_bytes = kUnitRecords * Kv4Record<D, NG>::kBytes;
   // the queries, [nt][D / 32][lane] 16 bytes, until the warps join; then accumulators,
   // [kLower][row][D]
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
     }
 
     // ---- join the warps: every warp under the rows' common maximum, the upper half's
-    // accumulators onto the lower half's, then those.
+    // accumulators onto the lower half's, then those (packed: all at once).
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -796,40 +797,65 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
         if (r == 0) sm_ml[warp * kRows + nt * 8 + 2 * c + i] = make_float2(mx[nt][i], l);
       }
     join_warps();
+    // an accumulator's dims 32 x + 4 r .. of column 2 c + i, under the rows' common maximum
+    auto share_of = [&](int nt, int i, float4 (&v)[NB]) {
+      const int row = nt * 8 + 2 * c + i;
+      float m = -INFINITY;
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      if ((warp < kLower) == (pass == 1)) {
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_ml[w * kRows + row].x);
+      const float w = mx[nt][i] == -INFINITY ? 0.f : ex2(mx[nt][i] - m);
+      // sums of codes' 2^-24, 2^-20, 2^-22, 2^-18 by dims, under 2^-ev
+      const float f = pow2f(min(ev[nt][i], 250) - 127) * 16777216.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = nt * 8 + 2 * c + i;
-            float m = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_ml[w * kRows + row].x);
-            const float w = mx[nt][i] == -INFINITY ? 0.f : ex2(mx[nt][i] - m);
-            // sums of codes' 2^-24, 2^-20, 2^-22, 2^-18 by dims, under 2^-ev
-            const float f = pow2f(min(ev[nt][i], 250) - 127) * 16777216.f;
-#pragma unroll
-            for (int x = 0; x < NB; ++x) {
-              const float k = corr[nt][x / (NB / NG)][i];
-              float4 v = make_float4(fmaf(o[nt][x][0][i], f, k),
-                                     fmaf(o[nt][x][0][i + 2], f * 0.0625f, k),
-                                     fmaf(o[nt][x][1][i], f * 0.25f, k),
-                                     fmaf(o[nt][x][1][i + 2], f * 0.015625f, k));
-              v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                           : make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
-              float4* at = reinterpret_cast<float4*>(
-                  sm_o + ((warp % kLower) * kRows + row) * D + 32 * x + 4 * r);
-              if (pass == 1 && warp + kLower < kWarps) {
-                const float4 t = *at;
-                v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
-              }
-              *at = v;
-            }
-          }
+      for (int x = 0; x < NB; ++x) {
+        const float k = corr[nt][x / (NB / NG)][i];
+        v[x] = make_float4(fmaf(o[nt][x][0][i], f, k), fmaf(o[nt][x][0][i + 2], f * 0.0625f, k),
+                           fmaf(o[nt][x][1][i], f * 0.25f, k),
+                           fmaf(o[nt][x][1][i + 2], f * 0.015625f, k));
+        v[x] = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                        : make_float4(v[x].x * w, v[x].y * w, v[x].z * w, v[x].w * w);
       }
+    };
+    if constexpr (PACK) {
+      // a row's two columns are two lanes' (c and c ^ 2): each sums one of the pair's rows
+      float4 keep[NB], give[NB];
+      share_of(0, 0, keep);
+      share_of(0, 1, give);
+      const int row = 2 * (c & 1) + (c >> 1);
+      auto sum_of = [&](float a, float b) {
+        const float mine = (c >> 1) ? b : a, other = (c >> 1) ? a : b;
+        return mine + __shfl_xor_sync(0xffffffffu, other, 2);
+      };
+#pragma unroll
+      for (int x = 0; x < NB; ++x)
+        *reinterpret_cast<float4*>(sm_o + (warp * 4 + row) * D + 32 * x + 4 * r) = make_float4(
+            sum_of(keep[x].x, give[x].x), sum_of(keep[x].y, give[x].y),
+            sum_of(keep[x].z, give[x].z), sum_of(keep[x].w, give[x].w));
       join_warps();
+    } else {
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+        if ((warp < kLower) == (pass == 1)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float4 v[NB];
+              share_of(nt, i, v);
+#pragma unroll
+              for (int x = 0; x < NB; ++x) {
+                float4* at = reinterpret_cast<float4*>(
+                    sm_o + ((warp % kLower) * kRows + nt * 8 + 2 * c + i) * D + 32 * x + 4 * r);
+                if (pass == 1 && warp + kLower < kWarps) {
+                  const float4 t = *at;
+                  v[x] = make_float4(v[x].x + t.x, v[x].y + t.y, v[x].z + t.z, v[x].w + t.w);
+                }
+                *at = v[x];
+              }
+            }
+        }
+        join_warps();
+      }
     }
     const bool whole = cur.lo == 0 && cur.hi == cur.w.chunks;
     auto part_of = [&](uint32_t cta, bool first) {
@@ -863,14 +889,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
       }
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kLower; ++w) {
-        const float4 t = *reinterpret_cast<const float4*>(sm_o + (w * kRows + row) * D + 4 * e);
+      for (int w = 0; w < (PACK ? kWarps : kLower); ++w) {
+        const float4 t =
+            *reinterpret_cast<const float4*>(sm_o + (w * (PACK ? 4 : kRows) + row) * D + 4 * e);
         v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
-        if constexpr (PACK) {
-          const float4 z =
-              *reinterpret_cast<const float4*>(sm_o + (w * kRows + row + 4) * D + 4 * e);
-          v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
-        }
       }
       if (whole) {
         store(row, e, v, m, l);
