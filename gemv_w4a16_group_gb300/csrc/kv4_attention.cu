@@ -18,9 +18,9 @@
 //
 // What bounds it: the cache is read once (D + 8 D / group bytes a token and head), at 4 heads a
 // key/value head about 8 operations a byte, so the aim is the memory's rate. 64 sequences of 8192
-// tokens, 32 heads on 8 of 128: 604 MB of cache in 105 us, 5.8 TB/s (0.85 of a copy's rate), with
-// weights 67 MB of logits more and read again, 132 us; one of 131072 tokens 32.8 us, 4.3 TB/s, of
-// which some 8 us are the launch, the first copies and the join. Issue slots (45 % of cycles), ALU
+// tokens, 32 heads on 8 of 128: 604 MB of cache in 102.6 us, 5.9 TB/s (0.87 of a copy's rate), with
+// weights 67 MB of logits more and read again, 130 us; one of 131072 tokens 31.6 us, 4.5 TB/s, of
+// which some 7 us are the launch, the first copies and the join. Issue slots (45 % of cycles), ALU
 // (46 %) and DRAM (55 %) are all half busy in 24 sequences of 8192: latency between the few warps
 // that the accumulators leave room for.
 //
@@ -53,8 +53,11 @@ constexpr int kUnitRecords = kUnit / 16;
 // Units that stand for what an item (sequence, head, row tile) costs beyond its own: loading its
 // queries, joining the warps, writing its rows. They come before its units in the list. Without
 // them the CTA that got the shortest sequences of a ragged batch (0, 1, 17 .. 4096 tokens, 32
-// sequences of 8 heads) took 42 us, its neighbours 10.
-constexpr int kItemCost = 12;
+// sequences of 8 heads) took 42 us, its neighbours 10. A unit is one of seven that run at once, so
+// an item's 4 us are many. At 12 / 26 / 40, us: that batch 17.4 / 16.9 / 18.4, 16 sequences of 100
+// to 16384 tokens 22.8 / 21.3 / 22.1, 8 of 300 to 8000 with 8 new tokens 41.7 (at 15) / 34.9 / 32.8,
+// 16 of 300 to 3001 with 5 (head size 64) 20.3 / 17.7 / 19.1, 64 of 8192 102.5 / 102.6 / 103.6.
+constexpr int kItemCost = 26;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
