@@ -1089,9 +1089,9 @@ cudaError_t by_rows(const Kv4AttentionArgs& a, cudaStream_t stream) {
 }
 
 // Above kFewRows the prompts' path takes over. It widens the whole cache to FP16 tiles first and
-// pads the rows to 128; here every 16 rows read the cache's codes again. 32 query heads on 8, us
-// at 32 / 36 rows (8 / 9 new tokens) with this path up to 32: 47 / 105 for 16 sequences of 2048,
-// 102 / 309 for 16 of 8192, 30 / 79 for one of 16384; a 16-row tile more costs 20, 50 and 13.
+// pads the rows to 128; here every 16 rows read the cache's codes again. 32 query heads on 8, us at
+// 80 and 96 rows here / 100 and 128 there: 94, 110 / 99, 97 for 16 sequences of 2048, 225, 267 /
+// 294, 286 for 16 of 8192, 42, 47 / 78, 77 for one of 16384.
 bool is_prompt(int max_new, int heads, int kv_heads) {
   return static_cast<int64_t>(max_new) * (heads / kv_heads) > kFewRows;
 }
