@@ -1,0 +1,182 @@
+"""Attention over the 4-bit key/value cache on the GPU: how near it is, and what no value, page or
+buffer may do to it. Against sums in 64 bits of the values that the cache holds.
+
+Bounds, from the arithmetic (a token's dim stands for c s + m, c a code of 0..15; "most" of it is
+15 s + |m|; of a row, L = |scale| times the largest sum over the dims of |q| most of a visible key):
+  * logits. A few rows: codes are FP16 subnormals 2^-22 c under an exponent of 2^-14, so a product's
+    sum loses up to 2^-24 of 2^-14 |q| a step, 2^-16 |q| in units of codes, over at most 2 D / 16
+    steps: 2^-12 |scale| max|q| s. Many rows: images exact or to 2^-22 of themselves. The rest is
+    fp32, at most sixteen roundings or truncations to 2^-24 of L. E = 2^-12 |scale| max|q| max s +
+    2^-20 L covers both;
+  * lse: E, and 2^-17 for the fp32 sum of exponentials that are within 2^-21 of themselves, and its
+    own rounding, 2^-22 |lse|;
+  * a weight: each probability by a factor within e^(+-2E), and 2^-16 of itself for exponentials
+    and sums; the sum with what was there before is rounded once, 2^-23 of it;
+  * out: rounded to BF16, 2^-9 of itself (and of itself with its error: 2^-8.9); probabilities (times
+    scales) rounded to FP16, 2^-12, a value's scale, minimum and sum likewise, each at most `most`:
+    2^-10 reach covers them, reach = sum p most; and (e^2E - 1) reach."""
+import numpy as np
+import pytest
+import torch
+
+import kv4_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+w4 = pytest.importorskip("gemv_w4a16_group_gb300") if torch.cuda.is_available() else None
+DEV = "cuda"
+FORMS = [(128, 64, 64), (128, 128, 16), (128, 32, 256), (64, 64, 16), (64, 32, 128)]
+
+
+def _gpu(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def _bf16(x):
+    return _gpu(np.asarray(x, np.float32)).bfloat16()
+
+
+def _starts(new):
+    return np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+
+
+def _held(x, group):
+    """(x_hat, most, largest scale a token), fp64, of fp32 [n, H, D]."""
+    q, s, m = ref.quantize(x, group)
+    most = np.repeat(15.0 * s.astype(np.float64) + np.abs(m.astype(np.float64)), group, axis=-1)
+    return ref.dequantize(q, s, m, group), most, s.astype(np.float64).max(-1)
+
+
+class Batch:
+    """Sequences whose keys and values are given as fp32 lists of [n, H, D], in a cache filled by
+    kv4_append (equal bit for bit to the reference's, as other tests check)."""
+
+    def __init__(self, ks, vs, group, page, seed=0):
+        ks, vs = [ref.bf16(k) for k in ks], [ref.bf16(v) for v in vs]
+        self.lens, self.group, self.page = [len(k) for k in ks], group, page
+        _, self.H, self.D = ks[0].shape
+        self.k, self.v = [_held(k, group) for k in ks], [_held(v, group) for v in vs]
+        need = [(n + page - 1) // page for n in self.lens]
+        order = np.random.default_rng(seed).permutation(sum(need) + 2).astype(np.int32)
+        self.table = np.full((len(ks), max(need) + 1), -1, np.int32)
+        at = 0
+        for b, c in enumerate(need):
+            self.table[b, :c] = order[at:at + c]
+            at += c
+        self.pages = len(order)
+        # stale bytes are NaN parameters
+        self.cache = torch.full((self.pages, self.H, page // 16, ref.record_bytes(self.D, group)),
+                                0xFF, dtype=torch.uint8, device=DEV)
+        w4.kv4_append(self.cache, _gpu(self.table), self.lens_t(), _gpu(_starts(self.lens)),
+                      _bf16(np.concatenate(ks)), _bf16(np.concatenate(vs)), group=group)
+        assert w4.w4a16_device_status() == 0
+
+    def lens_t(self):
+        return _gpu(np.array(self.lens, np.int32))
+
+
+def _check(batch, q, new, scale=None, weights=True, table=None, gone=None, rows=None, status=0,
+           copies=1):
+    """Runs the attention of q (fp32 [T, heads, D]) and holds it to the bounds. gone[b]: positions
+    that the call leaves out; rows: which of the T rows to look at; copies: the batch that many
+    times over in one call, on the same pages, so that a CTA's share is long."""
+    q = ref.bf16(q)
+    T, heads, D = q.shape
+    H, G = batch.H, heads // batch.H
+    scale = D ** -0.5 if scale is None else scale
+    starts = _starts(new)
+    table = batch.table if table is None else table
+    width = table.shape[1] * batch.page
+    before = np.random.default_rng(1).random((len(new), H, width)).astype(np.float32)
+    lse_t = torch.full((copies * T, heads), 9.0, device=DEV)
+    out_t = torch.full((copies * T, heads, D), 9.0, dtype=torch.bfloat16, device=DEV)
+    w_t = torch.full((copies * len(new), H, width), 7.0, device=DEV) if weights else None
+    w4.kv4_attention(_bf16(np.tile(q, (copies, 1, 1))), batch.cache,
+                     _gpu(np.tile(table, (copies, 1))), batch.lens_t().repeat(copies),
+                     _gpu(_starts(list(new) * copies)), max(max(batch.lens), 1), max(new),
+                     group=batch.group, scale=scale, lse=lse_t, out=out_t,
+                     weights=_gpu(np.tile(before, (copies, 1, 1))) if weights else None,
+                     weights_out=w_t)
+    assert w4.w4a16_device_status() == status
+
+    def each(t):  # the copies first
+        return t.double().cpu().numpy().reshape(copies, t.shape[0] // copies, *t.shape[1:])
+
+    got, lse_g = each(out_t), each(lse_t)
+    w_g = each(w_t) if weights else None
+    look = np.ones(T, bool) if rows is None else rows
+    for b, n in enumerate(batch.lens):
+        mine = slice(starts[b], starts[b + 1])
+        m = new[b]
+        hide = np.arange(n) > np.arange(n - m, n)[:, None]
+        if gone is not None:
+            hide[:, gone[b]] = True
+        w, w_tol = np.zeros((H, n)), np.zeros((H, n))
+        for h in range(heads):
+            g = h // G
+            k, k_most, k_s = (x[:, g] for x in batch.k[b])
+            v, v_most, _ = (x[:, g] for x in batch.v[b])
+            x = q[mine, h].astype(np.float64)
+            s = np.where(hide, -np.inf, scale * (x @ k.T))
+            some = ~hide.all(1) if n else np.zeros(m, bool)
+            top = s.max(1, keepdims=True, initial=-np.inf)
+            top[~some] = 0
+            e = np.exp(s - top)
+            total = e.sum(1, keepdims=True)
+            total[~some] = 1
+            p, lse = e / total, (top + np.log(total))[:, 0]
+            if m and n:
+                L = abs(scale) * np.where(hide, 0, np.abs(x) @ k_most.T).max(1)
+                E = (2.0 ** -12 * abs(scale) * np.abs(x).max(1)
+                     * np.where(hide, 0, k_s[None]).max(1) + 2.0 ** -20 * L)
+            else:
+                E = np.zeros(m)
+            grow = np.expm1(2 * E)
+            want, reach = p @ v, p @ v_most
+            ok = look[mine]
+            tol = 2.0 ** -8.9 * np.abs(want) + (2.0 ** -10 + grow)[:, None] * reach
+            here, z = got[:, mine, h], lse_g[:, mine, h]
+            assert np.isfinite(here[:, ok]).all()
+            over = (np.abs(here - want) - tol)[:, ok]
+            assert (over <= 0).all(), (b, h, over.max(), np.abs(want).max())
+            assert np.isneginf(z[:, ~some]).all() and (here[:, ~some] == 0).all()
+            over = (np.abs(z - lse) - (E + 2.0 ** -17 + 2.0 ** -22 * np.abs(lse)))[:, some & ok]
+            assert (over <= 0).all(), (b, h, over.max())
+            w[g] += p[some].sum(0)
+            w_tol[g] += ((grow + 2.0 ** -16)[:, None] * p)[some].sum(0)
+        if weights:
+            old = before[b].astype(np.float64)
+            assert (w_g[:, b, :, n:] == 7.0).all()
+            if rows is None:
+                d = np.abs(w_g[:, b, :, :n] - old[:, :n] - w)
+                assert (d <= w_tol + 2.0 ** -23 * (old[:, :n] + w)).all(), d.max()
+
+
+def _normal(g, n, H, D, wide=True):
+    chan = np.where(g.random((H, D)) < 0.05, 4.0, 1.0) if wide else 1.0
+    return g.standard_normal((n, H, D)) * chan, g.standard_normal((n, H, D))
+
+
+def _random(lens, H, D, group, page, seed):
+    g = np.random.default_rng(seed)
+    kv = [_normal(g, n, H, D) for n in lens]
+    return Batch([k for k, _ in kv], [v for _, v in kv], group, page, seed), g
+
+
+# ---- nearness, with and without weights ---------------------------------------------------
+@pytest.mark.parametrize("D,group,page", FORMS)
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("heads,H,lens,new", [
+    (4, 1, [1], [1]), (4, 2, [17, 1, 64, 129], [1, 1, 1, 1]), (12, 2, [900, 3], [1, 1]),
+    (4, 1, [700, 40], [5, 8]), (8, 4, [333, 1000], [4, 1]), (3, 1, [90, 2], [30, 2]),
+    (4, 1, [150, 60], [150, 1]), (6, 2, [700, 257, 5], [300, 257, 5])])
+def test_out_lse_and_weights(D, group, page, weights, heads, H, lens, new):
+    batch, g = _random(lens, H, D, group, page, 40)
+    _check(batch, g.standard_normal((sum(new), heads, D)), new, weights=weights)
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("new", [1, 9, 130])
+def test_a_long_sequence(weights, new):
+    batch, g = _random([9000], 2, 128, 64, 64, 41)
+    _check(batch, g.standard_normal((new, 8, 128)), [new], weights=weights)
