@@ -60,6 +60,9 @@ constexpr int kUnitRecords = kUnit / 16;
 constexpr int kItemCost = 26;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// The least exponent field that products come under, whatever the V scales (0 where a group's values
+// are equal): 2^8 times 2^(127 - this) is still a number, and 0 times it 0.
+constexpr int kLeastEv = 16;
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
         unscale[nt][i] = sm_row[NG * kRows + row];
         mx[nt][i] = -INFINITY;
         sum[nt][i] = 0.f;
-        ev[nt][i] = 0;
+        ev[nt][i] = kLeastEv;
         down[nt][i] = 0.f;
       }
 #pragma unroll

@@ -180,3 +180,34 @@ def test_out_lse_and_weights(D, group, page, weights, heads, H, lens, new):
 def test_a_long_sequence(weights, new):
     batch, g = _random([9000], 2, 128, 64, 64, 41)
     _check(batch, g.standard_normal((new, 8, 128)), [new], weights=weights)
+
+
+# ---- values of one size in a group --------------------------------------------------------
+def _rising(n, H, D, a_unit, seed):
+    """Keys whose logits under q near 1 rise by a_unit (base 2) in 32 tokens."""
+    step = a_unit / 32 / (D ** 0.5 * 1.4426950408889634)
+    g = np.random.default_rng(seed)
+    return np.arange(n)[:, None, None] * step + 1e-3 * g.standard_normal((n, H, D)), g
+
+
+@pytest.mark.parametrize("D,group,value", [(128, 64, 0.0), (128, 128, 1.0), (64, 32, 1.0),
+                                           (64, 64, 0.0), (128, 32, -3e-38)])
+@pytest.mark.parametrize("a_unit", [0.2, 0.6, 1.1])
+@pytest.mark.parametrize("heads", [4, 8, 16])
+def test_constant_values(D, group, value, a_unit, heads):
+    """Scales of 0 and logits that rise from unit to unit, in a batch that gives every warp several
+    units of a segment."""
+    n, B, H = 2048, 32, 2
+    k, g = _rising(n, H, D, a_unit, 42)
+    batch = Batch([k], [np.full((n, H, D), value)], group, 64)
+    q = 1 + 0.02 * g.standard_normal((1, heads, D))
+    # every sequence of the batch reads the same pages
+    table = _gpu(np.repeat(batch.table, B, 0))
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    out = w4.kv4_attention(_bf16(np.repeat(q, B, 0)), batch.cache, table, lens,
+                           _gpu(_starts([1] * B)), n, 1, group=group).float()
+    assert w4.w4a16_device_status() == 0
+    want = torch.tensor(value).bfloat16().item()
+    # probabilities sum to 1 within 2^-17 and the BF16 value is rounded to again
+    assert torch.isfinite(out).all()
+    assert ((out - want).abs() <= 2.0 ** -8 * abs(want)).all()
