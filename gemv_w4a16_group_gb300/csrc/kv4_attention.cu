@@ -60,8 +60,16 @@ constexpr int kUnitRecords = kUnit / 16;
 constexpr int kItemCost = 26;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// The least exponent field that products come under, whatever the V scales (0 where a group's values
-// are equal): 2^8 times 2^(127 - this) is still a number, and 0 times it 0.
+// Probabilities times V scales, as the second product's FP16 operand. A row's products come under
+// 2^-e, e the exponent of the largest one that it has met (at most 1 times a scale, while the
+// running maximum is exact), and have these bits to spare above it: the running maximum lags by up to
+// 2^kLag, a scale may be 2^kScaleLag times the largest product, and what is left lifts the products,
+// so that they are rounded to 2^-12 of themselves or 2^-28 of the largest. (Under the largest scale
+// that the row had met, attended or not, one token of values 2^20 times the others' took 20 bits
+// of theirs.)
+constexpr int kLag = 4, kScaleLag = 8, kLift = 15 - kLag - kScaleLag;
+// The least e (exponent field): 2^kLag times 2^(127 + kLift - e) is still a number, and 0 times it 0
+// where a group's values are equal and their scale is 0.
 constexpr int kLeastEv = 16;
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
@@ -455,8 +463,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
     join_warps();
     float sq[NT][NG][2], unscale[NT][2];  // of rows 2c, 2c + 1
     float o[NT][NB][2][4], corr[NT][NG][2], mx[NT][2], sum[NT][2];
-    int ev[NT][2];         // exponent field of the largest V scale that the rows have met
-    float down[NT][2];     // 2^-ev
+    int ev[NT][2];         // exponent field of the rows' largest products under the maximum
+    float down[NT][2];     // 2^(kLift - ev)
     float cap = -1.f;      // V scales up to this may come under every row's 2^-ev
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -588,9 +596,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
           hide_and_keep(j);
         }
       }
-      // ---- running maximum, and the largest V scale's exponent among the visible tokens. Both
-      // may lag, by 2^8 and 2^6: p times a scale stays an FP16 number, and most units need
-      // neither the reductions over the warp nor a rescale.
+      // ---- running maximum, and the largest product's exponent under it. Both may lag: p times a
+      // scale stays an FP16 number, and most units need neither the reductions over the warp nor a
+      // rescale.
       constexpr int kScales = kUnitRecords * NG * 16;
       auto scale_bits = [&](int x) {
         return lds32(base + (x / (16 * NG)) * R::kBytes + R::kVParams + (x % (16 * NG)) * 4) &
@@ -609,39 +617,15 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
 #pragma unroll
             for (int j = 1; j < kSets; ++j)
               v = fmaxf(v, fmaxf(s[j][nt][i], s[j][nt][i + 2]));
-            fits = fits && v * unscale[nt][i] <= mx[nt][i] + 8.f;
+            fits = fits && v * unscale[nt][i] <= mx[nt][i] + kLag;
           }
       }
       if (kMasked || !__all_sync(0xffffffffu, fits)) {
-        uint32_t unit_top = 0;  // of all the unit's scales
-        if constexpr (!kMasked) {
-#pragma unroll
-          for (int x = 0; x < kScales; x += 32) {
-            const uint32_t sc = scale_bits(x + lane);
-            unit_top = max(unit_top, sc >= 0x7F80u ? 0u : sc);
-          }
-          unit_top = __reduce_max_sync(0xffffffffu, unit_top);
-        }
         int least = 255;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            uint32_t top = unit_top;
-            if constexpr (kMasked) {
-#pragma unroll
-              for (int j = 0; j < kSets; ++j)
-#pragma unroll
-                for (int x = 0; x < 2 * NG; ++x) {
-                  if (s[j][nt][i + 2 * (x & 1)] == -INFINITY) continue;
-                  const uint32_t sc = lds32(base + (PACK ? half : j) * R::kBytes + R::kVParams +
-                                            (16 * (x / 2) + r + 8 * (x & 1)) * 4) & 0xFFFFu;
-                  if (sc < 0x7F80u) top = max(top, sc);
-                }
-              top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
-              top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
-              top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            }
             float v = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
 #pragma unroll
             for (int j = 1; j < kSets; ++j)
@@ -651,12 +635,34 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             if constexpr (PACK) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
             const float now = fmaxf(mx[nt][i], v * unscale[nt][i]);
-            const int ev_now = max(ev[nt][i], static_cast<int>(top >> 7));
+            uint32_t top = 0;  // largest product, fp32 bits
+#pragma unroll
+            for (int j = 0; j < kSets; ++j)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float x = s[j][nt][i + 2 * u];
+                if (kMasked && x == -INFINITY) continue;
+                uint32_t sc = 0;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                  const uint32_t z = lds32(base + (PACK ? half : j) * R::kBytes + R::kVParams +
+                                           (16 * g + r + 8 * u) * 4) & 0xFFFFu;
+                  if (z < 0x7F80u) sc = max(sc, z);
+                }
+                top = max(top, __float_as_uint(ex2(fmaf(x, unscale[nt][i], -now)) *
+                                               __uint_as_float(sc << 16)));
+              }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
             const float alpha = now == -INFINITY ? 1.f : ex2(mx[nt][i] - now);
+            // the largest product so far is alpha times what it was
+            const int before = ev[nt][i] + static_cast<int>(__float_as_uint(alpha) >> 23) - 127;
+            const int ev_now = max(max(before, static_cast<int>(top >> 23)), kLeastEv);
             const float beta = alpha * ex2(static_cast<float>(ev[nt][i] - ev_now));
             mx[nt][i] = now;
             ev[nt][i] = ev_now;
-            down[nt][i] = pow2f(127 - min(ev_now, 250));
+            down[nt][i] = pow2f(127 + kLift - min(ev_now, 250));
             least = min(least, ev_now);
             sum[nt][i] *= alpha;
 #pragma unroll
@@ -670,7 +676,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
               }
           }
         least = __reduce_min_sync(0xffffffffu, least);
-        cap = pow2f(min(least - 121, 127));
+        cap = pow2f(min(least + kScaleLag - 127, 127));
       }
       // ---- P V
       auto probabilities = [&](int j, float (&p)[NT][4], float (&pd)[NT][4]) {
@@ -810,14 +816,15 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_ml[w * kRows + row].x);
       const float w = mx[nt][i] == -INFINITY ? 0.f : ex2(mx[nt][i] - m);
-      // sums of codes' 2^-24, 2^-20, 2^-22, 2^-18 by dims, under 2^-ev
-      const float f = pow2f(min(ev[nt][i], 250) - 127) * 16777216.f;
+      // sums of codes' 2^-24, 2^-20, 2^-22, 2^-18 by dims, under 2^(kLift - ev)
+      const float f = pow2f(min(ev[nt][i], 250) - 127), two = pow2f(24 - kLift);
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
         const float k = corr[nt][x / (NB / NG)][i];
-        v[x] = make_float4(fmaf(o[nt][x][0][i], f, k), fmaf(o[nt][x][0][i + 2], f * 0.0625f, k),
-                           fmaf(o[nt][x][1][i], f * 0.25f, k),
-                           fmaf(o[nt][x][1][i + 2], f * 0.015625f, k));
+        v[x] = make_float4(fmaf(o[nt][x][0][i] * two, f, k),
+                           fmaf(o[nt][x][0][i + 2] * (two * 0.0625f), f, k),
+                           fmaf(o[nt][x][1][i] * (two * 0.25f), f, k),
+                           fmaf(o[nt][x][1][i + 2] * (two * 0.015625f), f, k));
         v[x] = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                         : make_float4(v[x].x * w, v[x].y * w, v[x].z * w, v[x].w * w);
       }

@@ -211,3 +211,71 @@ def test_constant_values(D, group, value, a_unit, heads):
     # probabilities sum to 1 within 2^-17 and the BF16 value is rounded to again
     assert torch.isfinite(out).all()
     assert ((out - want).abs() <= 2.0 ** -8 * abs(want)).all()
+
+
+# ---- values of any size -------------------------------------------------------------------
+# (heads on two, new tokens, copies): a call that is cut to the last unit, and one whose CTAs go
+# through whole sequences
+PATHS = [(8, 1, 1), (8, 1, 60), (8, 4, 60), (4, 30, 60)]
+
+
+@pytest.mark.parametrize("heads,new,copies", PATHS)
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("size", [1e-30, 1e-3, 1e-2, 1e30, 1e35])
+def test_values_of_one_size(heads, new, copies, D, group, size):
+    g = np.random.default_rng(43)
+    k, v = _normal(g, 900, 2, D)
+    _check(Batch([k], [v * size], group, 64), g.standard_normal((new, heads, D)), [new],
+           copies=copies)
+
+
+@pytest.mark.parametrize("heads,new,copies", PATHS)
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3])
+@pytest.mark.parametrize("zeros", [[(0, 128)], [(256, 512)], [(0, 128), (300, 301), (640, 768)]])
+def test_tiles_of_zeros(heads, new, copies, D, group, size, zeros):
+    g = np.random.default_rng(44)
+    k, v = _normal(g, 900, 2, D)
+    v *= size
+    for lo, hi in zeros:
+        v[lo:hi] = 0
+    _check(Batch([k], [v], group, 64), g.standard_normal((new, heads, D)), [new], copies=copies)
+
+
+def _with_unlikely(g, n, D, at, size, far):
+    """Keys under which the tokens `at` have logits `far` nats below the others', and values that
+    are `size` times the others' there. Queries are near 1 in half of the dims."""
+    k, v = _normal(g, n, 2, D, wide=False)
+    k[at] = -far / (D ** 0.5 / 2) + 0.1 * k[at]
+    k[..., D // 2:] = 0.5 * g.standard_normal((n, 2, D // 2))
+    v[at] *= size
+    return k, v
+
+
+def _near_one(g, new, heads, D):
+    q = 1 + 0.05 * g.standard_normal((new, heads, D))
+    q[..., D // 2:] = 0.3 * g.standard_normal((new, heads, D // 2))
+    return q
+
+
+@pytest.mark.parametrize("heads,new,copies", PATHS)
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("at", [[3], [400], [5, 600]])
+@pytest.mark.parametrize("power", [14, 20, 30])
+def test_a_large_value_that_is_hardly_attended(heads, new, copies, D, group, at, power):
+    """A token whose values are 2^power times the others' and whose probability is e^-60 or less
+    takes no bits from the others'."""
+    g = np.random.default_rng(45)
+    k, v = _with_unlikely(g, 900, D, at, 2.0 ** power, 60.0)
+    _check(Batch([k], [v], group, 64), _near_one(g, new, heads, D), [new], copies=copies)
+
+
+@pytest.mark.parametrize("heads,new,copies", PATHS)
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+def test_a_first_token_with_most_of_the_weight_and_small_values(heads, new, copies, D, group):
+    g = np.random.default_rng(46)
+    k, v = _normal(g, 900, 2, D, wide=False)
+    k[0] = 0.8 + 0.1 * k[0]
+    v[0] *= 2.0 ** -10
+    _check(Batch([k], [v], group, 64), 1 + 0.3 * g.standard_normal((new, heads, D)), [new],
+           copies=copies)
