@@ -50,6 +50,7 @@ constexpr int ctas_per_sm(int d, int nt) { return d * nt <= 128 ? 2 : 1; }
 constexpr int ring_stages(int d, int ng) { return d == 128 && ng == 4 ? 2 : 3; }
 constexpr int kUnit = 32;  // tokens
 constexpr int kUnitRecords = kUnit / 16;
+constexpr uint32_t kAllRecords = (1u << kUnitRecords) - 1u;
 // Units that stand for what an item (sequence, head, row tile) costs beyond its own: loading its
 // queries, joining the warps, writing its rows. They come before its units in the list. Without
 // them the CTA that got the shortest sequences of a ragged batch (0, 1, 17 .. 4096 tokens, 32
@@ -224,7 +225,8 @@ struct Shape {
   static constexpr uint32_t ml_off = o_off + kLower * kRows * D * 4;  // [warp][row] (m, l)
   static constexpr uint32_t row_off = ml_off + kWarps * kRows * 8;   // [row] (sums of q, unscale)
   static constexpr uint32_t bar_off = row_off + kRows * (NG + 1) * 4;
-  static constexpr uint32_t misc_off = bar_off + 2 * kWarps * kStages * 8;
+  static constexpr uint32_t have_off = bar_off + 2 * kWarps * kStages * 8;  // [warp][stage]
+  static constexpr uint32_t misc_off = have_off + kWarps * kStages * 4;
   static constexpr uint32_t total = misc_off + 16;
   static constexpr int part_floats = kRows * D + 2 * kRows;
   static_assert(total <= (ctas_per_sm(D, NT) == 2 ? 113u : 227u) * 1024u, "shared memory");
@@ -240,6 +242,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bar_off);  // [warp][stage]
   uint64_t* empty = full + kWarps * kStages;
+  // bit j: a stage holds its unit's record j (not past the length, nor of a page out of range)
+  volatile uint32_t* stage_has = reinterpret_cast<uint32_t*>(smem + S::have_off);
   volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + S::misc_off);
   volatile uint32_t* arrived = abort_flag + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -339,16 +343,25 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
                                  mbar_test(&empty[stage], (given / kStages - 1) & 1u));
       if (free) {
         const uint8_t* src[kUnitRecords];
-        uint32_t sum = 0;
+        uint32_t has = 0;
 #pragma unroll
         for (int j = 0; j < kUnitRecords; ++j) {
           src[j] = j < records ? kv4_in_page(a.c, page[j], at.h, unit * kUnitRecords + j, R::kBytes)
                                : nullptr;
-          if (src[j] != nullptr) sum += R::kBytes;
+          if (src[j] != nullptr) has |= 1u << j;
         }
-        mbar_arrive_expect_tx(&full[stage], sum);
         uint8_t* dst = smem + stage * S::stage_bytes;
-        if (shift > 0 && sum == kUnitRecords * R::kBytes) {
+        stage_has[stage] = has;
+        if (has != (1u << records) - 1u) {
+          // a page out of range: V scales of NaN send the unit to the masked body (64 sequences of
+          // 8192 with weights 132.8 us; 133.4 with a look at stage_has for every unit)
+          for (int j = 0; j < records; ++j)
+            for (int x = 0; !((has >> j) & 1u) && x < 16 * NG; ++x)
+              reinterpret_cast<uint32_t*>(dst + j * R::kBytes + R::kVParams)[x] = 0xFFFFFFFFu;
+          fence_proxy_async();  // before the copies that this place holds later
+        }
+        mbar_arrive_expect_tx(&full[stage], __popc(has) * R::kBytes);
+        if (shift > 0 && has == kAllRecords) {
           bulk_load_once(dst, src[0], kUnitRecords * R::kBytes, &full[stage], policy);  // one page
         } else {
 #pragma unroll
@@ -492,9 +505,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
     // first key that some row of the tile does not see
     const int clear = rows > 0 ? seq.n - seq.m + row0 / G + 1 : 0;
 
-    auto compute = [&](auto mask, uint32_t base, int key0) {
+    // Records of bits `has`; false, with nothing done, if the body without a mask met a unit that
+    // does not have all of them.
+    auto compute = [&](auto mask, uint32_t base, int key0, volatile uint32_t* stage_bits) {
       constexpr bool kMasked = decltype(mask)::value;
-      const int records = kMasked ? min(kUnitRecords, (seq.n - key0 + 15) / 16) : kUnitRecords;
+      const uint32_t has = kMasked ? *stage_bits : kAllRecords;
       // ---- logits, times 1 / unscale. Set j holds record j's tokens (packed: the lane's record's)
       constexpr int kSets = PACK ? 1 : kUnitRecords;
       const int half = c >> 1;  // packed: this lane's record
@@ -518,7 +533,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
             const int row = PACK ? 2 * (c & 1) + (i & 1) : nt * 8 + 2 * c + (i & 1);
             const int key = key0 + 16 * (PACK ? half : j) + r + (i >= 2 ? 8 : 0);
             if constexpr (kMasked) {
-              if (key > (row < rows ? seq.n - seq.m + (row0 + row) / G : -1))
+              if (key > (row < rows ? seq.n - seq.m + (row0 + row) / G : -1) ||
+                  !((has >> (PACK ? half : j)) & 1u))
                 s[j][nt][i] = -INFINITY;
             }
             if constexpr (LOGITS) {
@@ -560,11 +576,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
       } else {
 #pragma unroll
         for (int j = 0; j < kUnitRecords; ++j) {
-          if (kMasked && j >= records) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s[j][nt][i] = -INFINITY;
+          if (kMasked && !((has >> j) & 1u)) {
+            hide_and_keep(j);
             continue;
           }
           const uint32_t rec = base + j * R::kBytes;
@@ -621,6 +634,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
           }
       }
       if (kMasked || !__all_sync(0xffffffffu, fits)) {
+        if (!kMasked && *stage_bits != kAllRecords) return false;
         int least = 255;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -743,7 +757,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
       } else {
 #pragma unroll
         for (int j = 0; j < kUnitRecords; ++j) {
-          if (kMasked && j >= records) continue;
+          if (kMasked && !((has >> j) & 1u)) continue;
           const uint32_t rec = base + j * R::kBytes;
           uint32_t w0[NB], w1[NB];
           load_words<NB>(rec + R::kV + ((c * 8 + r) * NB) * 4, w0);
@@ -769,6 +783,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
           }
         }
       }
+      return true;
     };
 
 #pragma unroll 1
@@ -782,12 +797,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
       if (!ok) continue;
       const uint32_t base = ring + stage * S::stage_bytes;
       const int key0 = unit * kUnit;
-      const bool masked = key0 + kUnit > clear;
+      volatile uint32_t* bits = &stage_has[warp * kStages + stage];
       // two bodies: the one that every unit but a sequence's last takes has no branches
-      if (masked)
-        compute(std::true_type(), base, key0);
-      else
-        compute(std::false_type(), base, key0);
+      if (key0 + kUnit > clear || !compute(std::false_type(), base, key0, bits))
+        compute(std::true_type(), base, key0, bits);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[warp * kStages + stage]);
     }

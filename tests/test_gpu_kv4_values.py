@@ -279,3 +279,30 @@ def test_a_first_token_with_most_of_the_weight_and_small_values(heads, new, copi
     v[0] *= 2.0 ** -10
     _check(Batch([k], [v], group, 64), 1 + 0.3 * g.standard_normal((new, heads, D)), [new],
            copies=copies)
+
+
+# ---- pages that are not there -------------------------------------------------------------
+@pytest.mark.parametrize("D,group,page", FORMS)
+@pytest.mark.parametrize("heads,new", [(4, [1, 1]), (4, [3, 1]), (8, [9, 2])])
+@pytest.mark.parametrize("weights", [False, True])
+def test_tokens_of_a_missing_page_are_left_out(D, group, page, heads, new, weights):
+    lens = [700, 300]
+    batch, g = _random(lens, 2, D, group, page, 48)
+    table = batch.table.copy()
+    gone = [np.zeros(n, bool) for n in lens]
+    for b, at, bad in ((0, 1, -1), (0, 500 // page, 1 << 30), (1, 0, batch.pages)):
+        table[b, at] = bad
+        gone[b][at * page:(at + 1) * page] = True
+    q = g.standard_normal((sum(new), heads, D))
+    _check(batch, q, new, weights=weights, table=table, gone=gone, status=8)
+    _check(batch, q, new, weights=weights)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_sequence_without_any_page(new):
+    lens = [300, 200]
+    batch, g = _random(lens, 2, 128, 64, 64, 49)
+    table = batch.table.copy()
+    table[1] = -1
+    gone = [np.zeros(300, bool), np.ones(200, bool)]
+    _check(batch, g.standard_normal((2 * new, 4, 128)), [new, new], table=table, gone=gone, status=8)
