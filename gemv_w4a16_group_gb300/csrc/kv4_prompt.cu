@@ -22,8 +22,9 @@
 //    that owns one row a thread (no shuffles), over tiles of 128 tokens in a ring of four bulk
 //    copies. One thread issues S = Q K^T (tensor memory, fp32) and O += P V with P read back from
 //    tensor memory, the halves in turn, so that one half's softmax runs under the other's
-//    products. The running maximum may lag by 2^8 before O is rescaled: P stays in FP16's range
-//    and the rescale is rare. The (sequence, head, 256-row tile) items, each as many units as it
+//    products. P comes under the largest product of a probability and a tile's values that its row
+//    has met, with 10 bits to spare; the running maximum may lag by 2^8 and that product by 2^5
+//    before O is rescaled: P stays in FP16's range and the rescale is rare. The (sequence, head, 256-row tile) items, each as many units as it
 //    has visible token tiles, are cut into equal ranges of units, one a CTA; an item that a
 //    boundary cuts is joined from fp32 parts by whoever arrives last, in order.
 // 3. With weights, kv4_prompt_weights_kernel makes S^T = K_hat Q^T from the same tiles, a thread
@@ -43,6 +44,10 @@ struct KeyMeta {
   float kf;  // a key's image times this is the key
   int ev;    // a value's image times 2^ev is the value
 };
+// ev of a tile whose values are all 0: below any other's, so that it makes no row's product larger.
+constexpr int kNoValue = -200;
+// P reaches 2^kLift where its row's largest product is made, and 2^15 once that product lags.
+constexpr int kLift = 10;
 
 // Where a CTA begins: an item, the units of it before the CTA's range, and the range's size.
 struct Start {
@@ -215,7 +220,7 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   // keys reach [2^7, 2^8): 128 times a minimum + 8 s still is an FP16 number
   const int kup = max(up_of(ktop) - 7, -126), vup = up_of(vtop);
   const float kf = pow2f(kup), vf = pow2f(vup);
-  if (tid == 0) ws.meta[at] = KeyMeta{pow2f(-kup), -vup};
+  if (tid == 0) ws.meta[at] = KeyMeta{pow2f(-kup), vtop == 0u ? kNoValue : -vup};
   uint8_t* kimg = ws.kv_img + at * Img<D>::kPair;
   uint8_t* vimg = kimg + Img<D>::kTile;
   constexpr int kWords = D / 8;
@@ -930,8 +935,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const KeyMeta* meta =
             ws.meta + (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) * ws.key_tiles;
         KeyMeta km = meta[g.lo];
-        float m = -INFINITY, l = 0.f;
-        int ev = km.ev;
+        // the running maximum; the sum of probabilities under it; and, under it too, the exponent
+        // (a whole number) that O and the row's products come under
+        float m = -INFINITY, l = 0.f, e = 0.f;
         for (int i = g.lo; i < g.hi; ++i) {
           const KeyMeta now = km;
           if (i + 1 < g.hi) km = meta[i + 1];
@@ -960,22 +966,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const float best = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]),
                                   fmaxf(top[6], top[7]));
           // -inf stays -inf: cf is positive
-          const bool raise = best * cf > m + 8.f;
-          float down = 0.f, undo = 1.f;
-          if (__any_sync(0xffffffffu, raise) || now.ev != ev) {
+          const float t = best * cf, ev = static_cast<float>(now.ev), product = t + ev;
+          const bool raise = t > m + 8.f || product - m > e + 15.f;
+          if (__any_sync(0xffffffffu, raise)) {
             float f = 1.f;
             if (raise) {
-              f = ex2(m - best * cf);
-              m = best * cf;
-              l *= f;
+              const float top = fmaxf(m, t), old = e + (m - top);
+              l *= ex2(m - top);
+              const float now_e = fmaxf(ceilf(old), ceilf(product - top) - kLift);
+              f = ex2(old - now_e);
+              m = top;
+              e = now_e;
             }
-            if (now.ev > ev) {
-              f *= exp2f(static_cast<float>(ev - now.ev));
-              ev = now.ev;
-            }
-            // past 2^100 the values are nothing beside those met before, and P is 0
-            down = static_cast<float>(min(ev - now.ev, 100));
-            undo = exp2f(down);
             if (i > g.lo && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
@@ -988,7 +990,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               }
             }
           }
+          // P is the probability (under m) times 2^-down, l takes that out again. Past 2^60 the
+          // tile's values are nothing beside the row's products and P is 0; before 2^-126 its
+          // probabilities are nothing beside l
+          const float down = fminf(e - ev, 60.f);
           const float bias = -((m == -INFINITY ? 0.f : m) + down);
+          const float undo = pow2f(static_cast<int>(fmaxf(down, -126.f)));
           float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -1012,7 +1019,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (!ok || !wait(&o_full[half], o_phase)) break;
         // ---- O is complete
-        const float vf = exp2f(static_cast<float>(ev));
+        const float vf = scalbnf(1.f, static_cast<int>(e));
         const bool whole = g.lo == 0 && g.hi == g.tiles;
         const bool have = R < rows;
         const int64_t at =
@@ -1035,13 +1042,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         };
         if (whole) {
-          const float inv = l == 0.f ? 0.f : vf / l;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld_32cols(t_o + 32 * c, o);
             tmem_ld_wait();
-            if (have) store32(c, reinterpret_cast<const float*>(o), inv);
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * vf;
+            if (have) store32(c, v, inv);
           }
           finish(m, l);
         } else {

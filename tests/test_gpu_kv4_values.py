@@ -216,7 +216,7 @@ def test_constant_values(D, group, value, a_unit, heads):
 # ---- values of any size -------------------------------------------------------------------
 # (heads on two, new tokens, copies): a call that is cut to the last unit, and one whose CTAs go
 # through whole sequences
-PATHS = [(8, 1, 1), (8, 1, 60), (8, 4, 60), (4, 30, 60)]
+PATHS = [(8, 1, 1), (8, 1, 60), (8, 4, 60), (4, 30, 60), (4, 130, 1), (4, 130, 60)]
 
 
 @pytest.mark.parametrize("heads,new,copies", PATHS)
@@ -258,7 +258,7 @@ def _near_one(g, new, heads, D):
     return q
 
 
-@pytest.mark.parametrize("heads,new,copies", PATHS)
+@pytest.mark.parametrize("heads,new,copies", PATHS[:4])
 @pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
 @pytest.mark.parametrize("at", [[3], [400], [5, 600]])
 @pytest.mark.parametrize("power", [14, 20, 30])
