@@ -14,6 +14,9 @@
 //    copy, and a code is widened once instead of once a row tile (a 4096-token prompt has 64 of
 //    them a head). Values come transposed, so that both products read K-major operands, rounded
 //    to FP16 under a power of two a tile (2^-11 of a value, a quarter of the output's rounding).
+//    A tile whose tokens differ by 2^8 or more (a token that is larger than the rest would take
+//    bits from them even in rows that do not see it) has powers of two a token, and the softmax a
+//    slower body for it.
 //    A key is exact: with c the code less 8, c s has at most 3 + 8 significant bits and is an
 //    FP16 number; what is left, (min + 8 s) times the sum of q over the group, goes through 16
 //    more columns, four a group, as FP16 pairs of high and low parts. Rounded keys (2^-12) put
@@ -42,8 +45,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 struct KeyMeta {
   float kf;  // a key's image times this is the key
-  int ev;    // a value's image times 2^ev is the value
+  int ev;    // a value's image times 2^ev is the value; kByToken: as ws.tokens says
 };
+struct TokenMeta {
+  float kf, ev;
+};
+constexpr int kByToken = 1 << 20;
+constexpr int kSpread = 8;  // exponents between a tile's tokens that one power of two bridges
 // ev of a tile whose values are all 0: below any other's, so that it makes no row's product larger.
 constexpr int kNoValue = -200;
 // P reaches 2^kLift where its row's largest product is made, and 2^15 once that product lags.
@@ -71,6 +79,7 @@ struct PromptWs {
   uint32_t* base;     // [batch + 1]: units before a sequence
   int32_t* pre;       // [batch, row_tiles + 1]: units of a head before a row tile
   KeyMeta* meta;      // [batch, kv_heads, key_tiles]
+  TokenMeta* tokens;  // [batch, kv_heads, key_tiles, 128], of the tiles with kByToken
   float* qf;          // [batch, kv_heads, row_tiles]: logit (base 2) per image product, without kf
   uint8_t* q_img;     // [batch, kv_heads, row_tiles] x 256 (D + 16) FP16
   uint8_t* kv_img;    // [batch, kv_heads, key_tiles] x (K 128 (D + 16), V^T D 128) FP16
@@ -166,7 +175,7 @@ template <int D, int NG>
 __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, int h, int tile,
                          uint8_t* raw) {
   using R = Kv4Record<D, NG>;
-  __shared__ uint32_t red[2][kImgThreads / 32];
+  __shared__ uint32_t reach[2][kTileKeys];  // largest magnitudes of the tokens' keys and values
   __shared__ uint64_t bar;
   __shared__ uint32_t present;  // bit j: record j is there
   __shared__ uint32_t abort_flag;
@@ -208,19 +217,44 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
     }
   }
   __syncthreads();
-  uint32_t ktop = 0, vtop = 0;
-  for (int x = tid; x < 8 * 16 * NG; x += kImgThreads) {
-    const int j = x / (16 * NG), w = x % (16 * NG);
-    const uint8_t* rec = raw + j * R::kBytes;
-    ktop = max(ktop, reach_bits(reinterpret_cast<const uint32_t*>(rec + R::kKParams)[w]));
-    vtop = max(vtop, reach_bits(reinterpret_cast<const uint32_t*>(rec + R::kVParams)[w]));
+  if (tid < 2 * kTileKeys) {
+    const uint32_t* params = reinterpret_cast<const uint32_t*>(
+        raw + (tid % kTileKeys) / 16 * R::kBytes + (tid < kTileKeys ? R::kKParams : R::kVParams));
+    uint32_t top = 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) top = max(top, reach_bits(params[16 * g + tid % 16]));
+    reach[tid / kTileKeys][tid % kTileKeys] = top;
   }
-  ktop = block_max(ktop, red[0]);
-  vtop = block_max(vtop, red[1]);
+  __syncthreads();
+  // exponents of the tile's largest token and of its smallest one that is not 0
+  uint32_t tops[2];
+  bool by_token = false;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    uint32_t top = 0, low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kTileKeys; i += 32) {
+      const uint32_t x = reach[y][i + tid % 32];
+      top = max(top, x);
+      low = min(low, x - 1u);  // 0 is the largest
+    }
+    tops[y] = __reduce_max_sync(0xffffffffu, top);
+    low = __reduce_min_sync(0xffffffffu, low);
+    by_token = by_token || (tops[y] != 0u && (tops[y] >> 23) - (low >> 23) >= kSpread);
+  }
   // keys reach [2^7, 2^8): 128 times a minimum + 8 s still is an FP16 number
-  const int kup = max(up_of(ktop) - 7, -126), vup = up_of(vtop);
-  const float kf = pow2f(kup), vf = pow2f(vup);
-  if (tid == 0) ws.meta[at] = KeyMeta{pow2f(-kup), vtop == 0u ? kNoValue : -vup};
+  auto key_up = [](uint32_t top) { return max(up_of(top) - 7, -126); };
+  const int kup = key_up(tops[0]), vup = up_of(tops[1]);
+  if (tid == 0)
+    ws.meta[at] = KeyMeta{pow2f(-kup), by_token ? kByToken : tops[1] == 0u ? kNoValue : -vup};
+  if (by_token && tid < kTileKeys) {
+    const uint32_t top = reach[1][tid];
+    ws.tokens[at * kTileKeys + tid] = TokenMeta{
+        pow2f(-key_up(reach[0][tid])), static_cast<float>(top == 0u ? kNoValue : -up_of(top))};
+  }
+  const float kf_tile = pow2f(kup), vf_tile = pow2f(vup);
+  auto key_factor = [&](int t) { return by_token ? pow2f(key_up(reach[0][t])) : kf_tile; };
+  auto value_factor = [&](int t) { return by_token ? pow2f(up_of(reach[1][t])) : vf_tile; };
   uint8_t* kimg = ws.kv_img + at * Img<D>::kPair;
   uint8_t* vimg = kimg + Img<D>::kTile;
   constexpr int kWords = D / 8;
@@ -231,7 +265,8 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
     const uint32_t word = reinterpret_cast<const uint32_t*>(rec)[(t % 16) * kWords + w];
     const uint32_t p =
         reinterpret_cast<const uint32_t*>(rec + R::kKParams)[16 * (d / R::kGroup) + t % 16];
-    const uint32_t sc = f16x2_bits(bf16_lo(p) * kf, bf16_lo(p) * kf);
+    const float scale = bf16_lo(p) * key_factor(t);
+    const uint32_t sc = f16x2_bits(scale, scale);
     uint32_t out[4];
     centred_pairs(word, out);
 #pragma unroll
@@ -242,6 +277,7 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   }
   if (tid < kTileKeys) {
     uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const float kf = key_factor(tid);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const uint32_t p = reinterpret_cast<const uint32_t*>(
@@ -270,10 +306,12 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
                     code);
       // P of a row that does not see a token is 0; 0 times a value that is not finite is not
       auto param = [&](float v) { return fabsf(v) <= 65504.f ? v : 0.f; };
-      const float s0 = bf16_lo(two.x) * vf, s1 = bf16_lo(two.y) * vf;
+      const int t = 16 * j + 8 * half + 2 * p;
+      const float f0 = value_factor(t), f1 = value_factor(t + 1);
+      const float s0 = bf16_lo(two.x) * f0, s1 = bf16_lo(two.y) * f1;
       const uint32_t sc = f16x2_bits(param(s0), param(s1));
-      const uint32_t mn = f16x2_bits(param(fmaf(8.f, s0, bf16_hi(two.x) * vf)),
-                                     param(fmaf(8.f, s1, bf16_hi(two.y) * vf)));
+      const uint32_t mn = f16x2_bits(param(fmaf(8.f, s0, bf16_hi(two.x) * f0)),
+                                     param(fmaf(8.f, s1, bf16_hi(two.y) * f1)));
 #pragma unroll
       for (int i = 0; i < 4; ++i) out[i][p] = fma_f16x2(code[i], sc, mn);
     }
@@ -932,23 +970,100 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int first_row = g.rt * kTileRows + half * 128;
         const int clear = first_row + 127 < rows ? seq.n - seq.m + first_row / G + 1 : 0;
         const float qf = ws.qf[item(g)];
-        const KeyMeta* meta =
-            ws.meta + (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) * ws.key_tiles;
+        const size_t tile0 = (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) * ws.key_tiles;
+        const KeyMeta* meta = ws.meta + tile0;
         KeyMeta km = meta[g.lo];
         // the running maximum; the sum of probabilities under it; and, under it too, the exponent
         // (a whole number) that O and the row's products come under
         float m = -INFINITY, l = 0.f, e = 0.f;
+        // a tile whose largest logit (base 2) is t, and whose largest product is `product`
+        auto meet = [&](float t, float product, bool first) {
+          const bool raise = t > m + 8.f || product - m > e + 15.f;
+          if (__any_sync(0xffffffffu, raise)) {
+            float f = 1.f;
+            if (raise) {
+              const float top = fmaxf(m, t), old = e + (m - top);
+              l *= ex2(m - top);
+              const float now_e = fmaxf(ceilf(old), ceilf(product - top) - kLift);
+              f = ex2(old - now_e);
+              m = top;
+              e = now_e;
+            }
+            if (!first && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld_16cols(t_o + 16 * c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st_16cols(t_o + 16 * c, o);
+              }
+            }
+          }
+        };
+        auto hand_over = [&]() {
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[half]);
+        };
         for (int i = g.lo; i < g.hi; ++i) {
           const KeyMeta now = km;
           if (i + 1 < g.hi) km = meta[i + 1];
           const float cf = fmaxf(qf * now.kf, 1e-37f);
           if (!wait(&s_full[half], s_phase)) break;
+          const int see = last_key - i * kTileKeys;  // columns up to this one are visible
+          if (now.ev == kByToken) {
+            // powers of two a token: S is read twice, 32 columns at a time
+            const TokenMeta* tok = ws.tokens + (tile0 + i) * kTileKeys;
+            uint32_t x[32];
+            auto logits = [&](int c) {
+              tmem_ld_32cols(t_s + 32 * c, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                x[j] = __float_as_uint(
+                    32 * c + j <= see
+                        ? __uint_as_float(x[j]) * fmaxf(qf * tok[32 * c + j].kf, 1e-37f)
+                        : -INFINITY);
+            };
+            float t = -INFINITY, product = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              logits(c);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                t = fmaxf(t, __uint_as_float(x[j]));
+                product = fmaxf(product, __uint_as_float(x[j]) + tok[32 * c + j].ev);
+              }
+            }
+            meet(t, product, i == g.lo);
+            const float under = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {  // P's columns are behind those of S still to be read
+              logits(c);
+              float acc = 0.f, p[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float y = __uint_as_float(x[j]) - under;
+                acc += ex2(y);
+                p[j] = ex2(y + (tok[32 * c + j].ev - e));
+              }
+              l += acc;
+              uint32_t pairs[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) pairs[j] = f16x2_bits(p[2 * j], p[2 * j + 1]);
+              tmem_st_16cols(t_s + 16 * c, pairs);
+            }
+            hand_over();
+            continue;
+          }
           float s[128];
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             tmem_ld_32cols(t_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
           tmem_ld_wait();
-          const int see = last_key - i * kTileKeys;  // columns up to this one are visible
           if ((i + 1) * kTileKeys > clear) {
 #pragma unroll
             for (int j = 0; j < 128; ++j) s[j] = j <= see ? s[j] : -INFINITY;
@@ -965,31 +1080,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int x = 0; x < 8; ++x) top[x] = fmaxf(top[x], s[120 + x]);
           const float best = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]),
                                   fmaxf(top[6], top[7]));
-          // -inf stays -inf: cf is positive
-          const float t = best * cf, ev = static_cast<float>(now.ev), product = t + ev;
-          const bool raise = t > m + 8.f || product - m > e + 15.f;
-          if (__any_sync(0xffffffffu, raise)) {
-            float f = 1.f;
-            if (raise) {
-              const float top = fmaxf(m, t), old = e + (m - top);
-              l *= ex2(m - top);
-              const float now_e = fmaxf(ceilf(old), ceilf(product - top) - kLift);
-              f = ex2(old - now_e);
-              m = top;
-              e = now_e;
-            }
-            if (i > g.lo && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld_16cols(t_o + 16 * c, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st_16cols(t_o + 16 * c, o);
-              }
-            }
-          }
+          const float ev = static_cast<float>(now.ev);
+          meet(best * cf, best * cf + ev, i == g.lo);  // -inf stays -inf: cf is positive
           // P is the probability (under m) times 2^-down, l takes that out again. Past 2^60 the
           // tile's values are nothing beside the row's products and P is 0; before 2^-126 its
           // probabilities are nothing beside l
@@ -1011,10 +1103,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             tmem_st_32cols(t_s + 32 * c, p);
           }
-          tmem_st_wait();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[half]);
+          hand_over();
           l = fmaf((acc[0] + acc[1]) + (acc[2] + acc[3]), undo, l);
         }
         if (!ok || !wait(&o_full[half], o_phase)) break;
@@ -1382,7 +1471,11 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     int n = 0;
     do {
       const int key = g.kt * kTileKeys + (warp & 3) * 32 + lane;
-      const float kf = ws.meta[head() * ws.key_tiles + g.kt].kf;
+      const size_t tile = head() * ws.key_tiles + g.kt;
+      const KeyMeta km = ws.meta[tile];
+      const float kf = km.ev == kByToken
+                           ? ws.tokens[tile * kTileKeys + key % kTileKeys].kf
+                           : km.kf;
       float acc = 0.f;
       auto qf_of = [&](int i) { return ws.qf[head() * ws.row_tiles + g.first + i]; };
       // rows that do not see the lane's token, and the first tile whose rows see all of them
@@ -1485,8 +1578,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-  size_t plan, starts, order, base, pre, meta, qf, q_img, kv_img, counters, parts, lse2, kbase, kpre,
-      kcounters, sums, total;
+  size_t plan, starts, order, base, pre, meta, token_meta, qf, q_img, kv_img, counters, parts, lse2,
+      kbase, kpre, kcounters, sums, total;
   int key_tiles, row_tiles;
 };
 
@@ -1511,6 +1604,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   l.base = take((static_cast<size_t>(batch) + 1) * 4);
   l.pre = take(static_cast<size_t>(batch) * (l.row_tiles + 1) * 4);
   l.meta = take(bh * l.key_tiles * sizeof(KeyMeta));
+  l.token_meta = take(bh * l.key_tiles * kTileKeys * sizeof(TokenMeta));
   l.qf = take(bh * l.row_tiles * 4);
   l.q_img = take(bh * l.row_tiles * kTileRows * (D + 16) * 2);
   l.kv_img = take(bh * l.key_tiles * kTileKeys * (2 * D + 16) * 2);
@@ -1538,6 +1632,7 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   ws.base = reinterpret_cast<uint32_t*>(w + l.base);
   ws.pre = reinterpret_cast<int32_t*>(w + l.pre);
   ws.meta = reinterpret_cast<KeyMeta*>(w + l.meta);
+  ws.tokens = reinterpret_cast<TokenMeta*>(w + l.token_meta);
   ws.qf = reinterpret_cast<float*>(w + l.qf);
   ws.q_img = w + l.q_img;
   ws.kv_img = w + l.kv_img;

@@ -467,8 +467,9 @@ w4a16_status kv4_read(const kv4_cache* cache, const int32_t* starts, uint16_t* k
  * A row that sees no token (an empty sequence) gives out = 0 and lse = -inf. Tokens that a row
  * does not see do not touch it, whatever they hold. Products are FP16 with fp32 sums: codes are
  * exact in them, probabilities (times a value's scale) rounded to 2^-12 of themselves or 2^-28 of
- * the row's largest, and, from 97 rows a key/value head on, probabilities and values to 2^-12 of
- * themselves; maxima, sums, lse and weights are fp32. out is within about a rounding to BF16 of the
+ * the row's largest, and, from 97 rows a key/value head on, probabilities to 2^-12 of themselves or,
+ * times the values, 2^-25 of the row's largest, and values to 2^-11 of the largest of their token
+ * and group; maxima, sums, lse and weights are fp32. out is within about a rounding to BF16 of the
  * exact result, lse and weights within 1e-6. Results do not depend on timing (no floating-point
  * atomics). Values must be finite where a row sees them.
  * Up to 96 rows (max_new * heads / kv_heads) the cache is read in place; above that it is widened

@@ -258,7 +258,7 @@ def _near_one(g, new, heads, D):
     return q
 
 
-@pytest.mark.parametrize("heads,new,copies", PATHS[:4])
+@pytest.mark.parametrize("heads,new,copies", PATHS)
 @pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
 @pytest.mark.parametrize("at", [[3], [400], [5, 600]])
 @pytest.mark.parametrize("power", [14, 20, 30])
@@ -279,6 +279,21 @@ def test_a_first_token_with_most_of_the_weight_and_small_values(heads, new, copi
     v[0] *= 2.0 ** -10
     _check(Batch([k], [v], group, 64), 1 + 0.3 * g.standard_normal((new, heads, D)), [new],
            copies=copies)
+
+
+@pytest.mark.parametrize("heads,new", [(4, 130), (8, 200), (2, 4), (4, 24)])
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("size", [1e5, 1e15, 1e30])
+def test_hidden_tokens_of_any_size(heads, new, D, group, size):
+    """The last tokens hold huge finite keys and values: rows that do not see them are as near as
+    without them."""
+    g = np.random.default_rng(47)
+    n, last = 600, 3
+    k, v = _normal(g, n, 2, D)
+    k[n - last:] *= size
+    v[n - last:] *= size
+    rows = np.arange(new) < new - last
+    _check(Batch([k], [v], group, 64), g.standard_normal((new, heads, D)), [new], rows=rows)
 
 
 # ---- pages that are not there -------------------------------------------------------------
