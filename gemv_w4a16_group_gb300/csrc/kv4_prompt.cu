@@ -48,7 +48,7 @@ struct KeyMeta {
   int ev;    // a value's image times 2^ev is the value; kByToken: as ws.tokens says
 };
 struct TokenMeta {
-  float kf, ev;
+  float kf, ev;  // kf 0: the token's page is out of range, no row sees it
 };
 constexpr int kByToken = 1 << 20;
 constexpr int kSpread = 8;  // exponents between a tile's tokens that one power of two bridges
@@ -228,7 +228,8 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   __syncthreads();
   // exponents of the tile's largest token and of its smallest one that is not 0
   uint32_t tops[2];
-  bool by_token = false;
+  const int records = min(8, (seq.n - key0 + 15) / 16);
+  bool by_token = present != (1u << records) - 1u;  // a page is out of range
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     uint32_t top = 0, low = 0xFFFFFFFFu;
@@ -249,8 +250,9 @@ __device__ void key_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
     ws.meta[at] = KeyMeta{pow2f(-kup), by_token ? kByToken : tops[1] == 0u ? kNoValue : -vup};
   if (by_token && tid < kTileKeys) {
     const uint32_t top = reach[1][tid];
-    ws.tokens[at * kTileKeys + tid] = TokenMeta{
-        pow2f(-key_up(reach[0][tid])), static_cast<float>(top == 0u ? kNoValue : -up_of(top))};
+    ws.tokens[at * kTileKeys + tid] =
+        TokenMeta{(present >> (tid / 16)) & 1u ? pow2f(-key_up(reach[0][tid])) : 0.f,
+                  static_cast<float>(top == 0u ? kNoValue : -up_of(top))};
   }
   const float kf_tile = pow2f(kup), vf_tile = pow2f(vup);
   auto key_factor = [&](int t) { return by_token ? pow2f(key_up(reach[0][t])) : kf_tile; };
@@ -1022,11 +1024,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               tmem_ld_32cols(t_s + 32 * c, x);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                x[j] = __float_as_uint(
-                    32 * c + j <= see
-                        ? __uint_as_float(x[j]) * fmaxf(qf * tok[32 * c + j].kf, 1e-37f)
-                        : -INFINITY);
+              for (int j = 0; j < 32; ++j) {
+                const float kf = tok[32 * c + j].kf;
+                x[j] = __float_as_uint(32 * c + j <= see && kf != 0.f
+                                           ? __uint_as_float(x[j]) * fmaxf(qf * kf, 1e-37f)
+                                           : -INFINITY);
+              }
             };
             float t = -INFINITY, product = -INFINITY;
 #pragma unroll 1
@@ -1540,7 +1543,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 #pragma unroll
         for (int x = 0; x < kSumParts - 1; ++x) acc += sum_s[128 * x + threadIdx.x];
       }
-      if (g.s.m == 0) acc = 0.f;  // no rows: nothing has written these tiles
+      // no rows: nothing has written these tiles; or the token's page is out of range
+      if (g.s.m == 0 || kf == 0.f) acc = 0.f;
       if (g.lo == 0 && g.hi == g.units) {
         store(acc);
       } else {

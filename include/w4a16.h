@@ -412,9 +412,10 @@ w4a16_status mxfp4_matmul(const uint16_t* x, const uint8_t* codes, const uint8_t
  * `lens`, already raised by the new tokens, serves a step's append and its attention.
  *
  * lens, starts, table, new lengths and kept indices are int32, weights fp32 (4-byte alignment is
- * enough for these). A page number, length or offset outside the arrays is never followed: the
- * tokens are left out (an attention row then is that of the tokens that remain), and
- * w4a16_device_status() returns W4A16_ERR_INDEX.
+ * enough for these). A page number, length or offset outside the arrays is never followed, and
+ * w4a16_device_status() returns W4A16_ERR_INDEX: the tokens of such a page are left out (an
+ * attention row then is that of the tokens that remain), and a length or offset counts as the
+ * nearest one that its arrays and bounds allow.
  *
  * head_dim 64 or 128; group 32, 64 or 128, at most head_dim; page_size a power of two from 16 to
  * 2^20; table_width * page_size at most 2^30; W4A16_ERR_UNSUPPORTED otherwise.
@@ -494,7 +495,9 @@ w4a16_status kv4_attention(const kv4_cache* cache, const int32_t* starts, const 
  *   out_table    int32 [batch, out_width]: pages of the same cache that no sequence of this call
  *                reads, out_width * page_size >= budget
  *   weights      fp32 [batch, kv_heads, weights_stride], weights_stride >= max_len >= lens
- *   kept         int32 [batch, kv_heads, budget]: old positions, ascending, -1 past new_lens
+ *   kept         int32 [batch, kv_heads, budget]: old positions, ascending, -1 past new_lens. The
+ *                weights alone choose them: a kept token of a page out of range (W4A16_ERR_INDEX)
+ *                is not moved, and its new place keeps what it held
  *   new_lens     int32 [batch]: min(lens, budget); not the array cache->lens
  *   weights_out  fp32 [batch, kv_heads, weights_out_stride] (>= budget): the kept tokens' weights
  * The old pages stay as they were: they may be shared, and heads keep different tokens of them.

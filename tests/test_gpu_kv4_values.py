@@ -298,7 +298,8 @@ def test_hidden_tokens_of_any_size(heads, new, D, group, size):
 
 # ---- pages that are not there -------------------------------------------------------------
 @pytest.mark.parametrize("D,group,page", FORMS)
-@pytest.mark.parametrize("heads,new", [(4, [1, 1]), (4, [3, 1]), (8, [9, 2])])
+@pytest.mark.parametrize("heads,new", [(4, [1, 1]), (4, [3, 1]), (8, [9, 2]), (4, [130, 1]),
+                                       (4, [90, 65])])
 @pytest.mark.parametrize("weights", [False, True])
 def test_tokens_of_a_missing_page_are_left_out(D, group, page, heads, new, weights):
     lens = [700, 300]
@@ -313,7 +314,7 @@ def test_tokens_of_a_missing_page_are_left_out(D, group, page, heads, new, weigh
     _check(batch, q, new, weights=weights)
 
 
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 40, 130])
 def test_a_sequence_without_any_page(new):
     lens = [300, 200]
     batch, g = _random(lens, 2, 128, 64, 64, 49)
@@ -321,3 +322,33 @@ def test_a_sequence_without_any_page(new):
     table[1] = -1
     gone = [np.zeros(300, bool), np.ones(200, bool)]
     _check(batch, g.standard_normal((2 * new, 4, 128)), [new, new], table=table, gone=gone, status=8)
+
+
+@pytest.mark.parametrize("D,group,page", FORMS[:4])
+def test_eviction_leaves_a_missing_page_where_it_is(D, group, page):
+    """The same tokens are kept; those of the page are not moved, and their places stay as they
+    were."""
+    n, budget, H = 520, 300, 2
+    batch, g = _random([n], H, D, group, page, 51)
+    fill = batch.pages
+    width = (budget + page - 1) // page
+    spare = torch.full((width,) + batch.cache.shape[1:], 0x3A, dtype=torch.uint8, device=DEV)
+    out_table = np.arange(fill, fill + width, dtype=np.int32)[None]
+    table = batch.table.copy()
+    table[0, 1] = -1
+    w = _gpu(g.random((1, H, n)).astype(np.float32))
+    res = []
+    for t, status in ((batch.table, 0), (table, 8)):
+        cache = torch.cat([batch.cache, spare])
+        kept, lens, _ = w4.kv4_evict(cache, _gpu(t), batch.lens_t(), w, _gpu(out_table), budget, n,
+                                     D, first=2, recent=20, group=group)
+        assert w4.w4a16_device_status() == status and lens.item() == budget
+        res.append((kept.cpu().numpy(), ref.Cache(cache.cpu().numpy(), out_table, D, group)))
+    before = ref.Cache(torch.cat([batch.cache, spare]).cpu().numpy(), out_table, D, group)
+    assert np.array_equal(res[0][0], res[1][0])
+    assert torch.equal(torch.from_numpy(res[1][1].data[:fill]), batch.cache.cpu())
+    for h in range(H):
+        gone = res[0][0][0, h] // page == 1
+        assert gone.any() and not gone.all()
+        for x, moved, old in zip(*(c.get(0, h, budget) for c in (res[1][1], res[0][1], before))):
+            assert np.array_equal(x, np.where(gone[:, None], old, moved))
