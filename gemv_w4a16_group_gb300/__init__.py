@@ -743,8 +743,9 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
     ``max_new`` bound the lengths and new tokens of a sequence; scale defaults to
     head_dim ** -0.5. ``lse`` (fp32 [tokens, heads]) receives ln sum exp; ``weights_out`` (fp32
     [batch, kv_heads, length]) ``weights`` (or 0) plus the attention weight of each cached token.
-    Without a ``workspace`` (kv4_attention_workspace_bytes, zero-filled once) one is allocated
-    and zero-filled for the call."""
+    A ``workspace`` of kv4_attention_workspace_bytes, zero-filled once, serves calls of any shapes
+    that it is large enough for, one after the other; without one, one is allocated and zero-filled
+    for the call."""
     T, heads, head_dim = q.shape
     c, batch, kv_heads = _kv4(cache, table, lens, head_dim, group)
     qp, qs = _tokens(q, "q")

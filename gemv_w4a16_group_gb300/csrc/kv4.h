@@ -56,6 +56,9 @@ struct Kv4AttentionArgs {
   uint8_t* workspace;
   uint64_t wait_limit_ns;
 };
+// The workspace's beginning, the same for calls of any shape: counters that every call leaves zero.
+constexpr size_t kKv4CounterBytes = 4096;
+inline size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 size_t kv4_attention_workspace(int batch, int tokens, int max_new, int max_len, int heads,
                                int kv_heads, int head_dim, int group, bool weights);
 cudaError_t launch_kv4_attention(const Kv4AttentionArgs& a, int head_dim, int group,

@@ -147,7 +147,7 @@ __device__ __forceinline__ void bulk_load_once(void* smem_dst, const void* gsrc,
 }
 
 struct Workspace {
-  uint32_t* counters;  // one an item, zero between calls
+  uint32_t* counters;  // [grid], of the item that a CTA's range begins and does not end
   float* lse2;         // [tokens, heads], base 2
   float* logits;       // [batch, kv_heads, max_new G, row_len], base 2 (weights only)
   float* parts;        // [2 grid] x (8 NT rows x D + 16 NT)
@@ -935,8 +935,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
       join_warps();
       if (threadIdx.x == 0) {
         __threadfence();  // the CTA's writes, which the barrier has ordered before this
-        uint32_t* cnt = ws.counters + (static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) *
-                                          ((a.max_new * G + kRows - 1) / kRows) + cur.tile;
+        uint32_t* cnt = ws.counters + i0;
         const bool last = atomicAdd(cnt, 1u) == i1 - i0;
         if (last) *cnt = 0u;
         __threadfence();
@@ -1043,27 +1042,25 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttentionArgs
     if (key0 + 256 * t < s.n) a.weights_out[at + 256 * t] = w[t] + acc[t];
 }
 
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
-
 // n8 tiles of a row tile. More than two are slower than several row tiles of two: head size 64,
 // 36 rows in three tiles 12.9 us (one sequence of 2048), 32 rows in one of four 18.0 us.
 int row_blocks(int max_new, int G) { return max_new * G <= 8 ? 1 : 2; }
 
 struct Layout {
-  size_t counters, lse2, logits, parts, total;
+  size_t lse2, logits, parts, total;
   int row_len;
 };
-int grid_limit(int d, int nt) { return ctas_per_sm(d, nt) * device_sm_count(); }
+int grid_limit(int d, int nt) {  // a counter a CTA
+  const int n = ctas_per_sm(d, nt) * device_sm_count(), most = kKv4CounterBytes / 4;
+  return n < most ? n : most;
+}
 
 Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv_heads, int D,
               bool weights) {
   Layout l;
   const int G = heads / kv_heads, nt = row_blocks(max_new, G);
   l.row_len = (max_len + 3) / 4 * 4;
-  size_t at = 0;
-  l.counters = at;
-  at += round256(static_cast<size_t>(batch) * kv_heads *
-                 ((static_cast<size_t>(max_new) * G + 7) / 8) * 4);
+  size_t at = kKv4CounterBytes;
   l.parts = at;
   at += round256(static_cast<size_t>(2) * grid_limit(D, nt) * nt * 8 * (D + 2) * 4);
   l.lse2 = at;
@@ -1081,7 +1078,7 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   const Layout l = layout(a.c.batch, a.tokens, a.max_new, a.max_len, a.heads, a.c.kv_heads, D,
                           a.weights_out != nullptr);
   Workspace ws;
-  ws.counters = reinterpret_cast<uint32_t*>(a.workspace + l.counters);
+  ws.counters = reinterpret_cast<uint32_t*>(a.workspace);
   ws.lse2 = reinterpret_cast<float*>(a.workspace + l.lse2);
   ws.logits = reinterpret_cast<float*>(a.workspace + l.logits);
   ws.parts = reinterpret_cast<float*>(a.workspace + l.parts);

@@ -1579,8 +1579,6 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   }
 }
 
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
-
 struct Layout {
   size_t plan, starts, order, base, pre, meta, token_meta, qf, q_img, kv_img, counters, parts, lse2,
       kbase, kpre, kcounters, sums, total;
@@ -1594,7 +1592,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   const size_t bh = static_cast<size_t>(batch) * kv_heads;
   l.key_tiles = (max_len + kTileKeys - 1) / kTileKeys;
   l.row_tiles = static_cast<int>((static_cast<int64_t>(max_new) * G + kTileRows - 1) / kTileRows);
-  size_t at = 0;
+  size_t at = kKv4CounterBytes;  // left alone: they stay zero for calls of few rows
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += round256(bytes);

@@ -477,8 +477,9 @@ w4a16_status kv4_read(const kv4_cache* cache, const int32_t* starts, uint16_t* k
  * into the workspace first (4 bytes a key/value pair of dims, 16-bit tiles for tcgen05.mma).
  * Workspace: kv4_attention_workspace_bytes() bytes, 16-byte aligned, zero-filled before its first
  * use (the kernels leave its counters zero) and not shared by calls that may run concurrently;
- * W4A16_ERR_WORKSPACE if NULL or smaller. Calls that differ in tokens, max_len and the lengths
- * themselves may share one; others need one of their own, or it zero-filled again.
+ * W4A16_ERR_WORKSPACE if NULL or smaller. Its first 4 KiB hold the counters, whatever the call's
+ * shape; the rest need not be zero and is scratch. So calls of any shapes, with weights or
+ * without, may share one that is large enough for each of them.
  */
 size_t kv4_attention_workspace_bytes(int batch, int tokens, int max_new, int max_len, int heads,
                                      int kv_heads, int head_dim, int group, int with_weights);

@@ -352,3 +352,35 @@ def test_eviction_leaves_a_missing_page_where_it_is(D, group, page):
         assert gone.any() and not gone.all()
         for x, moved, old in zip(*(c.get(0, h, budget) for c in (res[1][1], res[0][1], before))):
             assert np.array_equal(x, np.where(gone[:, None], old, moved))
+
+
+# ---- one workspace for calls of any shape -------------------------------------------------
+def test_one_workspace_for_calls_of_any_shape():
+    """Larger and smaller batches, few rows and prompts, with weights and without: each call gives
+    what it gives with a workspace of its own."""
+    D, H, group = 128, 2, 64
+    shapes = [([3000], [1], 4), ([3000] * 40, [1] * 40, 4), ([2000] * 48, [2] * 48, 12),
+              ([3000], [300], 4), ([2000] * 48, [2] * 48, 12), ([3000, 700, 90], [1, 5, 3], 8),
+              ([3000, 2000], [150, 1], 4), ([500] * 90, [3] * 90, 6), ([3000], [1], 4)]
+    batch, g = _random([3000], H, D, group, 64, 50)
+
+    def size(lens, new, heads, weights):
+        return w4.kv4_attention_workspace_bytes(len(lens), sum(new), max(new), max(lens), heads, H,
+                                                D, group, weights)
+
+    shared = torch.zeros(max(size(*s, True) for s in shapes), dtype=torch.uint8, device=DEV)
+    for weights in (True, False, True):
+        for lens, new, heads in shapes:
+            q = _bf16(g.standard_normal((sum(new), heads, D)))
+            args = (q, batch.cache, _gpu(np.repeat(batch.table, len(lens), 0)),
+                    _gpu(np.array(lens, np.int32)), _gpu(_starts(new)), max(lens), max(new))
+            res = []
+            for ws in (shared, torch.zeros(size(lens, new, heads, weights), dtype=torch.uint8,
+                                           device=DEV)):
+                out = torch.full_like(q, 9.0)
+                w = torch.full((len(lens), H, max(lens)), 9.0, device=DEV) if weights else None
+                w4.kv4_attention(*args, group=group, out=out, weights_out=w, workspace=ws)
+                res.append((out, w))
+            assert torch.equal(res[0][0], res[1][0])
+            assert not weights or torch.equal(res[0][1], res[1][1])
+    assert w4.w4a16_device_status() == 0
