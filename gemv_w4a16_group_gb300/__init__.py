@@ -678,13 +678,25 @@ def _kv4_weights(t, name: str, batch: int, kv_heads: int):
     return _dev(t, name, torch.float32), shape[2]
 
 
-def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
-    """A result for a call on `stream`, allocated on it (the caching allocator reuses a freed
-    block in the order of the stream it was allocated on)."""
-    if isinstance(stream, torch.cuda.Stream):
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=like.device)
-    return torch.empty(shape, dtype=dtype, device=like.device)  # half of new_empty's time
+def _torch_stream(stream):
+    """A stream argument as torch's, None for the current stream. Raw handles are wrapped (0 and 1
+    are names of the default stream)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    return torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+
+
+def _new(like: torch.Tensor, shape, dtype, stream, zero: bool = False) -> torch.Tensor:
+    """A result or scratch for a call on `stream`, allocated (and zero-filled) on it: the caching
+    allocator reuses a freed block in the order of the stream it was allocated on."""
+    stream = _torch_stream(stream)
+    if stream is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)  # half of new_empty's time
+        return t.zero_() if zero else t
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t.zero_() if zero else t
 
 
 def _result(t, name: str, like: torch.Tensor, shape, dtype, stream):
@@ -752,12 +764,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
     if workspace is None:
         workspace = _new(q, kv4_attention_workspace_bytes(
             batch, T, max_new, max_len, heads, kv_heads, head_dim, group,
-            weights_out is not None), torch.uint8, stream)
-        if isinstance(stream, torch.cuda.Stream):
-            with torch.cuda.stream(stream):
-                workspace.zero_()
-        else:
-            workspace.zero_()
+            weights_out is not None), torch.uint8, stream, zero=True)
     out, out_p = _result(out, "out", q, (T, heads, head_dim), torch.bfloat16, stream)
     wp, wl = _kv4_weights(weights, "weights", batch, kv_heads)
     op, ol = _kv4_weights(weights_out, "weights_out", batch, kv_heads)

@@ -354,6 +354,46 @@ def test_eviction_leaves_a_missing_page_where_it_is(D, group, page):
             assert np.array_equal(x, np.where(gone[:, None], old, moved))
 
 
+# ---- streams ------------------------------------------------------------------------------
+def test_a_raw_stream_handle():
+    """A call on a raw handle runs on that stream alone, its scratch and results included: nothing
+    of it waits for the current stream, which is kept busy meanwhile."""
+    batch, g = _random([3000, 700], 2, 128, 64, 64, 52)
+    table, lens = _gpu(batch.table), batch.lens_t()
+    spare = torch.zeros((8,) + batch.cache.shape[1:], dtype=torch.uint8, device=DEV)
+    cache = torch.cat([batch.cache, spare])
+    out_table = _gpu(np.arange(8, dtype=np.int32).reshape(2, 4) + batch.pages)
+    weights = _gpu(g.random((2, 2, 3000)).astype(np.float32))
+    calls = []
+    for new in (1, 30, 90):
+        starts = _gpu(_starts([new, new]))
+        q = _bf16(g.standard_normal((2 * new, 8, 128)))
+        calls.append(lambda s, q=q, new=new, starts=starts: [w4.kv4_attention(
+            q, cache, table, lens, starts, 3000, new, stream=s)])
+    starts = _gpu(_starts([300, 90]))
+    calls.append(lambda s: w4.kv4_read(cache, table, lens, starts, 390, 128, stream=s))
+    calls.append(lambda s: w4.kv4_evict(cache, table, lens, weights, out_table, 200, 3000, 128,
+                                        first=1, recent=9, stream=s))
+    want = [call(None) for call in calls]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for call in calls:  # allocations that wait for the device are behind us
+        call(side.cuda_stream)
+    side.synchronize()
+    torch.cuda._sleep(400_000_000)
+    busy = torch.cuda.Event()
+    busy.record()
+    got = [call(side.cuda_stream) for call in calls]
+    side.synchronize()
+    assert not busy.query()
+    got = [[t.cpu() for t in r] for r in got]
+    for a, b in zip(want, got):
+        assert all(torch.equal(x.cpu(), y) for x, y in zip(a, b))
+    for handle in (0, torch.cuda.default_stream().cuda_stream):
+        assert torch.equal(calls[0](handle)[0], want[0][0])
+    assert w4.w4a16_device_status() == 0
+
+
 # ---- one workspace for calls of any shape -------------------------------------------------
 def test_one_workspace_for_calls_of_any_shape():
     """Larger and smaller batches, few rows and prompts, with weights and without: each call gives

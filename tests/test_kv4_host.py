@@ -180,3 +180,32 @@ def test_reference_layout_words():
         w = cache.data[0, 0, 0].view(np.uint32)
         v0 = (8 * D + 64 * 2) // 4
         assert w[kw] == 9 << kbit and w[v0 + vw] == 9 << vbit and np.count_nonzero(w) == 2
+
+
+@pytest.mark.parametrize("stream,on", [(None, None), (0, "default"), (1, "default"),
+                                       (0x5550, 0x5550)])
+@pytest.mark.parametrize("zero", [False, True])
+def test_memory_of_a_call_is_its_streams(cuda_lib, monkeypatch, stream, on, zero):
+    """Scratch and results of a call on a raw handle are allocated, and filled, under it."""
+    import contextlib
+
+    import gemv_w4a16_group_gb300 as w4
+
+    under, seen = [None], []
+
+    @contextlib.contextmanager
+    def enter(s):
+        under.append(s)
+        yield
+        under.pop()
+
+    def empty(*args, real=torch.empty, **kw):
+        seen.append(under[-1])
+        return real(*args, **kw)
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: handle)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(torch, "empty", empty)
+    t = w4._new(torch.zeros(1), (5,), torch.uint8, stream, zero=zero)
+    assert seen == [on] and t.shape == (5,) and (not zero or not t.any())
