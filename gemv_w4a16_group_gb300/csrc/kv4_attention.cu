@@ -12,9 +12,9 @@
 // the offset's sum taken out again; the MMA truncates its sums, and over 131072 tokens the offset,
 // hundreds of times the result, cost 1.2 % of it. Centring the pairs cures that for four more
 // operations.) q is FP16 under a power of two a row, exact down to 2^-27 of the row's largest; p s
-// is rounded to FP16 under the largest scale's power of two that the row has met (relative 2^-12;
-// BF16's 2^-9 was twice the output's own rounding error). Sums, maxima and the softmax's
-// statistics are fp32.
+// is rounded to FP16, a power of two a row above it (kLift: relative 2^-12 of itself or 2^-28 of the
+// row's largest; BF16's 2^-9 was twice the output's own rounding error). Sums, maxima and the
+// softmax's statistics are fp32.
 //
 // What bounds it: the cache is read once (D + 8 D / group bytes a token and head), at 4 heads a
 // key/value head about 8 operations a byte, so the aim is the memory's rate. 64 sequences of 8192
@@ -96,12 +96,6 @@ __device__ __forceinline__ void value_pairs(uint32_t w, uint32_t (&p)[4]) {
   p[1] = w & 0x00F000F0u;
   p[2] = (w >> 6) & 0x003C003Cu;
   p[3] = (w >> 6) & 0x03C003C0u;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // D(16x8) = A(16x16) B(16x8), FP16 in, fp32 out.

@@ -85,13 +85,7 @@ __device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
   asm("min.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
   return y;
 }
-// (x, y) += a and (x, y) *= a, and |x| or the largest so far; a NaN stays.
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
-      "add.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
+// (x, y) *= a, and |x| or the largest so far; a NaN stays.
 __device__ __forceinline__ void mul2(float& x, float& y, float a) {
   asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\t"
       "mul.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"

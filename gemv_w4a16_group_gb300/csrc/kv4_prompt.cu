@@ -419,7 +419,6 @@ __device__ __forceinline__ int key_units_of(const Kv4Seq& s, int G, int kt) {
   return max(1, (s.m * G + kTileRows - 1) / kTileRows - first_row_tile(s, G, kt));
 }
 
-// Where every sequence's and row tile's units begin.
 // Largest i < n with x[i] <= u, x non-decreasing from 0.
 template <typename T>
 __device__ __forceinline__ int last_at_most(const T* x, int n, T u) {
@@ -631,11 +630,6 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -656,13 +650,6 @@ __device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float
       "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b), "f"(c));
-}
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, s;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
-      "add.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
 }
 
 constexpr int kRing = 4;
@@ -689,12 +676,12 @@ struct Smem {
   static constexpr uint32_t alloc = total + 1024;
 };
 
-// A segment: the part of one (sequence, head, row tile) in this CTA's range of units.
 // Halves of a row tile that have rows.
 __device__ __forceinline__ int halves_of(const Kv4Seq& s, int G, int rt) {
   return s.m * G - rt * kTileRows > 128 ? 2 : 1;
 }
 
+// A segment: the part of one (sequence, head, row tile) in this CTA's range of units.
 struct Segment {
   int b, h, rt;
   int units;   // of the item
