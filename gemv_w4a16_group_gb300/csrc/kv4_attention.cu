@@ -504,7 +504,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
     auto compute = [&](auto mask, uint32_t base, int key0, volatile uint32_t* stage_bits) {
       constexpr bool kMasked = decltype(mask)::value;
       const uint32_t has = kMasked ? *stage_bits : kAllRecords;
-      // ---- logits, times 1 / unscale. Set j holds record j's tokens (packed: the lane's record's)
+      // ---- logits. Set j holds record j's tokens (packed: the lane's record's)
       constexpr int kSets = PACK ? 1 : kUnitRecords;
       const int half = c >> 1;  // packed: this lane's record
       float s[kSets][NT][4];
@@ -526,6 +526,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
           for (int i = 0; i < 4; ++i) {
             const int row = PACK ? 2 * (c & 1) + (i & 1) : nt * 8 + 2 * c + (i & 1);
             const int key = key0 + 16 * (PACK ? half : j) + r + (i >= 2 ? 8 : 0);
+            // rounded before the maximum comes off: a logit of 2^28 and more would overflow P by
+            // what an fma keeps of it beyond the maximum
+            s[j][nt][i] = __fmul_rn(s[j][nt][i], unscale[nt][i & 1]);
             if constexpr (kMasked) {
               if (key > (row < rows ? seq.n - seq.m + (row0 + row) / G : -1) ||
                   !((has >> (PACK ? half : j)) & 1u))
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
             if constexpr (LOGITS) {
               if (row < rows && key < seq.n)
                 ws.logits[((static_cast<size_t>(cur.b) * a.c.kv_heads + cur.h) * a.max_new * G +
-                           row0 + row) * ws.row_len + key] = s[j][nt][i] * unscale[nt][i & 1];
+                           row0 + row) * ws.row_len + key] = s[j][nt][i];
             }
           }
       };
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
 #pragma unroll
             for (int j = 1; j < kSets; ++j)
               v = fmaxf(v, fmaxf(s[j][nt][i], s[j][nt][i + 2]));
-            fits = fits && v * unscale[nt][i] <= mx[nt][i] + kLag;
+            fits = fits && v <= mx[nt][i] + kLag;
           }
       }
       if (kMasked || !__all_sync(0xffffffffu, fits)) {
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             if constexpr (PACK) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            const float now = fmaxf(mx[nt][i], v * unscale[nt][i]);
+            const float now = fmaxf(mx[nt][i], v);
             uint32_t top = 0;  // largest product, fp32 bits
 #pragma unroll
             for (int j = 0; j < kSets; ++j)
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
                                            (16 * g + r + 8 * u) * 4) & 0xFFFFu;
                   if (z < 0x7F80u) sc = max(sc, z);
                 }
-                top = max(top, __float_as_uint(ex2(fmaf(x, unscale[nt][i], -now)) *
+                top = max(top, __float_as_uint(ex2(x - now) *
                                                __uint_as_float(sc << 16)));
               }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
@@ -693,8 +696,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float m = mx[nt][i & 1];
-            p[nt][i] = ex2(fmaf(s[j][nt][i], unscale[nt][i & 1],
-                                kMasked && m == -INFINITY ? 0.f : -m));
+            p[nt][i] = ex2(s[j][nt][i] - (kMasked && m == -INFINITY ? 0.f : m));
             sum[nt][i & 1] += p[nt][i];
             pd[nt][i] = p[nt][i] * down[nt][i & 1];
           }

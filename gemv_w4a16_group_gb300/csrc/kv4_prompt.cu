@@ -52,6 +52,10 @@ struct TokenMeta {
 };
 constexpr int kByToken = 1 << 20;
 constexpr int kSpread = 8;  // exponents between a tile's tokens that one power of two bridges
+// An fma takes the maximum off a logit (base 2) up to this size; beyond it the maximum's own rounding
+// would be seen (and overflow P from 2^28 on), so the logit is rounded first, as the maximum was.
+constexpr float kHuge = 1048576.f;
+constexpr float kByRow = -1.f;
 // ev of a tile whose values are all 0: below any other's, so that it makes no row's product larger.
 constexpr int kNoValue = -200;
 // P reaches 2^kLift where its row's largest product is made, and 2^15 once that product lags.
@@ -80,7 +84,11 @@ struct PromptWs {
   int32_t* pre;       // [batch, row_tiles + 1]: units of a head before a row tile
   KeyMeta* meta;      // [batch, kv_heads, key_tiles]
   TokenMeta* tokens;  // [batch, kv_heads, key_tiles, 128], of the tiles with kByToken
-  float* qf;          // [batch, kv_heads, row_tiles]: logit (base 2) per image product, without kf
+  // [batch, kv_heads, row_tiles, 256]: logit (base 2) per image product, without kf
+  float* row_qf;
+  // [batch, kv_heads, row_tiles]: the same of all rows, for the weights; kByRow: the weights go by
+  // row_qf, as there are kHuge logits
+  float* qf;
   uint8_t* q_img;     // [batch, kv_heads, row_tiles] x 256 (D + 16) FP16
   uint8_t* kv_img;    // [batch, kv_heads, key_tiles] x (K 128 (D + 16), V^T D 128) FP16
   uint32_t* counters; // [batch, kv_heads, row_tiles, 2], zeroed beside the images
@@ -343,7 +351,6 @@ __device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
   int token = (row0 + r0) / G, head = (row0 + r0) % G;
   const int token_step = kStep / G, head_step = kStep % G;
   uint4 v[kPer];
-  uint32_t tops = 0;  // largest magnitudes of even and odd dims, BF16 bits
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     v[i] = make_uint4(0, 0, 0, 0);
@@ -357,6 +364,7 @@ __device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
       ++token;
     }
   }
+  uint32_t tops = 0;  // largest magnitudes of even and odd dims, BF16 bits
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
     tops = __vmaxu2(__vmaxu2(__vmaxu2(tops, v[i].x & 0x7FFF7FFFu), v[i].y & 0x7FFF7FFFu),
@@ -376,12 +384,15 @@ __device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
     top = block_max(top, red);
   }
   const int up = up_of(top << 16);
-  const float f = a.scale < 0.f ? -pow2f(up) : a.scale > 0.f ? pow2f(up) : 0.f;
-  if (threadIdx.x == 0) ws.qf[at] = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e * pow2f(-up);
+  const float qf1 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e;
+  const float sign = a.scale < 0.f ? -1.f : a.scale > 0.f ? 1.f : 0.f;
+  const float f = sign * pow2f(up), qf = qf1 * pow2f(-up);
+  if (threadIdx.x == 0) ws.qf[at] = qf;
   uint8_t* img = ws.q_img + at * Img<D>::kQ;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = r0 + i * kStep;
+    if (ch == 0) ws.row_qf[at * kTileRows + r] = qf;
     const float q[8] = {bf16_lo(v[i].x) * f, bf16_hi(v[i].x) * f, bf16_lo(v[i].y) * f,
                         bf16_hi(v[i].y) * f, bf16_lo(v[i].z) * f, bf16_hi(v[i].z) * f,
                         bf16_lo(v[i].w) * f, bf16_hi(v[i].w) * f};
@@ -958,39 +969,41 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // first key that some row of this half does not see
         const int first_row = g.rt * kTileRows + half * 128;
         const int clear = first_row + 127 < rows ? seq.n - seq.m + first_row / G + 1 : 0;
-        const float qf = ws.qf[item(g)];
+        const float qf = ws.row_qf[item(g) * kTileRows + half * 128 + row];
         const size_t tile0 = (static_cast<size_t>(g.b) * a.c.kv_heads + g.h) * ws.key_tiles;
         const KeyMeta* meta = ws.meta + tile0;
         KeyMeta km = meta[g.lo];
         // the running maximum; the sum of probabilities under it; and, under it too, the exponent
         // (a whole number) that O and the row's products come under
         float m = -INFINITY, l = 0.f, e = 0.f;
+        bool huge = false;  // a row of the warp has met a logit beyond kHuge
         // a tile whose largest logit (base 2) is t, and whose largest product is `product`
-        auto meet = [&](float t, float product, bool first) {
-          const bool raise = t > m + 8.f || product - m > e + 15.f;
-          if (__any_sync(0xffffffffu, raise)) {
-            float f = 1.f;
-            if (raise) {
-              const float top = fmaxf(m, t), old = e + (m - top);
-              l *= ex2(m - top);
-              const float now_e = fmaxf(ceilf(old), ceilf(product - top) - kLift);
-              f = ex2(old - now_e);
-              m = top;
-              e = now_e;
-            }
-            if (!first && __any_sync(0xffffffffu, f != 1.f)) {
+        auto raises = [&](float t, float product) {
+          return t > m + 8.f || product - m > e + 15.f;
+        };
+        auto raise = [&](float t, float product, bool first) {
+          float f = 1.f;
+          if (raises(t, product)) {
+            const float top = fmaxf(m, t), old = e + (m - top);
+            l *= ex2(m - top);
+            const float now_e = fmaxf(ceilf(old), ceilf(product - top) - kLift);
+            f = ex2(old - now_e);
+            m = top;
+            e = now_e;
+          }
+          if (!first && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld_16cols(t_o + 16 * c, o);
-                tmem_ld_wait();
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld_16cols(t_o + 16 * c, o);
+              tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st_16cols(t_o + 16 * c, o);
-              }
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st_16cols(t_o + 16 * c, o);
             }
           }
         };
+        auto is_huge = [](float t) { return fabsf(t) > kHuge && t != -INFINITY; };
         auto hand_over = [&]() {
           tmem_st_wait();
           tc_fence_before_sync();
@@ -1003,100 +1016,111 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const float cf = fmaxf(qf * now.kf, 1e-37f);
           if (!wait(&s_full[half], s_phase)) break;
           const int see = last_key - i * kTileKeys;  // columns up to this one are visible
-          if (now.ev == kByToken) {
-            // powers of two a token: S is read twice, 32 columns at a time
-            const TokenMeta* tok = ws.tokens + (tile0 + i) * kTileKeys;
-            uint32_t x[32];
-            auto logits = [&](int c) {
-              tmem_ld_32cols(t_s + 32 * c, x);
-              tmem_ld_wait();
+          if (now.ev != kByToken && !huge) {
+            float s[128];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float kf = tok[32 * c + j].kf;
-                x[j] = __float_as_uint(32 * c + j <= see && kf != 0.f
-                                           ? __uint_as_float(x[j]) * fmaxf(qf * kf, 1e-37f)
-                                           : -INFINITY);
-              }
-            };
-            float t = -INFINITY, product = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              logits(c);
+            for (int c = 0; c < 4; ++c)
+              tmem_ld_32cols(t_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
+            tmem_ld_wait();
+            if ((i + 1) * kTileKeys > clear) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                t = fmaxf(t, __uint_as_float(x[j]));
-                product = fmaxf(product, __uint_as_float(x[j]) + tok[32 * c + j].ev);
-              }
+              for (int j = 0; j < 128; ++j) s[j] = j <= see ? s[j] : -INFINITY;
             }
-            meet(t, product, i == g.lo);
-            const float under = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {  // P's columns are behind those of S still to be read
-              logits(c);
-              float acc = 0.f, p[32];
+            float top[8];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float y = __uint_as_float(x[j]) - under;
-                acc += ex2(y);
-                p[j] = ex2(y + (tok[32 * c + j].ev - e));
-              }
-              l += acc;
-              uint32_t pairs[16];
+            for (int x = 0; x < 8; ++x) top[x] = max3(s[x], s[x + 8], s[x + 16]);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) pairs[j] = f16x2_bits(p[2 * j], p[2 * j + 1]);
-              tmem_st_16cols(t_s + 16 * c, pairs);
+            for (int j = 24; j < 120; j += 16) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) top[x] = max3(top[x], s[j + x], s[j + 8 + x]);
             }
-            hand_over();
-            continue;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) top[x] = fmaxf(top[x], s[120 + x]);
+            const float best = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]),
+                                    fmaxf(top[6], top[7]));
+            const float ev = static_cast<float>(now.ev);
+            const float t = best * cf;  // -inf stays -inf: cf is positive
+            if (__any_sync(0xffffffffu, raises(t, t + ev) || is_huge(t))) {
+              huge = __any_sync(0xffffffffu, is_huge(t));
+              if (!huge) raise(t, t + ev, i == g.lo);
+            }
+            if (!huge) {
+              // P is the probability (under m) times 2^-down, l takes that out again. Past 2^60 the
+              // tile's values are nothing beside the row's products and P is 0; before 2^-126 its
+              // probabilities are nothing beside l
+              const float down = fminf(e - ev, 60.f);
+              const float bias = -((m == -INFINITY ? 0.f : m) + down);
+              const float undo = pow2f(static_cast<int>(fmaxf(down, -126.f)));
+              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t p[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  float x = s[64 * c + 2 * j], y = s[64 * c + 2 * j + 1];
+                  fma2(x, y, cf, bias);
+                  x = ex2(x);
+                  y = ex2(y);
+                  add2(acc[2 * (j & 1)], acc[2 * (j & 1) + 1], x, y);
+                  p[j] = f16x2_bits(x, y);
+                }
+                tmem_st_32cols(t_s + 32 * c, p);
+              }
+              hand_over();
+              l = fmaf((acc[0] + acc[1]) + (acc[2] + acc[3]), undo, l);
+              continue;
+            }
           }
-          float s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            tmem_ld_32cols(t_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
-          tmem_ld_wait();
-          if ((i + 1) * kTileKeys > clear) {
-#pragma unroll
-            for (int j = 0; j < 128; ++j) s[j] = j <= see ? s[j] : -INFINITY;
-          }
-          float top[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) top[x] = max3(s[x], s[x + 8], s[x + 16]);
-#pragma unroll
-          for (int j = 24; j < 120; j += 16) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x) top[x] = max3(top[x], s[j + x], s[j + 8 + x]);
-          }
-#pragma unroll
-          for (int x = 0; x < 8; ++x) top[x] = fmaxf(top[x], s[120 + x]);
-          const float best = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]),
-                                  fmaxf(top[6], top[7]));
-          const float ev = static_cast<float>(now.ev);
-          meet(best * cf, best * cf + ev, i == g.lo);  // -inf stays -inf: cf is positive
-          // P is the probability (under m) times 2^-down, l takes that out again. Past 2^60 the
-          // tile's values are nothing beside the row's products and P is 0; before 2^-126 its
-          // probabilities are nothing beside l
-          const float down = fminf(e - ev, 60.f);
-          const float bias = -((m == -INFINITY ? 0.f : m) + down);
-          const float undo = pow2f(static_cast<int>(fmaxf(down, -126.f)));
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t p[32];
+          // powers of two a token, or logits rounded before the maximum comes off: S is read
+          // twice, 32 columns at a time
+          const TokenMeta* tok = ws.tokens + (tile0 + i) * kTileKeys;
+          const TokenMeta tile{now.kf, static_cast<float>(now.ev)};
+          auto token = [&](int j) { return now.ev == kByToken ? tok[j] : tile; };
+          uint32_t x[32];
+          auto logits = [&](int c) {
+            tmem_ld_32cols(t_s + 32 * c, x);
+            tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              float x = s[64 * c + 2 * j], y = s[64 * c + 2 * j + 1];
-              fma2(x, y, cf, bias);
-              x = ex2(x);
-              y = ex2(y);
-              add2(acc[2 * (j & 1)], acc[2 * (j & 1) + 1], x, y);
-              p[j] = f16x2_bits(x, y);
+              const float kf = token(32 * c + j).kf;
+              x[j] = __float_as_uint(
+                  32 * c + j <= see && kf != 0.f
+                      ? __fmul_rn(__uint_as_float(x[j]), fmaxf(qf * kf, 1e-37f)) : -INFINITY);
             }
-            tmem_st_32cols(t_s + 32 * c, p);
+          };
+          float t = -INFINITY, product = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            logits(c);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              t = fmaxf(t, __uint_as_float(x[j]));
+              product = fmaxf(product, __uint_as_float(x[j]) + token(32 * c + j).ev);
+            }
+          }
+          huge = huge || __any_sync(0xffffffffu, is_huge(t));
+          raise(t, product, i == g.lo);
+          const float under = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {  // P's columns are behind those of S still to be read
+            logits(c);
+            float acc = 0.f, p[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float y = __uint_as_float(x[j]) - under;
+              acc += ex2(y);
+              p[j] = ex2(y + (token(32 * c + j).ev - e));
+            }
+            l += acc;
+            uint32_t pairs[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pairs[j] = f16x2_bits(p[2 * j], p[2 * j + 1]);
+            tmem_st_16cols(t_s + 16 * c, pairs);
           }
           hand_over();
-          l = fmaf((acc[0] + acc[1]) + (acc[2] + acc[3]), undo, l);
         }
         if (!ok || !wait(&o_full[half], o_phase)) break;
+        if (huge && ws.lse2 != nullptr && lane == 0) ws.qf[item(g)] = kByRow;
         // ---- O is complete
         const float vf = scalbnf(1.f, static_cast<int>(e));
         const bool whole = g.lo == 0 && g.hi == g.tiles;
@@ -1477,7 +1501,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       float qf_next = g.lo < g.hi ? qf_of(g.lo) : 0.f;
       for (int i = g.lo; i < g.hi; ++i, ++n) {
         const int s = n & 1, rt = g.first + i;
-        const float cf = fmaxf(qf_next * kf, 1e-37f);
+        const float qf = qf_next;
+        const float cf = fmaxf(qf * kf, 1e-37f);
         if (i + 1 < g.hi) qf_next = qf_of(i + 1);
         ok = ok && mbar_wait_bounded(&lse_full[n % kLseRing], (n / kLseRing) & 1u, abort_flag,
                                      status, limit) &&
@@ -1487,6 +1512,28 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         tc_fence_after_sync();
         const float* lse = lse_s + (n % kLseRing) * kTileRows + part * kSumCols;
         float p[4] = {0.f, 0.f, 0.f, 0.f};
+        if (qf == kByRow) {
+          // a factor a row, and logits rounded before the log-sum comes off, as it was made
+          const float* rows =
+              ws.row_qf + (head() * ws.row_tiles + rt) * kTileRows + part * kSumCols;
+          const int64_t hide = need - static_cast<int64_t>(rt) * kTileRows - part * kSumCols;
+#pragma unroll 1
+          for (int c = 0; c < kSumCols; c += 16) {
+            float x[16];
+            tmem_ld_16cols(t_s + s * 256 + c, reinterpret_cast<uint32_t*>(x));
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float f = fmaxf(rows[c + j] * kf, 1e-37f);
+              p[j & 3] += c + j < hide ? 0.f : ex2(fminf(__fmul_rn(x[j], f) + lse[c + j], 0.f));
+            }
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[s]);
+          acc += (p[0] + p[1]) + (p[2] + p[3]);
+          continue;
+        }
 #pragma unroll
         for (int c = 0; c < kSumCols; c += 32) {
           float x[32];
@@ -1567,8 +1614,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 }
 
 struct Layout {
-  size_t plan, starts, order, base, pre, meta, token_meta, qf, q_img, kv_img, counters, parts, lse2,
-      kbase, kpre, kcounters, sums, total;
+  size_t plan, starts, order, base, pre, meta, token_meta, qf, row_qf, q_img, kv_img, counters, parts,
+      lse2, kbase, kpre, kcounters, sums, total;
   int key_tiles, row_tiles;
 };
 
@@ -1595,6 +1642,7 @@ Layout layout(int batch, int tokens, int max_new, int max_len, int heads, int kv
   l.meta = take(bh * l.key_tiles * sizeof(KeyMeta));
   l.token_meta = take(bh * l.key_tiles * kTileKeys * sizeof(TokenMeta));
   l.qf = take(bh * l.row_tiles * 4);
+  l.row_qf = take(bh * l.row_tiles * kTileRows * 4);
   l.q_img = take(bh * l.row_tiles * kTileRows * (D + 16) * 2);
   l.kv_img = take(bh * l.key_tiles * kTileKeys * (2 * D + 16) * 2);
   l.parts = take(static_cast<size_t>(device_sm_count()) * 4 * (D + 2) * 128 * 4);
@@ -1623,6 +1671,7 @@ cudaError_t run(const Kv4AttentionArgs& a, cudaStream_t stream) {
   ws.meta = reinterpret_cast<KeyMeta*>(w + l.meta);
   ws.tokens = reinterpret_cast<TokenMeta*>(w + l.token_meta);
   ws.qf = reinterpret_cast<float*>(w + l.qf);
+  ws.row_qf = reinterpret_cast<float*>(w + l.row_qf);
   ws.q_img = w + l.q_img;
   ws.kv_img = w + l.kv_img;
   ws.counters = reinterpret_cast<uint32_t*>(w + l.counters);

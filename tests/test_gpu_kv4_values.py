@@ -12,9 +12,11 @@ Bounds, from the arithmetic (a token's dim stands for c s + m, c a code of 0..15
     own rounding, 2^-22 |lse|;
   * a weight: each probability by a factor within e^(+-2E), and 2^-16 of itself for exponentials
     and sums; the sum with what was there before is rounded once, 2^-23 of it;
-  * out: rounded to BF16, 2^-9 of itself (and of itself with its error: 2^-8.9); probabilities (times
-    scales) rounded to FP16, 2^-12, a value's scale, minimum and sum likewise, each at most `most`:
-    2^-10 reach covers them, reach = sum p most; and (e^2E - 1) reach."""
+  * out: 2^-8.9 |out| + 2^-10 reach, reach = sum p most, and (e^2E - 1) reach. Rounding to BF16 takes
+    up to 2^-8 |out|; where reach is twice |out| or more, as in sums of many values, the terms
+    leave 2^-11 reach and more for the FP16 roundings of probabilities (times scales) and images,
+    2^-11 each of a token's part and of either sign. So this is a bound on the kernels as they
+    are, not one that every correct rounding keeps: a row of one value has its own (`sharp`)."""
 import numpy as np
 import pytest
 import torch
@@ -76,10 +78,12 @@ class Batch:
 
 
 def _check(batch, q, new, scale=None, weights=True, table=None, gone=None, rows=None, status=0,
-           copies=1):
+           copies=1, sharp=None):
     """Runs the attention of q (fp32 [T, heads, D]) and holds it to the bounds. gone[b]: positions
     that the call leaves out; rows: which of the T rows to look at; copies: the batch that many
-    times over in one call, on the same pages, so that a CTA's share is long."""
+    times over in one call, on the same pages, so that a CTA's share is long; sharp: rows whose
+    logits lie so far apart that one token has all of the probability, whatever E (their out is one
+    value to BF16, 2^-8 of itself, from an image of three roundings to FP16, 2^-9 most)."""
     q = ref.bf16(q)
     T, heads, D = q.shape
     H, G = batch.H, heads // batch.H
@@ -131,10 +135,13 @@ def _check(batch, q, new, scale=None, weights=True, table=None, gone=None, rows=
                      * np.where(hide, 0, k_s[None]).max(1) + 2.0 ** -20 * L)
             else:
                 E = np.zeros(m)
-            grow = np.expm1(2 * E)
+            grow = np.expm1(2 * (E if sharp is None else np.where(sharp[mine], 0, E)))
             want, reach = p @ v, p @ v_most
             ok = look[mine]
             tol = 2.0 ** -8.9 * np.abs(want) + (2.0 ** -10 + grow)[:, None] * reach
+            if sharp is not None:
+                one = 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * reach
+                tol = np.where(sharp[mine][:, None], one, tol)
             here, z = got[:, mine, h], lse_g[:, mine, h]
             assert np.isfinite(here[:, ok]).all()
             over = (np.abs(here - want) - tol)[:, ok]
@@ -294,6 +301,36 @@ def test_hidden_tokens_of_any_size(heads, new, D, group, size):
     v[n - last:] *= size
     rows = np.arange(new) < new - last
     _check(Batch([k], [v], group, 64), g.standard_normal((new, heads, D)), [new], rows=rows)
+
+
+def _sharp(batch, q, new, big, power):
+    """Which rows of `big` (one sequence, queries of 2^power) have a best logit ahead of the next by
+    far more than its error, 2^-20 L, L about 50 2^power, in all heads."""
+    heads, D = q.shape[1:]
+    x, n = ref.bf16(q).astype(np.float64), batch.lens[0]
+    big = big.copy()
+    for h in range(heads):
+        k = batch.k[0][0][:, h // (heads // batch.H)]
+        for i in np.flatnonzero(big):
+            s = np.sort(D ** -0.5 * x[i, h] @ k[:n - new + i + 1].T)
+            big[i] &= s[-1] - s[-2] > 2.0 ** (power - 10)
+    return big
+
+
+@pytest.mark.parametrize("heads,new", [(4, 130), (8, 300), (8, 4), (4, 24)])
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("power", [14, 24, 40])
+def test_logits_of_any_size(heads, new, D, group, power):
+    """Logits far beyond what exponentials of a difference rounded once would bear: a row is the
+    token of its largest logit."""
+    g = np.random.default_rng(54)
+    n = 600
+    k, v = _normal(g, n, 2, D)
+    q = g.standard_normal((new, heads, D)) * 2.0 ** power
+    batch = Batch([k], [v], group, 64)
+    big = _sharp(batch, q, new, np.ones(new, bool), power)
+    assert big.mean() > 0.8
+    _check(batch, q, [new], rows=None if big.all() else big, sharp=big)
 
 
 # ---- pages that are not there -------------------------------------------------------------
