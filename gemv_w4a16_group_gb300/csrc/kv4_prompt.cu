@@ -16,7 +16,7 @@
 //    to FP16 under a power of two a tile (2^-11 of a value, a quarter of the output's rounding).
 //    A tile whose tokens differ by 2^8 or more (a token that is larger than the rest would take
 //    bits from them even in rows that do not see it) has powers of two a token, and the softmax a
-//    slower body for it.
+//    slower body for it; 256 rows of queries that differ by 2^12 have them a row.
 //    A key is exact: with c the code less 8, c s has at most 3 + 8 significant bits and is an
 //    FP16 number; what is left, (min + 8 s) times the sum of q over the group, goes through 16
 //    more columns, four a group, as FP16 pairs of high and low parts. Rounded keys (2^-12) put
@@ -56,6 +56,7 @@ constexpr int kSpread = 8;  // exponents between a tile's tokens that one power 
 // would be seen (and overflow P from 2^28 on), so the logit is rounded first, as the maximum was.
 constexpr float kHuge = 1048576.f;
 constexpr float kByRow = -1.f;
+constexpr int kRowSpread = 12;  // the same between a tile's rows
 // ev of a tile whose values are all 0: below any other's, so that it makes no row's product larger.
 constexpr int kNoValue = -200;
 // P reaches 2^kLift where its row's largest product is made, and 2^15 once that product lags.
@@ -87,7 +88,7 @@ struct PromptWs {
   // [batch, kv_heads, row_tiles, 256]: logit (base 2) per image product, without kf
   float* row_qf;
   // [batch, kv_heads, row_tiles]: the same of all rows, for the weights; kByRow: the weights go by
-  // row_qf, as there are kHuge logits
+  // row_qf, as the rows have powers of two of their own or kHuge logits
   float* qf;
   uint8_t* q_img;     // [batch, kv_heads, row_tiles] x 256 (D + 16) FP16
   uint8_t* kv_img;    // [batch, kv_heads, key_tiles] x (K 128 (D + 16), V^T D 128) FP16
@@ -128,14 +129,21 @@ __device__ __forceinline__ int units_of(const Kv4Seq& s, int G, int rt) {
 // ---- images ------------------------------------------------------------------------------
 constexpr int kImgThreads = 512;
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* sm) {
-  v = __reduce_max_sync(0xffffffffu, v);
+// Largest a and b (16 bits) of the block, a in the low half.
+__device__ __forceinline__ uint32_t block_max(uint32_t a, uint32_t b, uint32_t* sm) {
+  uint32_t v = __reduce_max_sync(0xffffffffu, a) | (__reduce_max_sync(0xffffffffu, b) << 16);
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
   v = sm[0];
 #pragma unroll
-  for (int i = 1; i < kImgThreads / 32; ++i) v = max(v, sm[i]);
+  for (int i = 1; i < kImgThreads / 32; ++i) v = __vmaxu2(v, sm[i]);
   return v;
+}
+// Largest magnitude of eight BF16 values, as bits.
+__device__ __forceinline__ uint32_t top_bits(const uint4& x) {
+  const uint32_t t = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                              __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+  return max(t & 0xFFFFu, t >> 16);
 }
 
 // Exponent that brings a largest magnitude (fp32 bits, finite) to [2^14, 2^15).
@@ -364,34 +372,40 @@ __device__ void row_tile(const Kv4AttentionArgs& a, const PromptWs& ws, int b, i
       ++token;
     }
   }
-  uint32_t tops = 0;  // largest magnitudes of even and odd dims, BF16 bits
+  // the rows' largest magnitudes, BF16 bits, two rows a word; 0 for a row of infinities or NaN
+  uint32_t tops[kPer / 2];
+  uint32_t top = 0, less = 0;  // of all rows (in both halves); 0xFFFF less the smallest but 0
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    tops = __vmaxu2(__vmaxu2(__vmaxu2(tops, v[i].x & 0x7FFF7FFFu), v[i].y & 0x7FFF7FFFu),
-                    __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-  uint32_t top = max(tops & 0xFFFFu, tops >> 16);
-  top = block_max(top, red);
-  if (top >= 0x7F80u) {  // infinities or NaN: the largest of the others
-    top = 0;
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t x = (w[j / 2] >> (16 * (j % 2))) & 0x7FFFu;
-        if (x < 0x7F80u) top = max(top, x);
-      }
-    }
-    __syncthreads();
-    top = block_max(top, red);
+  for (int i = 0; i < kPer; i += 2) {
+    uint32_t t = top_bits(v[i]) | (top_bits(v[i + 1]) << 16);
+#pragma unroll
+    for (int o = 1; o < kChunks; o <<= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+    if ((t & 0xFFFFu) >= 0x7F80u) t &= 0xFFFF0000u;
+    if (t >= 0x7F800000u) t &= 0xFFFFu;
+    tops[i / 2] = t;
+    top = __vmaxu2(top, t);
+    if ((t & 0xFFFFu) != 0u) less = max(less, 0xFFFFu - (t & 0xFFFFu));
+    if ((t >> 16) != 0u) less = max(less, 0xFFFFu - (t >> 16));
   }
-  const int up = up_of(top << 16);
+  top = block_max(max(top & 0xFFFFu, top >> 16), less, red);
+  less = top >> 16;
+  top &= 0xFFFFu;
+  const bool by_row = top != 0u && (top >> 7) - ((0xFFFFu - less) >> 7) >= kRowSpread;
+  const int up_tile = up_of(top << 16);
   const float qf1 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e;
   const float sign = a.scale < 0.f ? -1.f : a.scale > 0.f ? 1.f : 0.f;
-  const float f = sign * pow2f(up), qf = qf1 * pow2f(-up);
-  if (threadIdx.x == 0) ws.qf[at] = qf;
+  const float f_tile = sign * pow2f(up_tile), qf_tile = qf1 * pow2f(-up_tile);
+  if (threadIdx.x == 0) ws.qf[at] = by_row ? kByRow : qf_tile;
   uint8_t* img = ws.q_img + at * Img<D>::kQ;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = r0 + i * kStep;
+    float f = f_tile, qf = qf_tile;
+    if (by_row) {
+      const int up = up_of((tops[i / 2] >> (16 * (i % 2))) << 16);
+      f = sign * pow2f(up);
+      qf = qf1 * pow2f(-up);
+    }
     if (ch == 0) ws.row_qf[at * kTileRows + r] = qf;
     const float q[8] = {bf16_lo(v[i].x) * f, bf16_hi(v[i].x) * f, bf16_lo(v[i].y) * f,
                         bf16_hi(v[i].y) * f, bf16_lo(v[i].z) * f, bf16_hi(v[i].z) * f,

@@ -333,6 +333,26 @@ def test_logits_of_any_size(heads, new, D, group, power):
     _check(batch, q, [new], rows=None if big.all() else big, sharp=big)
 
 
+@pytest.mark.parametrize("heads,new", [(4, 130), (8, 300), (8, 4), (4, 24)])
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("power", [14, 24, 40])
+@pytest.mark.parametrize("at", [0, 7])
+def test_rows_of_any_size(heads, new, D, group, power, at):
+    """Queries of every eighth token are 2^power times the others': each row as near as without
+    them. Theirs see one token alone."""
+    g = np.random.default_rng(53)
+    n = 600
+    k, v = _normal(g, n, 2, D)
+    large = np.arange(new) % 8 == at
+    q = g.standard_normal((new, heads, D))
+    q[large] *= 2.0 ** power
+    batch = Batch([k], [v], group, 64)
+    big = _sharp(batch, q, new, large, power)
+    rows = big | ~large
+    assert rows.mean() > 0.9
+    _check(batch, q, [new], rows=None if rows.all() else rows, sharp=big)
+
+
 # ---- pages that are not there -------------------------------------------------------------
 @pytest.mark.parametrize("D,group,page", FORMS)
 @pytest.mark.parametrize("heads,new", [(4, [1, 1]), (4, [3, 1]), (8, [9, 2]), (4, [130, 1]),
