@@ -632,6 +632,20 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
       }
       if (kMasked || !__all_sync(0xffffffffu, fits)) {
         if (!kMasked && *stage_bits != kAllRecords) return false;
+        float reach[kSets][2];  // largest V scale of the lane's tokens
+#pragma unroll
+        for (int j = 0; j < kSets; ++j)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              const uint32_t z = lds32(base + (PACK ? half : j) * R::kBytes + R::kVParams +
+                                       (16 * g + r + 8 * u) * 4) & 0xFFFFu;
+              if (z < 0x7F80u) top = max(top, z);
+            }
+            reach[j][u] = __uint_as_float(top << 16);
+          }
         int least = 255;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -653,15 +667,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_per_sm(D, NT))
               for (int u = 0; u < 2; ++u) {
                 const float x = s[j][nt][i + 2 * u];
                 if (kMasked && x == -INFINITY) continue;
-                uint32_t sc = 0;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                  const uint32_t z = lds32(base + (PACK ? half : j) * R::kBytes + R::kVParams +
-                                           (16 * g + r + 8 * u) * 4) & 0xFFFFu;
-                  if (z < 0x7F80u) sc = max(sc, z);
-                }
-                top = max(top, __float_as_uint(ex2(x - now) *
-                                               __uint_as_float(sc << 16)));
+                top = max(top, __float_as_uint(ex2(x - now) * reach[j][u]));
               }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
