@@ -12,16 +12,16 @@
 // the offset's sum taken out again; the MMA truncates its sums, and over 131072 tokens the offset,
 // hundreds of times the result, cost 1.2 % of it. Centring the pairs cures that for four more
 // operations.) q is FP16 under a power of two a row, exact down to 2^-27 of the row's largest; p s
-// is rounded to FP16, a power of two a row above it (kLift: relative 2^-12 of itself or 2^-28 of the
-// row's largest; BF16's 2^-9 was twice the output's own rounding error). Sums, maxima and the
-// softmax's statistics are fp32.
+// is rounded to FP16 under a power of two a row (2^-11 of itself or 2^-28 of the row's largest, see
+// kLift; BF16's 2^-8 was twice the output's own rounding error). Sums, maxima and the softmax's
+// statistics are fp32.
 //
 // What bounds it: the cache is read once (D + 8 D / group bytes a token and head), at 4 heads a
 // key/value head about 8 operations a byte, so the aim is the memory's rate. 64 sequences of 8192
-// tokens, 32 heads on 8 of 128: 604 MB of cache in 102.6 us, 5.9 TB/s (0.87 of a copy's rate), with
-// weights 67 MB of logits more and read again, 130 us; one of 131072 tokens 31.6 us, 4.5 TB/s, of
-// which some 7 us are the launch, the first copies and the join. Issue slots (45 % of cycles), ALU
-// (46 %) and DRAM (55 %) are all half busy in 24 sequences of 8192: latency between the few warps
+// tokens, 32 heads on 8 of 128: 604 MB of cache in 104.5 us, 5.8 TB/s (0.85 of a copy's rate), with
+// weights 67 MB of logits more and read again, 130 us; one of 131072 tokens 32.0 us, 4.5 TB/s, of
+// which some 7 us are the launch, the first copies and the join. Issue slots (48 % of cycles), ALU
+// (48 %) and DRAM (60 %) are all half busy in 24 sequences of 8192: latency between the few warps
 // that the accumulators leave room for.
 //
 // Work split. A unit is 32 tokens of one (sequence, head, row tile); the units of all sequences
@@ -55,22 +55,22 @@ constexpr uint32_t kAllRecords = (1u << kUnitRecords) - 1u;
 // queries, joining the warps, writing its rows. They come before its units in the list. Without
 // them the CTA that got the shortest sequences of a ragged batch (0, 1, 17 .. 4096 tokens, 32
 // sequences of 8 heads) took 42 us, its neighbours 10. A unit is one of seven that run at once, so
-// an item's 4 us are many. At 12 / 26 / 40, us: that batch 17.4 / 16.9 / 18.4, 16 sequences of 100
-// to 16384 tokens 22.8 / 21.3 / 22.1, 8 of 300 to 8000 with 8 new tokens 41.7 (at 15) / 34.9 / 32.8,
-// 16 of 300 to 3001 with 5 (head size 64) 20.3 / 17.7 / 19.1, 64 of 8192 102.5 / 102.6 / 103.6.
+// an item's 4 us are many. At 12 / 26 / 40, us: that batch 18.0 / 17.7 / 18.8, 16 sequences of 100
+// to 16384 tokens 23.4 / 21.7 / 22.6, 8 of 300 to 8000 with 8 new tokens 37.8 / 34.6 / 32.5, 16 of
+// 300 to 3001 with 5 (head size 64) 20.6 / 18.0 / 19.6, 64 of 8192 104.5 / 104.5 / 105.2.
 constexpr int kItemCost = 26;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Probabilities times V scales, as the second product's FP16 operand. A row's products come under
 // 2^-e, e the exponent of the largest one that it has met (at most 1 times a scale, while the
-// running maximum is exact), and have these bits to spare above it: the running maximum lags by up to
-// 2^kLag, a scale may be 2^kScaleLag times the largest product, and what is left lifts the products,
-// so that they are rounded to 2^-12 of themselves or 2^-28 of the largest. (Under the largest scale
-// that the row had met, attended or not, one token of values 2^20 times the others' took 20 bits
-// of theirs.)
+// running maximum is exact), and have these bits to spare above it: the running maximum lags by up
+// to 2^kLag, a scale may be 2^kScaleLag times the largest product, and what is left lifts the
+// products, so that they are rounded to 2^-11 of themselves or 2^-28 of the largest. (Under the
+// largest scale that the row had met, attended or not, one token of values 2^20 times the others'
+// took 20 bits of theirs.)
 constexpr int kLag = 4, kScaleLag = 8, kLift = 15 - kLag - kScaleLag;
-// The least e (exponent field): 2^kLag times 2^(127 + kLift - e) is still a number, and 0 times it 0
-// where a group's values are equal and their scale is 0.
+// The least e (exponent field): 2^kLag times 2^(127 + kLift - e) is still a number, and 0 times it
+// 0 where a group's values are equal and their scale is 0.
 constexpr int kLeastEv = 16;
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
@@ -128,9 +128,9 @@ __device__ __forceinline__ void join_warps() {
   asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
 }
 
-// bulk_load of bytes that the call reads once and that leave L2 first: the logits stay (64 sequences
-// of 8192 with weights 137.5 -> 132 us, 16 of them 48 -> 43; without weights 107.8 -> 105). A cache
-// that fits L2 and is read again at once is the other side: 4 sequences of 8192 17.7 -> 18.2 us.
+// bulk_load of bytes that the call reads once and that leave L2 first: the logits stay (64
+// sequences of 8192 with weights 135.8 -> 130.4 us, 16 of them 46 -> 41; without weights 106.8 ->
+// 104.5; 4 of them, a cache that fits L2 and is read again at once, 15.5 either way).
 __device__ __forceinline__ void bulk_load_once(void* smem_dst, const void* gsrc, uint32_t bytes,
                                                uint64_t* bar, uint64_t policy) {
   asm volatile(
@@ -1112,8 +1112,10 @@ cudaError_t by_rows(const Kv4AttentionArgs& a, cudaStream_t stream) {
 
 // Above kFewRows the prompts' path takes over. It widens the whole cache to FP16 tiles first and
 // pads the rows to 128; here every 16 rows read the cache's codes again. 32 query heads on 8, us at
-// 80 and 96 rows here / 100 and 128 there: 94, 110 / 99, 97 for 16 sequences of 2048, 225, 267 /
-// 294, 286 for 16 of 8192, 42, 47 / 78, 77 for one of 16384.
+// 80 and 96 rows here / 100 and 128 there: 94, 111 / 105, 102 for 16 sequences of 2048, 226, 267 /
+// 307, 298 for 16 of 8192, 42, 47 / 79, 78 for one of 16384. So the border is a compromise: for
+// many short sequences it lies a little late, for one long one early, and there the next row costs
+// 30 us.
 bool is_prompt(int max_new, int heads, int kv_heads) {
   return static_cast<int64_t>(max_new) * (heads / kv_heads) > kFewRows;
 }

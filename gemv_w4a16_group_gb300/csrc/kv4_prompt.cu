@@ -6,30 +6,33 @@
 // 4 D operations a visible (row, token) pair and one exponential: the tensor pipe bounds it. A unit
 // of 256 rows and 128 tokens (D 128) needs 2176 cycles of multiplication; with both operands of
 // the first product in shared memory it takes 2758, as reading them saturates it, and the whole
-// loop 2890. A prompt of 4096 tokens, 32 heads on 8: images 19.5 us, attention 116 us (0.62 of
-// cuBLAS's BF16 rate on the visible pairs); 512 tokens behind 15872: 26.4 and 115 us.
+// loop took 2890 while P came under the tiles' powers of two alone (the kernel is 3 % slower with
+// the rows' products). A prompt of 4096 tokens, 32 heads on 8: images 20.5 us, attention 120 us
+// (0.60 of cuBLAS's BF16 rate on the visible pairs); 512 tokens behind 15872: 27 and 117 us.
 //
 // 1. kv4_prompt_images_kernel writes the sequence's keys and values, and the queries, as FP16
 //    tiles in the swizzled order that tcgen05.mma reads: every later load is one contiguous bulk
 //    copy, and a code is widened once instead of once a row tile (a 4096-token prompt has 64 of
 //    them a head). Values come transposed, so that both products read K-major operands, rounded
-//    to FP16 under a power of two a tile (2^-11 of a value, a quarter of the output's rounding).
+//    to FP16 under a power of two a tile (scale, minimum and sum to 2^-11 of themselves; the
+//    output's own rounding is 2^-8).
 //    A tile whose tokens differ by 2^8 or more (a token that is larger than the rest would take
 //    bits from them even in rows that do not see it) has powers of two a token, and the softmax a
 //    slower body for it; 256 rows of queries that differ by 2^12 have them a row.
 //    A key is exact: with c the code less 8, c s has at most 3 + 8 significant bits and is an
 //    FP16 number; what is left, (min + 8 s) times the sum of q over the group, goes through 16
-//    more columns, four a group, as FP16 pairs of high and low parts. Rounded keys (2^-12) put
-//    3e-5 into the accumulated weights, which are fp32.
+//    more columns, four a group, as FP16 pairs of high and low parts. Rounded keys put 3e-5 into
+//    the accumulated weights, which are fp32.
 // 2. kv4_prompt_kernel, one CTA an SM: 256 rows as two row halves of 128, each with a warpgroup
 //    that owns one row a thread (no shuffles), over tiles of 128 tokens in a ring of four bulk
 //    copies. One thread issues S = Q K^T (tensor memory, fp32) and O += P V with P read back from
 //    tensor memory, the halves in turn, so that one half's softmax runs under the other's
 //    products. P comes under the largest product of a probability and a tile's values that its row
 //    has met, with 10 bits to spare; the running maximum may lag by 2^8 and that product by 2^5
-//    before O is rescaled: P stays in FP16's range and the rescale is rare. The (sequence, head, 256-row tile) items, each as many units as it
-//    has visible token tiles, are cut into equal ranges of units, one a CTA; an item that a
-//    boundary cuts is joined from fp32 parts by whoever arrives last, in order.
+//    before O is rescaled: P stays in FP16's range and the rescale is rare. The (sequence, head,
+//    256-row tile) items, each as many units as it has visible token tiles, are cut into equal
+//    ranges of units, one a CTA; an item that a boundary cuts is joined from fp32 parts by whoever
+//    arrives last, in order.
 // 3. With weights, kv4_prompt_weights_kernel makes S^T = K_hat Q^T from the same tiles, a thread
 //    a token, and sums exp2(S - lse) along the row.
 #include "kv4_common.cuh"
@@ -52,8 +55,9 @@ struct TokenMeta {
 };
 constexpr int kByToken = 1 << 20;
 constexpr int kSpread = 8;  // exponents between a tile's tokens that one power of two bridges
-// An fma takes the maximum off a logit (base 2) up to this size; beyond it the maximum's own rounding
-// would be seen (and overflow P from 2^28 on), so the logit is rounded first, as the maximum was.
+// An fma takes the maximum off a logit (base 2) up to this size; beyond it the maximum's own
+// rounding would be seen (and overflow P from 2^28 on), so the logit is rounded first, as the
+// maximum was.
 constexpr float kHuge = 1048576.f;
 constexpr float kByRow = -1.f;
 constexpr int kRowSpread = 12;  // the same between a tile's rows
@@ -1628,8 +1632,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 }
 
 struct Layout {
-  size_t plan, starts, order, base, pre, meta, token_meta, qf, row_qf, q_img, kv_img, counters, parts,
-      lse2, kbase, kpre, kcounters, sums, total;
+  size_t plan, starts, order, base, pre, meta, token_meta, qf, row_qf, q_img, kv_img, counters,
+      parts, lse2, kbase, kpre, kcounters, sums, total;
   int key_tiles, row_tiles;
 };
 

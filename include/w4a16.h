@@ -466,15 +466,21 @@ w4a16_status kv4_read(const kv4_cache* cache, const int32_t* starts, uint16_t* k
  *   max_new, max_len  upper bounds, known on the host, of a sequence's new tokens and length; they
  *           size the launch, while the work is that of the real lengths.
  * A row that sees no token (an empty sequence) gives out = 0 and lse = -inf. Tokens that a row
- * does not see do not touch it, whatever they hold. Products are FP16 with fp32 sums: codes are
- * exact in them, probabilities (times a value's scale) rounded to 2^-12 of themselves or 2^-28 of
- * the row's largest, and, from 97 rows a key/value head on, probabilities to 2^-12 of themselves or,
- * times the values, 2^-25 of the row's largest, and values to 2^-11 of the largest of their token
- * and group; maxima, sums, lse and weights are fp32. out is within about a rounding to BF16 of the
- * exact result, lse and weights within 1e-6. Results do not depend on timing (no floating-point
- * atomics). Values must be finite where a row sees them.
- * Up to 96 rows (max_new * heads / kv_heads) the cache is read in place; above that it is widened
- * into the workspace first (4 bytes a key/value pair of dims, 16-bit tiles for tcgen05.mma).
+ * does not see do not touch it, whatever they hold. Results do not depend on timing (no
+ * floating-point atomics). Values must be finite where a row sees them, queries and logits below
+ * 2^100.
+ * Accuracy. Products are FP16 with fp32 sums; maxima, sums, lse and weights are fp32, and codes
+ * are exact. What is rounded to FP16 (2^-11 of itself, a choice for the tensor pipe's rate; the
+ * output's own rounding to BF16 is 2^-8): up to 96 rows a key/value head (max_new * heads /
+ * kv_heads) probabilities times a value's scale, those below 2^-17 of the row's largest to 2^-28
+ * of that; above, probabilities (times the values, to 2^-25 of the row's largest at least) and
+ * values (scale, minimum and sum). out is within about a rounding to BF16 of the exact result; a
+ * logit as a rule within 2^-20 of the largest sum of its terms' magnitudes that the row sees (at
+ * worst 2^-15), lse within that and 1e-5, a weight within twice that of itself.
+ * Up to 96 rows the cache is read in place; above that it is widened into the workspace first.
+ * The workspace grows with the bounds, not with the lengths: up to 96 rows, with weights, by 4
+ * bytes a row, sequence, key/value head and token of max_len; above, by some 4 (head_dim + 8)
+ * bytes a token of max_len, sequence and key/value head.
  * Workspace: kv4_attention_workspace_bytes() bytes, 16-byte aligned, zero-filled before its first
  * use (the kernels leave its counters zero) and not shared by calls that may run concurrently;
  * W4A16_ERR_WORKSPACE if NULL or smaller. Its first 4 KiB hold the counters, whatever the call's
@@ -515,7 +521,8 @@ w4a16_status kv4_evict(const kv4_cache* cache, const int32_t* out_table, int out
  * up a bounded wait since the last query, W4A16_ERR_LAYOUT if a kernel found its
  * dynamic shared memory less than 128-byte aligned and skipped its work (its output is
  * then not written), W4A16_ERR_INDEX if a kernel met a page number, a length or an offset
- * outside the arrays it was given and left those tokens out, W4A16_ERR_CUDA if the synchronization failed, W4A16_OK otherwise.
+ * outside the arrays it was given and left those tokens out, W4A16_ERR_CUDA if the
+ * synchronization failed, W4A16_OK otherwise.
  * (The pages have no counterpart; this is the library's failure-detection hook.)
  */
 w4a16_status w4a16_device_status(w4a16_stream_t stream);
