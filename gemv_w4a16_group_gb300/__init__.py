@@ -25,6 +25,9 @@ Formats ("Low-Precision Kernels: INT4, INT8 and FP8 Matmuls, Measured", Step 2;
     x bfloat16 [K]; y bfloat16 [N]; w_hat = e2m1(q) * e4m3(scale) * tensor_scale.
   * MXFP4A16 ("Low-Precision Kernels ...", Step 6): codes as NVFP4; scales uint8 [N, K/32]
     (E8M0 bits); w_hat = e2m1(q) * 2^(scale - 127).
+  * Quantized activations ("nvfp4", "mxfp4", "mxfp8"): codes uint8 [M, K/2] (E2M1) or [M, K]
+    (E4M3); block scales in tiles uint8 [ceil(M/128), ceil(blocks/4), 512] (see include/w4a16.h),
+    as ``fp4_prepare_scales`` makes them of weights'; row scales float32 [M] (NVFP4).
   * KV4, a paged key/value cache in 4 bits: uint8 [pages, kv_heads, page_size / 16, record] as
     ``kv4_cache`` allocates it (see include/w4a16.h), a page table int32 [batch, width], lengths
     int32 [batch] and the packed new tokens' offsets ``starts`` int32 [batch + 1].
@@ -52,7 +55,8 @@ __all__ = [
     "w4a16_matmul_prepared_uses_prepared", "testing_set_fp4_variant",
     "fp4_matmul_workspace_bytes", "nvfp4_matmul", "mxfp4_matmul", "testing_set_w8_variant",
     "kv4_cache", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_workspace_bytes",
-    "kv4_evict",
+    "kv4_evict", "fp4_prepare_scales", "act_quantize", "act_rmsnorm", "nvfp4_matmul_act",
+    "mxfp4_matmul_act",
 ]
 
 STATUS_NAMES = {0: "W4A16_OK", 1: "W4A16_ERR_INVALID_ARG", 2: "W4A16_ERR_UNSUPPORTED",
@@ -110,6 +114,11 @@ def _load():
         "kv4_read": [C, P, P, P, I, P],
         "kv4_attention": [C, P, P, L, P, P, I, I, I, I, F, P, P, I, P, S, P],
         "kv4_evict": [C, P, I, P, I, I, I, I, I, P, P, P, I, P],
+        "fp4_prepare_scales": [P, I, I, P, P],
+        "act_quantize": [P, L, I, I, I, P, P, P, P],
+        "act_rmsnorm": [P, L, P, L, P, L, P, F, I, I, I, P, P, P, P],
+        "nvfp4_matmul_act": [P, P, P, P, P, P, P, I, I, I, P],
+        "mxfp4_matmul_act": [P, P, I, P, P, P, I, I, I, P],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -122,6 +131,8 @@ def _load():
     lib.w4a16_prepared_bytes.restype = S
     lib.fp4_matmul_workspace_bytes.argtypes = [I, I]
     lib.fp4_matmul_workspace_bytes.restype = S
+    lib.fp4_scale_tiles_bytes.argtypes = [I, I]
+    lib.fp4_scale_tiles_bytes.restype = S
     lib.kv4_cache_bytes.argtypes = [I, I, I, I, I]
     lib.kv4_cache_bytes.restype = S
     lib.kv4_attention_workspace_bytes.argtypes = [I] * 9
@@ -801,3 +812,127 @@ def kv4_evict(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weig
         c, _dev(out_table, "out_table", torch.int32), out_table.shape[1], wp, wl, budget, first,
         recent, max_len, kept_p, new_p, op, ol, _stream(stream)))
     return kept, new_lens, weights_out
+
+
+_ACT_FORMATS = {"nvfp4": (0, 16, 2), "mxfp4": (1, 32, 2), "mxfp8": (2, 32, 1)}
+
+
+def _tiles_shape(rows: int, cols: int):
+    return (rows + 127) // 128, (cols + 3) // 4, 512
+
+
+def fp4_prepare_scales(scales: torch.Tensor, tiles=None, stream=None) -> torch.Tensor:
+    """uint8 block scales [N, blocks] of nvfp4_quantize or mxfp4_quantize -> the tiles that
+    nvfp4_matmul_act and mxfp4_matmul_act read, uint8 [ceil(N/128), ceil(blocks/4), 512]."""
+    N, blocks = scales.shape
+    tiles, p = _result(tiles, "tiles", scales, _tiles_shape(N, blocks), torch.uint8, stream)
+    _check("fp4_prepare_scales", _lib.fp4_prepare_scales(
+        _dev(scales, "scales", torch.uint8), N, blocks, p, _stream(stream)))
+    return tiles
+
+
+def _rows(t: torch.Tensor, name: str, shape=None):
+    """(address, elements between rows) of BF16 rows that may lie in a wider array."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {'[M, K]' if shape is None else list(shape)}, "
+                         f"got {list(t.shape)}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _act_out(x, format: str, codes, scales, row_scales, stream):
+    """(number of the format, codes, scales, row_scales, their addresses)"""
+    if format not in _ACT_FORMATS:
+        raise ValueError(f"format must be one of {sorted(_ACT_FORMATS)}, got {format!r}")
+    number, block, per_byte = _ACT_FORMATS[format]
+    M, K = x.shape
+    codes, cp = _result(codes, "codes", x, (M, K // per_byte), torch.uint8, stream)
+    scales, sp = _result(scales, "scales", x, _tiles_shape(M, (K + block - 1) // block),
+                         torch.uint8, stream)
+    rp = None
+    if number == 0:
+        row_scales, rp = _result(row_scales, "row_scales", x, (M,), torch.float32, stream)
+    elif row_scales is not None:
+        raise ValueError(f"{format} has no row scales")
+    return number, codes, scales, row_scales, cp, sp, rp
+
+
+def act_quantize(x: torch.Tensor, format: str = "nvfp4", codes=None, scales=None, row_scales=None,
+                 stream=None):
+    """x bf16 [M, K] (rows may be strided) -> (codes, scales, row_scales or None) in "nvfp4",
+    "mxfp4" or "mxfp8". Rows of the scale tiles past M are not written."""
+    xp, xs = _rows(x, "x")
+    M, K = x.shape
+    number, codes, scales, row_scales, cp, sp, rp = _act_out(x, format, codes, scales, row_scales,
+                                                             stream)
+    _check("act_quantize", _lib.act_quantize(xp, xs, M, K, number, cp, sp, rp, _stream(stream)))
+    return codes, scales, row_scales
+
+
+def act_rmsnorm(x: torch.Tensor, weight: torch.Tensor, format: str = "nvfp4", eps: float = 1e-6,
+                residual=None, residual_out=None, codes=None, scales=None, row_scales=None,
+                stream=None):
+    """h = x + residual (bf16 [M, K], rows may be strided), quantized h * weight / rms(h) ->
+    (codes, scales, row_scales or None, h). h goes to ``residual_out``, which may be ``residual``
+    itself; without a residual h is x, and None is returned for it."""
+    xp, xs = _rows(x, "x")
+    M, K = x.shape
+    qp, qs, op, os_ = None, 0, None, 0
+    if residual is not None:
+        qp, qs = _rows(residual, "residual", x.shape)
+        if residual_out is None:
+            residual_out = _new(x, (M, K), torch.bfloat16, stream)
+        op, os_ = _rows(residual_out, "residual_out", x.shape)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    number, codes, scales, row_scales, cp, sp, rp = _act_out(x, format, codes, scales, row_scales,
+                                                             stream)
+    _check("act_rmsnorm", _lib.act_rmsnorm(
+        xp, xs, qp, qs, op, os_, _dev(weight, "weight", torch.bfloat16, (K,)), eps, M, K, number,
+        cp, sp, rp, _stream(stream)))
+    return codes, scales, row_scales, residual_out
+
+
+def nvfp4_matmul_act(x_codes: torch.Tensor, x_scales: torch.Tensor, x_row_scales: torch.Tensor,
+                     codes: torch.Tensor, scale_tiles: torch.Tensor, tensor_scale: torch.Tensor,
+                     y=None, stream=None) -> torch.Tensor:
+    """y [M, N] (bf16) = X_hat . W_hat^T of NVFP4 activations (from act_quantize or act_rmsnorm)
+    and NVFP4 weights: codes and tensor_scale of nvfp4_quantize, scale_tiles of
+    fp4_prepare_scales."""
+    M, N, K = x_codes.shape[0], codes.shape[0], codes.shape[1] * 2
+    blocks = (K + 15) // 16
+    y, yp = _result(y, "y", x_codes, (M, N), torch.bfloat16, stream)
+    _check("nvfp4_matmul_act", _lib.nvfp4_matmul_act(
+        _dev(x_codes, "x_codes", torch.uint8, (M, K // 2)),
+        _dev(x_scales, "x_scales", torch.uint8, _tiles_shape(M, blocks)),
+        _dev(x_row_scales, "x_row_scales", torch.float32, (M,)),
+        _dev(codes, "codes", torch.uint8),
+        _dev(scale_tiles, "scale_tiles", torch.uint8, _tiles_shape(N, blocks)),
+        _dev(tensor_scale, "tensor_scale", torch.float32, (1,)), yp, M, N, K, _stream(stream)))
+    return y
+
+
+def mxfp4_matmul_act(x_codes: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor,
+                     scale_tiles: torch.Tensor, y=None, stream=None) -> torch.Tensor:
+    """y [M, N] (bf16) = X_hat . W_hat^T of MXFP4 (x_codes [M, K/2]) or MXFP8 (x_codes [M, K])
+    activations and MXFP4 weights: codes of mxfp4_quantize, scale_tiles of fp4_prepare_scales."""
+    M, N, K = x_codes.shape[0], codes.shape[0], codes.shape[1] * 2
+    blocks = (K + 31) // 32
+    if x_codes.dim() != 2 or x_codes.shape[1] not in (K // 2, K):
+        raise ValueError(f"x_codes must be [M, {K // 2}] (MXFP4) or [M, {K}] (MXFP8), "
+                         f"got {list(x_codes.shape)}")
+    y, yp = _result(y, "y", x_codes, (M, N), torch.bfloat16, stream)
+    _check("mxfp4_matmul_act", _lib.mxfp4_matmul_act(
+        _dev(x_codes, "x_codes", torch.uint8),
+        _dev(x_scales, "x_scales", torch.uint8, _tiles_shape(M, blocks)),
+        2 if x_codes.shape[1] == K else 1, _dev(codes, "codes", torch.uint8),
+        _dev(scale_tiles, "scale_tiles", torch.uint8, _tiles_shape(N, blocks)), yp, M, N, K,
+        _stream(stream)))
+    return y

@@ -27,9 +27,9 @@ SOURCES = ["api.cu", "quant_pack.cu", "gemv.cu", "q4b32.cu", "q4b32_mma.cu", "ge
            "no_alloc.cu", "host_cache.cu", "skinny.cu", "w8a16.cu",
            "nvfp4.cu", "fp4_mma.cu", "fp4_matmul.cu", "prepared.cu", "w8a16_mma.cu",
            "kv4_api.cu", "kv4_cache.cu", "kv4_attention.cu", "kv4_prompt.cu",
-           "kv4_evict.cu"]
+           "kv4_evict.cu", "act_api.cu", "act_quant.cu", "act_matmul.cu"]
 HEADERS = ["common.cuh", "fp4_common.cuh", "launch.h", "kv4.h", "kv4_prompt.h",
-           "kv4_common.cuh"]
+           "kv4_common.cuh", "act.h"]
 PUBLIC_HEADERS = ["w4a16.h", "w4a16_testing.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -386,6 +386,84 @@ w4a16_status mxfp4_matmul(const uint16_t* x, const uint8_t* codes, const uint8_t
                           size_t workspace_bytes, w4a16_stream_t stream);
 
 /*
+ * Activations in 4 and 8 bits, and their products with NVFP4 and MXFP4 weights on the block-scaled
+ * tensor pipe. (The pages stop at weight-only products and name the FP4 tensor path as what lies
+ * beyond; the formats are theirs: "Hardware-invariant NVFP4 progress report 1", "The NVFP4
+ * layout", and "Low-Precision Kernels ...", Step 6.)
+ *
+ * Formats of quantized rows of K values (K % 32 == 0):
+ *   W4A16_ACT_NVFP4  E2M1 codes uint8 [M, K/2] (byte j: k = 2j in the low nibble), an E4M3 scale
+ *                    per 16, a fp32 scale per row: x_hat = e2m1 * e4m3 * r
+ *   W4A16_ACT_MXFP4  E2M1 codes uint8 [M, K/2], an E8M0 scale per 32: x_hat = e2m1 * 2^(s - 127)
+ *   W4A16_ACT_MXFP8  E4M3 codes uint8 [M, K], an E8M0 scale per 32: x_hat = e4m3 * 2^(s - 127)
+ * A row's result depends on that row alone: NVFP4's second scale is per row, not per tensor.
+ *
+ * Scale tiles. Scales [R, C] (rows by blocks along K) lie in uint8 [ceil(R/128), ceil(C/4), 512]:
+ * (r, c) at byte (r % 32) 16 + (r / 32 % 4) 4 + c % 4 of tile (r / 128, c / 4), as tensor memory
+ * takes them. fp4_scale_tiles_bytes(R, C) bytes. The quantizers write whole 4-byte words of the
+ * rows they are given (0 past column C) and nothing else; words of rows past R may hold anything.
+ *
+ * fp4_prepare_scales -- scales uint8 [rows, cols] of nvfp4_quantize or mxfp4_quantize (cols = K/16
+ *   or K/32) into tiles, once per weight; places past rows and cols become 0. scales need no
+ *   alignment.
+ */
+enum { W4A16_ACT_NVFP4 = 0, W4A16_ACT_MXFP4 = 1, W4A16_ACT_MXFP8 = 2 };
+
+size_t fp4_scale_tiles_bytes(int rows, int cols);
+w4a16_status fp4_prepare_scales(const uint8_t* scales, int rows, int cols, uint8_t* tiles,
+                                w4a16_stream_t stream);
+
+/*
+ * act_quantize -- x bf16 [M, K], x_stride elements between rows (a multiple of 8, at least K;
+ *   not read for M = 1), into `format`:
+ *   codes, scales (tiles), row_scales fp32 [M] (NVFP4 only, else not touched and may be NULL).
+ *   NVFP4: a = the row's largest |x|, at least 2^-80; r = fl(a / 2688); a block's scale is the
+ *     smallest E4M3 value >= 448 max|block| / a; codes are 2688 x / (s a) rounded to the nearest
+ *     E2M1 value, ties to the even code, saturating at 6.
+ *   MXFP4, MXFP8: a block's scale is 2^X, X = floor(log2 max|block|) - 2 (MXFP4) or - 8 (MXFP8), at
+ *     least -127; codes are x 2^-X rounded to the nearest E2M1 / E4M3 value, ties to the even code,
+ *     saturating at 6 / 448.
+ *   A block of zeros has scale code 0 and codes 0. NaN or an infinity makes its block's scale NaN
+ *   (MXFP4, MXFP8: code 0xFF) or its row's (NVFP4), so that products with that row are NaN.
+ *   Requires M > 0, K > 0, K % 32 == 0; K up to 65,536 (W4A16_ERR_UNSUPPORTED beyond).
+ *
+ * act_rmsnorm -- the same of y = h * weight / sqrt(mean(h^2) + eps), h = bf16(x + residual):
+ *   residual, residual_out  bf16 [M, K] with strides as x's; h is written to residual_out, which
+ *     may be residual itself or x. Both NULL: h = x.
+ *   weight  bf16 [K]; eps >= 1e-30
+ *   fp32 sums; h * weight is exact, so y is rounded to fp32 once before it is to its code. NVFP4's
+ *   codes and block scales are those of h * weight, and 1 / sqrt(...) goes into r. A row whose
+ *   squares pass fp32's range becomes NaN.
+ */
+w4a16_status act_quantize(const uint16_t* x, int64_t x_stride, int M, int K, int format,
+                          uint8_t* codes, uint8_t* scales, float* row_scales,
+                          w4a16_stream_t stream);
+w4a16_status act_rmsnorm(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
+                         int64_t residual_stride, uint16_t* residual_out,
+                         int64_t residual_out_stride, const uint16_t* weight, float eps, int M,
+                         int K, int format, uint8_t* codes, uint8_t* scales, float* row_scales,
+                         w4a16_stream_t stream);
+
+/*
+ * nvfp4_matmul_act -- y[m, n] = r[m] S sum_k x_hat[m, k] w_hat[n, k] (block scales inside the sum),
+ *   NVFP4 activations by NVFP4 weights: codes uint8 [N, K/2] and tensor_scale S of nvfp4_quantize,
+ *   scale_tiles of fp4_prepare_scales; y bf16 [M, N].
+ * mxfp4_matmul_act -- MXFP4 (x_format W4A16_ACT_MXFP4) or MXFP8 (W4A16_ACT_MXFP8) activations by
+ *   MXFP4 weights.
+ *   Products of codes and scales are exact, sums fp32, y is rounded once to BF16: the tolerance of
+ *   w4a16_matmul with x_hat for x. Rows of x do not touch one another. No workspace.
+ *   Requires M > 0, N > 0, K > 0, K % 32 == 0 (K % 128 == 0 and codes 32-byte aligned for
+ *   W4A16_ACT_MXFP8); each at most 2^23 (W4A16_ERR_UNSUPPORTED beyond).
+ */
+w4a16_status nvfp4_matmul_act(const uint8_t* x_codes, const uint8_t* x_scales,
+                              const float* x_row_scales, const uint8_t* codes,
+                              const uint8_t* scale_tiles, const float* tensor_scale, uint16_t* y,
+                              int M, int N, int K, w4a16_stream_t stream);
+w4a16_status mxfp4_matmul_act(const uint8_t* x_codes, const uint8_t* x_scales, int x_format,
+                              const uint8_t* codes, const uint8_t* scale_tiles, uint16_t* y, int M,
+                              int N, int K, w4a16_stream_t stream);
+
+/*
  * The 4-bit key/value cache: what a decoder on 4-bit weights needs beside its matrix products.
  * (The pages stop at the linear layers; the value format is their group rule, "Low-Precision
  * Kernels ...", Step 2, along the head dimension.)
