@@ -30,55 +30,95 @@ struct Form<kActMxfp8> {
 };
 
 // Instruction descriptor of the block-scaled kinds: fp32 accumulator, both operands K-major.
-// `sf` is the first scale's byte in its 32-bit word.
-template <int FORM>
-__host__ __device__ constexpr uint32_t idesc_scaled(int m, int n, int sf) {
-  // element types: kind::mxf4nvf4 E2M1 = 1; kind::mxf8f6f4 E4M3 = 0, E2M1 = 5 (a: weights)
-  const uint32_t ta = FORM == kActMxfp8 ? 5u : 1u, tb = FORM == kActMxfp8 ? 0u : 1u;
-  return (static_cast<uint32_t>(sf) << 4) | (ta << 7) | (tb << 10) |
-         (static_cast<uint32_t>(n >> 3) << 17) | ((FORM == kActNvfp4 ? 0u : 1u) << 23) |
-         (static_cast<uint32_t>(m >> 4) << 24) | (static_cast<uint32_t>(sf) << 29);
+// (The first scale's byte in its 32-bit word goes into bits 4 and 29 on.) W_IS_A: the weights are
+// the A operand.
+template <int FORM, bool W_IS_A>
+__host__ __device__ constexpr uint32_t idesc_scaled(int m, int n) {
+  // element types: kind::mxf4nvf4 E2M1 = 1; kind::mxf8f6f4 E4M3 = 0, E2M1 = 5
+  const uint32_t w = FORM == kActMxfp8 ? 5u : 1u, x = FORM == kActMxfp8 ? 0u : 1u;
+  const uint32_t ta = W_IS_A ? w : x, tb = W_IS_A ? x : w;
+  return (ta << 7) | (tb << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         ((FORM == kActNvfp4 ? 0u : 1u) << 23) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-template <int FORM>
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+// Operands as the low words of shared-memory descriptors; the high words are the layout's.
+// Neighbouring pieces differ by an addition to the low word, and the whole warp computes them, so
+// that they stay in uniform registers: a product costs its issuing warp a few instructions.
+constexpr uint32_t kDescSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);  // see smem_desc_kmajor_sw128
+// A scale tile: no swizzle, 8-row atoms of 128 bytes.
+constexpr uint32_t kDescScales = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_low(const void* smem) {
+  return (smem_addr(smem) & 0x3FFFFu) >> 4;
+}
+
+#define W4K_MMA_SCALED(GROUP, KIND)                                                              \
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\t"              \
+               "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"                              \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a, b, %3, [%4], [%5], "    \
+               "p;\n\t}" ::"r"(d),                                                               \
+               "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescSw128)  \
+               : "memory")
+
+// D (+)= A B with the scales at sfa and sfb; GROUP: the CTAs of a pair that hold the operands.
+template <int FORM, int GROUP>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  if constexpr (FORM == kActNvfp4)
+  if constexpr (FORM == kActNvfp4) {
+    if constexpr (GROUP == 1) W4K_MMA_SCALED("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    else W4K_MMA_SCALED("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  } else if constexpr (FORM == kActMxfp4) {
+    if constexpr (GROUP == 1) W4K_MMA_SCALED("1", "mxf4nvf4.block_scale.scale_vec::2X");
+    else W4K_MMA_SCALED("2", "mxf4nvf4.block_scale.scale_vec::2X");
+  } else {
+    if constexpr (GROUP == 1) W4K_MMA_SCALED("1", "mxf8f6f4.block_scale.scale_vec::1X");
+    else W4K_MMA_SCALED("2", "mxf8f6f4.block_scale.scale_vec::1X");
+  }
+}
+#undef W4K_MMA_SCALED
+
+// A 512-byte scale tile (32 rows of 16 bytes) into 4 columns of all four lane quarters; a pair's
+// CTAs each from their own shared memory into their own tensor memory.
+template <int GROUP>
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t desc) {
+  if constexpr (GROUP == 1)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-  else if constexpr (FORM == kActMxfp4)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(desc), "n"(kDescScales)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(desc), "n"(kDescScales)
         : "memory");
 }
 
-// A 512-byte scale tile (32 rows of 16 bytes) into 4 columns of all four lane quarters.
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-               : "memory");
-}
-
-// Descriptor of a scale tile: no swizzle, 8-row atoms of 128 bytes.
-__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(128u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  return d;
+// One stage's scales and products: `a` and `b` the operands' tiles, sa and sb their scale tiles
+// (low words of descriptors), BLOCKS_B row blocks of b's scales; columns of the scales in tensor
+// memory at ca and cb. WHOLE: all of the stage's k lies in the row; else `left` values of it.
+template <int FORM, int GROUP, int BLOCKS_B, bool WHOLE>
+__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t b, uint32_t sa,
+                                            uint32_t sb, uint32_t ca, uint32_t cb, uint32_t idesc,
+                                            bool first, int left) {
+  using F = Form<FORM>;
+  constexpr int kTiles = F::KS / F::KT, kSteps = F::KS / F::KM, per_tile = F::KT / F::KM;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    if (!WHOLE && t * F::KT >= left) break;
+    scales_to_tmem<GROUP>(ca + 4 * t, sa + t * 32);
+#pragma unroll
+    for (int blk = 0; blk < BLOCKS_B; ++blk)
+      scales_to_tmem<GROUP>(cb + 4 * (t * BLOCKS_B + blk), sb + (blk * kTiles + t) * 32);
+  }
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    if (!WHOLE && j * F::KM >= left) break;
+    const int t = j / per_tile;
+    const uint32_t sf = j % per_tile * (4 / per_tile);  // first scale's byte of the step
+    mma_scaled<FORM, GROUP>(d, a + 2 * j, b + 2 * j, idesc | (sf << 4) | (sf << 29), ca + 4 * t,
+                            cb + 4 * t * BLOCKS_B, !first || j != 0 ? 1u : 0u);
+  }
 }
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -96,6 +136,75 @@ __device__ __forceinline__ float2 peer_lds64(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Arrives on the barrier at this address of CTA `rank` of the cluster.
+__device__ __forceinline__ void peer_arrive(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+                   peer_addr(smem_addr(bar), rank))
+               : "memory");
+}
+// Tile load into this CTA's shared memory that completes on a barrier of either CTA of the pair
+// (its shared::cluster address). x (innermost) must be a multiple of 16 bytes.
+__device__ __forceinline__ void pair_load_2d(void* smem_dst, const CUtensorMap* map,
+                                             uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(void* smem_dst, const CUtensorMap* map,
+                                             uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// mbar_wait_bounded without a hint to suspend: the pair's stages change hands faster.
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity,
+                                          volatile uint32_t* abort_flag, uint32_t* status,
+                                          uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*abort_flag) return false;
+    if (i == 0) t0 = global_timer_ns();
+    else if ((i & 15u) == 0 && global_timer_ns() - t0 > limit_ns) {
+      *abort_flag = 1u;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+// Arrives (once) on `bar` of both CTAs of the pair when every MMA issued before has completed.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int x,
+                                             int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::
+                   "l"(reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(smem_src)), "r"(x), "r"(y)
+               : "memory");
+}
+
 struct NarrowMaps {
   CUtensorMap w, x;
 };
@@ -107,7 +216,6 @@ template <int FORM, int NT>
 struct Narrow {
   using F = Form<FORM>;
   static constexpr int kTiles = F::KS / F::KT;
-  static constexpr int kSteps = F::KS / F::KM;
   // bytes that a copy of weights counts: those of the 4-bit values, also where it widens them
   static constexpr uint32_t w_tx = FORM == kActMxfp8 ? 128 * 64 : 128 * 128;
   static constexpr uint32_t w_bytes = 128 * 128, x_bytes = NT * 128, s_bytes = kTiles * 512;
@@ -201,39 +309,31 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       }
     }
   } else if (warp == 5) {
-    if (lane == 0) {
-      for (int i = 0; i < count; ++i) {
-        const int s = i % S;
-        if (!mbar_wait_bounded(&full[s], (i / S) & 1u, abort_flag, a.status, a.wait_limit_ns)) break;
-        tc_fence_after_sync();
-        const int k0 = (first + i) * F::KS;
-        const uint32_t cols = tmem + L::acc_cols + (i & 1) * 2 * L::s_cols;
-        const uint32_t sw = smem_addr(smem + L::sw_off + s * L::s_bytes);
-        const uint32_t sx = smem_addr(smem + L::sx_off + s * L::s_bytes);
-#pragma unroll
-        for (int t = 0; t < L::kTiles; ++t) {
-          if (k0 + t * F::KT >= a.K) break;
-          scales_to_tmem(cols + 4 * t, smem_desc_scales(sw + t * 512));
-          scales_to_tmem(cols + L::s_cols + 4 * t, smem_desc_scales(sx + t * 512));
-        }
-        const uint32_t ws = smem_addr(smem + s * L::w_bytes);
-        const uint32_t xs = smem_addr(smem + L::x_off + s * L::x_bytes);
-        constexpr int per_tile = F::KT / F::KM;
-#pragma unroll
-        for (int j = 0; j < L::kSteps; ++j) {
-          if (k0 + j * F::KM >= a.K) break;
-          const int t = j / per_tile;
-          const int sf = j % per_tile * (4 / per_tile);
-          const uint32_t idesc = idesc_scaled<FORM>(128, NT, sf);
-          mma_scaled<FORM>(tmem, smem_desc_kmajor_sw128(ws + j * 32),
-                           smem_desc_kmajor_sw128(xs + j * 32), idesc, cols + 4 * t,
-                           cols + L::s_cols + 4 * t, (i | j) != 0 ? 1u : 0u);
-        }
+    // the whole warp walks the stages, one lane issues
+    constexpr uint32_t idesc = idesc_scaled<FORM, true>(128, NT);
+    const uint32_t w0 = desc_low(smem), x0 = desc_low(smem + L::x_off);
+    const uint32_t sw0 = desc_low(smem + L::sw_off), sx0 = desc_low(smem + L::sx_off);
+    for (int i = 0; i < count; ++i) {
+      const int s = i % S;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (i / S) & 1u, abort_flag, a.status,
+                                                     a.wait_limit_ns)))
+        break;
+      tc_fence_after_sync();
+      const int left = a.K - (first + i) * F::KS;
+      const uint32_t ca = tmem + L::acc_cols + (i & 1) * 2 * L::s_cols;
+      const uint32_t aw = w0 + s * (L::w_bytes >> 4), ax = x0 + s * (L::x_bytes >> 4);
+      const uint32_t as = sw0 + s * (L::s_bytes >> 4), bs = sx0 + s * (L::s_bytes >> 4);
+      if (elect_one()) {
+        if (left >= F::KS)
+          issue_stage<FORM, 1, 1, true>(tmem, aw, ax, as, bs, ca, ca + L::s_cols, idesc, i == 0, left);
+        else
+          issue_stage<FORM, 1, 1, false>(tmem, aw, ax, as, bs, ca, ca + L::s_cols, idesc, i == 0, left);
         tc_commit(&empty[s]);
       }
-      // whatever happened, every MMA issued here completes before the tile is read or freed
-      tc_commit(done);
+      __syncwarp();
     }
+    // whatever happened, every MMA issued here completes before the tile is read or freed
+    if (elect_one()) tc_commit(done);
   }
   __syncwarp();
   volatile uint32_t none = 0u;
@@ -310,6 +410,282 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   }
 }
 
+// Many rows of x: a pair of CTAs on one MMA of 256 rows of x (A, 128 a CTA, D's lanes) by NT
+// columns (B, half of the weights' rows in either CTA's shared memory), so that an operand's
+// byte feeds twice the products of one CTA's tile. Persistent pairs; the accumulator has two
+// places, so that a tile's MMAs run while the last one's sums are scaled, rounded and stored.
+struct WideMaps {
+  CUtensorMap w, x, sw, sx, y;
+};
+
+template <int FORM, int NT>
+struct Wide {
+  using F = Form<FORM>;
+  static constexpr int kTiles = F::KS / F::KT;
+  static constexpr int kBlocks = NT / 128;  // row blocks of weights' scales
+  static constexpr uint32_t x_bytes = 128 * 128, w_bytes = NT / 2 * 128;
+  static constexpr uint32_t w_tx = FORM == kActMxfp8 ? w_bytes / 2 : w_bytes;
+  static constexpr uint32_t s_bytes = kTiles * 512;
+  static constexpr uint32_t stage_bytes = x_bytes + w_bytes + (1 + kBlocks) * s_bytes;
+  static constexpr uint32_t tx_bytes = x_bytes + w_tx + (1 + kBlocks) * s_bytes;  // of a CTA
+  static constexpr uint32_t out_bytes = 4 * 2 * 4096;  // two pieces of 32 rows x 64 a warp
+  static constexpr int kMost = (227 * 1024 - 1024 - 512 - static_cast<int>(out_bytes)) /
+                               static_cast<int>(stage_bytes);
+  static constexpr int kStages = kMost < 8 ? kMost : 8;
+  static constexpr uint32_t w_off = kStages * x_bytes;
+  static constexpr uint32_t out_off = w_off + kStages * w_bytes;
+  static constexpr uint32_t sx_off = out_off + out_bytes;
+  static constexpr uint32_t sw_off = sx_off + kStages * s_bytes;
+  static constexpr uint32_t bar_off = sw_off + kStages * kBlocks * s_bytes;
+  // full (both CTAs' copies, in the first), empty; the accumulators' full (2), empty (2); done
+  static constexpr uint32_t misc_off = bar_off + (2 * kStages + 5) * 8;
+  static constexpr uint32_t total = misc_off + 16;
+  static constexpr uint32_t alloc = total + 1024;
+  static_assert(alloc <= 227 * 1024, "shared memory");
+  // Tensor memory: 512 columns hold two accumulators of 256 only without the scales (48 at most).
+  // The two overlap by 64 columns, which a tile's epilogue empties first.
+  static constexpr uint32_t acc_step = NT == 256 ? 192 : NT;
+  static constexpr int kLag = NT == 256 ? 1 : 2;  // tiles between an accumulator's fill and reuse
+  static constexpr uint32_t sx_col = acc_step + NT;
+  static constexpr uint32_t sw_col = sx_col + 4 * kTiles;
+  static_assert(sw_col + 4 * kTiles * kBlocks <= 512, "tensor memory");
+};
+
+// Tiles in the order of their work: kGroup row tiles side by side, columns in turn, so that what
+// the resident pairs read together stays in L2.
+struct WideOrder {
+  int tm, tn;
+  static constexpr int kGroup = 16;
+  __device__ __forceinline__ void at(int i, int& m, int& n) const {
+    const int per = kGroup * tn, g = i / per, r = i - g * per;
+    const int rows = min(kGroup, tm - g * kGroup);
+    n = r / rows;
+    m = g * kGroup + r - n * rows;
+  }
+};
+
+template <int FORM, int NT>
+__global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
+    act_wide_kernel(const __grid_constant__ WideMaps maps, const ActMatmulArgs a, const WideOrder order,
+                    int use_store) {
+  using L = Wide<FORM, NT>;
+  using F = Form<FORM>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* done = acc_empty + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
+  volatile uint32_t* abort_flag = holder + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = order.tm * order.tn;
+  const int stages = (a.K + F::KS - 1) / F::KS;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);  // the epilogue's warps of both CTAs
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.sw);
+    tma_prefetch_desc(&maps.sx);
+    if (use_store) tma_prefetch_desc(&maps.y);
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(holder)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers stand
+  tc_fence_after_sync();
+  const uint32_t tmem = *holder;
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 4) {
+    if (lane == 0) {
+      const uint32_t full0 = peer_addr(smem_addr(full), 0);
+      const int w_row = static_cast<int>(rank) * (NT / 2);
+      int s = 0;
+      uint32_t phase = 1;  // of the stage's last use
+      bool go = true;
+      for (int t = pair; t < tiles && go; t += pairs) {
+        int tm, tn;
+        order.at(t, tm, tn);
+        const int bm = tm * 2 + static_cast<int>(rank);
+        for (int i = 0; i < stages; ++i) {
+          if (!pair_wait(&empty[s], phase, abort_flag, a.status, a.wait_limit_ns)) {
+            go = false;
+            break;
+          }
+          const uint32_t bar = full0 + s * 8;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::tx_bytes);
+          // rows past the arrays come as zeros, tiles of scales past a row's end as another's:
+          // the first are not stored, the second not multiplied
+          pair_load_2d(smem + s * L::x_bytes, &maps.x, bar, i * 128, bm * 128);
+          pair_load_2d(smem + L::w_off + s * L::w_bytes, &maps.w, bar, i * 128, tn * NT + w_row);
+          pair_load_3d(smem + L::sx_off + s * L::s_bytes, &maps.sx, bar, 0, i * L::kTiles, bm);
+          pair_load_3d(smem + L::sw_off + s * L::kBlocks * L::s_bytes, &maps.sw, bar, 0,
+                       i * L::kTiles, tn * L::kBlocks);
+          if (++s == S) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 5 && rank == 0) {
+    // the whole warp walks the stages, one lane issues the pair's MMAs
+    constexpr uint32_t idesc = idesc_scaled<FORM, false>(256, NT);
+    const uint32_t x0 = desc_low(smem), w0 = desc_low(smem + L::w_off);
+    const uint32_t sx0 = desc_low(smem + L::sx_off), sw0 = desc_low(smem + L::sw_off);
+    const uint32_t ca = tmem + L::sx_col, cb = tmem + L::sw_col;
+    int s = 0, n_tile = 0;
+    uint32_t phase = 0;
+    bool go = true;
+    for (int t = pair; t < tiles && go; t += pairs, ++n_tile) {
+      const int b = n_tile & 1;
+      const uint32_t acc = tmem + b * L::acc_step;
+      if (n_tile >= L::kLag) {
+        const int q = n_tile - L::kLag;  // the tile whose columns must be empty
+        go = __all_sync(0xffffffffu,
+                        pair_wait(&acc_empty[q & 1], (q >> 1) & 1u, abort_flag, a.status,
+                                             a.wait_limit_ns));
+        if (!go) break;
+        tc_fence_after_sync();
+      }
+      for (int i = 0; i < stages; ++i) {
+        go = __all_sync(0xffffffffu,
+                        pair_wait(&full[s], phase, abort_flag, a.status, a.wait_limit_ns));
+        if (!go) break;
+        tc_fence_after_sync();
+        const int left = a.K - i * F::KS;
+        const uint32_t ax = x0 + s * (L::x_bytes >> 4), bw = w0 + s * (L::w_bytes >> 4);
+        const uint32_t as = sx0 + s * (L::s_bytes >> 4);
+        const uint32_t bs = sw0 + s * (L::kBlocks * L::s_bytes >> 4);
+        if (elect_one()) {
+          if (left >= F::KS)
+            issue_stage<FORM, 2, L::kBlocks, true>(acc, ax, bw, as, bs, ca, cb, idesc, i == 0, left);
+          else
+            issue_stage<FORM, 2, L::kBlocks, false>(acc, ax, bw, as, bs, ca, cb, idesc, i == 0, left);
+          pair_commit(&empty[s]);
+          if (i == stages - 1) pair_commit(&acc_full[b]);
+        }
+        __syncwarp();
+        if (++s == S) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (elect_one()) pair_commit(done);
+  } else if (warp < 4) {
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const float wscale = FORM == kActNvfp4 ? __ldg(a.w_scale) : 1.f;
+    uint8_t* out = smem + L::out_off + warp * 8192;
+    int n_tile = 0, piece = 0;
+    for (int t = pair; t < tiles; t += pairs, ++n_tile) {
+      const int b = n_tile & 1;
+      int tm, tn;
+      order.at(t, tm, tn);
+      const int row0 = tm * 256 + static_cast<int>(rank) * 128 + warp * 32, row = row0 + lane;
+      float f = wscale;
+      if constexpr (FORM == kActNvfp4) f *= row < a.M ? __ldg(a.x_rows + row) : 0.f;
+      bool ok = pair_wait(&acc_full[b], (n_tile >> 1) & 1u, abort_flag, a.status,
+                                     a.wait_limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+#pragma unroll 1
+      for (int cc = 0; cc < NT / 64; ++cc) {
+        // the columns that the other accumulator shares come first
+        const int c = L::kLag == 1 && b == 0 ? NT / 64 - 1 - cc : cc;
+        uint32_t v[64];
+        tmem_ld_32cols(lane_base + b * L::acc_step + c * 64, v);
+        tmem_ld_32cols(lane_base + b * L::acc_step + c * 64 + 32, v + 32);
+        tmem_ld_wait();
+        if (L::kLag == 1 ? cc == 0 : cc == NT / 64 - 1) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) peer_arrive(&acc_empty[b], 0);
+        }
+        const int n0 = tn * NT + c * 64;
+        uint32_t p[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float lo = __uint_as_float(v[2 * j]), hi = __uint_as_float(v[2 * j + 1]);
+          if constexpr (FORM == kActNvfp4) {
+            lo *= f;
+            hi *= f;
+          }
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[j]) : "f"(hi), "f"(lo));
+        }
+        if (use_store) {
+          // a piece of 32 rows by 64 columns through shared memory (128-byte swizzle)
+          if (row0 < a.M && n0 < a.N) {  // warp-uniform
+            uint8_t* dst = out + (piece & 1) * 4096;
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(dst + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                  make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&maps.y, dst, n0, row0);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            ++piece;
+          }
+        } else if (row < a.M) {  // rows of y that are not 16-byte aligned
+          uint16_t* dst = a.y + static_cast<size_t>(row) * a.N;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (n0 + 2 * j < a.N) dst[n0 + 2 * j] = static_cast<uint16_t>(p[j]);
+            if (n0 + 2 * j + 1 < a.N) dst[n0 + 2 * j + 1] = static_cast<uint16_t>(p[j] >> 16);
+          }
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  volatile uint32_t none = 0u;
+  if (!pair_wait(done, 0u, &none, a.status, a.wait_limit_ns) || *abort_flag) {
+    // a wait has run out: the copies in flight (microseconds) land before anything else
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 2000000u) {
+    }
+  }
+  tc_fence_before_sync();
+  __syncwarp();
+  cluster_sync_all();  // neither CTA leaves while the other's MMAs or arrivals reach it
+  if (warp == 5) {
+    tc_fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+  }
+}
+
 // Rows of `K` values as the copies see them: bytes (E2M1 pairs, E4M3), or 4-bit values that the
 // copy widens to a byte each (16 values in the first 8 of 16 bytes, the form kind::mxf8f6f4 reads).
 cudaError_t make_map(CUtensorMap* map, const uint8_t* codes, int rows, int K, int box_rows,
@@ -363,8 +739,55 @@ cudaError_t launch_narrow(const ActMatmulArgs& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, maps, a, splits);
 }
 
+// Scale tiles: 512 bytes (128 words), tiles along k, row blocks.
+cudaError_t make_scale_map(CUtensorMap* map, const uint8_t* scales, int rows, int tiles_k,
+                           int box_tiles, int box_blocks) {
+  const uint64_t dims[3] = {128, static_cast<uint64_t>(tiles_k),
+                            (static_cast<uint64_t>(rows) + 127) / 128};
+  const uint64_t strides[2] = {512, static_cast<uint64_t>(tiles_k) * 512};
+  const uint32_t box[3] = {128, static_cast<uint32_t>(box_tiles),
+                           static_cast<uint32_t>(box_blocks)};
+  return encode_tensor_map_3d(map, CU_TENSOR_MAP_DATA_TYPE_INT32, scales, dims, strides, box,
+                              CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <int FORM, int NT>
+cudaError_t launch_wide(const ActMatmulArgs& a, cudaStream_t stream) {
+  using L = Wide<FORM, NT>;
+  WideMaps maps = {};
+  constexpr bool x8 = FORM == kActMxfp8;
+  cudaError_t e = make_map(&maps.w, a.w_codes, a.N, a.K, NT / 2, false, x8);
+  if (e != cudaSuccess) return e;
+  e = make_map(&maps.x, a.x_codes, a.M, a.K, 128, x8, false);
+  if (e != cudaSuccess) return e;
+  const int tiles_k = (a.K + Form<FORM>::KT - 1) / Form<FORM>::KT;
+  e = make_scale_map(&maps.sx, a.x_scales, a.M, tiles_k, L::kTiles, 1);
+  if (e != cudaSuccess) return e;
+  e = make_scale_map(&maps.sw, a.w_scales, a.N, tiles_k, L::kTiles, L::kBlocks);
+  if (e != cudaSuccess) return e;
+  const int use_store = a.N % 8 == 0;
+  if (use_store) {
+    e = encode_tensor_map(&maps.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.y, static_cast<uint64_t>(a.N),
+                          static_cast<uint64_t>(a.M), static_cast<uint64_t>(a.N) * 2, 64, 32,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+  }
+  auto kern = act_wide_kernel<FORM, NT>;
+  e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(L::alloc));
+  if (e != cudaSuccess) return e;
+  const int sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  WideOrder order = {(a.M + 255) / 256, (a.N + NT - 1) / NT};
+  const long long tiles = static_cast<long long>(order.tm) * order.tn;
+  if (tiles > 0x7fffffffLL - 2 * sms) return cudaErrorInvalidConfiguration;
+  const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+  return launch_with_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kNarrowThreads),
+                         L::alloc, stream, maps, a, order, use_store);
+}
+
 template <int FORM>
 cudaError_t launch_form(const ActMatmulArgs& a, cudaStream_t stream) {
+  if (a.M > 128) return launch_wide<FORM, 256>(a, stream);
   if (a.M <= 16) return launch_narrow<FORM, 16>(a, stream);
   if (a.M <= 32) return launch_narrow<FORM, 32>(a, stream);
   if (a.M <= 64) return launch_narrow<FORM, 64>(a, stream);

@@ -646,14 +646,6 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescSw128)
       : "memory");
 }
-// True in one lane, always the same; the whole warp comes here, so that the values the elected
-// lane issues products with stay uniform.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(p));
-  return p != 0;
-}
 // Instruction descriptor, kind::f16: fp32 accumulator, FP16 A and B, both K-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
