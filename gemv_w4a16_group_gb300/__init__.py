@@ -56,7 +56,7 @@ __all__ = [
     "fp4_matmul_workspace_bytes", "nvfp4_matmul", "mxfp4_matmul", "testing_set_w8_variant",
     "kv4_cache", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_workspace_bytes",
     "kv4_evict", "fp4_prepare_scales", "act_quantize", "act_rmsnorm", "nvfp4_matmul_act",
-    "mxfp4_matmul_act",
+    "mxfp4_matmul_act", "testing_set_act_kernel",
 ]
 
 STATUS_NAMES = {0: "W4A16_OK", 1: "W4A16_ERR_INVALID_ARG", 2: "W4A16_ERR_UNSUPPORTED",
@@ -142,7 +142,7 @@ def _load():
     for name in ("w4a16_testing_force_kernel", "w4a16_testing_set_gemv_max_m",
                  "w4a16_testing_set_q4_variant", "w4a16_testing_set_prepared_min_m",
                  "w4a16_testing_set_prepared_max_m", "w4a16_testing_set_fp4_variant",
-                 "w4a16_testing_set_w8_variant"):
+                 "w4a16_testing_set_w8_variant", "w4a16_testing_set_act_kernel"):
         getattr(lib, name).argtypes = [I]
         getattr(lib, name).restype = I
     lib.w4a16_testing_set_skinny_range.argtypes = [I, I]
@@ -635,6 +635,13 @@ def testing_set_fp4_variant(v: int) -> int:
     """Kernel of nvfp4_gemv / mxfp4_gemv: 1 = tensor-pipe ring (default), 0 = plain loads;
     other values only query. Returns the previous value."""
     return int(_lib.w4a16_testing_set_fp4_variant(v))
+
+
+def testing_set_act_kernel(kernel: int) -> int:
+    """Kernel of nvfp4_matmul_act / mxfp4_matmul_act: 0 = by size (default), 1 = the one for few
+    rows, 2 and 3 = pairs of CTAs on tiles of 256 and 128 columns; other values only query.
+    Returns the previous value."""
+    return int(_lib.w4a16_testing_set_act_kernel(kernel))
 
 
 def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, group: int = 64,

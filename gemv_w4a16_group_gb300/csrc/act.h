@@ -47,6 +47,7 @@ struct ActMatmulArgs {
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
-cudaError_t launch_act_matmul(const ActMatmulArgs& a, int format, cudaStream_t stream);
+// kernel: 0 = by size, 1 = few rows, 2 and 3 = pairs of CTAs on tiles of 256 and 128 columns.
+cudaError_t launch_act_matmul(const ActMatmulArgs& a, int format, int kernel, cudaStream_t stream);
 
 }  // namespace w4k

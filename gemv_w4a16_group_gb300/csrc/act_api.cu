@@ -5,8 +5,11 @@
 #include "act.h"
 #include "launch.h"
 #include "w4a16.h"
+#include "w4a16_testing.h"
 
 namespace {
+
+int g_act_kernel = 0;  // see launch_act_matmul
 
 static_assert(W4A16_ACT_NVFP4 == w4k::kActNvfp4 && W4A16_ACT_MXFP4 == w4k::kActMxfp4 &&
                   W4A16_ACT_MXFP8 == w4k::kActMxfp8,
@@ -48,7 +51,8 @@ w4a16_status matmul(const w4k::ActMatmulArgs& args, int format, w4a16_stream_t s
   a.status = w4k::status_word();
   if (a.status == nullptr) return W4A16_ERR_CUDA;
   a.wait_limit_ns = w4k::kDefaultWaitLimitNs;
-  return from_cuda(w4k::launch_act_matmul(a, format, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(w4k::launch_act_matmul(a, format, g_act_kernel,
+                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -148,6 +152,12 @@ w4a16_status mxfp4_matmul_act(const uint8_t* x_codes, const uint8_t* x_scales, i
   a.N = N;
   a.K = K;
   return matmul(a, x_format, stream);
+}
+
+int w4a16_testing_set_act_kernel(int kernel) {
+  const int prev = g_act_kernel;
+  if (kernel >= 0 && kernel <= 3) g_act_kernel = kernel;
+  return prev;
 }
 
 }  // extern "C"

@@ -786,8 +786,9 @@ cudaError_t launch_wide(const ActMatmulArgs& a, cudaStream_t stream) {
 }
 
 template <int FORM>
-cudaError_t launch_form(const ActMatmulArgs& a, cudaStream_t stream) {
-  if (a.M > 128) return launch_wide<FORM, 256>(a, stream);
+cudaError_t launch_form(const ActMatmulArgs& a, int kernel, cudaStream_t stream) {
+  if (kernel == 2 || (kernel == 0 && a.M > 128)) return launch_wide<FORM, 256>(a, stream);
+  if (kernel == 3) return launch_wide<FORM, 128>(a, stream);
   if (a.M <= 16) return launch_narrow<FORM, 16>(a, stream);
   if (a.M <= 32) return launch_narrow<FORM, 32>(a, stream);
   if (a.M <= 64) return launch_narrow<FORM, 64>(a, stream);
@@ -796,10 +797,10 @@ cudaError_t launch_form(const ActMatmulArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_act_matmul(const ActMatmulArgs& a, int format, cudaStream_t stream) {
-  if (format == kActNvfp4) return launch_form<kActNvfp4>(a, stream);
-  if (format == kActMxfp4) return launch_form<kActMxfp4>(a, stream);
-  return launch_form<kActMxfp8>(a, stream);
+cudaError_t launch_act_matmul(const ActMatmulArgs& a, int format, int kernel, cudaStream_t stream) {
+  if (format == kActNvfp4) return launch_form<kActNvfp4>(a, kernel, stream);
+  if (format == kActMxfp4) return launch_form<kActMxfp4>(a, kernel, stream);
+  return launch_form<kActMxfp8>(a, kernel, stream);
 }
 
 }  // namespace w4k

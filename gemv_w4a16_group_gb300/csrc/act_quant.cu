@@ -12,151 +12,269 @@
 //     value s >= 448 max|z| / a, codes of 2688 z / (s a). Both quotients are taken with numerator
 //     and denominator under powers of two: exact for BF16 rows but for the division, and in range.
 //
-// What bounds it: a row is read once (2 bytes a value, 4 with a residual) and 0.56 to 1.03 bytes
-// (and 2 of the residual) written; a CTA holds its row in registers between the row's sums and
-// the codes. A thread takes pieces of 8 consecutive values (one 16-byte load), so that a block of
+// What bounds it: a row is read once (2 bytes a value, 4 with a residual) and 0.53 to 1.03 bytes
+// (and 2 of the residual) written, so HBM for many rows: 4096 x 4096 with residual and norm 21.1 us
+// (MXFP8, 0.82 of the copy rate) and 18.6 (NVFP4, 0.87), 4096 x 14336 alone 28.6 us (MXFP8, 0.92);
+// a CTA's chain of loads, joins and root for few: one row of 4096 1.3 us alone, 2.2 with norm.
+// A CTA holds its row in registers between the row's sums and the codes, and loads everything the
+// row needs (weights and residual too) at once, before it waits for any of it (26 us of the 21.1
+// with the weights loaded where they are used). Resident CTAs that take rows in turn, the next
+// rows' bulk copies under way, were no faster (24.5): the SMs hold enough CTAs to overlap them.
+// A thread takes pieces of 8 consecutive values (one 16-byte load), so that a block of
 // 16 or 32 is 2 or 4 neighbouring lanes, four blocks' scales make one 32-bit word of a tile, and
-// a warp's codes are contiguous.
+// a warp's codes are contiguous. The arithmetic is on pairs (fp32x2, bf16x2): unpaired it was as
+// long as the copies.
 #include "act.h"
 #include "common.cuh"
 
 namespace w4k {
 namespace {
 
-// Largest |value| by its bits: NaN above infinity above finite.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
+// Largest |value| of 8 BF16 values as a float's bits (NaN above infinity above finite).
+__device__ __forceinline__ uint32_t top_bf16x8(uint4 v) {
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t t = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  return max(t << 16, t & 0xFFFF0000u);
+}
+
+// Smallest E4M3 code whose value is >= v (v > 0), at most 0x7E (448), and that value. From 2^-6 on
+// a code is the float's exponent and three bits of its fraction, below a multiple of 2^-9.
+__device__ __forceinline__ uint32_t e4m3_not_below(float v, float& value) {
+  if (v < 0x1p-6f) {
+    const uint32_t code = __float2uint_ru(v * 512.0f);
+    value = static_cast<float>(code) * 0x1p-9f;
+    return code;
+  }
+  const uint32_t up = min(__float_as_uint(v) + 0xFFFFFu, 0x43E00000u) & 0xFFF00000u;
+  value = __uint_as_float(up);
+  return (up >> 20) - (120u << 3);
+}
+
+// E2M1 codes of 8 values, the first in the lowest bits (nearest, ties to even, saturating at 6).
+__device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
   uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "r"(code));
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(r & 0xFFFFu)));
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x),
+        "f"(v[3].y));
+  return r;
 }
-
-// Smallest E4M3 code whose value is >= v (v >= 0), at most 0x7E (448).
-__device__ __forceinline__ uint32_t e4m3_not_below(float v) {
+// E4M3 codes of two values (nearest, ties to even, saturating at 448).
+__device__ __forceinline__ uint32_t e4m3_pair(float2 v) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(r) : "f"(v));
-  const uint32_t code = r & 0xFFu;
-  return code + (e4m3_value(code) < v && code < 0x7Eu ? 1u : 0u);
-}
-
-// Byte of two E2M1 codes, `lo` in the low half (nearest, ties to even, saturating at 6).
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u16.u8 %0, t;\n\t}"
-      : "=h"(r)
-      : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v.y), "f"(v.x));
   return r;
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ void bf16x8(uint4 in, float (&v)[8]) {
+__device__ __forceinline__ void bf16x8(uint4 in, float2 (&v)[4]) {
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    v[2 * h] = __uint_as_float(w[h] << 16);
-    v[2 * h + 1] = __uint_as_float(w[h] & 0xFFFF0000u);
-  }
+  for (int h = 0; h < 4; ++h)
+    v[h] = make_float2(__uint_as_float(w[h] << 16), __uint_as_float(w[h] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+// bf16(a + b) of each half, rounded once.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
-template <int FORM, bool NORM, int V>
-__global__ void __launch_bounds__(1024) act_quantize_kernel(const ActQuantArgs a) {
-  __shared__ float s_sum[32];
-  __shared__ uint32_t s_max[32];
-  const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, warps = T >> 5;
-  const int m = blockIdx.x, pieces = a.K >> 3;
-  constexpr bool NV = FORM == kActNvfp4;
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "f"(b.x), "f"(b.y));
+  return a;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) { return mul2(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mov.b64 z, {%4, %5};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return a;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "f"(b.x), "f"(b.y));
+  return a;
+}
 
-  pdl_wait();
-  pdl_launch_dependents();
-  const uint4* src = reinterpret_cast<const uint4*>(a.x + m * a.x_stride);
-  uint4 held[V];
+// About 1 / v, for quotients whose residual is put back: the quotient is then within half a last
+// place and 2^-22 of one, so one that fp32 holds comes out exactly.
+__device__ __forceinline__ float near_reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float2 quotient2(float2 num, float den, float inv) {
+  const float2 t = mul2(num, inv);
+  return fma2(fma2(t, make_float2(-den, -den), num), make_float2(inv, inv), t);
+}
+
+// Largest magnitude; NaN above infinity.
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t top_of(const float2 (&v)[4]) {
+  const float t = top3(v[0].x, v[0].y, v[1].x);
+  return abs_bits(top3(top3(t, v[1].y, v[2].x), v[2].y, top3(v[3].x, v[3].y, 0.f)));
+}
+
+// ---- sums and the root in two floats -------------------------------------------------------
+// hi + lo, lo below hi's last place. A code is the exact y's where y is near a border between two
+// codes only if 1 / rms is known well past fp32: with plain fp32 sums about one code in four
+// million was its neighbour. (What an addition loses is kept, exactly but where a square passes
+// the thread's sum so far.)
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const float t = a.hi + b.hi, bb = t - a.hi;
+  return {t, (a.lo + b.lo) + ((a.hi - (t - bb)) + (b.hi - bb))};
+}
+__device__ __forceinline__ Two normal(Two a) {
+  const float t = a.hi + a.lo;
+  return {t, a.lo - (t - a.hi)};
+}
+__device__ __forceinline__ Two warp_sum(Two a) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int p = v * T + tid;
-    held[v] = p < pieces ? src[p] : make_uint4(0u, 0u, 0u, 0u);
-  }
-  float rinv = 1.f;
+  for (int o = 16; o > 0; o >>= 1)
+    a = add(a, {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
+  return a;
+}
+// (s, c) of two sums += v^2, what the sums lose going to c
+__device__ __forceinline__ void add_squares(float2& s, float2& c, float2 v) {
+  const float2 n = fma2(v, v, s);
+  c = add2(c, fma2(v, v, fma2(n, make_float2(-1.f, -1.f), s)));
+  s = n;
+}
+// 1 / sqrt(sum / K + eps) = sqrt(K / T), T = sum + K eps: a first guess r and one step of Newton
+// on K - T r^2, which is taken exactly.
+__device__ __forceinline__ Two inverse_rms(Two sum, float K, float eps) {
+  const float ke = K * eps;
+  const Two T = normal(add(sum, {ke, fmaf(K, eps, -ke)}));
+  const float r = rsqrtf(__fdiv_rn(T.hi, K));
+  const float p = r * r, p_lo = fmaf(r, r, -p);
+  const float q = T.hi * p, q_lo = fmaf(T.hi, p, -q) + fmaf(T.hi, p_lo, T.lo * p);
+  const float step = r * ((K - q) - q_lo) * __fdiv_rn(0.5f, K);
+  // squares past fp32's range: the row becomes NaN, not 0
+  if (!(sum.hi < __uint_as_float(0x7F800000u))) return {__uint_as_float(0x7FC00000u), 0.f};
+  return normal({r, step});
+}
+// z (f.hi + f.lo) in fp32, a last place off towards the exact product where it falls on a value of
+// few bits: there lie the borders between codes, and the exact product may be on either side.
+__device__ __forceinline__ float off_border(float y, float z, Two f) {
+  const float e = fmaf(z, f.lo, fmaf(z, f.hi, -y));
+  const uint32_t b = __float_as_uint(y);
+  if (e == 0.f || !(fabsf(e) < __uint_as_float(0x7F800000u)) || (b << 1) == 0u) return y;
+  return __uint_as_float((e > 0.f) == (y > 0.f) ? b + 1u : b - 1u);
+}
+__device__ __forceinline__ bool few_bits(float y) { return (__float_as_uint(y) & 0x7FFFFu) == 0u; }
+
+// Whether one of the values falls on one of few bits.
+__device__ __forceinline__ bool any_few_bits(const float2 (&y)[4]) {
+  uint32_t t = 0xFFFFFFFFu;
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+    t = min(t, min(__float_as_uint(y[h].x) << 13, __float_as_uint(y[h].y) << 13));
+  return t == 0u;
+}
+
+// What a row's pieces need of the whole row.
+struct RowTerms {
+  Two rinv;        // 1 / rms (1 without a norm)
+  float a10, a12;  // NVFP4: the row's largest |z| under powers of two
+  float i10;       // about 1 / a10
+};
+
+__device__ __forceinline__ uint4 add_rows(uint4 a, uint4 b) {
+  return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z),
+                    add_bf16x2(a.w, b.w));
+}
+
+// A thread's part of the row's sum of squares (NORM) and largest |z| (NVFP4), over its warp.
+template <int FORM, bool NORM, int V>
+__device__ __forceinline__ void warp_terms(const uint4 (&held)[V], const uint4 (&w)[V], Two& sum,
+                                           uint32_t& top) {
   if constexpr (NORM) {
-    if (a.residual) {
-      const uint4* res = reinterpret_cast<const uint4*>(a.residual + m * a.residual_stride);
-      uint4* out = reinterpret_cast<uint4*>(a.residual_out + m * a.residual_out_stride);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int p = v * T + tid;
-        if (p < pieces) {
-          float f[8], g[8];
-          bf16x8(held[v], f);
-          bf16x8(res[p], g);
-          held[v] = make_uint4(bf16_pair(f[0] + g[0], f[1] + g[1]), bf16_pair(f[2] + g[2], f[3] + g[3]),
-                               bf16_pair(f[4] + g[4], f[5] + g[5]), bf16_pair(f[6] + g[6], f[7] + g[7]));
-          out[p] = held[v];
-        }
-      }
-    }
-    float sum = 0.f;
+    float2 s = make_float2(0.f, 0.f), c = make_float2(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float f[8];
+      float2 f[4];
       bf16x8(held[v], f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
+      for (int i = 0; i < 4; ++i) add_squares(s, c, f[i]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    sum = lane < warps ? s_sum[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    rinv = __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, static_cast<float>(a.K)) + a.eps));
-    // squares past fp32's range: the row becomes NaN, not 0
-    if (!(sum < __uint_as_float(0x7F800000u))) rinv = __uint_as_float(0x7FC00000u);
+    sum = warp_sum(add({s.x, c.x}, {s.y, c.y}));
   }
-  const uint4* wsrc = reinterpret_cast<const uint4*>(a.weight);
-  float amax = 1.f, a10 = 1.f, a12 = 1.f;
-  if constexpr (NV) {
-    uint32_t top = 0u;
+  if constexpr (FORM == kActNvfp4) {
+    top = 0u;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int p = v * T + tid;
-      float f[8];
-      bf16x8(held[v], f);
       if constexpr (NORM) {
-        float w[8];
-        bf16x8(p < pieces ? wsrc[p] : make_uint4(0u, 0u, 0u, 0u), w);
+        float2 f[4], g[4];
+        bf16x8(held[v], f);
+        bf16x8(w[v], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= w[i];
+        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], g[i]);
+        top = max(top, top_of(f));
+      } else {
+        top = max(top, top_bf16x8(held[v]));
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, abs_bits(f[i]));
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) s_max[warp] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
+  }
+}
+
+// The row's terms from its warps' (in shared memory), the same in every thread; thread 0 writes
+// the row's scale.
+template <int FORM, bool NORM>
+__device__ __forceinline__ RowTerms row_terms(const ActQuantArgs& a, int m, const Two* s_sum,
+                                              const uint32_t* s_max, int warps, int group) {
+  const int lane = threadIdx.x & 31, at = lane & (group - 1);
+  RowTerms r = {{1.f, 0.f}, 1.f, 1.f, 1.f};
+  if constexpr (NORM) {
+    Two sum = at < warps ? s_sum[at] : Two{0.f, 0.f};
+    for (int o = group >> 1; o > 0; o >>= 1)
+      sum = add(sum, {__shfl_xor_sync(0xffffffffu, sum.hi, o),
+                      __shfl_xor_sync(0xffffffffu, sum.lo, o)});
+    r.rinv = inverse_rms(sum, static_cast<float>(a.K), a.eps);
+  }
+  if constexpr (FORM == kActNvfp4) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, at < warps ? s_max[at] : 0u);
     // an infinity makes the row's scale NaN, as a NaN does
-    amax = top < 0x7F800000u ? fmaxf(__uint_as_float(top), 0x1p-80f) : __uint_as_float(0x7FC00000u);
-    a10 = amax * 0x1p-10f;
-    a12 = amax * 0x1p-12f;
-    if (tid == 0) {
+    const float amax =
+        top < 0x7F800000u ? fmaxf(__uint_as_float(top), 0x1p-80f) : __uint_as_float(0x7FC00000u);
+    r.a10 = amax * 0x1p-10f;
+    r.a12 = amax * 0x1p-12f;
+    r.i10 = near_reciprocal(r.a10);
+    if (threadIdx.x == 0) {
       const float s = __fdiv_rn(amax, 2688.0f);
-      a.row_scales[m] = NORM ? s * rinv : s;
+      a.row_scales[m] = NORM ? s * r.rinv.hi : s;
     }
   }
+  return r;
+}
+
+// Codes and scales of a thread's pieces of row m.
+template <int FORM, bool NORM, int V>
+__device__ __forceinline__ void write_row(const ActQuantArgs& a, int m, const uint4 (&held)[V],
+                                          const uint4 (&weight)[V], const RowTerms& row) {
+  constexpr bool NV = FORM == kActNvfp4;
+  const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31;
+  const int pieces = a.K >> 3;
   // scale words of this row: tile (m / 128, word), 512 bytes apart
   const int words = (a.K + (NV ? 63 : 127)) / (NV ? 64 : 128);
   uint32_t* stile = reinterpret_cast<uint32_t*>(a.scales) +
@@ -166,40 +284,40 @@ __global__ void __launch_bounds__(1024) act_quantize_kernel(const ActQuantArgs a
     if (v * T + warp * 32 >= pieces) break;  // warp-uniform
     const int p = v * T + tid;
     const bool in = p < pieces;
-    float f[8];
+    float2 f[4];
     bf16x8(held[v], f);
+    uint32_t top;
     if constexpr (NORM) {
-      float w[8];
-      bf16x8(in ? wsrc[p] : make_uint4(0u, 0u, 0u, 0u), w);
+      float2 w[4];
+      bf16x8(weight[v], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = NV ? f[i] * w[i] : f[i] * w[i] * rinv;
+      for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w[i]);
+      top = top_of(f);
+    } else {
+      top = top_bf16x8(held[v]);
     }
-    uint32_t top = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, abs_bits(f[i]));
-    if (!in) top = 0u;  // a NaN row times the weights' zeros behind its end
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     if constexpr (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     uint32_t sc = 0u;
     if constexpr (NV) {
-      float q[8];
-      if (top != 0u) sc = e4m3_not_below(__fdiv_rn(__uint_as_float(top) * 0.4375f, a10));
-      const float den = sc != 0u ? e4m3_value(sc) * a12 : 1.f;
-      const float inv = __frcp_rn(den);
+      // quotients with the residual put back: the ties among them come out exactly
+      const float2 top2 = make_float2(__uint_as_float(top) * 0.4375f, 0.f);
+      float value = 1.f;
+      if (top != 0u) sc = e4m3_not_below(quotient2(top2, row.a10, row.i10).x, value);
+      const float den = value * row.a12, inv = near_reciprocal(den);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // num / den: the quotient's residual put back, so that quotients that fp32 holds
-        // (the ties among them) come out exactly
-        const float num = f[i] * 0.65625f;
-        const float t = num * inv;
-        q[i] = fmaf(fmaf(-t, den, num), inv, t);
-      }
-      const uint32_t c = e2m1_pair(q[0], q[1]) | (e2m1_pair(q[2], q[3]) << 8) |
-                         (e2m1_pair(q[4], q[5]) << 16) | (e2m1_pair(q[6], q[7]) << 24);
+      for (int i = 0; i < 4; ++i) f[i] = quotient2(mul2(f[i], 0.65625f), den, inv);
+      const uint32_t c = e2m1x8(f);
       if (in)
         reinterpret_cast<uint32_t*>(a.codes + static_cast<size_t>(m) * (a.K >> 1))[p] =
             sc != 0u ? c : 0u;
     } else {
+      if constexpr (NORM) {
+        // the largest |y|, towards its exact value where it is a power of two
+        const float z = __uint_as_float(top), y = z * row.rinv.hi;
+        top = abs_bits(few_bits(y) ? off_border(y, z, row.rinv) : y);
+        if (!in) top = 0u;  // a NaN row's NaN does not reach past its end
+      }
       // exponent of the block's largest value (subnormal ones too), less E2M1's or E4M3's top
       int X = -127;
       if (top != 0u) {
@@ -208,20 +326,30 @@ __global__ void __launch_bounds__(1024) act_quantize_kernel(const ActQuantArgs a
         X = max(X, -127);
         sc = top < 0x7F800000u ? static_cast<uint32_t>(X + 127) : 0xFFu;
       }
-      // 2^-X in two normal factors: -X reaches 127 and falls to -125
-      const float s1 = __uint_as_float(static_cast<uint32_t>(127 - (X >> 1)) << 23);
-      const float s2 = __uint_as_float(static_cast<uint32_t>(127 - (X - (X >> 1))) << 23);
+      const float scale = __uint_as_float(static_cast<uint32_t>(127 - X) << 23);  // 2^-X
+      if constexpr (NORM) {
+        float2 y[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * s1 * s2;
+        for (int i = 0; i < 4; ++i) y[i] = mul2(f[i], row.rinv.hi);
+        if (any_few_bits(y))
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (few_bits(y[i].x)) y[i].x = off_border(y[i].x, f[i].x, row.rinv);
+            if (few_bits(y[i].y)) y[i].y = off_border(y[i].y, f[i].y, row.rinv);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = y[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], scale);
       if constexpr (FORM == kActMxfp4) {
-        const uint32_t c = e2m1_pair(f[0], f[1]) | (e2m1_pair(f[2], f[3]) << 8) |
-                           (e2m1_pair(f[4], f[5]) << 16) | (e2m1_pair(f[6], f[7]) << 24);
+        const uint32_t c = e2m1x8(f);
         if (in)
           reinterpret_cast<uint32_t*>(a.codes + static_cast<size_t>(m) * (a.K >> 1))[p] =
               top != 0u ? c : 0u;
       } else {
-        const uint32_t lo = e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
-        const uint32_t hi = e4m3_pair(f[4], f[5]) | (e4m3_pair(f[6], f[7]) << 16);
+        const uint32_t lo = e4m3_pair(f[0]) | (e4m3_pair(f[1]) << 16);
+        const uint32_t hi = e4m3_pair(f[2]) | (e4m3_pair(f[3]) << 16);
         if (in)
           reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m) * a.K)[p] =
               top != 0u ? make_uint2(lo, hi) : make_uint2(0u, 0u);
@@ -237,18 +365,87 @@ __global__ void __launch_bounds__(1024) act_quantize_kernel(const ActQuantArgs a
   }
 }
 
+// A CTA a row.
+template <int FORM, bool NORM, int V>
+__global__ void __launch_bounds__(V > 2 ? 512 : 1024)
+    act_row_kernel(const ActQuantArgs a, int group) {
+  __shared__ Two s_sum[32];
+  __shared__ uint32_t s_max[32];
+  const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, warps = T >> 5;
+  const int m = blockIdx.x, pieces = a.K >> 3;
+
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint4* src = reinterpret_cast<const uint4*>(a.x + m * a.x_stride);
+  const uint4* res = reinterpret_cast<const uint4*>(a.residual + m * a.residual_stride);
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 held[V], w[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = v * T + tid;
+    held[v] = p < pieces ? src[p] : zero;
+    w[v] = NORM && p < pieces ? reinterpret_cast<const uint4*>(a.weight)[p] : zero;
+  }
+  if (NORM && a.residual) {
+    uint4* out = reinterpret_cast<uint4*>(a.residual_out + m * a.residual_out_stride);
+    uint4 r[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = v * T + tid;
+      r[v] = p < pieces ? res[p] : zero;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = v * T + tid;
+      held[v] = add_rows(held[v], r[v]);
+      if (p < pieces) out[p] = held[v];
+    }
+  }
+  if constexpr (NORM || FORM == kActNvfp4) {
+    Two sum = {0.f, 0.f};
+    uint32_t top = 0u;
+    warp_terms<FORM, NORM, V>(held, w, sum, top);
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_max[warp] = top;
+    }
+    __syncthreads();
+  }
+  const RowTerms row = row_terms<FORM, NORM>(a, m, s_sum, s_max, warps, group);
+  write_row<FORM, NORM, V>(a, m, held, w, row);
+}
+
+template <int FORM, bool NORM, int V>
+cudaError_t launch_pieces(const ActQuantArgs& a, cudaStream_t stream) {
+  const int pieces = a.K / 8;
+  const int threads = ((pieces + V - 1) / V + 31) / 32 * 32;
+  int group = 1;  // the power of two not below the number of warps
+  while (group < threads / 32) group *= 2;
+  return launch_with_pdl(act_row_kernel<FORM, NORM, V>, dim3(static_cast<unsigned>(a.M)),
+                         dim3(static_cast<unsigned>(threads)), 0, stream, a, group);
+}
+
 template <int FORM, bool NORM>
 cudaError_t launch_form(const ActQuantArgs& a, cudaStream_t stream) {
-  const int pieces = a.K / 8;
+  // Pieces a thread. Few rows are a matter of latency: one piece each, while 1024 threads hold the
+  // row (one row of 4096 with norm 2.2 us, with two pieces 2.8, four 4.2). Many rows keep the SMs
+  // full whatever a CTA's size, and fewer threads a row join in fewer steps: four (4096 x 4096
+  // with norm 21.1 us, two 22.5, one 28), down to some 100 threads. Longer rows take what 512
+  // threads need.
+  const int pieces = a.K / 8, sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   int v = 1;
-  while (v < 8 && pieces > 256 * v) v *= 2;
-  int threads = ((pieces + v - 1) / v + 31) / 32 * 32;
-  const dim3 grid(static_cast<unsigned>(a.M)), block(static_cast<unsigned>(threads));
+  if (a.M < 2 * sms)
+    while (v < 2 && pieces > 1024 * v) v *= 2;
+  else
+    while (v < 4 && pieces >= 96 * 2 * v) v *= 2;
+  while (pieces > (v <= 2 ? 1024 : 512) * v) v *= 2;
   switch (v) {
-    case 1: return launch_with_pdl(act_quantize_kernel<FORM, NORM, 1>, grid, block, 0, stream, a);
-    case 2: return launch_with_pdl(act_quantize_kernel<FORM, NORM, 2>, grid, block, 0, stream, a);
-    case 4: return launch_with_pdl(act_quantize_kernel<FORM, NORM, 4>, grid, block, 0, stream, a);
-    default: return launch_with_pdl(act_quantize_kernel<FORM, NORM, 8>, grid, block, 0, stream, a);
+    case 1: return launch_pieces<FORM, NORM, 1>(a, stream);
+    case 2: return launch_pieces<FORM, NORM, 2>(a, stream);
+    case 4: return launch_pieces<FORM, NORM, 4>(a, stream);
+    case 8: return launch_pieces<FORM, NORM, 8>(a, stream);
+    default: return launch_pieces<FORM, NORM, 16>(a, stream);
   }
 }
 

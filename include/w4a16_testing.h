@@ -51,6 +51,11 @@ int w4a16_testing_set_fp4_variant(int v);
  * values only query. Returns the previous value. */
 int w4a16_testing_set_w8_variant(int v);
 
+/* Kernel of nvfp4_matmul_act / mxfp4_matmul_act: 0 = by size (default), 1 = the one for few rows,
+ * 2 and 3 = pairs of CTAs on tiles of 256 x 256 and 256 x 128. Other values only query. Returns
+ * the previous value. */
+int w4a16_testing_set_act_kernel(int kernel);
+
 #ifdef __cplusplus
 }
 #endif
