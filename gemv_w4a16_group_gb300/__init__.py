@@ -639,8 +639,8 @@ def testing_set_fp4_variant(v: int) -> int:
 
 def testing_set_act_kernel(kernel: int) -> int:
     """Kernel of nvfp4_matmul_act / mxfp4_matmul_act: 0 = by size (default), 1 = the one for few
-    rows, 2 and 3 = pairs of CTAs on tiles of 256 and 128 columns; other values only query.
-    Returns the previous value."""
+    rows, 2 = pairs of CTAs on tiles of 256 x 256, 3 and 4 = two and four pairs a tile; other
+    values only query. Returns the previous value."""
     return int(_lib.w4a16_testing_set_act_kernel(kernel))
 
 

@@ -47,7 +47,7 @@ struct ActMatmulArgs {
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
-// kernel: 0 = by size, 1 = few rows, 2 and 3 = pairs of CTAs on tiles of 256 and 128 columns.
+// kernel: 0 = by size, 1 = few rows, 2 = pairs of CTAs, 3 and 4 = two and four pairs a tile.
 cudaError_t launch_act_matmul(const ActMatmulArgs& a, int format, int kernel, cudaStream_t stream);
 
 }  // namespace w4k

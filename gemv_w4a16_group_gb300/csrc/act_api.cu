@@ -156,7 +156,7 @@ w4a16_status mxfp4_matmul_act(const uint8_t* x_codes, const uint8_t* x_scales, i
 
 int w4a16_testing_set_act_kernel(int kernel) {
   const int prev = g_act_kernel;
-  if (kernel >= 0 && kernel <= 3) g_act_kernel = kernel;
+  if (kernel >= 0 && kernel <= 4) g_act_kernel = kernel;
   return prev;
 }
 

@@ -94,9 +94,39 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t desc) {
         : "memory");
 }
 
+// mbar_wait_bounded for stages that change hands every few hundred nanoseconds: without a hint to
+// suspend, and with the clock, whose reading takes longer than most waits, first read after some
+// tries.
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity,
+                                           volatile uint32_t* abort_flag, uint32_t* status,
+                                           uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 31u) != 0) continue;
+    if (*abort_flag) return false;
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0) {
+      t0 = t;
+    } else if (t - t0 > limit_ns) {
+      *abort_flag = 1u;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
 // One stage's scales and products: `a` and `b` the operands' tiles, sa and sb their scale tiles
 // (low words of descriptors), BLOCKS_B row blocks of b's scales; columns of the scales in tensor
-// memory at ca and cb. WHOLE: all of the stage's k lies in the row; else `left` values of it.
+// memory at ca and cb. (Tiles begin at a block: scales that begin at an odd column fault.) WHOLE: all of the stage's k lies in the row; else `left` values of it.
 template <int FORM, int GROUP, int BLOCKS_B, bool WHOLE>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t b, uint32_t sa,
                                             uint32_t sb, uint32_t ca, uint32_t cb, uint32_t idesc,
@@ -129,6 +159,13 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
+}
+__device__ __forceinline__ float4 peer_lds128(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
 }
 __device__ __forceinline__ float2 peer_lds64(uint32_t addr) {
   float2 v;
@@ -165,36 +202,13 @@ __device__ __forceinline__ void pair_load_3d(void* smem_dst, const CUtensorMap* 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// mbar_wait_bounded without a hint to suspend: the pair's stages change hands faster.
-__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity,
-                                          volatile uint32_t* abort_flag, uint32_t* status,
-                                          uint64_t limit_ns) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (*abort_flag) return false;
-    if (i == 0) t0 = global_timer_ns();
-    else if ((i & 15u) == 0 && global_timer_ns() - t0 > limit_ns) {
-      *abort_flag = 1u;
-      atomicOr(status, kStatusTimeout);
-      return false;
-    }
-  }
-}
-// Arrives (once) on `bar` of both CTAs of the pair when every MMA issued before has completed.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+// Arrives (once) on `bar` of the pair's two CTAs (a bit each in `mask`, by rank in the cluster)
+// when every MMA issued before has completed.
+__device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(smem_addr(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(mask)
       : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int x,
@@ -292,7 +306,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       const uint8_t* sx = a.x_scales + static_cast<size_t>(m0 >> 7) * tiles_all * 512;
       for (int i = 0; i < count; ++i) {
         const int s = i % S;
-        if (i >= S && !mbar_wait_bounded(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, a.status,
+        if (i >= S && !stage_wait(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, a.status,
                                          a.wait_limit_ns))
           break;
         const int t0 = (first + i) * L::kTiles;
@@ -315,7 +329,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     const uint32_t sw0 = desc_low(smem + L::sw_off), sx0 = desc_low(smem + L::sx_off);
     for (int i = 0; i < count; ++i) {
       const int s = i % S;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (i / S) & 1u, abort_flag, a.status,
+      if (!__all_sync(0xffffffffu, stage_wait(&full[s], (i / S) & 1u, abort_flag, a.status,
                                                      a.wait_limit_ns)))
         break;
       tc_fence_after_sync();
@@ -337,11 +351,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   }
   __syncwarp();
   volatile uint32_t none = 0u;
-  bool ok = mbar_wait_bounded(done, 0u, &none, a.status, a.wait_limit_ns);
+  bool ok = stage_wait(done, 0u, &none, a.status, a.wait_limit_ns);
   if (!ok || *abort_flag)  // a wait has run out: the copies in flight land before anything else
     for (int s = 0; s < S && s < issued; ++s) {
       const int last = issued - 1 - ((issued - 1 - s) % S);
-      mbar_wait_bounded(&full[s], (last / S) & 1u, &none, a.status, a.wait_limit_ns);
+      stage_wait(&full[s], (last / S) & 1u, &none, a.status, a.wait_limit_ns);
     }
   __syncwarp();
   __syncthreads();
@@ -414,6 +428,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 // columns (B, half of the weights' rows in either CTA's shared memory), so that an operand's
 // byte feeds twice the products of one CTA's tile. Persistent pairs; the accumulator has two
 // places, so that a tile's MMAs run while the last one's sums are scaled, rounded and stored.
+// With fewer tiles than pairs, a cluster of SPLIT pairs shares a tile, each with its part of k, and
+// adds the parts up through distributed shared memory in the pairs' order.
 struct WideMaps {
   CUtensorMap w, x, sw, sx, y;
 };
@@ -422,16 +438,17 @@ template <int FORM, int NT>
 struct Wide {
   using F = Form<FORM>;
   static constexpr int kTiles = F::KS / F::KT;
-  static constexpr int kBlocks = NT / 128;  // row blocks of weights' scales
+  static constexpr int kBlocks = NT / 128;  // row blocks of the weights' scales
   static constexpr uint32_t x_bytes = 128 * 128, w_bytes = NT / 2 * 128;
   static constexpr uint32_t w_tx = FORM == kActMxfp8 ? w_bytes / 2 : w_bytes;
   static constexpr uint32_t s_bytes = kTiles * 512;
   static constexpr uint32_t stage_bytes = x_bytes + w_bytes + (1 + kBlocks) * s_bytes;
   static constexpr uint32_t tx_bytes = x_bytes + w_tx + (1 + kBlocks) * s_bytes;  // of a CTA
-  static constexpr uint32_t out_bytes = 4 * 2 * 4096;  // two pieces of 32 rows x 64 a warp
-  static constexpr int kMost = (227 * 1024 - 1024 - 512 - static_cast<int>(out_bytes)) /
-                               static_cast<int>(stage_bytes);
-  static constexpr int kStages = kMost < 8 ? kMost : 8;
+  // pieces of y on their way out, 32 rows by 64 columns: two a warp where that costs no stage
+  static constexpr int kRoom = 227 * 1024 - 256;
+  static constexpr int kStages = (kRoom - 4 * 4096) / static_cast<int>(stage_bytes);
+  static constexpr int kOut = (kRoom - 2 * 4 * 4096) / static_cast<int>(stage_bytes) == kStages ? 2 : 1;
+  static constexpr uint32_t out_bytes = 4 * kOut * 4096;
   static constexpr uint32_t w_off = kStages * x_bytes;
   static constexpr uint32_t out_off = w_off + kStages * w_bytes;
   static constexpr uint32_t sx_off = out_off + out_bytes;
@@ -439,16 +456,21 @@ struct Wide {
   static constexpr uint32_t bar_off = sw_off + kStages * kBlocks * s_bytes;
   // full (both CTAs' copies, in the first), empty; the accumulators' full (2), empty (2); done
   static constexpr uint32_t misc_off = bar_off + (2 * kStages + 5) * 8;
-  static constexpr uint32_t total = misc_off + 16;
-  static constexpr uint32_t alloc = total + 1024;
+  static constexpr uint32_t alloc = misc_off + 16;
   static_assert(alloc <= 227 * 1024, "shared memory");
-  // Tensor memory: 512 columns hold two accumulators of 256 only without the scales (48 at most).
-  // The two overlap by 64 columns, which a tile's epilogue empties first.
-  static constexpr uint32_t acc_step = NT == 256 ? 192 : NT;
-  static constexpr int kLag = NT == 256 ? 1 : 2;  // tiles between an accumulator's fill and reuse
+  // Tensor memory: the scales, and two accumulators, which overlap where 512 columns do not hold
+  // them apart; a tile's epilogue empties the columns that they share first.
+  static constexpr uint32_t s_cols = 4 * kTiles * (1 + kBlocks);
+  static constexpr uint32_t acc_step =
+      512 - 2 * NT >= s_cols ? NT : (512 - NT - s_cols) / 64 * 64;
+  static constexpr int kShared = (NT - static_cast<int>(acc_step)) / 64;  // 64-column pieces
+  // a part of the sums between pairs: rows of NT floats, four apart in their banks
+  static constexpr int kPartRow = NT + 4;
+  static_assert(128 * kPartRow * 4 <= kStages * (x_bytes + w_bytes), "parts reuse the ring");
+  static constexpr int kLag = kShared > 0 ? 1 : 2;  // tiles between an accumulator's fill and reuse
   static constexpr uint32_t sx_col = acc_step + NT;
   static constexpr uint32_t sw_col = sx_col + 4 * kTiles;
-  static_assert(sw_col + 4 * kTiles * kBlocks <= 512, "tensor memory");
+  static_assert(sx_col + s_cols <= 512, "tensor memory");
 };
 
 // Tiles in the order of their work: kGroup row tiles side by side, columns in turn, so that what
@@ -464,16 +486,14 @@ struct WideOrder {
   }
 };
 
-template <int FORM, int NT>
-__global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
+template <int FORM, int NT, int SPLIT>
+__global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
     act_wide_kernel(const __grid_constant__ WideMaps maps, const ActMatmulArgs a, const WideOrder order,
                     int use_store) {
   using L = Wide<FORM, NT>;
   using F = Form<FORM>;
   constexpr int S = L::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // (no room to align it by hand)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
@@ -482,10 +502,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile uint32_t* abort_flag = holder + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // rank in the pair; the pair's part of k, its first CTA and both as a mask
+  const uint32_t rank = cluster_rank() & 1u, part = cluster_rank() >> 1, lead = 2 * part;
+  const uint16_t both = static_cast<uint16_t>(3u << lead);
+  const int first = blockIdx.x / (2 * SPLIT), step = gridDim.x / (2 * SPLIT);
   const int tiles = order.tm * order.tn;
-  const int stages = (a.K + F::KS - 1) / F::KS;
+  const int stages = (a.K + F::KS - 1) / F::KS;  // SPLIT at least: no part is empty
+  const int begin = static_cast<int>(part) * stages / SPLIT;
+  const int end = (static_cast<int>(part) + 1) * stages / SPLIT;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -522,17 +546,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (warp == 4) {
     if (lane == 0) {
-      const uint32_t full0 = peer_addr(smem_addr(full), 0);
+      const uint32_t full0 = peer_addr(smem_addr(full), lead);
       const int w_row = static_cast<int>(rank) * (NT / 2);
       int s = 0;
       uint32_t phase = 1;  // of the stage's last use
       bool go = true;
-      for (int t = pair; t < tiles && go; t += pairs) {
+      for (int t = first; t < tiles && go; t += step) {
         int tm, tn;
         order.at(t, tm, tn);
         const int bm = tm * 2 + static_cast<int>(rank);
-        for (int i = 0; i < stages; ++i) {
-          if (!pair_wait(&empty[s], phase, abort_flag, a.status, a.wait_limit_ns)) {
+        for (int i = begin; i < end; ++i) {
+          if (!stage_wait(&empty[s], phase, abort_flag, a.status, a.wait_limit_ns)) {
             go = false;
             break;
           }
@@ -541,8 +565,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
           // rows past the arrays come as zeros, tiles of scales past a row's end as another's:
           // the first are not stored, the second not multiplied
           pair_load_2d(smem + s * L::x_bytes, &maps.x, bar, i * 128, bm * 128);
-          pair_load_2d(smem + L::w_off + s * L::w_bytes, &maps.w, bar, i * 128, tn * NT + w_row);
           pair_load_3d(smem + L::sx_off + s * L::s_bytes, &maps.sx, bar, 0, i * L::kTiles, bm);
+          pair_load_2d(smem + L::w_off + s * L::w_bytes, &maps.w, bar, i * 128, tn * NT + w_row);
           pair_load_3d(smem + L::sw_off + s * L::kBlocks * L::s_bytes, &maps.sw, bar, 0,
                        i * L::kTiles, tn * L::kBlocks);
           if (++s == S) {
@@ -561,20 +585,20 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
     int s = 0, n_tile = 0;
     uint32_t phase = 0;
     bool go = true;
-    for (int t = pair; t < tiles && go; t += pairs, ++n_tile) {
+    for (int t = first; t < tiles && go; t += step, ++n_tile) {
       const int b = n_tile & 1;
       const uint32_t acc = tmem + b * L::acc_step;
       if (n_tile >= L::kLag) {
         const int q = n_tile - L::kLag;  // the tile whose columns must be empty
         go = __all_sync(0xffffffffu,
-                        pair_wait(&acc_empty[q & 1], (q >> 1) & 1u, abort_flag, a.status,
+                        stage_wait(&acc_empty[q & 1], (q >> 1) & 1u, abort_flag, a.status,
                                              a.wait_limit_ns));
         if (!go) break;
         tc_fence_after_sync();
       }
-      for (int i = 0; i < stages; ++i) {
+      for (int i = begin; i < end; ++i) {
         go = __all_sync(0xffffffffu,
-                        pair_wait(&full[s], phase, abort_flag, a.status, a.wait_limit_ns));
+                        stage_wait(&full[s], phase, abort_flag, a.status, a.wait_limit_ns));
         if (!go) break;
         tc_fence_after_sync();
         const int left = a.K - i * F::KS;
@@ -583,11 +607,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t bs = sw0 + s * (L::kBlocks * L::s_bytes >> 4);
         if (elect_one()) {
           if (left >= F::KS)
-            issue_stage<FORM, 2, L::kBlocks, true>(acc, ax, bw, as, bs, ca, cb, idesc, i == 0, left);
+            issue_stage<FORM, 2, L::kBlocks, true>(acc, ax, bw, as, bs, ca, cb, idesc, i == begin, left);
           else
-            issue_stage<FORM, 2, L::kBlocks, false>(acc, ax, bw, as, bs, ca, cb, idesc, i == 0, left);
-          pair_commit(&empty[s]);
-          if (i == stages - 1) pair_commit(&acc_full[b]);
+            issue_stage<FORM, 2, L::kBlocks, false>(acc, ax, bw, as, bs, ca, cb, idesc, i == begin, left);
+          pair_commit(&empty[s], both);
+          if (i == end - 1) pair_commit(&acc_full[b], both);
         }
         __syncwarp();
         if (++s == S) {
@@ -596,20 +620,21 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
     }
-    if (elect_one()) pair_commit(done);
+    if (elect_one()) pair_commit(done, both);
   } else if (warp < 4) {
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float wscale = FORM == kActNvfp4 ? __ldg(a.w_scale) : 1.f;
-    uint8_t* out = smem + L::out_off + warp * 8192;
+    uint8_t* out = smem + L::out_off + warp * (L::kOut * 4096);
     int n_tile = 0, piece = 0;
-    for (int t = pair; t < tiles; t += pairs, ++n_tile) {
+    for (int t = first; t < tiles; t += step, ++n_tile) {
       const int b = n_tile & 1;
       int tm, tn;
       order.at(t, tm, tn);
-      const int row0 = tm * 256 + static_cast<int>(rank) * 128 + warp * 32, row = row0 + lane;
+      const int row0 = tm * 256 + static_cast<int>(rank) * 128 + warp * 32;
+      const int row = row0 + lane;
       float f = wscale;
       if constexpr (FORM == kActNvfp4) f *= row < a.M ? __ldg(a.x_rows + row) : 0.f;
-      bool ok = pair_wait(&acc_full[b], (n_tile >> 1) & 1u, abort_flag, a.status,
+      bool ok = stage_wait(&acc_full[b], (n_tile >> 1) & 1u, abort_flag, a.status,
                                      a.wait_limit_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -617,15 +642,24 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
       for (int cc = 0; cc < NT / 64; ++cc) {
         // the columns that the other accumulator shares come first
-        const int c = L::kLag == 1 && b == 0 ? NT / 64 - 1 - cc : cc;
+        const int c = L::kShared > 0 && b == 0 ? NT / 64 - 1 - cc : cc;
         uint32_t v[64];
         tmem_ld_32cols(lane_base + b * L::acc_step + c * 64, v);
         tmem_ld_32cols(lane_base + b * L::acc_step + c * 64 + 32, v + 32);
         tmem_ld_wait();
-        if (L::kLag == 1 ? cc == 0 : cc == NT / 64 - 1) {
+        if (cc == (L::kShared > 0 ? L::kShared : NT / 64) - 1) {
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) peer_arrive(&acc_empty[b], 0);
+          if (lane == 0) peer_arrive(&acc_empty[b], lead);
+        }
+        if constexpr (SPLIT > 1) {
+          // the pair's part of the sums, where its stages were
+          float4* to = reinterpret_cast<float4*>(smem) + (warp * 32 + lane) * (L::kPartRow / 4) + c * 16;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            to[j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+          continue;
         }
         const int n0 = tn * NT + c * 64;
         uint32_t p[32];
@@ -641,8 +675,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
         if (use_store) {
           // a piece of 32 rows by 64 columns through shared memory (128-byte swizzle)
           if (row0 < a.M && n0 < a.N) {  // warp-uniform
-            uint8_t* dst = out + (piece & 1) * 4096;
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            uint8_t* dst = out + piece * 4096;
+            if constexpr (L::kOut == 2) piece ^= 1;
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(L::kOut - 1) : "memory");
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -654,7 +689,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
               tma_store_2d(&maps.y, dst, n0, row0);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
-            ++piece;
           }
         } else if (row < a.M) {  // rows of y that are not 16-byte aligned
           uint16_t* dst = a.y + static_cast<size_t>(row) * a.N;
@@ -670,7 +704,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
   }
   __syncwarp();
   volatile uint32_t none = 0u;
-  if (!pair_wait(done, 0u, &none, a.status, a.wait_limit_ns) || *abort_flag) {
+  if (!stage_wait(done, 0u, &none, a.status, a.wait_limit_ns) || *abort_flag) {
     // a wait has run out: the copies in flight (microseconds) land before anything else
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 2000000u) {
@@ -678,6 +712,59 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2, 1, 1)
   }
   tc_fence_before_sync();
   __syncwarp();
+  if constexpr (SPLIT > 1) {
+    cluster_sync_all();  // the parts stand
+    int tm, tn;
+    order.at(first, tm, tn);
+    const bool ok = *abort_flag == 0u;
+    const float wscale = FORM == kActNvfp4 ? __ldg(a.w_scale) : 1.f;
+    const uint32_t base = smem_addr(smem);
+    // this pair's share of the columns, four at a time; neighbouring threads take neighbours, and
+    // the loads of kBatch turns are on their way together
+    constexpr int kQuads = NT / SPLIT / 4, kBatch = 4;
+    for (int q0 = threadIdx.x; q0 < 128 * kQuads; q0 += kBatch * kNarrowThreads) {
+      float4 v[kBatch][SPLIT];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int q = min(q0 + u * kNarrowThreads, 128 * kQuads - 1), r = q / kQuads;
+        const int c = (static_cast<int>(part) * kQuads + q % kQuads) * 4;
+#pragma unroll
+        for (int p = 0; p < SPLIT; ++p)
+          v[u][p] = peer_lds128(peer_addr(base + (r * L::kPartRow + c) * 4, 2 * p + rank));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int q = q0 + u * kNarrowThreads, r = q / kQuads;
+        const int c = (static_cast<int>(part) * kQuads + q % kQuads) * 4;
+        const int row = tm * 256 + static_cast<int>(rank) * 128 + r, n = tn * NT + c;
+        if (!ok || q >= 128 * kQuads || row >= a.M || n >= a.N) continue;
+        float4 sum = v[u][0];
+#pragma unroll
+        for (int p = 1; p < SPLIT; ++p) {
+          sum.x += v[u][p].x;
+          sum.y += v[u][p].y;
+          sum.z += v[u][p].z;
+          sum.w += v[u][p].w;
+        }
+        float f = wscale;
+        if constexpr (FORM == kActNvfp4) f *= __ldg(a.x_rows + row);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x * f, sum.y * f);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z * f, sum.w * f);
+        uint16_t* out = a.y + static_cast<size_t>(row) * a.N + n;
+        const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                   *reinterpret_cast<const uint32_t*>(&hi));
+        if (a.N % 4 == 0) {
+          *reinterpret_cast<uint2*>(out) = w;
+        } else {
+          out[0] = static_cast<uint16_t>(w.x);
+          if (n + 1 < a.N) out[1] = static_cast<uint16_t>(w.x >> 16);
+          if (n + 2 < a.N) out[2] = static_cast<uint16_t>(w.y);
+          if (n + 3 < a.N) out[3] = static_cast<uint16_t>(w.y >> 16);
+        }
+      }
+    }
+    __syncwarp();
+  }
   cluster_sync_all();  // neither CTA leaves while the other's MMAs or arrivals reach it
   if (warp == 5) {
     tc_fence_after_sync();
@@ -719,8 +806,13 @@ cudaError_t launch_narrow(const ActMatmulArgs& a, cudaStream_t stream) {
   const long long tn = (a.N + 127) / 128, tm = (a.M + NT - 1) / NT;
   if (tm > 65535) return cudaErrorInvalidConfiguration;
   const int stages = (a.K + F::KS - 1) / F::KS;
-  int splits = 1;
-  while (splits < 8 && tn * tm * (splits + 1) <= 2 * sms && stages >= 2 * (splits + 1)) ++splits;
+  // As many CTAs a tile as the SMs hold at once, two each (clusters of 4 and 8 leave some SMs of a
+  // GPC without: 74 and 36 fit on 152 SMs), with two stages each at least. Powers of two: 48
+  // tiles took 22 us with clusters of 6, two waves of them, and 18 with 4.
+  int splits = 8;
+  while (splits > 1 &&
+         (stages < 2 * splits || tn * tm > 2 * sms / splits - (splits > 2 ? 2 : 0)))
+    splits /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tn), static_cast<unsigned>(tm),
                      static_cast<unsigned>(splits));
@@ -751,7 +843,7 @@ cudaError_t make_scale_map(CUtensorMap* map, const uint8_t* scales, int rows, in
                               CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <int FORM, int NT>
+template <int FORM, int NT, int SPLIT>
 cudaError_t launch_wide(const ActMatmulArgs& a, cudaStream_t stream) {
   using L = Wide<FORM, NT>;
   WideMaps maps = {};
@@ -772,23 +864,40 @@ cudaError_t launch_wide(const ActMatmulArgs& a, cudaStream_t stream) {
                           CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
-  auto kern = act_wide_kernel<FORM, NT>;
+  auto kern = act_wide_kernel<FORM, NT, SPLIT>;
   e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(L::alloc));
   if (e != cudaSuccess) return e;
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  WideOrder order = {(a.M + 255) / 256, (a.N + NT - 1) / NT};
+  const WideOrder order = {(a.M + 255) / 256, (a.N + NT - 1) / NT};
   const long long tiles = static_cast<long long>(order.tm) * order.tn;
   if (tiles > 0x7fffffffLL - 2 * sms) return cudaErrorInvalidConfiguration;
-  const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_with_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kNarrowThreads),
-                         L::alloc, stream, maps, a, order, use_store);
+  const int clusters = static_cast<int>(SPLIT > 1 || tiles < sms / 2 ? tiles : sms / 2);
+  return launch_with_pdl(kern, dim3(static_cast<unsigned>(2 * SPLIT * clusters)),
+                         dim3(kNarrowThreads), L::alloc, stream, maps, a, order, use_store);
 }
 
 template <int FORM>
 cudaError_t launch_form(const ActMatmulArgs& a, int kernel, cudaStream_t stream) {
-  if (kernel == 2 || (kernel == 0 && a.M > 128)) return launch_wide<FORM, 256>(a, stream);
-  if (kernel == 3) return launch_wide<FORM, 128>(a, stream);
+  const int stages = (a.K + Form<FORM>::KS - 1) / Form<FORM>::KS;
+  const int sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long long tiles =
+      ((static_cast<long long>(a.M) + 255) / 256) * ((static_cast<long long>(a.N) + 255) / 256);
+  if (kernel == 0) {
+    // The pairs' tiles of 256 x 256 want 256 rows of x or enough columns: 14336 x 4096 NVFP4 at 64
+    // rows 10.4 us (narrow 12.7), at 48 12.1 (11.6), 4096 x 14336 at 128 17.9 (13.9), at 512 18.7
+    // (23.9).
+    kernel = a.M <= 48 || (a.M <= 256 && tiles * 5 < sms) ? 1 : 2;
+    // With few tiles pairs share them, where each part of k outweighs adding the parts up (4096 x
+    // 14336 MXFP4 at 512 rows 20.4 -> 16.1 us; 16 stages are even). 36 clusters of two pairs and
+    // 15 of four fit on 152 SMs.
+    if (kernel == 2 && stages >= 24)
+      kernel = tiles * 10 <= sms ? 4 : tiles * 4 <= sms - 8 ? 3 : 2;
+  }
+  if (kernel == 4 && stages >= 4) return launch_wide<FORM, 256, 4>(a, stream);
+  if (kernel >= 3 && stages >= 2) return launch_wide<FORM, 256, 2>(a, stream);
+  if (kernel >= 2) return launch_wide<FORM, 256, 1>(a, stream);
   if (a.M <= 16) return launch_narrow<FORM, 16>(a, stream);
   if (a.M <= 32) return launch_narrow<FORM, 32>(a, stream);
   if (a.M <= 64) return launch_narrow<FORM, 64>(a, stream);

@@ -52,8 +52,8 @@ int w4a16_testing_set_fp4_variant(int v);
 int w4a16_testing_set_w8_variant(int v);
 
 /* Kernel of nvfp4_matmul_act / mxfp4_matmul_act: 0 = by size (default), 1 = the one for few rows,
- * 2 and 3 = pairs of CTAs on tiles of 256 x 256 and 256 x 128. Other values only query. Returns
- * the previous value. */
+ * 2 = pairs of CTAs on tiles of 256 x 256, 3 and 4 = two and four pairs a tile (as far as K has
+ * stages for them). Other values only query. Returns the previous value. */
 int w4a16_testing_set_act_kernel(int kernel);
 
 #ifdef __cplusplus

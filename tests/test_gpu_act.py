@@ -278,6 +278,29 @@ def test_product(form, M, N, K):
     assert (y[M] == 7).all(), "the row behind the last is left as it was"
 
 
+@pytest.fixture(params=[1, 2, 3, 4], ids=["narrow", "pairs", "pairs-2", "pairs-4"])
+def forced(request):
+    """Each kernel of the products at sizes that the choice by size may give to another."""
+    prev = w4.testing_set_act_kernel(request.param)
+    yield request.param
+    w4.testing_set_act_kernel(prev)
+
+
+@pytest.mark.parametrize("form,M,N,K", [(f, *s) for f in FORMS for s in
+                                        [(1, 8, 128), (5, 129, 384), (100, 1001, 640),
+                                         (129, 264, 256), (256, 520, 1152), (257, 256, 2048),
+                                         (520, 1288, 512), (1100, 4096, 128), (700, 136, 4096),
+                                         (2100, 6144, 1024)]])
+def test_product_of_each_kernel(forced, form, M, N, K):
+    x = w4.act_quantize(_rows(M, K, M + N).to(DEV), form)
+    w = _weights(form, N, K, N + K)
+    y = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    _matmul(form, x, w, y=y[:M])
+    _ok()
+    _check_product(y[:M], _x_held(form, x, K), w[3], K)
+    assert (y[M] == 7).all()
+
+
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("M", [1, 5, 130, 700])
 def test_product_ignores_what_lies_past_its_rows(form, M):
