@@ -840,6 +840,10 @@ def fp4_prepare_scales(scales: torch.Tensor, tiles=None, stream=None) -> torch.T
 
 def _rows(t: torch.Tensor, name: str, shape=None):
     """(address, elements between rows) of BF16 rows that may lie in a wider array."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda:
+        strides = t.stride()
+        if len(strides) == 2 and strides[1] == 1 and (shape is None or t.shape == shape):
+            return t.data_ptr(), strides[0]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -849,25 +853,33 @@ def _rows(t: torch.Tensor, name: str, shape=None):
     if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be {'[M, K]' if shape is None else list(shape)}, "
                          f"got {list(t.shape)}")
-    if t.stride(1) != 1:
-        raise ValueError(f"{name} must have dense rows")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    raise ValueError(f"{name} must have dense rows")
 
 
-def _act_out(x, format: str, codes, scales, row_scales, stream):
+def _act_out(x, M: int, K: int, format: str, codes, scales, row_scales, stream):
     """(number of the format, codes, scales, row_scales, their addresses)"""
-    if format not in _ACT_FORMATS:
-        raise ValueError(f"format must be one of {sorted(_ACT_FORMATS)}, got {format!r}")
-    number, block, per_byte = _ACT_FORMATS[format]
-    M, K = x.shape
-    codes, cp = _result(codes, "codes", x, (M, K // per_byte), torch.uint8, stream)
-    scales, sp = _result(scales, "scales", x, _tiles_shape(M, (K + block - 1) // block),
-                         torch.uint8, stream)
-    rp = None
-    if number == 0:
-        row_scales, rp = _result(row_scales, "row_scales", x, (M,), torch.float32, stream)
-    elif row_scales is not None:
-        raise ValueError(f"{format} has no row scales")
+    try:
+        number, block, per_byte = _ACT_FORMATS[format]
+    except (KeyError, TypeError):
+        raise ValueError(
+            f"format must be one of {sorted(_ACT_FORMATS)}, got {format!r}") from None
+    shape = (M, K // per_byte)
+    tiles = ((M + 127) // 128, (K + 4 * block - 1) // (4 * block), 512)
+    if codes is None:
+        codes = _new(x, shape, torch.uint8, stream)
+        cp = codes.data_ptr()
+    else:
+        cp = _dev(codes, "codes", torch.uint8, shape)
+    if scales is None:
+        scales = _new(x, tiles, torch.uint8, stream)
+        sp = scales.data_ptr()
+    else:
+        sp = _dev(scales, "scales", torch.uint8, tiles)
+    if number != 0:
+        if row_scales is not None:
+            raise ValueError(f"{format} has no row scales")
+        return number, codes, scales, None, cp, sp, None
+    row_scales, rp = _result(row_scales, "row_scales", x, (M,), torch.float32, stream)
     return number, codes, scales, row_scales, cp, sp, rp
 
 
@@ -877,9 +889,11 @@ def act_quantize(x: torch.Tensor, format: str = "nvfp4", codes=None, scales=None
     "mxfp4" or "mxfp8". Rows of the scale tiles past M are not written."""
     xp, xs = _rows(x, "x")
     M, K = x.shape
-    number, codes, scales, row_scales, cp, sp, rp = _act_out(x, format, codes, scales, row_scales,
-                                                             stream)
-    _check("act_quantize", _lib.act_quantize(xp, xs, M, K, number, cp, sp, rp, _stream(stream)))
+    number, codes, scales, row_scales, cp, sp, rp = _act_out(x, M, K, format, codes, scales,
+                                                             row_scales, stream)
+    status = _lib.act_quantize(xp, xs, M, K, number, cp, sp, rp, _stream(stream))
+    if status:
+        raise W4A16Error("act_quantize", status)
     return codes, scales, row_scales
 
 
@@ -890,20 +904,24 @@ def act_rmsnorm(x: torch.Tensor, weight: torch.Tensor, format: str = "nvfp4", ep
     (codes, scales, row_scales or None, h). h goes to ``residual_out``, which may be ``residual``
     itself; without a residual h is x, and None is returned for it."""
     xp, xs = _rows(x, "x")
-    M, K = x.shape
+    shape = x.shape
+    M, K = shape
     qp, qs, op, os_ = None, 0, None, 0
     if residual is not None:
-        qp, qs = _rows(residual, "residual", x.shape)
+        qp, qs = _rows(residual, "residual", shape)
         if residual_out is None:
-            residual_out = _new(x, (M, K), torch.bfloat16, stream)
-        op, os_ = _rows(residual_out, "residual_out", x.shape)
+            residual_out = _new(x, shape, torch.bfloat16, stream)
+            op, os_ = residual_out.data_ptr(), K
+        else:
+            op, os_ = _rows(residual_out, "residual_out", shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    number, codes, scales, row_scales, cp, sp, rp = _act_out(x, format, codes, scales, row_scales,
-                                                             stream)
-    _check("act_rmsnorm", _lib.act_rmsnorm(
-        xp, xs, qp, qs, op, os_, _dev(weight, "weight", torch.bfloat16, (K,)), eps, M, K, number,
-        cp, sp, rp, _stream(stream)))
+    number, codes, scales, row_scales, cp, sp, rp = _act_out(x, M, K, format, codes, scales,
+                                                             row_scales, stream)
+    status = _lib.act_rmsnorm(xp, xs, qp, qs, op, os_, _dev(weight, "weight", torch.bfloat16, (K,)),
+                              eps, M, K, number, cp, sp, rp, _stream(stream))
+    if status:
+        raise W4A16Error("act_rmsnorm", status)
     return codes, scales, row_scales, residual_out
 
 
@@ -913,16 +931,24 @@ def nvfp4_matmul_act(x_codes: torch.Tensor, x_scales: torch.Tensor, x_row_scales
     """y [M, N] (bf16) = X_hat . W_hat^T of NVFP4 activations (from act_quantize or act_rmsnorm)
     and NVFP4 weights: codes and tensor_scale of nvfp4_quantize, scale_tiles of
     fp4_prepare_scales."""
-    M, N, K = x_codes.shape[0], codes.shape[0], codes.shape[1] * 2
-    blocks = (K + 15) // 16
-    y, yp = _result(y, "y", x_codes, (M, N), torch.bfloat16, stream)
-    _check("nvfp4_matmul_act", _lib.nvfp4_matmul_act(
-        _dev(x_codes, "x_codes", torch.uint8, (M, K // 2)),
-        _dev(x_scales, "x_scales", torch.uint8, _tiles_shape(M, blocks)),
+    M, half = x_codes.shape
+    N = codes.shape[0]
+    words = (half + 31) // 32
+    if y is None:
+        y = _new(x_codes, (M, N), torch.bfloat16, stream)
+        yp = y.data_ptr()
+    else:
+        yp = _dev(y, "y", torch.bfloat16, (M, N))
+    status = _lib.nvfp4_matmul_act(
+        _dev(x_codes, "x_codes", torch.uint8),
+        _dev(x_scales, "x_scales", torch.uint8, ((M + 127) // 128, words, 512)),
         _dev(x_row_scales, "x_row_scales", torch.float32, (M,)),
-        _dev(codes, "codes", torch.uint8),
-        _dev(scale_tiles, "scale_tiles", torch.uint8, _tiles_shape(N, blocks)),
-        _dev(tensor_scale, "tensor_scale", torch.float32, (1,)), yp, M, N, K, _stream(stream)))
+        _dev(codes, "codes", torch.uint8, (N, half)),
+        _dev(scale_tiles, "scale_tiles", torch.uint8, ((N + 127) // 128, words, 512)),
+        _dev(tensor_scale, "tensor_scale", torch.float32, (1,)), yp, M, N, 2 * half,
+        _stream(stream))
+    if status:
+        raise W4A16Error("nvfp4_matmul_act", status)
     return y
 
 
@@ -930,16 +956,23 @@ def mxfp4_matmul_act(x_codes: torch.Tensor, x_scales: torch.Tensor, codes: torch
                      scale_tiles: torch.Tensor, y=None, stream=None) -> torch.Tensor:
     """y [M, N] (bf16) = X_hat . W_hat^T of MXFP4 (x_codes [M, K/2]) or MXFP8 (x_codes [M, K])
     activations and MXFP4 weights: codes of mxfp4_quantize, scale_tiles of fp4_prepare_scales."""
-    M, N, K = x_codes.shape[0], codes.shape[0], codes.shape[1] * 2
-    blocks = (K + 31) // 32
-    if x_codes.dim() != 2 or x_codes.shape[1] not in (K // 2, K):
-        raise ValueError(f"x_codes must be [M, {K // 2}] (MXFP4) or [M, {K}] (MXFP8), "
+    M, width = x_codes.shape
+    N, half = codes.shape
+    if width != half and width != 2 * half:
+        raise ValueError(f"x_codes must be [M, {half}] (MXFP4) or [M, {2 * half}] (MXFP8), "
                          f"got {list(x_codes.shape)}")
-    y, yp = _result(y, "y", x_codes, (M, N), torch.bfloat16, stream)
-    _check("mxfp4_matmul_act", _lib.mxfp4_matmul_act(
+    words = (half + 63) // 64
+    if y is None:
+        y = _new(x_codes, (M, N), torch.bfloat16, stream)
+        yp = y.data_ptr()
+    else:
+        yp = _dev(y, "y", torch.bfloat16, (M, N))
+    status = _lib.mxfp4_matmul_act(
         _dev(x_codes, "x_codes", torch.uint8),
-        _dev(x_scales, "x_scales", torch.uint8, _tiles_shape(M, blocks)),
-        2 if x_codes.shape[1] == K else 1, _dev(codes, "codes", torch.uint8),
-        _dev(scale_tiles, "scale_tiles", torch.uint8, _tiles_shape(N, blocks)), yp, M, N, K,
-        _stream(stream)))
+        _dev(x_scales, "x_scales", torch.uint8, ((M + 127) // 128, words, 512)),
+        1 if width == half else 2, _dev(codes, "codes", torch.uint8),
+        _dev(scale_tiles, "scale_tiles", torch.uint8, ((N + 127) // 128, words, 512)), yp, M, N,
+        2 * half, _stream(stream))
+    if status:
+        raise W4A16Error("mxfp4_matmul_act", status)
     return y

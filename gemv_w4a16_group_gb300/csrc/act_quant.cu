@@ -17,8 +17,8 @@
 // (MXFP8, 0.82 of the copy rate) and 18.6 (NVFP4, 0.87), 4096 x 14336 alone 28.6 us (MXFP8, 0.92);
 // a CTA's chain of loads, joins and root for few: one row of 4096 1.3 us alone, 2.2 with norm.
 // A CTA holds its row in registers between the row's sums and the codes, and loads everything the
-// row needs (weights and residual too) at once, before it waits for any of it (26 us of the 21.1
-// with the weights loaded where they are used). Resident CTAs that take rows in turn, the next
+// row needs (weights and residual too) at once, before it waits for any of it (26 us with the
+// weights loaded where they are used). Resident CTAs that take rows in turn, the next
 // rows' bulk copies under way, were no faster (24.5): the SMs hold enough CTAs to overlap them.
 // A thread takes pieces of 8 consecutive values (one 16-byte load), so that a block of
 // 16 or 32 is 2 or 4 neighbouring lanes, four blocks' scales make one 32-bit word of a tile, and
@@ -135,8 +135,7 @@ __device__ __forceinline__ uint32_t top_of(const float2 (&v)[4]) {
 // ---- sums and the root in two floats -------------------------------------------------------
 // hi + lo, lo below hi's last place. A code is the exact y's where y is near a border between two
 // codes only if 1 / rms is known well past fp32: with plain fp32 sums about one code in four
-// million was its neighbour. (What an addition loses is kept, exactly but where a square passes
-// the thread's sum so far.)
+// million was its neighbour.
 struct Two {
   float hi, lo;
 };
@@ -154,10 +153,12 @@ __device__ __forceinline__ Two warp_sum(Two a) {
     a = add(a, {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
   return a;
 }
-// (s, c) of two sums += v^2, what the sums lose going to c
+// (s, c) of two sums += v^2 (exact, of BF16 numbers), what the sums lose going to c
 __device__ __forceinline__ void add_squares(float2& s, float2& c, float2 v) {
-  const float2 n = fma2(v, v, s);
-  c = add2(c, fma2(v, v, fma2(n, make_float2(-1.f, -1.f), s)));
+  const float2 minus = make_float2(-1.f, -1.f);
+  const float2 q = mul2(v, v), n = add2(s, q);
+  const float2 t = fma2(s, minus, n);  // of n what came of q; the rest came of s
+  c = add2(c, add2(fma2(t, minus, q), fma2(fma2(t, minus, n), minus, s)));
   s = n;
 }
 // 1 / sqrt(sum / K + eps) = sqrt(K / T), T = sum + K eps: a first guess r and one step of Newton
