@@ -234,22 +234,27 @@ struct Narrow {
   static constexpr uint32_t w_tx = FORM == kActMxfp8 ? 128 * 64 : 128 * 128;
   static constexpr uint32_t w_bytes = 128 * 128, x_bytes = NT * 128, s_bytes = kTiles * 512;
   static constexpr uint32_t stage_bytes = w_bytes + x_bytes + 2 * s_bytes;
+  // Parts of a shared tile: up to 32 rows a CTA sends its sums to the CTA that adds them up, into
+  // a place of their own, once its MMAs are done; more rows would cost stages, and are read from
+  // where the sender's stages were.
+  static constexpr bool kSend = NT <= 32;
+  static constexpr uint32_t part_bytes = kSend ? NT * 128 * 4 : 0;
   // two CTAs an SM
-  static constexpr int kStages = (110 * 1024) / stage_bytes;
+  static constexpr int kStages = (112 * 1024 - part_bytes) / stage_bytes;
   static constexpr uint32_t x_off = kStages * w_bytes;
   static constexpr uint32_t sw_off = x_off + kStages * x_bytes;
   static constexpr uint32_t sx_off = sw_off + kStages * s_bytes;
-  static constexpr uint32_t bar_off = sx_off + kStages * s_bytes;  // full, empty, done
+  static constexpr uint32_t part_off = sx_off + kStages * s_bytes;
+  static constexpr uint32_t bar_off = part_off + part_bytes;  // full, empty, done
   static constexpr uint32_t misc_off = bar_off + (2 * kStages + 1) * 8;
-  static constexpr uint32_t total = misc_off + 16;
-  static constexpr uint32_t alloc = total + 1024;
+  static constexpr uint32_t alloc = misc_off + 16;
   // tensor memory: the accumulator, two sets of scale columns
   static constexpr uint32_t s_cols = 4 * kTiles;
   static constexpr uint32_t acc_cols = NT < 32 ? 32 : NT;
   static constexpr uint32_t need_cols = acc_cols + 4 * s_cols;
   static constexpr uint32_t tmem_cols = need_cols <= 64 ? 64 : need_cols <= 128 ? 128 : 256;
   static_assert(need_cols <= 256, "two CTAs share the tensor memory");
-  static_assert(NT * 128 * 4 <= kStages * (w_bytes + x_bytes), "the partial tile reuses the ring");
+  static_assert(kSend || NT * 128 * 4 <= kStages * (w_bytes + x_bytes), "parts reuse the ring");
   static_assert(alloc <= 113 * 1024, "two CTAs share the shared memory");
 };
 constexpr int kNarrowThreads = 192;  // four warps for the tile, one for copies, one for the MMAs
@@ -260,9 +265,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   using L = Narrow<FORM, NT>;
   using F = Form<FORM>;
   constexpr int S = L::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
   uint64_t* empty = full + S;
   uint64_t* done = empty + S;
@@ -296,7 +299,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   tc_fence_after_sync();
   const uint32_t tmem = *holder;
   if (threadIdx.x == 0) pdl_launch_dependents();
+  __syncwarp();
+  // (waited for before the parts are sent: every CTA of the cluster has begun)
+  if (L::kSend && splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
+  const int rows = min(NT, a.M - m0);
+  // a CTA of a cluster adds up 2^shift columns of the tile
+  const int shift = 8 - __ffs(splits);
+  const float wscale = FORM == kActNvfp4 ? __ldg(a.w_scale) : 1.f;
+  // the row's scale of the first sums that this thread rounds
+  const int j0 = static_cast<int>(threadIdx.x) >> (shift - 1);
+  const float f0 = FORM == kActNvfp4 && j0 < rows ? __ldg(a.x_rows + m0 + j0) : 1.f;
 
   int issued = 0;  // stages whose copies this thread has issued
   if (warp == 4) {
@@ -362,22 +375,31 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   ok = ok && *abort_flag == 0u;
   tc_fence_after_sync();
 
-  const float wscale = FORM == kActNvfp4 ? __ldg(a.w_scale) : 1.f;
-  const int rows = min(NT, a.M - m0);
+  if (L::kSend && splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (warp < 4) {
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float* parts = reinterpret_cast<float*>(smem);  // [NT][128]
-    const int n = n0 + warp * 32 + lane;
+    const int col = warp * 32 + lane, n = n0 + col;
+    // the CTA that adds up this column's sums, and where it has this one's: [splits][NT][width]
+    const uint32_t to = peer_addr(smem_addr(smem + L::part_off), col >> shift) +
+                        4 * (((part * NT) << shift) + (col & ((1 << shift) - 1)));
 #pragma unroll 1
     for (int c = 0; c < NT && c < rows; c += 16) {
       uint32_t v[16];
       __syncwarp();
       tmem_ld_16cols(lane_base + c, v);
       tmem_ld_wait();
-      if (splits > 1) {
+      if (L::kSend && splits > 1) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          parts[(c + j) * 128 + warp * 32 + lane] = count > 0 ? __uint_as_float(v[j]) : 0.f;
+          if (c + j < rows)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + ((c + j) << (shift + 2))),
+                         "r"(count > 0 ? v[j] : 0u)
+                         : "memory");
+      } else if (splits > 1) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          parts[(c + j) * 128 + col] = count > 0 ? __uint_as_float(v[j]) : 0.f;
       } else if (ok && n < a.N) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -393,28 +415,57 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   if (splits > 1) {
     __syncwarp();
     cluster_sync_all();
-    // pairs of columns; the cluster's CTAs take the pairs in turn
-    const uint32_t base = smem_addr(smem);
-    for (int p = part * kNarrowThreads + threadIdx.x; p < rows * 64;
-         p += splits * kNarrowThreads) {
-      const int j = p >> 6, c = (p & 63) * 2;
-      float2 sum = make_float2(0.f, 0.f);
-      for (int r = 0; r < splits; ++r) {
-        const float2 v = peer_lds64(peer_addr(base + (j * 128 + c) * 4, r));
-        sum.x += v.x;
-        sum.y += v.y;
+    if constexpr (L::kSend) {
+      const float2* parts = reinterpret_cast<const float2*>(smem + L::part_off);
+      const int half = shift - 1;  // pairs of columns
+      float f = f0;
+      for (int p = threadIdx.x; p < rows << half; p += kNarrowThreads) {
+        const int j = p >> half, c = p & ((1 << half) - 1), n = n0 + (part << shift) + 2 * c;
+        if (FORM == kActNvfp4 && p >= kNarrowThreads) f = __ldg(a.x_rows + m0 + j);
+        float2 sum = make_float2(0.f, 0.f);
+        for (int r = 0; r < splits; ++r) {
+          const float2 v = parts[((r * NT + j) << half) + c];
+          sum.x += v.x;
+          sum.y += v.y;
+        }
+        if constexpr (FORM == kActNvfp4) {
+          sum.x *= f * wscale;
+          sum.y *= f * wscale;
+        }
+        uint16_t* out = a.y + static_cast<size_t>(m0 + j) * a.N + n;
+        if (!ok || n >= a.N) continue;
+        if (a.N % 2 == 0) {
+          const __nv_bfloat162 w = __floats2bfloat162_rn(sum.x, sum.y);
+          *reinterpret_cast<__nv_bfloat162*>(out) = w;
+        } else {
+          out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(sum.x));
+          if (n + 1 < a.N) out[1] = __bfloat16_as_ushort(__float2bfloat16_rn(sum.y));
+        }
       }
-      if constexpr (FORM == kActNvfp4) {
-        const float f = __ldg(a.x_rows + m0 + j) * wscale;
-        sum.x *= f;
-        sum.y *= f;
+    } else {
+      // pairs of columns; the cluster's CTAs take the pairs in turn
+      const uint32_t base = smem_addr(smem);
+      for (int p = part * kNarrowThreads + threadIdx.x; p < rows * 64;
+           p += splits * kNarrowThreads) {
+        const int j = p >> 6, c = (p & 63) * 2;
+        float2 sum = make_float2(0.f, 0.f);
+        for (int r = 0; r < splits; ++r) {
+          const float2 v = peer_lds64(peer_addr(base + (j * 128 + c) * 4, r));
+          sum.x += v.x;
+          sum.y += v.y;
+        }
+        if constexpr (FORM == kActNvfp4) {
+          const float f = __ldg(a.x_rows + m0 + j) * wscale;
+          sum.x *= f;
+          sum.y *= f;
+        }
+        uint16_t* out = a.y + static_cast<size_t>(m0 + j) * a.N + n0 + c;
+        if (ok && n0 + c < a.N) out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(sum.x));
+        if (ok && n0 + c + 1 < a.N) out[1] = __bfloat16_as_ushort(__float2bfloat16_rn(sum.y));
       }
-      uint16_t* out = a.y + static_cast<size_t>(m0 + j) * a.N + n0 + c;
-      if (ok && n0 + c < a.N) out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(sum.x));
-      if (ok && n0 + c + 1 < a.N) out[1] = __bfloat16_as_ushort(__float2bfloat16_rn(sum.y));
+      __syncwarp();
+      cluster_sync_all();  // no CTA leaves while another reads its part
     }
-    __syncwarp();
-    cluster_sync_all();  // no CTA leaves while another reads its part
   }
   tc_fence_before_sync();
   __syncthreads();
