@@ -167,12 +167,6 @@ __device__ __forceinline__ float4 peer_lds128(uint32_t addr) {
                : "r"(addr));
   return v;
 }
-__device__ __forceinline__ float2 peer_lds64(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
-  return v;
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -217,6 +211,23 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                    "l"(reinterpret_cast<uint64_t>(map)),
                "r"(smem_addr(smem_src)), "r"(x), "r"(y)
                : "memory");
+}
+
+// bf16(v f) to four columns of y, `left` of them inside it.
+__device__ __forceinline__ void store_four(uint16_t* out, int left, int N, float4 v, float f) {
+  if (left <= 0) return;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+  const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                             *reinterpret_cast<const uint32_t*>(&hi));
+  if (N % 4 == 0) {
+    *reinterpret_cast<uint2*>(out) = w;
+  } else {
+    out[0] = static_cast<uint16_t>(w.x);
+    if (left > 1) out[1] = static_cast<uint16_t>(w.x >> 16);
+    if (left > 2) out[2] = static_cast<uint16_t>(w.y);
+    if (left > 3) out[3] = static_cast<uint16_t>(w.y >> 16);
+  }
 }
 
 struct NarrowMaps {
@@ -443,25 +454,27 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         }
       }
     } else {
-      // pairs of columns; the cluster's CTAs take the pairs in turn
+      // four columns at a time; the cluster's CTAs take them in turn, with the loads of all parts
+      // on their way together
       const uint32_t base = smem_addr(smem);
-      for (int p = part * kNarrowThreads + threadIdx.x; p < rows * 64;
+      for (int p = part * kNarrowThreads + threadIdx.x; p < rows * 32;
            p += splits * kNarrowThreads) {
-        const int j = p >> 6, c = (p & 63) * 2;
-        float2 sum = make_float2(0.f, 0.f);
-        for (int r = 0; r < splits; ++r) {
-          const float2 v = peer_lds64(peer_addr(base + (j * 128 + c) * 4, r));
-          sum.x += v.x;
-          sum.y += v.y;
-        }
-        if constexpr (FORM == kActNvfp4) {
-          const float f = __ldg(a.x_rows + m0 + j) * wscale;
-          sum.x *= f;
-          sum.y *= f;
-        }
-        uint16_t* out = a.y + static_cast<size_t>(m0 + j) * a.N + n0 + c;
-        if (ok && n0 + c < a.N) out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(sum.x));
-        if (ok && n0 + c + 1 < a.N) out[1] = __bfloat16_as_ushort(__float2bfloat16_rn(sum.y));
+        const int j = p >> 5, c = (p & 31) * 4, n = n0 + c;
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < splits) v[r] = peer_lds128(peer_addr(base + (j * 128 + c) * 4, r));
+        float4 sum = v[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < splits) {
+            sum.x += v[r].x;
+            sum.y += v[r].y;
+            sum.z += v[r].z;
+            sum.w += v[r].w;
+          }
+        const float f = FORM == kActNvfp4 ? __ldg(a.x_rows + m0 + j) * wscale : 1.f;
+        if (ok) store_four(a.y + static_cast<size_t>(m0 + j) * a.N + n, a.N - n, a.N, sum, f);
       }
       __syncwarp();
       cluster_sync_all();  // no CTA leaves while another reads its part
@@ -799,19 +812,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
         }
         float f = wscale;
         if constexpr (FORM == kActNvfp4) f *= __ldg(a.x_rows + row);
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x * f, sum.y * f);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z * f, sum.w * f);
-        uint16_t* out = a.y + static_cast<size_t>(row) * a.N + n;
-        const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                   *reinterpret_cast<const uint32_t*>(&hi));
-        if (a.N % 4 == 0) {
-          *reinterpret_cast<uint2*>(out) = w;
-        } else {
-          out[0] = static_cast<uint16_t>(w.x);
-          if (n + 1 < a.N) out[1] = static_cast<uint16_t>(w.x >> 16);
-          if (n + 2 < a.N) out[2] = static_cast<uint16_t>(w.y);
-          if (n + 3 < a.N) out[3] = static_cast<uint16_t>(w.y >> 16);
-        }
+        store_four(a.y + static_cast<size_t>(row) * a.N + n, a.N - n, a.N, sum, f);
       }
     }
     __syncwarp();
@@ -937,9 +938,10 @@ cudaError_t launch_form(const ActMatmulArgs& a, int kernel, cudaStream_t stream)
       ((static_cast<long long>(a.M) + 255) / 256) * ((static_cast<long long>(a.N) + 255) / 256);
   if (kernel == 0) {
     // The pairs' tiles of 256 x 256 want 256 rows of x or enough columns: 14336 x 4096 NVFP4 at 64
-    // rows 10.4 us (narrow 12.7), at 48 12.1 (11.6), 4096 x 14336 at 128 17.9 (13.9), at 512 18.7
-    // (23.9).
-    kernel = a.M <= 48 || (a.M <= 256 && tiles * 5 < sms) ? 1 : 2;
+    // rows 10.4 us (narrow 10.9), at 48 12.1 (10.1), MXFP8 at 96 14.1 (14.7), at 64 13.8 (12.1);
+    // 4096 x 14336 NVFP4 at 256 17.9 (15.1), at 512 18.7 (23.9).
+    const int few = FORM == kActMxfp8 ? 80 : 48;
+    kernel = a.M <= few || (a.M <= 256 && tiles * 5 < sms) ? 1 : 2;
     // With few tiles pairs share them, where each part of k outweighs adding the parts up (4096 x
     // 14336 MXFP4 at 512 rows 20.4 -> 16.1 us; 16 stages are even). 36 clusters of two pairs and
     // 15 of four fit on 152 SMs.
