@@ -277,6 +277,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   using F = Form<FORM>;
   constexpr int S = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_addr(smem) & 1023u) != 0) {  // the same in every CTA
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusLayout);
+    return;
+  }
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
   uint64_t* empty = full + S;
   uint64_t* done = empty + S;
@@ -558,6 +562,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
   using F = Form<FORM>;
   constexpr int S = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];  // (no room to align it by hand)
+  if ((smem_addr(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusLayout);
+    return;
+  }
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
