@@ -12,6 +12,11 @@
 namespace w4k {
 namespace {
 
+// Launches. The kernels may begin while the one before them runs, up to their wait for it, but
+// never let a kernel begin that waits for them: with launch_dependents in these (cluster) kernels
+// a chain of norms and products in a graph came to stand still, the next norm's CTAs on the SMs
+// that the rest of the product's clusters wanted.
+
 // A stage is a 128-byte swizzle row of k per row: 256 E2M1 or 128 E4M3 values. TILES scale tiles
 // (128 rows x 4 scales, 512 bytes) cover it; an MMA takes KM values, STEPS of them a stage.
 template <int FORM>
@@ -313,7 +318,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *holder;
-  if (threadIdx.x == 0) pdl_launch_dependents();
   __syncwarp();
   // (waited for before the parts are sent: every CTA of the cluster has begun)
   if (L::kSend && splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -613,7 +617,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
   cluster_sync_all();  // both CTAs' barriers stand
   tc_fence_after_sync();
   const uint32_t tmem = *holder;
-  if (threadIdx.x == 0) pdl_launch_dependents();
   pdl_wait();
 
   if (warp == 4) {

@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(V > 2 ? 512 : 1024)
   const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, warps = T >> 5;
   const int m = blockIdx.x, pieces = a.K >> 3;
 
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // after the wait: no more than one kernel waits for another
   const uint4* src = reinterpret_cast<const uint4*>(a.x + m * a.x_stride);
   const uint4* res = reinterpret_cast<const uint4*>(a.residual + m * a.residual_stride);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);

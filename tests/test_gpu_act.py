@@ -423,6 +423,38 @@ def test_streams_and_graphs(form):
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 1024), (64, 14336, 1024), (128, 14336, 1024),
+                                   (128, 1024, 7168), (300, 4096, 1024)])
+def test_long_chains_in_graphs(form, M, N, K):
+    """Norm and product twenty times in one graph, on two sets of buffers in turn, replayed a
+    hundred times without a pause: kernels that begin before the last one has ended must leave
+    it, and one another, the SMs that they need."""
+    weight = torch.ones(K, device=DEV).bfloat16()
+    w = _weights(form, N, K, 6)
+    states = []
+    for seed in (60, 70):
+        x, res = _rows(M, K, seed).to(DEV), _rows(M, K, seed + 1).to(DEV)
+        states.append((x, res, torch.empty_like(res), w4.act_quantize(x, form)))
+
+    def step(x, res, out, q):
+        c, s, r, _ = w4.act_rmsnorm(x, weight, form, residual=res, residual_out=out, codes=q[0],
+                                    scales=q[1], row_scales=q[2])
+        return _matmul(form, (c, s, r), w)
+
+    want = [step(*st).clone() for st in states]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [step(*states[i % 2]) for i in range(20)]
+    for _ in range(100):
+        graph.replay()
+    torch.cuda.synchronize()
+    _ok()
+    for i, y in enumerate(outs):
+        assert torch.equal(y, want[i % 2])
+
+
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("M", [1, 6, 150])
 def test_a_layer_as_it_is_used(form, M):
     """Residual and norm, the up and gate projections, their product quantized, the down
