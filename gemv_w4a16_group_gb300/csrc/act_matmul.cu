@@ -12,10 +12,10 @@
 namespace w4k {
 namespace {
 
-// Launches. The kernels may begin while the one before them runs, up to their wait for it, but
-// never let a kernel begin that waits for them: with launch_dependents in these (cluster) kernels
-// a chain of norms and products in a graph came to stand still, the next norm's CTAs on the SMs
-// that the rest of the product's clusters wanted.
+// Launches. The kernels may begin while the one before them runs, up to their wait for it, but do
+// not let the next one begin before they end: with launch_dependents in them, graphs of norms and
+// products, several grids in flight and each waiting for the one before, came to a standstill (the
+// clusters that were still to be placed and the next norm's CTAs want the same SMs).
 
 // A stage is a 128-byte swizzle row of k per row: 256 E2M1 or 128 E4M3 values. TILES scale tiles
 // (128 rows x 4 scales, 512 bytes) cover it; an MMA takes KM values, STEPS of them a stage.

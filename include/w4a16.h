@@ -401,7 +401,8 @@ w4a16_status mxfp4_matmul(const uint16_t* x, const uint8_t* codes, const uint8_t
  * Scale tiles. Scales [R, C] (rows by blocks along K) lie in uint8 [ceil(R/128), ceil(C/4), 512]:
  * (r, c) at byte (r % 32) 16 + (r / 32 % 4) 4 + c % 4 of tile (r / 128, c / 4), as tensor memory
  * takes them. fp4_scale_tiles_bytes(R, C) bytes. The quantizers write whole 4-byte words of the
- * rows they are given (0 past column C) and nothing else; words of rows past R may hold anything.
+ * rows they are given (0 past column C) and nothing else; words of rows past R may hold anything,
+ * bytes past column C of a row anything but NaN.
  *
  * fp4_prepare_scales -- scales uint8 [rows, cols] of nvfp4_quantize or mxfp4_quantize (cols = K/16
  *   or K/32) into tiles, once per weight; places past rows and cols become 0. scales need no
@@ -431,9 +432,10 @@ w4a16_status fp4_prepare_scales(const uint8_t* scales, int rows, int cols, uint8
  *   residual, residual_out  bf16 [M, K] with strides as x's; h is written to residual_out, which
  *     may be residual itself or x. Both NULL: h = x.
  *   weight  bf16 [K]; eps >= 1e-30
- *   fp32 sums; h * weight is exact, so y is rounded to fp32 once before it is to its code. NVFP4's
- *   codes and block scales are those of h * weight, and 1 / sqrt(...) goes into r. A row whose
- *   squares pass fp32's range becomes NaN.
+ *   MXFP4 and MXFP8 codes are those of the exact y (sums of squares and 1 / sqrt(...) are carried
+ *   in two fp32 numbers; about one code in 10^8, at a border, is its neighbour). NVFP4's codes and
+ *   block scales are those of h * weight, and 1 / sqrt(...) goes into r. A row whose squares pass
+ *   fp32's range becomes NaN.
  */
 w4a16_status act_quantize(const uint16_t* x, int64_t x_stride, int M, int K, int format,
                           uint8_t* codes, uint8_t* scales, float* row_scales,
