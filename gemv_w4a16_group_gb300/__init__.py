@@ -152,18 +152,23 @@ def _load():
 
 _lib = _load()
 
+# names that every call looks up, bound once
+_Tensor = torch.Tensor
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # none in a build without CUDA
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
 
 def _stream(stream) -> int:
     if stream is None:
         # torch.cuda.current_stream() builds a Stream object: 3 us of a call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> int:
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
+    if (isinstance(t, _Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
             and t.is_cuda and t.is_contiguous()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
@@ -708,10 +713,10 @@ def _torch_stream(stream):
 def _new(like: torch.Tensor, shape, dtype, stream, zero: bool = False) -> torch.Tensor:
     """A result or scratch for a call on `stream`, allocated (and zero-filled) on it: the caching
     allocator reuses a freed block in the order of the stream it was allocated on."""
-    stream = _torch_stream(stream)
     if stream is None:
         t = torch.empty(shape, dtype=dtype, device=like.device)  # half of new_empty's time
         return t.zero_() if zero else t
+    stream = _torch_stream(stream)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=like.device)
         return t.zero_() if zero else t
@@ -840,7 +845,7 @@ def fp4_prepare_scales(scales: torch.Tensor, tiles=None, stream=None) -> torch.T
 
 def _rows(t: torch.Tensor, name: str, shape=None):
     """(address, elements between rows) of BF16 rows that may lie in a wider array."""
-    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda:
+    if isinstance(t, _Tensor) and t.dtype is torch.bfloat16 and t.is_cuda:
         strides = t.stride()
         if len(strides) == 2 and strides[1] == 1 and (shape is None or t.shape == shape):
             return t.data_ptr(), strides[0]

@@ -46,10 +46,14 @@ struct MapKeyEq {
   }
 };
 struct MapKeyHash {
-  size_t operator()(const MapKey& k) const {  // FNV-1a over the key's bytes
-    const unsigned char* p = reinterpret_cast<const unsigned char*>(&k);
-    uint64_t h = 1469598103934665603ull;
-    for (size_t i = 0; i < sizeof(MapKey); ++i) h = (h ^ p[i]) * 1099511628211ull;
+  size_t operator()(const MapKey& k) const {  // FNV-1a over the key's 64-bit words
+    static_assert(sizeof(MapKey) % 8 == 0, "the key is whole words");
+    uint64_t words[sizeof(MapKey) / 8], h = 1469598103934665603ull;
+    std::memcpy(words, &k, sizeof(words));
+    for (const uint64_t w : words) {
+      h = (h ^ w) * 1099511628211ull;
+      h ^= h >> 32;  // the high bits reach the low ones, which choose the bucket
+    }
     return static_cast<size_t>(h);
   }
 };
