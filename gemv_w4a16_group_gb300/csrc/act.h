@@ -11,7 +11,7 @@ namespace w4k {
 // Formats of quantized activations (the public header's W4A16_ACT_* values).
 constexpr int kActNvfp4 = 0, kActMxfp4 = 1, kActMxfp8 = 2;
 
-// Longest row the quantizers hold in a CTA's registers (1024 threads of 8 pieces of 8).
+// Longest row the quantizers hold in a CTA's registers (512 threads of 8 pieces of 16).
 constexpr int kActMaxK = 65536;
 
 struct ActQuantArgs {

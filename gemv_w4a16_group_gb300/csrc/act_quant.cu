@@ -13,17 +13,17 @@
 //     and denominator under powers of two: exact for BF16 rows but for the division, and in range.
 //
 // What bounds it: a row is read once (2 bytes a value, 4 with a residual) and 0.53 to 1.03 bytes
-// (and 2 of the residual) written, so HBM for many rows: 4096 x 4096 with residual and norm 21.1 us
-// (MXFP8, 0.82 of the copy rate) and 18.6 (NVFP4, 0.87), 4096 x 14336 alone 28.6 us (MXFP8, 0.92);
-// a CTA's chain of loads, joins and root for few: one row of 4096 1.3 us alone, 2.2 with norm.
-// A CTA holds its row in registers between the row's sums and the codes, and loads everything the
-// row needs (weights and residual too) at once, before it waits for any of it (26 us with the
-// weights loaded where they are used). Resident CTAs that take rows in turn, the next
-// rows' bulk copies under way, were no faster (24.5): the SMs hold enough CTAs to overlap them.
-// A thread takes pieces of 8 consecutive values (one 16-byte load), so that a block of
-// 16 or 32 is 2 or 4 neighbouring lanes, four blocks' scales make one 32-bit word of a tile, and
-// a warp's codes are contiguous. The arithmetic is on pairs (fp32x2, bf16x2): unpaired it was as
-// long as the copies.
+// (and 2 of the residual) written, so HBM for many rows: 4096 x 14336 26.5 us (MXFP8, 0.99 of the
+// copy rate) and 26.4 (NVFP4, 0.84), 4096 x 4096 with residual and norm 20.8 (MXFP8, 0.84) and 18.2
+// (NVFP4, 0.89); a CTA's chain of loads, joins and root for few: one row of 4096 1.3 us alone, 2.2
+// with norm. A CTA holds its row in registers between the row's sums and the codes, and loads
+// everything the row needs (weights and residual too) at once, before it waits for any of it (26
+// us for 4096 x 4096 with the weights loaded where they are used). Resident CTAs that take rows in
+// turn, the next rows' bulk copies under way, were no faster: the SMs hold enough CTAs to overlap
+// them. A thread takes pieces of 16 consecutive values, so that a block is one lane or two
+// neighbouring ones and its scale is found once or twice (pieces of 8: 28.4 and 36 us for 4096 x
+// 14336), four blocks' scales make one 32-bit word of a tile, and a warp's codes are contiguous.
+// The arithmetic is on pairs (fp32x2, bf16x2): unpaired it was as long as the copies.
 #include "act.h"
 #include "common.cuh"
 
@@ -32,10 +32,25 @@ namespace {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Largest |value| of 8 BF16 values as a float's bits (NaN above infinity above finite).
-__device__ __forceinline__ uint32_t top_bf16x8(uint4 v) {
+// 16 consecutive BF16 values.
+struct Piece {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ Piece no_piece() {
+  return {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+}
+// Piece p of a row.
+__device__ __forceinline__ Piece load_piece(const uint16_t* row, int p) {
+  const uint4* at = reinterpret_cast<const uint4*>(row) + 2 * p;
+  return {at[0], at[1]};
+}
+
+// Largest |value| of a piece as a float's bits (NaN above infinity above finite).
+__device__ __forceinline__ uint32_t top_of(const Piece& v) {
   const uint32_t m = 0x7FFF7FFFu;
-  const uint32_t t = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  const uint32_t a = __vmaxu2(__vmaxu2(v.lo.x & m, v.lo.y & m), __vmaxu2(v.lo.z & m, v.lo.w & m));
+  const uint32_t b = __vmaxu2(__vmaxu2(v.hi.x & m, v.hi.y & m), __vmaxu2(v.hi.z & m, v.hi.w & m));
+  const uint32_t t = __vmaxu2(a, b);
   return max(t << 16, t & 0xFFFF0000u);
 }
 
@@ -53,7 +68,7 @@ __device__ __forceinline__ uint32_t e4m3_not_below(float v, float& value) {
 }
 
 // E2M1 codes of 8 values, the first in the lowest bits (nearest, ties to even, saturating at 6).
-__device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
+__device__ __forceinline__ uint32_t e2m1x8(const float2* v) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -71,10 +86,10 @@ __device__ __forceinline__ uint32_t e4m3_pair(float2 v) {
   return r;
 }
 
-__device__ __forceinline__ void bf16x8(uint4 in, float2 (&v)[4]) {
-  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+__device__ __forceinline__ void unpack(const Piece& in, float2 (&v)[8]) {
+  const uint32_t w[8] = {in.lo.x, in.lo.y, in.lo.z, in.lo.w, in.hi.x, in.hi.y, in.hi.z, in.hi.w};
 #pragma unroll
-  for (int h = 0; h < 4; ++h)
+  for (int h = 0; h < 8; ++h)
     v[h] = make_float2(__uint_as_float(w[h] << 16), __uint_as_float(w[h] & 0xFFFF0000u));
 }
 
@@ -127,9 +142,11 @@ __device__ __forceinline__ float top3(float a, float b, float c) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t top_of(const float2 (&v)[4]) {
-  const float t = top3(v[0].x, v[0].y, v[1].x);
-  return abs_bits(top3(top3(t, v[1].y, v[2].x), v[2].y, top3(v[3].x, v[3].y, 0.f)));
+__device__ __forceinline__ uint32_t top_of(const float2 (&v)[8]) {
+  float t = top3(v[0].x, v[0].y, 0.f);
+#pragma unroll
+  for (int h = 1; h < 8; ++h) t = top3(t, v[h].x, v[h].y);
+  return abs_bits(t);
 }
 
 // ---- sums and the root in two floats -------------------------------------------------------
@@ -185,10 +202,10 @@ __device__ __forceinline__ float off_border(float y, float z, Two f) {
 __device__ __forceinline__ bool few_bits(float y) { return (__float_as_uint(y) & 0x7FFFFu) == 0u; }
 
 // Whether one of the values falls on one of few bits.
-__device__ __forceinline__ bool any_few_bits(const float2 (&y)[4]) {
+__device__ __forceinline__ bool any_few_bits(const float2 (&y)[8]) {
   uint32_t t = 0xFFFFFFFFu;
 #pragma unroll
-  for (int h = 0; h < 4; ++h)
+  for (int h = 0; h < 8; ++h)
     t = min(t, min(__float_as_uint(y[h].x) << 13, __float_as_uint(y[h].y) << 13));
   return t == 0u;
 }
@@ -204,19 +221,22 @@ __device__ __forceinline__ uint4 add_rows(uint4 a, uint4 b) {
   return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z),
                     add_bf16x2(a.w, b.w));
 }
+__device__ __forceinline__ Piece add_rows(const Piece& a, const Piece& b) {
+  return {add_rows(a.lo, b.lo), add_rows(a.hi, b.hi)};
+}
 
 // A thread's part of the row's sum of squares (NORM) and largest |z| (NVFP4), over its warp.
 template <int FORM, bool NORM, int V>
-__device__ __forceinline__ void warp_terms(const uint4 (&held)[V], const uint4 (&w)[V], Two& sum,
+__device__ __forceinline__ void warp_terms(const Piece (&held)[V], const Piece (&w)[V], Two& sum,
                                            uint32_t& top) {
   if constexpr (NORM) {
     float2 s = make_float2(0.f, 0.f), c = make_float2(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float2 f[4];
-      bf16x8(held[v], f);
+      float2 f[8];
+      unpack(held[v], f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) add_squares(s, c, f[i]);
+      for (int i = 0; i < 8; ++i) add_squares(s, c, f[i]);
     }
     sum = warp_sum(add({s.x, c.x}, {s.y, c.y}));
   }
@@ -225,14 +245,14 @@ __device__ __forceinline__ void warp_terms(const uint4 (&held)[V], const uint4 (
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if constexpr (NORM) {
-        float2 f[4], g[4];
-        bf16x8(held[v], f);
-        bf16x8(w[v], g);
+        float2 f[8], g[8];
+        unpack(held[v], f);
+        unpack(w[v], g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], g[i]);
+        for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], g[i]);
         top = max(top, top_of(f));
       } else {
-        top = max(top, top_bf16x8(held[v]));
+        top = max(top, top_of(held[v]));
       }
     }
     top = __reduce_max_sync(0xffffffffu, top);
@@ -271,11 +291,11 @@ __device__ __forceinline__ RowTerms row_terms(const ActQuantArgs& a, int m, cons
 
 // Codes and scales of a thread's pieces of row m.
 template <int FORM, bool NORM, int V>
-__device__ __forceinline__ void write_row(const ActQuantArgs& a, int m, const uint4 (&held)[V],
-                                          const uint4 (&weight)[V], const RowTerms& row) {
+__device__ __forceinline__ void write_row(const ActQuantArgs& a, int m, const Piece (&held)[V],
+                                          const Piece (&weight)[V], const RowTerms& row) {
   constexpr bool NV = FORM == kActNvfp4;
   const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31;
-  const int pieces = a.K >> 3;
+  const int pieces = a.K >> 4;
   // scale words of this row: tile (m / 128, word), 512 bytes apart
   const int words = (a.K + (NV ? 63 : 127)) / (NV ? 64 : 128);
   uint32_t* stile = reinterpret_cast<uint32_t*>(a.scales) +
@@ -285,20 +305,19 @@ __device__ __forceinline__ void write_row(const ActQuantArgs& a, int m, const ui
     if (v * T + warp * 32 >= pieces) break;  // warp-uniform
     const int p = v * T + tid;
     const bool in = p < pieces;
-    float2 f[4];
-    bf16x8(held[v], f);
+    float2 f[8];
+    unpack(held[v], f);
     uint32_t top;
     if constexpr (NORM) {
-      float2 w[4];
-      bf16x8(weight[v], w);
+      float2 w[8];
+      unpack(weight[v], w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w[i]);
+      for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], w[i]);
       top = top_of(f);
     } else {
-      top = top_bf16x8(held[v]);
+      top = top_of(held[v]);
     }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    if constexpr (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if constexpr (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     uint32_t sc = 0u;
     if constexpr (NV) {
       // quotients with the residual put back: the ties among them come out exactly
@@ -307,11 +326,11 @@ __device__ __forceinline__ void write_row(const ActQuantArgs& a, int m, const ui
       if (top != 0u) sc = e4m3_not_below(quotient2(top2, row.a10, row.i10).x, value);
       const float den = value * row.a12, inv = near_reciprocal(den);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = quotient2(mul2(f[i], 0.65625f), den, inv);
-      const uint32_t c = e2m1x8(f);
+      for (int i = 0; i < 8; ++i) f[i] = quotient2(mul2(f[i], 0.65625f), den, inv);
+      const uint2 c = make_uint2(e2m1x8(f), e2m1x8(f + 4));
       if (in)
-        reinterpret_cast<uint32_t*>(a.codes + static_cast<size_t>(m) * (a.K >> 1))[p] =
-            sc != 0u ? c : 0u;
+        reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m) * (a.K >> 1))[p] =
+            sc != 0u ? c : make_uint2(0u, 0u);
     } else {
       if constexpr (NORM) {
         // the largest |y|, towards its exact value where it is a power of two
@@ -329,35 +348,36 @@ __device__ __forceinline__ void write_row(const ActQuantArgs& a, int m, const ui
       }
       const float scale = __uint_as_float(static_cast<uint32_t>(127 - X) << 23);  // 2^-X
       if constexpr (NORM) {
-        float2 y[4];
+        float2 y[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mul2(f[i], row.rinv.hi);
+        for (int i = 0; i < 8; ++i) y[i] = mul2(f[i], row.rinv.hi);
         if (any_few_bits(y))
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 8; ++i) {
             if (few_bits(y[i].x)) y[i].x = off_border(y[i].x, f[i].x, row.rinv);
             if (few_bits(y[i].y)) y[i].y = off_border(y[i].y, f[i].y, row.rinv);
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = y[i];
+        for (int i = 0; i < 8; ++i) f[i] = y[i];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], scale);
+      for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], scale);
       if constexpr (FORM == kActMxfp4) {
-        const uint32_t c = e2m1x8(f);
+        const uint2 c = make_uint2(e2m1x8(f), e2m1x8(f + 4));
         if (in)
-          reinterpret_cast<uint32_t*>(a.codes + static_cast<size_t>(m) * (a.K >> 1))[p] =
-              top != 0u ? c : 0u;
+          reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m) * (a.K >> 1))[p] =
+              top != 0u ? c : make_uint2(0u, 0u);
       } else {
-        const uint32_t lo = e4m3_pair(f[0]) | (e4m3_pair(f[1]) << 16);
-        const uint32_t hi = e4m3_pair(f[2]) | (e4m3_pair(f[3]) << 16);
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = e4m3_pair(f[2 * i]) | (e4m3_pair(f[2 * i + 1]) << 16);
         if (in)
-          reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(m) * a.K)[p] =
-              top != 0u ? make_uint2(lo, hi) : make_uint2(0u, 0u);
+          reinterpret_cast<uint4*>(a.codes + static_cast<size_t>(m) * a.K)[p] =
+              top != 0u ? make_uint4(c[0], c[1], c[2], c[3]) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
-    // four blocks' scales (2 or 4 lanes each) in one word
-    constexpr int G = NV ? 2 : 4;
+    // four blocks' scales (a lane or two each) in one word
+    constexpr int G = NV ? 1 : 2;
     const uint32_t w1 = __shfl_down_sync(0xffffffffu, sc, G);
     const uint32_t w2 = __shfl_down_sync(0xffffffffu, sc, 2 * G);
     const uint32_t w3 = __shfl_down_sync(0xffffffffu, sc, 3 * G);
@@ -368,38 +388,40 @@ __device__ __forceinline__ void write_row(const ActQuantArgs& a, int m, const ui
 
 // A CTA a row.
 template <int FORM, bool NORM, int V>
-__global__ void __launch_bounds__(V > 2 ? 512 : 1024)
+__global__ void __launch_bounds__(V > 1 ? 512 : 1024)
     act_row_kernel(const ActQuantArgs a, int group) {
   __shared__ Two s_sum[32];
   __shared__ uint32_t s_max[32];
   const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, warps = T >> 5;
-  const int m = blockIdx.x, pieces = a.K >> 3;
+  const int m = blockIdx.x, pieces = a.K >> 4;
 
   pdl_wait();
   pdl_launch_dependents();  // after the wait: no more than one kernel waits for another
-  const uint4* src = reinterpret_cast<const uint4*>(a.x + m * a.x_stride);
-  const uint4* res = reinterpret_cast<const uint4*>(a.residual + m * a.residual_stride);
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 held[V], w[V];
+  const uint16_t* src = a.x + m * a.x_stride;
+  Piece held[V], w[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int p = v * T + tid;
-    held[v] = p < pieces ? src[p] : zero;
-    w[v] = NORM && p < pieces ? reinterpret_cast<const uint4*>(a.weight)[p] : zero;
+    held[v] = p < pieces ? load_piece(src, p) : no_piece();
+    w[v] = NORM && p < pieces ? load_piece(a.weight, p) : no_piece();
   }
   if (NORM && a.residual) {
+    const uint16_t* res = a.residual + m * a.residual_stride;
     uint4* out = reinterpret_cast<uint4*>(a.residual_out + m * a.residual_out_stride);
-    uint4 r[V];
+    Piece r[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = v * T + tid;
-      r[v] = p < pieces ? res[p] : zero;
+      r[v] = p < pieces ? load_piece(res, p) : no_piece();
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = v * T + tid;
       held[v] = add_rows(held[v], r[v]);
-      if (p < pieces) out[p] = held[v];
+      if (p < pieces) {
+        out[2 * p] = held[v].lo;
+        out[2 * p + 1] = held[v].hi;
+      }
     }
   }
   if constexpr (NORM || FORM == kActNvfp4) {
@@ -418,7 +440,7 @@ __global__ void __launch_bounds__(V > 2 ? 512 : 1024)
 
 template <int FORM, bool NORM, int V>
 cudaError_t launch_pieces(const ActQuantArgs& a, cudaStream_t stream) {
-  const int pieces = a.K / 8;
+  const int pieces = a.K / 16;
   const int threads = ((pieces + V - 1) / V + 31) / 32 * 32;
   int group = 1;  // the power of two not below the number of warps
   while (group < threads / 32) group *= 2;
@@ -428,25 +450,21 @@ cudaError_t launch_pieces(const ActQuantArgs& a, cudaStream_t stream) {
 
 template <int FORM, bool NORM>
 cudaError_t launch_form(const ActQuantArgs& a, cudaStream_t stream) {
-  // Pieces a thread. Few rows are a matter of latency: one piece each, while 1024 threads hold the
-  // row (one row of 4096 with norm 2.2 us, with two pieces 2.8, four 4.2). Many rows keep the SMs
-  // full whatever a CTA's size, and fewer threads a row join in fewer steps: four (4096 x 4096
-  // with norm 21.1 us, two 22.5, one 28), down to some 100 threads. Longer rows take what 512
-  // threads need.
-  const int pieces = a.K / 8, sms = device_sm_count();
+  const int pieces = a.K / 16, sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
+  // Pieces a thread. Few rows are a matter of latency: one each (one row of 4096 with norm 2.2 us,
+  // with two pieces 2.6, four 3.4). Many rows keep the SMs full whatever a CTA's size, and fewer
+  // threads join in fewer steps: two from 256 pieces on (4096 x 4096 with norm 20.8 us, one 23.4,
+  // four 23.5; rows of 1536 10.0 with one, 11.1 with two), four where NVFP4 waits for the row's
+  // largest value alone (4096 x 14336 26.4, two 33.6). Longer rows take what 512 threads need.
   int v = 1;
-  if (a.M < 2 * sms)
-    while (v < 2 && pieces > 1024 * v) v *= 2;
-  else
-    while (v < 4 && pieces >= 96 * 2 * v) v *= 2;
-  while (pieces > (v <= 2 ? 1024 : 512) * v) v *= 2;
+  if (a.M >= 2 * sms && pieces >= 256) v = FORM == kActNvfp4 && !NORM && pieces >= 768 ? 4 : 2;
+  while (pieces > (v == 1 ? 1024 : 512) * v) v *= 2;
   switch (v) {
     case 1: return launch_pieces<FORM, NORM, 1>(a, stream);
     case 2: return launch_pieces<FORM, NORM, 2>(a, stream);
     case 4: return launch_pieces<FORM, NORM, 4>(a, stream);
-    case 8: return launch_pieces<FORM, NORM, 8>(a, stream);
-    default: return launch_pieces<FORM, NORM, 16>(a, stream);
+    default: return launch_pieces<FORM, NORM, 8>(a, stream);
   }
 }
 
