@@ -131,7 +131,8 @@ __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity,
 
 // One stage's scales and products: `a` and `b` the operands' tiles, sa and sb their scale tiles
 // (low words of descriptors), BLOCKS_B row blocks of b's scales; columns of the scales in tensor
-// memory at ca and cb. (Tiles begin at a block: scales that begin at an odd column fault.) WHOLE: all of the stage's k lies in the row; else `left` values of it.
+// memory at ca and cb. (Tiles begin at a block of 128 rows: scales that begin at an odd column
+// fault.) WHOLE: all of the stage's k lies in the row; else `left` values of it.
 template <int FORM, int GROUP, int BLOCKS_B, bool WHOLE>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t b, uint32_t sa,
                                             uint32_t sb, uint32_t ca, uint32_t cb, uint32_t idesc,
@@ -273,10 +274,10 @@ struct Narrow {
   static_assert(kSend || NT * 128 * 4 <= kStages * (w_bytes + x_bytes), "parts reuse the ring");
   static_assert(alloc <= 113 * 1024, "two CTAs share the shared memory");
 };
-constexpr int kNarrowThreads = 192;  // four warps for the tile, one for copies, one for the MMAs
+constexpr int kThreads = 192;  // four warps for the tile, one for copies, one for the MMAs
 
 template <int FORM, int NT>
-__global__ void __launch_bounds__(kNarrowThreads, 2)
+__global__ void __launch_bounds__(kThreads, 2)
     act_narrow_kernel(const __grid_constant__ NarrowMaps maps, const ActMatmulArgs a, int splits) {
   using L = Narrow<FORM, NT>;
   using F = Form<FORM>;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       for (int i = 0; i < count; ++i) {
         const int s = i % S;
         if (i >= S && !stage_wait(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, a.status,
-                                         a.wait_limit_ns))
+                                  a.wait_limit_ns))
           break;
         const int t0 = (first + i) * L::kTiles;
         const uint32_t sb = static_cast<uint32_t>(min(L::kTiles, tiles_all - t0)) * 512u;
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     for (int i = 0; i < count; ++i) {
       const int s = i % S;
       if (!__all_sync(0xffffffffu, stage_wait(&full[s], (i / S) & 1u, abort_flag, a.status,
-                                                     a.wait_limit_ns)))
+                                              a.wait_limit_ns)))
         break;
       tc_fence_after_sync();
       const int left = a.K - (first + i) * F::KS;
@@ -371,9 +372,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       const uint32_t as = sw0 + s * (L::s_bytes >> 4), bs = sx0 + s * (L::s_bytes >> 4);
       if (elect_one()) {
         if (left >= F::KS)
-          issue_stage<FORM, 1, 1, true>(tmem, aw, ax, as, bs, ca, ca + L::s_cols, idesc, i == 0, left);
+          issue_stage<FORM, 1, 1, true>(tmem, aw, ax, as, bs, ca, ca + L::s_cols, idesc, i == 0,
+                                        left);
         else
-          issue_stage<FORM, 1, 1, false>(tmem, aw, ax, as, bs, ca, ca + L::s_cols, idesc, i == 0, left);
+          issue_stage<FORM, 1, 1, false>(tmem, aw, ax, as, bs, ca, ca + L::s_cols, idesc, i == 0,
+                                         left);
         tc_commit(&empty[s]);
       }
       __syncwarp();
@@ -438,9 +441,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       const float2* parts = reinterpret_cast<const float2*>(smem + L::part_off);
       const int half = shift - 1;  // pairs of columns
       float f = f0;
-      for (int p = threadIdx.x; p < rows << half; p += kNarrowThreads) {
+      for (int p = threadIdx.x; p < rows << half; p += kThreads) {
         const int j = p >> half, c = p & ((1 << half) - 1), n = n0 + (part << shift) + 2 * c;
-        if (FORM == kActNvfp4 && p >= kNarrowThreads) f = __ldg(a.x_rows + m0 + j);
+        if (FORM == kActNvfp4 && p >= kThreads) f = __ldg(a.x_rows + m0 + j);
         float2 sum = make_float2(0.f, 0.f);
         for (int r = 0; r < splits; ++r) {
           const float2 v = parts[((r * NT + j) << half) + c];
@@ -465,8 +468,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       // four columns at a time; the cluster's CTAs take them in turn, with the loads of all parts
       // on their way together
       const uint32_t base = smem_addr(smem);
-      for (int p = part * kNarrowThreads + threadIdx.x; p < rows * 32;
-           p += splits * kNarrowThreads) {
+      for (int p = part * kThreads + threadIdx.x; p < rows * 32;
+           p += splits * kThreads) {
         const int j = p >> 5, c = (p & 31) * 4, n = n0 + c;
         float4 v[8];
 #pragma unroll
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   }
 }
 
-// Many rows of x: a pair of CTAs on one MMA of 256 rows of x (A, 128 a CTA, D's lanes) by NT
+// Many rows of x: a pair of CTAs on one MMA of 256 rows of x (A, 128 a CTA, D's lanes) by 256
 // columns (B, half of the weights' rows in either CTA's shared memory), so that an operand's
 // byte feeds twice the products of one CTA's tile. Persistent pairs; the accumulator has two
 // places, so that a tile's MMAs run while the last one's sums are scaled, rounded and stored.
@@ -506,12 +509,14 @@ struct WideMaps {
   CUtensorMap w, x, sw, sx, y;
 };
 
-template <int FORM, int NT>
+constexpr int kWideN = 256;  // columns of a tile
+
+template <int FORM>
 struct Wide {
   using F = Form<FORM>;
   static constexpr int kTiles = F::KS / F::KT;
-  static constexpr int kBlocks = NT / 128;  // row blocks of the weights' scales
-  static constexpr uint32_t x_bytes = 128 * 128, w_bytes = NT / 2 * 128;
+  static constexpr int kBlocks = kWideN / 128;  // row blocks of the weights' scales
+  static constexpr uint32_t x_bytes = 128 * 128, w_bytes = kWideN / 2 * 128;
   static constexpr uint32_t w_tx = FORM == kActMxfp8 ? w_bytes / 2 : w_bytes;
   static constexpr uint32_t s_bytes = kTiles * 512;
   static constexpr uint32_t stage_bytes = x_bytes + w_bytes + (1 + kBlocks) * s_bytes;
@@ -519,7 +524,8 @@ struct Wide {
   // pieces of y on their way out, 32 rows by 64 columns: two a warp where that costs no stage
   static constexpr int kRoom = 227 * 1024 - 256;
   static constexpr int kStages = (kRoom - 4 * 4096) / static_cast<int>(stage_bytes);
-  static constexpr int kOut = (kRoom - 2 * 4 * 4096) / static_cast<int>(stage_bytes) == kStages ? 2 : 1;
+  static constexpr int kOut =
+      (kRoom - 2 * 4 * 4096) / static_cast<int>(stage_bytes) == kStages ? 2 : 1;
   static constexpr uint32_t out_bytes = 4 * kOut * 4096;
   static constexpr uint32_t w_off = kStages * x_bytes;
   static constexpr uint32_t out_off = w_off + kStages * w_bytes;
@@ -530,17 +536,15 @@ struct Wide {
   static constexpr uint32_t misc_off = bar_off + (2 * kStages + 5) * 8;
   static constexpr uint32_t alloc = misc_off + 16;
   static_assert(alloc <= 227 * 1024, "shared memory");
-  // Tensor memory: the scales, and two accumulators, which overlap where 512 columns do not hold
+  // Tensor memory: the scales, and two accumulators, which overlap, since 512 columns do not hold
   // them apart; a tile's epilogue empties the columns that they share first.
   static constexpr uint32_t s_cols = 4 * kTiles * (1 + kBlocks);
-  static constexpr uint32_t acc_step =
-      512 - 2 * NT >= s_cols ? NT : (512 - NT - s_cols) / 64 * 64;
-  static constexpr int kShared = (NT - static_cast<int>(acc_step)) / 64;  // 64-column pieces
-  // a part of the sums between pairs: rows of NT floats, four apart in their banks
-  static constexpr int kPartRow = NT + 4;
+  static constexpr uint32_t acc_step = (512 - kWideN - s_cols) / 64 * 64;
+  static constexpr int kShared = (kWideN - static_cast<int>(acc_step)) / 64;  // 64-column pieces
+  // a part of the sums between pairs: rows of floats, four apart in their banks
+  static constexpr int kPartRow = kWideN + 4;
   static_assert(128 * kPartRow * 4 <= kStages * (x_bytes + w_bytes), "parts reuse the ring");
-  static constexpr int kLag = kShared > 0 ? 1 : 2;  // tiles between an accumulator's fill and reuse
-  static constexpr uint32_t sx_col = acc_step + NT;
+  static constexpr uint32_t sx_col = acc_step + kWideN;
   static constexpr uint32_t sw_col = sx_col + 4 * kTiles;
   static_assert(sx_col + s_cols <= 512, "tensor memory");
 };
@@ -558,11 +562,11 @@ struct WideOrder {
   }
 };
 
-template <int FORM, int NT, int SPLIT>
-__global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
-    act_wide_kernel(const __grid_constant__ WideMaps maps, const ActMatmulArgs a, const WideOrder order,
-                    int use_store) {
-  using L = Wide<FORM, NT>;
+template <int FORM, int SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
+    act_wide_kernel(const __grid_constant__ WideMaps maps, const ActMatmulArgs a,
+                    const WideOrder order, int use_store) {
+  using L = Wide<FORM>;
   using F = Form<FORM>;
   constexpr int S = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];  // (no room to align it by hand)
@@ -622,7 +626,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
   if (warp == 4) {
     if (lane == 0) {
       const uint32_t full0 = peer_addr(smem_addr(full), lead);
-      const int w_row = static_cast<int>(rank) * (NT / 2);
+      const int w_row = static_cast<int>(rank) * (kWideN / 2);
       int s = 0;
       uint32_t phase = 1;  // of the stage's last use
       bool go = true;
@@ -637,11 +641,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
           }
           const uint32_t bar = full0 + s * 8;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::tx_bytes);
-          // rows past the arrays come as zeros, tiles of scales past a row's end as another's:
-          // the first are not stored, the second not multiplied
+          // rows and scale tiles past the arrays come as zeros
           pair_load_2d(smem + s * L::x_bytes, &maps.x, bar, i * 128, bm * 128);
           pair_load_3d(smem + L::sx_off + s * L::s_bytes, &maps.sx, bar, 0, i * L::kTiles, bm);
-          pair_load_2d(smem + L::w_off + s * L::w_bytes, &maps.w, bar, i * 128, tn * NT + w_row);
+          pair_load_2d(smem + L::w_off + s * L::w_bytes, &maps.w, bar, i * 128, tn * kWideN + w_row);
           pair_load_3d(smem + L::sw_off + s * L::kBlocks * L::s_bytes, &maps.sw, bar, 0,
                        i * L::kTiles, tn * L::kBlocks);
           if (++s == S) {
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
     }
   } else if (warp == 5 && rank == 0) {
     // the whole warp walks the stages, one lane issues the pair's MMAs
-    constexpr uint32_t idesc = idesc_scaled<FORM, false>(256, NT);
+    constexpr uint32_t idesc = idesc_scaled<FORM, false>(256, kWideN);
     const uint32_t x0 = desc_low(smem), w0 = desc_low(smem + L::w_off);
     const uint32_t sx0 = desc_low(smem + L::sx_off), sw0 = desc_low(smem + L::sw_off);
     const uint32_t ca = tmem + L::sx_col, cb = tmem + L::sw_col;
@@ -663,11 +666,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
     for (int t = first; t < tiles && go; t += step, ++n_tile) {
       const int b = n_tile & 1;
       const uint32_t acc = tmem + b * L::acc_step;
-      if (n_tile >= L::kLag) {
-        const int q = n_tile - L::kLag;  // the tile whose columns must be empty
-        go = __all_sync(0xffffffffu,
-                        stage_wait(&acc_empty[q & 1], (q >> 1) & 1u, abort_flag, a.status,
-                                             a.wait_limit_ns));
+      if (n_tile > 0) {
+        const int q = n_tile - 1;  // the tile whose shared columns must be empty
+        go = __all_sync(0xffffffffu, stage_wait(&acc_empty[q & 1], (q >> 1) & 1u, abort_flag,
+                                                a.status, a.wait_limit_ns));
         if (!go) break;
         tc_fence_after_sync();
       }
@@ -682,9 +684,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
         const uint32_t bs = sw0 + s * (L::kBlocks * L::s_bytes >> 4);
         if (elect_one()) {
           if (left >= F::KS)
-            issue_stage<FORM, 2, L::kBlocks, true>(acc, ax, bw, as, bs, ca, cb, idesc, i == begin, left);
+            issue_stage<FORM, 2, L::kBlocks, true>(acc, ax, bw, as, bs, ca, cb, idesc, i == begin,
+                                                   left);
           else
-            issue_stage<FORM, 2, L::kBlocks, false>(acc, ax, bw, as, bs, ca, cb, idesc, i == begin, left);
+            issue_stage<FORM, 2, L::kBlocks, false>(acc, ax, bw, as, bs, ca, cb, idesc, i == begin,
+                                                    left);
           pair_commit(&empty[s], both);
           if (i == end - 1) pair_commit(&acc_full[b], both);
         }
@@ -710,33 +714,34 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
       float f = wscale;
       if constexpr (FORM == kActNvfp4) f *= row < a.M ? __ldg(a.x_rows + row) : 0.f;
       bool ok = stage_wait(&acc_full[b], (n_tile >> 1) & 1u, abort_flag, a.status,
-                                     a.wait_limit_ns);
+                           a.wait_limit_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after_sync();
 #pragma unroll 1
-      for (int cc = 0; cc < NT / 64; ++cc) {
+      for (int cc = 0; cc < kWideN / 64; ++cc) {
         // the columns that the other accumulator shares come first
-        const int c = L::kShared > 0 && b == 0 ? NT / 64 - 1 - cc : cc;
+        const int c = b == 0 ? kWideN / 64 - 1 - cc : cc;
         uint32_t v[64];
         tmem_ld_32cols(lane_base + b * L::acc_step + c * 64, v);
         tmem_ld_32cols(lane_base + b * L::acc_step + c * 64 + 32, v + 32);
         tmem_ld_wait();
-        if (cc == (L::kShared > 0 ? L::kShared : NT / 64) - 1) {
+        if (cc == L::kShared - 1) {
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) peer_arrive(&acc_empty[b], lead);
         }
         if constexpr (SPLIT > 1) {
           // the pair's part of the sums, where its stages were
-          float4* to = reinterpret_cast<float4*>(smem) + (warp * 32 + lane) * (L::kPartRow / 4) + c * 16;
+          float4* to =
+              reinterpret_cast<float4*>(smem) + (warp * 32 + lane) * (L::kPartRow / 4) + c * 16;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             to[j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
                                 __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
           continue;
         }
-        const int n0 = tn * NT + c * 64;
+        const int n0 = tn * kWideN + c * 64;
         uint32_t p[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -752,7 +757,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
           if (row0 < a.M && n0 < a.N) {  // warp-uniform
             uint8_t* dst = out + piece * 4096;
             if constexpr (L::kOut == 2) piece ^= 1;
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(L::kOut - 1) : "memory");
+            if (lane == 0)
+              asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(L::kOut - 1) : "memory");
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -779,7 +785,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
   }
   __syncwarp();
   volatile uint32_t none = 0u;
-  if (!stage_wait(done, 0u, &none, a.status, a.wait_limit_ns) || *abort_flag) {
+  // (a warp without a part in the work does not wait for all of it, which may pass the limit)
+  const bool idle = warp == 5 && rank != 0;
+  if (!idle && (!stage_wait(done, 0u, &none, a.status, a.wait_limit_ns) || *abort_flag)) {
     // a wait has run out: the copies in flight (microseconds) land before anything else
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 2000000u) {
@@ -796,12 +804,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
     const uint32_t base = smem_addr(smem);
     // this pair's share of the columns, four at a time; neighbouring threads take neighbours, and
     // the loads of kBatch turns are on their way together
-    constexpr int kQuads = NT / SPLIT / 4, kBatch = 4;
-    for (int q0 = threadIdx.x; q0 < 128 * kQuads; q0 += kBatch * kNarrowThreads) {
+    constexpr int kQuads = kWideN / SPLIT / 4, kBatch = 4;
+    for (int q0 = threadIdx.x; q0 < 128 * kQuads; q0 += kBatch * kThreads) {
       float4 v[kBatch][SPLIT];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int q = min(q0 + u * kNarrowThreads, 128 * kQuads - 1), r = q / kQuads;
+        const int q = min(q0 + u * kThreads, 128 * kQuads - 1), r = q / kQuads;
         const int c = (static_cast<int>(part) * kQuads + q % kQuads) * 4;
 #pragma unroll
         for (int p = 0; p < SPLIT; ++p)
@@ -809,9 +817,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) __cluster_dims__(2 * SPLIT,
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int q = q0 + u * kNarrowThreads, r = q / kQuads;
+        const int q = q0 + u * kThreads, r = q / kQuads;
         const int c = (static_cast<int>(part) * kQuads + q % kQuads) * 4;
-        const int row = tm * 256 + static_cast<int>(rank) * 128 + r, n = tn * NT + c;
+        const int row = tm * 256 + static_cast<int>(rank) * 128 + r, n = tn * kWideN + c;
         if (!ok || q >= 128 * kQuads || row >= a.M || n >= a.N) continue;
         float4 sum = v[u][0];
 #pragma unroll
@@ -879,7 +887,7 @@ cudaError_t launch_narrow(const ActMatmulArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tn), static_cast<unsigned>(tm),
                      static_cast<unsigned>(splits));
-  cfg.blockDim = dim3(kNarrowThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::alloc;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -906,12 +914,12 @@ cudaError_t make_scale_map(CUtensorMap* map, const uint8_t* scales, int rows, in
                               CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <int FORM, int NT, int SPLIT>
+template <int FORM, int SPLIT>
 cudaError_t launch_wide(const ActMatmulArgs& a, cudaStream_t stream) {
-  using L = Wide<FORM, NT>;
+  using L = Wide<FORM>;
   WideMaps maps = {};
   constexpr bool x8 = FORM == kActMxfp8;
-  cudaError_t e = make_map(&maps.w, a.w_codes, a.N, a.K, NT / 2, false, x8);
+  cudaError_t e = make_map(&maps.w, a.w_codes, a.N, a.K, kWideN / 2, false, x8);
   if (e != cudaSuccess) return e;
   e = make_map(&maps.x, a.x_codes, a.M, a.K, 128, x8, false);
   if (e != cudaSuccess) return e;
@@ -927,17 +935,17 @@ cudaError_t launch_wide(const ActMatmulArgs& a, cudaStream_t stream) {
                           CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
-  auto kern = act_wide_kernel<FORM, NT, SPLIT>;
+  auto kern = act_wide_kernel<FORM, SPLIT>;
   e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(L::alloc));
   if (e != cudaSuccess) return e;
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const WideOrder order = {(a.M + 255) / 256, (a.N + NT - 1) / NT};
+  const WideOrder order = {(a.M + 255) / 256, (a.N + kWideN - 1) / kWideN};
   const long long tiles = static_cast<long long>(order.tm) * order.tn;
   if (tiles > 0x7fffffffLL - 2 * sms) return cudaErrorInvalidConfiguration;
   const int clusters = static_cast<int>(SPLIT > 1 || tiles < sms / 2 ? tiles : sms / 2);
   return launch_with_pdl(kern, dim3(static_cast<unsigned>(2 * SPLIT * clusters)),
-                         dim3(kNarrowThreads), L::alloc, stream, maps, a, order, use_store);
+                         dim3(kThreads), L::alloc, stream, maps, a, order, use_store);
 }
 
 template <int FORM>
@@ -959,9 +967,9 @@ cudaError_t launch_form(const ActMatmulArgs& a, int kernel, cudaStream_t stream)
     if (kernel == 2 && stages >= 24)
       kernel = tiles * 10 <= sms ? 4 : tiles * 4 <= sms - 8 ? 3 : 2;
   }
-  if (kernel == 4 && stages >= 4) return launch_wide<FORM, 256, 4>(a, stream);
-  if (kernel >= 3 && stages >= 2) return launch_wide<FORM, 256, 2>(a, stream);
-  if (kernel >= 2) return launch_wide<FORM, 256, 1>(a, stream);
+  if (kernel == 4 && stages >= 4) return launch_wide<FORM, 4>(a, stream);
+  if (kernel >= 3 && stages >= 2) return launch_wide<FORM, 2>(a, stream);
+  if (kernel >= 2) return launch_wide<FORM, 1>(a, stream);
   if (a.M <= 16) return launch_narrow<FORM, 16>(a, stream);
   if (a.M <= 32) return launch_narrow<FORM, 32>(a, stream);
   if (a.M <= 64) return launch_narrow<FORM, 64>(a, stream);
