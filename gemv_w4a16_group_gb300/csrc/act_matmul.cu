@@ -12,10 +12,12 @@
 namespace w4k {
 namespace {
 
-// Launches. The kernels may begin while the one before them runs, up to their wait for it, but do
-// not let the next one begin before they end: with launch_dependents in them, graphs of norms and
-// products, several grids in flight and each waiting for the one before, came to a standstill (the
-// clusters that were still to be placed and the next norm's CTAs want the same SMs).
+// Launches are plain ones: a kernel begins when the one before it on its stream has ended. Begun
+// early (programmatic launches), graphs of norms and products came to a standstill, on one stream
+// when every kernel let the next begin, on three streams even when no cluster kernel did. What a
+// resident CTA waits for without a limit is now its own cluster, which is placed as a whole, and
+// its columns of tensor memory: two narrow CTAs' fit in an SM, a wide CTA has the SM's shared
+// memory to itself.
 
 // A stage is a 128-byte swizzle row of k per row: 256 E2M1 or 128 E4M3 values. TILES scale tiles
 // (128 rows x 4 scales, 512 bytes) cover it; an MMA takes KM values, STEPS of them a stage.
@@ -322,7 +324,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncwarp();
   // (waited for before the parts are sent: every CTA of the cluster has begun)
   if (L::kSend && splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  pdl_wait();
   const int rows = min(NT, a.M - m0);
   // a CTA of a cluster adds up 2^shift columns of the tile
   const int shift = 8 - __ffs(splits);
@@ -621,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
   cluster_sync_all();  // both CTAs' barriers stand
   tc_fence_after_sync();
   const uint32_t tmem = *holder;
-  pdl_wait();
 
   if (warp == 4) {
     if (lane == 0) {
@@ -890,15 +890,13 @@ cudaError_t launch_narrow(const ActMatmulArgs& a, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::alloc;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = static_cast<unsigned>(splits);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, maps, a, splits);
 }
 
@@ -944,8 +942,9 @@ cudaError_t launch_wide(const ActMatmulArgs& a, cudaStream_t stream) {
   const long long tiles = static_cast<long long>(order.tm) * order.tn;
   if (tiles > 0x7fffffffLL - 2 * sms) return cudaErrorInvalidConfiguration;
   const int clusters = static_cast<int>(SPLIT > 1 || tiles < sms / 2 ? tiles : sms / 2);
-  return launch_with_pdl(kern, dim3(static_cast<unsigned>(2 * SPLIT * clusters)),
-                         dim3(kThreads), L::alloc, stream, maps, a, order, use_store);
+  kern<<<static_cast<unsigned>(2 * SPLIT * clusters), kThreads, L::alloc, stream>>>(maps, a, order,
+                                                                                    use_store);
+  return cudaGetLastError();
 }
 
 template <int FORM>

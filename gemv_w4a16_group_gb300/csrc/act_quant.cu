@@ -395,8 +395,6 @@ __global__ void __launch_bounds__(V > 1 ? 512 : 1024)
   const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, warps = T >> 5;
   const int m = blockIdx.x, pieces = a.K >> 4;
 
-  pdl_wait();
-  pdl_launch_dependents();  // after the wait: no more than one kernel waits for another
   const uint16_t* src = a.x + m * a.x_stride;
   Piece held[V], w[V];
 #pragma unroll
@@ -444,8 +442,10 @@ cudaError_t launch_pieces(const ActQuantArgs& a, cudaStream_t stream) {
   const int threads = ((pieces + V - 1) / V + 31) / 32 * 32;
   int group = 1;  // the power of two not below the number of warps
   while (group < threads / 32) group *= 2;
-  return launch_with_pdl(act_row_kernel<FORM, NORM, V>, dim3(static_cast<unsigned>(a.M)),
-                         dim3(static_cast<unsigned>(threads)), 0, stream, a, group);
+  // (a plain launch, like the products': no CTA is resident while it waits for another grid)
+  act_row_kernel<FORM, NORM, V><<<static_cast<unsigned>(a.M), static_cast<unsigned>(threads), 0,
+                                  stream>>>(a, group);
+  return cudaGetLastError();
 }
 
 template <int FORM, bool NORM>

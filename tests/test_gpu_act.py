@@ -454,6 +454,46 @@ def test_long_chains_in_graphs(form, M, N, K):
         assert torch.equal(y, want[i % 2])
 
 
+@pytest.mark.parametrize("calls", [
+    [("nvfp4", 64, 14336, 1024), ("mxfp8", 8, 4096, 4096), ("mxfp4", 512, 4096, 8192)],
+    [("nvfp4", 300, 4096, 4096), ("nvfp4", 17, 14336, 2048), ("mxfp8", 64, 4096, 7168)],
+    [("mxfp4", 128, 1536, 8960), ("mxfp8", 1000, 2048, 2048), ("nvfp4", 1, 4096, 4096)],
+])
+def test_chains_on_three_streams(calls):
+    """Graphs of norms and products on three streams at once: pairs, clusters of pairs and
+    clusters of single CTAs want the same SMs, and every one of them gets them."""
+    runs = []
+    for form, M, N, K in calls:
+        weight = torch.ones(K, device=DEV).bfloat16()
+        w = _weights(form, N, K, 6)
+        states = []
+        for seed in (60, 70):
+            x, res = _rows(M, K, seed).to(DEV), _rows(M, K, seed + 1).to(DEV)
+            states.append((x, res, torch.empty_like(res), w4.act_quantize(x, form)))
+
+        def step(x, res, out, q):
+            c, s, r, _ = w4.act_rmsnorm(x, weight, form, residual=res, residual_out=out,
+                                        codes=q[0], scales=q[1], row_scales=q[2])
+            return _matmul(form, (c, s, r), w)
+
+        want = [step(*st).clone() for st in states]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = [step(*states[i % 2]) for i in range(20)]
+        runs.append((graph, outs, want, torch.cuda.Stream(), (weight, w, states)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, _, _, stream, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    _ok()
+    for _, outs, want, _, _ in runs:
+        for i, y in enumerate(outs):
+            assert torch.equal(y, want[i % 2])
+
+
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("M", [1, 6, 150])
 def test_a_layer_as_it_is_used(form, M):
