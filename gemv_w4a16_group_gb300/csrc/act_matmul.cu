@@ -956,12 +956,12 @@ cudaError_t launch_form(const ActMatmulArgs& a, int kernel, cudaStream_t stream)
       ((static_cast<long long>(a.M) + 255) / 256) * ((static_cast<long long>(a.N) + 255) / 256);
   if (kernel == 0) {
     // The pairs' tiles of 256 x 256 want 256 rows of x or enough columns: 14336 x 4096 NVFP4 at 64
-    // rows 10.4 us (narrow 10.9), at 48 12.1 (10.1), MXFP8 at 96 14.1 (14.7), at 64 13.8 (12.1);
-    // 4096 x 14336 NVFP4 at 256 17.9 (15.1), at 512 18.7 (23.9).
+    // rows 11.7 us (narrow 12.4), at 48 12.5 (11.2), MXFP8 at 96 15.5 (15.4), at 64 15.1 (12.7);
+    // 4096 x 14336 NVFP4 at 256 19.4 (16.0), at 512 19.9 (22.0).
     const int few = FORM == kActMxfp8 ? 80 : 48;
     kernel = a.M <= few || (a.M <= 256 && tiles * 5 < sms) ? 1 : 2;
     // With few tiles pairs share them, where each part of k outweighs adding the parts up (4096 x
-    // 14336 MXFP4 at 512 rows 20.4 -> 16.1 us; 16 stages are even). 36 clusters of two pairs and
+    // 14336 MXFP4 at 512 rows 21.6 -> 17.2 us; 16 stages are even). 36 clusters of two pairs and
     // 15 of four fit on 152 SMs.
     if (kernel == 2 && stages >= 24)
       kernel = tiles * 10 <= sms ? 4 : tiles * 4 <= sms - 8 ? 3 : 2;
