@@ -56,7 +56,7 @@ __all__ = [
     "fp4_matmul_workspace_bytes", "nvfp4_matmul", "mxfp4_matmul", "testing_set_w8_variant",
     "kv4_cache", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_workspace_bytes",
     "kv4_evict", "fp4_prepare_scales", "act_quantize", "act_rmsnorm", "nvfp4_matmul_act",
-    "mxfp4_matmul_act", "testing_set_act_kernel",
+    "mxfp4_matmul_act", "testing_set_act_kernel", "testing_set_act_wait_limit",
 ]
 
 STATUS_NAMES = {0: "W4A16_OK", 1: "W4A16_ERR_INVALID_ARG", 2: "W4A16_ERR_UNSUPPORTED",
@@ -145,6 +145,8 @@ def _load():
                  "w4a16_testing_set_w8_variant", "w4a16_testing_set_act_kernel"):
         getattr(lib, name).argtypes = [I]
         getattr(lib, name).restype = I
+    lib.w4a16_testing_set_act_wait_limit.argtypes = [ctypes.c_uint64]
+    lib.w4a16_testing_set_act_wait_limit.restype = ctypes.c_uint64
     lib.w4a16_testing_set_skinny_range.argtypes = [I, I]
     lib.w4a16_testing_set_skinny_range.restype = I
     return lib
@@ -647,6 +649,12 @@ def testing_set_act_kernel(kernel: int) -> int:
     rows, 2 = pairs of CTAs on tiles of 256 x 256, 3 and 4 = two and four pairs a tile; other
     values only query. Returns the previous value."""
     return int(_lib.w4a16_testing_set_act_kernel(kernel))
+
+
+def testing_set_act_wait_limit(ns: int) -> int:
+    """Limit (1 to 10^9 ns, the default) of the waits of nvfp4_matmul_act / mxfp4_matmul_act; other
+    values only query. Returns the previous value."""
+    return int(_lib.w4a16_testing_set_act_wait_limit(ns))
 
 
 def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, group: int = 64,

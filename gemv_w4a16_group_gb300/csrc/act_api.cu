@@ -10,6 +10,7 @@
 namespace {
 
 int g_act_kernel = 0;  // see launch_act_matmul
+uint64_t g_act_wait_limit_ns = w4k::kDefaultWaitLimitNs;
 
 static_assert(W4A16_ACT_NVFP4 == w4k::kActNvfp4 && W4A16_ACT_MXFP4 == w4k::kActMxfp4 &&
                   W4A16_ACT_MXFP8 == w4k::kActMxfp8,
@@ -50,7 +51,7 @@ w4a16_status matmul(const w4k::ActMatmulArgs& args, int format, w4a16_stream_t s
     return W4A16_ERR_MISALIGNED;
   a.status = w4k::status_word();
   if (a.status == nullptr) return W4A16_ERR_CUDA;
-  a.wait_limit_ns = w4k::kDefaultWaitLimitNs;
+  a.wait_limit_ns = g_act_wait_limit_ns;
   return from_cuda(w4k::launch_act_matmul(a, format, g_act_kernel,
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -157,6 +158,12 @@ w4a16_status mxfp4_matmul_act(const uint8_t* x_codes, const uint8_t* x_scales, i
 int w4a16_testing_set_act_kernel(int kernel) {
   const int prev = g_act_kernel;
   if (kernel >= 0 && kernel <= 4) g_act_kernel = kernel;
+  return prev;
+}
+
+uint64_t w4a16_testing_set_act_wait_limit(uint64_t ns) {
+  const uint64_t prev = g_act_wait_limit_ns;
+  if (ns > 0 && ns <= w4k::kDefaultWaitLimitNs) g_act_wait_limit_ns = ns;
   return prev;
 }
 

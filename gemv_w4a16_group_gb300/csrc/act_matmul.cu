@@ -131,6 +131,10 @@ __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// How long a CTA that has given up a wait stays for its products and copies that are under way
+// (microseconds in truth), whatever the limit of the waits themselves is.
+constexpr uint64_t kSettleNs = 1000ull * 1000ull * 1000ull;
+
 // One stage's scales and products: `a` and `b` the operands' tiles, sa and sb their scale tiles
 // (low words of descriptors), BLOCKS_B row blocks of b's scales; columns of the scales in tensor
 // memory at ca and cb. (Tiles begin at a block of 128 rows: scales that begin at an odd column
@@ -173,6 +177,11 @@ __device__ __forceinline__ float4 peer_lds128(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t peer_lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -266,7 +275,8 @@ struct Narrow {
   static constexpr uint32_t part_off = sx_off + kStages * s_bytes;
   static constexpr uint32_t bar_off = part_off + part_bytes;  // full, empty, done
   static constexpr uint32_t misc_off = bar_off + (2 * kStages + 1) * 8;
-  static constexpr uint32_t alloc = misc_off + 16;
+  static constexpr uint32_t whole_off = misc_off + 8;  // a word of each CTA of the cluster
+  static constexpr uint32_t alloc = whole_off + 8 * 4;
   // tensor memory: the accumulator, two sets of scale columns
   static constexpr uint32_t s_cols = 4 * kTiles;
   static constexpr uint32_t acc_cols = NT < 32 ? 32 : NT;
@@ -294,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* done = empty + S;
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile uint32_t* abort_flag = holder + 1;
+  uint32_t* whole = reinterpret_cast<uint32_t*>(smem + L::whole_off);  // whether its sums are
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * 128, m0 = blockIdx.y * NT;
   const int part = blockIdx.z;  // this CTA's rank in its cluster
@@ -322,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after_sync();
   const uint32_t tmem = *holder;
   __syncwarp();
-  // (waited for before the parts are sent: every CTA of the cluster has begun)
-  if (L::kSend && splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  // (waited for before anything is sent: every CTA of the cluster has begun)
+  if (splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int rows = min(NT, a.M - m0);
   // a CTA of a cluster adds up 2^shift columns of the tile
   const int shift = 8 - __ffs(splits);
@@ -386,19 +397,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (elect_one()) tc_commit(done);
   }
   __syncwarp();
-  volatile uint32_t none = 0u;
-  bool ok = stage_wait(done, 0u, &none, a.status, a.wait_limit_ns);
-  if (!ok || *abort_flag)  // a wait has run out: the copies in flight land before anything else
+  bool ok = stage_wait(done, 0u, abort_flag, a.status, a.wait_limit_ns);
+  if (!ok || *abort_flag) {
+    // a wait has run out: products and copies that are under way end before anything else
+    volatile uint32_t none = 0u;
+    stage_wait(done, 0u, &none, a.status, kSettleNs);
     for (int s = 0; s < S && s < issued; ++s) {
       const int last = issued - 1 - ((issued - 1 - s) % S);
-      stage_wait(&full[s], (last / S) & 1u, &none, a.status, a.wait_limit_ns);
+      stage_wait(&full[s], (last / S) & 1u, &none, a.status, kSettleNs);
     }
+  }
   __syncwarp();
-  __syncthreads();
-  ok = ok && *abort_flag == 0u;
+  ok = __syncthreads_and(ok && *abort_flag == 0u);
   tc_fence_after_sync();
 
-  if (L::kSend && splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (splits > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (static_cast<int>(threadIdx.x) < splits)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                       peer_addr(smem_addr(whole + part), threadIdx.x)),
+                   "r"(ok ? 1u : 0u)
+                   : "memory");
+  }
   if (warp < 4) {
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float* parts = reinterpret_cast<float*>(smem);  // [NT][128]
@@ -438,6 +458,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (splits > 1) {
     __syncwarp();
     cluster_sync_all();
+    // a tile is stored where the sums of all its parts are whole
+    for (int r = 0; r < splits; ++r) ok = ok && whole[r] != 0u;
     if constexpr (L::kSend) {
       const float2* parts = reinterpret_cast<const float2*>(smem + L::part_off);
       const int half = shift - 1;  // pairs of columns
@@ -788,7 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
   // (a warp without a part in the work does not wait for all of it, which may pass the limit)
   const bool idle = warp == 5 && rank != 0;
   if (!idle && (!stage_wait(done, 0u, &none, a.status, a.wait_limit_ns) || *abort_flag)) {
-    // a wait has run out: the copies in flight (microseconds) land before anything else
+    // a wait has run out: products and copies under way (microseconds) end before anything else; a
+    // fixed time, since the first CTA's barriers, on which copies end, count both CTAs' whole stages
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 2000000u) {
     }
@@ -799,7 +822,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
     cluster_sync_all();  // the parts stand
     int tm, tn;
     order.at(first, tm, tn);
-    const bool ok = *abort_flag == 0u;
+    // stored where the sums of all pairs are whole
+    bool ok = true;
+#pragma unroll
+    for (int p = 0; p < SPLIT; ++p)
+      ok = ok && peer_lds32(peer_addr(smem_addr(holder + 1), 2 * p + rank)) == 0u;
     const float wscale = FORM == kActNvfp4 ? __ldg(a.w_scale) : 1.f;
     const uint32_t base = smem_addr(smem);
     // this pair's share of the columns, four at a time; neighbouring threads take neighbours, and

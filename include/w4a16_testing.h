@@ -10,6 +10,8 @@
 #ifndef W4A16_GB300_TESTING_H
 #define W4A16_GB300_TESTING_H
 
+#include <stdint.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -55,6 +57,11 @@ int w4a16_testing_set_w8_variant(int v);
  * 2 = pairs of CTAs on tiles of 256 x 256, 3 and 4 = two and four pairs a tile (as far as K has
  * stages for them). Other values only query. Returns the previous value. */
 int w4a16_testing_set_act_kernel(int kernel);
+
+/* Limit in nanoseconds (1 to 1e9, the default) of every wait of nvfp4_matmul_act and
+ * mxfp4_matmul_act, so that a test makes one run out. Other values only query. Returns the previous
+ * value. */
+uint64_t w4a16_testing_set_act_wait_limit(uint64_t ns);
 
 #ifdef __cplusplus
 }
