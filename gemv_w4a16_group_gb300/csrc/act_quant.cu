@@ -54,11 +54,12 @@ __device__ __forceinline__ uint32_t top_of(const Piece& v) {
   return max(t << 16, t & 0xFFFF0000u);
 }
 
-// Smallest E4M3 code whose value is >= v (v > 0), at most 0x7E (448), and that value. From 2^-6 on
-// a code is the float's exponent and three bits of its fraction, below a multiple of 2^-9.
+// Smallest code of an E4M3 value >= v, not 0 (v > 0, or too small for fp32) and at most 0x7E (448),
+// and that value. From 2^-6 on a code is the float's exponent and three bits of its fraction, below a
+// multiple of 2^-9.
 __device__ __forceinline__ uint32_t e4m3_not_below(float v, float& value) {
   if (v < 0x1p-6f) {
-    const uint32_t code = __float2uint_ru(v * 512.0f);
+    const uint32_t code = max(__float2uint_ru(v * 512.0f), 1u);
     value = static_cast<float>(code) * 0x1p-9f;
     return code;
   }
