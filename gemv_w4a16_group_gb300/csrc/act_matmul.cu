@@ -12,12 +12,10 @@
 namespace w4k {
 namespace {
 
-// Launches are plain ones: a kernel begins when the one before it on its stream has ended. Begun
-// early (programmatic launches), graphs of norms and products came to a standstill, on one stream
-// when every kernel let the next begin, on three streams even when no cluster kernel did. What a
-// resident CTA waits for without a limit is now its own cluster, which is placed as a whole, and
-// its columns of tensor memory: two narrow CTAs' fit in an SM, a wide CTA has the SM's shared
-// memory to itself.
+// Launches are plain ones: a kernel begins when the one before it on its stream has ended. What a
+// resident CTA waits for without a limit is its own cluster, which is placed as a whole, and its
+// columns of tensor memory: two narrow CTAs' fit in an SM, a wide CTA has the SM's shared memory to
+// itself.
 
 // A stage is a 128-byte swizzle row of k per row: 256 E2M1 or 128 E4M3 values. TILES scale tiles
 // (128 rows x 4 scales, 512 bytes) cover it; an MMA takes KM values, STEPS of them a stage.
@@ -163,9 +161,15 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t b, 
   }
 }
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
   uint32_t r;
@@ -632,6 +636,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
     tma_prefetch_desc(&maps.sx);
     if (use_store) tma_prefetch_desc(&maps.y);
   }
+  // Both CTAs have begun and their barriers stand. Tensor memory comes after that: the pair takes it
+  // together, and a request that finds no peer yet is never answered (one CTA may begin later where
+  // other kernels' CTAs leave the pair's SMs; chains on several streams stood still). Nor is it used
+  // before both have it; the copies do not wait for that.
+  __syncwarp();
+  cluster_sync_all();
   if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(holder)),
@@ -640,10 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before_sync();
-  __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers stand
-  tc_fence_after_sync();
-  const uint32_t tmem = *holder;
+  cluster_arrive();
+  uint32_t tmem = 0;
+  if (warp != 4) {
+    cluster_wait();
+    tc_fence_after_sync();
+    tmem = *holder;
+  }
 
   if (warp == 4) {
     if (lane == 0) {
@@ -676,6 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
         }
       }
     }
+    __syncwarp();
+    cluster_wait();  // (of the arrival above)
   } else if (warp == 5 && rank == 0) {
     // the whole warp walks the stages, one lane issues the pair's MMAs
     constexpr uint32_t idesc = idesc_scaled<FORM, false>(256, kWideN);
