@@ -234,11 +234,25 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+// What a row's sums are multiplied by, one factor after the other: r S and 1, or r and S where r S
+// is at or past the ends of fp32's range (rows of 2^-60 by weights of 2^-60, say), though the sum times
+// both need not be. Sums are 0 or 2^-20 to 2^46, act_quantize's r is 2^-92 to 2^117: sum r is then in
+// range, or the result is not.
+struct RowFactors {
+  float f, g;
+  __device__ __forceinline__ float of(float v) const { return v * f * g; }
+};
+__device__ __forceinline__ RowFactors row_factors(float r, float S) {
+  const float f = r * S;
+  return (f >= 0x1p-100f && f < 0x1p120f) || S == 0.f ? RowFactors{f, 1.f} : RowFactors{r, S};
+}
+
 // bf16(v f) to four columns of y, `left` of them inside it.
-__device__ __forceinline__ void store_four(uint16_t* out, int left, int N, float4 v, float f) {
+__device__ __forceinline__ void store_four(uint16_t* out, int left, int N, float4 v,
+                                           RowFactors f) {
   if (left <= 0) return;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(f.of(v.x), f.of(v.y));
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(f.of(v.z), f.of(v.w));
   const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                              *reinterpret_cast<const uint32_t*>(&hi));
   if (N % 4 == 0) {
@@ -452,7 +466,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int j = 0; j < 16; ++j)
           if (c + j < rows) {
             float f = __uint_as_float(v[j]);
-            if constexpr (FORM == kActNvfp4) f *= __ldg(a.x_rows + m0 + c + j) * wscale;
+            if constexpr (FORM == kActNvfp4)
+              f = row_factors(__ldg(a.x_rows + m0 + c + j), wscale).of(f);
             a.y[static_cast<size_t>(m0 + c + j) * a.N + n] =
                 __bfloat16_as_ushort(__float2bfloat16_rn(f));
           }
@@ -478,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           sum.y += v.y;
         }
         if constexpr (FORM == kActNvfp4) {
-          sum.x *= f * wscale;
-          sum.y *= f * wscale;
+          const RowFactors by = row_factors(f, wscale);
+          sum = make_float2(by.of(sum.x), by.of(sum.y));
         }
         uint16_t* out = a.y + static_cast<size_t>(m0 + j) * a.N + n;
         if (!ok || n >= a.N) continue;
@@ -511,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             sum.z += v[r].z;
             sum.w += v[r].w;
           }
-        const float f = FORM == kActNvfp4 ? __ldg(a.x_rows + m0 + j) * wscale : 1.f;
+        const RowFactors f = FORM == kActNvfp4 ? row_factors(__ldg(a.x_rows + m0 + j), wscale)
+                                               : RowFactors{1.f, 1.f};
         if (ok) store_four(a.y + static_cast<size_t>(m0 + j) * a.N + n, a.N - n, a.N, sum, f);
       }
       __syncwarp();
@@ -748,8 +764,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
       order.at(t, tm, tn);
       const int row0 = tm * 256 + static_cast<int>(rank) * 128 + warp * 32;
       const int row = row0 + lane;
-      float f = wscale;
-      if constexpr (FORM == kActNvfp4) f *= row < a.M ? __ldg(a.x_rows + row) : 0.f;
+      RowFactors f = {1.f, 1.f};
+      if constexpr (FORM == kActNvfp4)
+        f = row_factors(row < a.M ? __ldg(a.x_rows + row) : 0.f, wscale);
       bool ok = stage_wait(&acc_full[b], (n_tile >> 1) & 1u, abort_flag, a.status,
                            a.wait_limit_ns);
       ok = __all_sync(0xffffffffu, ok);
@@ -784,8 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
         for (int j = 0; j < 32; ++j) {
           float lo = __uint_as_float(v[2 * j]), hi = __uint_as_float(v[2 * j + 1]);
           if constexpr (FORM == kActNvfp4) {
-            lo *= f;
-            hi *= f;
+            lo = f.of(lo);
+            hi = f.of(hi);
           }
           asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[j]) : "f"(hi), "f"(lo));
         }
@@ -871,8 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
           sum.z += v[u][p].z;
           sum.w += v[u][p].w;
         }
-        float f = wscale;
-        if constexpr (FORM == kActNvfp4) f *= __ldg(a.x_rows + row);
+        RowFactors f = {1.f, 1.f};
+        if constexpr (FORM == kActNvfp4) f = row_factors(__ldg(a.x_rows + row), wscale);
         store_four(a.y + static_cast<size_t>(row) * a.N + n, a.N - n, a.N, sum, f);
       }
     }

@@ -1,6 +1,7 @@
 """Activations in 4 and 8 bits at the ends of fp32's range, against tests/act_reference.py (64 bits).
 
-Codes and scales of BF16 rows are exact, as in tests/test_gpu_act.py."""
+Codes and scales of BF16 rows are exact, and a product's bound is that of tests/test_gpu_act.py; a
+result below BF16's normal range is off by half of its smallest step, 2^-134, more."""
 import numpy as np
 import pytest
 import torch
@@ -39,3 +40,43 @@ def test_block_far_below_its_row():
     assert ws[0, 1] == ws[1, 2] == ws[2, 3] == 2.0 ** -9
     assert np.array_equal(s, ws) and np.array_equal(e, we)
     assert (np.abs(_f64(rows) - wr) <= 2.0 ** -23 * wr).all()
+
+
+# ---- NVFP4 products: a row's scale times the tensor's --------------------------------------
+@pytest.mark.parametrize("kernel,M,K", [(1, 5, 256), (1, 5, 4096), (1, 40, 4096), (1, 3, 1024),
+                                        (2, 140, 256), (3, 140, 1024), (4, 140, 2048)])
+@pytest.mark.parametrize("N", [130, 136])
+def test_scales_whose_product_leaves_fp32(kernel, M, N, K):
+    """Rows of 2^-78 to 2^120 by tensors of 2^-80 to 2^60: r S may leave fp32's range where y
+    does not, and rows of zeros stay zeros."""
+    g = torch.Generator().manual_seed(K)
+    size = torch.tensor([-78.0, -60, -20, 0, 40, 80, 120]).repeat(20)[:M]
+    x = (torch.randn(M, K, generator=g) * torch.exp2(size)[:, None]).bfloat16()
+    x[M - 1] = 0
+    q = w4.act_quantize(x.to(DEV), "nvfp4")
+    codes, scales, _ = w4.nvfp4_quantize(torch.randn(N, K, generator=g).to(DEV))
+    codes[3] = 0
+    tiles = w4.fp4_prepare_scales(scales)
+    e, s = _held(q[0], q[1], "nvfp4", K)
+    xh = (e.reshape(M, -1, 16) * s[..., None]).reshape(M, K)
+    wh = ref.values(codes.cpu().numpy(), scales.cpu().numpy(), "nvfp4")
+    sums, terms = xh @ wh.T, np.abs(xh) @ np.abs(wh).T
+    prev = w4.testing_set_act_kernel(kernel)
+    try:
+        for power in (-80, -60, -30, 0, 30, 60):
+            S = torch.tensor([1.37 * 2.0 ** power], device=DEV)
+            y = _f64(w4.nvfp4_matmul_act(q[0], q[1], q[2], codes, tiles, S))
+            f = _f64(q[2])[:, None] * _f64(S)
+            want, bound = sums * f, terms * f
+            tol = 2.0 ** -8 * np.abs(want) + (K * 2.0 ** -27 + 2.0 ** -22) * bound + 2.0 ** -134
+            top = float(torch.finfo(torch.bfloat16).max)
+            big = np.abs(want) - tol > top  # infinite for certain; else near it, or in range
+            near = (np.abs(want) + tol > top) & ~big
+            assert (y[big] == np.copysign(np.inf, want[big])).all()
+            inside = ~big & ~near
+            off = np.abs(y[inside] - want[inside])
+            assert (off <= tol[inside]).all(), f"2^{power}: {(~(off <= tol[inside])).sum()}"
+            assert (y[:, 3] == 0).all() and (y[M - 1] == 0).all()
+    finally:
+        w4.testing_set_act_kernel(prev)
+    assert w4.w4a16_device_status() == 0
