@@ -3,10 +3,12 @@
 //
 //   h = bf16(x + residual),  z = h * weight,  r = 1 / sqrt(mean(h^2) + eps),  y = z r
 //
-// (without a norm y = z = x, r = 1). z of two BF16 numbers is exact in fp32, so y is rounded
+// (without a norm y = z = x, r = 1). A product of two BF16 numbers is exact in fp32, so y is rounded
 // once before its codes are.
 //
 //   MXFP4, MXFP8: per 32 values X = floor(log2 max|y|) - 2 or - 8, codes of y 2^-X (exact).
+//     y = ((h 2^e) weight) (r 2^-e), 1 <= r 2^-e < 2: h 2^e is at most sqrt(K), so that the product
+//     leaves fp32's range only where y does (rows of 2^-74 by weights of 2^-70 without it: 0).
 //   NVFP4: r belongs to the whole row and goes into the row's scale, so the codes are those of z:
 //     a = max(max|z|, 2^-80) over the row, row scale a / 2688 r; per 16 values the smallest E4M3
 //     value s >= 448 max|z| / a, codes of 2688 z / (s a). Both quotients are taken with numerator
@@ -213,7 +215,8 @@ __device__ __forceinline__ bool any_few_bits(const float2 (&y)[8]) {
 
 // What a row's pieces need of the whole row.
 struct RowTerms {
-  Two rinv;        // 1 / rms (1 without a norm)
+  Two rinv;        // 1 / rms (1 without a norm), in MX formats without its power of two,
+  float base;      // which goes to h
   float a10, a12;  // NVFP4: the row's largest |z| under powers of two
   float i10;       // about 1 / a10
 };
@@ -266,13 +269,19 @@ template <int FORM, bool NORM>
 __device__ __forceinline__ RowTerms row_terms(const ActQuantArgs& a, int m, const Two* s_sum,
                                               const uint32_t* s_max, int warps, int group) {
   const int lane = threadIdx.x & 31, at = lane & (group - 1);
-  RowTerms r = {{1.f, 0.f}, 1.f, 1.f, 1.f};
+  RowTerms r = {{1.f, 0.f}, 1.f, 1.f, 1.f, 1.f};
   if constexpr (NORM) {
     Two sum = at < warps ? s_sum[at] : Two{0.f, 0.f};
     for (int o = group >> 1; o > 0; o >>= 1)
       sum = add(sum, {__shfl_xor_sync(0xffffffffu, sum.hi, o),
                       __shfl_xor_sync(0xffffffffu, sum.lo, o)});
     r.rinv = inverse_rms(sum, static_cast<float>(a.K), a.eps);
+    if constexpr (FORM != kActNvfp4) {
+      const uint32_t e = __float_as_uint(r.rinv.hi) & 0x7F800000u;
+      r.base = __uint_as_float(e);  // (a NaN's is infinity, and 0 times that NaN)
+      const float back = __uint_as_float((254u << 23) - e);
+      r.rinv = {r.rinv.hi * back, r.rinv.lo * back};
+    }
   }
   if constexpr (FORM == kActNvfp4) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, at < warps ? s_max[at] : 0u);
@@ -313,7 +322,7 @@ __device__ __forceinline__ void write_row(const ActQuantArgs& a, int m, const Pi
       float2 w[8];
       unpack(weight[v], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], w[i]);
+      for (int i = 0; i < 8; ++i) f[i] = mul2(NV ? f[i] : mul2(f[i], row.base), w[i]);
       top = top_of(f);
     } else {
       top = top_of(held[v]);

@@ -434,8 +434,8 @@ w4a16_status fp4_prepare_scales(const uint8_t* scales, int rows, int cols, uint8
  *   weight  bf16 [K]; eps >= 1e-30
  *   MXFP4 and MXFP8 codes are those of the exact y (sums of squares and 1 / sqrt(...) are carried
  *   in two fp32 numbers; about one code in 10^8, at a border, is its neighbour). NVFP4's codes and
- *   block scales are those of h * weight, and 1 / sqrt(...) goes into r. A row whose squares pass
- *   fp32's range becomes NaN.
+ *   block scales are those of h * weight, and 1 / sqrt(...) goes into r. A row whose squares (in
+ *   NVFP4 also one whose h * weight) pass fp32's range becomes NaN, as does a block with such a y.
  */
 w4a16_status act_quantize(const uint16_t* x, int64_t x_stride, int M, int K, int format,
                           uint8_t* codes, uint8_t* scales, float* row_scales,

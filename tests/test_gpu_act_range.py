@@ -1,5 +1,9 @@
 """Activations in 4 and 8 bits at the ends of fp32's range, against tests/act_reference.py (64 bits).
 
+Behind the norm y = h * weight / rms is rounded to fp32 and then, where that falls on a border between
+codes, moved to the side of the exact value; one that falls beside a border may have crossed it by what
+fp32 does not hold of 1 / rms, 2^-24 of itself: MX codes and scales are those of some y (1 + d),
+|d| <= 2^-23.
 Codes and scales of BF16 rows are exact, and a product's bound is that of tests/test_gpu_act.py; a
 result below BF16's normal range is off by half of its smallest step, 2^-134, more."""
 import numpy as np
@@ -21,6 +25,10 @@ def _f64(t):
 def _held(codes, scales, form, K):
     b = ref.untile(scales.cpu().numpy(), codes.shape[0], K // ref.BLOCK[form])
     return ref.element_values(codes.cpu().numpy(), form), ref.scale_values(b, form)
+
+
+def _randn(*shape, seed):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
 
 
 # ---- NVFP4: blocks far below their row -----------------------------------------------------
@@ -80,3 +88,47 @@ def test_scales_whose_product_leaves_fp32(kernel, M, N, K):
     finally:
         w4.testing_set_act_kernel(prev)
     assert w4.w4a16_device_status() == 0
+
+
+# ---- the norm: products that leave fp32 ----------------------------------------------------
+@pytest.mark.parametrize("form", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,K", [(5, 64), (9, 1056), (400, 4096)])
+def test_norm_of_products_below_fp32(form, M, K):
+    """Rows of 2^-74 by weights of 2^-70 to 1: h * weight leaves fp32's normal range, and fp32's
+    range, where h * weight / rms does not."""
+    eps = float(np.float32(1e-30))
+    h = (_randn(M, K, seed=K) * torch.exp2(torch.linspace(-78, -60, M))[:, None]).bfloat16()
+    block = torch.arange(K) // 32
+    weight = (_randn(K, seed=K + 1) * torch.exp2(-(block % 8) * 10.0)).bfloat16()
+    h[1, 64:] = 0
+    codes, scales, _, _ = w4.act_rmsnorm(h.to(DEV), weight.to(DEV), form, eps=eps)
+    e, s = _held(codes, scales, form, K)
+    z, rinv, _ = ref.rmsnorm(_f64(h), None, _f64(weight), eps)
+    fits = False
+    for d in (-2.0 ** -23, 0, 2.0 ** -23):
+        we, ws, _ = ref.quantize(z * rinv[:, None] * (1 + d), form)
+        fits |= (e == we) & (np.repeat(s == ws, 32, 1))
+    assert fits.all(), f"{(~fits).sum()} of {fits.size}"
+
+
+@pytest.mark.parametrize("form", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("power", [60, 50])
+def test_norm_of_products_above_fp32(form, power):
+    """Rows of 2^50 by weights of 2^80: h * weight is past fp32's range, h * weight / rms is not.
+    At 2^60 the sum of the row's squares is, too (512 * 2^120), and the row is NaN."""
+    M, K = 6, 512
+    h = (_randn(M, K, seed=1) * 2.0 ** power).bfloat16()
+    h[2, :64] *= 2.0 ** -80
+    weight = (_randn(K, seed=2) * torch.exp2((torch.arange(K) // 32 % 3) * 40.0)).bfloat16()
+    codes, scales, _, _ = w4.act_rmsnorm(h.to(DEV), weight.to(DEV), form)
+    e, s = _held(codes, scales, form, K)
+    if power == 60:
+        assert ((_f64(h) ** 2).sum(1) > 2.0 ** 128).all() and np.isnan(s).all()
+        return
+    z, rinv, _ = ref.rmsnorm(_f64(h), None, _f64(weight), 1e-6)
+    assert np.abs(z).max() > 2.0 ** 128
+    fits = False
+    for d in (-2.0 ** -23, 0, 2.0 ** -23):
+        we, ws, _ = ref.quantize(z * rinv[:, None] * (1 + d), form)
+        fits |= (e == we) & (np.repeat(s == ws, 32, 1))
+    assert fits.all(), f"{(~fits).sum()} of {fits.size}"
