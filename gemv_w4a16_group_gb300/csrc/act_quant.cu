@@ -482,13 +482,13 @@ cudaError_t launch_form(const ActQuantArgs& a, cudaStream_t stream) {
 __global__ void __launch_bounds__(256)
     fp4_prepare_scales_kernel(const uint8_t* __restrict__ scales, int rows, int cols,
                               uint32_t* __restrict__ tiles, long long words) {
-  const int cb = (cols + 3) / 4;
+  const int cb = (cols - 1) / 4 + 1;
   for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < words;
        i += static_cast<long long>(gridDim.x) * 256) {
     const long long tile = i >> 7;
     const int in = static_cast<int>(i & 127);
     const long long row = tile / cb * 128 + (in & 3) * 32 + (in >> 2);
-    const int c0 = static_cast<int>(tile % cb) * 4;
+    const long long c0 = tile % cb * 4;
     uint32_t w = 0u;
     if (row < rows)
 #pragma unroll
@@ -513,7 +513,7 @@ cudaError_t launch_act_quantize(const ActQuantArgs& a, int format, cudaStream_t 
 cudaError_t launch_fp4_prepare_scales(const uint8_t* scales, int rows, int cols, uint8_t* tiles,
                                       cudaStream_t stream) {
   const long long words =
-      static_cast<long long>((rows + 127) / 128) * ((cols + 3) / 4) * 128;
+      static_cast<long long>((rows - 1) / 128 + 1) * ((cols - 1) / 4 + 1) * 128;
   long long blocks = (words + 255) / 256;
   if (blocks > 8192) blocks = 8192;
   fp4_prepare_scales_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(

@@ -132,3 +132,19 @@ def test_norm_of_products_above_fp32(form, power):
         we, ws, _ = ref.quantize(z * rinv[:, None] * (1 + d), form)
         fits |= (e == we) & (np.repeat(s == ws, 32, 1))
     assert fits.all(), f"{(~fits).sum()} of {fits.size}"
+
+
+# ---- scale tiles of as many rows as an int counts ------------------------------------------
+def test_scale_tiles_of_the_most_rows():
+    R = (1 << 31) - 1
+    scales = torch.arange(1 << 20, device=DEV).mul_(2654435761).bitwise_right_shift_(7).to(torch.uint8)
+    scales = scales.repeat(1 << 11)[:R].view(R, 1)
+    tiles = w4.fp4_prepare_scales(scales)
+    assert tiles.shape == (1 << 24, 1, 512)
+    for first in (0, 12345, (1 << 24) - 100):  # blocks of 128 rows
+        part = tiles[first:first + 100]
+        full = ref.untile(part.cpu().numpy(), 12800, 4)
+        want = np.zeros((12800, 4), np.uint8)
+        rows = scales[first * 128:first * 128 + 12800].cpu().numpy()
+        want[:rows.shape[0], :1] = rows
+        assert np.array_equal(full, want)
