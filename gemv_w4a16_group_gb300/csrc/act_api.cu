@@ -23,6 +23,20 @@ bool format_ok(int format) { return format >= W4A16_ACT_NVFP4 && format <= W4A16
 
 bool stride_ok(int64_t stride, int M, int K) { return M == 1 || (stride >= K && stride % 8 == 0); }
 
+// Whether rows of K values at p and at q share memory in another way than row by row the same: a row
+// that is written would then be one that another CTA may still read.
+bool overlap_in_part(const uint16_t* p, int64_t p_stride, const uint16_t* q, int64_t q_stride, int M,
+                     int K) {
+  if (M == 1) p_stride = q_stride = K;
+  if (p == q && p_stride == q_stride) return false;
+  const intptr_t a = reinterpret_cast<intptr_t>(p) / 2, b = reinterpret_cast<intptr_t>(q) / 2;
+  if (a + (M - 1) * p_stride + K <= b || b + (M - 1) * q_stride + K <= a) return false;
+  if (p_stride != q_stride) return true;
+  // rows in equal steps lie apart where they do within a step
+  const int64_t apart = (a > b ? a - b : b - a) % p_stride;
+  return apart < K || p_stride - apart < K;
+}
+
 w4a16_status check_quantize(const w4k::ActQuantArgs& a, int format) {
   if (!a.x || !a.codes || !a.scales) return W4A16_ERR_INVALID_ARG;
   if (a.M <= 0 || a.K <= 0 || a.K % 32 != 0 || !format_ok(format)) return W4A16_ERR_INVALID_ARG;
@@ -115,8 +129,12 @@ w4a16_status act_rmsnorm(const uint16_t* x, int64_t x_stride, const uint16_t* re
   if (s != W4A16_OK) return s;
   if (residual && (!stride_ok(residual_stride, M, K) || !stride_ok(residual_out_stride, M, K)))
     return W4A16_ERR_INVALID_ARG;
-  if (!aligned(weight, 16) || !aligned(residual, 16) || !aligned(residual_out, 16))
-    return W4A16_ERR_MISALIGNED;
+  if (!aligned(residual, 16) || !aligned(residual_out, 16)) return W4A16_ERR_MISALIGNED;
+  if (residual &&
+      (overlap_in_part(residual_out, residual_out_stride, x, x_stride, M, K) ||
+       overlap_in_part(residual_out, residual_out_stride, residual, residual_stride, M, K)))
+    return W4A16_ERR_INVALID_ARG;
+  if (!aligned(weight, 16)) return W4A16_ERR_MISALIGNED;
   return from_cuda(
       w4k::launch_act_quantize(a, format, reinterpret_cast<cudaStream_t>(stream)));
 }

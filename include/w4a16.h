@@ -430,7 +430,7 @@ w4a16_status fp4_prepare_scales(const uint8_t* scales, int rows, int cols, uint8
  *
  * act_rmsnorm -- the same of y = h * weight / sqrt(mean(h^2) + eps), h = bf16(x + residual):
  *   residual, residual_out  bf16 [M, K] with strides as x's; h is written to residual_out, which
- *     may be residual itself or x. Both NULL: h = x.
+ *     may be residual itself or x, and overlaps neither otherwise. Both NULL: h = x.
  *   weight  bf16 [K]; eps 1e-30 to 1e30
  *   MXFP4 and MXFP8 codes are those of the exact y (sums of squares and 1 / sqrt(...) are carried
  *   in two fp32 numbers; about one code in 10^8, at a border, is its neighbour). NVFP4's codes and
