@@ -160,18 +160,28 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # none in a 
 _device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _stream(stream) -> int:
+def _current():
+    """Number of the current device; None without a driver, where no tensor is a CUDA tensor."""
+    try:
+        return _device()
+    except (RuntimeError, TypeError):
+        return None
+
+
+def _stream(stream, device=None) -> int:
     if stream is None:
         # torch.cuda.current_stream() builds a Stream object: 3 us of a call
-        return _raw_stream(_device())
+        return _raw_stream(_device() if device is None else device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
-def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> int:
+def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, device=None) -> int:
+    """t's address, after its checks; `device`: the number of the one it must be on."""
     if (isinstance(t, _Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
-            and t.is_cuda and t.is_contiguous()):
+            and (t.is_cuda if device is None else t.get_device() == device)
+            and t.is_contiguous()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -183,7 +193,15 @@ def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> int:
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None:
+        _same_device(t, name, device)
     return t.data_ptr()
+
+
+def _same_device(t: torch.Tensor, name: str, device: int):
+    # (kernels are launched on the current device, which may not reach another one's memory)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current device, cuda:{device}, got {t.device}")
 
 
 def _check(name: str, status: int):
@@ -730,12 +748,12 @@ def _new(like: torch.Tensor, shape, dtype, stream, zero: bool = False) -> torch.
         return t.zero_() if zero else t
 
 
-def _result(t, name: str, like: torch.Tensor, shape, dtype, stream):
+def _result(t, name: str, like: torch.Tensor, shape, dtype, stream, device=None):
     """(t, its address), with a new t for None."""
     if t is None:
         t = _new(like, shape, dtype, stream)
         return t, t.data_ptr()
-    return t, _dev(t, name, dtype, shape)
+    return t, _dev(t, name, dtype, shape, device)
 
 
 def kv4_append(cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -845,15 +863,16 @@ def fp4_prepare_scales(scales: torch.Tensor, tiles=None, stream=None) -> torch.T
     """uint8 block scales [N, blocks] of nvfp4_quantize or mxfp4_quantize -> the tiles that
     nvfp4_matmul_act and mxfp4_matmul_act read, uint8 [ceil(N/128), ceil(blocks/4), 512]."""
     N, blocks = scales.shape
-    tiles, p = _result(tiles, "tiles", scales, _tiles_shape(N, blocks), torch.uint8, stream)
+    device = _current()
+    tiles, p = _result(tiles, "tiles", scales, _tiles_shape(N, blocks), torch.uint8, stream, device)
     _check("fp4_prepare_scales", _lib.fp4_prepare_scales(
-        _dev(scales, "scales", torch.uint8), N, blocks, p, _stream(stream)))
+        _dev(scales, "scales", torch.uint8, None, device), N, blocks, p, _stream(stream, device)))
     return tiles
 
 
-def _rows(t: torch.Tensor, name: str, shape=None):
+def _rows(t: torch.Tensor, name: str, device, shape=None):
     """(address, elements between rows) of BF16 rows that may lie in a wider array."""
-    if isinstance(t, _Tensor) and t.dtype is torch.bfloat16 and t.is_cuda:
+    if isinstance(t, _Tensor) and t.dtype is torch.bfloat16 and t.get_device() == device:
         strides = t.stride()
         if len(strides) == 2 and strides[1] == 1 and (shape is None or t.shape == shape):
             return t.data_ptr(), strides[0]
@@ -866,10 +885,11 @@ def _rows(t: torch.Tensor, name: str, shape=None):
     if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be {'[M, K]' if shape is None else list(shape)}, "
                          f"got {list(t.shape)}")
+    _same_device(t, name, device)
     raise ValueError(f"{name} must have dense rows")
 
 
-def _act_out(x, M: int, K: int, format: str, codes, scales, row_scales, stream):
+def _act_out(x, M: int, K: int, format: str, codes, scales, row_scales, stream, device):
     """(number of the format, codes, scales, row_scales, their addresses)"""
     try:
         number, block, per_byte = _ACT_FORMATS[format]
@@ -882,17 +902,17 @@ def _act_out(x, M: int, K: int, format: str, codes, scales, row_scales, stream):
         codes = _new(x, shape, torch.uint8, stream)
         cp = codes.data_ptr()
     else:
-        cp = _dev(codes, "codes", torch.uint8, shape)
+        cp = _dev(codes, "codes", torch.uint8, shape, device)
     if scales is None:
         scales = _new(x, tiles, torch.uint8, stream)
         sp = scales.data_ptr()
     else:
-        sp = _dev(scales, "scales", torch.uint8, tiles)
+        sp = _dev(scales, "scales", torch.uint8, tiles, device)
     if number != 0:
         if row_scales is not None:
             raise ValueError(f"{format} has no row scales")
         return number, codes, scales, None, cp, sp, None
-    row_scales, rp = _result(row_scales, "row_scales", x, (M,), torch.float32, stream)
+    row_scales, rp = _result(row_scales, "row_scales", x, (M,), torch.float32, stream, device)
     return number, codes, scales, row_scales, cp, sp, rp
 
 
@@ -900,11 +920,12 @@ def act_quantize(x: torch.Tensor, format: str = "nvfp4", codes=None, scales=None
                  stream=None):
     """x bf16 [M, K] (rows may be strided) -> (codes, scales, row_scales or None) in "nvfp4",
     "mxfp4" or "mxfp8". Rows of the scale tiles past M are not written."""
-    xp, xs = _rows(x, "x")
+    device = _current()
+    xp, xs = _rows(x, "x", device)
     M, K = x.shape
     number, codes, scales, row_scales, cp, sp, rp = _act_out(x, M, K, format, codes, scales,
-                                                             row_scales, stream)
-    status = _lib.act_quantize(xp, xs, M, K, number, cp, sp, rp, _stream(stream))
+                                                             row_scales, stream, device)
+    status = _lib.act_quantize(xp, xs, M, K, number, cp, sp, rp, _stream(stream, device))
     if status:
         raise W4A16Error("act_quantize", status)
     return codes, scales, row_scales
@@ -916,23 +937,25 @@ def act_rmsnorm(x: torch.Tensor, weight: torch.Tensor, format: str = "nvfp4", ep
     """h = x + residual (bf16 [M, K], rows may be strided), quantized h * weight / rms(h) ->
     (codes, scales, row_scales or None, h). h goes to ``residual_out``, which may be ``residual``
     itself; without a residual h is x, and None is returned for it."""
-    xp, xs = _rows(x, "x")
+    device = _current()
+    xp, xs = _rows(x, "x", device)
     shape = x.shape
     M, K = shape
     qp, qs, op, os_ = None, 0, None, 0
     if residual is not None:
-        qp, qs = _rows(residual, "residual", shape)
+        qp, qs = _rows(residual, "residual", device, shape)
         if residual_out is None:
             residual_out = _new(x, shape, torch.bfloat16, stream)
             op, os_ = residual_out.data_ptr(), K
         else:
-            op, os_ = _rows(residual_out, "residual_out", shape)
+            op, os_ = _rows(residual_out, "residual_out", device, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     number, codes, scales, row_scales, cp, sp, rp = _act_out(x, M, K, format, codes, scales,
-                                                             row_scales, stream)
-    status = _lib.act_rmsnorm(xp, xs, qp, qs, op, os_, _dev(weight, "weight", torch.bfloat16, (K,)),
-                              eps, M, K, number, cp, sp, rp, _stream(stream))
+                                                             row_scales, stream, device)
+    wp = _dev(weight, "weight", torch.bfloat16, (K,), device)
+    status = _lib.act_rmsnorm(xp, xs, qp, qs, op, os_, wp, eps, M, K, number, cp, sp, rp,
+                              _stream(stream, device))
     if status:
         raise W4A16Error("act_rmsnorm", status)
     return codes, scales, row_scales, residual_out
@@ -947,19 +970,20 @@ def nvfp4_matmul_act(x_codes: torch.Tensor, x_scales: torch.Tensor, x_row_scales
     M, half = x_codes.shape
     N = codes.shape[0]
     words = (half + 31) // 32
+    device = _current()
     if y is None:
         y = _new(x_codes, (M, N), torch.bfloat16, stream)
         yp = y.data_ptr()
     else:
-        yp = _dev(y, "y", torch.bfloat16, (M, N))
+        yp = _dev(y, "y", torch.bfloat16, (M, N), device)
     status = _lib.nvfp4_matmul_act(
-        _dev(x_codes, "x_codes", torch.uint8),
-        _dev(x_scales, "x_scales", torch.uint8, ((M + 127) // 128, words, 512)),
-        _dev(x_row_scales, "x_row_scales", torch.float32, (M,)),
-        _dev(codes, "codes", torch.uint8, (N, half)),
-        _dev(scale_tiles, "scale_tiles", torch.uint8, ((N + 127) // 128, words, 512)),
-        _dev(tensor_scale, "tensor_scale", torch.float32, (1,)), yp, M, N, 2 * half,
-        _stream(stream))
+        _dev(x_codes, "x_codes", torch.uint8, None, device),
+        _dev(x_scales, "x_scales", torch.uint8, ((M + 127) // 128, words, 512), device),
+        _dev(x_row_scales, "x_row_scales", torch.float32, (M,), device),
+        _dev(codes, "codes", torch.uint8, (N, half), device),
+        _dev(scale_tiles, "scale_tiles", torch.uint8, ((N + 127) // 128, words, 512), device),
+        _dev(tensor_scale, "tensor_scale", torch.float32, (1,), device), yp, M, N, 2 * half,
+        _stream(stream, device))
     if status:
         raise W4A16Error("nvfp4_matmul_act", status)
     return y
@@ -975,17 +999,18 @@ def mxfp4_matmul_act(x_codes: torch.Tensor, x_scales: torch.Tensor, codes: torch
         raise ValueError(f"x_codes must be [M, {half}] (MXFP4) or [M, {2 * half}] (MXFP8), "
                          f"got {list(x_codes.shape)}")
     words = (half + 63) // 64
+    device = _current()
     if y is None:
         y = _new(x_codes, (M, N), torch.bfloat16, stream)
         yp = y.data_ptr()
     else:
-        yp = _dev(y, "y", torch.bfloat16, (M, N))
+        yp = _dev(y, "y", torch.bfloat16, (M, N), device)
     status = _lib.mxfp4_matmul_act(
-        _dev(x_codes, "x_codes", torch.uint8),
-        _dev(x_scales, "x_scales", torch.uint8, ((M + 127) // 128, words, 512)),
-        1 if width == half else 2, _dev(codes, "codes", torch.uint8),
-        _dev(scale_tiles, "scale_tiles", torch.uint8, ((N + 127) // 128, words, 512)), yp, M, N,
-        2 * half, _stream(stream))
+        _dev(x_codes, "x_codes", torch.uint8, None, device),
+        _dev(x_scales, "x_scales", torch.uint8, ((M + 127) // 128, words, 512), device),
+        1 if width == half else 2, _dev(codes, "codes", torch.uint8, None, device),
+        _dev(scale_tiles, "scale_tiles", torch.uint8, ((N + 127) // 128, words, 512), device), yp,
+        M, N, 2 * half, _stream(stream, device))
     if status:
         raise W4A16Error("mxfp4_matmul_act", status)
     return y
