@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2 * SPLIT, 1, 1)
     tma_prefetch_desc(&maps.x);
     tma_prefetch_desc(&maps.sw);
     tma_prefetch_desc(&maps.sx);
-    if (use_store) tma_prefetch_desc(&maps.y);
+    if (SPLIT == 1 && use_store) tma_prefetch_desc(&maps.y);
   }
   // Both CTAs have begun and their barriers stand. Tensor memory comes after that: the pair takes it
   // together, and a request that finds no peer yet is never answered (one CTA may begin later where
@@ -985,7 +985,8 @@ cudaError_t launch_wide(const ActMatmulArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = make_scale_map(&maps.sw, a.w_scales, a.N, tiles_k, L::kTiles, L::kBlocks);
   if (e != cudaSuccess) return e;
-  const int use_store = a.N % 8 == 0;
+  // (sums of several parts are stored from registers)
+  const int use_store = SPLIT == 1 && a.N % 8 == 0;
   if (use_store) {
     e = encode_tensor_map(&maps.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.y, static_cast<uint64_t>(a.N),
                           static_cast<uint64_t>(a.M), static_cast<uint64_t>(a.N) * 2, 64, 32,
