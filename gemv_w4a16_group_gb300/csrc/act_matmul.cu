@@ -4,8 +4,9 @@
 //
 // with E2M1 (or, for 8-bit activations, E4M3) elements and the blocks' scales multiplied by the
 // tensor pipe itself (tcgen05.mma, block_scale): an MMA takes 128 rows of weights by up to 128
-// rows of x and 64 values of k (32 with 8-bit x), the elements from shared memory, one scale per
-// 16 or 32 of them and row from tensor memory, and adds in fp32.
+// rows of x (few rows), or 256 rows of x by 256 of weights (a pair of CTAs), and 64 values of k (32
+// with 8-bit x), the elements from shared memory, one scale per 16 or 32 of them and row from tensor
+// memory, and adds in fp32.
 #include "act.h"
 #include "common.cuh"
 
@@ -1016,13 +1017,15 @@ cudaError_t launch_form(const ActMatmulArgs& a, int kernel, cudaStream_t stream)
       ((static_cast<long long>(a.M) + 255) / 256) * ((static_cast<long long>(a.N) + 255) / 256);
   if (kernel == 0) {
     // The pairs' tiles of 256 x 256 want 256 rows of x or enough columns: 14336 x 4096 NVFP4 at 64
-    // rows 11.7 us (narrow 12.4), at 48 12.5 (11.2), MXFP8 at 96 15.5 (15.4), at 64 15.1 (12.7);
-    // 4096 x 14336 NVFP4 at 256 19.4 (16.0), at 512 19.9 (22.0).
+    // rows 12.1 us (narrow 12.7), at 56 12.4 either way, at 48 12.7 (11.9), MXFP8 at 96 15.6 (15.8), at
+    // 80 15.5 (15.3), at 64 15.2 (13.1); 4096 x 14336 NVFP4 at 256 rows 19.5 (16.6), at 320 19.7
+    // (21.4). (Of the narrow kernel's end at 256 rows: with few columns it would win a little longer,
+    // 1536 x 8960 at 384 rows NVFP4 12.4 against 13.7 of four pairs a tile, MXFP8 13.8 against 15.3.)
     const int few = FORM == kActMxfp8 ? 80 : 48;
     kernel = a.M <= few || (a.M <= 256 && tiles * 5 < sms) ? 1 : 2;
     // With few tiles pairs share them, where each part of k outweighs adding the parts up (4096 x
-    // 14336 MXFP4 at 512 rows 21.6 -> 17.2 us; 16 stages are even). 36 clusters of two pairs and
-    // 15 of four fit on 152 SMs.
+    // 14336 MXFP4 at 512 rows 21.8 -> 17.2 us with two a tile, 1536 x 8960 MXFP8 at 384 25.1 -> 17.3 with
+    // two, 15.3 with four; 16 stages are even). 36 clusters of two pairs and 15 of four fit on 152 SMs.
     if (kernel == 2 && stages >= 24)
       kernel = tiles * 10 <= sms ? 4 : tiles * 4 <= sms - 8 ? 3 : 2;
   }

@@ -16,9 +16,9 @@
 //
 // What bounds it: a row is read once (2 bytes a value, 4 with a residual) and 0.53 to 1.03 bytes
 // (and 2 of the residual) written, so HBM for many rows: 4096 x 14336 27.0 us (MXFP8, 0.97 of the
-// copy rate) and 26.8 (NVFP4, 0.83), 4096 x 4096 with residual and norm 20.5 (MXFP8, 0.85) and 18.5
-// (NVFP4, 0.88); a CTA's chain of loads, joins and root for few: one row of 4096 1.2 us alone, 2.3
-// with norm. A CTA holds its row in registers between the row's sums and the codes, and loads
+// copy rate), 23.6 (MXFP4, 0.93) and 27.1 (NVFP4, 0.82), 4096 x 4096 with residual and norm 20.5
+// (MXFP8, 0.85; MXFP4 20.4, 0.79) and 18.6 (NVFP4, 0.87); a CTA's chain of loads, joins and root for
+// few: one row of 4096 1.3 us alone, 2.3 with norm. A CTA holds its row in registers between the row's sums and the codes, and loads
 // everything the row needs (weights and residual too) at once, before it waits for any of it (26
 // us for 4096 x 4096 with the weights loaded where they are used). Resident CTAs that take rows in
 // turn, the next rows' bulk copies under way, were no faster: the SMs hold enough CTAs to overlap
@@ -127,8 +127,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return a;
 }
 
-// About 1 / v, for quotients whose residual is put back: the quotient is then within half a last
-// place and 2^-22 of one, so one that fp32 holds comes out exactly.
+// About 1 / v, for quotients whose residual, taken exactly by a fused multiply-add, is put back
+// (Markstein's correction of a quotient): the quotient is then within half a last place and 2^-22 of
+// one, so one that fp32 holds comes out exactly.
 __device__ __forceinline__ float near_reciprocal(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -462,12 +463,12 @@ template <int FORM, bool NORM>
 cudaError_t launch_form(const ActQuantArgs& a, cudaStream_t stream) {
   const int pieces = a.K / 16, sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // Pieces a thread (times with launches that overlapped; plain ones add up to 0.6 us). Few rows are
-  // a matter of latency: one each (one row of 4096 with norm 2.2 us, with two pieces 2.6, four 3.4).
-  // Many rows keep the SMs full whatever a CTA's size, and fewer threads join in fewer steps: two
-  // from 256 pieces on (4096 x 4096 with norm 20.8 us, one 23.4, four 23.5; rows of 1536 10.0 with
-  // one, 11.1 with two), four where NVFP4 waits for the row's largest value alone (4096 x 14336
-  // 26.4, two 33.6). Longer rows take what 512 threads need.
+  // Pieces a thread. Few rows are a matter of latency: one each (one row of 4096 with norm 2.5 us, with
+  // two pieces 2.7, four 3.3). Many rows keep the SMs full whatever a CTA's size, and fewer threads join
+  // in fewer steps: two from 256 pieces on (4096 x 4096 MXFP8 with norm 15.8 us, one 18.1, four 16.1;
+  // with residual 20.9, 22.2 and 23.2; rows of 1536 8.3 with one, 9.2 with two), four where NVFP4 waits
+  // for the row's largest value alone (4096 x 14336 27.1, two 35.2, one 36.5; MXFP8 27.9, 27.1 and 28.8).
+  // Longer rows take what 512 threads need.
   int v = 1;
   if (a.M >= 2 * sms && pieces >= 256) v = FORM == kActNvfp4 && !NORM && pieces >= 768 ? 4 : 2;
   while (pieces > (v == 1 ? 1024 : 512) * v) v *= 2;
